@@ -87,6 +87,8 @@ typedef struct CUstream_st* kda_stream_t;
 #define KDA_ERR_CUDA (-9)                /* a CUDA runtime call failed        */
 #define KDA_ERR_BAD_OUT_INDEX (-10)      /* (device) an out_index entry lies
                                             outside [0, out_rows)            */
+#define KDA_ERR_BAD_CACHE_INDEX (-11)    /* (device) a page index, cache length
+                                            or position out of its range     */
 
 /* kernel selectors for kda_chunk_prefill_fwd_ex */
 #define KDA_KERNEL_AUTO 0  /* SPLIT_STREAMED when N * heads * P <= SMs / 2 for
@@ -317,6 +319,90 @@ int kda_skinny_proj(const void* x, int64_t ldx, const void* w_ab, const void* w_
                     int64_t ldy, void* z, int64_t ldz, int32_t m, int32_t k, int32_t n_ab,
                     int32_t r, int32_t n_b, void* workspace, size_t workspace_bytes,
                     kda_stream_t stream);
+
+/*
+ * ---- The full-attention layer beside the KDA layers ----
+ *
+ * Models that use KDA interleave its layers with full-attention layers.  The three calls
+ * below are such a layer's memory-side half, for prefill, decode and speculative verify:
+ * the norm in front of its projections, the rotation and append of its keys and values to
+ * a paged 8-bit cache, and the attention over that cache.  The conventions above hold (device
+ * pointers, caller-owned memory, asynchronous on `stream`, status word in the workspace,
+ * head dim 128, sequences packed by cu_seqlens).
+ *
+ * kda_add_rms_norm: s = x + residual; y = s * (mean(s^2) + eps)^(-1/2) * weight, per row.
+ *   x            bf16 [rows, cols]
+ *   residual     bf16 or fp32 (residual_dtype: KDA_STATE_BF16 / KDA_STATE_F32), or NULL: s = x
+ *   residual_out s in the residual's type (may be residual itself, or x when both are bf16);
+ *                not written when residual is NULL
+ *   weight       bf16 or fp32 (weight_dtype) [cols]
+ *   y            bf16 [rows, cols] or NULL
+ *   y8, y_scale  e4m3 [rows, cols] with fp32 scales, or both NULL: group 128 gives one scale per
+ *                128 columns ([rows, ceil(cols / 128)]), group 0 one per row ([rows]);
+ *                scale = max(max|y| / 448, 2^-40), y8 = e4m3(y / scale).  y enters in fp32.
+ * ld*: row strides in elements, at least cols.  1 <= cols <= 32768, rows <= 2^31 - 1.  Any
+ * alignment of the elements' own type is accepted; 16-byte rows (8-byte for y8) and cols a
+ * multiple of 8 take the wide path.  At least one of y and y8 must be given.
+ */
+int kda_add_rms_norm(const void* x, int64_t ldx, const void* residual, int64_t ldr,
+                     int residual_dtype, const void* weight, int weight_dtype, float eps,
+                     void* residual_out, int64_t lds, void* y, int64_t ldy, void* y8, int64_t ldy8,
+                     float* y_scale, int32_t group, int64_t rows, int32_t cols,
+                     kda_stream_t stream);
+
+/*
+ * A paged key / value cache in e4m3 with one fp32 scale per (page, kv head).  Element
+ * (page, head, slot, channel) of keys and values is at page * page_stride + head * head_stride +
+ * slot * token_stride + channel (bytes; multiples of 16, token_stride at least 128), so dense
+ * [pages, kv_heads, page_size, 128], [pages, page_size, kv_heads, 128] and keys and values
+ * interleaved in one pool are all accepted.  Position j of sequence n sits in slot
+ * j % page_size of page block_table[n * table_stride + j / page_size].  kv_lens[n] counts
+ * the sequence's cached tokens INCLUDING the new ones of the step, for the append and for the
+ * attention alike.  The value of an entry is its e4m3 value times its page's scale; a scale is
+ * positive, and kda_rope_append makes it a power of two.
+ */
+typedef struct kda_kv_cache {
+  void* k;                     /* 16-byte aligned                                */
+  void* v;                     /* 16-byte aligned                                */
+  float* k_scale;              /* [num_pages, kv_heads], page stride below       */
+  float* v_scale;
+  int64_t page_stride, head_stride, token_stride;
+  int64_t scale_stride;        /* floats between the scales of successive pages  */
+  int32_t num_pages;
+  int32_t page_size;           /* 16, 32, 64 or 128                              */
+  int32_t kv_heads;
+  int32_t max_blocks;          /* columns of block_table                         */
+  const int32_t* block_table;  /* [num_seqs, max_blocks]                         */
+  int64_t table_stride;
+  const int32_t* kv_lens;      /* [num_seqs]                                     */
+} kda_kv_cache;
+
+/*
+ * Rotates the new queries and keys and appends the new keys and values to the cache.
+ *   q            bf16 [T, heads, 128] or NULL (then q_out is not written)
+ *   k, v         bf16 [T, kv_heads, 128]
+ *   q_out        bf16 [T, heads, 128]; may be q
+ *   rope         fp32 [rope_rows, rot_dim], row p = cos then sin of position p (rot_dim / 2 each);
+ *                16-byte aligned.  rot_dim a multiple of 16 in [0, 128]; 0: no rotation
+ *                (rope may be NULL).  Whatever scaling long contexts want is in the table.
+ *   interleaved  0: channel j pairs with j + rot_dim / 2; 1: 2j pairs with 2j + 1
+ *   positions    int32 [T]: the table row of each token, or NULL: its cache position
+ * Strides: elements between tokens, multiples of 8, at least heads * 128 (kv_heads * 128);
+ * pointers 16-byte aligned.  Token i of a sequence with t new tokens goes to cache position
+ * kv_lens - t + i.  A page that the step starts takes the scale of its new tokens; a page
+ * that held tokens already keeps its scale unless the new ones need a larger one, and then its
+ * older entries are requantised.  No two sequences may append to one page in one call.
+ * Device errors: KDA_ERR_BAD_CU_SEQLENS; KDA_ERR_BAD_CACHE_INDEX for a cache length below
+ * the new tokens' count or beyond the block table, a page outside [0, num_pages) (its tokens
+ * are not stored), or a position outside the table (the token is left unrotated).
+ * The workspace needs the 256 bytes of status words.
+ */
+int kda_rope_append(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                    const void* v, int64_t v_stride, const float* rope, int64_t rope_rows,
+                    int32_t rot_dim, int32_t interleaved, const int32_t* positions, void* q_out,
+                    int64_t q_out_stride, const kda_kv_cache* cache, const int32_t* cu_seqlens,
+                    void* workspace, kda_stream_t stream, int64_t total_tokens, int32_t num_seqs,
+                    int32_t heads, size_t workspace_bytes);
 
 /*
  * The value-dimension split factor the automatic path uses for a batch of

@@ -19,6 +19,8 @@ names follow the C ABI in ``include/kda.h``:
     KERNEL_REF / KERNEL_PIPE
     last_device_status(workspace) -> int
     status_string(code) -> str
+    add_rms_norm, rope_table, rope_append: the full-attention layer beside the KDA layers
+        (layer.py)
 
 There is no CPU fallback: if the library is missing or the device is not an
 sm_103 GPU, these calls raise.
@@ -49,6 +51,7 @@ ERR_DEVICE_TIMEOUT = -7
 ERR_BAD_CU_SEQLENS = -8
 ERR_CUDA = -9
 ERR_BAD_OUT_INDEX = -10
+ERR_BAD_CACHE_INDEX = -11
 
 # every symbol include/kda.h declares
 EXPORTS = ("kda_workspace_size", "kda_chunk_prefill_fwd", "kda_chunk_prefill_fwd_ex",
@@ -56,7 +59,7 @@ EXPORTS = ("kda_workspace_size", "kda_chunk_prefill_fwd", "kda_chunk_prefill_fwd
            "kda_device_check", "kda_plan", "kda_plan_for", "kda_chunk_prefill_fwd_strided",
            "kda_recurrent_fwd", "kda_chunk_prefill_fwd_noalloc", "kda_chunk_prefill_fwd_scatter",
            "kda_recurrent_fwd_scatter", "kda_skinny_proj_workspace_size", "kda_skinny_proj",
-           "kda_test_drop_one_record")
+           "kda_test_drop_one_record", "kda_add_rms_norm", "kda_rope_append")
 
 _lib = None
 _lock = threading.Lock()
@@ -135,6 +138,13 @@ def lib() -> ctypes.CDLL:
             L.kda_chunk_prefill_fwd_noalloc.restype = ctypes.c_int
             L.kda_chunk_prefill_fwd_noalloc.argtypes = [P, P, P, P, P, P, P, F, F, P, P, P, P,
                                                         ctypes.c_int, P, I64, I32, I32]
+            I = ctypes.c_int
+            L.kda_add_rms_norm.restype = I
+            L.kda_add_rms_norm.argtypes = [P, I64, P, I64, I, P, I, F, P, I64, P, I64, P, I64, P,
+                                           I32, I64, I32, P]
+            L.kda_rope_append.restype = I
+            L.kda_rope_append.argtypes = [P, I64, P, I64, P, I64, P, I64, I32, I32, P, P, I64, P,
+                                          P, P, P, I64, I32, I32, SZ]
             _lib = L
     return _lib
 
@@ -452,3 +462,6 @@ def chunk_prefill_fwd_noalloc(q, k, v, g, beta, A_log, dt_bias, lower_bound, sca
     if rc != OK:
         raise KDAError(rc, "kda_chunk_prefill_fwd_noalloc")
     return out, final_state
+
+
+from .layer import add_rms_norm, rope_append, rope_table  # noqa: E402  (uses the names above)

@@ -482,6 +482,7 @@ const char* kda_status_string(int status) {
     case KDA_ERR_BAD_CU_SEQLENS: return "cu_seqlens not non-decreasing from 0 or past total_tokens";
     case KDA_ERR_CUDA: return "CUDA runtime error";
     case KDA_ERR_BAD_OUT_INDEX: return "an out_index entry lies outside [0, out_rows)";
+    case KDA_ERR_BAD_CACHE_INDEX: return "a page index, cache length or position out of its range";
     default: return "unknown status";
   }
 }

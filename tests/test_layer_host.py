@@ -1,0 +1,116 @@
+"""The full-attention layer's C entry points and binding on a host without a GPU: refusals come
+before any device is touched, and the rotation table is the definition's."""
+import ctypes
+import math
+
+import pytest
+import torch
+
+import kda_gated_delta_chunk_gb300 as kda
+from kda_gated_delta_chunk_gb300 import build as kbuild
+from kda_gated_delta_chunk_gb300 import layer
+
+A = 1 << 20        # a 16-byte aligned stand-in for a device pointer: never dereferenced here
+
+
+@pytest.fixture(scope="module")
+def L():
+    kbuild.build()
+    return kda.lib()
+
+
+def norm(L, **over):
+    a = dict(x=A, ldx=64, r=A, ldr=64, rdt=1, w=A, wdt=1, eps=1e-6, ro=A, lds=64, y=A, ldy=64, y8=A,
+             ldy8=64, ys=A, group=128, rows=4, cols=64)
+    a.update(over)
+    return L.kda_add_rms_norm(*a.values(), None)
+
+
+@pytest.mark.parametrize("over", [
+    dict(rows=-1), dict(cols=0), dict(cols=32769, ldx=1 << 20), dict(group=64), dict(wdt=2),
+    dict(rdt=5), dict(eps=float("inf")), dict(w=None), dict(y=None, y8=None, ys=None), dict(ys=None),
+    dict(ro=None), dict(x=None), dict(ldx=63), dict(ldr=63), dict(lds=63), dict(ldy=63), dict(ldy8=63)])
+def test_norm_refuses(L, over):
+    assert norm(L, **over) == kda.ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("over", [dict(x=A + 1), dict(r=A + 2, rdt=0), dict(w=A + 1), dict(ys=A + 2)])
+def test_norm_refuses_misaligned_elements(L, over):
+    assert norm(L, **over) == kda.ERR_MISALIGNED
+
+
+def cache(**over):
+    a = dict(k=A, v=A, k_scale=A, v_scale=A, page_stride=4096, head_stride=2048, token_stride=128,
+             scale_stride=2, num_pages=3, page_size=16, kv_heads=2, max_blocks=4, block_table=A,
+             table_stride=4, kv_lens=A)
+    a.update(over)
+    return layer._Cache(*a.values())
+
+
+def append(L, c=None, **over):
+    a = dict(q=A, qs=512, k=A, ks=256, v=A, vs=256, rope=A, rows=9, rot=32, inter=0, pos=None, qo=A,
+             qos=512, c=ctypes.byref(c if c is not None else cache()), cu=A, ws=A, stream=None, T=4,
+             N=1, H=4, wsb=256)
+    a.update(over)
+    return L.kda_rope_append(*a.values())
+
+
+@pytest.mark.parametrize("over", [
+    dict(page_size=24), dict(page_size=256), dict(num_pages=0), dict(kv_heads=0), dict(max_blocks=-1),
+    dict(table_stride=3), dict(scale_stride=1), dict(token_stride=112), dict(head_stride=64),
+    dict(page_stride=0), dict(page_stride=1 << 40), dict(k=None), dict(v_scale=None),
+    dict(block_table=None), dict(kv_lens=None), dict(max_blocks=1 << 28, table_stride=1 << 28)])
+def test_cache_refusals(L, over):
+    assert append(L, cache(**over)) == kda.ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("over", [dict(k=A + 8), dict(token_stride=136), dict(page_stride=4104),
+                                  dict(k_scale=A + 2), dict(kv_lens=A + 1)])
+def test_cache_alignment(L, over):
+    assert append(L, cache(**over)) == kda.ERR_MISALIGNED
+
+
+@pytest.mark.parametrize("over,code", [
+    (dict(rot=24), kda.ERR_INVALID_ARG), (dict(rot=144), kda.ERR_INVALID_ARG),
+    (dict(rot=-16), kda.ERR_INVALID_ARG), (dict(rope=None), kda.ERR_INVALID_ARG),
+    (dict(rows=0), kda.ERR_INVALID_ARG), (dict(inter=2), kda.ERR_INVALID_ARG),
+    (dict(T=-1), kda.ERR_INVALID_ARG), (dict(N=-1), kda.ERR_INVALID_ARG), (dict(H=0), kda.ERR_INVALID_ARG),
+    (dict(cu=None), kda.ERR_INVALID_ARG), (dict(ws=None), kda.ERR_INVALID_ARG), (dict(k=None), kda.ERR_INVALID_ARG),
+    (dict(qo=None), kda.ERR_INVALID_ARG), (dict(ks=248), kda.ERR_INVALID_ARG), (dict(qos=500), kda.ERR_INVALID_ARG),
+    (dict(ks=260), kda.ERR_MISALIGNED), (dict(rope=A + 4), kda.ERR_MISALIGNED), (dict(v=A + 2), kda.ERR_MISALIGNED),
+    (dict(wsb=128), kda.ERR_WORKSPACE_TOO_SMALL)])
+def test_append_refuses(L, over, code):
+    assert append(L, **over) == code
+
+
+def test_binding_refuses_host_tensors():
+    x = torch.zeros(2, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="CUDA tensor"):
+        kda.add_rms_norm(x, x, x[0])
+    k = torch.zeros(2, 1, 128, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="CUDA tensor"):
+        kda.rope_append(None, k, k, None, k, k, k, k, k, k, torch.zeros(2))
+
+
+def test_rope_table():
+    t = kda.rope_table(50, 32, base=500.0, device="cpu").double()
+    for p in (0, 1, 49):
+        for j in (0, 7, 15):
+            a = p * 500.0 ** (-2 * j / 32)
+            assert abs(t[p, j] - math.cos(a)) < 1e-7 and abs(t[p, 16 + j] - math.sin(a)) < 1e-7
+    lin = kda.rope_table(50, 32, base=500.0, scaling="linear", factor=2.0, device="cpu").double()
+    assert torch.equal(lin[40], t[20])
+    up = kda.rope_table(50, 32, base=500.0, scaling="base", factor=2.0, device="cpu").double()
+    assert torch.equal(up[:, 0], t[:, 0])                       # the highest frequency stays
+    a = 40 * 500.0 ** (-30 / 32) / 2.0                          # the lowest is divided by the factor
+    assert abs(up[40, 15] - math.cos(a)) < 1e-7
+    ramp = kda.rope_table(4096, 128, scaling="ramp", factor=4.0, original_positions=1024,
+                          device="cpu").double()
+    m = 0.1 * math.log(4.0) + 1.0
+    assert abs(ramp[1000, 0] - m * math.cos(1000.0)) < 1e-6     # turns often: as it was
+    a = 1000 * 10000.0 ** (-126 / 128) / 4.0                    # turns less than once: divided
+    assert abs(ramp[1000, 63] - m * math.cos(a)) < 1e-6
+    for bad in (dict(rot_dim=24), dict(rot_dim=0), dict(rot_dim=160), dict(rot_dim=32, scaling="x"),
+                dict(rot_dim=32, scaling="linear", factor=0.5)):
+        with pytest.raises(ValueError):
+            kda.rope_table(8, device="cpu", **bad)
