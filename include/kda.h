@@ -405,6 +405,32 @@ int kda_rope_append(const void* q, int64_t q_stride, const void* k, int64_t k_st
                     int32_t heads, size_t workspace_bytes);
 
 /*
+ * Attention of the new queries over the cache, which holds their own keys and values already:
+ *   s_j = scale * q . k_j     (softcap > 0: s_j = softcap * tanh(s_j / softcap))
+ *   out = sum_j softmax(s)_j v_j     lse = log sum_j exp(s_j)
+ * per token and head, where query i of a sequence with t new tokens sits at position
+ * p = kv_lens - t + i and sees j with max(0, p - window + 1) <= j <= p (window 0: from 0).
+ * Query head h reads kv head h / (heads / kv_heads); heads is a multiple of kv_heads.
+ *   q, out  bf16 [T, heads, 128], strides as in kda_rope_append; out must not overlap q
+ *   lse     fp32 [T, heads] or NULL
+ * A query that sees no key (p < 0) gets a row of zeros and lse = -infinity.  Cache entries that
+ * no query of the sequence sees (slots past the cache length, other pages) may hold anything,
+ * NaN included; an entry that one query does not see does not reach that query's row.
+ * max_q_len: an upper bound of the new tokens of one sequence (host-known); a sequence with
+ * more records KDA_ERR_INVALID_ARG on the device and its rows are not written.  The workspace
+ * holds the status words and partial results: kda_attention_workspace_size() bytes for the
+ * same num_seqs, heads, kv_heads and max_q_len (or larger ones), zero-filled once before its
+ * first use; calls that overlap need one each.  Device errors otherwise as kda_rope_append.
+ */
+size_t kda_attention_workspace_size(int32_t num_seqs, int32_t heads, int32_t kv_heads,
+                                    int32_t max_q_len);
+int kda_cached_attention(const void* q, int64_t q_stride, const kda_kv_cache* cache,
+                         const int32_t* cu_seqlens, float scale, float softcap, int32_t window,
+                         void* out, int64_t out_stride, float* lse, void* workspace,
+                         kda_stream_t stream, int64_t total_tokens, int32_t num_seqs, int32_t heads,
+                         int32_t max_q_len, size_t workspace_bytes);
+
+/*
  * The value-dimension split factor the automatic path uses for a batch of
  * `num_seqs` sequences and `heads` heads on a GPU with `sm_count` SMs.
  * The trigger is PR #52458's: split only when 2 * heads * num_seqs <=

@@ -19,7 +19,7 @@ names follow the C ABI in ``include/kda.h``:
     KERNEL_REF / KERNEL_PIPE
     last_device_status(workspace) -> int
     status_string(code) -> str
-    add_rms_norm, rope_table, rope_append: the full-attention layer beside the KDA layers
+    add_rms_norm, rope_table, rope_append, cached_attention: the full-attention layer beside the KDA layers
         (layer.py)
 
 There is no CPU fallback: if the library is missing or the device is not an
@@ -59,7 +59,8 @@ EXPORTS = ("kda_workspace_size", "kda_chunk_prefill_fwd", "kda_chunk_prefill_fwd
            "kda_device_check", "kda_plan", "kda_plan_for", "kda_chunk_prefill_fwd_strided",
            "kda_recurrent_fwd", "kda_chunk_prefill_fwd_noalloc", "kda_chunk_prefill_fwd_scatter",
            "kda_recurrent_fwd_scatter", "kda_skinny_proj_workspace_size", "kda_skinny_proj",
-           "kda_test_drop_one_record", "kda_add_rms_norm", "kda_rope_append")
+           "kda_test_drop_one_record", "kda_add_rms_norm", "kda_rope_append",
+           "kda_attention_workspace_size", "kda_cached_attention")
 
 _lib = None
 _lock = threading.Lock()
@@ -145,6 +146,11 @@ def lib() -> ctypes.CDLL:
             L.kda_rope_append.restype = I
             L.kda_rope_append.argtypes = [P, I64, P, I64, P, I64, P, I64, I32, I32, P, P, I64, P,
                                           P, P, P, I64, I32, I32, SZ]
+            L.kda_attention_workspace_size.restype = SZ
+            L.kda_attention_workspace_size.argtypes = [I32, I32, I32, I32]
+            L.kda_cached_attention.restype = I
+            L.kda_cached_attention.argtypes = [P, I64, P, P, F, F, I32, P, I64, P, P, P, I64, I32,
+                                               I32, I32, SZ]
             _lib = L
     return _lib
 
@@ -464,4 +470,5 @@ def chunk_prefill_fwd_noalloc(q, k, v, g, beta, A_log, dt_bias, lower_bound, sca
     return out, final_state
 
 
-from .layer import add_rms_norm, rope_append, rope_table  # noqa: E402  (uses the names above)
+from .layer import (add_rms_norm, alloc_attention_workspace,  # noqa: E402  (uses the names above)
+                    attention_workspace_size, cached_attention, rope_append, rope_table)

@@ -111,6 +111,22 @@ struct AppendParams {
 };
 cudaError_t launch_append(const AppendParams& p, cudaStream_t stream);
 
+struct AttnParams {
+  const __nv_bfloat16* q;
+  __nv_bfloat16* out;
+  float* lse;                // [total_tokens, heads] or null
+  int64_t q_stride, out_stride;
+  const int32_t* cu_seqlens;
+  CacheView c;
+  float scale, softcap;      // softcap 0: none
+  int32_t window;            // 0: none
+  int64_t total_tokens;
+  int32_t num_seqs, heads, max_q_len;
+  int* status;               // workspace: 256 bytes of status words, then the partial results
+};
+size_t attn_workspace_bytes(int32_t num_seqs, int32_t heads, int32_t kv_heads, int32_t max_q_len);
+cudaError_t launch_attn(const AttnParams& p, int sms, cudaStream_t stream);
+
 // The sequence that token t belongs to: the last n with cu[n] <= t (cu non-decreasing,
 // cu[0] <= t < cu[N]).
 __device__ __forceinline__ int seq_of(const int32_t* cu, int num_seqs, int64_t t) {

@@ -190,4 +190,51 @@ int kda_rope_append(const void* q, int64_t q_stride, const void* k, int64_t k_st
   return launched(kda::attn::launch_append(p, reinterpret_cast<cudaStream_t>(stream)));
 }
 
+size_t kda_attention_workspace_size(int32_t num_seqs, int32_t heads, int32_t kv_heads,
+                                    int32_t max_q_len) {
+  if (num_seqs < 0 || heads < 1 || kv_heads < 1 || heads % kv_heads != 0 || max_q_len < 0) return 0;
+  return (kda::attn::attn_workspace_bytes(num_seqs, heads, kv_heads, max_q_len) + 15) & ~(size_t)15;
+}
+
+int kda_cached_attention(const void* q, int64_t q_stride, const kda_kv_cache* cache,
+                         const int32_t* cu_seqlens, float scale, float softcap, int32_t window,
+                         void* out, int64_t out_stride, float* lse, void* workspace,
+                         kda_stream_t stream, int64_t total_tokens, int32_t num_seqs, int32_t heads,
+                         int32_t max_q_len, size_t workspace_bytes) {
+  kda::attn::AttnParams p{};
+  int rc = check_batch(cu_seqlens, workspace, total_tokens, num_seqs, heads, workspace_bytes);
+  if (rc != KDA_OK) return rc;
+  rc = check_cache(cache, num_seqs, &p.c);
+  if (rc != KDA_OK) return rc;
+  if (heads % cache->kv_heads != 0 || max_q_len < 0 || window < 0) return KDA_ERR_INVALID_ARG;
+  if (!std::isfinite(scale) || !std::isfinite(softcap) || softcap < 0.0f) return KDA_ERR_INVALID_ARG;
+  if (total_tokens > 0) {
+    if ((rc = check_rows(q, q_stride, heads)) != KDA_OK) return rc;
+    if ((rc = check_rows(out, out_stride, heads)) != KDA_OK) return rc;
+    if (max_q_len < 1) return KDA_ERR_INVALID_ARG;
+  }
+  if (!aligned(lse, 4)) return KDA_ERR_MISALIGNED;
+  if (workspace_bytes < kda::attn::attn_workspace_bytes(num_seqs, heads, cache->kv_heads, max_q_len))
+    return KDA_ERR_WORKSPACE_TOO_SMALL;
+  int sms = 0;
+  rc = current_device(&sms);
+  if (rc != KDA_OK) return rc;
+  if (num_seqs == 0 || total_tokens == 0) return KDA_OK;
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.out = static_cast<__nv_bfloat16*>(out);
+  p.lse = lse;
+  p.q_stride = q_stride;
+  p.out_stride = out_stride;
+  p.cu_seqlens = cu_seqlens;
+  p.scale = scale;
+  p.softcap = softcap;
+  p.window = window;
+  p.total_tokens = total_tokens;
+  p.num_seqs = num_seqs;
+  p.heads = heads;
+  p.max_q_len = max_q_len;
+  p.status = static_cast<int*>(workspace);
+  return launched(kda::attn::launch_attn(p, sms, reinterpret_cast<cudaStream_t>(stream)));
+}
+
 }  // extern "C"

@@ -1,4 +1,5 @@
-"""The full-attention layer's operators: residual norm, rotary append to a paged 8-bit cache.
+"""The full-attention layer's operators: residual norm, rotary append to a paged 8-bit cache,
+attention over that cache.
 
 The calls of ``include/kda.h``'s section on the full-attention layer, on torch tensors; like
 the rest of the binding, marshalling only.  A cache is four tensors and two indexes:
@@ -250,3 +251,60 @@ def rope_append(q, k, v, rope, k_cache, v_cache, k_scale, v_scale, block_table, 
     if rc != OK:
         raise KDAError(rc, "kda_rope_append")
     return q_out
+
+
+def attention_workspace_size(num_seqs: int, heads: int, kv_heads: int, max_q_len: int) -> int:
+    return int(lib().kda_attention_workspace_size(int(num_seqs), int(heads), int(kv_heads),
+                                                  int(max_q_len)))
+
+
+def alloc_attention_workspace(num_seqs: int, heads: int, kv_heads: int, max_q_len: int,
+                              device=None) -> torch.Tensor:
+    """A zero-filled uint8 workspace for ``cached_attention``."""
+    n = attention_workspace_size(num_seqs, heads, kv_heads, max_q_len)
+    return torch.zeros(max(n, 256), dtype=torch.uint8, device=device or "cuda")
+
+
+def cached_attention(q, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, cu_seqlens,
+                     scale: float, max_q_len: int, softcap: float = 0.0, window: int = 0,
+                     out=None, lse=False, workspace=None, stream=None):
+    """Run ``kda_cached_attention``: causal attention of the new queries over the cache.
+
+    q: bf16 [T, heads, 128]; cu_seqlens: int32 [num_seqs + 1]; max_q_len: an upper bound of one
+    sequence's new tokens.  softcap > 0 caps the scores by softcap * tanh(s / softcap); window >
+    0 limits each query to the last ``window`` positions, its own included.  lse: False, True
+    (allocate fp32 [T, heads]) or a tensor.  workspace: ``alloc_attention_workspace`` of the same
+    sizes or larger ones.  Returns (out, lse or None).
+    """
+    if q.dim() != 3:
+        raise ValueError("q must be [T, heads, 128]")
+    dev = q.device
+    T, heads, d = q.shape
+    if d != HEAD_DIM:
+        raise KDAError(ERR_INVALID_ARG, f"head_dim {d} (only {HEAD_DIM} is supported)")
+    N = cu_seqlens.numel() - 1
+    _check(q, "q", (_BF16,), q.shape, None)
+    _check(cu_seqlens, "cu_seqlens", (torch.int32,), (N + 1,), dev, 0)
+    c = _cache(k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, N, dev)
+    if out is None:
+        out = torch.empty((T, heads, d), dtype=_BF16, device=dev)
+    else:
+        _check(out, "out", (_BF16,), q.shape, dev)
+    if lse is True:
+        lse = torch.empty((T, heads), dtype=_F32, device=dev)
+    elif lse is False:
+        lse = None
+    else:
+        _check(lse, "lse", (_F32,), (T, heads), dev, 0)
+    if workspace is None:
+        workspace = alloc_attention_workspace(N, heads, c.kv_heads, max_q_len, dev)
+    else:
+        _check(workspace, "workspace", (torch.uint8,), workspace.shape, dev, 0)
+    rc = lib().kda_cached_attention(
+        q.data_ptr(), _row_stride(q, heads * d), ctypes.byref(c), cu_seqlens.data_ptr(), scale,
+        softcap, window, out.data_ptr(), _row_stride(out, heads * d),
+        None if lse is None else lse.data_ptr(), workspace.data_ptr(), _stream(stream, dev), T, N,
+        heads, max_q_len, workspace.numel())
+    if rc != OK:
+        raise KDAError(rc, "kda_cached_attention")
+    return out, lse

@@ -114,3 +114,29 @@ def test_rope_table():
                 dict(rot_dim=32, scaling="linear", factor=0.5)):
         with pytest.raises(ValueError):
             kda.rope_table(8, device="cpu", **bad)
+
+
+def attend(L, c=None, **over):
+    a = dict(q=A, qs=512, c=ctypes.byref(c if c is not None else cache()), cu=A, scale=0.1, cap=0.0,
+             window=0, o=A, os=512, lse=A, ws=A, stream=None, T=4, N=1, H=4, mq=4, wsb=1 << 30)
+    a.update(over)
+    return L.kda_cached_attention(*a.values())
+
+
+@pytest.mark.parametrize("over,code", [
+    (dict(H=3, qs=512), kda.ERR_INVALID_ARG), (dict(mq=0), kda.ERR_INVALID_ARG),
+    (dict(mq=-1), kda.ERR_INVALID_ARG), (dict(window=-1), kda.ERR_INVALID_ARG),
+    (dict(scale=float("nan")), kda.ERR_INVALID_ARG), (dict(cap=-0.5), kda.ERR_INVALID_ARG),
+    (dict(q=None), kda.ERR_INVALID_ARG), (dict(o=None), kda.ERR_INVALID_ARG), (dict(qs=504), kda.ERR_INVALID_ARG),
+    (dict(os=516), kda.ERR_MISALIGNED), (dict(q=A + 8), kda.ERR_MISALIGNED), (dict(lse=A + 2), kda.ERR_MISALIGNED),
+    (dict(wsb=0), kda.ERR_WORKSPACE_TOO_SMALL)])
+def test_attention_refuses(L, over, code):
+    assert attend(L, **over) == code
+
+
+def test_attention_workspace_size(L):
+    assert kda.attention_workspace_size(-1, 8, 2, 1) == 0
+    assert kda.attention_workspace_size(1, 8, 3, 1) == 0
+    a = kda.attention_workspace_size(4, 8, 2, 1)
+    assert a >= 256 and a % 16 == 0
+    assert L.kda_cached_attention is not None
