@@ -127,6 +127,11 @@ struct AttnParams {
 size_t attn_workspace_bytes(int32_t num_seqs, int32_t heads, int32_t kv_heads, int32_t max_q_len);
 cudaError_t launch_attn(const AttnParams& p, int sms, cudaStream_t stream);
 
+// Sequences with min_rows <= new tokens x heads per kv head <= max_rows (at most 32).
+size_t decode_workspace_bytes(int sms);
+cudaError_t launch_attn_decode(const AttnParams& p, int min_rows, int max_rows, void* work, int sms,
+                               cudaStream_t stream);
+
 // The sequence that token t belongs to: the last n with cu[n] <= t (cu non-decreasing,
 // cu[0] <= t < cu[N]).
 __device__ __forceinline__ int seq_of(const int32_t* cu, int num_seqs, int64_t t) {

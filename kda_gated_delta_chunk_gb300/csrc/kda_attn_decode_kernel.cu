@@ -1,0 +1,726 @@
+// Attention over the paged e4m3 cache for few query rows (decode, speculative verify): up to 32
+// rows -- new tokens x query heads of one kv head -- share a pass over the keys.  For a tile of
+// 128 keys, on tcgen05 with the e4m3 cache as it lies in memory as the A operand of both
+// products (nothing of the cache is converted):
+//   S^T  = K8 [q1; q2]^T     M = 128 keys, N = 2 x rows: q = q1 + q2, two e4m3 terms
+//   P^T  = softmax numerators, thread = key, written as two e4m3 terms
+//   O^T  = V8^T [P1; P2]^T   M = 128 channels (V read MN-major), N = 2 x rows
+// Two e4m3 terms hold the 8 significant bits of a bf16 query exactly (relative to the row's
+// largest entry: to 2^-18), and a numerator to 2^-8 of itself or 2^-18 of the tile's largest: a
+// tile's P is scaled by its own maximum, and O^T is added to fp32 registers (thread = channel)
+// with the factor to the running maximum, so no tile loses range to an earlier one.  The value
+// scale of a key's page enters the exponent, max and all (P = 2^(s + log2 v_scale - max)), and
+// leaves again in the sum of the denominators, which takes the unrounded fp32 numerators.
+//
+// Bound by the cache's bytes (2 x 128 per key and kv head; the products take a few percent of the
+// tensor cores).  So that every SM streams the same amount whatever the lengths, the tiles
+// of all (sequence, kv head) items are laid end to end and cut into one equal range per CTA, two
+// CTAs per SM, each with three 32 KB stages in flight.  A CTA's range covers the end of one
+// item, whole items and the beginning of another; the (at most two) partial results go to the
+// workspace and a second kernel, launched as the first's programmatic dependent, merges them.
+//
+// Warps: 0-3 softmax and accumulation, 4 the TMA producer, 5 the MMA issuer.  Every wait is
+// bounded; one that gives up records KDA_ERR_DEVICE_TIMEOUT and the CTA leaves.
+//
+// Masked entries: scores by selection; a V row that no query sees (past the length, before every
+// window) is zeroed in shared memory before the product, since 0 x NaN is NaN; a NaN in a row that
+// only some of the queries see is zeroed too and put into those queries' sums by hand.
+#include "kda_attn_tc.cuh"
+
+namespace kda {
+namespace attn {
+namespace {
+
+constexpr int kThreads = 192;
+constexpr int kStageBytes = 2 * kTile * kHeadDim;   // K and V
+constexpr float kPScale = 256.0f;                    // largest numerator, in the e4m3 operand
+
+template <int NR>
+struct Cfg {
+  static constexpr int kN = 2 * NR;                  // MMA N: both terms
+  static constexpr int kStages = NR <= 16 ? 3 : 2;   // what leaves room for two CTAs an SM
+  static constexpr uint32_t kTmemCols = kN * 3 <= 64 ? 64 : (kN * 3 <= 128 ? 128 : 256);
+  static constexpr uint32_t kTO = 2 * kN;            // S in columns [0, 2 kN), O after it
+  // shared memory, from a 1024-byte aligned base
+  static constexpr int kOffQ = kStages * kStageBytes;
+  static constexpr int kOffP = kOffQ + kN * 128;
+  static constexpr int kOffFac = kOffP + kN * 128;              // float4 [2][4 warps][NR]
+  static constexpr int kOffMax = kOffFac + 2 * 4 * NR * 16;     // float [2][NR][4]
+  static constexpr int kOffSum = kOffMax + 2 * NR * 16;         // float [NR][4]
+  static constexpr int kOffPoison = kOffSum + NR * 16;          // uint4 [2][128]
+  static constexpr int kOffQmul = kOffPoison + 2 * 128 * 16;    // float [NR]
+  static constexpr int kOffScale = kOffQmul + NR * 4;           // float [stages][2][8]
+  static constexpr int kOffBar = kOffScale + kStages * 64;      // full, empty, s[2], o, p, q, end
+  static constexpr int kOffMisc = kOffBar + 8 * (2 * kStages + 6);
+  static constexpr int kBytes = kOffMisc + 128 + 1024;
+};
+
+// Workspace after the status words: desc [ctas], then per CTA two slots of [NR][128] sums,
+// [NR] maxima and [NR] denominators.
+struct PartDesc {
+  int n, h, parts, pad;
+};
+template <int NR>
+constexpr int kSlotFloats = NR * 130;
+
+struct DecodeParams {
+  AttnParams a;
+  CacheMaps maps;
+  int min_rows, max_rows;
+  PartDesc* desc;
+  float* slots;
+};
+
+// The walk over a CTA's range of tiles, segment by segment (every role runs its own).
+struct Walk {
+  int64_t pos, end, base;   // global tile index; base: of sequence n's first
+  int n;
+  SeqInfo s;
+  int h, a, b;              // segment: kv head, tiles [a, b) of the item (relative to tile0)
+  __device__ __forceinline__ bool next(const DecodeParams& p) {
+    if (pos >= end) return false;
+    while (true) {
+      const int64_t size = (int64_t)s.tiles * p.a.c.kv_heads;
+      if (pos < base + size) break;
+      base += size;
+      int err;
+      if (++n >= p.a.num_seqs) return false;   // (lengths that changed under the kernel)
+      s = seq_info(p.a, n, p.min_rows, p.max_rows, &err);
+    }
+    const int64_t x = pos - base;
+    h = (int)(x / s.tiles);
+    a = (int)(x % s.tiles);
+    b = (int)min((int64_t)s.tiles, a + (end - pos));
+    pos += b - a;
+    return true;
+  }
+};
+
+template <int NR, bool kCap>
+__global__ void __launch_bounds__(kThreads, 2)
+    kda_attn_decode_kernel(const __grid_constant__ DecodeParams p) {
+  using C = Cfg<NR>;
+  constexpr int kStages = C::kStages;
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  unsigned char* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  const uint32_t sb = smem_u32(sm);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t bar_full = sb + C::kOffBar, bar_empty = bar_full + 8 * kStages;
+  const uint32_t bar_s = bar_empty + 8 * kStages, bar_o = bar_s + 16, bar_p = bar_o + 8, bar_q = bar_p + 8,
+                 bar_end = bar_q + 8;
+  struct Misc {
+    long long part[8];
+    long long total, start_base;
+    int start_n;
+    uint32_t tmem;
+  };
+  Misc* misc = reinterpret_cast<Misc*>(sm + C::kOffMisc);
+  static_assert(sizeof(Misc) <= 128, "misc");
+  const int hk = p.a.c.kv_heads, N = p.a.num_seqs, G = p.a.heads / hk, P = p.a.c.page_size;
+
+  if (tid == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(bar_full + 8 * i, 1);
+      mbar_init(bar_empty + 8 * i, 1);
+    }
+    mbar_init(bar_s, 1);
+    mbar_init(bar_s + 8, 1);
+    mbar_init(bar_o, 1);
+    mbar_init(bar_p, 128);
+    mbar_init(bar_q, 128);
+    mbar_init(bar_end, 1);
+    mbar_fence_init();
+    tma_prefetch_desc(&p.maps.k);
+    tma_prefetch_desc(&p.maps.v);
+    if (blockIdx.x == 0 && p.a.cu_seqlens[0] != 0) record_error(p.a.status, KDA_ERR_BAD_CU_SEQLENS, 310);
+  }
+  if (warp == 5) {
+    tmem_alloc(smem_u32(&misc->tmem), C::kTmemCols);
+    tmem_relinquish();
+  }
+  pdl_launch_dependents();
+
+  // ---- this CTA's range: total tiles, then the sequence its first tile lies in
+  auto cost = [&](int n, bool report) -> long long {
+    if (n >= N) return 0;
+    int err;
+    const SeqInfo s = seq_info(p.a, n, p.min_rows, p.max_rows, &err);
+    if (err != KDA_OK && report && blockIdx.x == 0) record_error(p.a.status, err, 311);
+    return (long long)s.tiles * hk;
+  };
+  long long mine = 0, first = 0;
+  for (int n0 = 0; n0 < N; n0 += kThreads) {
+    const long long w = cost(n0 + tid, true);
+    if (n0 == 0) first = w;
+    mine += w;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+  if (lane == 0) misc->part[warp] = mine;
+  __syncthreads();
+  long long total = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) total += misc->part[w];
+  __syncthreads();
+  Walk walk;
+  walk.pos = (int64_t)blockIdx.x * total / gridDim.x;
+  walk.end = (int64_t)(blockIdx.x + 1) * total / gridDim.x;
+  if (walk.pos < walk.end) {
+    long long before = 0;
+    for (int n0 = 0; n0 < N; n0 += kThreads) {
+      const long long w = n0 == 0 ? first : cost(n0 + tid, false);
+      long long inc = w;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long u = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += u;
+      }
+      if (lane == 31) misc->part[warp] = inc;
+      __syncthreads();
+      long long off = before;
+      for (int x = 0; x < warp; ++x) off += misc->part[x];
+      if (w > 0 && walk.pos >= off + inc - w && walk.pos < off + inc) {
+        misc->start_n = n0 + tid;
+        misc->start_base = off + inc - w;
+      }
+      for (int x = 0; x < kThreads / 32; ++x) before += misc->part[x];
+      __syncthreads();
+      if (before > walk.pos) break;
+    }
+    walk.n = misc->start_n;
+    walk.base = misc->start_base;
+    int err;
+    walk.s = seq_info(p.a, walk.n, p.min_rows, p.max_rows, &err);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = misc->tmem;
+
+  if (warp == 4) {
+    // ================= producer: pages of each tile, K and V of one head
+    uint32_t it = 0;
+    bool ok = true;
+    while (ok && walk.next(p)) {
+      const int32_t* bt = p.a.c.block_table + walk.n * p.a.c.table_stride;
+      const int boxes = kTile / P;                     // pages of a tile
+      const int used = (walk.s.len + P - 1) / P;       // pages of the sequence
+      // lanes below `boxes`: this tile's page (one tile ahead), with its scales
+      auto page_of = [&](int t) -> int {
+        const int b = (walk.s.tile0 + t) * boxes + lane;
+        if (lane >= boxes || t >= walk.b || b >= used) return -2;     // not loaded
+        const int pg = bt[b];
+        if (pg < 0 || pg >= p.a.c.num_pages) {
+          record_error(p.a.status, KDA_ERR_BAD_CACHE_INDEX, 312);
+          return p.a.c.num_pages;                      // outside the map: the load gives zeros
+        }
+        return pg;
+      };
+      auto scale_of = [&](const float* sc, int pg) -> float {
+        return pg >= 0 && pg < p.a.c.num_pages ? sc[(int64_t)pg * p.a.c.scale_stride + walk.h] : 1.0f;
+      };
+      int pg = page_of(walk.a);
+      for (int t = walk.a; t < walk.b && ok; ++t, ++it) {
+        const uint32_t st = it % kStages;
+        const float ks = scale_of(p.a.c.k_scale, pg), vs = scale_of(p.a.c.v_scale, pg);
+        const int pg_next = page_of(t + 1);
+        if (it >= kStages) ok = mbar_wait(bar_empty + 8 * st, (it / kStages - 1) & 1);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) {
+          if (lane == 0) record_error(p.a.status, KDA_ERR_DEVICE_TIMEOUT, 313);
+          break;
+        }
+        const uint32_t dst = sb + st * kStageBytes;
+        if (lane < boxes) {
+          float* sc = reinterpret_cast<float*>(sm + C::kOffScale + st * 64);
+          sc[lane] = ks;
+          sc[8 + lane] = vs;
+        }
+        const uint32_t loads = __popc(__ballot_sync(0xffffffffu, pg != -2));
+        __syncwarp();
+        if (lane == 0) mbar_expect_tx(bar_full + 8 * st, loads * 2 * P * kHeadDim);
+        __syncwarp();
+        if (pg != -2) {
+          tma_load_4d(dst + lane * P * 128, &p.maps.k, 0, 0, walk.h, pg, bar_full + 8 * st);
+          tma_load_4d(dst + kTile * 128 + lane * P * 128, &p.maps.v, 0, 0, walk.h, pg, bar_full + 8 * st);
+        }
+        pg = pg_next;
+      }
+    }
+    // the copies in flight end before the CTA does
+    for (uint32_t i = it > kStages ? it - kStages : 0; i < it; ++i)
+      mbar_wait(bar_full + 8 * (i % kStages), (i / kStages) & 1);
+  } else if (warp == 5) {
+    // ================= MMA issuer
+    if (elect_one()) {
+      constexpr uint32_t id_s = idesc_e4m3(128, C::kN, 0, 0), id_o = idesc_e4m3(128, C::kN, 1, 0);
+      uint32_t it = 0, seg = 0;
+      bool ok = true;
+      auto pv = [&](uint32_t i) {       // O^T of tile i, once its P is written
+        ok = mbar_wait(bar_p, i & 1);
+        if (!ok) return;
+        tc_fence_after();
+        const uint32_t v = sb + (i % kStages) * kStageBytes + kTile * 128;
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks)
+          mma_e4m3(tmem + C::kTO, mnmajor8(v, ks), kmajor8(sb + C::kOffP, ks), id_o, ks > 0);
+        mma_commit(bar_o);
+        mma_commit(bar_empty + 8 * (i % kStages));
+      };
+      while (ok && walk.next(p)) {
+        ok = mbar_wait(bar_q, seg & 1);
+        ++seg;
+        for (int t = walk.a; t < walk.b && ok; ++t, ++it) {
+          ok = mbar_wait(bar_full + 8 * (it % kStages), (it / kStages) & 1);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t k = sb + (it % kStages) * kStageBytes;
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks)
+            mma_e4m3(tmem + (it & 1) * C::kN, kmajor8(k, ks), kmajor8(sb + C::kOffQ, ks), id_s, ks > 0);
+          mma_commit(bar_s + 8 * (it & 1));
+          if (t > walk.a) pv(it - 1);
+        }
+        if (ok) pv(it - 1);
+      }
+      if (!ok) record_error(p.a.status, KDA_ERR_DEVICE_TIMEOUT, 314);
+      // what was issued ends, its arrivals included, before shared and tensor memory go
+      mma_commit(bar_end);
+      mbar_wait(bar_end, 0);
+      for (uint32_t i = it > kStages ? it - kStages : 0; ok && i < it; ++i)
+        mbar_wait(bar_empty + 8 * (i % kStages), (i / kStages) & 1);
+    }
+    __syncwarp();
+  } else {
+    // ================= softmax and accumulation: thread = key of S^T, channel of O^T
+    const uint32_t lane_base = (uint32_t)(32 * warp) << 16;
+    float4* fac = reinterpret_cast<float4*>(sm + C::kOffFac);     // [2][4][NR]: max, f1, f2
+    float* wmax = reinterpret_cast<float*>(sm + C::kOffMax);      // [2][NR][4]
+    float* sums = reinterpret_cast<float*>(sm + C::kOffSum);
+    uint4* poison = reinterpret_cast<uint4*>(sm + C::kOffPoison);
+    float* qmul = reinterpret_cast<float*>(sm + C::kOffQmul);
+    const float cap2 = kCap ? 2.0f * kLog2e / p.a.softcap : 0.0f, cap1 = kCap ? p.a.softcap * kLog2e : 0.0f;
+    PartDesc part = {0, 0, 0, 0};
+    uint32_t it = 0;
+    bool ok = true;
+    while (walk.next(p)) {
+      const int rows = walk.s.q_len * G;
+      const int first_pos = walk.s.len - walk.s.q_len;   // position of query 0
+      // ---- queries: two e4m3 terms each, 16 lanes a row
+#pragma unroll
+      for (int r0 = 0; r0 < NR; r0 += 8) {
+        const int r = r0 + (tid >> 4), c = tid & 15;
+        float x[8];
+        float top = 0.0f;
+        if (r < rows) {
+          const int i = r / G, g = r % G;
+          unpack8(*reinterpret_cast<const uint4*>(p.a.q + (int64_t)(walk.s.tok0 + i) * p.a.q_stride +
+                                                  (walk.h * G + g) * kHeadDim + 8 * c), x);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[e] = 0.0f;
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) top = max_nan(top, fabsf(x[e]));
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
+        // a power of two that brings the row's largest entry into (224, 448]
+        const int e2 = (int)((__float_as_uint(top) >> 23) & 255) - 127 - 8 +
+                       ((__float_as_uint(top) & 0x7fffffu) > 0x600000u ? 1 : 0);
+        const int e2c = max(e2, -100);
+        const float inv = __uint_as_float((uint32_t)(127 - e2c) << 23);
+        float y1[8], y2[8];
+        uint32_t w1[2], w2[2];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y1[e] = x[e] * inv;
+        w1[0] = e4m3x4(y1[0], y1[1], y1[2], y1[3]);
+        w1[1] = e4m3x4(y1[4], y1[5], y1[6], y1[7]);
+#pragma unroll
+        for (int e = 0; e < 8; e += 2) {
+          const float2 b = from_e4m3x2((w1[e >> 2] >> (8 * (e & 3))) & 0xffff);
+          y2[e] = y1[e] - b.x;
+          y2[e + 1] = y1[e + 1] - b.y;
+        }
+        w2[0] = e4m3x4(y2[0], y2[1], y2[2], y2[3]);
+        w2[1] = e4m3x4(y2[4], y2[5], y2[6], y2[7]);
+        *reinterpret_cast<uint2*>(sm + C::kOffQ + tile_off(r, 8 * c)) = make_uint2(w1[0], w1[1]);
+        *reinterpret_cast<uint2*>(sm + C::kOffQ + tile_off(NR + r, 8 * c)) = make_uint2(w2[0], w2[1]);
+        if (c == 0) {   // a non-finite query makes its row NaN
+          const float sq = top <= 3.402823466e38f ? __uint_as_float((uint32_t)(127 + e2c) << 23) : NAN;
+          qmul[r] = sq * p.a.scale * (kCap ? 1.0f : kLog2e);
+        }
+      }
+      fence_proxy_async();
+      mbar_arrive(bar_q);
+      if (bar_any(1, 128, !ok)) { ok = false; break; }   // qmul is written (and nobody gave up)
+
+      float acc[NR], l[NR];
+#pragma unroll
+      for (int r = 0; r < NR; ++r) acc[r] = l[r] = 0.0f;
+      float run = -INFINITY;         // lane r: running maximum of row r
+      bool poisoned = false;         // the tile before has NaN entries that some rows do not see
+      // O^T of tile i added to the sums (its factors and poison words: parity i & 1)
+      auto add_o = [&](uint32_t i, int t) {
+        ok = mbar_wait(bar_o, i & 1) && ok;
+        tc_fence_after();
+        const float4* f = fac + ((i & 1) * 4 + warp) * NR;
+        if (NR <= 16) {
+          uint32_t o[C::kN <= 16 ? 16 : 32];
+          if constexpr (C::kN <= 16) tmem_ld16(tmem + lane_base + C::kTO, o);
+          else tmem_ld32(tmem + lane_base + C::kTO, o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int r = 0; r < NR; ++r) {
+            const float4 c = f[r];
+            acc[r] = acc[r] * c.y + (__uint_as_float(o[r]) + __uint_as_float(o[NR + r])) * c.z;
+          }
+        } else {
+#pragma unroll
+          for (int q = 0; q < NR; q += 16) {
+            uint32_t o1[16], o2[16];
+            tmem_ld16(tmem + lane_base + C::kTO + q, o1);
+            tmem_ld16(tmem + lane_base + C::kTO + NR + q, o2);
+            tmem_wait_ld();
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+              const float4 c = f[q + r];
+              acc[q + r] = acc[q + r] * c.y + (__uint_as_float(o1[r]) + __uint_as_float(o2[r])) * c.z;
+            }
+          }
+        }
+        if (poisoned) {
+          const uint32_t* w = reinterpret_cast<const uint32_t*>(poison + (i & 1) * 128);
+          for (int x = 0; x < kTile; ++x) {
+            if (!((w[4 * x + warp] >> lane) & 1)) continue;
+            const int key = (walk.s.tile0 + t) * kTile + x;
+#pragma unroll
+            for (int r = 0; r < NR; ++r) {
+              const int pos = first_pos + r / G;
+              if (key <= pos && (p.a.window <= 0 || key > pos - p.a.window)) acc[r] = NAN;
+            }
+          }
+        }
+      };
+      for (int t = walk.a; t < walk.b; ++t, ++it) {
+        const uint32_t par = it & 1, st = it % kStages;
+        ok = mbar_wait(bar_s + 8 * par, (it >> 1) & 1) && ok;
+        ok = mbar_wait(bar_full + 8 * st, (it / kStages) & 1) && ok;   // (V is read here too)
+        tc_fence_after();
+        const int key0 = (walk.s.tile0 + t) * kTile, key = key0 + tid;
+        // some key of the tile is hidden from some row
+        const bool masked = key0 + kTile - 1 > first_pos ||
+                            (p.a.window > 0 && key0 <= walk.s.len - 1 - p.a.window);
+        const float* sc = reinterpret_cast<const float*>(sm + C::kOffScale + st * 64);
+        float ks = 1.0f, vs = 1.0f;
+        if (key < walk.s.len) {
+          ks = sc[tid / P];
+          vs = sc[8 + tid / P];
+        }
+        const float lvs = lg2(vs), ivs = __fdividef(1.0f / kPScale, vs);
+        float x[NR];
+        if (NR <= 16) {
+          uint32_t o[C::kN <= 16 ? 16 : 32];
+          if constexpr (C::kN <= 16) tmem_ld16(tmem + lane_base + par * C::kN, o);
+          else tmem_ld32(tmem + lane_base + par * C::kN, o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int r = 0; r < NR; ++r) x[r] = __uint_as_float(o[r]) + __uint_as_float(o[NR + r]);
+        } else {
+#pragma unroll
+          for (int q = 0; q < NR; q += 16) {
+            uint32_t o1[16], o2[16];
+            tmem_ld16(tmem + lane_base + par * C::kN + q, o1);
+            tmem_ld16(tmem + lane_base + par * C::kN + NR + q, o2);
+            tmem_wait_ld();
+#pragma unroll
+            for (int r = 0; r < 16; ++r) x[q + r] = __uint_as_float(o1[r]) + __uint_as_float(o2[r]);
+          }
+        }
+#pragma unroll
+        for (int r = 0; r < NR; r += 4) {
+          const float4 m4 = *reinterpret_cast<const float4*>(qmul + r);
+          const float m[4] = {m4.x, m4.y, m4.z, m4.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float s = x[r + e] * (m[e] * ks);
+            x[r + e] = (kCap ? cap_score(s, cap2, cap1) : s) + lvs;
+          }
+        }
+        bool hidden_nan = false;
+        if (masked) {
+          bool all = true, any = false;
+          for (int i = 0; i < walk.s.q_len; ++i) {
+            const int pos = first_pos + i;
+            const bool see = key <= pos && (p.a.window <= 0 || key > pos - p.a.window);
+            all = all && see;
+            any = any || see;
+          }
+          unsigned char* vrow = sm + st * kStageBytes + kTile * 128 + (tid >> 3) * 1024 + (tid & 7) * 128;
+          if (!any) {
+#pragma unroll
+            for (int c = 0; c < 8; ++c) reinterpret_cast<uint4*>(vrow)[c] = make_uint4(0, 0, 0, 0);
+          }
+          if (walk.s.q_len > 1) {   // NaN channels of a row that some queries see and others do not
+            uint32_t bits[4] = {0, 0, 0, 0};
+            if (any && !all) {
+#pragma unroll
+              for (int c = 0; c < 8; ++c) {
+                uint4* chunk = reinterpret_cast<uint4*>(vrow) + (c ^ (tid & 7));
+                const uint4 u = *chunk;
+                const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+                uint32_t nan[4], some = 0;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  nan[e] = __vcmpeq4(w[e] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                  some |= nan[e];
+#pragma unroll
+                  for (int b = 0; b < 4; ++b)
+                    bits[c >> 1] |= ((nan[e] >> (8 * b)) & 1u) << (16 * (c & 1) + 4 * e + b);
+                }
+                if (some) *chunk = make_uint4(w[0] & ~nan[0], w[1] & ~nan[1], w[2] & ~nan[2], w[3] & ~nan[3]);
+              }
+            }
+            poison[par * 128 + tid] = make_uint4(bits[0], bits[1], bits[2], bits[3]);
+            hidden_nan = (bits[0] | bits[1] | bits[2] | bits[3]) != 0;
+          }
+#pragma unroll
+          for (int r = 0; r < NR; ++r) {
+            const int pos = first_pos + r / G;
+            if (!(key <= pos && (p.a.window <= 0 || key > pos - p.a.window))) x[r] = -INFINITY;
+          }
+        }
+        // ---- the tile's maxima: the warp's by redux, the four warps' through shared memory
+        float mine_max = -INFINITY;
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+          const float m = warp_max(x[r]);
+          if (lane == r) mine_max = m;
+        }
+        if (lane < NR) wmax[(par * NR + lane) * 4 + warp] = mine_max;
+        if (bar_any(1, 128, !ok)) { ok = false; break; }
+        if (lane < NR) {
+          const float4 w = *reinterpret_cast<const float4*>(wmax + (par * NR + lane) * 4);
+          const float m = fmaxf(fmaxf(w.x, w.y), fmaxf(w.z, w.w));
+          const float next = fmaxf(run, m), ref = next == -INFINITY ? 0.0f : next;
+          fac[(par * 4 + warp) * NR + lane] =
+              make_float4(m == -INFINITY ? 0.0f : m, ex2(run - ref), ex2(m - ref) * (1.0f / kPScale), 0.0f);
+          run = next;
+        }
+        const bool poison_now = masked && walk.s.q_len > 1 && bar_any(2, 128, hidden_nan);
+        __syncwarp();
+        // ---- numerators and denominators
+        const float4* f = fac + (par * 4 + warp) * NR;
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+          const float4 c = f[r];
+          x[r] = ex2(x[r] - c.x) * kPScale;
+          l[r] = l[r] * c.y + x[r] * (ivs * kPScale) * c.z;
+        }
+        // ---- O of the tile before, whose P operand this one replaces
+        if (t > walk.a) add_o(it - 1, t - 1);
+        poisoned = poison_now;
+        unsigned char* pt = sm + C::kOffP;
+#pragma unroll
+        for (int r = 0; r < NR; r += 2) {
+          const uint32_t q1 = e4m3x2(x[r], x[r + 1]);
+          const float2 b = from_e4m3x2(q1);
+          const uint32_t q2 = e4m3x2(x[r] - b.x, x[r + 1] - b.y);
+          pt[tile_off(r, tid)] = (unsigned char)q1;
+          pt[tile_off(r + 1, tid)] = (unsigned char)(q1 >> 8);
+          pt[tile_off(NR + r, tid)] = (unsigned char)q2;
+          pt[tile_off(NR + r + 1, tid)] = (unsigned char)(q2 >> 8);
+        }
+        tc_fence_before();
+        fence_proxy_async();
+        mbar_arrive(bar_p);
+      }
+      if (!ok) break;
+      add_o(it - 1, walk.b - 1);
+      // ---- denominators over the 128 key threads
+      // (each step exchanges half of the rows: after log2 NR steps a lane holds row lane * NR / 32)
+#pragma unroll
+      for (int o = 16, n = NR / 2; o > 0; o >>= 1, n >>= 1) {
+        if (n >= 1) {
+#pragma unroll
+          for (int k = 0; k < n; ++k) {
+            const float keep = (lane & o) ? l[k + n] : l[k], send = (lane & o) ? l[k] : l[k + n];
+            l[k] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+          }
+        } else {
+          l[0] += __shfl_xor_sync(0xffffffffu, l[0], o);
+        }
+      }
+      if (lane % (32 / NR) == 0) sums[(lane / (32 / NR)) * 4 + warp] = l[0];
+      if (bar_any(1, 128, !ok)) { ok = false; break; }
+      float den = 0.0f;     // lane r: row r's, the same in every warp
+      if (lane < NR) {
+        const float4 q = *reinterpret_cast<const float4*>(sums + 4 * lane);
+        den = (q.x + q.y) + (q.z + q.w);
+      }
+      if (walk.a == 0 && walk.b == walk.s.tiles) {   // the whole item: its rows of out and lse
+        const float inv_l = den == 0.0f ? 0.0f : 1.0f / den;
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+          const float il = __shfl_sync(0xffffffffu, inv_l, r);
+          if (r < rows) {
+            const int64_t tok = walk.s.tok0 + r / G;
+            p.a.out[tok * p.a.out_stride + (walk.h * G + r % G) * kHeadDim + tid] =
+                __float2bfloat16_rn(acc[r] * il);
+          }
+        }
+        if (p.a.lse && warp == 0 && lane < rows) {
+          const int64_t tok = walk.s.tok0 + lane / G;
+          p.a.lse[tok * p.a.heads + walk.h * G + lane % G] =
+              den == 0.0f ? -INFINITY : (run + lg2(den)) * kLn2;
+        }
+      } else {
+        // slot 0: an item that an earlier CTA began; slot 1: one that this CTA begins
+        const bool begins = walk.a == 0;
+        float* slot = p.slots + ((int64_t)2 * blockIdx.x + (begins ? 1 : 0)) * kSlotFloats<NR>;
+#pragma unroll
+        for (int r = 0; r < NR; ++r)
+          if (r < rows) slot[r * 128 + tid] = acc[r];
+        if (warp == 0 && lane < rows) {
+          slot[NR * 128 + lane] = run;
+          slot[NR * 129 + lane] = den;
+        }
+        if (begins) {   // the CTA that its last tile lies in, from the cut of the ranges
+          const int64_t last = walk.base + (int64_t)walk.h * walk.s.tiles + walk.s.tiles - 1;
+          const int64_t c = ((last + 1) * gridDim.x - 1) / total;
+          part.n = walk.n;
+          part.h = walk.h;
+          part.parts = (int)(c - blockIdx.x) + 1;
+        }
+      }
+    }
+    if (!ok && tid == 0) record_error(p.a.status, KDA_ERR_DEVICE_TIMEOUT, 315);
+    if (!ok) part.parts = 0;
+    if (tid == 0) p.desc[blockIdx.x] = part;
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 5) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::kTmemCols);
+  }
+}
+
+// Merges the parts of the item that CTA blockIdx.x of the first kernel began and did not
+// finish: sums and denominators by their maxima, in CTA order.  A warp a row, 4 channels a lane.
+template <int NR>
+__global__ void __launch_bounds__(128) kda_attn_merge_kernel(const __grid_constant__ DecodeParams p) {
+  pdl_wait();
+  const PartDesc d = p.desc[blockIdx.x];
+  if (d.parts == 0) return;
+  const int lane = threadIdx.x & 31, r = blockIdx.y * 4 + (threadIdx.x >> 5);
+  const int hk = p.a.c.kv_heads, G = p.a.heads / hk;
+  const int tok0 = p.a.cu_seqlens[d.n], rows = (p.a.cu_seqlens[d.n + 1] - tok0) * G;
+  if (r >= rows) return;
+  auto slot = [&](int i) {
+    return p.slots + ((int64_t)2 * (blockIdx.x + i) + (i == 0 ? 1 : 0)) * kSlotFloats<NR>;
+  };
+  float m = -INFINITY;
+  for (int i = lane; i < d.parts; i += 32) m = fmaxf(m, slot(i)[NR * 128 + r]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  const float ref = m == -INFINITY ? 0.0f : m;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float den = 0.0f;
+#pragma unroll 4
+  for (int i = 0; i < d.parts; ++i) {
+    const float* s = slot(i);
+    const float w = ex2(s[NR * 128 + r] - ref);
+    const float4 a = *reinterpret_cast<const float4*>(s + r * 128 + 4 * lane);
+    den += s[NR * 129 + r] * w;
+    acc.x += a.x * w;
+    acc.y += a.y * w;
+    acc.z += a.z * w;
+    acc.w += a.w * w;
+  }
+  const float il = den == 0.0f ? 0.0f : 1.0f / den;
+  const int64_t tok = tok0 + r / G;
+  const int head = d.h * G + r % G;
+  __nv_bfloat162 o2[2] = {__floats2bfloat162_rn(acc.x * il, acc.y * il),
+                          __floats2bfloat162_rn(acc.z * il, acc.w * il)};
+  *reinterpret_cast<uint2*>(p.a.out + tok * p.a.out_stride + head * kHeadDim + 4 * lane) =
+      *reinterpret_cast<const uint2*>(o2);
+  if (p.a.lse && lane == 0)
+    p.a.lse[tok * p.a.heads + head] = den == 0.0f ? -INFINITY : (m + lg2(den)) * kLn2;
+}
+
+int decode_ctas(int sms) { return 2 * sms; }
+
+template <int NR, bool kCap>
+cudaError_t launch_nr(DecodeParams& d, int sms, cudaStream_t stream) {
+  static PerDeviceOnce once;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  e = once.run(dev, [&]() -> cudaError_t {
+    return cudaFuncSetAttribute(kda_attn_decode_kernel<NR, kCap>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<NR>::kBytes);
+  });
+  if (e != cudaSuccess) return e;
+  const int ctas = decode_ctas(sms);
+  kda_attn_decode_kernel<NR, kCap><<<ctas, kThreads, Cfg<NR>::kBytes, stream>>>(d);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)ctas, NR / 4);
+  cfg.blockDim = dim3(128);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kda_attn_merge_kernel<NR>, d);
+}
+
+}  // namespace
+
+typedef CUresult (*EncodeTiled)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+bool make_cache_maps(const CacheView& c, CacheMaps* m) {
+  EncodeTiled enc = reinterpret_cast<EncodeTiled>(tensor_map_encoder());
+  if (!enc) return false;
+  const cuuint64_t dims[4] = {(cuuint64_t)kHeadDim, (cuuint64_t)c.page_size, (cuuint64_t)c.kv_heads,
+                              (cuuint64_t)c.num_pages};
+  const cuuint64_t strides[3] = {(cuuint64_t)c.token_stride, (cuuint64_t)c.head_stride,
+                                 (cuuint64_t)c.page_stride};
+  const cuuint32_t box[4] = {(cuuint32_t)kHeadDim, (cuuint32_t)c.page_size, 1, 1};
+  const cuuint32_t es[4] = {1, 1, 1, 1};
+  for (int i = 0; i < 2; ++i)
+    if (enc(i ? &m->v : &m->k, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, i ? c.v : c.k, dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return false;
+  return true;
+}
+
+size_t decode_workspace_bytes(int sms) {
+  const size_t ctas = (size_t)decode_ctas(sms);
+  return ctas * sizeof(PartDesc) + ctas * 2 * kSlotFloats<32> * sizeof(float);
+}
+
+cudaError_t launch_attn_decode(const AttnParams& a, int min_rows, int max_rows, void* work, int sms,
+                               cudaStream_t stream) {
+  DecodeParams d;
+  d.a = a;
+  if (!make_cache_maps(a.c, &d.maps)) return cudaErrorNotSupported;
+  d.min_rows = min_rows;
+  d.max_rows = max_rows;
+  d.desc = static_cast<PartDesc*>(work);
+  d.slots = reinterpret_cast<float*>(d.desc + decode_ctas(sms));
+  const bool cap = a.softcap > 0.0f;
+  // the row count the operands are padded to
+  if (max_rows <= 8) return cap ? launch_nr<8, true>(d, sms, stream) : launch_nr<8, false>(d, sms, stream);
+  if (max_rows <= 16) return cap ? launch_nr<16, true>(d, sms, stream) : launch_nr<16, false>(d, sms, stream);
+  return cap ? launch_nr<32, true>(d, sms, stream) : launch_nr<32, false>(d, sms, stream);
+}
+
+}  // namespace attn
+}  // namespace kda

@@ -8,7 +8,7 @@ namespace kda {
 namespace attn {
 namespace {
 
-__global__ void __launch_bounds__(128) kda_attn_kernel(const __grid_constant__ AttnParams p) {
+__global__ void __launch_bounds__(128) kda_attn_kernel(const __grid_constant__ AttnParams p, int min_rows) {
   const int lane = threadIdx.x & 31;
   const int64_t w = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
   const int32_t* cu = p.cu_seqlens;
@@ -26,6 +26,7 @@ __global__ void __launch_bounds__(128) kda_attn_kernel(const __grid_constant__ A
     if (lane == 0) record_error(p.status, KDA_ERR_INVALID_ARG, 303);
     return;
   }
+  if ((cu[n + 1] - cu[n]) * (p.heads / p.c.kv_heads) < min_rows) return;
   const int pos = len - (int)(cu[n + 1] - t);
   const int P = p.c.page_size;
   if (len < 0 || (int64_t)len > (int64_t)p.c.max_blocks * P) {
@@ -72,12 +73,30 @@ __global__ void __launch_bounds__(128) kda_attn_kernel(const __grid_constant__ A
 
 }  // namespace
 
-size_t attn_workspace_bytes(int32_t, int32_t, int32_t, int32_t) { return (size_t)kWorkspaceBytes; }
+size_t attn_workspace_bytes(int32_t, int32_t, int32_t, int32_t) {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0) {
+    cudaGetLastError();
+    sms = kDefaultSmCount;
+  }
+  return (size_t)kWorkspaceBytes + decode_workspace_bytes(sms);
+}
 
-cudaError_t launch_attn(const AttnParams& p, int, cudaStream_t stream) {
-  const int64_t grid = (p.total_tokens * p.heads + 3) / 4;
-  if (grid > 0x7fffffff) return cudaErrorInvalidValue;
-  kda_attn_kernel<<<(unsigned)grid, 128, 0, stream>>>(p);
+cudaError_t launch_attn(const AttnParams& p, int sms, cudaStream_t stream) {
+  const int group = p.heads / p.c.kv_heads;
+  const int64_t rows = (int64_t)p.max_q_len * group;
+  const int decode_rows = group <= 32 ? (int)(rows < 32 ? rows : 32) : 0;
+  if (decode_rows > 0) {
+    cudaError_t e = launch_attn_decode(p, 1, decode_rows, reinterpret_cast<char*>(p.status) + kWorkspaceBytes,
+                                       sms, stream);
+    if (e != cudaSuccess) return e;
+  }
+  if (rows > decode_rows) {
+    const int64_t grid = (p.total_tokens * p.heads + 3) / 4;
+    if (grid > 0x7fffffff) return cudaErrorInvalidValue;
+    kda_attn_kernel<<<(unsigned)grid, 128, 0, stream>>>(p, decode_rows + 1);
+  }
   return cudaGetLastError();
 }
 

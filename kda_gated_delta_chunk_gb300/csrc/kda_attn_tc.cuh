@@ -1,0 +1,128 @@
+// Shared by the tcgen05 attention kernels: e4m3 matrix instructions, the paged cache's tensor
+// maps, and the split of a batch's key tiles over the CTAs.
+#pragma once
+
+#include <cuda.h>
+
+#include "kda_attn.cuh"
+#include "kda_sm100.cuh"
+
+namespace kda {
+namespace attn {
+
+using namespace sm100;
+
+constexpr int kTile = 128;              // keys of a tile
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float lg2(float x) {
+  float y;
+  asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// Maximum over the warp (NaN lanes do not count).
+__device__ __forceinline__ float warp_max(float x) {
+  float y;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+  return y;
+}
+// cap * tanh(x / cap) * log2(e), to fp32's absolute precision: tanh y = 1 - 2 / (1 + e^(2 y)).
+__device__ __forceinline__ float cap_score(float x, float two_over_cap_log2e, float cap_log2e) {
+  return cap_log2e - __fdividef(2.0f * cap_log2e, 1.0f + ex2(x * two_over_cap_log2e));
+}
+
+// D[tmem] (+)= A[smem] * B[smem]^T, kind::f8f6f4 with e4m3 operands, fp32 accumulate; K = 32.
+__device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
+                                         uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Instruction descriptor of kind::f8f6f4: fp32 accumulator, A and B e4m3 (format 0).
+__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N, int a_mn, int b_mn) {
+  return (1u << 4) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16) | ((uint32_t)(N >> 3) << 17) |
+         ((uint32_t)(M >> 4) << 24);
+}
+// 8-bit tiles with the 128-byte swizzle: a row of 128 bytes per token (key, query row), rows in
+// groups of 8; the 16-byte chunk index is XORed with row % 8.  As a K-major operand (channels
+// along K) a K step of 32 is 32 bytes on; as an MN-major one (tokens along K) 32 rows.
+__device__ __forceinline__ uint32_t tile_off(int row, int byte) {
+  return (uint32_t)((row >> 3) * 1024 + (row & 7) * 128 + (((byte >> 4) ^ (row & 7)) << 4) + (byte & 15));
+}
+__device__ __forceinline__ uint64_t kmajor8(uint32_t tile, int ks) {
+  return sdesc_sw128(tile + 32 * ks, 16, 1024);
+}
+__device__ __forceinline__ uint64_t mnmajor8(uint32_t tile, int ks) {
+  return sdesc_sw128(tile + 4096 * ks, 16, 1024);
+}
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* tmap, int x, int y, int z,
+                                            int w, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
+
+// Keys and values as [page][head][slot][128 bytes]; a box is one page of one head.
+struct CacheMaps {
+  CUtensorMap k, v;
+};
+bool make_cache_maps(const CacheView& c, CacheMaps* m);
+
+// ------------------------------------------------------------ one sequence of a batch
+struct SeqInfo {
+  int tok0, q_len, len;   // first new token, new tokens, cached tokens (new ones included)
+  int tile0, tiles;       // key tiles any of its queries sees; at least one (whose keys may all
+                          // be masked), so that every query row is written; 0: not in this launch
+};
+// Sequences with min_rows <= q_len * group <= max_rows are this launch's.  `err`: the code to
+// record for a malformed sequence (which is left out), or KDA_OK.
+__device__ __forceinline__ SeqInfo seq_info(const AttnParams& p, int n, int min_rows, int max_rows,
+                                            int* err) {
+  SeqInfo s;
+  const int t0 = p.cu_seqlens[n], t1 = p.cu_seqlens[n + 1];
+  s.tok0 = t0;
+  s.q_len = t1 - t0;
+  s.len = p.c.kv_lens[n];
+  s.tile0 = s.tiles = 0;
+  *err = KDA_OK;
+  if (t0 < 0 || t1 < t0 || (int64_t)t1 > p.total_tokens) {
+    *err = KDA_ERR_BAD_CU_SEQLENS;
+    return s;
+  }
+  if (s.len < 0 || (int64_t)s.len > (int64_t)p.c.max_blocks * p.c.page_size) {
+    *err = KDA_ERR_BAD_CACHE_INDEX;
+    return s;
+  }
+  if (s.q_len > p.max_q_len) {
+    *err = KDA_ERR_INVALID_ARG;
+    return s;
+  }
+  const int64_t rows = (int64_t)s.q_len * (p.heads / p.c.kv_heads);
+  if (s.q_len == 0 || rows < min_rows || rows > max_rows) return s;
+  const int lo = p.window > 0 ? max(0, s.len - s.q_len - p.window + 1) : 0;
+  s.tile0 = lo / kTile;
+  s.tiles = max(1, (s.len + kTile - 1) / kTile - s.tile0);
+  return s;
+}
+
+}  // namespace attn
+}  // namespace kda
