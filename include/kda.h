@@ -410,7 +410,8 @@ int kda_rope_append(const void* q, int64_t q_stride, const void* k, int64_t k_st
  *   out = sum_j softmax(s)_j v_j     lse = log sum_j exp(s_j)
  * per token and head, where query i of a sequence with t new tokens sits at position
  * p = kv_lens - t + i and sees j with max(0, p - window + 1) <= j <= p (window 0: from 0).
- * Query head h reads kv head h / (heads / kv_heads); heads is a multiple of kv_heads.
+ * Query head h reads kv head h / (heads / kv_heads); heads is a multiple of kv_heads, at most
+ * 256 times it.
  *   q, out  bf16 [T, heads, 128], strides as in kda_rope_append; out must not overlap q
  *   lse     fp32 [T, heads] or NULL
  * A query that sees no key (p < 0) gets a row of zeros and lse = -infinity.  Cache entries that

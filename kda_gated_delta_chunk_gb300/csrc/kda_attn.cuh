@@ -132,6 +132,11 @@ size_t decode_workspace_bytes(int sms);
 cudaError_t launch_attn_decode(const AttnParams& p, int min_rows, int max_rows, void* work, int sms,
                                cudaStream_t stream);
 
+// Sequences with at least min_rows of them (heads per kv head at most 256).
+size_t prefill_workspace_bytes(int sms);
+cudaError_t launch_attn_prefill(const AttnParams& p, int min_rows, void* work, int sms,
+                                cudaStream_t stream);
+
 // The sequence that token t belongs to: the last n with cu[n] <= t (cu non-decreasing,
 // cu[0] <= t < cu[N]).
 __device__ __forceinline__ int seq_of(const int32_t* cu, int num_seqs, int64_t t) {

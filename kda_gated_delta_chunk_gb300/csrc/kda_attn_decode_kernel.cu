@@ -163,8 +163,13 @@ __global__ void __launch_bounds__(kThreads, 2)
   for (int w = 0; w < kThreads / 32; ++w) total += misc->part[w];
   __syncthreads();
   Walk walk;
-  walk.pos = (int64_t)blockIdx.x * total / gridDim.x;
-  walk.end = (int64_t)(blockIdx.x + 1) * total / gridDim.x;
+  // (no more ranges than tiles: between two CTAs of an item there is none without a part)
+  const int ranges = (int)min((long long)gridDim.x, total);
+  walk.pos = walk.end = 0;
+  if ((int)blockIdx.x < ranges) {
+    walk.pos = (int64_t)blockIdx.x * total / ranges;
+    walk.end = (int64_t)(blockIdx.x + 1) * total / ranges;
+  }
   if (walk.pos < walk.end) {
     long long before = 0;
     for (int n0 = 0; n0 < N; n0 += kThreads) {
@@ -586,7 +591,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
         if (begins) {   // the CTA that its last tile lies in, from the cut of the ranges
           const int64_t last = walk.base + (int64_t)walk.h * walk.s.tiles + walk.s.tiles - 1;
-          const int64_t c = ((last + 1) * gridDim.x - 1) / total;
+          const int64_t c = ((last + 1) * ranges - 1) / total;
           part.n = walk.n;
           part.h = walk.h;
           part.parts = (int)(c - blockIdx.x) + 1;

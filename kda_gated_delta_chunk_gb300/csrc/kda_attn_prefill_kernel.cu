@@ -1,0 +1,795 @@
+// Attention over the paged e4m3 cache for many query rows (prefill, long verifies): the rows --
+// new tokens x query heads of one kv head, token-major -- are cut into tiles of up to 256 (whole
+// tokens), two halves A and B of 128 rows that share the stream of key tiles:
+//   S   = q1 K8^T + q2 K8^T   e4m3 on tcgen05, the cache's keys as they lie in memory; a bf16
+//                             query is two e4m3 terms (exact to 2^-18 of its row's largest entry,
+//                             at the tensor time of one bf16 product)
+//   P   = 2^(s + log2 v_scale(page) - m)   thread = row, written as bf16 over S in tensor memory
+//   O  += P V                 bf16 on tcgen05, P from tensor memory, V widened to bf16 by four
+//                             warps (an e4m3 value is exact in bf16; page scales are in P)
+// The row maximum m is brought up only when it grows by more than 2^8 (P is then at most 2^8, and
+// bf16 keeps its 8 bits at every magnitude), so O is rescaled rarely; the denominators take the
+// fp32 numerators, divided by the page's value scale.
+//
+// Bound by the tensor cores: 4 x 128 flops per visible (row, key).  Two halves keep them busy:
+// while one half's softmax runs, the other half's products do.  The matrix instructions of a CTA
+// run in the order they are issued, so S(i+1) of a half may follow its O += P(i) V, whose P it
+// overwrites, without a wait.  Key tiles of all (sequence, kv head, row tile) items are laid end
+// to end and cut into one equal range per CTA, one CTA per SM (as in the decode kernel), and a
+// dependent kernel merges the items that were cut.
+//
+// Warps: 0-3 / 4-7 softmax of the halves, 8-11 the widening of V, 12 the TMA producer, 13 the MMA
+// issuer (14, 15 only give their registers).  Every wait is bounded.
+//
+// Masked entries as in the decode kernel: scores by selection, V rows that no row of the tile
+// sees as zeros, and a NaN in a V row that only some rows see as zero, put back into those rows
+// at the end from the cache itself.
+#include "kda_attn_tc.cuh"
+
+namespace kda {
+namespace attn {
+namespace {
+
+constexpr int kThreadsP = 512;
+constexpr int kRowsP = 256;
+constexpr int kKStages = 3, kVStages = 2;
+constexpr int kRegsSoftmax = 184, kRegsOther = 64;
+constexpr int kRegsNeeded = 256 * kRegsSoftmax + 256 * kRegsOther;   // of the launch's 512 x 128
+constexpr float kSlack = 8.0f;              // log2 growth of the maximum before O is rescaled
+
+// shared memory, from a 1024-byte aligned base
+constexpr int kOffQ = 0;                                    // [half][term] 128 x 128 e4m3
+constexpr int kOffVB = kOffQ + 4 * 16384;                   // [2] V as bf16, two 64-channel blocks
+constexpr int kOffK = kOffVB + 2 * 32768;                   // [kKStages] K tiles
+constexpr int kOffV8 = kOffK + kKStages * 16384;            // [kVStages] V tiles
+constexpr int kOffSc = kOffV8 + kVStages * 16384;           // float4 [4][8]: k scale, log2 v scale, 1 / v scale
+constexpr int kOffBars = kOffSc + 4 * 8 * 16;
+constexpr int kNumBars = 2 * kKStages + 2 * kVStages + 4 + 2 * 5 + 1 + 4;
+constexpr int kOffMiscP = kOffBars + 8 * kNumBars;
+constexpr int kSmemP = kOffMiscP + 256 + 1024;
+static_assert(kSmemP <= 227 * 1024, "shared memory");
+
+// tensor memory columns
+constexpr uint32_t kTS = 0, kTOP = 256;     // S (P) of half h at 128 h, O at 256 + 128 h
+
+constexpr int kSlotFloatsP = kRowsP * 130;
+
+struct PartDescP {
+  int n, h, rt, parts;
+};
+
+struct PrefillParams {
+  AttnParams a;
+  CacheMaps maps;
+  int min_rows, tokens;      // tokens: new tokens per row tile (256 / group)
+  PartDescP* desc;
+  float* slots;
+};
+
+// Row tile rt of a sequence: its tokens, and the key tiles they see.
+struct ItemP {
+  int tok, cnt;              // tokens [tok, tok + cnt) of the sequence's new ones
+  int tile0, tiles;
+};
+__device__ __forceinline__ ItemP item_of(int q_len, int len, int rt, int tokens, int window) {
+  ItemP it;
+  it.tok = rt * tokens;
+  it.cnt = min(tokens, q_len - it.tok);
+  const int p_first = len - q_len + it.tok, p_last = p_first + it.cnt - 1;
+  const int lo = window > 0 ? max(0, p_first - window + 1) : 0;
+  it.tile0 = lo / kTile;
+  it.tiles = max(1, (max(p_last, -1) + kTile) / kTile - it.tile0);
+  return it;
+}
+
+// The walk over a CTA's range of key tiles; every role runs its own.
+struct WalkP {
+  int64_t pos, end;
+  int n, h, rt, off;         // the next item and the tiles of it that lie before this range
+  SeqInfo s;
+  ItemP it;
+  int a, b;                  // segment: tiles [a, b) of the item
+  int ch, crt;               // its head and row tile
+  __device__ __forceinline__ bool next(const PrefillParams& p) {
+    if (pos >= end) return false;
+    while (s.tiles == 0 || rt * p.tokens >= s.q_len) {   // to the next head or sequence
+      if (s.tiles != 0 && h + 1 < p.a.c.kv_heads) {
+        ++h;
+        rt = 0;
+        continue;
+      }
+      int err;
+      if (++n >= p.a.num_seqs) return false;             // (lengths that changed under the kernel)
+      s = seq_info(p.a, n, p.min_rows, 0x7fffffff, &err);
+      h = rt = 0;
+    }
+    it = item_of(s.q_len, s.len, rt, p.tokens, p.a.window);
+    ch = h;
+    crt = rt;
+    a = off;
+    b = (int)min((int64_t)it.tiles, a + (end - pos));
+    pos += b - a;
+    off = 0;
+    ++rt;
+    return true;
+  }
+};
+
+__device__ __forceinline__ uint32_t bf16x2_of(float lo, float hi) { return pack_bf16x2(lo, hi); }
+
+template <bool kCap>
+__global__ void __launch_bounds__(kThreadsP, 1)
+    kda_attn_prefill_kernel(const __grid_constant__ PrefillParams p) {
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  unsigned char* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  const uint32_t sb = smem_u32(sm);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t bar_kf = sb + kOffBars, bar_ke = bar_kf + 8 * kKStages;
+  const uint32_t bar_vf = bar_ke + 8 * kKStages, bar_ve = bar_vf + 8 * kVStages;
+  const uint32_t bar_bf = bar_ve + 8 * kVStages, bar_be = bar_bf + 16;       // widened V
+  const uint32_t bar_q = bar_be + 16, bar_s = bar_q + 16, bar_p = bar_s + 16, bar_o = bar_p + 16;
+  const uint32_t bar_of = bar_o + 16, bar_end = bar_of + 16, bar_sc = bar_end + 8;   // bar_sc: scales
+  struct Misc {
+    long long part[16];
+    long long rest;          // first tile's place in its sequence
+    int start_n, poison[8];
+    int start_h, start_rt, start_off;
+    uint32_t tmem;
+  };
+  Misc* misc = reinterpret_cast<Misc*>(sm + kOffMiscP);
+  static_assert(sizeof(Misc) <= 256, "misc");
+  const int hk = p.a.c.kv_heads, N = p.a.num_seqs, G = p.a.heads / hk, P = p.a.c.page_size;
+
+  if (tid == 0) {
+    for (int i = 0; i < kKStages; ++i) {
+      mbar_init(bar_kf + 8 * i, 1);
+      mbar_init(bar_ke + 8 * i, 1);
+    }
+    for (int i = 0; i < kVStages; ++i) {
+      mbar_init(bar_vf + 8 * i, 1);
+      mbar_init(bar_ve + 8 * i, 128);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar_bf + 8 * i, 128);
+      mbar_init(bar_be + 8 * i, 1);
+      mbar_init(bar_q + 8 * i, 128);
+      mbar_init(bar_s + 8 * i, 1);
+      mbar_init(bar_p + 8 * i, 128);
+      mbar_init(bar_o + 8 * i, 1);
+      mbar_init(bar_of + 8 * i, 128);
+    }
+    mbar_init(bar_end, 1);
+    for (int i = 0; i < 4; ++i) mbar_init(bar_sc + 8 * i, 1);
+    mbar_fence_init();
+    for (int i = 0; i < 8; ++i) misc->poison[i] = 0;
+    tma_prefetch_desc(&p.maps.k);
+    tma_prefetch_desc(&p.maps.v);
+    if (blockIdx.x == 0 && p.a.cu_seqlens[0] != 0) record_error(p.a.status, KDA_ERR_BAD_CU_SEQLENS, 330);
+  }
+  if (warp == 13) {
+    tmem_alloc(smem_u32(&misc->tmem), 512);
+    tmem_relinquish();
+  }
+  pdl_launch_dependents();
+
+  // ---- this CTA's range.  A thread reads its sequence's lengths; the warp adds up the row
+  // tiles of each of its sequences together.
+  auto cost = [&](int n, bool report) -> long long {     // key tiles of sequence n (all heads)
+    int q_len = 0, len = 0;
+    if (n < N) {
+      int err;
+      const SeqInfo s = seq_info(p.a, n, p.min_rows, 0x7fffffff, &err);
+      if (err != KDA_OK && report && blockIdx.x == 0) record_error(p.a.status, err, 331);
+      if (s.tiles) {
+        q_len = s.q_len;
+        len = s.len;
+      }
+    }
+    long long mine = 0;
+    uint32_t todo = __ballot_sync(0xffffffffu, q_len > 0);
+    while (todo) {
+      const int k = __ffs(todo) - 1;
+      todo &= todo - 1;
+      const int ql = __shfl_sync(0xffffffffu, q_len, k), ln = __shfl_sync(0xffffffffu, len, k);
+      long long sum = 0;
+      for (int rt = lane; rt * p.tokens < ql; rt += 32) sum += item_of(ql, ln, rt, p.tokens, p.a.window).tiles;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      if (lane == k) mine = sum * hk;
+    }
+    return mine;
+  };
+  long long mine = 0, first = 0;
+  for (int n0 = 0; n0 < N; n0 += kThreadsP) {
+    const long long w = cost(n0 + tid, true);
+    if (n0 == 0) first = w;
+    mine += w;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+  if (lane == 0) misc->part[warp] = mine;
+  __syncthreads();
+  long long total = 0;
+#pragma unroll
+  for (int w = 0; w < kThreadsP / 32; ++w) total += misc->part[w];
+  __syncthreads();
+  WalkP walk;
+  // (no more ranges than tiles: between two CTAs of an item there is none without a part)
+  const int ranges = (int)min((long long)gridDim.x, total);
+  walk.pos = walk.end = 0;
+  if ((int)blockIdx.x < ranges) {
+    walk.pos = (int64_t)blockIdx.x * total / ranges;
+    walk.end = (int64_t)(blockIdx.x + 1) * total / ranges;
+  }
+  if (walk.pos < walk.end) {
+    long long before = 0;
+    for (int n0 = 0; n0 < N; n0 += kThreadsP) {
+      const long long w = n0 == 0 ? first : cost(n0 + tid, false);
+      long long inc = w;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long u = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += u;
+      }
+      if (lane == 31) misc->part[warp] = inc;
+      __syncthreads();
+      long long off = before;
+      for (int x = 0; x < warp; ++x) off += misc->part[x];
+      if (w > 0 && walk.pos >= off + inc - w && walk.pos < off + inc) {
+        const long long x = walk.pos - (off + inc - w), per_head = w / hk;
+        misc->start_n = n0 + tid;
+        misc->start_h = (int)(x / per_head);
+        misc->rest = x % per_head;
+      }
+      for (int x = 0; x < kThreadsP / 32; ++x) before += misc->part[x];
+      __syncthreads();
+      if (before > walk.pos) break;
+    }
+    walk.n = misc->start_n;
+    walk.h = misc->start_h;
+    int err;
+    walk.s = seq_info(p.a, walk.n, p.min_rows, 0x7fffffff, &err);
+    if (warp == 0) {     // the row tile: 32 at a time
+      long long left = misc->rest;
+      for (int r0 = 0;; r0 += 32) {
+        const int rt = r0 + lane;
+        const int c = rt * p.tokens < walk.s.q_len
+                          ? item_of(walk.s.q_len, walk.s.len, rt, p.tokens, p.a.window).tiles : 0;
+        int inc = c;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int u = __shfl_up_sync(0xffffffffu, inc, o);
+          if (lane >= o) inc += u;
+        }
+        const uint32_t here = __ballot_sync(0xffffffffu, left < inc && left >= inc - c);
+        if (here) {
+          if (lane == __ffs(here) - 1) {
+            misc->start_rt = rt;
+            misc->start_off = (int)(left - (inc - c));
+          }
+          break;
+        }
+        if (r0 * p.tokens >= walk.s.q_len) break;   // (lengths that changed under the kernel)
+        left -= __shfl_sync(0xffffffffu, inc, 31);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = misc->tmem;
+  if (walk.pos < walk.end) {
+    walk.rt = misc->start_rt;
+    walk.off = misc->start_off;
+  }
+
+  if (warp >= 12) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
+    if (warp == 12) {
+      // ================= producer
+      uint32_t it = 0;
+      bool ok = true;
+      while (ok && walk.next(p)) {
+        const int32_t* bt = p.a.c.block_table + walk.n * p.a.c.table_stride;
+        const int boxes = kTile / P, used = (walk.s.len + P - 1) / P;
+        // lanes 0-7: the page that holds keys 16 lane .. of a tile (its first lane loads it)
+        const int per = P / 16;                          // 16-key groups per page
+        auto page_of = [&](int t) -> int {
+          const int b = (walk.it.tile0 + t) * boxes + lane / per;
+          if (lane >= 8 || t >= walk.b || b >= used) return -2;
+          const int pg = bt[b];
+          if (pg < 0 || pg >= p.a.c.num_pages) {
+            record_error(p.a.status, KDA_ERR_BAD_CACHE_INDEX, 332);
+            return p.a.c.num_pages;                      // outside the map: the load gives zeros
+          }
+          return pg;
+        };
+        auto scale_of = [&](const float* sc, int pg) -> float {
+          return pg >= 0 && pg < p.a.c.num_pages ? sc[(int64_t)pg * p.a.c.scale_stride + walk.ch] : 1.0f;
+        };
+        int pg = page_of(walk.a);
+        for (int t = walk.a; t < walk.b; ++t, ++it) {
+          const float ks = scale_of(p.a.c.k_scale, pg), vs = scale_of(p.a.c.v_scale, pg);
+          const int pg_next = page_of(t + 1);
+          const uint32_t sk = it % kKStages, sv = it % kVStages;
+          if (it >= kKStages) ok = mbar_wait(bar_ke + 8 * sk, (it / kKStages - 1) & 1);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          // (slot it % 4 was last read for tile it - 4, whose P precedes the products of tile
+          // it - 3 that the wait above saw done)
+          if (lane < 8)
+            reinterpret_cast<float4*>(sm + kOffSc)[(it & 3) * 8 + lane] =
+                make_float4(ks, lg2(vs), __fdividef(1.0f, vs), 0.0f);
+          const bool loads = pg != -2 && lane % per == 0;
+          const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, loads)) * P * kHeadDim;
+          const int row = lane * 16;
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(bar_sc + 8 * (it & 3));
+            mbar_expect_tx(bar_kf + 8 * sk, bytes);
+          }
+          __syncwarp();
+          if (loads) tma_load_4d(sb + kOffK + sk * 16384 + row * 128, &p.maps.k, 0, 0, walk.ch, pg, bar_kf + 8 * sk);
+          if (it >= kVStages) ok = mbar_wait(bar_ve + 8 * sv, (it / kVStages - 1) & 1);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          if (lane == 0) mbar_expect_tx(bar_vf + 8 * sv, bytes);
+          __syncwarp();
+          if (loads) tma_load_4d(sb + kOffV8 + sv * 16384 + row * 128, &p.maps.v, 0, 0, walk.ch, pg, bar_vf + 8 * sv);
+          pg = pg_next;
+        }
+      }
+      if (!ok && lane == 0) record_error(p.a.status, KDA_ERR_DEVICE_TIMEOUT, 333);
+      // the copies in flight end before the CTA does (a failed wait left at most one K behind)
+      for (uint32_t i = it > kKStages ? it - kKStages : 0; i < it + (ok ? 0 : 1); ++i)
+        mbar_wait(bar_kf + 8 * (i % kKStages), (i / kKStages) & 1);
+      for (uint32_t i = it > kVStages ? it - kVStages : 0; i < it; ++i)
+        mbar_wait(bar_vf + 8 * (i % kVStages), (i / kVStages) & 1);
+    } else if (warp == 13) {
+      // ================= MMA issuer
+      if (elect_one()) {
+        constexpr uint32_t id_s = idesc_e4m3(128, 128, 0, 0), id_o = idesc_bf16(128, 128, 0, 1);
+        uint32_t it = 0, seg = 0;
+        bool ok = true;
+        auto qk = [&](uint32_t i, int h) {               // S of tile i, half h
+          const uint32_t k = sb + kOffK + (i % kKStages) * 16384, q = sb + kOffQ + h * 32768;
+#pragma unroll
+          for (int x = 0; x < 8; ++x)
+            mma_e4m3(tmem + kTS + 128 * h, kmajor8(q + (x >> 2) * 16384, x & 3), kmajor8(k, x & 3), id_s, x > 0);
+          mma_commit(bar_s + 8 * h);
+        };
+        auto pv = [&](uint32_t i, int h, bool first_tile) {   // O of half h += P(i) V(i)
+          ok = ok && mbar_wait(bar_p + 8 * h, i & 1);
+          if (h == 0) ok = ok && mbar_wait(bar_bf + 8 * (i & 1), (i >> 1) & 1);
+          // (the segment before has read its O)
+          if (first_tile && seg > 0) ok = ok && mbar_wait(bar_of + 8 * h, (seg - 1) & 1);
+          if (!ok) return;
+          tc_fence_after();
+          const uint32_t v = sb + kOffVB + (i & 1) * 32768;
+#pragma unroll
+          for (int ks = 0; ks < 8; ++ks)
+            mma_bf16_ts(tmem + kTOP + 128 * h, tmem + kTS + 128 * h + 8 * ks,
+                        sdesc_sw128(v + 2048 * ks, 16384, 1024), id_o, !(first_tile && ks == 0));
+          mma_commit(bar_o + 8 * h);
+          if (h == 1) mma_commit(bar_be + 8 * (i & 1));
+        };
+        while (ok && walk.next(p)) {
+          for (int t = walk.a; t < walk.b && ok; ++t, ++it) {
+            for (int h = 0; h < 2 && ok; ++h) {
+              if (t > walk.a) pv(it - 1, h, t - 1 == walk.a);
+              else ok = mbar_wait(bar_q + 8 * h, seg & 1);
+              if (h == 0) ok = ok && mbar_wait(bar_kf + 8 * (it % kKStages), (it / kKStages) & 1);
+              if (!ok) break;
+              tc_fence_after();
+              qk(it, h);
+            }
+            if (ok) mma_commit(bar_ke + 8 * (it % kKStages));
+          }
+          for (int h = 0; h < 2 && ok; ++h) pv(it - 1, h, walk.b - 1 == walk.a);
+          ++seg;
+        }
+        if (!ok) record_error(p.a.status, KDA_ERR_DEVICE_TIMEOUT, 334);
+        // what was issued ends, its arrivals included, before shared and tensor memory go
+        mma_commit(bar_end);
+        mbar_wait(bar_end, 0);
+        for (uint32_t i = it > kKStages ? it - kKStages : 0; ok && i < it; ++i)
+          mbar_wait(bar_ke + 8 * (i % kKStages), (i / kKStages) & 1);
+        for (uint32_t i = it > 2 ? it - 2 : 0; ok && i < it; ++i)
+          mbar_wait(bar_be + 8 * (i & 1), (i >> 1) & 1);
+      }
+      __syncwarp();
+    }
+  } else if (warp >= 8) {
+    // ================= V to bf16, MN-major, 64-channel blocks 16 KB apart
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
+    const int vt = tid - 256, c = vt & 7;                // 16-channel chunk of this thread
+    uint32_t it = 0, seg = 0;
+    bool ok = true;
+    while (ok && walk.next(p)) {
+      const int p_first = walk.s.len - walk.s.q_len + walk.it.tok, p_last = p_first + walk.it.cnt - 1;
+      if (vt == 0) misc->poison[(seg + 4) & 7] = 0;      // last read four segments ago
+      for (int t = walk.a; t < walk.b; ++t, ++it) {
+        const uint32_t sv = it % kVStages, vb = it & 1;
+        ok = mbar_wait(bar_vf + 8 * sv, (it / kVStages) & 1);
+        if (it >= 2) ok = ok && mbar_wait(bar_be + 8 * vb, ((it >> 1) - 1) & 1);
+        if (!ok) break;
+        const unsigned char* src = sm + kOffV8 + sv * 16384;
+        unsigned char* dst = sm + kOffVB + vb * 32768 + (c >> 2) * 16384;
+        const int key0 = (walk.it.tile0 + t) * kTile;
+        const bool masked = key0 + kTile - 1 > p_first || (p.a.window > 0 && key0 <= p_last - p.a.window);
+#pragma unroll 2
+        for (int j = 0; j < 8; ++j) {
+          const int row = (vt >> 3) + 16 * j, key = key0 + row;
+          uint4 u = *reinterpret_cast<const uint4*>(src + row * 128 + ((c ^ (row & 7)) << 4));
+          // seen by no row of the tile: whatever is there reads as zero
+          if (masked && (key > p_last || (p.a.window > 0 && key <= p_first - p.a.window)))
+            u = make_uint4(0, 0, 0, 0);
+          uint32_t w[4] = {u.x, u.y, u.z, u.w}, nan = 0, o[8];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            nan |= __vcmpeq4(w[e] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+            // bytes (0, 1), (2, 3) to the high bytes of 16-bit halves; sign to bit 15, exponent
+            // and mantissa down to bits 10..4: the value times 2^-120 in bf16
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+              const uint32_t h2 = __byte_perm(w[e], 0, g ? 0x3424 : 0x1404);
+              const uint32_t b = (h2 & 0x80008000u) | ((h2 >> 4) & 0x07f007f0u);
+              asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(o[2 * e + g]) : "r"(b), "r"(0x7b807b80u));   // 2^120
+            }
+          }
+          if (nan) {        // rare: NaN to NaN, or to zero and noted where some rows do not see it
+            if (masked) misc->poison[seg & 7] = 1;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const uint32_t m = __vcmpeq4(w[e] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+#pragma unroll
+              for (int g = 0; g < 2; ++g) {
+                const uint32_t mm = __byte_perm(m, 0, g ? 0x3322 : 0x1100);
+                o[2 * e + g] = (o[2 * e + g] & ~mm) | (masked ? 0u : (mm & 0x7fff7fffu));
+              }
+            }
+          }
+          unsigned char* d = dst + (row >> 3) * 1024 + (row & 7) * 128;
+          const int k0 = (2 * c) & 7;
+          *reinterpret_cast<uint4*>(d + ((k0 ^ (row & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+          *reinterpret_cast<uint4*>(d + (((k0 + 1) ^ (row & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
+        }
+        fence_proxy_async();
+        mbar_arrive(bar_bf + 8 * vb);
+        mbar_arrive(bar_ve + 8 * sv);
+      }
+      ++seg;
+    }
+    if (!ok && vt == 0) record_error(p.a.status, KDA_ERR_DEVICE_TIMEOUT, 335);
+  } else {
+    // ================= softmax: thread = row
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+    const int half = warp >> 2, row = tid;               // row of the tile (half B: 128 ..)
+    const uint32_t ts = tmem + kTS + 128 * half + ((uint32_t)(32 * (warp & 3)) << 16);
+    const uint32_t to = tmem + kTOP + 128 * half + ((uint32_t)(32 * (warp & 3)) << 16);
+    const float cap2 = kCap ? 2.0f * kLog2e / p.a.softcap : 0.0f, cap1 = kCap ? p.a.softcap * kLog2e : 0.0f;
+    const float sign = p.a.scale < 0.0f ? -1.0f : 1.0f;  // (the row maximum is taken before the scale)
+    PartDescP part = {0, 0, 0, 0};
+    uint32_t it = 0, seg = 0;
+    bool ok = true;
+    while (ok && walk.next(p)) {
+      const int rows = walk.it.cnt * G;
+      const bool live = row < rows;
+      const int i_tok = live ? row / G : walk.it.cnt - 1, head = walk.ch * G + (live ? row % G : 0);
+      const int64_t tok = walk.s.tok0 + walk.it.tok + i_tok;
+      const int pos = walk.s.len - walk.s.q_len + walk.it.tok + i_tok;
+      // positions of this half's first and last row
+      const int r_lo = 128 * half, r_hi = min(rows, 128 * half + 128) - 1;
+      const int p_lo = walk.s.len - walk.s.q_len + walk.it.tok + min(r_lo / G, walk.it.cnt - 1);
+      const int p_hi = walk.s.len - walk.s.q_len + walk.it.tok + max(r_hi, 0) / G;
+      float qmul;
+      {   // ---- this row's query as two e4m3 terms
+        uint4 u[16];
+        const uint4* src = reinterpret_cast<const uint4*>(p.a.q + tok * p.a.q_stride + head * kHeadDim);
+        float top = 0.0f;
+#pragma unroll
+        for (int c = 0; c < 16; ++c) u[c] = live ? src[c] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int c = 0; c < 16; ++c) {
+          float x[8];
+          unpack8(u[c], x);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) top = max_nan(top, fabsf(x[e]));
+        }
+        const int e2 = (int)((__float_as_uint(top) >> 23) & 255) - 127 - 8 +
+                       ((__float_as_uint(top) & 0x7fffffu) > 0x600000u ? 1 : 0);
+        const int e2c = max(e2, -100);
+        const float inv = sign * __uint_as_float((uint32_t)(127 - e2c) << 23);
+        unsigned char* q1 = sm + kOffQ + half * 32768;
+        const int r = row & 127;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {       // 16 channels: one 16-byte chunk of each term
+          uint32_t w1[4], w2[4];
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            float x[8];
+            unpack8(u[2 * c + g], x);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] *= inv;
+            w1[2 * g] = e4m3x4(x[0], x[1], x[2], x[3]);
+            w1[2 * g + 1] = e4m3x4(x[4], x[5], x[6], x[7]);
+#pragma unroll
+            for (int e = 0; e < 8; e += 2) {
+              const float2 b = from_e4m3x2((w1[2 * g + (e >> 2)] >> (8 * (e & 3))) & 0xffff);
+              x[e] -= b.x;
+              x[e + 1] -= b.y;
+            }
+            w2[2 * g] = e4m3x4(x[0], x[1], x[2], x[3]);
+            w2[2 * g + 1] = e4m3x4(x[4], x[5], x[6], x[7]);
+          }
+          *reinterpret_cast<uint4*>(q1 + tile_off(r, 16 * c)) = make_uint4(w1[0], w1[1], w1[2], w1[3]);
+          *reinterpret_cast<uint4*>(q1 + 16384 + tile_off(r, 16 * c)) = make_uint4(w2[0], w2[1], w2[2], w2[3]);
+        }
+        const float sq = top <= 3.402823466e38f ? __uint_as_float((uint32_t)(127 + e2c) << 23) : NAN;
+        qmul = sq * fabsf(p.a.scale) * (kCap ? 1.0f : kLog2e);
+      }
+      fence_proxy_async();
+      mbar_arrive(bar_q + 8 * half);
+
+      float m = -INFINITY, l = 0.0f;
+      for (int t = walk.a; t < walk.b; ++t, ++it) {
+        ok = mbar_wait(bar_s + 8 * half, it & 1);
+        ok = ok && mbar_wait(bar_sc + 8 * (it & 3), (it >> 2) & 1);
+        // (done by now: S of this tile was issued after O of the one before)
+        if (t > walk.a) ok = ok && mbar_wait(bar_o + 8 * half, (it - 1) & 1);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t s[128];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32(ts + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(s + 32 * c));
+        tmem_wait_ld();
+        const float4* sc = reinterpret_cast<const float4*>(sm + kOffSc) + (it & 3) * 8;
+        const int key0 = (walk.it.tile0 + t) * kTile;
+        const bool masked = key0 + kTile - 1 > p_lo || (p.a.window > 0 && key0 <= p_hi - p.a.window);
+        float mt = -INFINITY;
+        const bool scaled = kCap || masked;    // s holds the finished exponents (else raw products)
+        if (scaled) {
+          const int hi = pos - key0, lo = p.a.window > 0 ? pos - p.a.window + 1 - key0 : -1;
+#pragma unroll
+          for (int g = 0; g < 8; ++g) {
+            const float4 f = sc[g];
+            const float mul = qmul * f.x;
+#pragma unroll
+            for (int e = 16 * g; e < 16 * g + 16; ++e) {
+              float x = __uint_as_float(s[e]) * mul;
+              x = (kCap ? cap_score(x, cap2, cap1) : x) + f.y;
+              if (e > hi || e < lo) x = -INFINITY;
+              mt = fmaxf(mt, x);
+              s[e] = __float_as_uint(x);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int g = 0; g < 8; ++g) {
+            const float4 f = sc[g];
+            float a = fmaxf(__uint_as_float(s[16 * g]), __uint_as_float(s[16 * g + 1]));
+            float b = fmaxf(__uint_as_float(s[16 * g + 2]), __uint_as_float(s[16 * g + 3]));
+#pragma unroll
+            for (int e = 16 * g + 4; e < 16 * g + 16; e += 4) {
+              a = fmaxf(a, fmaxf(__uint_as_float(s[e]), __uint_as_float(s[e + 1])));
+              b = fmaxf(b, fmaxf(__uint_as_float(s[e + 2]), __uint_as_float(s[e + 3])));
+            }
+            mt = fmaxf(mt, fmaf(fmaxf(a, b), qmul * f.x, f.y));
+          }
+        }
+        if (__any_sync(0xffffffffu, mt > m + kSlack)) {
+          const float next = fmaxf(m, mt), f = ex2(m - (next == -INFINITY ? 0.0f : next));
+          if (t > walk.a) {       // O, the tile before included, by the factor
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+              uint32_t o[16];
+              tmem_ld16(to + 16 * c, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+              tmem_st16(to + 16 * c, o);
+            }
+          }
+          l *= f;
+          m = next;
+        }
+        const float ref = m == -INFINITY ? 0.0f : m;
+        uint32_t pk[64];
+#pragma unroll
+        for (int g = 0; g < 8; ++g) {
+          const float4 f = sc[g];
+          const float mul = scaled ? 1.0f : qmul * f.x, add = scaled ? -ref : f.y - ref;
+          float sum0 = 0.0f, sum1 = 0.0f;
+#pragma unroll
+          for (int e = 16 * g; e < 16 * g + 16; e += 2) {
+            const float a = ex2(fmaf(__uint_as_float(s[e]), mul, add));
+            const float b = ex2(fmaf(__uint_as_float(s[e + 1]), mul, add));
+            sum0 += a;
+            sum1 += b;
+            pk[e >> 1] = bf16x2_of(a, b);
+          }
+          l = fmaf(sum0 + sum1, f.z, l);
+        }
+        tmem_st32(ts, *reinterpret_cast<uint32_t(*)[32]>(pk));
+        tmem_st32(ts + 32, *reinterpret_cast<uint32_t(*)[32]>(pk + 32));
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(bar_p + 8 * half);
+      }
+      if (ok) ok = mbar_wait(bar_o + 8 * half, (it - 1) & 1);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      tc_fence_after();
+      // ---- the segment's rows out
+      const bool poisoned = *reinterpret_cast<volatile int*>(&misc->poison[seg & 7]) != 0;
+      const bool whole = walk.a == 0 && walk.b == walk.it.tiles;
+      const float inv_l = l == 0.0f ? 0.0f : 1.0f / l;
+      float* slot = p.slots + ((int64_t)2 * blockIdx.x + (walk.a == 0 ? 1 : 0)) * kSlotFloatsP;
+#pragma unroll 1
+      for (int c = 0; c < 4; ++c) {
+        uint32_t o[32];
+        tmem_ld32(to + 32 * c, o);
+        tmem_wait_ld();
+        if (poisoned && live) {    // NaN entries that this row sees, in tiles that some rows do not
+          const int p0 = walk.s.len - walk.s.q_len + walk.it.tok, p1 = p0 + walk.it.cnt - 1;
+          for (int t = walk.a; t < walk.b; ++t) {
+            const int key0 = (walk.it.tile0 + t) * kTile;
+            if (!(key0 + kTile - 1 > p0 || (p.a.window > 0 && key0 <= p1 - p.a.window))) continue;
+            for (int key = max(key0, p.a.window > 0 ? pos - p.a.window + 1 : 0); key <= min(key0 + kTile - 1, pos); ++key) {
+              const int pg = p.a.c.block_table[walk.n * p.a.c.table_stride + key / P];
+              if (pg < 0 || pg >= p.a.c.num_pages) continue;
+              const uint8_t* v = p.a.c.v + pg * p.a.c.page_stride + walk.ch * p.a.c.head_stride +
+                                 (key % P) * p.a.c.token_stride + 32 * c;
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if ((v[e] & 0x7f) == 0x7f) o[e] = 0x7fffffffu;
+            }
+          }
+        }
+        if (live) {
+          if (whole) {
+            uint4* dst = reinterpret_cast<uint4*>(p.a.out + tok * p.a.out_stride + head * kHeadDim + 32 * c);
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+              float x[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) x[e] = __uint_as_float(o[8 * g + e]) * inv_l;
+              dst[g] = pack8(x);
+            }
+          } else {
+#pragma unroll
+            for (int g = 0; g < 8; ++g)
+              *reinterpret_cast<uint4*>(slot + row * 128 + 32 * c + 4 * g) =
+                  make_uint4(o[4 * g], o[4 * g + 1], o[4 * g + 2], o[4 * g + 3]);
+          }
+        }
+      }
+      tc_fence_before();
+      mbar_arrive(bar_of + 8 * half);
+      if (whole) {
+        if (live && p.a.lse)
+          p.a.lse[tok * p.a.heads + head] = l == 0.0f ? -INFINITY : (m + lg2(l)) * kLn2;
+      } else {
+        if (live) {
+          slot[kRowsP * 128 + row] = m;
+          slot[kRowsP * 129 + row] = l;
+        }
+        if (walk.a == 0) {        // this CTA begins the item: the CTA that its last tile lies in
+          const int64_t last = walk.pos - (walk.b - walk.a) + walk.it.tiles - 1;
+          part.n = walk.n;
+          part.h = walk.ch;
+          part.rt = walk.crt;
+          part.parts = (int)(((last + 1) * ranges - 1) / total - blockIdx.x) + 1;
+        }
+      }
+      ++seg;
+    }
+    if (!ok) part.parts = 0;
+    if (!ok && lane == 0) record_error(p.a.status, KDA_ERR_DEVICE_TIMEOUT, 336);
+    if (tid == 0) p.desc[blockIdx.x] = part;
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 13) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Merges the parts of the item that CTA blockIdx.x began and did not finish, in CTA order: a warp
+// takes 4 rows, a lane 4 channels.
+constexpr int kMergeRows = 16;
+__global__ void __launch_bounds__(128) kda_attn_prefill_merge_kernel(const __grid_constant__ PrefillParams p) {
+  pdl_wait();
+  const PartDescP d = p.desc[blockIdx.x];
+  if (d.parts == 0) return;
+  const int lane = threadIdx.x & 31, G = p.a.heads / p.a.c.kv_heads;
+  const int tok0 = p.a.cu_seqlens[d.n], q_len = p.a.cu_seqlens[d.n + 1] - tok0;
+  const int first = d.rt * p.tokens, rows = min(p.tokens, q_len - first) * G;
+  auto slot = [&](int i) {
+    return p.slots + ((int64_t)2 * (blockIdx.x + i) + (i == 0 ? 1 : 0)) * kSlotFloatsP;
+  };
+#pragma unroll 1
+  for (int j = 0; j < kMergeRows / 4; ++j) {
+    const int r = blockIdx.y * kMergeRows + 4 * j + (threadIdx.x >> 5);
+    if (r >= rows) return;
+    float m = -INFINITY;
+    for (int i = lane; i < d.parts; i += 32) m = fmaxf(m, slot(i)[kRowsP * 128 + r]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const float ref = m == -INFINITY ? 0.0f : m;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float den = 0.0f;
+#pragma unroll 4
+    for (int i = 0; i < d.parts; ++i) {
+      const float* s = slot(i);
+      const float w = ex2(s[kRowsP * 128 + r] - ref);
+      const float4 a = *reinterpret_cast<const float4*>(s + r * 128 + 4 * lane);
+      den += s[kRowsP * 129 + r] * w;
+      acc.x += a.x * w;
+      acc.y += a.y * w;
+      acc.z += a.z * w;
+      acc.w += a.w * w;
+    }
+    const float il = den == 0.0f ? 0.0f : 1.0f / den;
+    const int64_t tok = tok0 + first + r / G;
+    const int head = d.h * G + r % G;
+    const uint2 o2 = make_uint2(bf16x2_of(acc.x * il, acc.y * il), bf16x2_of(acc.z * il, acc.w * il));
+    *reinterpret_cast<uint2*>(p.a.out + tok * p.a.out_stride + head * kHeadDim + 4 * lane) = o2;
+    if (p.a.lse && lane == 0)
+      p.a.lse[tok * p.a.heads + head] = den == 0.0f ? -INFINITY : (m + lg2(den)) * kLn2;
+  }
+}
+
+template <bool kCap>
+cudaError_t launch_cap(const PrefillParams& d, int sms, cudaStream_t stream) {
+  static PerDeviceOnce once;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  e = once.run(dev, [&]() -> cudaError_t {
+    cudaFuncAttributes at;
+    cudaError_t x = cudaFuncGetAttributes(&at, kda_attn_prefill_kernel<kCap>);
+    if (x != cudaSuccess) return x;
+    // the warpgroups' register shares must fit what the block is launched with
+    if ((at.numRegs + 7) / 8 * 8 * kThreadsP < kRegsNeeded) return cudaErrorInvalidConfiguration;
+    return cudaFuncSetAttribute(kda_attn_prefill_kernel<kCap>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemP);
+  });
+  if (e != cudaSuccess) return e;
+  kda_attn_prefill_kernel<kCap><<<sms, kThreadsP, kSmemP, stream>>>(d);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)sms, kRowsP / kMergeRows);
+  cfg.blockDim = dim3(128);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kda_attn_prefill_merge_kernel, d);
+}
+
+}  // namespace
+
+size_t prefill_workspace_bytes(int sms) {
+  return (size_t)sms * sizeof(PartDescP) + (size_t)sms * 2 * kSlotFloatsP * sizeof(float);
+}
+
+cudaError_t launch_attn_prefill(const AttnParams& a, int min_rows, void* work, int sms,
+                                cudaStream_t stream) {
+  PrefillParams d;
+  d.a = a;
+  if (!make_cache_maps(a.c, &d.maps)) return cudaErrorNotSupported;
+  d.min_rows = min_rows;
+  d.tokens = kRowsP / (a.heads / a.c.kv_heads);
+  d.desc = static_cast<PartDescP*>(work);
+  d.slots = reinterpret_cast<float*>(d.desc + sms);
+  return a.softcap > 0.0f ? launch_cap<true>(d, sms, stream) : launch_cap<false>(d, sms, stream);
+}
+
+}  // namespace attn
+}  // namespace kda

@@ -192,7 +192,9 @@ int kda_rope_append(const void* q, int64_t q_stride, const void* k, int64_t k_st
 
 size_t kda_attention_workspace_size(int32_t num_seqs, int32_t heads, int32_t kv_heads,
                                     int32_t max_q_len) {
-  if (num_seqs < 0 || heads < 1 || kv_heads < 1 || heads % kv_heads != 0 || max_q_len < 0) return 0;
+  if (num_seqs < 0 || heads < 1 || kv_heads < 1 || heads % kv_heads != 0 ||
+      heads / kv_heads > 256 || max_q_len < 0)
+    return 0;
   return (kda::attn::attn_workspace_bytes(num_seqs, heads, kv_heads, max_q_len) + 15) & ~(size_t)15;
 }
 
@@ -206,7 +208,8 @@ int kda_cached_attention(const void* q, int64_t q_stride, const kda_kv_cache* ca
   if (rc != KDA_OK) return rc;
   rc = check_cache(cache, num_seqs, &p.c);
   if (rc != KDA_OK) return rc;
-  if (heads % cache->kv_heads != 0 || max_q_len < 0 || window < 0) return KDA_ERR_INVALID_ARG;
+  if (heads % cache->kv_heads != 0 || heads / cache->kv_heads > 256 || max_q_len < 0 || window < 0)
+    return KDA_ERR_INVALID_ARG;
   if (!std::isfinite(scale) || !std::isfinite(softcap) || softcap < 0.0f) return KDA_ERR_INVALID_ARG;
   if (total_tokens > 0) {
     if ((rc = check_rows(q, q_stride, heads)) != KDA_OK) return rc;

@@ -70,6 +70,7 @@ def launch(d, softcap=0.0, window=0, max_q=None, caches=None, **kw):
     max_q = max(d["q_lens"] + [1]) if max_q is None else max_q
     if ws is None:
         ws = kda.alloc_attention_workspace(len(d["q_lens"]), H, hk, max_q)
+        ws[256:] = 0xFF      # what another call may have left beyond the status words: NaN here
     k, v = caches if caches else (d["k"].cuda(), d["v"].cuda())
     out, lse = kda.cached_attention(d["q"].cuda(), k, v, d["ks"].cuda(), d["vs"].cuda(),
                                     d["table"].cuda(), d["kv"].cuda(), d["cu"].cuda(), SCALE, max_q,
