@@ -33,7 +33,7 @@ namespace {
 constexpr int kThreadsP = 512;
 constexpr int kRowsP = 256;
 constexpr int kKStages = 3, kVStages = 2;
-constexpr int kRegsSoftmax = 184, kRegsOther = 64;
+constexpr int kRegsSoftmax = 200, kRegsOther = 56;
 constexpr int kRegsNeeded = 256 * kRegsSoftmax + 256 * kRegsOther;   // of the launch's 512 x 128
 constexpr float kSlack = 8.0f;              // log2 growth of the maximum before O is rescaled
 
@@ -568,13 +568,13 @@ __global__ void __launch_bounds__(kThreadsP, 1)
 #pragma unroll
           for (int g = 0; g < 8; ++g) {
             const float4 f = sc[g];
-            float a = fmaxf(__uint_as_float(s[16 * g]), __uint_as_float(s[16 * g + 1]));
-            float b = fmaxf(__uint_as_float(s[16 * g + 2]), __uint_as_float(s[16 * g + 3]));
+            float a = __uint_as_float(s[16 * g]), b = __uint_as_float(s[16 * g + 1]);
 #pragma unroll
-            for (int e = 16 * g + 4; e < 16 * g + 16; e += 4) {
-              a = fmaxf(a, fmaxf(__uint_as_float(s[e]), __uint_as_float(s[e + 1])));
-              b = fmaxf(b, fmaxf(__uint_as_float(s[e + 2]), __uint_as_float(s[e + 3])));
+            for (int e = 16 * g + 2; e < 16 * g + 14; e += 4) {
+              a = max3(a, __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
+              b = max3(b, __uint_as_float(s[e + 2]), __uint_as_float(s[e + 3]));
             }
+            a = max3(a, __uint_as_float(s[16 * g + 14]), __uint_as_float(s[16 * g + 15]));
             mt = fmaxf(mt, fmaf(fmaxf(a, b), qmul * f.x, f.y));
           }
         }
@@ -595,24 +595,28 @@ __global__ void __launch_bounds__(kThreadsP, 1)
           m = next;
         }
         const float ref = m == -INFINITY ? 0.0f : m;
-        uint32_t pk[64];
+        // P over the columns of S, half at a time (all of S is in registers)
 #pragma unroll
-        for (int g = 0; g < 8; ++g) {
-          const float4 f = sc[g];
-          const float mul = scaled ? 1.0f : qmul * f.x, add = scaled ? -ref : f.y - ref;
-          float sum0 = 0.0f, sum1 = 0.0f;
+        for (int hc = 0; hc < 2; ++hc) {
+          uint32_t pk[32];
 #pragma unroll
-          for (int e = 16 * g; e < 16 * g + 16; e += 2) {
-            const float a = ex2(fmaf(__uint_as_float(s[e]), mul, add));
-            const float b = ex2(fmaf(__uint_as_float(s[e + 1]), mul, add));
-            sum0 += a;
-            sum1 += b;
-            pk[e >> 1] = bf16x2_of(a, b);
+          for (int g = 4 * hc; g < 4 * hc + 4; ++g) {
+            const float4 f = sc[g];
+            const float mul = scaled ? 1.0f : qmul * f.x, add = scaled ? -ref : f.y - ref;
+            const float2 mul2 = make_float2(mul, mul), add_2 = make_float2(add, add);
+            float2 sum = make_float2(0.0f, 0.0f);
+#pragma unroll
+            for (int e = 16 * g; e < 16 * g + 16; e += 2) {
+              float2 x = fma2(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), mul2, add_2);
+              x.x = ex2(x.x);
+              x.y = ex2(x.y);
+              sum = add2(sum, x);
+              pk[(e >> 1) - 32 * hc] = bf16x2_of(x.x, x.y);
+            }
+            l = fmaf(sum.x + sum.y, f.z, l);
           }
-          l = fmaf(sum0 + sum1, f.z, l);
+          tmem_st32(ts + 32 * hc, pk);
         }
-        tmem_st32(ts, *reinterpret_cast<uint32_t(*)[32]>(pk));
-        tmem_st32(ts + 32, *reinterpret_cast<uint32_t(*)[32]>(pk + 32));
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive(bar_p + 8 * half);
