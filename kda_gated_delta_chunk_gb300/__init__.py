@@ -89,6 +89,8 @@ def use_library(path: str) -> None:
 def lib() -> ctypes.CDLL:
     """Load libkda.so (built in-tree by ``build.build()``); raise if absent."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(_lib_path):

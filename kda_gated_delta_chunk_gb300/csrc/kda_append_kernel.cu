@@ -16,11 +16,12 @@
 // +-448 * scale, NaN as NaN.  The rotation's products and sums are fp32, each rounded on its
 // own; keys are quantised from the fp32 values.
 //
-// One launch, two kinds of CTA.  The first ones each take one page slot and kv head: half of
-// the threads the keys, half the values, 16 lanes a token row with its values in registers
-// between the maximum and the store.  Sequence n's pages are given the slots from
-// floor(cu[n] / P) + 2 n on, which leaves room for the partial pages at both ends without a
-// prefix sum; unused slots exit.  The rest rotate the queries, 16 lanes a (token, 4 heads).
+// One launch, two kinds of CTA.  The first ones share out the (page, kv head, keys or values) units
+// of the step: every CTA adds up the pages of all sequences (a load and a scan), takes an equal,
+// contiguous range of units and holds a unit's rows in registers, 16 lanes a row, between the
+// maximum and the store.  The others rotate the queries, 16 lanes a (token, group of heads) with
+// the token's table row in registers.  A lane holds both channels of its pairs -- four and four
+// half the rotated part apart, or eight in a row -- so that the rotation needs no exchange.
 // Bound by memory in a prefill, by the chain of dependent loads in a decode step.
 #include "kda_attn.cuh"
 
@@ -28,63 +29,57 @@ namespace kda {
 namespace attn {
 namespace {
 
-constexpr int kHeadsPerUnit = 4;
+constexpr int kSearchRounds = 4;   // sequences per thread that a CTA looks through for its tokens
+constexpr int kRegs = 64;   // of a thread: with 1024 threads an SM, 64 KB of loads in flight
 
-// cos / sin of the 8 channels of `lane` (16 lanes a row) at table row `cs`.
-struct Turn {
-  float c[8], s[8];   // half layout: [e] per channel; interleaved: [0..3] per pair
+// The channels of lane `lane` of 16: two runs of four, [c0, c0 + 4) and [c1, c1 + 4), and the
+// column of its first cosine (negative: these channels are not rotated).
+struct Lane {
+  int c0, c1, col;
 };
-__device__ __forceinline__ void load4(const float* p, float* v) {
-  const float4 a = *reinterpret_cast<const float4*>(p);
-  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-}
 template <bool kInter>
-__device__ __forceinline__ void load_turn(const float* cs, int rot, int lane, Turn& t) {
-  const int half = rot >> 1;
-  if (8 * lane >= rot) return;
-  if (kInter) {
-    load4(cs + 4 * lane, t.c);
-    load4(cs + half + 4 * lane, t.s);
+__device__ __forceinline__ Lane lane_of(int lane, int rot) {
+  Lane l;
+  if (kInter || 8 * lane >= rot) {       // eight in a row: four interleaved pairs, or the rest
+    l.c0 = 8 * lane;
+    l.c1 = 8 * lane + 4;
   } else {
-    const int j = 8 * lane < half ? 8 * lane : 8 * lane - half;
-    load4(cs + j, t.c);
-    load4(cs + j + 4, t.c + 4);
-    load4(cs + half + j, t.s);
-    load4(cs + half + j + 4, t.s + 4);
+    l.c0 = 4 * lane;
+    l.c1 = (rot >> 1) + 4 * lane;
   }
+  l.col = 8 * lane < rot ? 4 * lane : -1;
+  return l;
+}
+struct Row8 {     // eight bf16 channels as loaded
+  uint2 a, b;
+};
+__device__ __forceinline__ Row8 load_row(const __nv_bfloat16* p, const Lane& l) {
+  return {*reinterpret_cast<const uint2*>(p + l.c0), *reinterpret_cast<const uint2*>(p + l.c1)};
+}
+__device__ __forceinline__ void unpack_row(const Row8& r, float (&v)[8]) {
+  unpack8(make_uint4(r.a.x, r.a.y, r.b.x, r.b.y), v);
+}
+struct Turn {
+  float4 c, s;
+};
+__device__ __forceinline__ Turn load_turn(const float* row, int rot, const Lane& l) {
+  if (l.col < 0) return {make_float4(1.f, 1.f, 1.f, 1.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+  return {*reinterpret_cast<const float4*>(row + l.col),
+          *reinterpret_cast<const float4*>(row + (rot >> 1) + l.col)};
 }
 // Products and sums rounded one by one (no contraction): the value does not depend on which
 // of the two products a fused multiply-add would keep unrounded.
-__device__ __forceinline__ float turn_a(float a, float b, float c, float s) {
-  return __fsub_rn(__fmul_rn(a, c), __fmul_rn(b, s));
+__device__ __forceinline__ void turn1(float& a, float& b, float c, float s) {
+  const float x = __fsub_rn(__fmul_rn(a, c), __fmul_rn(b, s));
+  b = __fadd_rn(__fmul_rn(b, c), __fmul_rn(a, s));
+  a = x;
 }
-__device__ __forceinline__ float turn_b(float a, float b, float c, float s) {
-  return __fadd_rn(__fmul_rn(b, c), __fmul_rn(a, s));
-}
-// Rotate the 8 channels of this lane (all 16 lanes of the row take part; `mask` names the
-// lanes of the warp that are here).
 template <bool kInter>
-__device__ __forceinline__ void rotate8(float (&v)[8], int rot, int lane, const Turn& t,
-                                        uint32_t mask) {
-  if (kInter) {
-    if (8 * lane < rot) {
+__device__ __forceinline__ void rotate8(float (&v)[8], const Lane& l, const Turn& t) {
+  if (l.col < 0) return;
+  const float c[4] = {t.c.x, t.c.y, t.c.z, t.c.w}, s[4] = {t.s.x, t.s.y, t.s.z, t.s.w};
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float a = v[2 * j], b = v[2 * j + 1];
-        v[2 * j] = turn_a(a, b, t.c[j], t.s[j]);
-        v[2 * j + 1] = turn_b(a, b, t.c[j], t.s[j]);
-      }
-    }
-  } else {
-    const int hl = rot >> 4;   // lanes per half (rot is a multiple of 16)
-    const bool first = lane < hl, in = lane < 2 * hl;
-    const int src = (threadIdx.x & 16) + (in ? (first ? lane + hl : lane - hl) : lane);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float o = __shfl_sync(mask, v[e], src);
-      if (in) v[e] = first ? turn_a(v[e], o, t.c[e], t.s[e]) : turn_b(o, v[e], t.c[e], t.s[e]);
-    }
-  }
+  for (int j = 0; j < 4; ++j) turn1(v[kInter ? 2 * j : j], v[kInter ? 2 * j + 1 : 4 + j], c[j], s[j]);
 }
 
 // The least 2^e >= 2^-64 with top <= 448 * 2^e (top finite, not negative).
@@ -97,176 +92,263 @@ __device__ __forceinline__ float pow2_scale(float top) {
   return __uint_as_float((uint32_t)(e + 127) << 23);
 }
 
-// kRows: token rows a 16-lane group takes of a page (page size = kRows * groups per half).
-template <int kRows, bool kInter>
-__global__ void __launch_bounds__(512) kda_append_kernel(const __grid_constant__ AppendParams p, int64_t page_ctas) {
-  __shared__ float top_s[2][16];
-  const int tid = threadIdx.x, lane = tid & 15;
-  const int32_t* cu = p.cu_seqlens;
-  const int N = p.num_seqs;
-  if (cu[0] != 0 || (int64_t)cu[N] > p.total_tokens) {
-    if (tid == 0) record_error(p.status, KDA_ERR_BAD_CU_SEQLENS, 200);
-    return;
+// Pages that sequence n's new tokens touch; 0 for a malformed one, whose error `report` records.
+struct SeqPages {
+  int t0, t1, len, start, pages;
+};
+__device__ __forceinline__ SeqPages seq_pages(const AppendParams& p, int n, bool report) {
+  SeqPages q = {p.cu_seqlens[n], p.cu_seqlens[n + 1], p.c.kv_lens[n], 0, 0};
+  const int P = p.c.page_size;
+  if (q.t0 < 0 || q.t1 < q.t0 || (int64_t)q.t1 > p.total_tokens) {
+    if (report) record_error(p.status, KDA_ERR_BAD_CU_SEQLENS, 201);
+    return q;
   }
-  if ((int64_t)blockIdx.x < page_ctas) {
-    // ---- keys and values of one (page slot, kv head)
-    const int hk = (int)(blockIdx.x % p.c.kv_heads);
-    const int64_t slot = blockIdx.x / p.c.kv_heads;
-    const int P = p.c.page_size;
-    int lo = 0, hi = N - 1;   // the last n with floor(cu[n] / P) + 2 n <= slot
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if ((int64_t)(cu[mid] / P) + 2 * (int64_t)mid <= slot) lo = mid;
-      else hi = mid - 1;
-    }
-    const int n = lo;
-    const int t0 = cu[n], t1 = cu[n + 1];
-    if (t0 < 0 || t1 < t0 || (int64_t)t1 > p.total_tokens) {
-      if (tid == 0) record_error(p.status, KDA_ERR_BAD_CU_SEQLENS, 201);
-      return;
-    }
-    const int len = p.c.kv_lens[n];
-    const int start = len - (t1 - t0);
-    if (t1 == t0) return;
-    if (start < 0 || (int64_t)len > (int64_t)p.c.max_blocks * P) {
-      if (tid == 0) record_error(p.status, KDA_ERR_BAD_CACHE_INDEX, 202);
-      return;
-    }
-    const int64_t b = start / P + (slot - (t0 / P + 2 * (int64_t)n));
-    if (b > (len - 1) / P) return;   // a slot this sequence does not use
-    const int s0 = b * P < start ? start - (int)b * P : 0;              // new rows of the page:
-    const int s1 = min(P, len - (int)b * P);                            // [s0, s1)
-    const int page = p.c.block_table[n * p.c.table_stride + b];
-    if (page < 0 || page >= p.c.num_pages) {
-      if (tid == 0) record_error(p.status, KDA_ERR_BAD_CACHE_INDEX, 203);
-      return;
-    }
-    const int hthreads = blockDim.x >> 1, groups = hthreads >> 4;
-    const bool is_v = tid >= hthreads;
-    const int ht = is_v ? tid - hthreads : tid, grp = ht >> 4;
-    const __nv_bfloat16* src = is_v ? p.v : p.k;
-    const int64_t stride = is_v ? p.v_stride : p.k_stride;
-    uint8_t* dst = (is_v ? p.c.v : p.c.k) + page * p.c.page_stride + hk * p.c.head_stride;
-    float* scale_p = (is_v ? p.c.v_scale : p.c.k_scale) + page * p.c.scale_stride + hk;
-    const float old = s0 > 0 ? *scale_p : 0.0f;
-    float x[kRows][8];
-    float top = 0.0f;
-    const uint32_t gmask = 0xffffu << (tid & 16);
-#pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-      const int row = grp + i * groups;
-      if (row >= s0 && row < s1) {
-        const int64_t t = t0 + (b * P + row - start);
-        unpack8(*reinterpret_cast<const uint4*>(src + t * stride + hk * kHeadDim + 8 * lane), x[i]);
-        if (!is_v && p.rot_dim) {
-          const int64_t pos = p.positions ? (int64_t)p.positions[t] : b * P + row;
-          if (pos < 0 || pos >= p.rope_rows) {   // the row is stored unrotated
-            if (lane == 0) record_error(p.status, KDA_ERR_BAD_CACHE_INDEX, 204);
-          } else {
-            Turn tn;
-            load_turn<kInter>(p.rope + pos * p.rot_dim, p.rot_dim, lane, tn);
-            rotate8<kInter>(x[i], p.rot_dim, lane, tn, gmask);
-          }
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float a = fabsf(x[i][e]);
-          if (a <= 3.402823466e38f) top = fmaxf(top, a);   // finite ones
-        }
-      }
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    if ((tid & 31) == 0) top_s[is_v][ht >> 5] = top;
-    __syncthreads();
-    for (int w = 0; w < hthreads / 32; ++w) top = fmaxf(top, top_s[is_v][w]);
-    float scale = pow2_scale(top);
-    if (s0 > 0) scale = fmaxf(scale, old);
-    const float inv = 1.0f / scale;
-#pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-      const int row = grp + i * groups;
-      if (row >= s0 && row < s1) {
-        uint2 o;
-        o.x = e4m3x4(x[i][0] * inv, x[i][1] * inv, x[i][2] * inv, x[i][3] * inv);
-        o.y = e4m3x4(x[i][4] * inv, x[i][5] * inv, x[i][6] * inv, x[i][7] * inv);
-        *reinterpret_cast<uint2*>(dst + row * p.c.token_stride + 8 * lane) = o;
-      }
-    }
-    if (s0 > 0 && scale > old) {   // the page's older rows, brought to the new scale
-      const float ratio = old * inv;
-      for (int row = grp; row < s0; row += groups) {
-        uint2* w = reinterpret_cast<uint2*>(dst + row * p.c.token_stride + 8 * lane);
-        const uint2 u = *w;
-        const float2 a = from_e4m3x2(u.x & 0xffff), b2 = from_e4m3x2(u.x >> 16);
-        const float2 c = from_e4m3x2(u.y & 0xffff), d = from_e4m3x2(u.y >> 16);
-        *w = make_uint2(e4m3x4(a.x * ratio, a.y * ratio, b2.x * ratio, b2.y * ratio),
-                        e4m3x4(c.x * ratio, c.y * ratio, d.x * ratio, d.y * ratio));
-      }
-    }
-    if (ht == 0 && !(s0 > 0 && scale == old)) *scale_p = scale;
-    return;
+  if (q.t1 == q.t0) return q;
+  q.start = q.len - (q.t1 - q.t0);
+  if (q.start < 0 || (int64_t)q.len > (int64_t)p.c.max_blocks * P) {
+    if (report) record_error(p.status, KDA_ERR_BAD_CACHE_INDEX, 202);
+    return q;
   }
-  // ---- queries: 16 lanes a (token, kHeadsPerUnit heads)
-  const int units = (p.heads + kHeadsPerUnit - 1) / kHeadsPerUnit;
-  const int64_t u = ((int64_t)blockIdx.x - page_ctas) * (blockDim.x >> 4) + (tid >> 4);
-  const int64_t t = u / units;
-  if (t >= (int64_t)cu[N]) return;
-  const int h0 = (int)(u % units) * kHeadsPerUnit;
-  const uint32_t gmask = 0xffffu << (tid & 16);
-  float x[kHeadsPerUnit][8];
-#pragma unroll
-  for (int i = 0; i < kHeadsPerUnit; ++i)
-    if (h0 + i < p.heads)
-      unpack8(*reinterpret_cast<const uint4*>(p.q + t * p.q_stride + (h0 + i) * kHeadDim + 8 * lane), x[i]);
-  if (p.rot_dim) {
-    int64_t pos;
-    if (p.positions) {
-      pos = p.positions[t];
-    } else {
-      const int n = seq_of(cu, N, t);
-      pos = (int64_t)p.c.kv_lens[n] - ((int64_t)cu[n + 1] - t);
-    }
-    if (pos < 0 || pos >= p.rope_rows) {
-      if (lane == 0) record_error(p.status, KDA_ERR_BAD_CACHE_INDEX, 205);
-    } else {
-      Turn tn;
-      load_turn<kInter>(p.rope + pos * p.rot_dim, p.rot_dim, lane, tn);
-#pragma unroll
-      for (int i = 0; i < kHeadsPerUnit; ++i)
-        if (h0 + i < p.heads) rotate8<kInter>(x[i], p.rot_dim, lane, tn, gmask);
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < kHeadsPerUnit; ++i)
-    if (h0 + i < p.heads)
-      *reinterpret_cast<uint4*>(p.q_out + t * p.qo_stride + (h0 + i) * kHeadDim + 8 * lane) = pack8(x[i]);
+  q.pages = (q.len - 1) / P - q.start / P + 1;
+  return q;
 }
 
-template <int kRows>
-cudaError_t launch_rows(const AppendParams& p, int threads, cudaStream_t stream) {
-  const int64_t slots = p.total_tokens / p.c.page_size + 2 * (int64_t)p.num_seqs;
-  const int64_t page_ctas = slots * p.c.kv_heads;
-  const int64_t units = p.q ? p.total_tokens * ((p.heads + kHeadsPerUnit - 1) / kHeadsPerUnit) : 0;
-  const int64_t grid = page_ctas + (units + threads / 16 - 1) / (threads / 16);
+// kRows: token rows a 16-lane group takes of a page (page size = kRows * groups).
+// kHeads: query heads a 16-lane group takes of a token.
+template <int kRows, int kHeads, int kThreads, bool kInter>
+__global__ void __launch_bounds__(kThreads, 65536 / kRegs / kThreads)
+    kda_append_kernel(const __grid_constant__ AppendParams p, int page_ctas) {
+  __shared__ float top_s[2][kThreads / 32];
+  __shared__ long long sum_s[kThreads / 32], first_s;
+  __shared__ int n_s;
+  __shared__ int64_t pos_s[kThreads / 16];
+  const int tid = threadIdx.x, lane16 = tid & 15, grp = tid >> 4;
+  constexpr int groups = kThreads / 16, warps = kThreads / 32;
+  const int warp = tid >> 5;
+  const Lane ln = lane_of<kInter>(lane16, p.rot_dim);
+  const int32_t* cu = p.cu_seqlens;
+  const int N = p.num_seqs;
+  if ((int)blockIdx.x < page_ctas) {
+    // ---- this CTA's range of units, and the sequence that it begins in
+    const int hk = p.c.kv_heads, P = p.c.page_size;
+    if (blockIdx.x == 0 && tid == 0 && (cu[0] != 0 || (int64_t)cu[N] > p.total_tokens))
+      record_error(p.status, KDA_ERR_BAD_CU_SEQLENS, 200);
+    long long mine = 0, first = 0;
+    for (int n0 = 0; n0 < N; n0 += blockDim.x) {
+      const int pages = n0 + tid < N ? seq_pages(p, n0 + tid, blockIdx.x == 0).pages : 0;
+      if (n0 == 0) first = pages;
+      mine += pages;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+    if ((tid & 31) == 0) sum_s[warp] = mine;
+    __syncthreads();
+    long long total = 0;
+    for (int w = 0; w < warps; ++w) total += sum_s[w];
+    total *= 2 * hk;
+    __syncthreads();
+    long long u = (long long)blockIdx.x * total / page_ctas;
+    const long long u_end = (long long)(blockIdx.x + 1) * total / page_ctas;
+    if (u >= u_end) return;
+    const long long page0 = u / (2 * hk);
+    long long before = 0;
+    for (int n0 = 0; n0 < N && before <= page0; n0 += blockDim.x) {
+      const long long w = n0 == 0 ? first : (n0 + tid < N ? seq_pages(p, n0 + tid, false).pages : 0);
+      long long inc = w;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long x = __shfl_up_sync(0xffffffffu, inc, o);
+        if ((tid & 31) >= o) inc += x;
+      }
+      if ((tid & 31) == 31) sum_s[warp] = inc;
+      __syncthreads();
+      long long off = before;
+      for (int x = 0; x < warp; ++x) off += sum_s[x];
+      if (w > 0 && page0 >= off + inc - w && page0 < off + inc) {
+        n_s = n0 + tid;
+        first_s = off + inc - w;
+      }
+      for (int x = 0; x < warps; ++x) before += sum_s[x];
+      __syncthreads();
+    }
+    int n = n_s;
+    SeqPages q = seq_pages(p, n, false);
+    int blk = (int)(page0 - first_s), unit = (int)(u % (2 * hk));   // page of the sequence, unit of the page
+    // ---- the units: keys or values of one (page, kv head)
+    for (uint32_t par = 0; u < u_end; ++u, par ^= 1) {
+      while (blk >= q.pages) {
+        if (++n >= N) return;   // (lengths that changed under the kernel)
+        q = seq_pages(p, n, false);
+        blk = 0;
+      }
+      const bool is_v = unit >= hk;
+      const int h = is_v ? unit - hk : unit;
+      const int b = q.start / P + blk;
+      const int s0 = b * P < q.start ? q.start - b * P : 0, s1 = min(P, q.len - b * P);   // new rows
+      const int t_row0 = q.t0 + b * P - q.start;            // token of the page's row 0
+      if (++unit == 2 * hk) {
+        unit = 0;
+        ++blk;
+      }
+      const int page = p.c.block_table[n * p.c.table_stride + b];
+      const __nv_bfloat16* src = (is_v ? p.v : p.k) + h * kHeadDim;
+      const int64_t stride = is_v ? p.v_stride : p.k_stride;
+      Row8 raw[kRows];
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) {
+        const int row = grp + i * groups;
+        raw[i] = {make_uint2(0, 0), make_uint2(0, 0)};
+        if (row >= s0 && row < s1) raw[i] = load_row(src + (int64_t)(t_row0 + row) * stride, ln);
+      }
+      if (page < 0 || page >= p.c.num_pages) {
+        if (tid == 0) record_error(p.status, KDA_ERR_BAD_CACHE_INDEX, 203);
+        continue;
+      }
+      uint8_t* dst = (is_v ? p.c.v : p.c.k) + page * p.c.page_stride + h * p.c.head_stride;
+      float* scale_p = (is_v ? p.c.v_scale : p.c.k_scale) + page * p.c.scale_stride + h;
+      const float old = s0 > 0 ? *scale_p : 0.0f;
+      float x[kRows][8];
+      float top = 0.0f;
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) {
+        const int row = grp + i * groups;
+        unpack_row(raw[i], x[i]);
+        if (!is_v && p.rot_dim && row >= s0 && row < s1) {
+          const int64_t pos = p.positions ? (int64_t)p.positions[t_row0 + row] : (int64_t)b * P + row;
+          if (pos >= 0 && pos < p.rope_rows)
+            rotate8<kInter>(x[i], ln, load_turn(p.rope + pos * p.rot_dim, p.rot_dim, ln));
+          else if (lane16 == 0)   // the row is stored unrotated
+            record_error(p.status, KDA_ERR_BAD_CACHE_INDEX, 204);
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(x[i][e]));
+      }
+      if (top > 3.402823466e38f) {   // an infinity: the maximum of the finite ones
+        top = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kRows; ++i)
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (fabsf(x[i][e]) <= 3.402823466e38f) top = fmaxf(top, fabsf(x[i][e]));
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      if ((tid & 31) == 0) top_s[par][warp] = top;
+      __syncthreads();              // (the other parity's readers are past the barrier before this)
+      for (int w = 0; w < warps; ++w) top = fmaxf(top, top_s[par][w]);
+      float scale = pow2_scale(top);
+      if (s0 > 0) scale = fmaxf(scale, old);
+      const float inv = 1.0f / scale;
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) {
+        const int row = grp + i * groups;
+        if (row >= s0 && row < s1) {
+          uint8_t* w = dst + row * p.c.token_stride;
+          *reinterpret_cast<uint32_t*>(w + ln.c0) = e4m3x4(x[i][0] * inv, x[i][1] * inv, x[i][2] * inv, x[i][3] * inv);
+          *reinterpret_cast<uint32_t*>(w + ln.c1) = e4m3x4(x[i][4] * inv, x[i][5] * inv, x[i][6] * inv, x[i][7] * inv);
+        }
+      }
+      if (s0 > 0 && scale > old) {   // the page's older rows, brought to the new scale
+        const float ratio = old * inv;
+        uint2 kept[kRows];
+#pragma unroll
+        for (int i = 0; i < kRows; ++i)
+          if (grp + i * groups < s0)
+            kept[i] = *reinterpret_cast<const uint2*>(dst + (grp + i * groups) * p.c.token_stride + 8 * lane16);
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+          if (grp + i * groups >= s0) continue;
+          const float2 a = from_e4m3x2(kept[i].x & 0xffff), b2 = from_e4m3x2(kept[i].x >> 16);
+          const float2 c = from_e4m3x2(kept[i].y & 0xffff), d = from_e4m3x2(kept[i].y >> 16);
+          *reinterpret_cast<uint2*>(dst + (grp + i * groups) * p.c.token_stride + 8 * lane16) =
+              make_uint2(e4m3x4(a.x * ratio, a.y * ratio, b2.x * ratio, b2.y * ratio),
+                         e4m3x4(c.x * ratio, c.y * ratio, d.x * ratio, d.y * ratio));
+        }
+      }
+      if (tid == 0 && (s0 == 0 || scale > old)) *scale_p = scale;
+    }
+    return;
+  }
+  // ---- queries: 16 lanes a (token, kHeads heads)
+  const int units = (p.heads + kHeads - 1) / kHeads;
+  const int64_t u0 = ((int64_t)blockIdx.x - page_ctas) * groups, u = u0 + grp;
+  const int64_t t = u / units, tok0 = u0 / units;
+  const int64_t tokens = min((int64_t)cu[N], p.total_tokens);
+  const int h0 = (int)(u % units) * kHeads;
+  Row8 raw[kHeads];
+#pragma unroll
+  for (int i = 0; i < kHeads; ++i)
+    if (t < tokens && h0 + i < p.heads) raw[i] = load_row(p.q + t * p.q_stride + (h0 + i) * kHeadDim, ln);
+  int64_t pos = 0;
+  if (p.rot_dim && !p.positions) {
+    // cache positions of this CTA's tokens (at most one per group), found as the slots are
+    const int64_t tok1 = min(tokens, (u0 + groups - 1) / units + 1);
+    if (N <= kSearchRounds * (int)blockDim.x) {
+      for (int n = tid; n < N; n += blockDim.x) {
+        const int64_t a = cu[n], b = cu[n + 1], len = p.c.kv_lens[n];
+        for (int64_t x = max(a, tok0); x < min(b, tok1); ++x) pos_s[x - tok0] = len - (b - x);
+      }
+    } else if (tid < tok1 - tok0) {
+      const int n = seq_of(cu, N, tok0 + tid);
+      pos_s[tid] = (int64_t)p.c.kv_lens[n] - ((int64_t)cu[n + 1] - (tok0 + tid));
+    }
+    __syncthreads();
+    if (t < tokens) pos = pos_s[t - tok0];
+  } else if (p.rot_dim && t < tokens) {
+    pos = p.positions[t];
+  }
+  if (t >= tokens) return;
+  const bool turns = p.rot_dim && pos >= 0 && pos < p.rope_rows;
+  Turn tn;
+  if (turns) tn = load_turn(p.rope + pos * p.rot_dim, p.rot_dim, ln);
+  else if (p.rot_dim && lane16 == 0) record_error(p.status, KDA_ERR_BAD_CACHE_INDEX, 205);
+#pragma unroll
+  for (int i = 0; i < kHeads; ++i) {
+    if (h0 + i >= p.heads) break;
+    float x[8];
+    unpack_row(raw[i], x);
+    if (turns) rotate8<kInter>(x, ln, tn);
+    const uint4 o = pack8(x);
+    __nv_bfloat16* dst = p.q_out + t * p.qo_stride + (h0 + i) * kHeadDim;
+    *reinterpret_cast<uint2*>(dst + ln.c0) = make_uint2(o.x, o.y);
+    *reinterpret_cast<uint2*>(dst + ln.c1) = make_uint2(o.z, o.w);
+  }
+}
+
+template <int kRows, int kHeads, int kThreads>
+cudaError_t launch_heads(const AppendParams& p, int sms, cudaStream_t stream) {
+  const int64_t resident = (int64_t)sms * (65536 / kRegs / kThreads);
+  // at most so many units: every sequence has a partial page at both ends
+  const int64_t most = 2 * (p.total_tokens / p.c.page_size + 2 * (int64_t)p.num_seqs) * p.c.kv_heads;
+  const int page_ctas = (int)(most < resident ? most : resident);
+  const int64_t units = p.q ? p.total_tokens * ((p.heads + kHeads - 1) / kHeads) : 0;
+  const int64_t grid = page_ctas + (units + kThreads / 16 - 1) / (kThreads / 16);
   if (grid > 0x7fffffff) return cudaErrorInvalidValue;
   if (p.interleaved)
-    kda_append_kernel<kRows, true><<<(unsigned)grid, threads, 0, stream>>>(p, page_ctas);
+    kda_append_kernel<kRows, kHeads, kThreads, true><<<(unsigned)grid, kThreads, 0, stream>>>(p, page_ctas);
   else
-    kda_append_kernel<kRows, false><<<(unsigned)grid, threads, 0, stream>>>(p, page_ctas);
+    kda_append_kernel<kRows, kHeads, kThreads, false><<<(unsigned)grid, kThreads, 0, stream>>>(p, page_ctas);
   return cudaGetLastError();
+}
+
+// Query heads of a token that share one read of its table row: 4 where there are tokens enough
+// to fill the GPU all the same, else 2 for the shorter chain.
+template <int kRows, int kThreads>
+cudaError_t launch_rows(const AppendParams& p, int sms, cudaStream_t stream) {
+  return p.total_tokens >= 1024 ? launch_heads<kRows, 4, kThreads>(p, sms, stream)
+                                : launch_heads<kRows, 2, kThreads>(p, sms, stream);
 }
 
 }  // namespace
 
-// Page sizes 16 to 128: 16 lanes a row and half of the threads for the keys, so that a group
-// takes 2, 4 or 8 rows, and 8 rows of 8 fp32 values stay in its registers.
-cudaError_t launch_append(const AppendParams& p, cudaStream_t stream) {
+// Page sizes 16 to 128: a group of 16 lanes takes one or two rows, whose fp32 values and table
+// entries fit 64 registers.
+cudaError_t launch_append(const AppendParams& p, int sms, cudaStream_t stream) {
   switch (p.c.page_size) {
-    case 16: return launch_rows<2>(p, 256, stream);
-    case 32: return launch_rows<4>(p, 256, stream);
-    case 64: return launch_rows<8>(p, 256, stream);
-    default: return launch_rows<8>(p, 512, stream);   // 128
+    case 16: return launch_rows<1, 256>(p, sms, stream);
+    case 32: return launch_rows<2, 256>(p, sms, stream);
+    case 64: return launch_rows<2, 512>(p, sms, stream);
+    default: return launch_rows<2, 1024>(p, sms, stream);   // 128
   }
 }
 

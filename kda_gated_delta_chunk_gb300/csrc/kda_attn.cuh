@@ -109,7 +109,7 @@ struct AppendParams {
   int32_t num_seqs, heads;
   int* status;
 };
-cudaError_t launch_append(const AppendParams& p, cudaStream_t stream);
+cudaError_t launch_append(const AppendParams& p, int sms, cudaStream_t stream);
 
 struct AttnParams {
   const __nv_bfloat16* q;

@@ -44,7 +44,7 @@ constexpr int kOffK = kOffVB + 2 * 32768;                   // [kKStages] K tile
 constexpr int kOffV8 = kOffK + kKStages * 16384;            // [kVStages] V tiles
 constexpr int kOffSc = kOffV8 + kVStages * 16384;           // float4 [4][8]: k scale, log2 v scale, 1 / v scale
 constexpr int kOffBars = kOffSc + 4 * 8 * 16;
-constexpr int kNumBars = 2 * kKStages + 2 * kVStages + 4 + 2 * 5 + 1 + 4;
+constexpr int kNumBars = 2 * kKStages + 2 * kVStages + 4 + 2 * 6 + 4;
 constexpr int kOffMiscP = kOffBars + 8 * kNumBars;
 constexpr int kSmemP = kOffMiscP + 256 + 1024;
 static_assert(kSmemP <= 227 * 1024, "shared memory");
@@ -128,7 +128,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
   const uint32_t bar_vf = bar_ke + 8 * kKStages, bar_ve = bar_vf + 8 * kVStages;
   const uint32_t bar_bf = bar_ve + 8 * kVStages, bar_be = bar_bf + 16;       // widened V
   const uint32_t bar_q = bar_be + 16, bar_s = bar_q + 16, bar_p = bar_s + 16, bar_o = bar_p + 16;
-  const uint32_t bar_of = bar_o + 16, bar_end = bar_of + 16, bar_sc = bar_end + 8;   // bar_sc: scales
+  const uint32_t bar_of = bar_o + 16, bar_end = bar_of + 16, bar_sc = bar_end + 16;   // bar_sc: scales
   struct Misc {
     long long part[16];
     long long rest;          // first tile's place in its sequence
@@ -157,8 +157,8 @@ __global__ void __launch_bounds__(kThreadsP, 1)
       mbar_init(bar_p + 8 * i, 128);
       mbar_init(bar_o + 8 * i, 1);
       mbar_init(bar_of + 8 * i, 128);
+      mbar_init(bar_end + 8 * i, 1);
     }
-    mbar_init(bar_end, 1);
     for (int i = 0; i < 4; ++i) mbar_init(bar_sc + 8 * i, 1);
     mbar_fence_init();
     for (int i = 0; i < 8; ++i) misc->poison[i] = 0;
@@ -346,57 +346,68 @@ __global__ void __launch_bounds__(kThreadsP, 1)
       for (uint32_t i = it > kVStages ? it - kVStages : 0; i < it; ++i)
         mbar_wait(bar_vf + 8 * (i % kVStages), (i / kVStages) & 1);
     } else if (warp == 13) {
-      // ================= MMA issuer
-      if (elect_one()) {
-        constexpr uint32_t id_s = idesc_e4m3(128, 128, 0, 0), id_o = idesc_bf16(128, 128, 0, 1);
-        uint32_t it = 0, seg = 0;
-        bool ok = true;
-        auto qk = [&](uint32_t i, int h) {               // S of tile i, half h
-          const uint32_t k = sb + kOffK + (i % kKStages) * 16384, q = sb + kOffQ + h * 32768;
+      // ================= MMA issuer (the warp stays together; one lane issues)
+      constexpr uint32_t id_s = idesc_e4m3(128, 128, 0, 0), id_o = idesc_bf16(128, 128, 0, 1);
+      const uint32_t lead = elect_one() ? 1u : 0u;
+      const uint64_t dq = kmajor8(sb + kOffQ, 0), dk0 = kmajor8(sb + kOffK, 0);
+      const uint64_t dv0 = sdesc_sw128(sb + kOffVB, 16384, 1024);
+      uint32_t it = 0, seg = 0;
+      bool ok = true;
+      auto qk = [&](uint32_t i, int h) {                 // S of tile i, half h
+        const uint64_t dk = dk0 + (i % kKStages) * (16384 >> 4), q = dq + h * (32768 >> 4);
 #pragma unroll
-          for (int x = 0; x < 8; ++x)
-            mma_e4m3(tmem + kTS + 128 * h, kmajor8(q + (x >> 2) * 16384, x & 3), kmajor8(k, x & 3), id_s, x > 0);
-          mma_commit(bar_s + 8 * h);
-        };
-        auto pv = [&](uint32_t i, int h, bool first_tile) {   // O of half h += P(i) V(i)
-          ok = ok && mbar_wait(bar_p + 8 * h, i & 1);
-          if (h == 0) ok = ok && mbar_wait(bar_bf + 8 * (i & 1), (i >> 1) & 1);
-          // (the segment before has read its O)
-          if (first_tile && seg > 0) ok = ok && mbar_wait(bar_of + 8 * h, (seg - 1) & 1);
-          if (!ok) return;
+        for (int x = 0; x < 8; ++x)
+          mma_e4m3_on(lead, tmem + kTS + 128 * h, q + ((x >> 2) * 16384 + (x & 3) * 32) / 16,
+                      dk + (x & 3) * 32 / 16, id_s, x > 0);
+        mma_commit_on(lead, bar_s + 8 * h);
+      };
+      auto pv = [&](uint32_t i, int h, bool first_tile) {   // O of half h += P(i) V(i)
+        // (the segment before has read its O)
+        if (first_tile && seg > 0) ok = ok && mbar_wait(bar_of + 8 * h, (seg - 1) & 1);
+        ok = ok && mbar_wait(bar_p + 8 * h, i & 1);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) return;
+        tc_fence_after();
+        const uint64_t dv = dv0 + (i & 1) * (32768 >> 4);
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks)
+          mma_bf16_ts_on(lead, tmem + kTOP + 128 * h, tmem + kTS + 128 * h + 8 * ks, dv + 2048 * ks / 16,
+                         id_o, !(first_tile && ks == 0));
+        mma_commit_on(lead, bar_o + 8 * h);
+      };
+      while (ok && walk.next(p)) {
+        for (int t = walk.a; t < walk.b && ok; ++t, ++it) {
+          // what the tile needs besides P: its keys, and the values of the tile before
+          ok = mbar_wait(bar_kf + 8 * (it % kKStages), (it / kKStages) & 1);
+          if (t > walk.a) ok = ok && mbar_wait(bar_bf + 8 * ((it - 1) & 1), ((it - 1) >> 1) & 1);
+          else ok = ok && mbar_wait(bar_q, seg & 1) && mbar_wait(bar_q + 8, seg & 1);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
           tc_fence_after();
-          const uint32_t v = sb + kOffVB + (i & 1) * 32768;
-#pragma unroll
-          for (int ks = 0; ks < 8; ++ks)
-            mma_bf16_ts(tmem + kTOP + 128 * h, tmem + kTS + 128 * h + 8 * ks,
-                        sdesc_sw128(v + 2048 * ks, 16384, 1024), id_o, !(first_tile && ks == 0));
-          mma_commit(bar_o + 8 * h);
-          if (h == 1) mma_commit(bar_be + 8 * (i & 1));
-        };
-        while (ok && walk.next(p)) {
-          for (int t = walk.a; t < walk.b && ok; ++t, ++it) {
-            for (int h = 0; h < 2 && ok; ++h) {
-              if (t > walk.a) pv(it - 1, h, t - 1 == walk.a);
-              else ok = mbar_wait(bar_q + 8 * h, seg & 1);
-              if (h == 0) ok = ok && mbar_wait(bar_kf + 8 * (it % kKStages), (it / kKStages) & 1);
-              if (!ok) break;
-              tc_fence_after();
-              qk(it, h);
-            }
-            if (ok) mma_commit(bar_ke + 8 * (it % kKStages));
+          if (t > walk.a) pv(it - 1, 0, t - 1 == walk.a);
+          if (!ok) break;
+          qk(it, 0);
+          if (t > walk.a) {
+            pv(it - 1, 1, t - 1 == walk.a);
+            if (!ok) break;
+            mma_commit_on(lead, bar_be + 8 * ((it - 1) & 1));
           }
-          for (int h = 0; h < 2 && ok; ++h) pv(it - 1, h, walk.b - 1 == walk.a);
-          ++seg;
+          qk(it, 1);
+          mma_commit_on(lead, bar_ke + 8 * (it % kKStages));
         }
-        if (!ok) record_error(p.a.status, KDA_ERR_DEVICE_TIMEOUT, 334);
-        // what was issued ends, its arrivals included, before shared and tensor memory go
-        mma_commit(bar_end);
-        mbar_wait(bar_end, 0);
-        for (uint32_t i = it > kKStages ? it - kKStages : 0; ok && i < it; ++i)
-          mbar_wait(bar_ke + 8 * (i % kKStages), (i / kKStages) & 1);
-        for (uint32_t i = it > 2 ? it - 2 : 0; ok && i < it; ++i)
-          mbar_wait(bar_be + 8 * (i & 1), (i >> 1) & 1);
+        if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar_bf + 8 * ((it - 1) & 1), ((it - 1) >> 1) & 1));
+        for (int h = 0; h < 2 && ok; ++h) pv(it - 1, h, walk.b - 1 == walk.a);
+        if (ok) mma_commit_on(lead, bar_be + 8 * ((it - 1) & 1));
+        ++seg;
       }
+      if (!ok && lead) record_error(p.a.status, KDA_ERR_DEVICE_TIMEOUT, 334);
+      // what was issued ends, its arrivals included, before shared and tensor memory go
+      mma_commit_on(lead, bar_end);
+      mbar_wait(bar_end, 0);
+      for (uint32_t i = it > kKStages ? it - kKStages : 0; ok && i < it; ++i)
+        mbar_wait(bar_ke + 8 * (i % kKStages), (i / kKStages) & 1);
+      for (uint32_t i = it > 2 ? it - 2 : 0; ok && i < it; ++i)
+        mbar_wait(bar_be + 8 * (i & 1), (i >> 1) & 1);
       __syncwarp();
     }
   } else if (warp >= 8) {
@@ -533,10 +544,10 @@ __global__ void __launch_bounds__(kThreadsP, 1)
 
       float m = -INFINITY, l = 0.0f;
       for (int t = walk.a; t < walk.b; ++t, ++it) {
-        ok = mbar_wait(bar_s + 8 * half, it & 1);
-        ok = ok && mbar_wait(bar_sc + 8 * (it & 3), (it >> 2) & 1);
-        // (done by now: S of this tile was issued after O of the one before)
+        // (a wait costs over 100 cycles even when it need not wait: S, the last to come, last)
+        ok = mbar_wait(bar_sc + 8 * (it & 3), (it >> 2) & 1);
         if (t > walk.a) ok = ok && mbar_wait(bar_o + 8 * half, (it - 1) & 1);
+        ok = ok && mbar_wait(bar_s + 8 * half, it & 1);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
@@ -702,48 +713,46 @@ __global__ void __launch_bounds__(kThreadsP, 1)
 }
 
 // Merges the parts of the item that CTA blockIdx.x began and did not finish, in CTA order: a warp
-// takes 4 rows, a lane 4 channels.
-constexpr int kMergeRows = 16;
-__global__ void __launch_bounds__(128) kda_attn_prefill_merge_kernel(const __grid_constant__ PrefillParams p) {
+// a row, a lane 4 channels.
+constexpr int kMergeRows = 8;
+__global__ void __launch_bounds__(32 * kMergeRows)
+    kda_attn_prefill_merge_kernel(const __grid_constant__ PrefillParams p) {
   pdl_wait();
   const PartDescP d = p.desc[blockIdx.x];
   if (d.parts == 0) return;
   const int lane = threadIdx.x & 31, G = p.a.heads / p.a.c.kv_heads;
   const int tok0 = p.a.cu_seqlens[d.n], q_len = p.a.cu_seqlens[d.n + 1] - tok0;
   const int first = d.rt * p.tokens, rows = min(p.tokens, q_len - first) * G;
+  const int r = blockIdx.y * kMergeRows + (threadIdx.x >> 5);
+  if (r >= rows) return;
   auto slot = [&](int i) {
     return p.slots + ((int64_t)2 * (blockIdx.x + i) + (i == 0 ? 1 : 0)) * kSlotFloatsP;
   };
-#pragma unroll 1
-  for (int j = 0; j < kMergeRows / 4; ++j) {
-    const int r = blockIdx.y * kMergeRows + 4 * j + (threadIdx.x >> 5);
-    if (r >= rows) return;
-    float m = -INFINITY;
-    for (int i = lane; i < d.parts; i += 32) m = fmaxf(m, slot(i)[kRowsP * 128 + r]);
+  float m = -INFINITY;
+  for (int i = lane; i < d.parts; i += 32) m = fmaxf(m, slot(i)[kRowsP * 128 + r]);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    const float ref = m == -INFINITY ? 0.0f : m;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    float den = 0.0f;
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  const float ref = m == -INFINITY ? 0.0f : m;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float den = 0.0f;
 #pragma unroll 4
-    for (int i = 0; i < d.parts; ++i) {
-      const float* s = slot(i);
-      const float w = ex2(s[kRowsP * 128 + r] - ref);
-      const float4 a = *reinterpret_cast<const float4*>(s + r * 128 + 4 * lane);
-      den += s[kRowsP * 129 + r] * w;
-      acc.x += a.x * w;
-      acc.y += a.y * w;
-      acc.z += a.z * w;
-      acc.w += a.w * w;
-    }
-    const float il = den == 0.0f ? 0.0f : 1.0f / den;
-    const int64_t tok = tok0 + first + r / G;
-    const int head = d.h * G + r % G;
-    const uint2 o2 = make_uint2(bf16x2_of(acc.x * il, acc.y * il), bf16x2_of(acc.z * il, acc.w * il));
-    *reinterpret_cast<uint2*>(p.a.out + tok * p.a.out_stride + head * kHeadDim + 4 * lane) = o2;
-    if (p.a.lse && lane == 0)
-      p.a.lse[tok * p.a.heads + head] = den == 0.0f ? -INFINITY : (m + lg2(den)) * kLn2;
+  for (int i = 0; i < d.parts; ++i) {
+    const float* s = slot(i);
+    const float w = ex2(s[kRowsP * 128 + r] - ref);
+    const float4 a = *reinterpret_cast<const float4*>(s + r * 128 + 4 * lane);
+    den += s[kRowsP * 129 + r] * w;
+    acc.x += a.x * w;
+    acc.y += a.y * w;
+    acc.z += a.z * w;
+    acc.w += a.w * w;
   }
+  const float il = den == 0.0f ? 0.0f : 1.0f / den;
+  const int64_t tok = tok0 + first + r / G;
+  const int head = d.h * G + r % G;
+  const uint2 o2 = make_uint2(bf16x2_of(acc.x * il, acc.y * il), bf16x2_of(acc.z * il, acc.w * il));
+  *reinterpret_cast<uint2*>(p.a.out + tok * p.a.out_stride + head * kHeadDim + 4 * lane) = o2;
+  if (p.a.lse && lane == 0)
+    p.a.lse[tok * p.a.heads + head] = den == 0.0f ? -INFINITY : (m + lg2(den)) * kLn2;
 }
 
 template <bool kCap>
@@ -767,7 +776,7 @@ cudaError_t launch_cap(const PrefillParams& d, int sms, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)sms, kRowsP / kMergeRows);
-  cfg.blockDim = dim3(128);
+  cfg.blockDim = dim3(32 * kMergeRows);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -187,7 +187,7 @@ int kda_rope_append(const void* q, int64_t q_stride, const void* k, int64_t k_st
   p.num_seqs = num_seqs;
   p.heads = heads;
   p.status = static_cast<int*>(workspace);
-  return launched(kda::attn::launch_append(p, reinterpret_cast<cudaStream_t>(stream)));
+  return launched(kda::attn::launch_append(p, sms, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 size_t kda_attention_workspace_size(int32_t num_seqs, int32_t heads, int32_t kv_heads,

@@ -21,6 +21,12 @@ from . import (ERR_INVALID_ARG, HEAD_DIM, KDAError, OK, STATE_BF16, STATE_F32, l
 
 _BF16, _F32 = torch.bfloat16, torch.float32
 _BYTES = (torch.float8_e4m3fn, torch.uint8)
+_HALF, _EITHER = (_BF16,), (_BF16, _F32)
+_FLOAT = (_F32,)
+_INT = (torch.int32,)
+# the current stream's handle without a Stream object around it (a call's host time counts in decode)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 class _Cache(ctypes.Structure):
@@ -35,6 +41,9 @@ class _Cache(ctypes.Structure):
 
 def _check(t, name, dtypes, shape, dev, dense_from=1):
     """Type, device and shape; dimensions from ``dense_from`` on are dense."""
+    if (isinstance(t, torch.Tensor) and t.device == dev and t.dtype in dtypes and t.shape == shape
+            and t.is_contiguous()):
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
@@ -45,14 +54,13 @@ def _check(t, name, dtypes, shape, dev, dense_from=1):
         raise TypeError(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.is_contiguous():
-        return
     inner = 1
-    for size, stride in zip(reversed(t.shape[dense_from:]), reversed(t.stride()[dense_from:])):
-        if size > 1 and stride != inner:
+    sizes, strides = t.shape, t.stride()
+    for d in range(len(sizes) - 1, dense_from - 1, -1):
+        if strides[d] != inner and sizes[d] > 1:
             raise ValueError(f"{name}: only the first {dense_from} dimension(s) may be strided"
                              if dense_from else f"{name} must be contiguous")
-        inner *= size
+        inner *= sizes[d]
 
 
 def _row_stride(t, dense):
@@ -60,34 +68,35 @@ def _row_stride(t, dense):
 
 
 def _stream(stream, dev):
-    return (stream if stream is not None else torch.cuda.current_stream(dev)).cuda_stream
+    return stream.cuda_stream if stream is not None else _raw_stream(dev.index)
 
 
 def _cache(k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, num_seqs, dev):
-    if k_cache.dim() != 4:
+    shape = k_cache.shape
+    if len(shape) != 4:
         raise ValueError("k_cache must be [pages, kv_heads, page_size, 128]")
-    pages, hk, page, d = k_cache.shape
+    pages, hk, page, d = shape
     if d != HEAD_DIM:
         raise KDAError(ERR_INVALID_ARG, f"head_dim {d} (only {HEAD_DIM} is supported)")
-    _check(k_cache, "k_cache", _BYTES, k_cache.shape, dev, 3)
-    _check(v_cache, "v_cache", _BYTES, k_cache.shape, dev, 3)
-    if v_cache.stride() != k_cache.stride():
+    _check(k_cache, "k_cache", _BYTES, shape, dev, 3)
+    _check(v_cache, "v_cache", _BYTES, shape, dev, 3)
+    st, sc = k_cache.stride(), k_scale.stride()
+    if v_cache.stride() != st:
         raise ValueError("k_cache and v_cache must have the same strides")
-    _check(k_scale, "k_scale", (_F32,), (pages, hk), dev)
-    _check(v_scale, "v_scale", (_F32,), (pages, hk), dev)
-    if v_scale.stride() != k_scale.stride():
+    _check(k_scale, "k_scale", _FLOAT, (pages, hk), dev)
+    _check(v_scale, "v_scale", _FLOAT, (pages, hk), dev)
+    if v_scale.stride() != sc:
         raise ValueError("k_scale and v_scale must have the same strides")
     if block_table.dim() != 2:
         raise ValueError("block_table must be [num_seqs, max_blocks]")
     blocks = block_table.shape[1]
-    _check(block_table, "block_table", (torch.int32,), (num_seqs, blocks), dev)
-    _check(kv_lens, "kv_lens", (torch.int32,), (num_seqs,), dev, 0)
+    _check(block_table, "block_table", _INT, (num_seqs, blocks), dev)
+    _check(kv_lens, "kv_lens", _INT, (num_seqs,), dev, 0)
     # dimensions of one element take the dense stride: torch leaves theirs arbitrary
-    st = k_cache.stride()
     tok = st[2] if page > 1 else HEAD_DIM
     head = st[1] if hk > 1 else page * tok
     return _Cache(k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
-                  st[0] if pages > 1 else hk * head, head, tok, _row_stride(k_scale, hk), pages,
+                  st[0] if pages > 1 else hk * head, head, tok, sc[0] if pages > 1 else hk, pages,
                   page, hk, blocks, block_table.data_ptr(), _row_stride(block_table, blocks),
                   kv_lens.data_ptr())
 
@@ -153,10 +162,10 @@ def add_rms_norm(x, residual, weight, eps: float = 1e-6, want: str = "bf16", gro
         raise ValueError(f"want must be 'bf16', 'fp8' or 'both', got {want!r}")
     dev = x.device
     T, C = x.shape
-    _check(x, "x", (_BF16,), x.shape, None)
-    _check(weight, "weight", (_BF16, _F32), (C,), dev, 0)
+    _check(x, "x", _HALF, x.shape, None)
+    _check(weight, "weight", _EITHER, (C,), dev, 0)
     if residual is not None:
-        _check(residual, "residual", (_BF16, _F32), x.shape, dev)
+        _check(residual, "residual", _EITHER, x.shape, dev)
         if residual_out is None:
             residual_out = torch.empty((T, C), dtype=residual.dtype, device=dev)
         else:
@@ -169,7 +178,7 @@ def add_rms_norm(x, residual, weight, eps: float = 1e-6, want: str = "bf16", gro
     elif y is None:
         y = torch.empty((T, C), dtype=_BF16, device=dev)
     else:
-        _check(y, "y", (_BF16,), x.shape, dev)
+        _check(y, "y", _HALF, x.shape, dev)
     if want == "bf16":
         if y8 is not None or y_scale is not None:
             raise ValueError("y8 and y_scale are not written with want='bf16'")
@@ -182,14 +191,17 @@ def add_rms_norm(x, residual, weight, eps: float = 1e-6, want: str = "bf16", gro
         if y_scale is None:
             y_scale = torch.empty((T, groups), dtype=_F32, device=dev)
         else:
-            _check(y_scale, "y_scale", (_F32,), (T, groups), dev, 0)
-    ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
-    ld = lambda t: C if t is None else _row_stride(t, C)  # noqa: E731
-    kind = lambda t: STATE_F32 if t is not None and t.dtype == _F32 else STATE_BF16  # noqa: E731
-    rc = lib().kda_add_rms_norm(ptr(x), ld(x), ptr(residual), ld(residual), kind(residual),
-                                ptr(weight), kind(weight), float(eps), ptr(residual_out),
-                                ld(residual_out), ptr(y), ld(y), ptr(y8), ld(y8), ptr(y_scale),
-                                int(group), T, C, _stream(stream, dev))
+            _check(y_scale, "y_scale", _FLOAT, (T, groups), dev, 0)
+    has_r, has_y, has_8 = residual is not None, y is not None, y8 is not None
+    rc = lib().kda_add_rms_norm(
+        x.data_ptr(), _row_stride(x, C), residual.data_ptr() if has_r else None,
+        _row_stride(residual, C) if has_r else C,
+        STATE_F32 if has_r and residual.dtype == _F32 else STATE_BF16, weight.data_ptr(),
+        STATE_F32 if weight.dtype == _F32 else STATE_BF16, eps,
+        residual_out.data_ptr() if has_r else None, _row_stride(residual_out, C) if has_r else C,
+        y.data_ptr() if has_y else None, _row_stride(y, C) if has_y else C,
+        y8.data_ptr() if has_8 else None, _row_stride(y8, C) if has_8 else C,
+        y_scale.data_ptr() if has_8 else None, group, T, C, _stream(stream, dev))
     if rc != OK:
         raise KDAError(rc, "kda_add_rms_norm")
     return residual_out, y, y8, y_scale
@@ -213,29 +225,29 @@ def rope_append(q, k, v, rope, k_cache, v_cache, k_scale, v_scale, block_table, 
     if d != HEAD_DIM:
         raise KDAError(ERR_INVALID_ARG, f"head_dim {d} (only {HEAD_DIM} is supported)")
     N = cu_seqlens.numel() - 1
-    _check(k, "k", (_BF16,), k.shape, None)
-    _check(v, "v", (_BF16,), k.shape, dev)
+    _check(k, "k", _HALF, k.shape, None)
+    _check(v, "v", _HALF, k.shape, dev)
     heads = hk
     if q is not None:
         if q.dim() != 3:
             raise ValueError("q must be [T, heads, 128]")
         heads = q.shape[1]
-        _check(q, "q", (_BF16,), (T, heads, d), dev)
+        _check(q, "q", _HALF, (T, heads, d), dev)
         if q_out is None:
             q_out = torch.empty((T, heads, d), dtype=_BF16, device=dev)
         else:
-            _check(q_out, "q_out", (_BF16,), (T, heads, d), dev)
+            _check(q_out, "q_out", _HALF, (T, heads, d), dev)
     elif q_out is not None:
         raise ValueError("q_out needs q")
-    _check(cu_seqlens, "cu_seqlens", (torch.int32,), (N + 1,), dev, 0)
+    _check(cu_seqlens, "cu_seqlens", _INT, (N + 1,), dev, 0)
     rows = rot = 0
     if rope is not None:
         if rope.dim() != 2:
             raise ValueError("rope must be [rows, rot_dim]")
         rows, rot = rope.shape
-        _check(rope, "rope", (_F32,), rope.shape, dev, 0)
+        _check(rope, "rope", _FLOAT, rope.shape, dev, 0)
     if positions is not None:
-        _check(positions, "positions", (torch.int32,), (T,), dev, 0)
+        _check(positions, "positions", _INT, (T,), dev, 0)
     c = _cache(k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, N, dev)
     if c.kv_heads != hk:
         raise ValueError(f"k has {hk} heads, the cache {c.kv_heads}")
@@ -283,19 +295,19 @@ def cached_attention(q, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens
     if d != HEAD_DIM:
         raise KDAError(ERR_INVALID_ARG, f"head_dim {d} (only {HEAD_DIM} is supported)")
     N = cu_seqlens.numel() - 1
-    _check(q, "q", (_BF16,), q.shape, None)
-    _check(cu_seqlens, "cu_seqlens", (torch.int32,), (N + 1,), dev, 0)
+    _check(q, "q", _HALF, q.shape, None)
+    _check(cu_seqlens, "cu_seqlens", _INT, (N + 1,), dev, 0)
     c = _cache(k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, N, dev)
     if out is None:
         out = torch.empty((T, heads, d), dtype=_BF16, device=dev)
     else:
-        _check(out, "out", (_BF16,), q.shape, dev)
+        _check(out, "out", _HALF, q.shape, dev)
     if lse is True:
         lse = torch.empty((T, heads), dtype=_F32, device=dev)
     elif lse is False:
         lse = None
     else:
-        _check(lse, "lse", (_F32,), (T, heads), dev, 0)
+        _check(lse, "lse", _FLOAT, (T, heads), dev, 0)
     if workspace is None:
         workspace = alloc_attention_workspace(N, heads, c.kv_heads, max_q_len, dev)
     else:
