@@ -15,7 +15,8 @@
 // Bound by the cache's bytes (2 x 128 per key and kv head; the products take a few percent of the
 // tensor cores).  So that every SM streams the same amount whatever the lengths, the tiles
 // of all (sequence, kv head) items are laid end to end and cut into one equal range per CTA, two
-// CTAs per SM, each with three 32 KB stages in flight.  A CTA's range covers the end of one
+// CTAs per SM, each with three 32 KB stages in flight; an item counts kOver tiles more than it
+// has, for the time that its queries and its end take.  A CTA's range covers the end of one
 // item, whole items and the beginning of another; the (at most two) partial results go to the
 // workspace and a second kernel, launched as the first's programmatic dependent, merges them.
 //
@@ -33,6 +34,8 @@ namespace {
 
 constexpr int kThreads = 192;
 constexpr int kStageBytes = 2 * kTile * kHeadDim;   // K and V
+constexpr int kOver = 2;                             // tiles' worth of time an item takes besides its tiles
+constexpr int kCached = 32;                          // sequences whose lengths a CTA keeps in shared memory
 constexpr float kPScale = 256.0f;                    // largest numerator, in the e4m3 operand
 
 template <int NR>
@@ -52,7 +55,8 @@ struct Cfg {
   static constexpr int kOffScale = kOffQmul + NR * 4;           // float [stages][2][8]
   static constexpr int kOffBar = kOffScale + kStages * 64;      // full, empty, s[2], o, p, q, end
   static constexpr int kOffMisc = kOffBar + 8 * (2 * kStages + 6);
-  static constexpr int kBytes = kOffMisc + 128 + 1024;
+  static constexpr int kOffSeq = kOffMisc + 128;                // SeqInfo [kCached]
+  static constexpr int kBytes = kOffSeq + kCached * 20 + 1024;
 };
 
 // Workspace after the status words: desc [ctas], then per CTA two slots of [NR][128] sums,
@@ -71,28 +75,42 @@ struct DecodeParams {
   float* slots;
 };
 
-// The walk over a CTA's range of tiles, segment by segment (every role runs its own).
+// The walk over a CTA's range, segment by segment (every role runs its own).  The range is in
+// units: an item has kOver of them, then one per tile.
 struct Walk {
-  int64_t pos, end, base;   // global tile index; base: of sequence n's first
-  int n;
+  int64_t pos, end, base;   // global unit; base: of sequence n's first
+  int n, n0;                // sequence; the first of the cached ones
+  const SeqInfo* cache;
   SeqInfo s;
   int h, a, b;              // segment: kv head, tiles [a, b) of the item (relative to tile0)
   __device__ __forceinline__ bool next(const DecodeParams& p) {
-    if (pos >= end) return false;
-    while (true) {
-      const int64_t size = (int64_t)s.tiles * p.a.c.kv_heads;
-      if (pos < base + size) break;
-      base += size;
-      int err;
-      if (++n >= p.a.num_seqs) return false;   // (lengths that changed under the kernel)
-      s = seq_info(p.a, n, p.min_rows, p.max_rows, &err);
+    while (pos < end) {
+      while (true) {
+        const int64_t size = s.tiles ? (int64_t)(s.tiles + kOver) * p.a.c.kv_heads : 0;
+        if (pos < base + size) break;
+        base += size;
+        if (++n >= p.a.num_seqs) return false;   // (lengths that changed under the kernel)
+        if (n - n0 < kCached) {
+          s = cache[n - n0];
+        } else {
+          int err;
+          s = seq_info(p.a, n, p.min_rows, p.max_rows, &err);
+        }
+      }
+      const int size = s.tiles + kOver;
+      const int64_t x = pos - base;
+      h = (int)(x / size);
+      const int o = (int)(x % size), o1 = (int)min((int64_t)size, o + (end - pos));
+      pos += o1 - o;
+      a = max(0, o - kOver);
+      b = o1 - kOver;
+      if (b > a) return true;       // (else the range ends before the item's first tile)
     }
-    const int64_t x = pos - base;
-    h = (int)(x / s.tiles);
-    a = (int)(x % s.tiles);
-    b = (int)min((int64_t)s.tiles, a + (end - pos));
-    pos += b - a;
-    return true;
+    return false;
+  }
+  // unit of the segment's item that its tile t takes
+  __device__ __forceinline__ int64_t unit_of(int t) const {
+    return base + (int64_t)h * (s.tiles + kOver) + kOver + t;
   }
 };
 
@@ -146,7 +164,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     int err;
     const SeqInfo s = seq_info(p.a, n, p.min_rows, p.max_rows, &err);
     if (err != KDA_OK && report && blockIdx.x == 0) record_error(p.a.status, err, 311);
-    return (long long)s.tiles * hk;
+    return s.tiles ? (long long)(s.tiles + kOver) * hk : 0;
   };
   long long mine = 0, first = 0;
   for (int n0 = 0; n0 < N; n0 += kThreads) {
@@ -194,63 +212,88 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     walk.n = misc->start_n;
     walk.base = misc->start_base;
-    int err;
-    walk.s = seq_info(p.a, walk.n, p.min_rows, p.max_rows, &err);
+    walk.n0 = walk.n;
+    walk.cache = reinterpret_cast<const SeqInfo*>(sm + C::kOffSeq);
+    if (tid < kCached && walk.n + tid < N) {
+      int err;
+      reinterpret_cast<SeqInfo*>(sm + C::kOffSeq)[tid] = seq_info(p.a, walk.n + tid, p.min_rows, p.max_rows, &err);
+    }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = misc->tmem;
+  if (walk.pos < walk.end) walk.s = walk.cache[0];
 
   if (warp == 4) {
     // ================= producer: pages of each tile, K and V of one head
+    // A tile's pages are looked up two tiles ahead and its scales one, over the segments' ends.
     uint32_t it = 0;
     bool ok = true;
-    while (ok && walk.next(p)) {
-      const int32_t* bt = p.a.c.block_table + walk.n * p.a.c.table_stride;
-      const int boxes = kTile / P;                     // pages of a tile
-      const int used = (walk.s.len + P - 1) / P;       // pages of the sequence
-      // lanes below `boxes`: this tile's page (one tile ahead), with its scales
-      auto page_of = [&](int t) -> int {
-        const int b = (walk.s.tile0 + t) * boxes + lane;
-        if (lane >= boxes || t >= walk.b || b >= used) return -2;     // not loaded
-        const int pg = bt[b];
-        if (pg < 0 || pg >= p.a.c.num_pages) {
-          record_error(p.a.status, KDA_ERR_BAD_CACHE_INDEX, 312);
-          return p.a.c.num_pages;                      // outside the map: the load gives zeros
-        }
-        return pg;
-      };
-      auto scale_of = [&](const float* sc, int pg) -> float {
-        return pg >= 0 && pg < p.a.c.num_pages ? sc[(int64_t)pg * p.a.c.scale_stride + walk.h] : 1.0f;
-      };
-      int pg = page_of(walk.a);
-      for (int t = walk.a; t < walk.b && ok; ++t, ++it) {
-        const uint32_t st = it % kStages;
-        const float ks = scale_of(p.a.c.k_scale, pg), vs = scale_of(p.a.c.v_scale, pg);
-        const int pg_next = page_of(t + 1);
-        if (it >= kStages) ok = mbar_wait(bar_empty + 8 * st, (it / kStages - 1) & 1);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) {
-          if (lane == 0) record_error(p.a.status, KDA_ERR_DEVICE_TIMEOUT, 313);
-          break;
-        }
-        const uint32_t dst = sb + st * kStageBytes;
-        if (lane < boxes) {
-          float* sc = reinterpret_cast<float*>(sm + C::kOffScale + st * 64);
-          sc[lane] = ks;
-          sc[8 + lane] = vs;
-        }
-        const uint32_t loads = __popc(__ballot_sync(0xffffffffu, pg != -2));
-        __syncwarp();
-        if (lane == 0) mbar_expect_tx(bar_full + 8 * st, loads * 2 * P * kHeadDim);
-        __syncwarp();
-        if (pg != -2) {
-          tma_load_4d(dst + lane * P * 128, &p.maps.k, 0, 0, walk.h, pg, bar_full + 8 * st);
-          tma_load_4d(dst + kTile * 128 + lane * P * 128, &p.maps.v, 0, 0, walk.h, pg, bar_full + 8 * st);
-        }
-        pg = pg_next;
+    const int boxes = kTile / P;                         // pages of a tile
+    struct Ahead {
+      int h, pg;
+      bool more, load;   // more: there is such a tile; load: this lane fetches page pg of it
+    };
+    int t = 0;
+    bool in_seg = false;
+    auto look = [&]() -> Ahead {
+      if (!in_seg || t >= walk.b) {
+        in_seg = walk.next(p);
+        if (!in_seg) return {0, 0, false, false};
+        t = walk.a;
       }
+      const int b = (walk.s.tile0 + t++) * boxes + lane;
+      if (lane >= boxes || b >= (walk.s.len + P - 1) / P) return {walk.h, 0, true, false};
+      return {walk.h, p.a.c.block_table[walk.n * p.a.c.table_stride + b], true, true};
+    };
+    float ks = 1.0f, vs = 1.0f;
+    auto scales = [&](Ahead& x) {
+      ks = vs = 1.0f;
+      if (!x.load) return;
+      if (x.pg < 0 || x.pg >= p.a.c.num_pages) {
+        record_error(p.a.status, KDA_ERR_BAD_CACHE_INDEX, 312);
+        x.pg = p.a.c.num_pages;                          // outside the map: the load gives zeros
+        return;
+      }
+      ks = p.a.c.k_scale[(int64_t)x.pg * p.a.c.scale_stride + x.h];
+      vs = p.a.c.v_scale[(int64_t)x.pg * p.a.c.scale_stride + x.h];
+    };
+    Ahead cur = look(), nxt = {0, 0, false, false};
+    if (cur.more) {
+      scales(cur);
+      nxt = look();
+    }
+    for (; cur.more; ++it) {
+      const uint32_t st = it % kStages;
+      const float ks_now = ks, vs_now = vs;
+      Ahead after = {0, 0, false, false};
+      if (nxt.more) {
+        scales(nxt);
+        after = look();
+      }
+      if (it >= kStages) ok = mbar_wait(bar_empty + 8 * st, (it / kStages - 1) & 1);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) {
+        if (lane == 0) record_error(p.a.status, KDA_ERR_DEVICE_TIMEOUT, 313);
+        break;
+      }
+      const uint32_t dst = sb + st * kStageBytes;
+      if (lane < boxes) {
+        float* sc = reinterpret_cast<float*>(sm + C::kOffScale + st * 64);
+        sc[lane] = ks_now;
+        sc[8 + lane] = vs_now;
+      }
+      const uint32_t loads = __popc(__ballot_sync(0xffffffffu, cur.load));
+      __syncwarp();
+      if (lane == 0) mbar_expect_tx(bar_full + 8 * st, loads * 2 * P * kHeadDim);
+      __syncwarp();
+      if (cur.load) {
+        tma_load_4d(dst + lane * P * 128, &p.maps.k, 0, 0, cur.h, cur.pg, bar_full + 8 * st);
+        tma_load_4d(dst + kTile * 128 + lane * P * 128, &p.maps.v, 0, 0, cur.h, cur.pg, bar_full + 8 * st);
+      }
+      cur = nxt;
+      nxt = after;
     }
     // the copies in flight end before the CTA does
     for (uint32_t i = it > kStages ? it - kStages : 0; i < it; ++i)
@@ -308,7 +351,20 @@ __global__ void __launch_bounds__(kThreads, 2)
     PartDesc part = {0, 0, 0, 0};
     uint32_t it = 0;
     bool ok = true;
-    while (walk.next(p)) {
+    uint4 qraw[NR / 8];     // this thread's part of the next segment's queries, 16 lanes a row
+    auto load_q = [&](const Walk& w) {
+#pragma unroll
+      for (int i = 0; i < NR / 8; ++i) {
+        const int r = 8 * i + (tid >> 4);
+        qraw[i] = make_uint4(0, 0, 0, 0);
+        if (r < w.s.q_len * G)
+          qraw[i] = *reinterpret_cast<const uint4*>(p.a.q + (int64_t)(w.s.tok0 + r / G) * p.a.q_stride +
+                                                    (w.h * G + r % G) * kHeadDim + 8 * (tid & 15));
+      }
+    };
+    bool more = walk.next(p);
+    if (more) load_q(walk);
+    while (more) {
       const int rows = walk.s.q_len * G;
       const int first_pos = walk.s.len - walk.s.q_len;   // position of query 0
       // ---- queries: two e4m3 terms each, 16 lanes a row
@@ -317,14 +373,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         const int r = r0 + (tid >> 4), c = tid & 15;
         float x[8];
         float top = 0.0f;
-        if (r < rows) {
-          const int i = r / G, g = r % G;
-          unpack8(*reinterpret_cast<const uint4*>(p.a.q + (int64_t)(walk.s.tok0 + i) * p.a.q_stride +
-                                                  (walk.h * G + g) * kHeadDim + 8 * c), x);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] = 0.0f;
-        }
+        unpack8(qraw[r0 / 8], x);
 #pragma unroll
         for (int e = 0; e < 8; ++e) top = max_nan(top, fabsf(x[e]));
 #pragma unroll
@@ -358,6 +407,9 @@ __global__ void __launch_bounds__(kThreads, 2)
       fence_proxy_async();
       mbar_arrive(bar_q);
       if (bar_any(1, 128, !ok)) { ok = false; break; }   // qmul is written (and nobody gave up)
+      Walk ahead = walk;
+      more = ahead.next(p);
+      if (more) load_q(ahead);
 
       float acc[NR], l[NR];
 #pragma unroll
@@ -408,8 +460,9 @@ __global__ void __launch_bounds__(kThreads, 2)
       };
       for (int t = walk.a; t < walk.b; ++t, ++it) {
         const uint32_t par = it & 1, st = it % kStages;
+        // (the scales and V are read here too; S comes last)
+        ok = mbar_wait(bar_full + 8 * st, (it / kStages) & 1) && ok;
         ok = mbar_wait(bar_s + 8 * par, (it >> 1) & 1) && ok;
-        ok = mbar_wait(bar_full + 8 * st, (it / kStages) & 1) && ok;   // (V is read here too)
         tc_fence_after();
         const int key0 = (walk.s.tile0 + t) * kTile, key = key0 + tid;
         // some key of the tile is hidden from some row
@@ -590,13 +643,14 @@ __global__ void __launch_bounds__(kThreads, 2)
           slot[NR * 129 + lane] = den;
         }
         if (begins) {   // the CTA that its last tile lies in, from the cut of the ranges
-          const int64_t last = walk.base + (int64_t)walk.h * walk.s.tiles + walk.s.tiles - 1;
+          const int64_t last = walk.unit_of(walk.s.tiles - 1);
           const int64_t c = ((last + 1) * ranges - 1) / total;
           part.n = walk.n;
           part.h = walk.h;
           part.parts = (int)(c - blockIdx.x) + 1;
         }
       }
+      walk = ahead;
     }
     if (!ok && tid == 0) record_error(p.a.status, KDA_ERR_DEVICE_TIMEOUT, 315);
     if (!ok) part.parts = 0;
@@ -611,44 +665,64 @@ __global__ void __launch_bounds__(kThreads, 2)
 }
 
 // Merges the parts of the item that CTA blockIdx.x of the first kernel began and did not
-// finish: sums and denominators by their maxima, in CTA order.  A warp a row, 4 channels a lane.
+// finish: sums and denominators by their maxima, in a fixed order.  Four warps a row (a part each
+// in turn), two rows a CTA, 4 channels a lane.
+constexpr int kMergeWarps = 4;
 template <int NR>
-__global__ void __launch_bounds__(128) kda_attn_merge_kernel(const __grid_constant__ DecodeParams p) {
+__global__ void __launch_bounds__(64 * kMergeWarps)
+    kda_attn_merge_kernel(const __grid_constant__ DecodeParams p) {
+  __shared__ float4 acc_s[2][kMergeWarps][32];
+  __shared__ float den_s[2][kMergeWarps];
   pdl_wait();
   const PartDesc d = p.desc[blockIdx.x];
   if (d.parts == 0) return;
-  const int lane = threadIdx.x & 31, r = blockIdx.y * 4 + (threadIdx.x >> 5);
-  const int hk = p.a.c.kv_heads, G = p.a.heads / hk;
+  const int lane = threadIdx.x & 31, w0 = (threadIdx.x >> 5) % kMergeWarps, rr = threadIdx.x / (32 * kMergeWarps);
+  const int r = blockIdx.y * 2 + rr;
+  const int G = p.a.heads / p.a.c.kv_heads;
   const int tok0 = p.a.cu_seqlens[d.n], rows = (p.a.cu_seqlens[d.n + 1] - tok0) * G;
-  if (r >= rows) return;
   auto slot = [&](int i) {
     return p.slots + ((int64_t)2 * (blockIdx.x + i) + (i == 0 ? 1 : 0)) * kSlotFloats<NR>;
   };
   float m = -INFINITY;
-  for (int i = lane; i < d.parts; i += 32) m = fmaxf(m, slot(i)[NR * 128 + r]);
+  if (r < rows) {
+    for (int i = lane; i < d.parts; i += 32) m = fmaxf(m, slot(i)[NR * 128 + r]);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  const float ref = m == -INFINITY ? 0.0f : m;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  float den = 0.0f;
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const float ref = m == -INFINITY ? 0.0f : m;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float den = 0.0f;
 #pragma unroll 4
-  for (int i = 0; i < d.parts; ++i) {
-    const float* s = slot(i);
-    const float w = ex2(s[NR * 128 + r] - ref);
-    const float4 a = *reinterpret_cast<const float4*>(s + r * 128 + 4 * lane);
-    den += s[NR * 129 + r] * w;
-    acc.x += a.x * w;
-    acc.y += a.y * w;
-    acc.z += a.z * w;
-    acc.w += a.w * w;
+    for (int i = w0; i < d.parts; i += kMergeWarps) {
+      const float* s = slot(i);
+      const float w = ex2(s[NR * 128 + r] - ref);
+      const float4 a = *reinterpret_cast<const float4*>(s + r * 128 + 4 * lane);
+      den += s[NR * 129 + r] * w;
+      acc.x += a.x * w;
+      acc.y += a.y * w;
+      acc.z += a.z * w;
+      acc.w += a.w * w;
+    }
+    acc_s[rr][w0][lane] = acc;
+    if (lane == 0) den_s[rr][w0] = den;
+  }
+  __syncthreads();
+  if (w0 != 0 || r >= rows) return;
+  float4 acc = acc_s[rr][0][lane];
+  float den = den_s[rr][0];
+#pragma unroll
+  for (int w = 1; w < kMergeWarps; ++w) {
+    const float4 a = acc_s[rr][w][lane];
+    acc.x += a.x;
+    acc.y += a.y;
+    acc.z += a.z;
+    acc.w += a.w;
+    den += den_s[rr][w];
   }
   const float il = den == 0.0f ? 0.0f : 1.0f / den;
   const int64_t tok = tok0 + r / G;
   const int head = d.h * G + r % G;
-  __nv_bfloat162 o2[2] = {__floats2bfloat162_rn(acc.x * il, acc.y * il),
-                          __floats2bfloat162_rn(acc.z * il, acc.w * il)};
   *reinterpret_cast<uint2*>(p.a.out + tok * p.a.out_stride + head * kHeadDim + 4 * lane) =
-      *reinterpret_cast<const uint2*>(o2);
+      make_uint2(pack_bf16x2(acc.x * il, acc.y * il), pack_bf16x2(acc.z * il, acc.w * il));
   if (p.a.lse && lane == 0)
     p.a.lse[tok * p.a.heads + head] = den == 0.0f ? -INFINITY : (m + lg2(den)) * kLn2;
 }
@@ -671,8 +745,8 @@ cudaError_t launch_nr(DecodeParams& d, int sms, cudaStream_t stream) {
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)ctas, NR / 4);
-  cfg.blockDim = dim3(128);
+  cfg.gridDim = dim3((unsigned)ctas, NR / 2);
+  cfg.blockDim = dim3(64 * kMergeWarps);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
