@@ -34,7 +34,7 @@ namespace {
 
 constexpr int kThreads = 192;
 constexpr int kStageBytes = 2 * kTile * kHeadDim;   // K and V
-constexpr int kOver = 2;                             // tiles' worth of time an item takes besides its tiles
+constexpr int kOver = 3;                             // tiles' worth of time an item takes besides its tiles
 constexpr int kCached = 32;                          // sequences whose lengths a CTA keeps in shared memory
 constexpr float kPScale = 256.0f;                    // largest numerator, in the e4m3 operand
 

@@ -4,7 +4,7 @@
 //   S   = q1 K8^T + q2 K8^T   e4m3 on tcgen05, the cache's keys as they lie in memory; a bf16
 //                             query is two e4m3 terms (exact to 2^-18 of its row's largest entry,
 //                             at the tensor time of one bf16 product)
-//   P   = 2^(s + log2 v_scale(page) - m)   thread = row, written as bf16 over S in tensor memory
+//   P   = 2^(s + log2 v_scale(page) - m)   two threads a row, written as bf16 over S in tensor memory
 //   O  += P V                 bf16 on tcgen05, P from tensor memory, V widened to bf16 by four
 //                             warps (an e4m3 value is exact in bf16; page scales are in P)
 // The row maximum m is brought up only when it grows by more than 2^8 (P is then at most 2^8, and
@@ -18,8 +18,9 @@
 // to end and cut into one equal range per CTA, one CTA per SM (as in the decode kernel), and a
 // dependent kernel merges the items that were cut.
 //
-// Warps: 0-3 / 4-7 softmax of the halves, 8-11 the widening of V, 12 the TMA producer, 13 the MMA
-// issuer (14, 15 only give their registers).  Every wait is bounded.
+// Warps: 0-7 / 8-15 softmax of the halves, 16-19 the widening of V, 20 the TMA producer, 21 the MMA
+// issuer, 22 the scheduler, which walks the CTA's range and hands its segments to the others
+// through a ring in shared memory (23 only gives its registers).  Every wait is bounded.
 //
 // Masked entries as in the decode kernel: scores by selection, V rows that no row of the tile
 // sees as zeros, and a NaN in a V row that only some rows see as zero, put back into those rows
@@ -30,11 +31,11 @@ namespace kda {
 namespace attn {
 namespace {
 
-constexpr int kThreadsP = 512;
+constexpr int kThreadsP = 768;
 constexpr int kRowsP = 256;
-constexpr int kKStages = 3, kVStages = 2;
-constexpr int kRegsSoftmax = 200, kRegsOther = 56;
-constexpr int kRegsNeeded = 256 * kRegsSoftmax + 256 * kRegsOther;   // of the launch's 512 x 128
+constexpr int kKStages = 3, kVStages = 2, kSegs = 4;
+constexpr int kSoftWarps = 16, kRegsSoftmax = 96, kRegsOther = 48;
+constexpr int kRegsNeeded = 32 * (kSoftWarps * kRegsSoftmax + (kThreadsP / 32 - kSoftWarps) * kRegsOther);
 constexpr float kSlack = 8.0f;              // log2 growth of the maximum before O is rescaled
 
 // shared memory, from a 1024-byte aligned base
@@ -43,10 +44,14 @@ constexpr int kOffVB = kOffQ + 4 * 16384;                   // [2] V as bf16, tw
 constexpr int kOffK = kOffVB + 2 * 32768;                   // [kKStages] K tiles
 constexpr int kOffV8 = kOffK + kKStages * 16384;            // [kVStages] V tiles
 constexpr int kOffSc = kOffV8 + kVStages * 16384;           // float4 [4][8]: k scale, log2 v scale, 1 / v scale
-constexpr int kOffBars = kOffSc + 4 * 8 * 16;
-constexpr int kNumBars = 2 * kKStages + 2 * kVStages + 4 + 2 * 6 + 4;
+constexpr int kOffQmul = kOffSc + 4 * 8 * 16;               // float [256]
+constexpr int kOffMx = kOffQmul + 4 * kRowsP;               // float [2][256][2]: maxima of a row's two threads
+constexpr int kOffL = kOffMx + 16 * kRowsP;                 // float [256][2]: denominators
+constexpr int kOffSeg = kOffL + 8 * kRowsP;                 // Segment [kSegs]
+constexpr int kOffBars = kOffSeg + 64 * 4;
+constexpr int kNumBars = 2 * kKStages + 2 * kVStages + 4 + 2 * 6 + 4 + 2 * kSegs;
 constexpr int kOffMiscP = kOffBars + 8 * kNumBars;
-constexpr int kSmemP = kOffMiscP + 256 + 1024;
+constexpr int kSmemP = kOffMiscP + 320 + 1024;
 static_assert(kSmemP <= 227 * 1024, "shared memory");
 
 // tensor memory columns
@@ -115,6 +120,19 @@ struct WalkP {
   }
 };
 
+// What the roles need of a segment: written by the scheduler warp, a ring of kSegs in shared memory.
+struct Segment {
+  int more;                  // 0: there is none, the CTA is done
+  int tok0, cnt;             // its tokens, as rows of q and out
+  int head0;                 // first query head
+  int p_first;               // position of the first token
+  int key0, key1;            // keys [key0, key1), whole tiles; those past the last position are masked
+  int ch;                    // kv head
+  int used;                  // pages of the sequence
+  int whole, begins;         // the item's tiles are all here / its first one is
+  int pad;
+  const int32_t* table;      // the sequence's pages
+};
 __device__ __forceinline__ uint32_t bf16x2_of(float lo, float hi) { return pack_bf16x2(lo, hi); }
 
 template <bool kCap>
@@ -129,15 +147,16 @@ __global__ void __launch_bounds__(kThreadsP, 1)
   const uint32_t bar_bf = bar_ve + 8 * kVStages, bar_be = bar_bf + 16;       // widened V
   const uint32_t bar_q = bar_be + 16, bar_s = bar_q + 16, bar_p = bar_s + 16, bar_o = bar_p + 16;
   const uint32_t bar_of = bar_o + 16, bar_end = bar_of + 16, bar_sc = bar_end + 16;   // bar_sc: scales
+  const uint32_t bar_gf = bar_sc + 32, bar_ge = bar_gf + 8 * kSegs;               // segment ring
   struct Misc {
-    long long part[16];
+    long long part[kThreadsP / 32];
     long long rest;          // first tile's place in its sequence
     int start_n, poison[8];
     int start_h, start_rt, start_off;
     uint32_t tmem;
   };
   Misc* misc = reinterpret_cast<Misc*>(sm + kOffMiscP);
-  static_assert(sizeof(Misc) <= 256, "misc");
+  static_assert(sizeof(Misc) <= 320, "misc");
   const int hk = p.a.c.kv_heads, N = p.a.num_seqs, G = p.a.heads / hk, P = p.a.c.page_size;
 
   if (tid == 0) {
@@ -152,21 +171,25 @@ __global__ void __launch_bounds__(kThreadsP, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar_bf + 8 * i, 128);
       mbar_init(bar_be + 8 * i, 1);
-      mbar_init(bar_q + 8 * i, 128);
+      mbar_init(bar_q + 8 * i, kSoftWarps / 2);
       mbar_init(bar_s + 8 * i, 1);
-      mbar_init(bar_p + 8 * i, 128);
+      mbar_init(bar_p + 8 * i, kSoftWarps / 2);
       mbar_init(bar_o + 8 * i, 1);
-      mbar_init(bar_of + 8 * i, 128);
+      mbar_init(bar_of + 8 * i, kSoftWarps / 2);
       mbar_init(bar_end + 8 * i, 1);
     }
     for (int i = 0; i < 4; ++i) mbar_init(bar_sc + 8 * i, 1);
+    for (int i = 0; i < kSegs; ++i) {
+      mbar_init(bar_gf + 8 * i, 1);
+      mbar_init(bar_ge + 8 * i, kSoftWarps + 6);   // softmax, V, producer, MMA
+    }
     mbar_fence_init();
     for (int i = 0; i < 8; ++i) misc->poison[i] = 0;
     tma_prefetch_desc(&p.maps.k);
     tma_prefetch_desc(&p.maps.v);
     if (blockIdx.x == 0 && p.a.cu_seqlens[0] != 0) record_error(p.a.status, KDA_ERR_BAD_CU_SEQLENS, 330);
   }
-  if (warp == 13) {
+  if (warp == kSoftWarps + 5) {
     tmem_alloc(smem_u32(&misc->tmem), 512);
     tmem_relinquish();
   }
@@ -185,18 +208,22 @@ __global__ void __launch_bounds__(kThreadsP, 1)
         len = s.len;
       }
     }
+    // a lane its own sequence when it has few row tiles, else the warp together
     long long mine = 0;
-    uint32_t todo = __ballot_sync(0xffffffffu, q_len > 0);
+    const int rts = (q_len + p.tokens - 1) / p.tokens;
+    if (rts <= 32)
+      for (int rt = 0; rt < rts; ++rt) mine += item_of(q_len, len, rt, p.tokens, p.a.window).tiles;
+    uint32_t todo = __ballot_sync(0xffffffffu, rts > 32);
     while (todo) {
       const int k = __ffs(todo) - 1;
       todo &= todo - 1;
       const int ql = __shfl_sync(0xffffffffu, q_len, k), ln = __shfl_sync(0xffffffffu, len, k);
-      long long sum = 0;
+      int sum = 0;
       for (int rt = lane; rt * p.tokens < ql; rt += 32) sum += item_of(ql, ln, rt, p.tokens, p.a.window).tiles;
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      if (lane == k) mine = sum * hk;
+      const int all = __reduce_add_sync(0xffffffffu, sum);
+      if (lane == k) mine = all;
     }
+    mine *= hk;
     return mine;
   };
   long long mine = 0, first = 0;
@@ -283,34 +310,48 @@ __global__ void __launch_bounds__(kThreadsP, 1)
     walk.off = misc->start_off;
   }
 
-  if (warp >= 12) {
+  const Segment* ring = reinterpret_cast<const Segment*>(sm + kOffSeg);
+  static_assert(sizeof(Segment) <= 64 && kSegs <= 4, "segment ring");
+  // The next segment (false when there is none, or the wait gave up), and done with one.
+  auto seg_wait = [&](uint32_t seg, bool& ok) -> const Segment* {
+    ok = ok && mbar_wait(bar_gf + 8 * (seg % kSegs), (seg / kSegs) & 1);
+    __syncwarp();
+    return ring + seg % kSegs;
+  };
+  auto seg_done = [&](uint32_t seg) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar_ge + 8 * (seg % kSegs));
+  };
+
+  if (warp >= kSoftWarps + 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
-    if (warp == 12) {
-      // ================= producer
-      uint32_t it = 0;
+    if (warp == kSoftWarps + 4) {
+      // ================= producer; a tile's pages and scales are looked up one tile ahead
+      uint32_t it = 0, seg = 0;
       bool ok = true;
-      while (ok && walk.next(p)) {
-        const int32_t* bt = p.a.c.block_table + walk.n * p.a.c.table_stride;
-        const int boxes = kTile / P, used = (walk.s.len + P - 1) / P;
-        // lanes 0-7: the page that holds keys 16 lane .. of a tile (its first lane loads it)
-        const int per = P / 16;                          // 16-key groups per page
-        auto page_of = [&](int t) -> int {
-          const int b = (walk.it.tile0 + t) * boxes + lane / per;
-          if (lane >= 8 || t >= walk.b || b >= used) return -2;
-          const int pg = bt[b];
-          if (pg < 0 || pg >= p.a.c.num_pages) {
-            record_error(p.a.status, KDA_ERR_BAD_CACHE_INDEX, 332);
-            return p.a.c.num_pages;                      // outside the map: the load gives zeros
-          }
-          return pg;
-        };
+      const int per = P / 16;                            // 16-key groups per page
+      // lanes 0-7: the page that holds keys 16 lane .. of a tile (its first lane loads it)
+      auto page_of = [&](const Segment& g, int key) -> int {
+        const int b = (key + 16 * lane) / P;
+        if (lane >= 8 || key >= g.key1 || b >= g.used) return -2;
+        const int pg = g.table[b];
+        if (pg < 0 || pg >= p.a.c.num_pages) {
+          record_error(p.a.status, KDA_ERR_BAD_CACHE_INDEX, 332);
+          return p.a.c.num_pages;                        // outside the map: the load gives zeros
+        }
+        return pg;
+      };
+      while (true) {
+        const Segment g = *seg_wait(seg, ok);
+        if (!ok || !g.more) break;
+        seg_done(seg++);
         auto scale_of = [&](const float* sc, int pg) -> float {
-          return pg >= 0 && pg < p.a.c.num_pages ? sc[(int64_t)pg * p.a.c.scale_stride + walk.ch] : 1.0f;
+          return pg >= 0 && pg < p.a.c.num_pages ? sc[(int64_t)pg * p.a.c.scale_stride + g.ch] : 1.0f;
         };
-        int pg = page_of(walk.a);
-        for (int t = walk.a; t < walk.b; ++t, ++it) {
+        int pg = page_of(g, g.key0);
+        for (int key = g.key0; key < g.key1; key += kTile, ++it) {
           const float ks = scale_of(p.a.c.k_scale, pg), vs = scale_of(p.a.c.v_scale, pg);
-          const int pg_next = page_of(t + 1);
+          const int pg_next = page_of(g, key + kTile);
           const uint32_t sk = it % kKStages, sv = it % kVStages;
           if (it >= kKStages) ok = mbar_wait(bar_ke + 8 * sk, (it / kKStages - 1) & 1);
           ok = __all_sync(0xffffffffu, ok);
@@ -329,15 +370,16 @@ __global__ void __launch_bounds__(kThreadsP, 1)
             mbar_expect_tx(bar_kf + 8 * sk, bytes);
           }
           __syncwarp();
-          if (loads) tma_load_4d(sb + kOffK + sk * 16384 + row * 128, &p.maps.k, 0, 0, walk.ch, pg, bar_kf + 8 * sk);
+          if (loads) tma_load_4d(sb + kOffK + sk * 16384 + row * 128, &p.maps.k, 0, 0, g.ch, pg, bar_kf + 8 * sk);
           if (it >= kVStages) ok = mbar_wait(bar_ve + 8 * sv, (it / kVStages - 1) & 1);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           if (lane == 0) mbar_expect_tx(bar_vf + 8 * sv, bytes);
           __syncwarp();
-          if (loads) tma_load_4d(sb + kOffV8 + sv * 16384 + row * 128, &p.maps.v, 0, 0, walk.ch, pg, bar_vf + 8 * sv);
+          if (loads) tma_load_4d(sb + kOffV8 + sv * 16384 + row * 128, &p.maps.v, 0, 0, g.ch, pg, bar_vf + 8 * sv);
           pg = pg_next;
         }
+        if (!ok) break;
       }
       if (!ok && lane == 0) record_error(p.a.status, KDA_ERR_DEVICE_TIMEOUT, 333);
       // the copies in flight end before the CTA does (a failed wait left at most one K behind)
@@ -345,7 +387,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
         mbar_wait(bar_kf + 8 * (i % kKStages), (i / kKStages) & 1);
       for (uint32_t i = it > kVStages ? it - kVStages : 0; i < it; ++i)
         mbar_wait(bar_vf + 8 * (i % kVStages), (i / kVStages) & 1);
-    } else if (warp == 13) {
+    } else if (warp == kSoftWarps + 5) {
       // ================= MMA issuer (the warp stays together; one lane issues)
       constexpr uint32_t id_s = idesc_e4m3(128, 128, 0, 0), id_o = idesc_bf16(128, 128, 0, 1);
       const uint32_t lead = elect_one() ? 1u : 0u;
@@ -375,20 +417,24 @@ __global__ void __launch_bounds__(kThreadsP, 1)
                          id_o, !(first_tile && ks == 0));
         mma_commit_on(lead, bar_o + 8 * h);
       };
-      while (ok && walk.next(p)) {
-        for (int t = walk.a; t < walk.b && ok; ++t, ++it) {
+      while (true) {
+        const Segment* sg = seg_wait(seg, ok);
+        if (!ok || !sg->more) break;
+        const int tiles = (sg->key1 - sg->key0) / kTile;
+        seg_done(seg);
+        for (int t = 0; t < tiles && ok; ++t, ++it) {
           // what the tile needs besides P: its keys, and the values of the tile before
           ok = mbar_wait(bar_kf + 8 * (it % kKStages), (it / kKStages) & 1);
-          if (t > walk.a) ok = ok && mbar_wait(bar_bf + 8 * ((it - 1) & 1), ((it - 1) >> 1) & 1);
+          if (t > 0) ok = ok && mbar_wait(bar_bf + 8 * ((it - 1) & 1), ((it - 1) >> 1) & 1);
           else ok = ok && mbar_wait(bar_q, seg & 1) && mbar_wait(bar_q + 8, seg & 1);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           tc_fence_after();
-          if (t > walk.a) pv(it - 1, 0, t - 1 == walk.a);
+          if (t > 0) pv(it - 1, 0, t == 1);
           if (!ok) break;
           qk(it, 0);
-          if (t > walk.a) {
-            pv(it - 1, 1, t - 1 == walk.a);
+          if (t > 0) {
+            pv(it - 1, 1, t == 1);
             if (!ok) break;
             mma_commit_on(lead, bar_be + 8 * ((it - 1) & 1));
           }
@@ -396,9 +442,10 @@ __global__ void __launch_bounds__(kThreadsP, 1)
           mma_commit_on(lead, bar_ke + 8 * (it % kKStages));
         }
         if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar_bf + 8 * ((it - 1) & 1), ((it - 1) >> 1) & 1));
-        for (int h = 0; h < 2 && ok; ++h) pv(it - 1, h, walk.b - 1 == walk.a);
+        for (int h = 0; h < 2 && ok; ++h) pv(it - 1, h, tiles == 1);
         if (ok) mma_commit_on(lead, bar_be + 8 * ((it - 1) & 1));
         ++seg;
+        if (!ok) break;
       }
       if (!ok && lead) record_error(p.a.status, KDA_ERR_DEVICE_TIMEOUT, 334);
       // what was issued ends, its arrivals included, before shared and tensor memory go
@@ -409,24 +456,65 @@ __global__ void __launch_bounds__(kThreadsP, 1)
       for (uint32_t i = it > 2 ? it - 2 : 0; ok && i < it; ++i)
         mbar_wait(bar_be + 8 * (i & 1), (i >> 1) & 1);
       __syncwarp();
+    } else if (warp == kSoftWarps + 6) {
+      // ================= scheduler: this CTA's segments, one after the other
+      if (lane == 0) {
+        PartDescP part = {0, 0, 0, 0};
+        bool ok = true;
+        for (uint32_t seg = 0;; ++seg) {
+          const bool more = walk.next(p);
+          if (seg >= kSegs) ok = mbar_wait(bar_ge + 8 * (seg % kSegs), (seg / kSegs - 1) & 1);
+          if (!ok) break;
+          Segment* g = reinterpret_cast<Segment*>(sm + kOffSeg) + seg % kSegs;
+          g->more = more;
+          if (more) {
+            g->tok0 = walk.s.tok0 + walk.it.tok;
+            g->cnt = walk.it.cnt;
+            g->head0 = walk.ch * G;
+            g->p_first = walk.s.len - walk.s.q_len + walk.it.tok;
+            g->key0 = (walk.it.tile0 + walk.a) * kTile;
+            g->key1 = (walk.it.tile0 + walk.b) * kTile;
+            g->ch = walk.ch;
+            g->used = (walk.s.len + P - 1) / P;
+            g->whole = walk.a == 0 && walk.b == walk.it.tiles;
+            g->begins = walk.a == 0;
+            g->table = p.a.c.block_table + walk.n * p.a.c.table_stride;
+            if (walk.a == 0 && walk.b < walk.it.tiles) {   // the CTA that the item's last tile lies in
+              const int64_t last = walk.pos - (walk.b - walk.a) + walk.it.tiles - 1;
+              part.n = walk.n;
+              part.h = walk.ch;
+              part.rt = walk.crt;
+              part.parts = (int)(((last + 1) * ranges - 1) / total - blockIdx.x) + 1;
+            }
+          }
+          mbar_arrive(bar_gf + 8 * (seg % kSegs));
+          if (!more) break;
+        }
+        if (!ok) record_error(p.a.status, KDA_ERR_DEVICE_TIMEOUT, 337);
+        p.desc[blockIdx.x] = part;
+      }
+      __syncwarp();
     }
-  } else if (warp >= 8) {
+  } else if (warp >= kSoftWarps) {
     // ================= V to bf16, MN-major, 64-channel blocks 16 KB apart
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
-    const int vt = tid - 256, c = vt & 7;                // 16-channel chunk of this thread
+    const int vt = tid - 32 * kSoftWarps, c = vt & 7;                // 16-channel chunk of this thread
     uint32_t it = 0, seg = 0;
     bool ok = true;
-    while (ok && walk.next(p)) {
-      const int p_first = walk.s.len - walk.s.q_len + walk.it.tok, p_last = p_first + walk.it.cnt - 1;
+    while (true) {
+      const Segment* sg = seg_wait(seg, ok);
+      if (!ok || !sg->more) break;
+      const int p_first = sg->p_first, p_last = p_first + sg->cnt - 1, key1 = sg->key1;
+      int key0 = sg->key0;
+      seg_done(seg);
       if (vt == 0) misc->poison[(seg + 4) & 7] = 0;      // last read four segments ago
-      for (int t = walk.a; t < walk.b; ++t, ++it) {
+      for (; key0 < key1; key0 += kTile, ++it) {
         const uint32_t sv = it % kVStages, vb = it & 1;
         ok = mbar_wait(bar_vf + 8 * sv, (it / kVStages) & 1);
         if (it >= 2) ok = ok && mbar_wait(bar_be + 8 * vb, ((it >> 1) - 1) & 1);
         if (!ok) break;
         const unsigned char* src = sm + kOffV8 + sv * 16384;
         unsigned char* dst = sm + kOffVB + vb * 32768 + (c >> 2) * 16384;
-        const int key0 = (walk.it.tile0 + t) * kTile;
         const bool masked = key0 + kTile - 1 > p_first || (p.a.window > 0 && key0 <= p_last - p.a.window);
 #pragma unroll 2
         for (int j = 0; j < 8; ++j) {
@@ -438,7 +526,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
           uint32_t w[4] = {u.x, u.y, u.z, u.w}, nan = 0, o[8];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            nan |= __vcmpeq4(w[e] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+            nan |= ((w[e] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;   // a byte of 7f carries
             // bytes (0, 1), (2, 3) to the high bytes of 16-bit halves; sign to bit 15, exponent
             // and mantissa down to bits 10..4: the value times 2^-120 in bf16
 #pragma unroll
@@ -470,106 +558,116 @@ __global__ void __launch_bounds__(kThreadsP, 1)
         mbar_arrive(bar_ve + 8 * sv);
       }
       ++seg;
+      if (!ok) break;
     }
     if (!ok && vt == 0) record_error(p.a.status, KDA_ERR_DEVICE_TIMEOUT, 335);
   } else {
-    // ================= softmax: thread = row
+    // ================= softmax: two threads a row, 64 keys (64 channels of O) each.  A wait that
+    // gives up clears `ok`, after which nothing is waited for any more but every barrier is met.
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
-    const int half = warp >> 2, row = tid;               // row of the tile (half B: 128 ..)
-    const uint32_t ts = tmem + kTS + 128 * half + ((uint32_t)(32 * (warp & 3)) << 16);
-    const uint32_t to = tmem + kTOP + 128 * half + ((uint32_t)(32 * (warp & 3)) << 16);
+    const int half = warp >> 3, cg = (warp >> 2) & 1, row = 128 * half + 32 * (warp & 3) + lane;
+    const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+    const uint32_t ts = tmem + kTS + 128 * half + lanes;
+    const uint32_t to = tmem + kTOP + 128 * half + 64 * cg + lanes;
+    const uint32_t id_pair = 1 + 4 * half + (warp & 3), id_half = 9 + half;
     const float cap2 = kCap ? 2.0f * kLog2e / p.a.softcap : 0.0f, cap1 = kCap ? p.a.softcap * kLog2e : 0.0f;
     const float sign = p.a.scale < 0.0f ? -1.0f : 1.0f;  // (the row maximum is taken before the scale)
-    PartDescP part = {0, 0, 0, 0};
+    float* qmul_s = reinterpret_cast<float*>(sm + kOffQmul);
+    float* mx_s = reinterpret_cast<float*>(sm + kOffMx) + 2 * row;
+    float* l_s = reinterpret_cast<float*>(sm + kOffL) + 2 * row;
     uint32_t it = 0, seg = 0;
     bool ok = true;
-    while (ok && walk.next(p)) {
-      const int rows = walk.it.cnt * G;
-      const bool live = row < rows;
-      const int i_tok = live ? row / G : walk.it.cnt - 1, head = walk.ch * G + (live ? row % G : 0);
-      const int64_t tok = walk.s.tok0 + walk.it.tok + i_tok;
-      const int pos = walk.s.len - walk.s.q_len + walk.it.tok + i_tok;
-      // positions of this half's first and last row
-      const int r_lo = 128 * half, r_hi = min(rows, 128 * half + 128) - 1;
-      const int p_lo = walk.s.len - walk.s.q_len + walk.it.tok + min(r_lo / G, walk.it.cnt - 1);
-      const int p_hi = walk.s.len - walk.s.q_len + walk.it.tok + max(r_hi, 0) / G;
-      float qmul;
-      {   // ---- this row's query as two e4m3 terms
-        uint4 u[16];
-        const uint4* src = reinterpret_cast<const uint4*>(p.a.q + tok * p.a.q_stride + head * kHeadDim);
-        float top = 0.0f;
+    while (true) {
+      const Segment* sg = seg_wait(seg, ok);
+      // (the half's threads go on or leave together; its staging of the segment before is over)
+      if (bar_any(id_half, 256, !ok)) {
+        ok = false;
+        break;
+      }
+      if (!sg->more) break;
+      const int rows = sg->cnt * G;
+      {   // ---- queries as two e4m3 terms: 16 lanes a row, 16 rows a warp
+        const int c = lane & 15, r0 = 128 * half + 16 * (warp & 7) + (lane >> 4);
+        const __nv_bfloat16* src = p.a.q + (int64_t)sg->tok0 * p.a.q_stride + sg->head0 * kHeadDim + 8 * c;
+        uint4 u[8];
 #pragma unroll
-        for (int c = 0; c < 16; ++c) u[c] = live ? src[c] : make_uint4(0, 0, 0, 0);
-#pragma unroll
-        for (int c = 0; c < 16; ++c) {
-          float x[8];
-          unpack8(u[c], x);
+        for (int j = 0; j < 8; ++j) {
+          const int r = r0 + 2 * j;
+          u[j] = make_uint4(0, 0, 0, 0);
+          if (r < rows)
+            u[j] = *reinterpret_cast<const uint4*>(src + (int64_t)(r / G) * p.a.q_stride + (r % G) * kHeadDim);
+        }
+        unsigned char* q1 = sm + kOffQ + half * 32768;
+#pragma unroll 2
+        for (int j = 0; j < 8; ++j) {
+          const int r = r0 + 2 * j;
+          float x[8], top = 0.0f;
+          unpack8(u[j], x);
 #pragma unroll
           for (int e = 0; e < 8; ++e) top = max_nan(top, fabsf(x[e]));
-        }
-        const int e2 = (int)((__float_as_uint(top) >> 23) & 255) - 127 - 8 +
-                       ((__float_as_uint(top) & 0x7fffffu) > 0x600000u ? 1 : 0);
-        const int e2c = max(e2, -100);
-        const float inv = sign * __uint_as_float((uint32_t)(127 - e2c) << 23);
-        unsigned char* q1 = sm + kOffQ + half * 32768;
-        const int r = row & 127;
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {       // 16 channels: one 16-byte chunk of each term
-          uint32_t w1[4], w2[4];
+          for (int o = 8; o > 0; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
+          // a power of two that brings the row's largest entry into (224, 448]
+          const int e2 = (int)((__float_as_uint(top) >> 23) & 255) - 127 - 8 +
+                         ((__float_as_uint(top) & 0x7fffffu) > 0x600000u ? 1 : 0);
+          const int e2c = max(e2, -100);
+          const float inv = sign * __uint_as_float((uint32_t)(127 - e2c) << 23);
+          uint32_t w1[2], w2[2];
 #pragma unroll
-          for (int g = 0; g < 2; ++g) {
-            float x[8];
-            unpack8(u[2 * c + g], x);
+          for (int e = 0; e < 8; ++e) x[e] *= inv;
+          w1[0] = e4m3x4(x[0], x[1], x[2], x[3]);
+          w1[1] = e4m3x4(x[4], x[5], x[6], x[7]);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] *= inv;
-            w1[2 * g] = e4m3x4(x[0], x[1], x[2], x[3]);
-            w1[2 * g + 1] = e4m3x4(x[4], x[5], x[6], x[7]);
-#pragma unroll
-            for (int e = 0; e < 8; e += 2) {
-              const float2 b = from_e4m3x2((w1[2 * g + (e >> 2)] >> (8 * (e & 3))) & 0xffff);
-              x[e] -= b.x;
-              x[e + 1] -= b.y;
-            }
-            w2[2 * g] = e4m3x4(x[0], x[1], x[2], x[3]);
-            w2[2 * g + 1] = e4m3x4(x[4], x[5], x[6], x[7]);
+          for (int e = 0; e < 8; e += 2) {
+            const float2 b = from_e4m3x2((w1[e >> 2] >> (8 * (e & 3))) & 0xffff);
+            x[e] -= b.x;
+            x[e + 1] -= b.y;
           }
-          *reinterpret_cast<uint4*>(q1 + tile_off(r, 16 * c)) = make_uint4(w1[0], w1[1], w1[2], w1[3]);
-          *reinterpret_cast<uint4*>(q1 + 16384 + tile_off(r, 16 * c)) = make_uint4(w2[0], w2[1], w2[2], w2[3]);
+          w2[0] = e4m3x4(x[0], x[1], x[2], x[3]);
+          w2[1] = e4m3x4(x[4], x[5], x[6], x[7]);
+          *reinterpret_cast<uint2*>(q1 + tile_off(r & 127, 8 * c)) = make_uint2(w1[0], w1[1]);
+          *reinterpret_cast<uint2*>(q1 + 16384 + tile_off(r & 127, 8 * c)) = make_uint2(w2[0], w2[1]);
+          if (c == 0) {   // a non-finite query makes its row NaN
+            const float sq = top <= 3.402823466e38f ? __uint_as_float((uint32_t)(127 + e2c) << 23) : NAN;
+            qmul_s[r] = sq * fabsf(p.a.scale) * (kCap ? 1.0f : kLog2e);
+          }
         }
-        const float sq = top <= 3.402823466e38f ? __uint_as_float((uint32_t)(127 + e2c) << 23) : NAN;
-        qmul = sq * fabsf(p.a.scale) * (kCap ? 1.0f : kLog2e);
+        fence_proxy_async();
+        group_sync(id_half, 256);
+        if (lane == 0) mbar_arrive(bar_q + 8 * half);
       }
-      fence_proxy_async();
-      mbar_arrive(bar_q + 8 * half);
-
+      const float qmul = qmul_s[row];
+      // relative to the tile's first key: this row's position, and those of the half's first and last
+      const int last = sg->cnt - 1, rel = sg->p_first - sg->key0;
+      int hi = rel + (row < rows ? row / G : last) - 64 * cg;
+      int p_lo = rel + min(128 * half / G, last), p_hi = rel + max(min(rows, 128 * half + 128) - 1, 0) / G;
+      const int tiles = (sg->key1 - sg->key0) / kTile;
       float m = -INFINITY, l = 0.0f;
-      for (int t = walk.a; t < walk.b; ++t, ++it) {
+      for (int t = 0; t < tiles; ++t, ++it, hi -= kTile, p_lo -= kTile, p_hi -= kTile) {
         // (a wait costs over 100 cycles even when it need not wait: S, the last to come, last)
-        ok = mbar_wait(bar_sc + 8 * (it & 3), (it >> 2) & 1);
-        if (t > walk.a) ok = ok && mbar_wait(bar_o + 8 * half, (it - 1) & 1);
+        ok = ok && mbar_wait(bar_sc + 8 * (it & 3), (it >> 2) & 1);
+        if (t > 0) ok = ok && mbar_wait(bar_o + 8 * half, (it - 1) & 1);
         ok = ok && mbar_wait(bar_s + 8 * half, it & 1);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
+        __syncwarp();
         tc_fence_after();
-        uint32_t s[128];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(ts + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(s + 32 * c));
+        uint32_t s[64];
+        tmem_ld32(ts + 64 * cg, *reinterpret_cast<uint32_t(*)[32]>(s));
+        tmem_ld32(ts + 64 * cg + 32, *reinterpret_cast<uint32_t(*)[32]>(s + 32));
         tmem_wait_ld();
-        const float4* sc = reinterpret_cast<const float4*>(sm + kOffSc) + (it & 3) * 8;
-        const int key0 = (walk.it.tile0 + t) * kTile;
-        const bool masked = key0 + kTile - 1 > p_lo || (p.a.window > 0 && key0 <= p_hi - p.a.window);
+        const float4* sc = reinterpret_cast<const float4*>(sm + kOffSc) + (it & 3) * 8 + 4 * cg;
+        const bool masked = kTile - 1 > p_lo || (p.a.window > 0 && p.a.window <= p_hi);
         float mt = -INFINITY;
         const bool scaled = kCap || masked;    // s holds the finished exponents (else raw products)
         if (scaled) {
-          const int hi = pos - key0, lo = p.a.window > 0 ? pos - p.a.window + 1 - key0 : -1;
+          const int lo = p.a.window > 0 ? hi - p.a.window + 1 : -1;
 #pragma unroll
-          for (int g = 0; g < 8; ++g) {
+          for (int g = 0; g < 4; ++g) {
             const float4 f = sc[g];
             const float mul = qmul * f.x;
 #pragma unroll
             for (int e = 16 * g; e < 16 * g + 16; ++e) {
-              float x = __uint_as_float(s[e]) * mul;
-              x = (kCap ? cap_score(x, cap2, cap1) : x) + f.y;
+              float x = __uint_as_float(s[e]);
+              x = kCap ? cap_score(x * mul, cap2, cap1) + f.y : fmaf(x, mul, f.y);
               if (e > hi || e < lo) x = -INFINITY;
               mt = fmaxf(mt, x);
               s[e] = __float_as_uint(x);
@@ -577,7 +675,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
           }
         } else {
 #pragma unroll
-          for (int g = 0; g < 8; ++g) {
+          for (int g = 0; g < 4; ++g) {
             const float4 f = sc[g];
             float a = __uint_as_float(s[16 * g]), b = __uint_as_float(s[16 * g + 1]);
 #pragma unroll
@@ -589,11 +687,15 @@ __global__ void __launch_bounds__(kThreadsP, 1)
             mt = fmaxf(mt, fmaf(fmaxf(a, b), qmul * f.x, f.y));
           }
         }
+        // the row's other 64 keys
+        mx_s[(it & 1) * 2 * kRowsP + cg] = mt;
+        group_sync(id_pair, 64);      // (also: both have S in registers, P may go over it)
+        mt = fmaxf(mt, mx_s[(it & 1) * 2 * kRowsP + (cg ^ 1)]);
         if (__any_sync(0xffffffffu, mt > m + kSlack)) {
           const float next = fmaxf(m, mt), f = ex2(m - (next == -INFINITY ? 0.0f : next));
-          if (t > walk.a) {       // O, the tile before included, by the factor
-#pragma unroll
-            for (int c = 0; c < 8; ++c) {
+          if (t > 0) {       // O, the tile before included, by the factor
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
               uint32_t o[16];
               tmem_ld16(to + 16 * c, o);
               tmem_wait_ld();
@@ -606,107 +708,116 @@ __global__ void __launch_bounds__(kThreadsP, 1)
           m = next;
         }
         const float ref = m == -INFINITY ? 0.0f : m;
-        // P over the columns of S, half at a time (all of S is in registers)
+        // P over the columns of S
+        uint32_t pk[32];
 #pragma unroll
-        for (int hc = 0; hc < 2; ++hc) {
-          uint32_t pk[32];
+        for (int g = 0; g < 4; ++g) {
+          const float4 f = sc[g];
+          const float mul = scaled ? 1.0f : qmul * f.x, add = scaled ? -ref : f.y - ref;
+          const float2 mul2 = make_float2(mul, mul), add_2 = make_float2(add, add);
+          float2 sum = make_float2(0.0f, 0.0f);
 #pragma unroll
-          for (int g = 4 * hc; g < 4 * hc + 4; ++g) {
-            const float4 f = sc[g];
-            const float mul = scaled ? 1.0f : qmul * f.x, add = scaled ? -ref : f.y - ref;
-            const float2 mul2 = make_float2(mul, mul), add_2 = make_float2(add, add);
-            float2 sum = make_float2(0.0f, 0.0f);
-#pragma unroll
-            for (int e = 16 * g; e < 16 * g + 16; e += 2) {
-              float2 x = fma2(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), mul2, add_2);
-              x.x = ex2(x.x);
-              x.y = ex2(x.y);
-              sum = add2(sum, x);
-              pk[(e >> 1) - 32 * hc] = bf16x2_of(x.x, x.y);
-            }
-            l = fmaf(sum.x + sum.y, f.z, l);
+          for (int e = 16 * g; e < 16 * g + 16; e += 2) {
+            float2 x = fma2(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), mul2, add_2);
+            x.x = ex2(x.x);
+            x.y = ex2(x.y);
+            sum = add2(sum, x);
+            pk[e >> 1] = bf16x2_of(x.x, x.y);
           }
-          tmem_st32(ts + 32 * hc, pk);
+          l = fmaf(sum.x + sum.y, f.z, l);
         }
+        tmem_st32(ts + 32 * cg, pk);
         tmem_wait_st();
         tc_fence_before();
-        mbar_arrive(bar_p + 8 * half);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_p + 8 * half);
       }
-      if (ok) ok = mbar_wait(bar_o + 8 * half, (it - 1) & 1);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
+      ok = ok && mbar_wait(bar_o + 8 * half, (it - 1) & 1);
+      l_s[cg] = l;
+      group_sync(id_pair, 64);
+      l = l_s[0] + l_s[1];
       tc_fence_after();
-      // ---- the segment's rows out
+      // ---- the segment's rows out: 128 bytes of a row at a time through this warp's 4 KB of the
+      // query area (all products of the half are done), so that the stores are whole lines
       const bool poisoned = *reinterpret_cast<volatile int*>(&misc->poison[seg & 7]) != 0;
-      const bool whole = walk.a == 0 && walk.b == walk.it.tiles;
+      const bool live = row < rows, whole = sg->whole;
       const float inv_l = l == 0.0f ? 0.0f : 1.0f / l;
-      float* slot = p.slots + ((int64_t)2 * blockIdx.x + (walk.a == 0 ? 1 : 0)) * kSlotFloatsP;
+      const int i_tok = live ? row / G : last, head = sg->head0 + (live ? row % G : 0);
+      const int64_t tok = sg->tok0 + i_tok;
+      float* slot = p.slots + ((int64_t)2 * blockIdx.x + (sg->begins ? 1 : 0)) * kSlotFloatsP;
+      unsigned char* stage = sm + kOffQ + half * 32768 + (warp & 7) * 4096;
+      uint64_t dst = whole ? reinterpret_cast<uint64_t>(p.a.out + tok * p.a.out_stride + head * kHeadDim + 64 * cg)
+                           : reinterpret_cast<uint64_t>(slot + row * 128 + 64 * cg);
+      if (!live) dst = 0;
 #pragma unroll 1
-      for (int c = 0; c < 4; ++c) {
+      for (int c = 0; c < 2; ++c) {     // 32 channels
         uint32_t o[32];
         tmem_ld32(to + 32 * c, o);
         tmem_wait_ld();
         if (poisoned && live) {    // NaN entries that this row sees, in tiles that some rows do not
-          const int p0 = walk.s.len - walk.s.q_len + walk.it.tok, p1 = p0 + walk.it.cnt - 1;
-          for (int t = walk.a; t < walk.b; ++t) {
-            const int key0 = (walk.it.tile0 + t) * kTile;
+          const int p0 = sg->p_first, p1 = p0 + last, pos = p0 + i_tok;
+          for (int key0 = sg->key0; key0 < sg->key1; key0 += kTile) {
             if (!(key0 + kTile - 1 > p0 || (p.a.window > 0 && key0 <= p1 - p.a.window))) continue;
             for (int key = max(key0, p.a.window > 0 ? pos - p.a.window + 1 : 0); key <= min(key0 + kTile - 1, pos); ++key) {
-              const int pg = p.a.c.block_table[walk.n * p.a.c.table_stride + key / P];
+              const int pg = sg->table[key / P];
               if (pg < 0 || pg >= p.a.c.num_pages) continue;
-              const uint8_t* v = p.a.c.v + pg * p.a.c.page_stride + walk.ch * p.a.c.head_stride +
-                                 (key % P) * p.a.c.token_stride + 32 * c;
-#pragma unroll
+              const uint8_t* v = p.a.c.v + pg * p.a.c.page_stride + sg->ch * p.a.c.head_stride +
+                                 (key % P) * p.a.c.token_stride + 64 * cg + 32 * c;
+#pragma unroll 1
               for (int e = 0; e < 32; ++e)
-                if ((v[e] & 0x7f) == 0x7f) o[e] = 0x7fffffffu;
+                if ((v[e] & 0x7f) == 0x7f) {
+#pragma unroll
+                  for (int f = 0; f < 32; ++f)
+                    if (f == e) o[f] = 0x7fffffffu;
+                }
             }
           }
         }
-        if (live) {
-          if (whole) {
-            uint4* dst = reinterpret_cast<uint4*>(p.a.out + tok * p.a.out_stride + head * kHeadDim + 32 * c);
+        const int sw = lane & 7;
+        if (whole) {
 #pragma unroll
-            for (int g = 0; g < 4; ++g) {
-              float x[8];
+          for (int g = 0; g < 4; ++g) {
+            float x[8];
 #pragma unroll
-              for (int e = 0; e < 8; ++e) x[e] = __uint_as_float(o[8 * g + e]) * inv_l;
-              dst[g] = pack8(x);
-            }
-          } else {
-#pragma unroll
-            for (int g = 0; g < 8; ++g)
-              *reinterpret_cast<uint4*>(slot + row * 128 + 32 * c + 4 * g) =
-                  make_uint4(o[4 * g], o[4 * g + 1], o[4 * g + 2], o[4 * g + 3]);
+            for (int e = 0; e < 8; ++e) x[e] = __uint_as_float(o[8 * g + e]) * inv_l;
+            *reinterpret_cast<uint4*>(stage + lane * 128 + (((4 * c + g) ^ sw) << 4)) = pack8(x);
           }
+          if (c == 0) continue;    // a row's 64 channels are 128 bytes of bf16
+        } else {
+#pragma unroll
+          for (int g = 0; g < 8; ++g)
+            *reinterpret_cast<uint4*>(stage + lane * 128 + ((g ^ sw) << 4)) =
+                make_uint4(o[4 * g], o[4 * g + 1], o[4 * g + 2], o[4 * g + 3]);
         }
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int r = 4 * j + (lane >> 3), g = lane & 7;
+          const uint64_t d = __shfl_sync(0xffffffffu, dst, r);
+          const uint4 v = *reinterpret_cast<const uint4*>(stage + r * 128 + ((g ^ (r & 7)) << 4));
+          if (d) *reinterpret_cast<uint4*>(d + (whole ? 0 : 128 * c) + 16 * g) = v;
+        }
+        __syncwarp();
       }
       tc_fence_before();
-      mbar_arrive(bar_of + 8 * half);
-      if (whole) {
-        if (live && p.a.lse)
-          p.a.lse[tok * p.a.heads + head] = l == 0.0f ? -INFINITY : (m + lg2(l)) * kLn2;
-      } else {
-        if (live) {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_of + 8 * half);
+      if (live && cg == 0) {
+        if (!whole) {
           slot[kRowsP * 128 + row] = m;
           slot[kRowsP * 129 + row] = l;
-        }
-        if (walk.a == 0) {        // this CTA begins the item: the CTA that its last tile lies in
-          const int64_t last = walk.pos - (walk.b - walk.a) + walk.it.tiles - 1;
-          part.n = walk.n;
-          part.h = walk.ch;
-          part.rt = walk.crt;
-          part.parts = (int)(((last + 1) * ranges - 1) / total - blockIdx.x) + 1;
+        } else if (p.a.lse) {
+          p.a.lse[tok * p.a.heads + head] = l == 0.0f ? -INFINITY : (m + lg2(l)) * kLn2;
         }
       }
+      seg_done(seg);
       ++seg;
     }
-    if (!ok) part.parts = 0;
     if (!ok && lane == 0) record_error(p.a.status, KDA_ERR_DEVICE_TIMEOUT, 336);
-    if (tid == 0) p.desc[blockIdx.x] = part;
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 13) {
+  if (warp == kSoftWarps + 5) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
