@@ -4,12 +4,13 @@
 //   S   = q1 K8^T + q2 K8^T   e4m3 on tcgen05, the cache's keys as they lie in memory; a bf16
 //                             query is two e4m3 terms (exact to 2^-18 of its row's largest entry,
 //                             at the tensor time of one bf16 product)
-//   P   = 2^(s + log2 v_scale(page) - m)   two threads a row, written as bf16 over S in tensor memory
-//   O  += P V                 bf16 on tcgen05, P from tensor memory, V widened to bf16 by four
-//                             warps (an e4m3 value is exact in bf16; page scales are in P)
-// The row maximum m is brought up only when it grows by more than 2^8 (P is then at most 2^8, and
-// bf16 keeps its 8 bits at every magnitude), so O is rescaled rarely; the denominators take the
-// fp32 numerators, divided by the page's value scale.
+//   P   = 2^(s + log2 v_scale(page) - m)   two threads a row, written as f16 over S in tensor memory
+//   O  += P V                 f16 on tcgen05, P from tensor memory, V widened to f16 by four
+//                             warps (an e4m3 value is exact in f16; page scales are in P)
+// The row maximum m is brought up only when it grows by more than 2^8, so O is rescaled rarely.
+// Numerators are 2^7 at the maximum, 2^15 with that slack: f16 then keeps 11 bits down to 2^-21 of
+// the maximum and rounds to 2^-31 of it, against bf16's 8 bits.  The denominators take the fp32
+// numerators, divided by the page's value scale.
 //
 // Bound by the tensor cores: 4 x 128 flops per visible (row, key).  Two halves keep them busy:
 // while one half's softmax runs, the other half's products do.  The matrix instructions of a CTA
@@ -37,10 +38,11 @@ constexpr int kKStages = 3, kVStages = 2, kSegs = 4;
 constexpr int kSoftWarps = 16, kRegsSoftmax = 96, kRegsOther = 48;
 constexpr int kRegsNeeded = 32 * (kSoftWarps * kRegsSoftmax + (kThreadsP / 32 - kSoftWarps) * kRegsOther);
 constexpr float kSlack = 8.0f;              // log2 growth of the maximum before O is rescaled
+constexpr float kPShift = 7.0f;             // log2 of the numerator at the maximum: at most 2^15 with the slack
 
 // shared memory, from a 1024-byte aligned base
 constexpr int kOffQ = 0;                                    // [half][term] 128 x 128 e4m3
-constexpr int kOffVB = kOffQ + 4 * 16384;                   // [2] V as bf16, two 64-channel blocks
+constexpr int kOffVB = kOffQ + 4 * 16384;                   // [2] V as f16, two 64-channel blocks
 constexpr int kOffK = kOffVB + 2 * 32768;                   // [kKStages] K tiles
 constexpr int kOffV8 = kOffK + kKStages * 16384;            // [kVStages] V tiles
 constexpr int kOffSc = kOffV8 + kVStages * 16384;           // float4 [4][8]: k scale, log2 v scale, 1 / v scale
@@ -133,7 +135,6 @@ struct Segment {
   int pad;
   const int32_t* table;      // the sequence's pages
 };
-__device__ __forceinline__ uint32_t bf16x2_of(float lo, float hi) { return pack_bf16x2(lo, hi); }
 
 template <bool kCap>
 __global__ void __launch_bounds__(kThreadsP, 1)
@@ -389,7 +390,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
         mbar_wait(bar_vf + 8 * (i % kVStages), (i / kVStages) & 1);
     } else if (warp == kSoftWarps + 5) {
       // ================= MMA issuer (the warp stays together; one lane issues)
-      constexpr uint32_t id_s = idesc_e4m3(128, 128, 0, 0), id_o = idesc_bf16(128, 128, 0, 1);
+      constexpr uint32_t id_s = idesc_e4m3(128, 128, 0, 0), id_o = idesc_f16(128, 128, 0, 1);
       const uint32_t lead = elect_one() ? 1u : 0u;
       const uint64_t dq = kmajor8(sb + kOffQ, 0), dk0 = kmajor8(sb + kOffK, 0);
       const uint64_t dv0 = sdesc_sw128(sb + kOffVB, 16384, 1024);
@@ -413,7 +414,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
         const uint64_t dv = dv0 + (i & 1) * (32768 >> 4);
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks)
-          mma_bf16_ts_on(lead, tmem + kTOP + 128 * h, tmem + kTS + 128 * h + 8 * ks, dv + 2048 * ks / 16,
+          mma_f16_ts_on(lead, tmem + kTOP + 128 * h, tmem + kTS + 128 * h + 8 * ks, dv + 2048 * ks / 16,
                          id_o, !(first_tile && ks == 0));
         mma_commit_on(lead, bar_o + 8 * h);
       };
@@ -496,7 +497,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
       __syncwarp();
     }
   } else if (warp >= kSoftWarps) {
-    // ================= V to bf16, MN-major, 64-channel blocks 16 KB apart
+    // ================= V to f16, MN-major, 64-channel blocks 16 KB apart
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
     const int vt = tid - 32 * kSoftWarps, c = vt & 7;                // 16-channel chunk of this thread
     uint32_t it = 0, seg = 0;
@@ -523,30 +524,19 @@ __global__ void __launch_bounds__(kThreadsP, 1)
           // seen by no row of the tile: whatever is there reads as zero
           if (masked && (key > p_last || (p.a.window > 0 && key <= p_first - p.a.window)))
             u = make_uint4(0, 0, 0, 0);
-          uint32_t w[4] = {u.x, u.y, u.z, u.w}, nan = 0, o[8];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            nan |= ((w[e] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;   // a byte of 7f carries
-            // bytes (0, 1), (2, 3) to the high bytes of 16-bit halves; sign to bit 15, exponent
-            // and mantissa down to bits 10..4: the value times 2^-120 in bf16
-#pragma unroll
-            for (int g = 0; g < 2; ++g) {
-              const uint32_t h2 = __byte_perm(w[e], 0, g ? 0x3424 : 0x1404);
-              const uint32_t b = (h2 & 0x80008000u) | ((h2 >> 4) & 0x07f007f0u);
-              asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(o[2 * e + g]) : "r"(b), "r"(0x7b807b80u));   // 2^120
-            }
-          }
-          if (nan) {        // rare: NaN to NaN, or to zero and noted where some rows do not see it
-            if (masked) misc->poison[seg & 7] = 1;
+          uint32_t w[4] = {u.x, u.y, u.z, u.w}, o[8];
+          if (masked) {     // NaN entries (rare) of a row that only some may see: noted, read as zero
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const uint32_t m = __vcmpeq4(w[e] & 0x7f7f7f7fu, 0x7f7f7f7fu);
-#pragma unroll
-              for (int g = 0; g < 2; ++g) {
-                const uint32_t mm = __byte_perm(m, 0, g ? 0x3322 : 0x1100);
-                o[2 * e + g] = (o[2 * e + g] & ~mm) | (masked ? 0u : (mm & 0x7fff7fffu));
-              }
+              if (m) misc->poison[seg & 7] = 1;
+              w[e] &= ~m;
             }
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            o[2 * e] = f16x2_of_e4m3x2(w[e] & 0xffff);
+            o[2 * e + 1] = f16x2_of_e4m3x2(w[e] >> 16);
           }
           unsigned char* d = dst + (row >> 3) * 1024 + (row & 7) * 128;
           const int k0 = (2 * c) & 7;
@@ -707,7 +697,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
           l *= f;
           m = next;
         }
-        const float ref = m == -INFINITY ? 0.0f : m;
+        const float ref = (m == -INFINITY ? 0.0f : m) - kPShift;
         // P over the columns of S
         uint32_t pk[32];
 #pragma unroll
@@ -722,7 +712,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
             x.x = ex2(x.x);
             x.y = ex2(x.y);
             sum = add2(sum, x);
-            pk[e >> 1] = bf16x2_of(x.x, x.y);
+            pk[e >> 1] = f16x2_of(x.x, x.y);
           }
           l = fmaf(sum.x + sum.y, f.z, l);
         }
@@ -733,6 +723,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
         if (lane == 0) mbar_arrive(bar_p + 8 * half);
       }
       ok = ok && mbar_wait(bar_o + 8 * half, (it - 1) & 1);
+      m -= kPShift;       // (the numerators' reference)
       l_s[cg] = l;
       group_sync(id_pair, 64);
       l = l_s[0] + l_s[1];
@@ -860,7 +851,7 @@ __global__ void __launch_bounds__(32 * kMergeRows)
   const float il = den == 0.0f ? 0.0f : 1.0f / den;
   const int64_t tok = tok0 + first + r / G;
   const int head = d.h * G + r % G;
-  const uint2 o2 = make_uint2(bf16x2_of(acc.x * il, acc.y * il), bf16x2_of(acc.z * il, acc.w * il));
+  const uint2 o2 = make_uint2(pack_bf16x2(acc.x * il, acc.y * il), pack_bf16x2(acc.z * il, acc.w * il));
   *reinterpret_cast<uint2*>(p.a.out + tok * p.a.out_stride + head * kHeadDim + 4 * lane) = o2;
   if (p.a.lse && lane == 0)
     p.a.lse[tok * p.a.heads + head] = den == 0.0f ? -INFINITY : (m + lg2(den)) * kLn2;

@@ -77,6 +77,20 @@ __host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N, int a_mn, int b_
   return (1u << 4) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16) | ((uint32_t)(N >> 3) << 17) |
          ((uint32_t)(M >> 4) << 24);
 }
+// ... of kind::f16 with f16 A and B.
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N, int a_mn, int b_mn) {
+  return idesc_e4m3(M, N, a_mn, b_mn);   // format 0 of both is f16 there
+}
+__device__ __forceinline__ uint32_t f16x2_of(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t f16x2_of_e4m3x2(uint32_t v) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)v));
+  return h;
+}
 // 8-bit tiles with the 128-byte swizzle: a row of 128 bytes per token (key, query row), rows in
 // groups of 8; the 16-byte chunk index is XORed with row % 8.  As a K-major operand (channels
 // along K) a K step of 32 is 32 bytes on; as an MN-major one (tokens along K) 32 rows.
@@ -109,7 +123,7 @@ __device__ __forceinline__ void mma_e4m3_on(uint32_t on, uint32_t d_tmem, uint64
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(on)
       : "memory");
 }
-__device__ __forceinline__ void mma_bf16_ts_on(uint32_t on, uint32_t d_tmem, uint32_t a_tmem,
+__device__ __forceinline__ void mma_f16_ts_on(uint32_t on, uint32_t d_tmem, uint32_t a_tmem,
                                                uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
