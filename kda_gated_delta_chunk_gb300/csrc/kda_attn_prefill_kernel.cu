@@ -51,7 +51,7 @@ constexpr int kOffMx = kOffQmul + 4 * kRowsP;               // float [2][256][2]
 constexpr int kOffL = kOffMx + 16 * kRowsP;                 // float [256][2]: denominators
 constexpr int kOffSeg = kOffL + 8 * kRowsP;                 // Segment [kSegs]
 constexpr int kOffBars = kOffSeg + 64 * 4;
-constexpr int kNumBars = 2 * kKStages + 2 * kVStages + 4 + 2 * 6 + 4 + 2 * kSegs;
+constexpr int kNumBars = 2 * kKStages + 2 * kVStages + 2 * 7 + 4 + 2 * kSegs;
 constexpr int kOffMiscP = kOffBars + 8 * kNumBars;
 constexpr int kSmemP = kOffMiscP + 320 + 1024;
 static_assert(kSmemP <= 227 * 1024, "shared memory");
@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t bar_kf = sb + kOffBars, bar_ke = bar_kf + 8 * kKStages;
   const uint32_t bar_vf = bar_ke + 8 * kKStages, bar_ve = bar_vf + 8 * kVStages;
-  const uint32_t bar_bf = bar_ve + 8 * kVStages, bar_be = bar_bf + 16;       // widened V
+  const uint32_t bar_be = bar_ve + 8 * kVStages;                             // widened V read
   const uint32_t bar_q = bar_be + 16, bar_s = bar_q + 16, bar_p = bar_s + 16, bar_o = bar_p + 16;
   const uint32_t bar_of = bar_o + 16, bar_end = bar_of + 16, bar_sc = bar_end + 16;   // bar_sc: scales
   const uint32_t bar_gf = bar_sc + 32, bar_ge = bar_gf + 8 * kSegs;               // segment ring
@@ -170,11 +170,10 @@ __global__ void __launch_bounds__(kThreadsP, 1)
       mbar_init(bar_ve + 8 * i, 128);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(bar_bf + 8 * i, 128);
       mbar_init(bar_be + 8 * i, 1);
       mbar_init(bar_q + 8 * i, kSoftWarps / 2);
       mbar_init(bar_s + 8 * i, 1);
-      mbar_init(bar_p + 8 * i, kSoftWarps / 2);
+      mbar_init(bar_p + 8 * i, kSoftWarps / 2 + 4);   // and the four V warps
       mbar_init(bar_o + 8 * i, 1);
       mbar_init(bar_of + 8 * i, kSoftWarps / 2);
       mbar_init(bar_end + 8 * i, 1);
@@ -396,8 +395,9 @@ __global__ void __launch_bounds__(kThreadsP, 1)
       const uint64_t dv0 = sdesc_sw128(sb + kOffVB, 16384, 1024);
       uint32_t it = 0, seg = 0;
       bool ok = true;
-      auto qk = [&](uint32_t i, int h) {                 // S of tile i, half h
-        const uint64_t dk = dk0 + (i % kKStages) * (16384 >> 4), q = dq + h * (32768 >> 4);
+      uint32_t sk = 0;                                   // stage of the next keys
+      auto qk = [&](int h) {                             // S of half h from the keys of stage sk
+        const uint64_t dk = dk0 + sk * (16384 >> 4), q = dq + h * (32768 >> 4);
 #pragma unroll
         for (int x = 0; x < 8; ++x)
           mma_e4m3_on(lead, tmem + kTS + 128 * h, q + ((x >> 2) * 16384 + (x & 3) * 32) / 16,
@@ -407,7 +407,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
       auto pv = [&](uint32_t i, int h, bool first_tile) {   // O of half h += P(i) V(i)
         // (the segment before has read its O)
         if (first_tile && seg > 0) ok = ok && mbar_wait(bar_of + 8 * h, (seg - 1) & 1);
-        ok = ok && mbar_wait(bar_p + 8 * h, i & 1);
+        ok = ok && mbar_wait(bar_p + 8 * h, i & 1);      // P(i), V(i) and the keys of the tile after
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) return;
         tc_fence_after();
@@ -415,7 +415,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks)
           mma_f16_ts_on(lead, tmem + kTOP + 128 * h, tmem + kTS + 128 * h + 8 * ks, dv + 2048 * ks / 16,
-                         id_o, !(first_tile && ks == 0));
+                        id_o, !(first_tile && ks == 0));
         mma_commit_on(lead, bar_o + 8 * h);
       };
       while (true) {
@@ -423,28 +423,29 @@ __global__ void __launch_bounds__(kThreadsP, 1)
         if (!ok || !sg->more) break;
         const int tiles = (sg->key1 - sg->key0) / kTile;
         seg_done(seg);
-        for (int t = 0; t < tiles && ok; ++t, ++it) {
-          // what the tile needs besides P: its keys, and the values of the tile before
-          ok = mbar_wait(bar_kf + 8 * (it % kKStages), (it / kKStages) & 1);
-          if (t > 0) ok = ok && mbar_wait(bar_bf + 8 * ((it - 1) & 1), ((it - 1) >> 1) & 1);
-          else ok = ok && mbar_wait(bar_q, seg & 1) && mbar_wait(bar_q + 8, seg & 1);
+        ok = mbar_wait(bar_kf + 8 * sk, (it / kKStages) & 1);
+        for (int h = 0; h < 2; ++h) {
+          ok = ok && mbar_wait(bar_q + 8 * h, seg & 1);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           tc_fence_after();
-          if (t > 0) pv(it - 1, 0, t == 1);
-          if (!ok) break;
-          qk(it, 0);
-          if (t > 0) {
-            pv(it - 1, 1, t == 1);
-            if (!ok) break;
-            mma_commit_on(lead, bar_be + 8 * ((it - 1) & 1));
-          }
-          qk(it, 1);
-          mma_commit_on(lead, bar_ke + 8 * (it % kKStages));
+          qk(h);
         }
-        if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar_bf + 8 * ((it - 1) & 1), ((it - 1) >> 1) & 1));
-        for (int h = 0; h < 2 && ok; ++h) pv(it - 1, h, tiles == 1);
-        if (ok) mma_commit_on(lead, bar_be + 8 * ((it - 1) & 1));
+        for (int t = 1; ok; ++t) {
+          // O of the tile before, S of this one, half by half
+          mma_commit_on(lead, bar_ke + 8 * sk);
+          if (++sk == kKStages) sk = 0;
+          ++it;
+          const bool more = t < tiles;
+          pv(it - 1, 0, t == 1);
+          if (!ok) break;
+          if (more) qk(0);
+          pv(it - 1, 1, t == 1);
+          if (!ok) break;
+          mma_commit_on(lead, bar_be + 8 * ((it - 1) & 1));
+          if (!more) break;
+          qk(1);
+        }
         ++seg;
         if (!ok) break;
       }
@@ -544,8 +545,18 @@ __global__ void __launch_bounds__(kThreadsP, 1)
           *reinterpret_cast<uint4*>(d + (((k0 + 1) ^ (row & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
         }
         fence_proxy_async();
-        mbar_arrive(bar_bf + 8 * vb);
         mbar_arrive(bar_ve + 8 * sv);
+        // This warp's arrival on the barriers of P(it) tells the MMA issuer that V(it) is there, and
+        // the next keys: it then has one thing to wait for (a wait behind matrix instructions takes
+        // until they have left its queue).  Not before P(it - 1), whose phase it would count in.
+        if (it > 0) ok = mbar_wait(bar_p, (it - 1) & 1) && mbar_wait(bar_p + 8, (it - 1) & 1);
+        if (key0 + kTile < key1) ok = ok && mbar_wait(bar_kf + 8 * ((it + 1) % kKStages), ((it + 1) / kKStages) & 1);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        if (lane == 0) {
+          mbar_arrive(bar_p);
+          mbar_arrive(bar_p + 8);
+        }
       }
       ++seg;
       if (!ok) break;

@@ -12,8 +12,8 @@ the rest of the binding, marshalling only.  A cache is four tensors and two inde
 """
 from __future__ import annotations
 
-import ctypes
 import math
+import struct
 
 import torch
 
@@ -24,32 +24,33 @@ _BYTES = (torch.float8_e4m3fn, torch.uint8)
 _HALF, _EITHER = (_BF16,), (_BF16, _F32)
 _FLOAT = (_F32,)
 _INT = (torch.int32,)
+_UINT8 = (torch.uint8,)
 # the current stream's handle without a Stream object around it (a call's host time counts in decode)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-class _Cache(ctypes.Structure):
-    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
-                ("v_scale", ctypes.c_void_p), ("page_stride", ctypes.c_int64),
-                ("head_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64),
-                ("scale_stride", ctypes.c_int64), ("num_pages", ctypes.c_int32),
-                ("page_size", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
-                ("max_blocks", ctypes.c_int32), ("block_table", ctypes.c_void_p),
-                ("table_stride", ctypes.c_int64), ("kv_lens", ctypes.c_void_p)]
+# kda_kv_cache of kda.h, as ``_cache`` packs it
+_CACHE = struct.Struct("@PPPPqqqqiiiiPqP")
 
 
 def _check(t, name, dtypes, shape, dev, dense_from=1):
-    """Type, device and shape; dimensions from ``dense_from`` on are dense."""
-    if (isinstance(t, torch.Tensor) and t.device == dev and t.dtype in dtypes and t.shape == shape
-            and t.is_contiguous()):
-        return
+    """Type, device (its index) and shape; dimensions from ``dense_from`` on are dense.  Returns the stride of
+    the first dimension.  (Kept short for the usual contiguous tensor: a decode step's calls are
+    bound by their host time.)"""
+    if (isinstance(t, torch.Tensor) and t.get_device() == dev and t.dtype in dtypes
+            and t.shape == shape and t.is_contiguous()):
+        return t.stride(0) if shape[0] != 1 else t.numel()
+    return _check_slowly(t, name, dtypes, shape, dev, dense_from)
+
+
+def _check_slowly(t, name, dtypes, shape, dev, dense_from):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if dev is not None and t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
     if t.shape != shape:
@@ -61,50 +62,55 @@ def _check(t, name, dtypes, shape, dev, dense_from=1):
             raise ValueError(f"{name}: only the first {dense_from} dimension(s) may be strided"
                              if dense_from else f"{name} must be contiguous")
         inner *= sizes[d]
+    # a dimension of one element takes the dense stride: torch leaves it arbitrary
+    return strides[0] if sizes[0] > 1 else t.numel()
 
 
-def _row_stride(t, dense):
-    return t.stride(0) if t.shape[0] > 1 else dense
+def _need_cuda(t, name):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return t.get_device()
 
 
 def _stream(stream, dev):
-    return stream.cuda_stream if stream is not None else _raw_stream(dev.index)
+    return stream.cuda_stream if stream is not None else _raw_stream(dev)
 
 
 def _cache(k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, num_seqs, dev):
+    """The packed kda_kv_cache, and its number of kv heads."""
     shape = k_cache.shape
     if len(shape) != 4:
         raise ValueError("k_cache must be [pages, kv_heads, page_size, 128]")
     pages, hk, page, d = shape
     if d != HEAD_DIM:
         raise KDAError(ERR_INVALID_ARG, f"head_dim {d} (only {HEAD_DIM} is supported)")
-    _check(k_cache, "k_cache", _BYTES, shape, dev, 3)
+    per_page = _check(k_cache, "k_cache", _BYTES, shape, dev, 3)
     _check(v_cache, "v_cache", _BYTES, shape, dev, 3)
-    st, sc = k_cache.stride(), k_scale.stride()
+    st = k_cache.stride()
     if v_cache.stride() != st:
         raise ValueError("k_cache and v_cache must have the same strides")
-    _check(k_scale, "k_scale", _FLOAT, (pages, hk), dev)
-    _check(v_scale, "v_scale", _FLOAT, (pages, hk), dev)
-    if v_scale.stride() != sc:
+    scales = (pages, hk)
+    sc = _check(k_scale, "k_scale", _FLOAT, scales, dev)
+    if _check(v_scale, "v_scale", _FLOAT, scales, dev) != sc:
         raise ValueError("k_scale and v_scale must have the same strides")
-    if block_table.dim() != 2:
+    blocks = block_table.size(-1) if block_table.dim() == 2 else -1
+    if blocks < 0:
         raise ValueError("block_table must be [num_seqs, max_blocks]")
-    blocks = block_table.shape[1]
-    _check(block_table, "block_table", _INT, (num_seqs, blocks), dev)
+    row = _check(block_table, "block_table", _INT, (num_seqs, blocks), dev)
     _check(kv_lens, "kv_lens", _INT, (num_seqs,), dev, 0)
-    # dimensions of one element take the dense stride: torch leaves theirs arbitrary
     tok = st[2] if page > 1 else HEAD_DIM
     head = st[1] if hk > 1 else page * tok
-    return _Cache(k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
-                  st[0] if pages > 1 else hk * head, head, tok, sc[0] if pages > 1 else hk, pages,
-                  page, hk, blocks, block_table.data_ptr(), _row_stride(block_table, blocks),
-                  kv_lens.data_ptr())
+    return _CACHE.pack(k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                       per_page if pages > 1 else hk * head, head, tok, sc, pages, page, hk, blocks,
+                       block_table.data_ptr(), row if num_seqs > 1 else blocks, kv_lens.data_ptr()), hk
 
 
 def _status_workspace(workspace, dev):
     if workspace is None:
         return torch.zeros(256, dtype=torch.uint8, device=dev)
-    _check(workspace, "workspace", (torch.uint8,), workspace.shape, dev, 0)
+    _check(workspace, "workspace", _UINT8, workspace.shape, dev, 0)
     return workspace
 
 
@@ -156,52 +162,56 @@ def add_rms_norm(x, residual, weight, eps: float = 1e-6, want: str = "bf16", gro
     residual_out may be residual (the update is then in place).  Returns
     (residual_out, y, y8, y_scale) with None for what was not asked for.
     """
-    if x.dim() != 2:
+    dev = _need_cuda(x, "x")
+    shape = x.shape
+    if len(shape) != 2:
         raise ValueError("x must be 2-D")
-    if want not in ("bf16", "fp8", "both"):
-        raise ValueError(f"want must be 'bf16', 'fp8' or 'both', got {want!r}")
-    dev = x.device
-    T, C = x.shape
-    _check(x, "x", _HALF, x.shape, None)
+    T, C = shape
+    ldx = _check(x, "x", _HALF, shape, dev)
     _check(weight, "weight", _EITHER, (C,), dev, 0)
+    ldr = lds = ldy = ldy8 = C
+    r_ptr = s_ptr = y_ptr = y8_ptr = sc_ptr = None
+    r_kind = STATE_BF16
     if residual is not None:
-        _check(residual, "residual", _EITHER, x.shape, dev)
+        ldr = _check(residual, "residual", _EITHER, shape, dev)
+        r_ptr = residual.data_ptr()
+        if residual.dtype is _F32:
+            r_kind = STATE_F32
         if residual_out is None:
-            residual_out = torch.empty((T, C), dtype=residual.dtype, device=dev)
+            residual_out = torch.empty(shape, dtype=residual.dtype, device=dev)
         else:
-            _check(residual_out, "residual_out", (residual.dtype,), x.shape, dev)
+            lds = _check(residual_out, "residual_out", (residual.dtype,), shape, dev)
+        s_ptr = residual_out.data_ptr()
     elif residual_out is not None:
         raise ValueError("residual_out needs residual")
     if want == "fp8":
         if y is not None:
             raise ValueError("y is not written with want='fp8'")
-    elif y is None:
-        y = torch.empty((T, C), dtype=_BF16, device=dev)
     else:
-        _check(y, "y", _HALF, x.shape, dev)
-    if want == "bf16":
-        if y8 is not None or y_scale is not None:
-            raise ValueError("y8 and y_scale are not written with want='bf16'")
-    else:
+        if y is None:
+            y = torch.empty(shape, dtype=_BF16, device=dev)
+        else:
+            ldy = _check(y, "y", _HALF, shape, dev)
+        y_ptr = y.data_ptr()
+    if want != "bf16":
+        if want not in ("fp8", "both"):
+            raise ValueError(f"want must be 'bf16', 'fp8' or 'both', got {want!r}")
         groups = -(-C // 128) if group == 128 else 1
         if y8 is None:
-            y8 = torch.empty((T, C), dtype=torch.float8_e4m3fn, device=dev)
+            y8 = torch.empty(shape, dtype=torch.float8_e4m3fn, device=dev)
         else:
-            _check(y8, "y8", _BYTES, x.shape, dev)
+            ldy8 = _check(y8, "y8", _BYTES, shape, dev)
         if y_scale is None:
             y_scale = torch.empty((T, groups), dtype=_F32, device=dev)
         else:
             _check(y_scale, "y_scale", _FLOAT, (T, groups), dev, 0)
-    has_r, has_y, has_8 = residual is not None, y is not None, y8 is not None
+        y8_ptr, sc_ptr = y8.data_ptr(), y_scale.data_ptr()
+    elif y8 is not None or y_scale is not None:
+        raise ValueError("y8 and y_scale are not written with want='bf16'")
     rc = lib().kda_add_rms_norm(
-        x.data_ptr(), _row_stride(x, C), residual.data_ptr() if has_r else None,
-        _row_stride(residual, C) if has_r else C,
-        STATE_F32 if has_r and residual.dtype == _F32 else STATE_BF16, weight.data_ptr(),
-        STATE_F32 if weight.dtype == _F32 else STATE_BF16, eps,
-        residual_out.data_ptr() if has_r else None, _row_stride(residual_out, C) if has_r else C,
-        y.data_ptr() if has_y else None, _row_stride(y, C) if has_y else C,
-        y8.data_ptr() if has_8 else None, _row_stride(y8, C) if has_8 else C,
-        y_scale.data_ptr() if has_8 else None, group, T, C, _stream(stream, dev))
+        x.data_ptr(), ldx, r_ptr, ldr, r_kind, weight.data_ptr(),
+        STATE_F32 if weight.dtype is _F32 else STATE_BF16, eps, s_ptr, lds, y_ptr, ldy, y8_ptr, ldy8,
+        sc_ptr, group, T, C, _stream(stream, dev))
     if rc != OK:
         raise KDAError(rc, "kda_add_rms_norm")
     return residual_out, y, y8, y_scale
@@ -218,48 +228,50 @@ def rope_append(q, k, v, rope, k_cache, v_cache, k_scale, v_scale, block_table, 
     for the cache positions.  The cache tensors are updated in place.  Returns q_out (None
     without q).  workspace: uint8, at least 256 bytes, zero-filled once (device status).
     """
-    if k.dim() != 3:
+    dev = _need_cuda(k, "k")
+    shape = k.shape
+    if len(shape) != 3:
         raise ValueError("k must be [T, kv_heads, 128]")
-    dev = k.device
-    T, hk, d = k.shape
+    T, heads, d = shape
     if d != HEAD_DIM:
         raise KDAError(ERR_INVALID_ARG, f"head_dim {d} (only {HEAD_DIM} is supported)")
     N = cu_seqlens.numel() - 1
-    _check(k, "k", _HALF, k.shape, None)
-    _check(v, "v", _HALF, k.shape, dev)
-    heads = hk
+    k_row = _check(k, "k", _HALF, shape, dev)
+    v_row = _check(v, "v", _HALF, shape, dev)
+    q_ptr = qo_ptr = rope_ptr = pos_ptr = None
+    q_row = qo_row = rows = rot = 0
     if q is not None:
         if q.dim() != 3:
             raise ValueError("q must be [T, heads, 128]")
         heads = q.shape[1]
-        _check(q, "q", _HALF, (T, heads, d), dev)
+        q_shape = (T, heads, HEAD_DIM)
+        q_row = _check(q, "q", _HALF, q_shape, dev)
         if q_out is None:
-            q_out = torch.empty((T, heads, d), dtype=_BF16, device=dev)
+            q_out = torch.empty(q_shape, dtype=_BF16, device=dev)
+            qo_row = heads * HEAD_DIM
         else:
-            _check(q_out, "q_out", _HALF, (T, heads, d), dev)
+            qo_row = _check(q_out, "q_out", _HALF, q_shape, dev)
+        q_ptr, qo_ptr = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
         raise ValueError("q_out needs q")
     _check(cu_seqlens, "cu_seqlens", _INT, (N + 1,), dev, 0)
-    rows = rot = 0
     if rope is not None:
         if rope.dim() != 2:
             raise ValueError("rope must be [rows, rot_dim]")
         rows, rot = rope.shape
         _check(rope, "rope", _FLOAT, rope.shape, dev, 0)
+        rope_ptr = rope.data_ptr()
     if positions is not None:
         _check(positions, "positions", _INT, (T,), dev, 0)
-    c = _cache(k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, N, dev)
-    if c.kv_heads != hk:
-        raise ValueError(f"k has {hk} heads, the cache {c.kv_heads}")
+        pos_ptr = positions.data_ptr()
+    c, hk = _cache(k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, N, dev)
+    if hk != shape[1]:
+        raise ValueError(f"k has {shape[1]} heads, the cache {hk}")
     workspace = _status_workspace(workspace, dev)
     rc = lib().kda_rope_append(
-        None if q is None else q.data_ptr(), heads * d if q is None else _row_stride(q, heads * d),
-        k.data_ptr(), _row_stride(k, hk * d), v.data_ptr(), _row_stride(v, hk * d),
-        None if rope is None else rope.data_ptr(), rows, rot, int(bool(interleaved)),
-        None if positions is None else positions.data_ptr(),
-        None if q is None else q_out.data_ptr(), heads * d if q is None else _row_stride(q_out, heads * d),
-        ctypes.byref(c), cu_seqlens.data_ptr(), workspace.data_ptr(), _stream(stream, dev), T, N,
-        heads, workspace.numel())
+        q_ptr, q_row, k.data_ptr(), k_row, v.data_ptr(), v_row, rope_ptr, rows, rot,
+        1 if interleaved else 0, pos_ptr, qo_ptr, qo_row, c, cu_seqlens.data_ptr(),
+        workspace.data_ptr(), _stream(stream, dev), T, N, heads, workspace.numel())
     if rc != OK:
         raise KDAError(rc, "kda_rope_append")
     return q_out
@@ -288,35 +300,38 @@ def cached_attention(q, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens
     (allocate fp32 [T, heads]) or a tensor.  workspace: ``alloc_attention_workspace`` of the same
     sizes or larger ones.  Returns (out, lse or None).
     """
-    if q.dim() != 3:
+    dev = _need_cuda(q, "q")
+    shape = q.shape
+    if len(shape) != 3:
         raise ValueError("q must be [T, heads, 128]")
-    dev = q.device
-    T, heads, d = q.shape
+    T, heads, d = shape
     if d != HEAD_DIM:
         raise KDAError(ERR_INVALID_ARG, f"head_dim {d} (only {HEAD_DIM} is supported)")
     N = cu_seqlens.numel() - 1
-    _check(q, "q", _HALF, q.shape, None)
+    q_row = _check(q, "q", _HALF, shape, dev)
     _check(cu_seqlens, "cu_seqlens", _INT, (N + 1,), dev, 0)
-    c = _cache(k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, N, dev)
+    c, hk = _cache(k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, N, dev)
+    out_row = heads * HEAD_DIM
     if out is None:
-        out = torch.empty((T, heads, d), dtype=_BF16, device=dev)
+        out = torch.empty(shape, dtype=_BF16, device=dev)
     else:
-        _check(out, "out", _HALF, q.shape, dev)
-    if lse is True:
-        lse = torch.empty((T, heads), dtype=_F32, device=dev)
-    elif lse is False:
+        out_row = _check(out, "out", _HALF, shape, dev)
+    lse_ptr = None
+    if lse is False:
         lse = None
     else:
-        _check(lse, "lse", _FLOAT, (T, heads), dev, 0)
+        if lse is True:
+            lse = torch.empty((T, heads), dtype=_F32, device=dev)
+        else:
+            _check(lse, "lse", _FLOAT, (T, heads), dev, 0)
+        lse_ptr = lse.data_ptr()
     if workspace is None:
-        workspace = alloc_attention_workspace(N, heads, c.kv_heads, max_q_len, dev)
+        workspace = alloc_attention_workspace(N, heads, hk, max_q_len, dev)
     else:
-        _check(workspace, "workspace", (torch.uint8,), workspace.shape, dev, 0)
+        _check(workspace, "workspace", _UINT8, workspace.shape, dev, 0)
     rc = lib().kda_cached_attention(
-        q.data_ptr(), _row_stride(q, heads * d), ctypes.byref(c), cu_seqlens.data_ptr(), scale,
-        softcap, window, out.data_ptr(), _row_stride(out, heads * d),
-        None if lse is None else lse.data_ptr(), workspace.data_ptr(), _stream(stream, dev), T, N,
-        heads, max_q_len, workspace.numel())
+        q.data_ptr(), q_row, c, cu_seqlens.data_ptr(), scale, softcap, window, out.data_ptr(), out_row,
+        lse_ptr, workspace.data_ptr(), _stream(stream, dev), T, N, heads, max_q_len, workspace.numel())
     if rc != OK:
         raise KDAError(rc, "kda_cached_attention")
     return out, lse

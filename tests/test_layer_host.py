@@ -8,9 +8,18 @@ import torch
 
 import kda_gated_delta_chunk_gb300 as kda
 from kda_gated_delta_chunk_gb300 import build as kbuild
-from kda_gated_delta_chunk_gb300 import layer
 
 A = 1 << 20        # a 16-byte aligned stand-in for a device pointer: never dereferenced here
+
+
+class Cache(ctypes.Structure):      # kda_kv_cache of kda.h
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("page_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64),
+                ("scale_stride", ctypes.c_int64), ("num_pages", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+                ("max_blocks", ctypes.c_int32), ("block_table", ctypes.c_void_p),
+                ("table_stride", ctypes.c_int64), ("kv_lens", ctypes.c_void_p)]
 
 
 @pytest.fixture(scope="module")
@@ -44,7 +53,7 @@ def cache(**over):
              scale_stride=2, num_pages=3, page_size=16, kv_heads=2, max_blocks=4, block_table=A,
              table_stride=4, kv_lens=A)
     a.update(over)
-    return layer._Cache(*a.values())
+    return Cache(*a.values())
 
 
 def append(L, c=None, **over):
@@ -140,3 +149,12 @@ def test_attention_workspace_size(L):
     a = kda.attention_workspace_size(4, 8, 2, 1)
     assert a >= 256 and a % 16 == 0
     assert L.kda_cached_attention is not None
+
+
+def test_binding_packs_the_cache_as_the_header_lays_it_out():
+    from kda_gated_delta_chunk_gb300 import layer
+    names = [n for n, _ in Cache._fields_]
+    raw = layer._CACHE.pack(*range(1, len(names) + 1))
+    got = Cache.from_buffer_copy(raw)
+    assert layer._CACHE.size == ctypes.sizeof(Cache)
+    assert [getattr(got, n) for n in names] == list(range(1, len(names) + 1))
