@@ -70,6 +70,8 @@ constexpr int kSlotFloats = NR * 130;
 struct DecodeParams {
   AttnParams a;
   CacheMaps maps;
+  int group;                 // query heads of a kv head
+  uint32_t group_magic;      // 65535 / group + 1 (div_small)
   int min_rows, max_rows;
   PartDesc* desc;
   float* slots;
@@ -134,7 +136,9 @@ __global__ void __launch_bounds__(kThreads, 2)
   };
   Misc* misc = reinterpret_cast<Misc*>(sm + C::kOffMisc);
   static_assert(sizeof(Misc) <= 128, "misc");
-  const int hk = p.a.c.kv_heads, N = p.a.num_seqs, G = p.a.heads / hk, P = p.a.c.page_size;
+  const int hk = p.a.c.kv_heads, N = p.a.num_seqs, P = p.a.c.page_size;
+  const int G = p.group;
+  const uint32_t gm = p.group_magic;
 
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
@@ -357,9 +361,10 @@ __global__ void __launch_bounds__(kThreads, 2)
       for (int i = 0; i < NR / 8; ++i) {
         const int r = 8 * i + (tid >> 4);
         qraw[i] = make_uint4(0, 0, 0, 0);
+        const int t = div_small(r, gm);
         if (r < w.s.q_len * G)
-          qraw[i] = *reinterpret_cast<const uint4*>(p.a.q + (int64_t)(w.s.tok0 + r / G) * p.a.q_stride +
-                                                    (w.h * G + r % G) * kHeadDim + 8 * (tid & 15));
+          qraw[i] = *reinterpret_cast<const uint4*>(p.a.q + (int64_t)(w.s.tok0 + t) * p.a.q_stride +
+                                                    (w.h * G + r - t * G) * kHeadDim + 8 * (tid & 15));
       }
     };
     bool more = walk.next(p);
@@ -383,20 +388,11 @@ __global__ void __launch_bounds__(kThreads, 2)
                        ((__float_as_uint(top) & 0x7fffffu) > 0x600000u ? 1 : 0);
         const int e2c = max(e2, -100);
         const float inv = __uint_as_float((uint32_t)(127 - e2c) << 23);
-        float y1[8], y2[8];
-        uint32_t w1[2], w2[2];
+        uint32_t t1[4], t2[4];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) y1[e] = x[e] * inv;
-        w1[0] = e4m3x4(y1[0], y1[1], y1[2], y1[3]);
-        w1[1] = e4m3x4(y1[4], y1[5], y1[6], y1[7]);
-#pragma unroll
-        for (int e = 0; e < 8; e += 2) {
-          const float2 b = from_e4m3x2((w1[e >> 2] >> (8 * (e & 3))) & 0xffff);
-          y2[e] = y1[e] - b.x;
-          y2[e + 1] = y1[e + 1] - b.y;
-        }
-        w2[0] = e4m3x4(y2[0], y2[1], y2[2], y2[3]);
-        w2[1] = e4m3x4(y2[4], y2[5], y2[6], y2[7]);
+        for (int e = 0; e < 4; ++e) split_e4m3x2(x[2 * e] * inv, x[2 * e + 1] * inv, t1[e], t2[e]);
+        const uint32_t w1[2] = {t1[0] | (t1[1] << 16), t1[2] | (t1[3] << 16)};
+        const uint32_t w2[2] = {t2[0] | (t2[1] << 16), t2[2] | (t2[3] << 16)};
         *reinterpret_cast<uint2*>(sm + C::kOffQ + tile_off(r, 8 * c)) = make_uint2(w1[0], w1[1]);
         *reinterpret_cast<uint2*>(sm + C::kOffQ + tile_off(NR + r, 8 * c)) = make_uint2(w2[0], w2[1]);
         if (c == 0) {   // a non-finite query makes its row NaN
@@ -452,7 +448,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             const int key = (walk.s.tile0 + t) * kTile + x;
 #pragma unroll
             for (int r = 0; r < NR; ++r) {
-              const int pos = first_pos + r / G;
+              const int pos = first_pos + div_small(r, gm);
               if (key <= pos && (p.a.window <= 0 || key > pos - p.a.window)) acc[r] = NAN;
             }
           }
@@ -543,7 +539,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           }
 #pragma unroll
           for (int r = 0; r < NR; ++r) {
-            const int pos = first_pos + r / G;
+            const int pos = first_pos + div_small(r, gm);
             if (!(key <= pos && (p.a.window <= 0 || key > pos - p.a.window))) x[r] = -INFINITY;
           }
         }
@@ -621,14 +617,14 @@ __global__ void __launch_bounds__(kThreads, 2)
         for (int r = 0; r < NR; ++r) {
           const float il = __shfl_sync(0xffffffffu, inv_l, r);
           if (r < rows) {
-            const int64_t tok = walk.s.tok0 + r / G;
-            p.a.out[tok * p.a.out_stride + (walk.h * G + r % G) * kHeadDim + tid] =
+            const int i = div_small(r, gm);
+            p.a.out[(int64_t)(walk.s.tok0 + i) * p.a.out_stride + (walk.h * G + r - i * G) * kHeadDim + tid] =
                 __float2bfloat16_rn(acc[r] * il);
           }
         }
         if (p.a.lse && warp == 0 && lane < rows) {
-          const int64_t tok = walk.s.tok0 + lane / G;
-          p.a.lse[tok * p.a.heads + walk.h * G + lane % G] =
+          const int i = div_small(lane, gm);
+          p.a.lse[(int64_t)(walk.s.tok0 + i) * p.a.heads + walk.h * G + lane - i * G] =
               den == 0.0f ? -INFINITY : (run + lg2(den)) * kLn2;
         }
       } else {
@@ -790,6 +786,8 @@ cudaError_t launch_attn_decode(const AttnParams& a, int min_rows, int max_rows, 
   DecodeParams d;
   d.a = a;
   if (!make_cache_maps(a.c, &d.maps)) return cudaErrorNotSupported;
+  d.group = a.heads / a.c.kv_heads;
+  d.group_magic = 65535u / (uint32_t)d.group + 1;
   d.min_rows = min_rows;
   d.max_rows = max_rows;
   d.desc = static_cast<PartDesc*>(work);

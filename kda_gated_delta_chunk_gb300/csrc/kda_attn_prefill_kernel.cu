@@ -35,7 +35,7 @@ namespace {
 constexpr int kThreadsP = 768;
 constexpr int kRowsP = 256;
 constexpr int kKStages = 3, kVStages = 2, kSegs = 4;
-constexpr int kSoftWarps = 16, kRegsSoftmax = 96, kRegsOther = 48;
+constexpr int kSoftWarps = 16, kRegsSoftmax = 104, kRegsOther = 32;
 constexpr int kRegsNeeded = 32 * (kSoftWarps * kRegsSoftmax + (kThreadsP / 32 - kSoftWarps) * kRegsOther);
 constexpr float kSlack = 8.0f;              // log2 growth of the maximum before O is rescaled
 constexpr float kPShift = 7.0f;             // log2 of the numerator at the maximum: at most 2^15 with the slack
@@ -68,6 +68,8 @@ struct PartDescP {
 struct PrefillParams {
   AttnParams a;
   CacheMaps maps;
+  int group;                 // query heads of a kv head
+  uint32_t group_magic;      // 65535 / group + 1 (div_small)
   int min_rows, tokens;      // tokens: new tokens per row tile (256 / group)
   PartDescP* desc;
   float* slots;
@@ -158,7 +160,9 @@ __global__ void __launch_bounds__(kThreadsP, 1)
   };
   Misc* misc = reinterpret_cast<Misc*>(sm + kOffMiscP);
   static_assert(sizeof(Misc) <= 320, "misc");
-  const int hk = p.a.c.kv_heads, N = p.a.num_seqs, G = p.a.heads / hk, P = p.a.c.page_size;
+  const int hk = p.a.c.kv_heads, N = p.a.num_seqs, P = p.a.c.page_size;
+  const int G = p.group;
+  const uint32_t gm = p.group_magic;
 
   if (tid == 0) {
     for (int i = 0; i < kKStages; ++i) {
@@ -460,17 +464,25 @@ __global__ void __launch_bounds__(kThreadsP, 1)
       __syncwarp();
     } else if (warp == kSoftWarps + 6) {
       // ================= scheduler: this CTA's segments, one after the other
-      if (lane == 0) {
-        PartDescP part = {0, 0, 0, 0};
-        bool ok = true;
-        for (uint32_t seg = 0;; ++seg) {
-          const bool more = walk.next(p);
-          if (seg >= kSegs) ok = mbar_wait(bar_ge + 8 * (seg % kSegs), (seg / kSegs - 1) & 1);
-          if (!ok) break;
+      PartDescP part = {0, 0, 0, 0};
+      bool ok = true;
+      for (uint32_t seg = 0;; ++seg) {
+        const bool more = walk.next(p);
+        const int tok0 = walk.s.tok0 + walk.it.tok;
+        if (more)       // its queries towards L2: a token's heads of this kv head are 256 * group bytes
+          for (int i = lane; i < walk.it.cnt * ((G + 15) / 16); i += 32) {
+            const int t = i / ((G + 15) / 16), h = (i % ((G + 15) / 16)) * 16;
+            l2_prefetch(p.a.q + (int64_t)(tok0 + t) * p.a.q_stride + (walk.ch * G + h) * kHeadDim,
+                        min(16, G - h) * kHeadDim * 2);
+          }
+        if (seg >= kSegs) ok = mbar_wait(bar_ge + 8 * (seg % kSegs), (seg / kSegs - 1) & 1);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        if (lane == 0) {
           Segment* g = reinterpret_cast<Segment*>(sm + kOffSeg) + seg % kSegs;
           g->more = more;
           if (more) {
-            g->tok0 = walk.s.tok0 + walk.it.tok;
+            g->tok0 = tok0;
             g->cnt = walk.it.cnt;
             g->head0 = walk.ch * G;
             g->p_first = walk.s.len - walk.s.q_len + walk.it.tok;
@@ -481,17 +493,19 @@ __global__ void __launch_bounds__(kThreadsP, 1)
             g->whole = walk.a == 0 && walk.b == walk.it.tiles;
             g->begins = walk.a == 0;
             g->table = p.a.c.block_table + walk.n * p.a.c.table_stride;
-            if (walk.a == 0 && walk.b < walk.it.tiles) {   // the CTA that the item's last tile lies in
-              const int64_t last = walk.pos - (walk.b - walk.a) + walk.it.tiles - 1;
-              part.n = walk.n;
-              part.h = walk.ch;
-              part.rt = walk.crt;
-              part.parts = (int)(((last + 1) * ranges - 1) / total - blockIdx.x) + 1;
-            }
           }
           mbar_arrive(bar_gf + 8 * (seg % kSegs));
-          if (!more) break;
         }
+        if (!more) break;
+        if (walk.a == 0 && walk.b < walk.it.tiles) {   // the CTA that the item's last tile lies in
+          const int64_t last = walk.pos - (walk.b - walk.a) + walk.it.tiles - 1;
+          part.n = walk.n;
+          part.h = walk.ch;
+          part.rt = walk.crt;
+          part.parts = (int)(((last + 1) * ranges - 1) / total - blockIdx.x) + 1;
+        }
+      }
+      if (lane == 0) {
         if (!ok) record_error(p.a.status, KDA_ERR_DEVICE_TIMEOUT, 337);
         p.desc[blockIdx.x] = part;
       }
@@ -595,8 +609,9 @@ __global__ void __launch_bounds__(kThreadsP, 1)
         for (int j = 0; j < 8; ++j) {
           const int r = r0 + 2 * j;
           u[j] = make_uint4(0, 0, 0, 0);
+          const int i = div_small(r, gm);
           if (r < rows)
-            u[j] = *reinterpret_cast<const uint4*>(src + (int64_t)(r / G) * p.a.q_stride + (r % G) * kHeadDim);
+            u[j] = *reinterpret_cast<const uint4*>(src + (int64_t)i * p.a.q_stride + (r - i * G) * kHeadDim);
         }
         unsigned char* q1 = sm + kOffQ + half * 32768;
 #pragma unroll 2
@@ -613,19 +628,11 @@ __global__ void __launch_bounds__(kThreadsP, 1)
                          ((__float_as_uint(top) & 0x7fffffu) > 0x600000u ? 1 : 0);
           const int e2c = max(e2, -100);
           const float inv = sign * __uint_as_float((uint32_t)(127 - e2c) << 23);
-          uint32_t w1[2], w2[2];
+          uint32_t t1[4], t2[4];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] *= inv;
-          w1[0] = e4m3x4(x[0], x[1], x[2], x[3]);
-          w1[1] = e4m3x4(x[4], x[5], x[6], x[7]);
-#pragma unroll
-          for (int e = 0; e < 8; e += 2) {
-            const float2 b = from_e4m3x2((w1[e >> 2] >> (8 * (e & 3))) & 0xffff);
-            x[e] -= b.x;
-            x[e + 1] -= b.y;
-          }
-          w2[0] = e4m3x4(x[0], x[1], x[2], x[3]);
-          w2[1] = e4m3x4(x[4], x[5], x[6], x[7]);
+          for (int e = 0; e < 4; ++e) split_e4m3x2(x[2 * e] * inv, x[2 * e + 1] * inv, t1[e], t2[e]);
+          const uint32_t w1[2] = {t1[0] | (t1[1] << 16), t1[2] | (t1[3] << 16)};
+          const uint32_t w2[2] = {t2[0] | (t2[1] << 16), t2[2] | (t2[3] << 16)};
           *reinterpret_cast<uint2*>(q1 + tile_off(r & 127, 8 * c)) = make_uint2(w1[0], w1[1]);
           *reinterpret_cast<uint2*>(q1 + 16384 + tile_off(r & 127, 8 * c)) = make_uint2(w2[0], w2[1]);
           if (c == 0) {   // a non-finite query makes its row NaN
@@ -640,8 +647,9 @@ __global__ void __launch_bounds__(kThreadsP, 1)
       const float qmul = qmul_s[row];
       // relative to the tile's first key: this row's position, and those of the half's first and last
       const int last = sg->cnt - 1, rel = sg->p_first - sg->key0;
-      int hi = rel + (row < rows ? row / G : last) - 64 * cg;
-      int p_lo = rel + min(128 * half / G, last), p_hi = rel + max(min(rows, 128 * half + 128) - 1, 0) / G;
+      int hi = rel + (row < rows ? div_small(row, gm) : last) - 64 * cg;
+      int p_lo = rel + min(div_small(128 * half, gm), last);
+      int p_hi = rel + div_small(max(min(rows, 128 * half + 128) - 1, 0), gm);
       const int tiles = (sg->key1 - sg->key0) / kTile;
       float m = -INFINITY, l = 0.0f;
       for (int t = 0; t < tiles; ++t, ++it, hi -= kTile, p_lo -= kTile, p_hi -= kTile) {
@@ -660,18 +668,22 @@ __global__ void __launch_bounds__(kThreadsP, 1)
         float mt = -INFINITY;
         const bool scaled = kCap || masked;    // s holds the finished exponents (else raw products)
         if (scaled) {
-          const int lo = p.a.window > 0 ? hi - p.a.window + 1 : -1;
+          // bits of the 64 keys that this row sees: lo <= e <= hi
+          const int lo = p.a.window > 0 ? hi - p.a.window + 1 : 0;
+          const uint64_t upto = hi < 0 ? 0 : (hi >= 63 ? ~0ull : (2ull << hi) - 1);
+          const uint64_t see = lo <= 0 ? upto : (lo >= 64 ? 0 : upto & (~0ull << lo));
 #pragma unroll
           for (int g = 0; g < 4; ++g) {
             const float4 f = sc[g];
             const float mul = qmul * f.x;
+            const uint32_t bits = (uint32_t)(see >> (32 * (g >> 1))) >> (16 * (g & 1));
 #pragma unroll
-            for (int e = 16 * g; e < 16 * g + 16; ++e) {
-              float x = __uint_as_float(s[e]);
+            for (int e = 0; e < 16; ++e) {
+              float x = __uint_as_float(s[16 * g + e]);
               x = kCap ? cap_score(x * mul, cap2, cap1) + f.y : fmaf(x, mul, f.y);
-              if (e > hi || e < lo) x = -INFINITY;
+              if (!((bits >> e) & 1)) x = -INFINITY;
               mt = fmaxf(mt, x);
-              s[e] = __float_as_uint(x);
+              s[16 * g + e] = __float_as_uint(x);
             }
           }
         } else {
@@ -744,7 +756,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
       const bool poisoned = *reinterpret_cast<volatile int*>(&misc->poison[seg & 7]) != 0;
       const bool live = row < rows, whole = sg->whole;
       const float inv_l = l == 0.0f ? 0.0f : 1.0f / l;
-      const int i_tok = live ? row / G : last, head = sg->head0 + (live ? row % G : 0);
+      const int i_tok = live ? div_small(row, gm) : last, head = sg->head0 + (live ? row - i_tok * G : 0);
       const int64_t tok = sg->tok0 + i_tok;
       float* slot = p.slots + ((int64_t)2 * blockIdx.x + (sg->begins ? 1 : 0)) * kSlotFloatsP;
       unsigned char* stage = sm + kOffQ + half * 32768 + (warp & 7) * 4096;
@@ -911,7 +923,9 @@ cudaError_t launch_attn_prefill(const AttnParams& a, int min_rows, void* work, i
   d.a = a;
   if (!make_cache_maps(a.c, &d.maps)) return cudaErrorNotSupported;
   d.min_rows = min_rows;
-  d.tokens = kRowsP / (a.heads / a.c.kv_heads);
+  d.group = a.heads / a.c.kv_heads;
+  d.group_magic = 65535u / (uint32_t)d.group + 1;
+  d.tokens = kRowsP / d.group;
   d.desc = static_cast<PartDescP*>(work);
   d.slots = reinterpret_cast<float*>(d.desc + sms);
   return a.softcap > 0.0f ? launch_cap<true>(d, sms, stream) : launch_cap<false>(d, sms, stream);

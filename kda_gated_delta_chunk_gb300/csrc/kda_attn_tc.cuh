@@ -91,6 +91,21 @@ __device__ __forceinline__ uint32_t f16x2_of_e4m3x2(uint32_t v) {
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)v));
   return h;
 }
+// Two e4m3 terms of a pair of values that f16 holds exactly (bf16 values scaled to at most 448):
+// x = first + second but for what lies below 2^-10.  Low halves of the results.
+__device__ __forceinline__ void split_e4m3x2(float x0, float x1, uint32_t& first, uint32_t& second) {
+  const uint32_t h = f16x2_of(x0, x1);
+  uint16_t a, b;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(a) : "r"(h));
+  const uint32_t back = f16x2_of_e4m3x2(a);
+  uint32_t r;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(h), "r"(back));
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(b) : "r"(r));
+  first = a;
+  second = b;
+}
+// r / g for 0 <= r < 256 and 1 <= g <= 256, with magic = 65535 / g + 1.
+__device__ __forceinline__ int div_small(int r, uint32_t magic) { return (int)(((uint32_t)r * magic) >> 16); }
 // 8-bit tiles with the 128-byte swizzle: a row of 128 bytes per token (key, query row), rows in
 // groups of 8; the 16-byte chunk index is XORed with row % 8.  As a K-major operand (channels
 // along K) a K step of 32 is 32 bytes on; as an MN-major one (tokens along K) 32 rows.
