@@ -72,6 +72,7 @@ struct DecodeParams {
   CacheMaps maps;
   int group;                 // query heads of a kv head
   uint32_t group_magic;      // 65535 / group + 1 (div_small)
+  int wait;                  // the merge waits for the kernel before it (programmatic launch)
   int min_rows, max_rows;
   PartDesc* desc;
   float* slots;
@@ -669,7 +670,8 @@ __global__ void __launch_bounds__(64 * kMergeWarps)
     kda_attn_merge_kernel(const __grid_constant__ DecodeParams p) {
   __shared__ float4 acc_s[2][kMergeWarps][32];
   __shared__ float den_s[2][kMergeWarps];
-  pdl_wait();
+  if (p.wait) pdl_wait();
+  else pdl_launch_dependents();
   const PartDesc d = p.desc[blockIdx.x];
   if (d.parts == 0) return;
   const int lane = threadIdx.x & 31, w0 = (threadIdx.x >> 5) % kMergeWarps, rr = threadIdx.x / (32 * kMergeWarps);
@@ -726,7 +728,7 @@ __global__ void __launch_bounds__(64 * kMergeWarps)
 int decode_ctas(int sms) { return 2 * sms; }
 
 template <int NR, bool kCap>
-cudaError_t launch_nr(DecodeParams& d, int sms, cudaStream_t stream) {
+cudaError_t launch_nr(const DecodeParams& d, int sms, cudaStream_t stream) {
   static PerDeviceOnce once;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -736,20 +738,13 @@ cudaError_t launch_nr(DecodeParams& d, int sms, cudaStream_t stream) {
                                 cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<NR>::kBytes);
   });
   if (e != cudaSuccess) return e;
-  const int ctas = decode_ctas(sms);
-  kda_attn_decode_kernel<NR, kCap><<<ctas, kThreads, Cfg<NR>::kBytes, stream>>>(d);
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)ctas, NR / 2);
-  cfg.blockDim = dim3(64 * kMergeWarps);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kda_attn_merge_kernel<NR>, d);
+  return launch(kda_attn_decode_kernel<NR, kCap>, dim3((unsigned)decode_ctas(sms)), dim3(kThreads),
+                Cfg<NR>::kBytes, false, stream, d);
+}
+template <int NR>
+cudaError_t launch_merge(const DecodeParams& d, int sms, cudaStream_t stream) {
+  return launch(kda_attn_merge_kernel<NR>, dim3((unsigned)decode_ctas(sms), NR / 2), dim3(64 * kMergeWarps),
+                0, d.wait != 0, stream, d);
 }
 
 }  // namespace
@@ -781,22 +776,40 @@ size_t decode_workspace_bytes(int sms) {
   return ctas * sizeof(PartDesc) + ctas * 2 * kSlotFloats<32> * sizeof(float);
 }
 
-cudaError_t launch_attn_decode(const AttnParams& a, int min_rows, int max_rows, void* work, int sms,
+namespace {
+bool make_params(const AttnParams& a, int max_rows, void* work, int sms, DecodeParams* d) {
+  d->a = a;
+  if (!make_cache_maps(a.c, &d->maps)) return false;
+  d->wait = 0;
+  d->group = a.heads / a.c.kv_heads;
+  d->group_magic = 65535u / (uint32_t)d->group + 1;
+  d->min_rows = 1;
+  d->max_rows = max_rows;
+  d->desc = static_cast<PartDesc*>(work);
+  d->slots = reinterpret_cast<float*>(d->desc + decode_ctas(sms));
+  return true;
+}
+}  // namespace
+
+// The operands are padded to 8, 16 or 32 rows.
+cudaError_t launch_attn_decode(const AttnParams& a, int max_rows, void* work, int sms,
                                cudaStream_t stream) {
   DecodeParams d;
-  d.a = a;
-  if (!make_cache_maps(a.c, &d.maps)) return cudaErrorNotSupported;
-  d.group = a.heads / a.c.kv_heads;
-  d.group_magic = 65535u / (uint32_t)d.group + 1;
-  d.min_rows = min_rows;
-  d.max_rows = max_rows;
-  d.desc = static_cast<PartDesc*>(work);
-  d.slots = reinterpret_cast<float*>(d.desc + decode_ctas(sms));
+  if (!make_params(a, max_rows, work, sms, &d)) return cudaErrorNotSupported;
   const bool cap = a.softcap > 0.0f;
-  // the row count the operands are padded to
   if (max_rows <= 8) return cap ? launch_nr<8, true>(d, sms, stream) : launch_nr<8, false>(d, sms, stream);
   if (max_rows <= 16) return cap ? launch_nr<16, true>(d, sms, stream) : launch_nr<16, false>(d, sms, stream);
   return cap ? launch_nr<32, true>(d, sms, stream) : launch_nr<32, false>(d, sms, stream);
+}
+
+cudaError_t launch_attn_decode_merge(const AttnParams& a, int max_rows, void* work, int sms, bool wait,
+                                     cudaStream_t stream) {
+  DecodeParams d;
+  if (!make_params(a, max_rows, work, sms, &d)) return cudaErrorNotSupported;
+  d.wait = wait;
+  return max_rows <= 8    ? launch_merge<8>(d, sms, stream)
+         : max_rows <= 16 ? launch_merge<16>(d, sms, stream)
+                          : launch_merge<32>(d, sms, stream);
 }
 
 }  // namespace attn

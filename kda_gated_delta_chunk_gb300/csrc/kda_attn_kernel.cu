@@ -17,6 +17,8 @@ int device_sms() {
   return sms;
 }
 
+size_t align16(size_t n) { return (n + 15) & ~(size_t)15; }
+
 // Rows (new tokens x heads per kv head) of a sequence that go to the decode kernel: up to 32.
 int decode_rows(int64_t rows, int group) {
   return group > kDecodeRows ? 0 : (int)(rows < kDecodeRows ? rows : kDecodeRows);
@@ -28,25 +30,28 @@ size_t attn_workspace_bytes(int32_t num_seqs, int32_t heads, int32_t kv_heads, i
   (void)num_seqs;
   const int sms = device_sms(), group = heads / kv_heads;
   const int64_t rows = (int64_t)max_q_len * group;
-  size_t need = 0;
-  if (decode_rows(rows, group) > 0) need = decode_workspace_bytes(sms);
-  if (rows > decode_rows(rows, group)) need = need > prefill_workspace_bytes(sms) ? need : prefill_workspace_bytes(sms);
-  return (size_t)kWorkspaceBytes + need;
+  const int few = decode_rows(rows, group);
+  return (size_t)kWorkspaceBytes + (few > 0 ? align16(decode_workspace_bytes(sms)) : 0) +
+         (rows > few ? prefill_workspace_bytes(sms) : 0);
 }
 
 // Sequences with at most 32 rows per kv head take the decode kernel, the others of the same call
-// the prefill kernel; a launch is left out when max_q_len says that no sequence can need it.  The
-// two run one after the other and share the area for partial results.
+// the prefill kernel; a launch is left out when max_q_len says that no sequence can need it.
+// With both, the prefill kernel is launched as the decode kernel's dependent and waits for
+// nothing (its CTAs start as SMs come free), the first merge is an ordinary launch behind both,
+// and the second one runs beside it.
 cudaError_t launch_attn(const AttnParams& p, int sms, cudaStream_t stream) {
   const int group = p.heads / p.c.kv_heads;
   const int64_t rows = (int64_t)p.max_q_len * group;
   const int few = decode_rows(rows, group);
+  const bool many = rows > few;
   char* work = reinterpret_cast<char*>(p.status) + kWorkspaceBytes;
-  if (few > 0) {
-    const cudaError_t e = launch_attn_decode(p, 1, few, work, sms, stream);
-    if (e != cudaSuccess) return e;
-  }
-  return rows > few ? launch_attn_prefill(p, few + 1, work, sms, stream) : cudaSuccess;
+  char* work2 = work + (few > 0 ? align16(decode_workspace_bytes(sms)) : 0);
+  cudaError_t e = cudaSuccess;
+  if (few > 0 && (e = launch_attn_decode(p, few, work, sms, stream)) != cudaSuccess) return e;
+  if (many && (e = launch_attn_prefill(p, few + 1, work2, sms, few > 0, stream)) != cudaSuccess) return e;
+  if (few > 0 && (e = launch_attn_decode_merge(p, few, work, sms, !many, stream)) != cudaSuccess) return e;
+  return many ? launch_attn_prefill_merge(p, few + 1, work2, sms, few == 0, stream) : cudaSuccess;
 }
 
 }  // namespace attn

@@ -70,6 +70,7 @@ struct PrefillParams {
   CacheMaps maps;
   int group;                 // query heads of a kv head
   uint32_t group_magic;      // 65535 / group + 1 (div_small)
+  int wait;                  // the merge waits for the kernel before it (programmatic launch)
   int min_rows, tokens;      // tokens: new tokens per row tile (256 / group)
   PartDescP* desc;
   float* slots;
@@ -469,12 +470,6 @@ __global__ void __launch_bounds__(kThreadsP, 1)
       for (uint32_t seg = 0;; ++seg) {
         const bool more = walk.next(p);
         const int tok0 = walk.s.tok0 + walk.it.tok;
-        if (more)       // its queries towards L2: a token's heads of this kv head are 256 * group bytes
-          for (int i = lane; i < walk.it.cnt * ((G + 15) / 16); i += 32) {
-            const int t = i / ((G + 15) / 16), h = (i % ((G + 15) / 16)) * 16;
-            l2_prefetch(p.a.q + (int64_t)(tok0 + t) * p.a.q_stride + (walk.ch * G + h) * kHeadDim,
-                        min(16, G - h) * kHeadDim * 2);
-          }
         if (seg >= kSegs) ok = mbar_wait(bar_ge + 8 * (seg % kSegs), (seg / kSegs - 1) & 1);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
@@ -497,6 +492,12 @@ __global__ void __launch_bounds__(kThreadsP, 1)
           mbar_arrive(bar_gf + 8 * (seg % kSegs));
         }
         if (!more) break;
+        if (seg > 0)    // its queries towards L2 (the first's are wanted at once)
+          for (int i = lane; i < walk.it.cnt * ((G + 15) / 16); i += 32) {
+            const int t = i / ((G + 15) / 16), h = (i % ((G + 15) / 16)) * 16;
+            l2_prefetch(p.a.q + (int64_t)(tok0 + t) * p.a.q_stride + (walk.ch * G + h) * kHeadDim,
+                        min(16, G - h) * kHeadDim * 2);
+          }
         if (walk.a == 0 && walk.b < walk.it.tiles) {   // the CTA that the item's last tile lies in
           const int64_t last = walk.pos - (walk.b - walk.a) + walk.it.tiles - 1;
           part.n = walk.n;
@@ -829,6 +830,8 @@ __global__ void __launch_bounds__(kThreadsP, 1)
     }
     if (!ok && lane == 0) record_error(p.a.status, KDA_ERR_DEVICE_TIMEOUT, 336);
   }
+  // (launched beside the decode kernel: this grid does not end before that one)
+  if (blockIdx.x == 0 && warp == 0) pdl_wait();
   tc_fence_before();
   __syncthreads();
   if (warp == kSoftWarps + 5) {
@@ -842,7 +845,8 @@ __global__ void __launch_bounds__(kThreadsP, 1)
 constexpr int kMergeRows = 8;
 __global__ void __launch_bounds__(32 * kMergeRows)
     kda_attn_prefill_merge_kernel(const __grid_constant__ PrefillParams p) {
-  pdl_wait();
+  // (not waiting: one CTA still does, so that this grid does not end before the one beside it)
+  if (p.wait || (blockIdx.x == 0 && blockIdx.y == 0)) pdl_wait();
   const PartDescP d = p.desc[blockIdx.x];
   if (d.parts == 0) return;
   const int lane = threadIdx.x & 31, G = p.a.heads / p.a.c.kv_heads;
@@ -881,7 +885,7 @@ __global__ void __launch_bounds__(32 * kMergeRows)
 }
 
 template <bool kCap>
-cudaError_t launch_cap(const PrefillParams& d, int sms, cudaStream_t stream) {
+cudaError_t launch_cap(const PrefillParams& d, int sms, bool beside, cudaStream_t stream) {
   static PerDeviceOnce once;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -896,19 +900,7 @@ cudaError_t launch_cap(const PrefillParams& d, int sms, cudaStream_t stream) {
                                 cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemP);
   });
   if (e != cudaSuccess) return e;
-  kda_attn_prefill_kernel<kCap><<<sms, kThreadsP, kSmemP, stream>>>(d);
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)sms, kRowsP / kMergeRows);
-  cfg.blockDim = dim3(32 * kMergeRows);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kda_attn_prefill_merge_kernel, d);
+  return launch(kda_attn_prefill_kernel<kCap>, dim3((unsigned)sms), dim3(kThreadsP), kSmemP, beside, stream, d);
 }
 
 }  // namespace
@@ -917,18 +909,36 @@ size_t prefill_workspace_bytes(int sms) {
   return (size_t)sms * sizeof(PartDescP) + (size_t)sms * 2 * kSlotFloatsP * sizeof(float);
 }
 
-cudaError_t launch_attn_prefill(const AttnParams& a, int min_rows, void* work, int sms,
+namespace {
+bool make_params(const AttnParams& a, int min_rows, void* work, int sms, PrefillParams* d) {
+  d->a = a;
+  if (!make_cache_maps(a.c, &d->maps)) return false;
+  d->wait = 0;
+  d->min_rows = min_rows;
+  d->group = a.heads / a.c.kv_heads;
+  d->group_magic = 65535u / (uint32_t)d->group + 1;
+  d->tokens = kRowsP / d->group;
+  d->desc = static_cast<PartDescP*>(work);
+  d->slots = reinterpret_cast<float*>(d->desc + sms);
+  return true;
+}
+}  // namespace
+
+cudaError_t launch_attn_prefill(const AttnParams& a, int min_rows, void* work, int sms, bool beside,
                                 cudaStream_t stream) {
   PrefillParams d;
-  d.a = a;
-  if (!make_cache_maps(a.c, &d.maps)) return cudaErrorNotSupported;
-  d.min_rows = min_rows;
-  d.group = a.heads / a.c.kv_heads;
-  d.group_magic = 65535u / (uint32_t)d.group + 1;
-  d.tokens = kRowsP / d.group;
-  d.desc = static_cast<PartDescP*>(work);
-  d.slots = reinterpret_cast<float*>(d.desc + sms);
-  return a.softcap > 0.0f ? launch_cap<true>(d, sms, stream) : launch_cap<false>(d, sms, stream);
+  if (!make_params(a, min_rows, work, sms, &d)) return cudaErrorNotSupported;
+  return a.softcap > 0.0f ? launch_cap<true>(d, sms, beside, stream)
+                          : launch_cap<false>(d, sms, beside, stream);
+}
+
+cudaError_t launch_attn_prefill_merge(const AttnParams& a, int min_rows, void* work, int sms, bool wait,
+                                      cudaStream_t stream) {
+  PrefillParams d;
+  if (!make_params(a, min_rows, work, sms, &d)) return cudaErrorNotSupported;
+  d.wait = wait;
+  return launch(kda_attn_prefill_merge_kernel, dim3((unsigned)sms, kRowsP / kMergeRows),
+                dim3(32 * kMergeRows), 0, true, stream, d);
 }
 
 }  // namespace attn
