@@ -277,7 +277,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         scales(nxt);
         after = look();
       }
-      if (it >= kStages) ok = mbar_wait(bar_empty + 8 * st, (it / kStages - 1) & 1);
+      if (it >= kStages) ok = mbar_wait_sleep(bar_empty + 8 * st, (it / kStages - 1) & 1);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) {
         if (lane == 0) record_error(p.a.status, KDA_ERR_DEVICE_TIMEOUT, 313);
@@ -302,7 +302,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     // the copies in flight end before the CTA does
     for (uint32_t i = it > kStages ? it - kStages : 0; i < it; ++i)
-      mbar_wait(bar_full + 8 * (i % kStages), (i / kStages) & 1);
+      mbar_wait_sleep(bar_full + 8 * (i % kStages), (i / kStages) & 1);
   } else if (warp == 5) {
     // ================= MMA issuer
     if (elect_one()) {
@@ -310,7 +310,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       uint32_t it = 0, seg = 0;
       bool ok = true;
       auto pv = [&](uint32_t i) {       // O^T of tile i, once its P is written
-        ok = mbar_wait(bar_p, i & 1);
+        ok = mbar_wait_sleep(bar_p, i & 1);
         if (!ok) return;
         tc_fence_after();
         const uint32_t v = sb + (i % kStages) * kStageBytes + kTile * 128;
@@ -321,10 +321,10 @@ __global__ void __launch_bounds__(kThreads, 2)
         mma_commit(bar_empty + 8 * (i % kStages));
       };
       while (ok && walk.next(p)) {
-        ok = mbar_wait(bar_q, seg & 1);
+        ok = mbar_wait_sleep(bar_q, seg & 1);
         ++seg;
         for (int t = walk.a; t < walk.b && ok; ++t, ++it) {
-          ok = mbar_wait(bar_full + 8 * (it % kStages), (it / kStages) & 1);
+          ok = mbar_wait_sleep(bar_full + 8 * (it % kStages), (it / kStages) & 1);
           if (!ok) break;
           tc_fence_after();
           const uint32_t k = sb + (it % kStages) * kStageBytes;
@@ -339,9 +339,9 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (!ok) record_error(p.a.status, KDA_ERR_DEVICE_TIMEOUT, 314);
       // what was issued ends, its arrivals included, before shared and tensor memory go
       mma_commit(bar_end);
-      mbar_wait(bar_end, 0);
+      mbar_wait_sleep(bar_end, 0);
       for (uint32_t i = it > kStages ? it - kStages : 0; ok && i < it; ++i)
-        mbar_wait(bar_empty + 8 * (i % kStages), (i / kStages) & 1);
+        mbar_wait_sleep(bar_empty + 8 * (i % kStages), (i / kStages) & 1);
     }
     __syncwarp();
   } else {
@@ -415,7 +415,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       bool poisoned = false;         // the tile before has NaN entries that some rows do not see
       // O^T of tile i added to the sums (its factors and poison words: parity i & 1)
       auto add_o = [&](uint32_t i, int t) {
-        ok = mbar_wait(bar_o, i & 1) && ok;
+        ok = mbar_wait_sleep(bar_o, i & 1) && ok;
         tc_fence_after();
         const float4* f = fac + ((i & 1) * 4 + warp) * NR;
         if (NR <= 16) {
@@ -458,8 +458,8 @@ __global__ void __launch_bounds__(kThreads, 2)
       for (int t = walk.a; t < walk.b; ++t, ++it) {
         const uint32_t par = it & 1, st = it % kStages;
         // (the scales and V are read here too; S comes last)
-        ok = mbar_wait(bar_full + 8 * st, (it / kStages) & 1) && ok;
-        ok = mbar_wait(bar_s + 8 * par, (it >> 1) & 1) && ok;
+        ok = mbar_wait_sleep(bar_full + 8 * st, (it / kStages) & 1) && ok;
+        ok = mbar_wait_sleep(bar_s + 8 * par, (it >> 1) & 1) && ok;
         tc_fence_after();
         const int key0 = (walk.s.tile0 + t) * kTile, key = key0 + tid;
         // some key of the tile is hidden from some row

@@ -47,7 +47,7 @@ constexpr int kOffK = kOffVB + 2 * 32768;                   // [kKStages] K tile
 constexpr int kOffV8 = kOffK + kKStages * 16384;            // [kVStages] V tiles
 constexpr int kOffSc = kOffV8 + kVStages * 16384;           // float4 [4][8]: k scale, log2 v scale, 1 / v scale
 constexpr int kOffQmul = kOffSc + 4 * 8 * 16;               // float [256]
-constexpr int kOffMx = kOffQmul + 4 * kRowsP;               // float [2][256][2]: maxima of a row's two threads
+constexpr int kOffMx = kOffQmul + 4 * kRowsP;               // float [2][2][256]: maxima of a row's two threads
 constexpr int kOffL = kOffMx + 16 * kRowsP;                 // float [256][2]: denominators
 constexpr int kOffSeg = kOffL + 8 * kRowsP;                 // Segment [kSegs]
 constexpr int kOffBars = kOffSeg + 64 * 4;
@@ -319,7 +319,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
   static_assert(sizeof(Segment) <= 64 && kSegs <= 4, "segment ring");
   // The next segment (false when there is none, or the wait gave up), and done with one.
   auto seg_wait = [&](uint32_t seg, bool& ok) -> const Segment* {
-    ok = ok && mbar_wait(bar_gf + 8 * (seg % kSegs), (seg / kSegs) & 1);
+    ok = ok && mbar_wait_sleep(bar_gf + 8 * (seg % kSegs), (seg / kSegs) & 1);
     __syncwarp();
     return ring + seg % kSegs;
   };
@@ -358,7 +358,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
           const float ks = scale_of(p.a.c.k_scale, pg), vs = scale_of(p.a.c.v_scale, pg);
           const int pg_next = page_of(g, key + kTile);
           const uint32_t sk = it % kKStages, sv = it % kVStages;
-          if (it >= kKStages) ok = mbar_wait(bar_ke + 8 * sk, (it / kKStages - 1) & 1);
+          if (it >= kKStages) ok = mbar_wait_sleep(bar_ke + 8 * sk, (it / kKStages - 1) & 1);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           // (slot it % 4 was last read for tile it - 4, whose P precedes the products of tile
@@ -376,7 +376,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
           }
           __syncwarp();
           if (loads) tma_load_4d(sb + kOffK + sk * 16384 + row * 128, &p.maps.k, 0, 0, g.ch, pg, bar_kf + 8 * sk);
-          if (it >= kVStages) ok = mbar_wait(bar_ve + 8 * sv, (it / kVStages - 1) & 1);
+          if (it >= kVStages) ok = mbar_wait_sleep(bar_ve + 8 * sv, (it / kVStages - 1) & 1);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           if (lane == 0) mbar_expect_tx(bar_vf + 8 * sv, bytes);
@@ -389,9 +389,9 @@ __global__ void __launch_bounds__(kThreadsP, 1)
       if (!ok && lane == 0) record_error(p.a.status, KDA_ERR_DEVICE_TIMEOUT, 333);
       // the copies in flight end before the CTA does (a failed wait left at most one K behind)
       for (uint32_t i = it > kKStages ? it - kKStages : 0; i < it + (ok ? 0 : 1); ++i)
-        mbar_wait(bar_kf + 8 * (i % kKStages), (i / kKStages) & 1);
+        mbar_wait_sleep(bar_kf + 8 * (i % kKStages), (i / kKStages) & 1);
       for (uint32_t i = it > kVStages ? it - kVStages : 0; i < it; ++i)
-        mbar_wait(bar_vf + 8 * (i % kVStages), (i / kVStages) & 1);
+        mbar_wait_sleep(bar_vf + 8 * (i % kVStages), (i / kVStages) & 1);
     } else if (warp == kSoftWarps + 5) {
       // ================= MMA issuer (the warp stays together; one lane issues)
       constexpr uint32_t id_s = idesc_e4m3(128, 128, 0, 0), id_o = idesc_f16(128, 128, 0, 1);
@@ -411,8 +411,8 @@ __global__ void __launch_bounds__(kThreadsP, 1)
       };
       auto pv = [&](uint32_t i, int h, bool first_tile) {   // O of half h += P(i) V(i)
         // (the segment before has read its O)
-        if (first_tile && seg > 0) ok = ok && mbar_wait(bar_of + 8 * h, (seg - 1) & 1);
-        ok = ok && mbar_wait(bar_p + 8 * h, i & 1);      // P(i), V(i) and the keys of the tile after
+        if (first_tile && seg > 0) ok = ok && mbar_wait_sleep(bar_of + 8 * h, (seg - 1) & 1);
+        ok = ok && mbar_wait_sleep(bar_p + 8 * h, i & 1);      // P(i), V(i) and the keys of the tile after
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) return;
         tc_fence_after();
@@ -428,9 +428,9 @@ __global__ void __launch_bounds__(kThreadsP, 1)
         if (!ok || !sg->more) break;
         const int tiles = (sg->key1 - sg->key0) / kTile;
         seg_done(seg);
-        ok = mbar_wait(bar_kf + 8 * sk, (it / kKStages) & 1);
+        ok = mbar_wait_sleep(bar_kf + 8 * sk, (it / kKStages) & 1);
         for (int h = 0; h < 2; ++h) {
-          ok = ok && mbar_wait(bar_q + 8 * h, seg & 1);
+          ok = ok && mbar_wait_sleep(bar_q + 8 * h, seg & 1);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           tc_fence_after();
@@ -457,11 +457,11 @@ __global__ void __launch_bounds__(kThreadsP, 1)
       if (!ok && lead) record_error(p.a.status, KDA_ERR_DEVICE_TIMEOUT, 334);
       // what was issued ends, its arrivals included, before shared and tensor memory go
       mma_commit_on(lead, bar_end);
-      mbar_wait(bar_end, 0);
+      mbar_wait_sleep(bar_end, 0);
       for (uint32_t i = it > kKStages ? it - kKStages : 0; ok && i < it; ++i)
-        mbar_wait(bar_ke + 8 * (i % kKStages), (i / kKStages) & 1);
+        mbar_wait_sleep(bar_ke + 8 * (i % kKStages), (i / kKStages) & 1);
       for (uint32_t i = it > 2 ? it - 2 : 0; ok && i < it; ++i)
-        mbar_wait(bar_be + 8 * (i & 1), (i >> 1) & 1);
+        mbar_wait_sleep(bar_be + 8 * (i & 1), (i >> 1) & 1);
       __syncwarp();
     } else if (warp == kSoftWarps + 6) {
       // ================= scheduler: this CTA's segments, one after the other
@@ -470,7 +470,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
       for (uint32_t seg = 0;; ++seg) {
         const bool more = walk.next(p);
         const int tok0 = walk.s.tok0 + walk.it.tok;
-        if (seg >= kSegs) ok = mbar_wait(bar_ge + 8 * (seg % kSegs), (seg / kSegs - 1) & 1);
+        if (seg >= kSegs) ok = mbar_wait_sleep(bar_ge + 8 * (seg % kSegs), (seg / kSegs - 1) & 1);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         if (lane == 0) {
@@ -527,8 +527,8 @@ __global__ void __launch_bounds__(kThreadsP, 1)
       if (vt == 0) misc->poison[(seg + 4) & 7] = 0;      // last read four segments ago
       for (; key0 < key1; key0 += kTile, ++it) {
         const uint32_t sv = it % kVStages, vb = it & 1;
-        ok = mbar_wait(bar_vf + 8 * sv, (it / kVStages) & 1);
-        if (it >= 2) ok = ok && mbar_wait(bar_be + 8 * vb, ((it >> 1) - 1) & 1);
+        ok = mbar_wait_sleep(bar_vf + 8 * sv, (it / kVStages) & 1);
+        if (it >= 2) ok = ok && mbar_wait_sleep(bar_be + 8 * vb, ((it >> 1) - 1) & 1);
         if (!ok) break;
         const unsigned char* src = sm + kOffV8 + sv * 16384;
         unsigned char* dst = sm + kOffVB + vb * 32768 + (c >> 2) * 16384;
@@ -555,17 +555,21 @@ __global__ void __launch_bounds__(kThreadsP, 1)
             o[2 * e + 1] = f16x2_of_e4m3x2(w[e] >> 16);
           }
           unsigned char* d = dst + (row >> 3) * 1024 + (row & 7) * 128;
-          const int k0 = (2 * c) & 7;
-          *reinterpret_cast<uint4*>(d + ((k0 ^ (row & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
-          *reinterpret_cast<uint4*>(d + (((k0 + 1) ^ (row & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
+          // the eight lanes of a row write even chunks of one block and odd ones of the other at a
+          // time, which is every bank once
+          const int k0 = (2 * c) & 7, odd = c >> 2;
+          *reinterpret_cast<uint4*>(d + (((k0 + odd) ^ (row & 7)) << 4)) =
+              odd ? make_uint4(o[4], o[5], o[6], o[7]) : make_uint4(o[0], o[1], o[2], o[3]);
+          *reinterpret_cast<uint4*>(d + (((k0 + 1 - odd) ^ (row & 7)) << 4)) =
+              odd ? make_uint4(o[0], o[1], o[2], o[3]) : make_uint4(o[4], o[5], o[6], o[7]);
         }
         fence_proxy_async();
         mbar_arrive(bar_ve + 8 * sv);
         // This warp's arrival on the barriers of P(it) tells the MMA issuer that V(it) is there, and
         // the next keys: it then has one thing to wait for (a wait behind matrix instructions takes
         // until they have left its queue).  Not before P(it - 1), whose phase it would count in.
-        if (it > 0) ok = mbar_wait(bar_p, (it - 1) & 1) && mbar_wait(bar_p + 8, (it - 1) & 1);
-        if (key0 + kTile < key1) ok = ok && mbar_wait(bar_kf + 8 * ((it + 1) % kKStages), ((it + 1) / kKStages) & 1);
+        if (it > 0) ok = mbar_wait_sleep(bar_p, (it - 1) & 1) && mbar_wait_sleep(bar_p + 8, (it - 1) & 1);
+        if (key0 + kTile < key1) ok = ok && mbar_wait_sleep(bar_kf + 8 * ((it + 1) % kKStages), ((it + 1) / kKStages) & 1);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         if (lane == 0) {
@@ -589,7 +593,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
     const float cap2 = kCap ? 2.0f * kLog2e / p.a.softcap : 0.0f, cap1 = kCap ? p.a.softcap * kLog2e : 0.0f;
     const float sign = p.a.scale < 0.0f ? -1.0f : 1.0f;  // (the row maximum is taken before the scale)
     float* qmul_s = reinterpret_cast<float*>(sm + kOffQmul);
-    float* mx_s = reinterpret_cast<float*>(sm + kOffMx) + 2 * row;
+    float* mx_s = reinterpret_cast<float*>(sm + kOffMx) + row;
     float* l_s = reinterpret_cast<float*>(sm + kOffL) + 2 * row;
     uint32_t it = 0, seg = 0;
     bool ok = true;
@@ -655,9 +659,9 @@ __global__ void __launch_bounds__(kThreadsP, 1)
       float m = -INFINITY, l = 0.0f;
       for (int t = 0; t < tiles; ++t, ++it, hi -= kTile, p_lo -= kTile, p_hi -= kTile) {
         // (a wait costs over 100 cycles even when it need not wait: S, the last to come, last)
-        ok = ok && mbar_wait(bar_sc + 8 * (it & 3), (it >> 2) & 1);
-        if (t > 0) ok = ok && mbar_wait(bar_o + 8 * half, (it - 1) & 1);
-        ok = ok && mbar_wait(bar_s + 8 * half, it & 1);
+        ok = ok && mbar_wait_sleep(bar_sc + 8 * (it & 3), (it >> 2) & 1);
+        if (t > 0) ok = ok && mbar_wait_sleep(bar_o + 8 * half, (it - 1) & 1);
+        ok = ok && mbar_wait_sleep(bar_s + 8 * half, it & 1);
         __syncwarp();
         tc_fence_after();
         uint32_t s[64];
@@ -702,9 +706,9 @@ __global__ void __launch_bounds__(kThreadsP, 1)
           }
         }
         // the row's other 64 keys
-        mx_s[(it & 1) * 2 * kRowsP + cg] = mt;
+        mx_s[((it & 1) * 2 + cg) * kRowsP] = mt;
         group_sync(id_pair, 64);      // (also: both have S in registers, P may go over it)
-        mt = fmaxf(mt, mx_s[(it & 1) * 2 * kRowsP + (cg ^ 1)]);
+        mt = fmaxf(mt, mx_s[((it & 1) * 2 + (cg ^ 1)) * kRowsP]);
         if (__any_sync(0xffffffffu, mt > m + kSlack)) {
           const float next = fmaxf(m, mt), f = ex2(m - (next == -INFINITY ? 0.0f : next));
           if (t > 0) {       // O, the tile before included, by the factor
@@ -746,7 +750,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(bar_p + 8 * half);
       }
-      ok = ok && mbar_wait(bar_o + 8 * half, (it - 1) & 1);
+      ok = ok && mbar_wait_sleep(bar_o + 8 * half, (it - 1) & 1);
       m -= kPShift;       // (the numerators' reference)
       l_s[cg] = l;
       group_sync(id_pair, 64);
