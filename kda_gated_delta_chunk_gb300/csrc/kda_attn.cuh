@@ -76,7 +76,7 @@ struct NormParams {
   int32_t residual_f32, weight_f32;
   float eps;
 };
-cudaError_t launch_norm(const NormParams& p, bool aligned, int sms, cudaStream_t stream);
+cudaError_t launch_norm(const NormParams& p, bool aligned, cudaStream_t stream);
 
 // ------------------------------------------------------------ paged cache
 // Mirrors kda_kv_cache of kda.h.

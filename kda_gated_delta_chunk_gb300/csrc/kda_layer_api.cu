@@ -139,7 +139,7 @@ int kda_add_rms_norm(const void* x, int64_t ldx, const void* residual, int64_t l
   p.residual_f32 = rf;
   p.weight_f32 = wf;
   p.eps = eps;
-  return launched(kda::attn::launch_norm(p, wide, sms, reinterpret_cast<cudaStream_t>(stream)));
+  return launched(kda::attn::launch_norm(p, wide, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 int kda_rope_append(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
