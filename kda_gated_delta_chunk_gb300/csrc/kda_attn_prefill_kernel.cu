@@ -16,8 +16,8 @@
 // while one half's softmax runs, the other half's products do.  The matrix instructions of a CTA
 // run in the order they are issued, so S(i+1) of a half may follow its O += P(i) V, whose P it
 // overwrites, without a wait.  Key tiles of all (sequence, kv head, row tile) items are laid end
-// to end and cut into one equal range per CTA, one CTA per SM (as in the decode kernel), and a
-// dependent kernel merges the items that were cut.
+// to end and cut into one equal range per CTA, one CTA per SM (as in the decode kernel; an item
+// counts kOverP tiles more), and a dependent kernel merges the items that were cut.
 //
 // Warps: 0-7 / 8-15 softmax of the halves, 16-19 the widening of V, 20 the TMA producer, 21 the MMA
 // issuer, 22 the scheduler, which walks the CTA's range and hands its segments to the others
@@ -37,6 +37,7 @@ constexpr int kRowsP = 256;
 constexpr int kKStages = 3, kVStages = 2, kSegs = 4;
 constexpr int kSoftWarps = 16, kRegsSoftmax = 104, kRegsOther = 32;
 constexpr int kRegsNeeded = 32 * (kSoftWarps * kRegsSoftmax + (kThreadsP / 32 - kSoftWarps) * kRegsOther);
+constexpr int kOverP = 3;                   // tiles' worth of time an item takes besides its tiles
 constexpr float kSlack = 8.0f;              // log2 growth of the maximum before O is rescaled
 constexpr float kPShift = 7.0f;             // log2 of the numerator at the maximum: at most 2^15 with the slack
 
@@ -92,36 +93,40 @@ __device__ __forceinline__ ItemP item_of(int q_len, int len, int rt, int tokens,
   return it;
 }
 
-// The walk over a CTA's range of key tiles; every role runs its own.
+// The walk over a CTA's range, in units: an item has kOverP of them, then one per key tile.
 struct WalkP {
   int64_t pos, end;
-  int n, h, rt, off;         // the next item and the tiles of it that lie before this range
+  int n, h, rt, off;         // the next item and the units of it that lie before this range
   SeqInfo s;
   ItemP it;
   int a, b;                  // segment: tiles [a, b) of the item
   int ch, crt;               // its head and row tile
+  int64_t last;              // unit of the item's last tile
   __device__ __forceinline__ bool next(const PrefillParams& p) {
-    if (pos >= end) return false;
-    while (s.tiles == 0 || rt * p.tokens >= s.q_len) {   // to the next head or sequence
-      if (s.tiles != 0 && h + 1 < p.a.c.kv_heads) {
-        ++h;
-        rt = 0;
-        continue;
+    while (pos < end) {
+      while (s.tiles == 0 || rt * p.tokens >= s.q_len) {   // to the next head or sequence
+        if (s.tiles != 0 && h + 1 < p.a.c.kv_heads) {
+          ++h;
+          rt = 0;
+          continue;
+        }
+        int err;
+        if (++n >= p.a.num_seqs) return false;             // (lengths that changed under the kernel)
+        s = seq_info(p.a, n, p.min_rows, 0x7fffffff, &err);
+        h = rt = 0;
       }
-      int err;
-      if (++n >= p.a.num_seqs) return false;             // (lengths that changed under the kernel)
-      s = seq_info(p.a, n, p.min_rows, 0x7fffffff, &err);
-      h = rt = 0;
+      it = item_of(s.q_len, s.len, rt, p.tokens, p.a.window);
+      ch = h;
+      crt = rt++;
+      const int size = it.tiles + kOverP, o = off, o1 = (int)min((int64_t)size, o + (end - pos));
+      last = pos - o + size - 1;
+      pos += o1 - o;
+      off = 0;
+      a = max(0, o - kOverP);
+      b = o1 - kOverP;
+      if (b > a) return true;                              // (else the range ends before its first tile)
     }
-    it = item_of(s.q_len, s.len, rt, p.tokens, p.a.window);
-    ch = h;
-    crt = rt;
-    a = off;
-    b = (int)min((int64_t)it.tiles, a + (end - pos));
-    pos += b - a;
-    off = 0;
-    ++rt;
-    return true;
+    return false;
   }
 };
 
@@ -217,14 +222,14 @@ __global__ void __launch_bounds__(kThreadsP, 1)
     long long mine = 0;
     const int rts = (q_len + p.tokens - 1) / p.tokens;
     if (rts <= 32)
-      for (int rt = 0; rt < rts; ++rt) mine += item_of(q_len, len, rt, p.tokens, p.a.window).tiles;
+      for (int rt = 0; rt < rts; ++rt) mine += item_of(q_len, len, rt, p.tokens, p.a.window).tiles + kOverP;
     uint32_t todo = __ballot_sync(0xffffffffu, rts > 32);
     while (todo) {
       const int k = __ffs(todo) - 1;
       todo &= todo - 1;
       const int ql = __shfl_sync(0xffffffffu, q_len, k), ln = __shfl_sync(0xffffffffu, len, k);
       int sum = 0;
-      for (int rt = lane; rt * p.tokens < ql; rt += 32) sum += item_of(ql, ln, rt, p.tokens, p.a.window).tiles;
+      for (int rt = lane; rt * p.tokens < ql; rt += 32) sum += item_of(ql, ln, rt, p.tokens, p.a.window).tiles + kOverP;
       const int all = __reduce_add_sync(0xffffffffu, sum);
       if (lane == k) mine = all;
     }
@@ -246,7 +251,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
   for (int w = 0; w < kThreadsP / 32; ++w) total += misc->part[w];
   __syncthreads();
   WalkP walk;
-  // (no more ranges than tiles: between two CTAs of an item there is none without a part)
+  // (no more ranges than units: between two CTAs of an item there is none without a part)
   const int ranges = (int)min((long long)gridDim.x, total);
   walk.pos = walk.end = 0;
   if ((int)blockIdx.x < ranges) {
@@ -265,15 +270,29 @@ __global__ void __launch_bounds__(kThreadsP, 1)
       }
       if (lane == 31) misc->part[warp] = inc;
       __syncthreads();
-      long long off = before;
-      for (int x = 0; x < warp; ++x) off += misc->part[x];
-      if (w > 0 && walk.pos >= off + inc - w && walk.pos < off + inc) {
-        const long long x = walk.pos - (off + inc - w), per_head = w / hk;
-        misc->start_n = n0 + tid;
-        misc->start_h = (int)(x / per_head);
-        misc->rest = x % per_head;
+      // the warps' sums scanned by every warp, a lane each
+      const long long mine_w = lane < kThreadsP / 32 ? misc->part[lane] : 0;
+      long long scan = mine_w;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long u = __shfl_up_sync(0xffffffffu, scan, o);
+        if (lane >= o) scan += u;
       }
-      for (int x = 0; x < kThreadsP / 32; ++x) before += misc->part[x];
+      const long long off = before + __shfl_sync(0xffffffffu, scan - mine_w, warp);
+      if (w > 0 && walk.pos >= off + inc - w && walk.pos < off + inc) {
+        const long long x = walk.pos - (off + inc - w);
+        misc->start_n = n0 + tid;
+        if (w >> 32 == 0) {            // (64-bit division takes hundreds of cycles)
+          const uint32_t per_head = (uint32_t)w / (uint32_t)hk;
+          misc->start_h = (int)((uint32_t)x / per_head);
+          misc->rest = (uint32_t)x % per_head;
+        } else {
+          const long long per_head = w / hk;
+          misc->start_h = (int)(x / per_head);
+          misc->rest = x % per_head;
+        }
+      }
+      before += __shfl_sync(0xffffffffu, scan, 31);
       __syncthreads();
       if (before > walk.pos) break;
     }
@@ -286,7 +305,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
       for (int r0 = 0;; r0 += 32) {
         const int rt = r0 + lane;
         const int c = rt * p.tokens < walk.s.q_len
-                          ? item_of(walk.s.q_len, walk.s.len, rt, p.tokens, p.a.window).tiles : 0;
+                          ? item_of(walk.s.q_len, walk.s.len, rt, p.tokens, p.a.window).tiles + kOverP : 0;
         int inc = c;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -499,11 +518,10 @@ __global__ void __launch_bounds__(kThreadsP, 1)
                         min(16, G - h) * kHeadDim * 2);
           }
         if (walk.a == 0 && walk.b < walk.it.tiles) {   // the CTA that the item's last tile lies in
-          const int64_t last = walk.pos - (walk.b - walk.a) + walk.it.tiles - 1;
           part.n = walk.n;
           part.h = walk.ch;
           part.rt = walk.crt;
-          part.parts = (int)(((last + 1) * ranges - 1) / total - blockIdx.x) + 1;
+          part.parts = (int)(((walk.last + 1) * ranges - 1) / total - blockIdx.x) + 1;
         }
       }
       if (lane == 0) {
@@ -619,7 +637,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
             u[j] = *reinterpret_cast<const uint4*>(src + (int64_t)i * p.a.q_stride + (r - i * G) * kHeadDim);
         }
         unsigned char* q1 = sm + kOffQ + half * 32768;
-#pragma unroll 2
+#pragma unroll
         for (int j = 0; j < 8; ++j) {
           const int r = r0 + 2 * j;
           float x[8], top = 0.0f;
