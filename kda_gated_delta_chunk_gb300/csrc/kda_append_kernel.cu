@@ -128,6 +128,8 @@ __global__ void __launch_bounds__(kThreads, 65536 / kRegs / kThreads)
   const Lane ln = lane_of<kInter>(lane16, p.rot_dim);
   const int32_t* cu = p.cu_seqlens;
   const int N = p.num_seqs;
+  sm100::pdl_wait();   // (launched as a programmatic dependent of the work before it)
+  sm100::pdl_launch_dependents();
   if ((int)blockIdx.x < page_ctas) {
     // ---- this CTA's range of units, and the sequence that it begins in
     const int hk = p.c.kv_heads, P = p.c.page_size;
@@ -324,11 +326,9 @@ cudaError_t launch_heads(const AppendParams& p, int sms, cudaStream_t stream) {
   const int64_t units = p.q ? p.total_tokens * ((p.heads + kHeads - 1) / kHeads) : 0;
   const int64_t grid = page_ctas + (units + kThreads / 16 - 1) / (kThreads / 16);
   if (grid > 0x7fffffff) return cudaErrorInvalidValue;
-  if (p.interleaved)
-    kda_append_kernel<kRows, kHeads, kThreads, true><<<(unsigned)grid, kThreads, 0, stream>>>(p, page_ctas);
-  else
-    kda_append_kernel<kRows, kHeads, kThreads, false><<<(unsigned)grid, kThreads, 0, stream>>>(p, page_ctas);
-  return cudaGetLastError();
+  const dim3 g((unsigned)grid), t(kThreads);
+  return p.interleaved ? launch(kda_append_kernel<kRows, kHeads, kThreads, true>, g, t, 0, true, stream, p, page_ctas)
+                       : launch(kda_append_kernel<kRows, kHeads, kThreads, false>, g, t, 0, true, stream, p, page_ctas);
 }
 
 // Query heads of a token that share one read of its table row: 4 where there are tokens enough

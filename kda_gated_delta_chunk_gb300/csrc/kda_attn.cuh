@@ -8,11 +8,31 @@
 
 #include "kda.h"
 #include "kda_internal.cuh"
+#include "kda_sm100.cuh"
 
 namespace kda {
 namespace attn {
 
 constexpr float kE4M3Max = 448.0f;
+
+// ------------------------------------------------------------ launches
+// A launch, on request as the programmatic dependent of the one before it on the stream (it may
+// then start before that one has ended, and waits in the kernel if it must).
+template <class... Args>
+cudaError_t launch(void (*kernel)(Args...), dim3 grid, dim3 block, size_t smem, bool dependent,
+                   cudaStream_t stream, const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = dependent ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
 
 // ------------------------------------------------------------ e4m3
 // Two floats -> two e4m3 bytes (round to nearest even, finite overflow and infinities to

@@ -155,15 +155,17 @@ __global__ void __launch_bounds__(kThreads, 2)
     mbar_fence_init();
     tma_prefetch_desc(&p.maps.k);
     tma_prefetch_desc(&p.maps.v);
-    if (blockIdx.x == 0 && p.a.cu_seqlens[0] != 0) record_error(p.a.status, KDA_ERR_BAD_CU_SEQLENS, 310);
   }
   if (warp == 5) {
     tmem_alloc(smem_u32(&misc->tmem), C::kTmemCols);
     tmem_relinquish();
   }
+  // (launched as a programmatic dependent: the work before this call is done from here on)
+  pdl_wait();
   pdl_launch_dependents();
 
   // ---- this CTA's range: total tiles, then the sequence its first tile lies in
+  if (tid == 0 && blockIdx.x == 0 && p.a.cu_seqlens[0] != 0) record_error(p.a.status, KDA_ERR_BAD_CU_SEQLENS, 310);
   auto cost = [&](int n, bool report) -> long long {
     if (n >= N) return 0;
     int err;
@@ -671,7 +673,7 @@ __global__ void __launch_bounds__(64 * kMergeWarps)
   __shared__ float4 acc_s[2][kMergeWarps][32];
   __shared__ float den_s[2][kMergeWarps];
   if (p.wait) pdl_wait();
-  else pdl_launch_dependents();
+  pdl_launch_dependents();
   const PartDesc d = p.desc[blockIdx.x];
   if (d.parts == 0) return;
   const int lane = threadIdx.x & 31, w0 = (threadIdx.x >> 5) % kMergeWarps, rr = threadIdx.x / (32 * kMergeWarps);
@@ -739,7 +741,7 @@ cudaError_t launch_nr(const DecodeParams& d, int sms, cudaStream_t stream) {
   });
   if (e != cudaSuccess) return e;
   return launch(kda_attn_decode_kernel<NR, kCap>, dim3((unsigned)decode_ctas(sms)), dim3(kThreads),
-                Cfg<NR>::kBytes, false, stream, d);
+                Cfg<NR>::kBytes, true, stream, d);
 }
 template <int NR>
 cudaError_t launch_merge(const DecodeParams& d, int sms, cudaStream_t stream) {

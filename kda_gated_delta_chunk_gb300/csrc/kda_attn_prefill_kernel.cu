@@ -71,7 +71,7 @@ struct PrefillParams {
   CacheMaps maps;
   int group;                 // query heads of a kv head
   uint32_t group_magic;      // 65535 / group + 1 (div_small)
-  int wait;                  // the merge waits for the kernel before it (programmatic launch)
+  int wait;                  // wait for the kernel before this one (programmatic launch)
   int min_rows, tokens;      // tokens: new tokens per row tile (256 / group)
   PartDescP* desc;
   float* slots;
@@ -197,13 +197,16 @@ __global__ void __launch_bounds__(kThreadsP, 1)
     for (int i = 0; i < 8; ++i) misc->poison[i] = 0;
     tma_prefetch_desc(&p.maps.k);
     tma_prefetch_desc(&p.maps.v);
-    if (blockIdx.x == 0 && p.a.cu_seqlens[0] != 0) record_error(p.a.status, KDA_ERR_BAD_CU_SEQLENS, 330);
   }
   if (warp == kSoftWarps + 5) {
     tmem_alloc(smem_u32(&misc->tmem), 512);
     tmem_relinquish();
   }
+  // (launched as a programmatic dependent: of the work before this call, or of the decode kernel,
+  // which has waited for that and shares nothing with this one)
+  if (p.wait) pdl_wait();
   pdl_launch_dependents();
+  if (tid == 0 && blockIdx.x == 0 && p.a.cu_seqlens[0] != 0) record_error(p.a.status, KDA_ERR_BAD_CU_SEQLENS, 330);
 
   // ---- this CTA's range.  A thread reads its sequence's lengths; the warp adds up the row
   // tiles of each of its sequences together.
@@ -852,7 +855,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
     }
     if (!ok && lane == 0) record_error(p.a.status, KDA_ERR_DEVICE_TIMEOUT, 336);
   }
-  // (launched beside the decode kernel: this grid does not end before that one)
+  // (beside the decode kernel: this grid does not end before that one)
   if (blockIdx.x == 0 && warp == 0) pdl_wait();
   tc_fence_before();
   __syncthreads();
@@ -869,6 +872,7 @@ __global__ void __launch_bounds__(32 * kMergeRows)
     kda_attn_prefill_merge_kernel(const __grid_constant__ PrefillParams p) {
   // (not waiting: one CTA still does, so that this grid does not end before the one beside it)
   if (p.wait || (blockIdx.x == 0 && blockIdx.y == 0)) pdl_wait();
+  if (p.wait) pdl_launch_dependents();
   const PartDescP d = p.desc[blockIdx.x];
   if (d.parts == 0) return;
   const int lane = threadIdx.x & 31, G = p.a.heads / p.a.c.kv_heads;
@@ -907,7 +911,7 @@ __global__ void __launch_bounds__(32 * kMergeRows)
 }
 
 template <bool kCap>
-cudaError_t launch_cap(const PrefillParams& d, int sms, bool beside, cudaStream_t stream) {
+cudaError_t launch_cap(const PrefillParams& d, int sms, cudaStream_t stream) {
   static PerDeviceOnce once;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -922,7 +926,7 @@ cudaError_t launch_cap(const PrefillParams& d, int sms, bool beside, cudaStream_
                                 cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemP);
   });
   if (e != cudaSuccess) return e;
-  return launch(kda_attn_prefill_kernel<kCap>, dim3((unsigned)sms), dim3(kThreadsP), kSmemP, beside, stream, d);
+  return launch(kda_attn_prefill_kernel<kCap>, dim3((unsigned)sms), dim3(kThreadsP), kSmemP, true, stream, d);
 }
 
 }  // namespace
@@ -950,8 +954,8 @@ cudaError_t launch_attn_prefill(const AttnParams& a, int min_rows, void* work, i
                                 cudaStream_t stream) {
   PrefillParams d;
   if (!make_params(a, min_rows, work, sms, &d)) return cudaErrorNotSupported;
-  return a.softcap > 0.0f ? launch_cap<true>(d, sms, beside, stream)
-                          : launch_cap<false>(d, sms, beside, stream);
+  d.wait = !beside;
+  return a.softcap > 0.0f ? launch_cap<true>(d, sms, stream) : launch_cap<false>(d, sms, stream);
 }
 
 cudaError_t launch_attn_prefill_merge(const AttnParams& a, int min_rows, void* work, int sms, bool wait,

@@ -98,6 +98,8 @@ __device__ __forceinline__ float row_reduce(float v, float* red) {
 template <typename R, typename Wt, int kV, bool kVec, bool kWarpRow>
 __global__ void __launch_bounds__(1024) kda_norm_kernel(const __grid_constant__ NormParams p) {
   __shared__ float red[2][32];
+  sm100::pdl_wait();   // (launched as a programmatic dependent of the work before it)
+  sm100::pdl_launch_dependents();
   const int tr = kWarpRow ? (threadIdx.x & 31) : threadIdx.x;   // thread within the row
   const int nt = kWarpRow ? 32 : blockDim.x;
   const int64_t row = kWarpRow ? (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5)
@@ -186,47 +188,42 @@ __global__ void __launch_bounds__(1024) kda_norm_kernel(const __grid_constant__ 
 }
 
 template <typename R, typename Wt, int kV, bool kVec>
-void launch_v(const NormParams& p, cudaStream_t stream) {
+cudaError_t launch_v(const NormParams& p, cudaStream_t stream) {
   const int chunks = (p.cols + 7) / 8;
   if constexpr (kV == 1) {
     if (chunks <= 32) {   // a warp per row, eight rows a CTA
       const unsigned grid = (unsigned)((p.rows + 7) / 8);
-      kda_norm_kernel<R, Wt, kV, kVec, true><<<grid, 256, 0, stream>>>(p);
-      return;
+      return launch(kda_norm_kernel<R, Wt, kV, kVec, true>, dim3(grid), dim3(256), 0, true, stream, p);
     }
   }
   const int threads = ((chunks + kV - 1) / kV + 31) / 32 * 32;
-  kda_norm_kernel<R, Wt, kV, kVec, false><<<(unsigned)p.rows, threads, 0, stream>>>(p);
+  return launch(kda_norm_kernel<R, Wt, kV, kVec, false>, dim3((unsigned)p.rows), dim3(threads), 0, true,
+                stream, p);
 }
 
 template <typename R, typename Wt, bool kVec>
-void launch_rw(const NormParams& p, cudaStream_t stream) {
+cudaError_t launch_rw(const NormParams& p, cudaStream_t stream) {
   // One chunk a thread as long as a CTA has the threads for a row (cols <= 8192): 32 registers, two
   // full CTAs an SM.  Against four chunks a thread on a GB300, bf16 in and out: 131072 x 256
   // 42.6 / 65.3 us, 16384 x 4096 82.3 / 89.7, 16384 x 7168 152.3 / 164.0 (93% / 86% of the copy
   // rate), and the shortest chain of loads for a few rows.  Wider rows take four (12288 columns:
   // two chunks 178.0 us, four 154.3).
-  if (p.cols <= 8 * 1024) launch_v<R, Wt, 1, kVec>(p, stream);
-  else launch_v<R, Wt, 4, kVec>(p, stream);
+  return p.cols <= 8 * 1024 ? launch_v<R, Wt, 1, kVec>(p, stream) : launch_v<R, Wt, 4, kVec>(p, stream);
 }
 
 template <typename R, typename Wt>
-void launch_r(const NormParams& p, bool aligned, cudaStream_t stream) {
-  if (aligned) launch_rw<R, Wt, true>(p, stream);
-  else launch_rw<R, Wt, false>(p, stream);
+cudaError_t launch_r(const NormParams& p, bool aligned, cudaStream_t stream) {
+  return aligned ? launch_rw<R, Wt, true>(p, stream) : launch_rw<R, Wt, false>(p, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_norm(const NormParams& p, bool aligned, cudaStream_t stream) {
-  if (p.residual_f32) {
-    if (p.weight_f32) launch_r<float, float>(p, aligned, stream);
-    else launch_r<float, __nv_bfloat16>(p, aligned, stream);
-  } else {
-    if (p.weight_f32) launch_r<__nv_bfloat16, float>(p, aligned, stream);
-    else launch_r<__nv_bfloat16, __nv_bfloat16>(p, aligned, stream);
-  }
-  return cudaGetLastError();
+  if (p.residual_f32)
+    return p.weight_f32 ? launch_r<float, float>(p, aligned, stream)
+                        : launch_r<float, __nv_bfloat16>(p, aligned, stream);
+  return p.weight_f32 ? launch_r<__nv_bfloat16, float>(p, aligned, stream)
+                      : launch_r<__nv_bfloat16, __nv_bfloat16>(p, aligned, stream);
 }
 
 }  // namespace attn
