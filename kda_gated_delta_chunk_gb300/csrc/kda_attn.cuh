@@ -147,22 +147,6 @@ struct AttnParams {
 size_t attn_workspace_bytes(int32_t num_seqs, int32_t heads, int32_t kv_heads, int32_t max_q_len);
 cudaError_t launch_attn(const AttnParams& p, int sms, cudaStream_t stream);
 
-// Sequences with at most max_rows (at most 32) rows: new tokens x heads per kv head.
-size_t decode_workspace_bytes(int sms);
-cudaError_t launch_attn_decode(const AttnParams& p, int max_rows, void* work, int sms,
-                               cudaStream_t stream);
-// Sequences with at least min_rows of them (heads per kv head at most 256).  `beside`: as the
-// programmatic dependent of the decode kernel, which it shares nothing with.
-size_t prefill_workspace_bytes(int sms);
-cudaError_t launch_attn_prefill(const AttnParams& p, int min_rows, void* work, int sms, bool beside,
-                                cudaStream_t stream);
-// The parts of items that the cut divided, merged.  `wait`: launched as the programmatic dependent
-// of the kernel whose parts they are, for which the merge waits.
-cudaError_t launch_attn_decode_merge(const AttnParams& p, int max_rows, void* work, int sms, bool wait,
-                                     cudaStream_t stream);
-cudaError_t launch_attn_prefill_merge(const AttnParams& p, int min_rows, void* work, int sms, bool wait,
-                                      cudaStream_t stream);
-
 // The sequence that token t belongs to: the last n with cu[n] <= t (cu non-decreasing,
 // cu[0] <= t < cu[N]).
 __device__ __forceinline__ int seq_of(const int32_t* cu, int num_seqs, int64_t t) {

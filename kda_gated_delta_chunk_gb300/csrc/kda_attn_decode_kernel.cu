@@ -779,9 +779,8 @@ size_t decode_workspace_bytes(int sms) {
 }
 
 namespace {
-bool make_params(const AttnParams& a, int max_rows, void* work, int sms, DecodeParams* d) {
+void make_params(const AttnParams& a, int max_rows, void* work, int sms, DecodeParams* d) {
   d->a = a;
-  if (!make_cache_maps(a.c, &d->maps)) return false;
   d->wait = 0;
   d->group = a.heads / a.c.kv_heads;
   d->group_magic = 65535u / (uint32_t)d->group + 1;
@@ -789,15 +788,15 @@ bool make_params(const AttnParams& a, int max_rows, void* work, int sms, DecodeP
   d->max_rows = max_rows;
   d->desc = static_cast<PartDesc*>(work);
   d->slots = reinterpret_cast<float*>(d->desc + decode_ctas(sms));
-  return true;
 }
 }  // namespace
 
 // The operands are padded to 8, 16 or 32 rows.
-cudaError_t launch_attn_decode(const AttnParams& a, int max_rows, void* work, int sms,
-                               cudaStream_t stream) {
+cudaError_t launch_attn_decode(const AttnParams& a, const CacheMaps& maps, int max_rows, void* work,
+                               int sms, cudaStream_t stream) {
   DecodeParams d;
-  if (!make_params(a, max_rows, work, sms, &d)) return cudaErrorNotSupported;
+  make_params(a, max_rows, work, sms, &d);
+  d.maps = maps;
   const bool cap = a.softcap > 0.0f;
   if (max_rows <= 8) return cap ? launch_nr<8, true>(d, sms, stream) : launch_nr<8, false>(d, sms, stream);
   if (max_rows <= 16) return cap ? launch_nr<16, true>(d, sms, stream) : launch_nr<16, false>(d, sms, stream);
@@ -806,8 +805,8 @@ cudaError_t launch_attn_decode(const AttnParams& a, int max_rows, void* work, in
 
 cudaError_t launch_attn_decode_merge(const AttnParams& a, int max_rows, void* work, int sms, bool wait,
                                      cudaStream_t stream) {
-  DecodeParams d;
-  if (!make_params(a, max_rows, work, sms, &d)) return cudaErrorNotSupported;
+  DecodeParams d = {};
+  make_params(a, max_rows, work, sms, &d);
   d.wait = wait;
   return max_rows <= 8    ? launch_merge<8>(d, sms, stream)
          : max_rows <= 16 ? launch_merge<16>(d, sms, stream)

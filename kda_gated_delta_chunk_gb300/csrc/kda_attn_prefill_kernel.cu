@@ -936,9 +936,8 @@ size_t prefill_workspace_bytes(int sms) {
 }
 
 namespace {
-bool make_params(const AttnParams& a, int min_rows, void* work, int sms, PrefillParams* d) {
+void make_params(const AttnParams& a, int min_rows, void* work, int sms, PrefillParams* d) {
   d->a = a;
-  if (!make_cache_maps(a.c, &d->maps)) return false;
   d->wait = 0;
   d->min_rows = min_rows;
   d->group = a.heads / a.c.kv_heads;
@@ -946,22 +945,22 @@ bool make_params(const AttnParams& a, int min_rows, void* work, int sms, Prefill
   d->tokens = kRowsP / d->group;
   d->desc = static_cast<PartDescP*>(work);
   d->slots = reinterpret_cast<float*>(d->desc + sms);
-  return true;
 }
 }  // namespace
 
-cudaError_t launch_attn_prefill(const AttnParams& a, int min_rows, void* work, int sms, bool beside,
-                                cudaStream_t stream) {
+cudaError_t launch_attn_prefill(const AttnParams& a, const CacheMaps& maps, int min_rows, void* work,
+                                int sms, bool beside, cudaStream_t stream) {
   PrefillParams d;
-  if (!make_params(a, min_rows, work, sms, &d)) return cudaErrorNotSupported;
+  make_params(a, min_rows, work, sms, &d);
+  d.maps = maps;
   d.wait = !beside;
   return a.softcap > 0.0f ? launch_cap<true>(d, sms, stream) : launch_cap<false>(d, sms, stream);
 }
 
 cudaError_t launch_attn_prefill_merge(const AttnParams& a, int min_rows, void* work, int sms, bool wait,
                                       cudaStream_t stream) {
-  PrefillParams d;
-  if (!make_params(a, min_rows, work, sms, &d)) return cudaErrorNotSupported;
+  PrefillParams d = {};
+  make_params(a, min_rows, work, sms, &d);
   d.wait = wait;
   return launch(kda_attn_prefill_merge_kernel, dim3((unsigned)sms, kRowsP / kMergeRows),
                 dim3(32 * kMergeRows), 0, true, stream, d);

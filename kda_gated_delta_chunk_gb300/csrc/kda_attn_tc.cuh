@@ -168,6 +168,23 @@ struct CacheMaps {
 };
 bool make_cache_maps(const CacheView& c, CacheMaps* m);
 
+// ------------------------------------------------------------ the kernels of a call
+// Sequences with at most max_rows (at most 32) rows: new tokens x heads per kv head.
+size_t decode_workspace_bytes(int sms);
+cudaError_t launch_attn_decode(const AttnParams& p, const CacheMaps& maps, int max_rows, void* work,
+                               int sms, cudaStream_t stream);
+// Sequences with at least min_rows of them (heads per kv head at most 256).  `beside`: as the
+// programmatic dependent of the decode kernel, which it shares nothing with.
+size_t prefill_workspace_bytes(int sms);
+cudaError_t launch_attn_prefill(const AttnParams& p, const CacheMaps& maps, int min_rows, void* work,
+                                int sms, bool beside, cudaStream_t stream);
+// The parts of items that the cut divided, merged.  `wait`: launched as the programmatic dependent
+// of the kernel whose parts they are, for which the merge waits.
+cudaError_t launch_attn_decode_merge(const AttnParams& p, int max_rows, void* work, int sms, bool wait,
+                                     cudaStream_t stream);
+cudaError_t launch_attn_prefill_merge(const AttnParams& p, int min_rows, void* work, int sms, bool wait,
+                                      cudaStream_t stream);
+
 // ------------------------------------------------------------ one sequence of a batch
 struct SeqInfo {
   int tok0, q_len, len;   // first new token, new tokens, cached tokens (new ones included)

@@ -21,9 +21,11 @@ from . import (ERR_INVALID_ARG, HEAD_DIM, KDAError, OK, STATE_BF16, STATE_F32, l
 
 _BF16, _F32 = torch.bfloat16, torch.float32
 _BYTES = (torch.float8_e4m3fn, torch.uint8)
+_DENSE = torch.contiguous_format
 _HALF, _EITHER = (_BF16,), (_BF16, _F32)
 _FLOAT = (_F32,)
-_INT = (torch.int32,)
+_I32 = torch.int32
+_INT = (_I32,)
 _UINT8 = (torch.uint8,)
 # the current stream's handle without a Stream object around it (a call's host time counts in decode)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
@@ -86,25 +88,43 @@ def _cache(k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, num_seqs, d
     pages, hk, page, d = shape
     if d != HEAD_DIM:
         raise KDAError(ERR_INVALID_ARG, f"head_dim {d} (only {HEAD_DIM} is supported)")
-    per_page = _check(k_cache, "k_cache", _BYTES, shape, dev, 3)
-    _check(v_cache, "v_cache", _BYTES, shape, dev, 3)
-    st = k_cache.stride()
-    if v_cache.stride() != st:
-        raise ValueError("k_cache and v_cache must have the same strides")
-    scales = (pages, hk)
-    sc = _check(k_scale, "k_scale", _FLOAT, scales, dev)
-    if _check(v_scale, "v_scale", _FLOAT, scales, dev) != sc:
-        raise ValueError("k_scale and v_scale must have the same strides")
     blocks = block_table.size(-1) if block_table.dim() == 2 else -1
-    if blocks < 0:
-        raise ValueError("block_table must be [num_seqs, max_blocks]")
-    row = _check(block_table, "block_table", _INT, (num_seqs, blocks), dev)
-    _check(kv_lens, "kv_lens", _INT, (num_seqs,), dev, 0)
-    tok = st[2] if page > 1 else HEAD_DIM
-    head = st[1] if hk > 1 else page * tok
+    scales = (pages, hk)
+    # the usual case at once: everything contiguous, of the right type, shape and device
+    if (k_cache.is_contiguous() and v_cache.is_contiguous() and k_scale.is_contiguous()
+            and v_scale.is_contiguous() and block_table.is_contiguous() and kv_lens.is_contiguous()
+            and k_cache.dtype in _BYTES and v_cache.dtype in _BYTES and k_scale.dtype is _F32
+            and v_scale.dtype is _F32 and block_table.dtype is _I32 and kv_lens.dtype is _I32
+            and v_cache.shape == shape and k_scale.shape == scales and v_scale.shape == scales
+            and block_table.shape == (num_seqs, blocks) and kv_lens.shape == (num_seqs,)
+            and k_cache.get_device() == dev and v_cache.get_device() == dev
+            and k_scale.get_device() == dev and v_scale.get_device() == dev
+            and block_table.get_device() == dev and kv_lens.get_device() == dev):
+        tok, row, sc = HEAD_DIM, blocks, hk
+        head = page * HEAD_DIM
+        per_page = hk * head
+    else:
+        per_page = _check(k_cache, "k_cache", _BYTES, shape, dev, 3)
+        _check(v_cache, "v_cache", _BYTES, shape, dev, 3)
+        st = k_cache.stride()
+        if v_cache.stride() != st:
+            raise ValueError("k_cache and v_cache must have the same strides")
+        sc = _check(k_scale, "k_scale", _FLOAT, scales, dev)
+        if _check(v_scale, "v_scale", _FLOAT, scales, dev) != sc:
+            raise ValueError("k_scale and v_scale must have the same strides")
+        if blocks < 0:
+            raise ValueError("block_table must be [num_seqs, max_blocks]")
+        row = _check(block_table, "block_table", _INT, (num_seqs, blocks), dev)
+        _check(kv_lens, "kv_lens", _INT, (num_seqs,), dev, 0)
+        tok = st[2] if page > 1 else HEAD_DIM
+        head = st[1] if hk > 1 else page * tok
+        if pages == 1:
+            per_page = hk * head
+        if num_seqs == 1:
+            row = blocks
     return _CACHE.pack(k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
-                       per_page if pages > 1 else hk * head, head, tok, sc, pages, page, hk, blocks,
-                       block_table.data_ptr(), row if num_seqs > 1 else blocks, kv_lens.data_ptr()), hk
+                       per_page, head, tok, sc, pages, page, hk, blocks, block_table.data_ptr(), row,
+                       kv_lens.data_ptr()), hk
 
 
 def _status_workspace(workspace, dev):
@@ -178,7 +198,7 @@ def add_rms_norm(x, residual, weight, eps: float = 1e-6, want: str = "bf16", gro
         if residual.dtype is _F32:
             r_kind = STATE_F32
         if residual_out is None:
-            residual_out = torch.empty(shape, dtype=residual.dtype, device=dev)
+            residual_out = torch.empty_like(residual, memory_format=_DENSE)
         else:
             lds = _check(residual_out, "residual_out", (residual.dtype,), shape, dev)
         s_ptr = residual_out.data_ptr()
@@ -189,7 +209,7 @@ def add_rms_norm(x, residual, weight, eps: float = 1e-6, want: str = "bf16", gro
             raise ValueError("y is not written with want='fp8'")
     else:
         if y is None:
-            y = torch.empty(shape, dtype=_BF16, device=dev)
+            y = torch.empty_like(x, memory_format=_DENSE)
         else:
             ldy = _check(y, "y", _HALF, shape, dev)
         y_ptr = y.data_ptr()
@@ -247,7 +267,7 @@ def rope_append(q, k, v, rope, k_cache, v_cache, k_scale, v_scale, block_table, 
         q_shape = (T, heads, HEAD_DIM)
         q_row = _check(q, "q", _HALF, q_shape, dev)
         if q_out is None:
-            q_out = torch.empty(q_shape, dtype=_BF16, device=dev)
+            q_out = torch.empty_like(q, memory_format=_DENSE)
             qo_row = heads * HEAD_DIM
         else:
             qo_row = _check(q_out, "q_out", _HALF, q_shape, dev)
@@ -313,7 +333,7 @@ def cached_attention(q, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens
     c, hk = _cache(k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, N, dev)
     out_row = heads * HEAD_DIM
     if out is None:
-        out = torch.empty(shape, dtype=_BF16, device=dev)
+        out = torch.empty_like(q, memory_format=_DENSE)
     else:
         out_row = _check(out, "out", _HALF, shape, dev)
     lse_ptr = None
