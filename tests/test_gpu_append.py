@@ -222,6 +222,22 @@ def test_strided_inputs_positions_and_in_place_queries():
     assert torch.equal(k.cpu(), d["k"]) and bool((qkv[:, :8] == 0).all()) and bool((qkv[:, -56:] == 0).all())
 
 
+def test_many_sequences():
+    """More sequences than a CTA has threads, for the pages and for the queries' positions."""
+    g = torch.Generator().manual_seed(3)
+    lens = torch.randint(0, 4, (1100,), generator=g).tolist()
+    starts = torch.randint(0, 20, (1100,), generator=g).tolist()
+    lens[700], starts[901] = 90, 50
+    d = make(lens, starts, 2, 1, 16, 32)
+    caches = on_gpu(d, "hpd")
+    q, status = run(d, caches)
+    assert status == kda.OK
+    q64, size = expect(d)
+    assert bool(((q.cpu().double() - q64).abs() <= 2.0 ** -8 * q64.abs() + 2.0 ** -22 * size).all())
+    check_cache(caches[0], caches[2], d["k_ref"], False)
+    check_cache(caches[1], caches[3], d["v_ref"], True)
+
+
 def test_device_errors_skip_and_report():
     """A page outside the pool, a cache longer than the table, fewer cached than new tokens, a
     position outside the rotation table: recorded, and the rest of the batch is right."""

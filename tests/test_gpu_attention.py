@@ -319,6 +319,20 @@ def test_offsets_past_32_bits():
         check(d2, out, lse)
 
 
+@pytest.mark.parametrize("N,long", [(300, []), (1100, [5, 800, 1099])])
+def test_many_sequences(N, long):
+    """More sequences than the threads that add up the batch's work at once, empty ones among them."""
+    g = torch.Generator().manual_seed(N)
+    q = torch.randint(0, 3, (N,), generator=g).tolist()
+    kv = [max(a, int(x)) for a, x in zip(q, torch.randint(0, 60, (N,), generator=g).tolist())]
+    for n in long:
+        q[n], kv[n] = 70 + n % 7, 90 + n % 200
+    d = make(q, kv, 2, 1, 16, seed=21)
+    out, lse, status = launch(d)
+    assert status == kda.OK
+    check(d, out, lse)
+
+
 def test_device_errors_skip_and_report():
     for q_lens, kv_lens in (([1, 1], [100, 200]), ([100, 120], [100, 200])):
         for broken in ("page", "long", "more"):
