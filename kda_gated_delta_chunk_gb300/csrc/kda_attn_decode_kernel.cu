@@ -62,7 +62,9 @@ struct Cfg {
 // Workspace after the status words: desc [ctas], then per CTA two slots of [NR][128] sums,
 // [NR] maxima and [NR] denominators.
 struct PartDesc {
-  int n, h, parts, pad;
+  int parts;          // CTAs whose parts make up the item that this CTA begins; 0: none is cut
+  int tok0, rows;     // its first token's row of q and out, its query rows
+  int head0;          // its first query head
 };
 template <int NR>
 constexpr int kSlotFloats = NR * 130;
@@ -644,8 +646,9 @@ __global__ void __launch_bounds__(kThreads, 2)
         if (begins) {   // the CTA that its last tile lies in, from the cut of the ranges
           const int64_t last = walk.unit_of(walk.s.tiles - 1);
           const int64_t c = ((last + 1) * ranges - 1) / total;
-          part.n = walk.n;
-          part.h = walk.h;
+          part.tok0 = walk.s.tok0;
+          part.rows = rows;
+          part.head0 = walk.h * G;
           part.parts = (int)(c - blockIdx.x) + 1;
         }
       }
@@ -664,63 +667,87 @@ __global__ void __launch_bounds__(kThreads, 2)
 }
 
 // Merges the parts of the item that CTA blockIdx.x of the first kernel began and did not
-// finish: sums and denominators by their maxima, in a fixed order.  Four warps a row (a part each
-// in turn), two rows a CTA, 4 channels a lane.
-constexpr int kMergeWarps = 4;
+// finish: sums and denominators by their maxima, in a fixed order.  Eight warps a CTA take NR / 8
+// rows; the warps of a row take its parts in turn, 4 channels a lane, four parts in flight.  (One
+// sequence of 65536 tokens leaves 76 parts an item: a chain of loads per part would cost more
+// than reading the cache.)
+constexpr int kMergeWarps = 8, kInFlight = 4;
 template <int NR>
-__global__ void __launch_bounds__(64 * kMergeWarps)
+__global__ void __launch_bounds__(32 * kMergeWarps)
     kda_attn_merge_kernel(const __grid_constant__ DecodeParams p) {
-  __shared__ float4 acc_s[2][kMergeWarps][32];
-  __shared__ float den_s[2][kMergeWarps];
+  constexpr int kPerRow = 64 / NR;     // warps of a row
+  __shared__ float4 acc_s[kMergeWarps][32];
+  __shared__ float2 ml_s[kMergeWarps];
   if (p.wait) pdl_wait();
   pdl_launch_dependents();
-  const PartDesc d = p.desc[blockIdx.x];
+  const int4 d4 = *reinterpret_cast<const int4*>(p.desc + blockIdx.x);
+  const PartDesc d = {d4.x, d4.y, d4.z, d4.w};
   if (d.parts == 0) return;
-  const int lane = threadIdx.x & 31, w0 = (threadIdx.x >> 5) % kMergeWarps, rr = threadIdx.x / (32 * kMergeWarps);
-  const int r = blockIdx.y * 2 + rr;
-  const int G = p.a.heads / p.a.c.kv_heads;
-  const int tok0 = p.a.cu_seqlens[d.n], rows = (p.a.cu_seqlens[d.n + 1] - tok0) * G;
-  auto slot = [&](int i) {
-    return p.slots + ((int64_t)2 * (blockIdx.x + i) + (i == 0 ? 1 : 0)) * kSlotFloats<NR>;
-  };
-  float m = -INFINITY;
-  if (r < rows) {
-    for (int i = lane; i < d.parts; i += 32) m = fmaxf(m, slot(i)[NR * 128 + r]);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, w0 = warp % kPerRow;
+  const int r = blockIdx.y * (NR / 8) + warp / kPerRow;
+  const bool live = r < d.rows;
+  float m = -INFINITY, den = 0.0f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  // four parts merged into the running maximum, sum and denominator
+  auto merge = [&](const float (&mi)[kInFlight], const float (&di)[kInFlight], const float4 (&ai)[kInFlight]) {
+    float top = m;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    const float ref = m == -INFINITY ? 0.0f : m;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    float den = 0.0f;
-#pragma unroll 4
-    for (int i = w0; i < d.parts; i += kMergeWarps) {
-      const float* s = slot(i);
-      const float w = ex2(s[NR * 128 + r] - ref);
-      const float4 a = *reinterpret_cast<const float4*>(s + r * 128 + 4 * lane);
-      den += s[NR * 129 + r] * w;
-      acc.x += a.x * w;
-      acc.y += a.y * w;
-      acc.z += a.z * w;
-      acc.w += a.w * w;
+    for (int u = 0; u < kInFlight; ++u) top = fmaxf(top, mi[u]);
+    const float ref = top == -INFINITY ? 0.0f : top, f = ex2(m - ref);
+    m = top;
+    den *= f;
+    acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
+#pragma unroll
+    for (int u = 0; u < kInFlight; ++u) {
+      const float w = ex2(mi[u] - ref);
+      den += di[u] * w;
+      acc.x += ai[u].x * w;
+      acc.y += ai[u].y * w;
+      acc.z += ai[u].z * w;
+      acc.w += ai[u].w * w;
     }
-    acc_s[rr][w0][lane] = acc;
-    if (lane == 0) den_s[rr][w0] = den;
+  };
+  if (live) {
+    for (int i0 = w0; i0 < d.parts; i0 += kPerRow * kInFlight) {
+      float mi[kInFlight], di[kInFlight];
+      float4 ai[kInFlight];
+#pragma unroll
+      for (int u = 0; u < kInFlight; ++u) {
+        const int i = i0 + u * kPerRow;
+        const float* s = p.slots + ((int64_t)2 * (blockIdx.x + i) + (i == 0 ? 1 : 0)) * kSlotFloats<NR>;
+        mi[u] = -INFINITY;
+        di[u] = 0.0f;
+        ai[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (i < d.parts) {
+          mi[u] = s[NR * 128 + r];
+          di[u] = s[NR * 129 + r];
+          ai[u] = *reinterpret_cast<const float4*>(s + r * 128 + 4 * lane);
+        }
+      }
+      merge(mi, di, ai);
+    }
+    acc_s[warp][lane] = acc;
+    if (lane == 0) ml_s[warp] = make_float2(m, den);
   }
   __syncthreads();
-  if (w0 != 0 || r >= rows) return;
-  float4 acc = acc_s[rr][0][lane];
-  float den = den_s[rr][0];
+  if (w0 != 0 || !live) return;
+  for (int w = 1; w < kPerRow; w += kInFlight) {
+    float mi[kInFlight], di[kInFlight];
+    float4 ai[kInFlight];
 #pragma unroll
-  for (int w = 1; w < kMergeWarps; ++w) {
-    const float4 a = acc_s[rr][w][lane];
-    acc.x += a.x;
-    acc.y += a.y;
-    acc.z += a.z;
-    acc.w += a.w;
-    den += den_s[rr][w];
+    for (int u = 0; u < kInFlight; ++u) {
+      const bool in = w + u < kPerRow;
+      const float2 ml = in ? ml_s[warp + w + u] : make_float2(-INFINITY, 0.0f);
+      mi[u] = ml.x;
+      di[u] = ml.y;
+      ai[u] = in ? acc_s[warp + w + u][lane] : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    merge(mi, di, ai);
   }
   const float il = den == 0.0f ? 0.0f : 1.0f / den;
-  const int64_t tok = tok0 + r / G;
-  const int head = d.h * G + r % G;
+  const int i = div_small(r, p.group_magic);
+  const int64_t tok = d.tok0 + i;
+  const int head = d.head0 + r - i * p.group;
   *reinterpret_cast<uint2*>(p.a.out + tok * p.a.out_stride + head * kHeadDim + 4 * lane) =
       make_uint2(pack_bf16x2(acc.x * il, acc.y * il), pack_bf16x2(acc.z * il, acc.w * il));
   if (p.a.lse && lane == 0)
@@ -745,7 +772,7 @@ cudaError_t launch_nr(const DecodeParams& d, int sms, cudaStream_t stream) {
 }
 template <int NR>
 cudaError_t launch_merge(const DecodeParams& d, int sms, cudaStream_t stream) {
-  return launch(kda_attn_merge_kernel<NR>, dim3((unsigned)decode_ctas(sms), NR / 2), dim3(64 * kMergeWarps),
+  return launch(kda_attn_merge_kernel<NR>, dim3((unsigned)decode_ctas(sms), 8), dim3(32 * kMergeWarps),
                 0, d.wait != 0, stream, d);
 }
 
