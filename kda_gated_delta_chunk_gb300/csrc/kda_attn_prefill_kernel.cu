@@ -880,26 +880,41 @@ __global__ void __launch_bounds__(32 * kMergeRows)
   const int first = d.rt * p.tokens, rows = min(p.tokens, q_len - first) * G;
   const int r = blockIdx.y * kMergeRows + (threadIdx.x >> 5);
   if (r >= rows) return;
-  auto slot = [&](int i) {
-    return p.slots + ((int64_t)2 * (blockIdx.x + i) + (i == 0 ? 1 : 0)) * kSlotFloatsP;
-  };
-  float m = -INFINITY;
-  for (int i = lane; i < d.parts; i += 32) m = fmaxf(m, slot(i)[kRowsP * 128 + r]);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  const float ref = m == -INFINITY ? 0.0f : m;
+  // four parts in flight, merged into the running maximum, sum and denominator
+  constexpr int kInFlight = 4;
+  float m = -INFINITY, den = 0.0f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  float den = 0.0f;
-#pragma unroll 4
-  for (int i = 0; i < d.parts; ++i) {
-    const float* s = slot(i);
-    const float w = ex2(s[kRowsP * 128 + r] - ref);
-    const float4 a = *reinterpret_cast<const float4*>(s + r * 128 + 4 * lane);
-    den += s[kRowsP * 129 + r] * w;
-    acc.x += a.x * w;
-    acc.y += a.y * w;
-    acc.z += a.z * w;
-    acc.w += a.w * w;
+  for (int i0 = 0; i0 < d.parts; i0 += kInFlight) {
+    float mi[kInFlight], di[kInFlight], top = m;
+    float4 ai[kInFlight];
+#pragma unroll
+    for (int u = 0; u < kInFlight; ++u) {
+      const int i = i0 + u;
+      const float* s = p.slots + ((int64_t)2 * (blockIdx.x + i) + (i == 0 ? 1 : 0)) * kSlotFloatsP;
+      mi[u] = -INFINITY;
+      di[u] = 0.0f;
+      ai[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (i < d.parts) {
+        mi[u] = s[kRowsP * 128 + r];
+        di[u] = s[kRowsP * 129 + r];
+        ai[u] = *reinterpret_cast<const float4*>(s + r * 128 + 4 * lane);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kInFlight; ++u) top = fmaxf(top, mi[u]);
+    const float ref = top == -INFINITY ? 0.0f : top, f = ex2(m - ref);
+    m = top;
+    den *= f;
+    acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
+#pragma unroll
+    for (int u = 0; u < kInFlight; ++u) {
+      const float w = ex2(mi[u] - ref);
+      den += di[u] * w;
+      acc.x += ai[u].x * w;
+      acc.y += ai[u].y * w;
+      acc.z += ai[u].z * w;
+      acc.w += ai[u].w * w;
+    }
   }
   const float il = den == 0.0f ? 0.0f : 1.0f / den;
   const int64_t tok = tok0 + first + r / G;
