@@ -233,7 +233,9 @@ __global__ void __launch_bounds__(kThreadsP, 1)
       const int ql = __shfl_sync(0xffffffffu, q_len, k), ln = __shfl_sync(0xffffffffu, len, k);
       int sum = 0;
       for (int rt = lane; rt * p.tokens < ql; rt += 32) sum += item_of(ql, ln, rt, p.tokens, p.a.window).tiles + kOverP;
-      const int all = __reduce_add_sync(0xffffffffu, sum);
+      // (millions of new tokens over as many keys: the warp's sum passes 31 bits)
+      const long long all = __reduce_add_sync(0xffffffffu, (unsigned)sum & 0xffffu) +
+                            ((long long)__reduce_add_sync(0xffffffffu, (unsigned)sum >> 16) << 16);
       if (lane == k) mine = all;
     }
     mine *= hk;
