@@ -693,68 +693,10 @@ __global__ void __launch_bounds__(kThreadsP, 1)
         tmem_wait_ld();
         const float4* sc = reinterpret_cast<const float4*>(sm + kOffSc) + (it & 3) * 8 + 4 * cg;
         const bool masked = kTile - 1 > p_lo || (p.a.window > 0 && p.a.window <= p_hi);
-        float mt = -INFINITY;
         const bool scaled = kCap || masked;    // s holds the finished exponents (else raw products)
-        if (scaled) {
-          // bits of the 64 keys that this row sees: lo <= e <= hi
-          const int lo = p.a.window > 0 ? hi - p.a.window + 1 : 0;
-          const uint64_t upto = hi < 0 ? 0 : (hi >= 63 ? ~0ull : (2ull << hi) - 1);
-          const uint64_t see = lo <= 0 ? upto : (lo >= 64 ? 0 : upto & (~0ull << lo));
-#pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            const float4 f = sc[g];
-            const float mul = qmul * f.x;
-            const uint32_t bits = (uint32_t)(see >> (32 * (g >> 1))) >> (16 * (g & 1));
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              float x = __uint_as_float(s[16 * g + e]);
-              x = kCap ? cap_score(x * mul, cap2, cap1) + f.y : fmaf(x, mul, f.y);
-              if (!((bits >> e) & 1)) x = -INFINITY;
-              mt = fmaxf(mt, x);
-              s[16 * g + e] = __float_as_uint(x);
-            }
-          }
-        } else {
-#pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            const float4 f = sc[g];
-            float a = __uint_as_float(s[16 * g]), b = __uint_as_float(s[16 * g + 1]);
-#pragma unroll
-            for (int e = 16 * g + 2; e < 16 * g + 14; e += 4) {
-              a = max3(a, __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
-              b = max3(b, __uint_as_float(s[e + 2]), __uint_as_float(s[e + 3]));
-            }
-            a = max3(a, __uint_as_float(s[16 * g + 14]), __uint_as_float(s[16 * g + 15]));
-            mt = fmaxf(mt, fmaf(fmaxf(a, b), qmul * f.x, f.y));
-          }
-        }
-        // the row's other 64 keys
-        mx_s[((it & 1) * 2 + cg) * kRowsP] = mt;
-        group_sync(id_pair, 64);      // (also: both have S in registers, P may go over it)
-        mt = fmaxf(mt, mx_s[((it & 1) * 2 + (cg ^ 1)) * kRowsP]);
-        if (__any_sync(0xffffffffu, mt > m + kSlack)) {
-          const float next = fmaxf(m, mt), f = ex2(m - (next == -INFINITY ? 0.0f : next));
-          if (t > 0) {       // O, the tile before included, by the factor
-#pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-              uint32_t o[16];
-              tmem_ld16(to + 16 * c, o);
-              tmem_wait_ld();
-#pragma unroll
-              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-              tmem_st16(to + 16 * c, o);
-            }
-          }
-          l *= f;
-          m = next;
-        }
-        const float ref = (m == -INFINITY ? 0.0f : m) - kPShift;
-        // P over the columns of S
-        uint32_t pk[32];
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          const float4 f = sc[g];
-          const float mul = scaled ? 1.0f : qmul * f.x, add = scaled ? -ref : f.y - ref;
+        float mt = -INFINITY;
+        // P of the group's 16 keys, and their part of the denominator
+        auto p_of = [&](int g, float mul, float add, uint32_t (&pk)[32]) -> float {
           const float2 mul2 = make_float2(mul, mul), add_2 = make_float2(add, add);
           float2 sum = make_float2(0.0f, 0.0f);
 #pragma unroll
@@ -765,8 +707,96 @@ __global__ void __launch_bounds__(kThreadsP, 1)
             sum = add2(sum, x);
             pk[e >> 1] = f16x2_of(x.x, x.y);
           }
-          l = fmaf(sum.x + sum.y, f.z, l);
+          return sum.x + sum.y;
+        };
+        auto max_of = [&](int g) -> float {    // of the group's raw products
+          float a = __uint_as_float(s[16 * g]), b = __uint_as_float(s[16 * g + 1]);
+#pragma unroll
+          for (int e = 16 * g + 2; e < 16 * g + 14; e += 4) {
+            a = max3(a, __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
+            b = max3(b, __uint_as_float(s[e + 2]), __uint_as_float(s[e + 3]));
+          }
+          a = max3(a, __uint_as_float(s[16 * g + 14]), __uint_as_float(s[16 * g + 15]));
+          return fmaxf(a, b);
+        };
+        auto with_pair = [&] {        // the row's other 64 keys
+          mx_s[((it & 1) * 2 + cg) * kRowsP] = mt;
+          group_sync(id_pair, 64);    // (also: both have S in registers, P may go over it)
+          mt = fmaxf(mt, mx_s[((it & 1) * 2 + (cg ^ 1)) * kRowsP]);
+        };
+        uint32_t pk[32];
+        bool keep = false;
+        const bool ahead = !scaled && t > 0;
+        if (ahead) {
+          // most tiles leave the reference where it is: P by it, the maximum beside that
+          const float ref = (m == -INFINITY ? 0.0f : m) - kPShift;
+          float sum = l;
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            const float4 f = sc[g];
+            const float mul = qmul * f.x;
+            mt = fmaxf(mt, fmaf(max_of(g), mul, f.y));
+            sum = fmaf(p_of(g, mul, f.y - ref, pk), f.z, sum);
+          }
+          with_pair();
+          keep = !__any_sync(0xffffffffu, mt > m + kSlack);
+          if (keep) l = sum;
         }
+        if (!keep) {
+          if (ahead) {
+            tmem_ld32(ts + 64 * cg, *reinterpret_cast<uint32_t(*)[32]>(s));
+            tmem_ld32(ts + 64 * cg + 32, *reinterpret_cast<uint32_t(*)[32]>(s + 32));
+            tmem_wait_ld();
+            group_sync(id_pair, 64);
+          } else if (scaled) {
+            // bits of the 64 keys that this row sees: lo <= e <= hi
+            const int lo = p.a.window > 0 ? hi - p.a.window + 1 : 0;
+            const uint64_t upto = hi < 0 ? 0 : (hi >= 63 ? ~0ull : (2ull << hi) - 1);
+            const uint64_t see = lo <= 0 ? upto : (lo >= 64 ? 0 : upto & (~0ull << lo));
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+              const float4 f = sc[g];
+              const float mul = qmul * f.x;
+              const uint32_t bits = (uint32_t)(see >> (32 * (g >> 1))) >> (16 * (g & 1));
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                float x = __uint_as_float(s[16 * g + e]);
+                x = kCap ? cap_score(x * mul, cap2, cap1) + f.y : fmaf(x, mul, f.y);
+                if (!((bits >> e) & 1)) x = -INFINITY;
+                mt = fmaxf(mt, x);
+                s[16 * g + e] = __float_as_uint(x);
+              }
+            }
+            with_pair();
+          } else {
+#pragma unroll
+            for (int g = 0; g < 4; ++g) mt = fmaxf(mt, fmaf(max_of(g), qmul * sc[g].x, sc[g].y));
+            with_pair();
+          }
+          if (__any_sync(0xffffffffu, mt > m + kSlack)) {
+            const float next = fmaxf(m, mt), f = ex2(m - (next == -INFINITY ? 0.0f : next));
+            if (t > 0) {       // O, the tile before included, by the factor
+#pragma unroll 1
+              for (int c = 0; c < 4; ++c) {
+                uint32_t o[16];
+                tmem_ld16(to + 16 * c, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                tmem_st16(to + 16 * c, o);
+              }
+            }
+            l *= f;
+            m = next;
+          }
+          const float ref = (m == -INFINITY ? 0.0f : m) - kPShift;
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            const float4 f = sc[g];
+            l = fmaf(p_of(g, scaled ? 1.0f : qmul * f.x, scaled ? -ref : f.y - ref, pk), f.z, l);
+          }
+        }
+        // P over the columns of S
         tmem_st32(ts + 32 * cg, pk);
         tmem_wait_st();
         tc_fence_before();
