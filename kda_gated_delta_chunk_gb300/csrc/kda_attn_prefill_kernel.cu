@@ -433,7 +433,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
                       dk + (x & 3) * 32 / 16, id_s, x > 0);
         mma_commit_on(lead, bar_s + 8 * h);
       };
-      auto pv = [&](uint32_t i, int h, bool first_tile) {   // O of half h += P(i) V(i)
+      auto pv = [&](uint32_t i, int h, bool first_tile, bool last_tile) {   // O of half h += P(i) V(i)
         // (the segment before has read its O)
         if (first_tile && seg > 0) ok = ok && mbar_wait_sleep(bar_of + 8 * h, (seg - 1) & 1);
         ok = ok && mbar_wait_sleep(bar_p + 8 * h, i & 1);      // P(i), V(i) and the keys of the tile after
@@ -445,7 +445,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
         for (int ks = 0; ks < 8; ++ks)
           mma_f16_ts_on(lead, tmem + kTOP + 128 * h, tmem + kTS + 128 * h + 8 * ks, dv + 2048 * ks / 16,
                         id_o, !(first_tile && ks == 0));
-        mma_commit_on(lead, bar_o + 8 * h);
+        if (last_tile) mma_commit_on(lead, bar_o + 8 * h);
       };
       while (true) {
         const Segment* sg = seg_wait(seg, ok);
@@ -466,10 +466,10 @@ __global__ void __launch_bounds__(kThreadsP, 1)
           if (++sk == kKStages) sk = 0;
           ++it;
           const bool more = t < tiles;
-          pv(it - 1, 0, t == 1);
+          pv(it - 1, 0, t == 1, !more);
           if (!ok) break;
           if (more) qk(0);
-          pv(it - 1, 1, t == 1);
+          pv(it - 1, 1, t == 1, !more);
           if (!ok) break;
           mma_commit_on(lead, bar_be + 8 * ((it - 1) & 1));
           if (!more) break;
@@ -683,7 +683,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
       for (int t = 0; t < tiles; ++t, ++it, hi -= kTile, p_lo -= kTile, p_hi -= kTile) {
         // (a wait costs over 100 cycles even when it need not wait: S, the last to come, last)
         ok = ok && mbar_wait_sleep(bar_sc + 8 * (it & 3), (it >> 2) & 1);
-        if (t > 0) ok = ok && mbar_wait_sleep(bar_o + 8 * half, (it - 1) & 1);
+        // (S was issued behind the O of the tile before, so that is there as well)
         ok = ok && mbar_wait_sleep(bar_s + 8 * half, it & 1);
         __syncwarp();
         tc_fence_after();
@@ -803,7 +803,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(bar_p + 8 * half);
       }
-      ok = ok && mbar_wait_sleep(bar_o + 8 * half, (it - 1) & 1);
+      ok = ok && mbar_wait_sleep(bar_o + 8 * half, seg & 1);
       m -= kPShift;       // (the numerators' reference)
       l_s[cg] = l;
       group_sync(id_pair, 64);
