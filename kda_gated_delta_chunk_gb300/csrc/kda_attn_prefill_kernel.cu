@@ -688,9 +688,10 @@ __global__ void __launch_bounds__(kThreadsP, 1)
         __syncwarp();
         tc_fence_after();
         uint32_t s[64];
+        uint32_t (&s_hi)[32] = *reinterpret_cast<uint32_t(*)[32]>(s + 32);
         tmem_ld32(ts + 64 * cg, *reinterpret_cast<uint32_t(*)[32]>(s));
-        tmem_ld32(ts + 64 * cg + 32, *reinterpret_cast<uint32_t(*)[32]>(s + 32));
-        tmem_wait_ld();
+        tmem_wait_ld_of(*reinterpret_cast<uint32_t(*)[32]>(s));
+        tmem_ld32(ts + 64 * cg + 32, s_hi);    // on its way while the first keys are worked on
         const float4* sc = reinterpret_cast<const float4*>(sm + kOffSc) + (it & 3) * 8 + 4 * cg;
         const bool masked = kTile - 1 > p_lo || (p.a.window > 0 && p.a.window <= p_hi);
         const bool scaled = kCap || masked;    // s holds the finished exponents (else raw products)
@@ -735,17 +736,20 @@ __global__ void __launch_bounds__(kThreadsP, 1)
           for (int g = 0; g < 4; ++g) {
             const float4 f = sc[g];
             const float mul = qmul * f.x;
+            if (g == 2) tmem_wait_ld_of(s_hi);
             mt = fmaxf(mt, fmaf(max_of(g), mul, f.y));
             sum = fmaf(p_of(g, mul, f.y - ref, pk), f.z, sum);
           }
           with_pair();
           keep = !__any_sync(0xffffffffu, mt > m + kSlack);
           if (keep) l = sum;
+        } else {
+          tmem_wait_ld_of(s_hi);
         }
         if (!keep) {
           if (ahead) {
             tmem_ld32(ts + 64 * cg, *reinterpret_cast<uint32_t(*)[32]>(s));
-            tmem_ld32(ts + 64 * cg + 32, *reinterpret_cast<uint32_t(*)[32]>(s + 32));
+            tmem_ld32(ts + 64 * cg + 32, s_hi);
             tmem_wait_ld();
             group_sync(id_pair, 64);
           } else if (scaled) {
