@@ -34,7 +34,6 @@ namespace {
 
 constexpr int kThreads = 192;
 constexpr int kStageBytes = 2 * kTile * kHeadDim;   // K and V
-constexpr int kOver = 3;                             // tiles' worth of time an item takes besides its tiles
 constexpr int kCached = 32;                          // sequences whose lengths a CTA keeps in shared memory
 constexpr float kPScale = 256.0f;                    // largest numerator, in the e4m3 operand
 
@@ -74,7 +73,8 @@ struct DecodeParams {
   CacheMaps maps;
   int group;                 // query heads of a kv head
   uint32_t group_magic;      // 65535 / group + 1 (div_small)
-  int wait;                  // the merge waits for the kernel before it (programmatic launch)
+  int wait;                  // wait for the kernel before (programmatic launch; kernel and merge)
+  int64_t least;             // units below which the prefill kernel takes these sequences too
   int min_rows, max_rows;
   PartDesc* desc;
   float* slots;
@@ -162,8 +162,9 @@ __global__ void __launch_bounds__(kThreads, 2)
     tmem_alloc(smem_u32(&misc->tmem), C::kTmemCols);
     tmem_relinquish();
   }
-  // (launched as a programmatic dependent: the work before this call is done from here on)
-  pdl_wait();
+  // (launched as a programmatic dependent: of the work before this call, or of the prefill kernel,
+  // which has waited for that and shares nothing with this one)
+  if (p.wait) pdl_wait();
   pdl_launch_dependents();
 
   // ---- this CTA's range: total tiles, then the sequence its first tile lies in
@@ -189,6 +190,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
   for (int w = 0; w < kThreads / 32; ++w) total += misc->part[w];
   __syncthreads();
+  if (total < p.least) total = 0;
   Walk walk;
   // (no more ranges than tiles: between two CTAs of an item there is none without a part)
   const int ranges = (int)min((long long)gridDim.x, total);
@@ -658,6 +660,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (!ok) part.parts = 0;
     if (tid == 0) p.desc[blockIdx.x] = part;
   }
+  // (beside the prefill kernel: this grid does not end before that one)
+  if (blockIdx.x == 0 && warp == 0) pdl_wait();
   tc_fence_before();
   __syncthreads();
   if (warp == 5) {
@@ -806,9 +810,10 @@ size_t decode_workspace_bytes(int sms) {
 }
 
 namespace {
-void make_params(const AttnParams& a, int max_rows, void* work, int sms, DecodeParams* d) {
+void make_params(const AttnParams& a, int max_rows, bool wait, void* work, int sms, DecodeParams* d) {
   d->a = a;
-  d->wait = 0;
+  d->wait = wait;
+  d->least = 0;
   d->group = a.heads / a.c.kv_heads;
   d->group_magic = 65535u / (uint32_t)d->group + 1;
   d->min_rows = 1;
@@ -819,11 +824,12 @@ void make_params(const AttnParams& a, int max_rows, void* work, int sms, DecodeP
 }  // namespace
 
 // The operands are padded to 8, 16 or 32 rows.
-cudaError_t launch_attn_decode(const AttnParams& a, const CacheMaps& maps, int max_rows, void* work,
-                               int sms, cudaStream_t stream) {
+cudaError_t launch_attn_decode(const AttnParams& a, const CacheMaps& maps, int max_rows, int64_t least,
+                               bool beside, void* work, int sms, cudaStream_t stream) {
   DecodeParams d;
-  make_params(a, max_rows, work, sms, &d);
+  make_params(a, max_rows, !beside, work, sms, &d);
   d.maps = maps;
+  d.least = least;
   const bool cap = a.softcap > 0.0f;
   if (max_rows <= 8) return cap ? launch_nr<8, true>(d, sms, stream) : launch_nr<8, false>(d, sms, stream);
   if (max_rows <= 16) return cap ? launch_nr<16, true>(d, sms, stream) : launch_nr<16, false>(d, sms, stream);
@@ -833,8 +839,7 @@ cudaError_t launch_attn_decode(const AttnParams& a, const CacheMaps& maps, int m
 cudaError_t launch_attn_decode_merge(const AttnParams& a, int max_rows, void* work, int sms, bool wait,
                                      cudaStream_t stream) {
   DecodeParams d = {};
-  make_params(a, max_rows, work, sms, &d);
-  d.wait = wait;
+  make_params(a, max_rows, wait, work, sms, &d);
   return max_rows <= 8    ? launch_merge<8>(d, sms, stream)
          : max_rows <= 16 ? launch_merge<16>(d, sms, stream)
                           : launch_merge<32>(d, sms, stream);

@@ -6,6 +6,13 @@ namespace attn {
 namespace {
 
 constexpr int kDecodeRows = 32;    // query rows per kv head that the decode kernel takes at most
+// Units (key tiles, and kOver an item) of such sequences per SM below which the prefill kernel takes
+// them with its own.  A tile of few rows takes it over twice the decode kernel's time, but a decode
+// kernel on the same SMs costs about ten microseconds of launch, start and end.  16 heads over 4, with one
+// prefill of 1024 tokens | four over 4096 keys each, decode kernel against prefill kernel: 16
+// sequences of 4096 tokens (14.7 units per SM) 63.6 : 57.8 us | 153.5 : 144.3 us, 32 (29.5 units)
+// 80.9 : 88.5 | 169.2 : 166.0, 64 (59 units) 113.7 : 139.8 | 202.0 : 210.8.
+constexpr int kFewUnits = 20;
 
 int device_sms() {
   int dev = 0, sms = 0;
@@ -36,11 +43,12 @@ size_t attn_workspace_bytes(int32_t num_seqs, int32_t heads, int32_t kv_heads, i
 }
 
 // Sequences with at most 32 rows per kv head take the decode kernel, the others of the same call
-// the prefill kernel.  A launch is left out when the sizes say that no sequence can need it: none
-// can have more rows than max_q_len gives, and with num_seqs * max_q_len tokens in the batch all
-// have that many.  With both, the prefill kernel is launched as the decode kernel's dependent and
-// waits for nothing (its CTAs start as SMs come free), the first merge is an ordinary launch
-// behind both, and the second one runs beside it.
+// the prefill kernel, which takes the first ones too when they are few (both kernels find that out
+// from the lengths on the device).  A launch is left out when the sizes say that no sequence can
+// need it: none can have more rows than max_q_len gives, and with num_seqs * max_q_len tokens in
+// the batch all have that many.  With both, the decode kernel is launched as the prefill kernel's
+// dependent and waits for nothing (its CTAs start as SMs come free), the first merge is an ordinary
+// launch behind both, and the second one runs beside it.
 cudaError_t launch_attn(const AttnParams& p, int sms, cudaStream_t stream) {
   const int group = p.heads / p.c.kv_heads;
   const int64_t rows = (int64_t)p.max_q_len * group;
@@ -52,10 +60,11 @@ cudaError_t launch_attn(const AttnParams& p, int sms, cudaStream_t stream) {
   CacheMaps maps;
   if (!make_cache_maps(p.c, &maps)) return cudaErrorNotSupported;
   cudaError_t e = cudaSuccess;
-  if (few > 0 && (e = launch_attn_decode(p, maps, few, work, sms, stream)) != cudaSuccess) return e;
-  if (many && (e = launch_attn_prefill(p, maps, few + 1, work2, sms, few > 0, stream)) != cudaSuccess) return e;
+  const int64_t least = many && few > 0 ? (int64_t)kFewUnits * sms : 0;
+  if (many && (e = launch_attn_prefill(p, maps, few, least, work2, sms, stream)) != cudaSuccess) return e;
+  if (few > 0 && (e = launch_attn_decode(p, maps, few, least, many, work, sms, stream)) != cudaSuccess) return e;
   if (few > 0 && (e = launch_attn_decode_merge(p, few, work, sms, !many, stream)) != cudaSuccess) return e;
-  return many ? launch_attn_prefill_merge(p, few + 1, work2, sms, few == 0, stream) : cudaSuccess;
+  return many ? launch_attn_prefill_merge(p, work2, sms, few == 0, stream) : cudaSuccess;
 }
 
 }  // namespace attn

@@ -17,7 +17,7 @@
 // run in the order they are issued, so S(i+1) of a half may follow its O += P(i) V, whose P it
 // overwrites, without a wait.  Key tiles of all (sequence, kv head, row tile) items are laid end
 // to end and cut into one equal range per CTA, one CTA per SM (as in the decode kernel; an item
-// counts kOverP tiles more), and a dependent kernel merges the items that were cut.
+// counts kOver tiles more), and a dependent kernel merges the items that were cut.
 //
 // Warps: 0-7 / 8-15 softmax of the halves, 16-19 the widening of V, 20 the TMA producer, 21 the MMA
 // issuer, 22 the scheduler, which walks the CTA's range and hands its segments to the others
@@ -37,7 +37,6 @@ constexpr int kRowsP = 256;
 constexpr int kKStages = 3, kVStages = 2, kSegs = 4;
 constexpr int kSoftWarps = 16, kRegsSoftmax = 104, kRegsOther = 32;
 constexpr int kRegsNeeded = 32 * (kSoftWarps * kRegsSoftmax + (kThreadsP / 32 - kSoftWarps) * kRegsOther);
-constexpr int kOverP = 3;                   // tiles' worth of time an item takes besides its tiles
 constexpr float kSlack = 8.0f;              // log2 growth of the maximum before O is rescaled
 constexpr float kPShift = 7.0f;             // log2 of the numerator at the maximum: at most 2^15 with the slack
 
@@ -54,7 +53,7 @@ constexpr int kOffSeg = kOffL + 8 * kRowsP;                 // Segment [kSegs]
 constexpr int kOffBars = kOffSeg + 64 * 4;
 constexpr int kNumBars = 2 * kKStages + 2 * kVStages + 2 * 7 + 4 + 2 * kSegs;
 constexpr int kOffMiscP = kOffBars + 8 * kNumBars;
-constexpr int kSmemP = kOffMiscP + 320 + 1024;
+constexpr int kSmemP = kOffMiscP + 384 + 1024;
 static_assert(kSmemP <= 227 * 1024, "shared memory");
 
 // tensor memory columns
@@ -72,7 +71,8 @@ struct PrefillParams {
   int group;                 // query heads of a kv head
   uint32_t group_magic;      // 65535 / group + 1 (div_small)
   int wait;                  // wait for the kernel before this one (programmatic launch)
-  int min_rows, tokens;      // tokens: new tokens per row tile (256 / group)
+  int few, tokens;           // rows of the decode kernel's sequences at most; new tokens per row tile (256 / group)
+  int64_t least;             // units of those below which this kernel takes them too
   PartDescP* desc;
   float* slots;
 };
@@ -93,10 +93,11 @@ __device__ __forceinline__ ItemP item_of(int q_len, int len, int rt, int tokens,
   return it;
 }
 
-// The walk over a CTA's range, in units: an item has kOverP of them, then one per key tile.
+// The walk over a CTA's range, in units: an item has kOver of them, then one per key tile.
 struct WalkP {
   int64_t pos, end;
   int n, h, rt, off;         // the next item and the units of it that lie before this range
+  int min_rows;              // sequences of fewer rows are the decode kernel's
   SeqInfo s;
   ItemP it;
   int a, b;                  // segment: tiles [a, b) of the item
@@ -112,18 +113,18 @@ struct WalkP {
         }
         int err;
         if (++n >= p.a.num_seqs) return false;             // (lengths that changed under the kernel)
-        s = seq_info(p.a, n, p.min_rows, 0x7fffffff, &err);
+        s = seq_info(p.a, n, min_rows, 0x7fffffff, &err);
         h = rt = 0;
       }
       it = item_of(s.q_len, s.len, rt, p.tokens, p.a.window);
       ch = h;
       crt = rt++;
-      const int size = it.tiles + kOverP, o = off, o1 = (int)min((int64_t)size, o + (end - pos));
+      const int size = it.tiles + kOver, o = off, o1 = (int)min((int64_t)size, o + (end - pos));
       last = pos - o + size - 1;
       pos += o1 - o;
       off = 0;
-      a = max(0, o - kOverP);
-      b = o1 - kOverP;
+      a = max(0, o - kOver);
+      b = o1 - kOver;
       if (b > a) return true;                              // (else the range ends before its first tile)
     }
     return false;
@@ -160,12 +161,13 @@ __global__ void __launch_bounds__(kThreadsP, 1)
   struct Misc {
     long long part[kThreadsP / 32];
     long long rest;          // first tile's place in its sequence
+    int few[kThreadsP / 32];
     int start_n, poison[8];
     int start_h, start_rt, start_off;
     uint32_t tmem;
   };
   Misc* misc = reinterpret_cast<Misc*>(sm + kOffMiscP);
-  static_assert(sizeof(Misc) <= 320, "misc");
+  static_assert(sizeof(Misc) <= 384, "misc");
   const int hk = p.a.c.kv_heads, N = p.a.num_seqs, P = p.a.c.page_size;
   const int G = p.group;
   const uint32_t gm = p.group_magic;
@@ -210,13 +212,16 @@ __global__ void __launch_bounds__(kThreadsP, 1)
 
   // ---- this CTA's range.  A thread reads its sequence's lengths; the warp adds up the row
   // tiles of each of its sequences together.
-  auto cost = [&](int n, bool report) -> long long {     // key tiles of sequence n (all heads)
+  auto cost = [&](int n, bool report, int& few) -> long long {   // units of sequence n (all heads)
     int q_len = 0, len = 0;
+    few = 0;                 // ... of one that the decode kernel may take
     if (n < N) {
       int err;
-      const SeqInfo s = seq_info(p.a, n, p.min_rows, 0x7fffffff, &err);
+      const SeqInfo s = seq_info(p.a, n, 1, 0x7fffffff, &err);
       if (err != KDA_OK && report && blockIdx.x == 0) record_error(p.a.status, err, 331);
-      if (s.tiles) {
+      if (s.tiles && (int64_t)s.q_len * G <= p.few) {
+        few = (int)min((long long)(s.tiles + kOver) * hk, 1ll << 24);   // (as the decode kernel counts)
+      } else if (s.tiles) {
         q_len = s.q_len;
         len = s.len;
       }
@@ -225,14 +230,14 @@ __global__ void __launch_bounds__(kThreadsP, 1)
     long long mine = 0;
     const int rts = (q_len + p.tokens - 1) / p.tokens;
     if (rts <= 32)
-      for (int rt = 0; rt < rts; ++rt) mine += item_of(q_len, len, rt, p.tokens, p.a.window).tiles + kOverP;
+      for (int rt = 0; rt < rts; ++rt) mine += item_of(q_len, len, rt, p.tokens, p.a.window).tiles + kOver;
     uint32_t todo = __ballot_sync(0xffffffffu, rts > 32);
     while (todo) {
       const int k = __ffs(todo) - 1;
       todo &= todo - 1;
       const int ql = __shfl_sync(0xffffffffu, q_len, k), ln = __shfl_sync(0xffffffffu, len, k);
       int sum = 0;
-      for (int rt = lane; rt * p.tokens < ql; rt += 32) sum += item_of(ql, ln, rt, p.tokens, p.a.window).tiles + kOverP;
+      for (int rt = lane; rt * p.tokens < ql; rt += 32) sum += item_of(ql, ln, rt, p.tokens, p.a.window).tiles + kOver;
       // (millions of new tokens over as many keys: the warp's sum passes 31 bits)
       const long long all = __reduce_add_sync(0xffffffffu, (unsigned)sum & 0xffffu) +
                             ((long long)__reduce_add_sync(0xffffffffu, (unsigned)sum >> 16) << 16);
@@ -242,20 +247,36 @@ __global__ void __launch_bounds__(kThreadsP, 1)
     return mine;
   };
   long long mine = 0, first = 0;
+  int few = 0, first_few = 0;
   for (int n0 = 0; n0 < N; n0 += kThreadsP) {
-    const long long w = cost(n0 + tid, true);
-    if (n0 == 0) first = w;
+    int f;
+    const long long w = cost(n0 + tid, true, f);
+    if (n0 == 0) {
+      first = w;
+      first_few = f;
+    }
     mine += w;
+    few = min(few + f, 1 << 24);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-  if (lane == 0) misc->part[warp] = mine;
+  few = __reduce_add_sync(0xffffffffu, few);
+  if (lane == 0) {
+    misc->part[warp] = mine;
+    misc->few[warp] = few;
+  }
   __syncthreads();
-  long long total = 0;
+  long long total = 0, total_few = 0;
 #pragma unroll
-  for (int w = 0; w < kThreadsP / 32; ++w) total += misc->part[w];
+  for (int w = 0; w < kThreadsP / 32; ++w) {
+    total += misc->part[w];
+    total_few += misc->few[w];
+  }
   __syncthreads();
+  const bool all = total_few < p.least;
+  if (all) total += total_few;
   WalkP walk;
+  walk.min_rows = all ? 1 : p.few + 1;
   // (no more ranges than units: between two CTAs of an item there is none without a part)
   const int ranges = (int)min((long long)gridDim.x, total);
   walk.pos = walk.end = 0;
@@ -266,7 +287,9 @@ __global__ void __launch_bounds__(kThreadsP, 1)
   if (walk.pos < walk.end) {
     long long before = 0;
     for (int n0 = 0; n0 < N; n0 += kThreadsP) {
-      const long long w = n0 == 0 ? first : cost(n0 + tid, false);
+      int f = first_few;
+      long long w = n0 == 0 ? first : cost(n0 + tid, false, f);
+      if (all) w += f;
       long long inc = w;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -304,13 +327,13 @@ __global__ void __launch_bounds__(kThreadsP, 1)
     walk.n = misc->start_n;
     walk.h = misc->start_h;
     int err;
-    walk.s = seq_info(p.a, walk.n, p.min_rows, 0x7fffffff, &err);
+    walk.s = seq_info(p.a, walk.n, walk.min_rows, 0x7fffffff, &err);
     if (warp == 0) {     // the row tile: 32 at a time
       long long left = misc->rest;
       for (int r0 = 0;; r0 += 32) {
         const int rt = r0 + lane;
         const int c = rt * p.tokens < walk.s.q_len
-                          ? item_of(walk.s.q_len, walk.s.len, rt, p.tokens, p.a.window).tiles + kOverP : 0;
+                          ? item_of(walk.s.q_len, walk.s.len, rt, p.tokens, p.a.window).tiles + kOver : 0;
         int inc = c;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -987,10 +1010,11 @@ size_t prefill_workspace_bytes(int sms) {
 }
 
 namespace {
-void make_params(const AttnParams& a, int min_rows, void* work, int sms, PrefillParams* d) {
+void make_params(const AttnParams& a, int few, int64_t least, void* work, int sms, PrefillParams* d) {
   d->a = a;
   d->wait = 0;
-  d->min_rows = min_rows;
+  d->few = few;
+  d->least = least;
   d->group = a.heads / a.c.kv_heads;
   d->group_magic = 65535u / (uint32_t)d->group + 1;
   d->tokens = kRowsP / d->group;
@@ -999,19 +1023,19 @@ void make_params(const AttnParams& a, int min_rows, void* work, int sms, Prefill
 }
 }  // namespace
 
-cudaError_t launch_attn_prefill(const AttnParams& a, const CacheMaps& maps, int min_rows, void* work,
-                                int sms, bool beside, cudaStream_t stream) {
+cudaError_t launch_attn_prefill(const AttnParams& a, const CacheMaps& maps, int few, int64_t least,
+                                void* work, int sms, cudaStream_t stream) {
   PrefillParams d;
-  make_params(a, min_rows, work, sms, &d);
+  make_params(a, few, least, work, sms, &d);
   d.maps = maps;
-  d.wait = !beside;
+  d.wait = 1;
   return a.softcap > 0.0f ? launch_cap<true>(d, sms, stream) : launch_cap<false>(d, sms, stream);
 }
 
-cudaError_t launch_attn_prefill_merge(const AttnParams& a, int min_rows, void* work, int sms, bool wait,
+cudaError_t launch_attn_prefill_merge(const AttnParams& a, void* work, int sms, bool wait,
                                       cudaStream_t stream) {
   PrefillParams d = {};
-  make_params(a, min_rows, work, sms, &d);
+  make_params(a, 0, 0, work, sms, &d);
   d.wait = wait;
   return launch(kda_attn_prefill_merge_kernel, dim3((unsigned)sms, kRowsP / kMergeRows),
                 dim3(32 * kMergeRows), 0, true, stream, d);

@@ -13,6 +13,7 @@ namespace attn {
 using namespace sm100;
 
 constexpr int kTile = 128;              // keys of a tile
+constexpr int kOver = 3;                // units (tiles' worth of time) an item takes besides its tiles
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -182,20 +183,22 @@ struct CacheMaps {
 bool make_cache_maps(const CacheView& c, CacheMaps* m);
 
 // ------------------------------------------------------------ the kernels of a call
-// Sequences with at most max_rows (at most 32) rows: new tokens x heads per kv head.
+// Sequences with at most max_rows (at most 32) rows: new tokens x heads per kv head, unless they
+// add up to fewer than `least` units.  `beside`: launched as the programmatic dependent of the
+// prefill kernel, which it shares nothing with.
 size_t decode_workspace_bytes(int sms);
-cudaError_t launch_attn_decode(const AttnParams& p, const CacheMaps& maps, int max_rows, void* work,
-                               int sms, cudaStream_t stream);
-// Sequences with at least min_rows of them (heads per kv head at most 256).  `beside`: as the
-// programmatic dependent of the decode kernel, which it shares nothing with.
+cudaError_t launch_attn_decode(const AttnParams& p, const CacheMaps& maps, int max_rows, int64_t least,
+                               bool beside, void* work, int sms, cudaStream_t stream);
+// Sequences with more than `few` rows, and the others when those add up to fewer than `least`
+// units (heads per kv head at most 256).
 size_t prefill_workspace_bytes(int sms);
-cudaError_t launch_attn_prefill(const AttnParams& p, const CacheMaps& maps, int min_rows, void* work,
-                                int sms, bool beside, cudaStream_t stream);
+cudaError_t launch_attn_prefill(const AttnParams& p, const CacheMaps& maps, int few, int64_t least,
+                                void* work, int sms, cudaStream_t stream);
 // The parts of items that the cut divided, merged.  `wait`: launched as the programmatic dependent
 // of the kernel whose parts they are, for which the merge waits.
 cudaError_t launch_attn_decode_merge(const AttnParams& p, int max_rows, void* work, int sms, bool wait,
                                      cudaStream_t stream);
-cudaError_t launch_attn_prefill_merge(const AttnParams& p, int min_rows, void* work, int sms, bool wait,
+cudaError_t launch_attn_prefill_merge(const AttnParams& p, void* work, int sms, bool wait,
                                       cudaStream_t stream);
 
 // ------------------------------------------------------------ one sequence of a batch

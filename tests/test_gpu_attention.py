@@ -333,6 +333,19 @@ def test_many_sequences(N, long):
     check(d, out, lse)
 
 
+@pytest.mark.parametrize("softcap", [0.0, 15.0])
+@pytest.mark.parametrize("short_kv", [2300, 40], ids=["both kernels", "one kernel"])
+def test_short_sequences_beside_long_ones(short_kv, softcap):
+    """Few rows a sequence, in a call that has long queries too: with enough keys in all these go
+    to the kernel for few rows, else to the one for many."""
+    q_lens = ([1, 2, 8, 1, 0, 1] * 8) + [100] + [1, 3] + [70]
+    kv_lens = [short_kv + 3 * n for n in range(48)] + [500, 0, 2, 70]
+    d = make(q_lens, kv_lens, 16, 4, 64, seed=5)
+    out, lse, status = launch(d, softcap=softcap)
+    assert status == kda.OK
+    check(d, out, lse, softcap=softcap)
+
+
 def test_device_errors_skip_and_report():
     for q_lens, kv_lens in (([1, 1], [100, 200]), ([100, 120], [100, 200])):
         for broken in ("page", "long", "more"):
