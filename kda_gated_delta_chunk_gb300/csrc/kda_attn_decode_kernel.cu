@@ -73,7 +73,7 @@ struct DecodeParams {
   CacheMaps maps;
   int group;                 // query heads of a kv head
   uint32_t group_magic;      // 65535 / group + 1 (div_small)
-  int wait;                  // wait for the kernel before (programmatic launch; kernel and merge)
+  int wait;                  // wait for the kernel before this one (programmatic launch)
   int64_t least;             // units below which the prefill kernel takes these sequences too
   int min_rows, max_rows;
   PartDesc* desc;
@@ -682,7 +682,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
   constexpr int kPerRow = 64 / NR;     // warps of a row
   __shared__ float4 acc_s[kMergeWarps][32];
   __shared__ float2 ml_s[kMergeWarps];
-  if (p.wait) pdl_wait();
+  pdl_wait();
   pdl_launch_dependents();
   const int4 d4 = *reinterpret_cast<const int4*>(p.desc + blockIdx.x);
   const PartDesc d = {d4.x, d4.y, d4.z, d4.w};
@@ -777,7 +777,7 @@ cudaError_t launch_nr(const DecodeParams& d, int sms, cudaStream_t stream) {
 template <int NR>
 cudaError_t launch_merge(const DecodeParams& d, int sms, cudaStream_t stream) {
   return launch(kda_attn_merge_kernel<NR>, dim3((unsigned)decode_ctas(sms), 8), dim3(32 * kMergeWarps),
-                0, d.wait != 0, stream, d);
+                0, true, stream, d);
 }
 
 }  // namespace
@@ -836,10 +836,10 @@ cudaError_t launch_attn_decode(const AttnParams& a, const CacheMaps& maps, int m
   return cap ? launch_nr<32, true>(d, sms, stream) : launch_nr<32, false>(d, sms, stream);
 }
 
-cudaError_t launch_attn_decode_merge(const AttnParams& a, int max_rows, void* work, int sms, bool wait,
+cudaError_t launch_attn_decode_merge(const AttnParams& a, int max_rows, void* work, int sms,
                                      cudaStream_t stream) {
   DecodeParams d = {};
-  make_params(a, max_rows, wait, work, sms, &d);
+  make_params(a, max_rows, true, work, sms, &d);
   return max_rows <= 8    ? launch_merge<8>(d, sms, stream)
          : max_rows <= 16 ? launch_merge<16>(d, sms, stream)
                           : launch_merge<32>(d, sms, stream);

@@ -47,8 +47,9 @@ size_t attn_workspace_bytes(int32_t num_seqs, int32_t heads, int32_t kv_heads, i
 // from the lengths on the device).  A launch is left out when the sizes say that no sequence can
 // need it: none can have more rows than max_q_len gives, and with num_seqs * max_q_len tokens in
 // the batch all have that many.  With both, the decode kernel is launched as the prefill kernel's
-// dependent and waits for nothing (its CTAs start as SMs come free), the first merge is an ordinary
-// launch behind both, and the second one runs beside it.
+// dependent and waits for nothing but, at its end, for the prefill kernel (its CTAs start as SMs
+// come free), the first merge waits for the decode kernel and so for both, and the second one
+// runs beside it.
 cudaError_t launch_attn(const AttnParams& p, int sms, cudaStream_t stream) {
   const int group = p.heads / p.c.kv_heads;
   const int64_t rows = (int64_t)p.max_q_len * group;
@@ -63,7 +64,7 @@ cudaError_t launch_attn(const AttnParams& p, int sms, cudaStream_t stream) {
   const int64_t least = many && few > 0 ? (int64_t)kFewUnits * sms : 0;
   if (many && (e = launch_attn_prefill(p, maps, few, least, work2, sms, stream)) != cudaSuccess) return e;
   if (few > 0 && (e = launch_attn_decode(p, maps, few, least, many, work, sms, stream)) != cudaSuccess) return e;
-  if (few > 0 && (e = launch_attn_decode_merge(p, few, work, sms, !many, stream)) != cudaSuccess) return e;
+  if (few > 0 && (e = launch_attn_decode_merge(p, few, work, sms, stream)) != cudaSuccess) return e;
   return many ? launch_attn_prefill_merge(p, work2, sms, few == 0, stream) : cudaSuccess;
 }
 

@@ -194,9 +194,10 @@ cudaError_t launch_attn_decode(const AttnParams& p, const CacheMaps& maps, int m
 size_t prefill_workspace_bytes(int sms);
 cudaError_t launch_attn_prefill(const AttnParams& p, const CacheMaps& maps, int few, int64_t least,
                                 void* work, int sms, cudaStream_t stream);
-// The parts of items that the cut divided, merged.  `wait`: launched as the programmatic dependent
-// of the kernel whose parts they are, for which the merge waits.
-cudaError_t launch_attn_decode_merge(const AttnParams& p, int max_rows, void* work, int sms, bool wait,
+// The parts of items that the cut divided, merged: as the programmatic dependent of the kernel
+// before (the decode kernel; with `wait` the prefill kernel, else the merge of the decode kernel's,
+// beside which this one runs).
+cudaError_t launch_attn_decode_merge(const AttnParams& p, int max_rows, void* work, int sms,
                                      cudaStream_t stream);
 cudaError_t launch_attn_prefill_merge(const AttnParams& p, void* work, int sms, bool wait,
                                       cudaStream_t stream);
