@@ -503,8 +503,8 @@ __global__ void __launch_bounds__(kThreads, 2)
           const float m[4] = {m4.x, m4.y, m4.z, m4.w};
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float s = x[r + e] * (m[e] * ks);
-            x[r + e] = (kCap ? cap_score(s, cap2, cap1) : s) + lvs;
+            if (kCap) x[r + e] = cap_score(x[r + e], m[e] * ks * cap2, -2.0f * cap1, cap1 + lvs);
+            else x[r + e] = x[r + e] * (m[e] * ks) + lvs;
           }
         }
         bool hidden_nan = false;

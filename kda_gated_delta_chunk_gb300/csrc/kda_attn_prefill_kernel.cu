@@ -783,12 +783,12 @@ __global__ void __launch_bounds__(kThreadsP, 1)
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
               const float4 f = sc[g];
-              const float mul = qmul * f.x;
+              const float mul = qmul * f.x * (kCap ? cap2 : 1.0f), add = kCap ? cap1 + f.y : f.y;
               const uint32_t bits = (uint32_t)(see >> (32 * (g >> 1))) >> (16 * (g & 1));
 #pragma unroll
               for (int e = 0; e < 16; ++e) {
                 float x = __uint_as_float(s[16 * g + e]);
-                x = kCap ? cap_score(x * mul, cap2, cap1) + f.y : fmaf(x, mul, f.y);
+                x = kCap ? cap_score(x, mul, -2.0f * cap1, add) : fmaf(x, mul, add);
                 if (!((bits >> e) & 1)) x = -INFINITY;
                 mt = fmaxf(mt, x);
                 s[16 * g + e] = __float_as_uint(x);

@@ -58,9 +58,15 @@ __device__ __forceinline__ float warp_max(float x) {
   asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
   return y;
 }
-// cap * tanh(x / cap) * log2(e), to fp32's absolute precision: tanh y = 1 - 2 / (1 + e^(2 y)).
-__device__ __forceinline__ float cap_score(float x, float two_over_cap_log2e, float cap_log2e) {
-  return cap_log2e - __fdividef(2.0f * cap_log2e, 1.0f + ex2(x * two_over_cap_log2e));
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// cap * tanh(x / cap) * log2(e) + a to fp32's absolute precision, from tanh y = 1 - 2 / (1 + e^(2 y)):
+// m2cap = -2 cap log2(e), to_e = 2 log2(e) / cap (a factor of x may be in it), cap_a = cap log2(e) + a.
+__device__ __forceinline__ float cap_score(float x, float to_e, float m2cap, float cap_a) {
+  return fmaf(m2cap, rcp(1.0f + ex2(x * to_e)), cap_a);
 }
 
 // D[tmem] (+)= A[smem] * B[smem]^T, kind::f8f6f4 with e4m3 operands, fp32 accumulate; K = 32.
