@@ -2,15 +2,18 @@
 
 One translation unit per .cu file, compiled in parallel, then linked into a
 shared library with the CUDA runtime linked statically (the library needs no
-libcuda at load time; driver entry points are looked up at run time).
+libcuda at load time; driver entry points are looked up at run time).  Beside it,
+the marshalling of the full-attention layer's calls, compiled against the torch in use.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
 import os
+import re
 import shutil
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -41,6 +44,36 @@ def _compile(src: str, extra: list, build_dir: str = BUILD) -> str:
 STAMPS_LIB = os.path.join(PKG, "libkda_stamps.so")
 
 
+BINDING_SRC = os.path.join(CSRC, "kda_layer_binding.cpp")
+
+
+def binding_path() -> str:
+    """The marshalling module of ``layer.py``, one per torch version (its C++ ABI)."""
+    import torch
+    return os.path.join(PKG, "_layer_" + re.sub(r"\W+", "_", torch.__version__) + ".so")
+
+
+def build_binding(force: bool = False) -> str:
+    """Build (if stale) and return the path of the marshalling module."""
+    import torch
+    path = binding_path()
+    deps = [BINDING_SRC] + glob.glob(os.path.join(INCLUDE, "*.h"))
+    if not force and os.path.exists(path) and os.path.getmtime(path) >= max(map(os.path.getmtime, deps)):
+        return path
+    base = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    dirs = (INCLUDE, sysconfig.get_paths()["include"], os.path.join(base, "include"),
+            os.path.join(cuda, "include"))
+    libs = os.path.join(base, "lib")
+    tmp = path + f".tmp{os.getpid()}"
+    subprocess.run(["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+                    f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+                    *(x for d in dirs for x in ("-isystem", d)), BINDING_SRC, "-o", tmp, "-L", libs, "-lc10",
+                    "-lc10_cuda", "-ltorch_cpu", "-ltorch_python", f"-Wl,-rpath,{libs}"], check=True)
+    os.replace(tmp, path)
+    return path
+
+
 def build(force: bool = False, verbose_ptxas: bool = False, stamps: bool = False) -> str:
     """Build (if stale) and return the path of libkda.so (or of the stamps variant)."""
     lib = STAMPS_LIB if stamps else LIB
@@ -48,6 +81,8 @@ def build(force: bool = False, verbose_ptxas: bool = False, stamps: bool = False
     os.makedirs(bdir, exist_ok=True)
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
     deps = srcs + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(INCLUDE, "*.h"))
+    if not stamps:
+        build_binding(force)
     if not force and os.path.exists(lib):
         if os.path.getmtime(lib) >= max(os.path.getmtime(d) for d in deps):
             return lib
