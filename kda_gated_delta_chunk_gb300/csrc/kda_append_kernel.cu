@@ -23,8 +23,8 @@
 // the token's table row in registers.  A lane holds both channels of its pairs -- four and four
 // half the rotated part apart, or eight in a row -- so that the rotation needs no exchange.
 // Bound by memory in a prefill, by the chain of dependent loads in a decode step: 8 x 2048 tokens of
-// 16 heads over 4 in 36.4 us (5.3 TB/s), 16 ragged sequences of up to 1000 in pages of 16 in 20.0 us
-// (4.0 TB/s), 64 x 1 token of 32 heads over 8 in 8.0 us.
+// 16 heads over 4 in 36.4 us (5.3 TB/s), 16 ragged sequences of up to 1000 in pages of 16 in 19.5 us
+// (4.1 TB/s), 64 x 1 token of 32 heads over 8 in 7.4 us.
 #include "kda_attn.cuh"
 
 namespace kda {
@@ -151,10 +151,15 @@ __global__ void __launch_bounds__(kThreads, 65536 / kRegs / kThreads)
     for (int w = 0; w < warps; ++w) total += sum_s[w];
     total *= 2 * hk;
     __syncthreads();
-    long long u = (long long)blockIdx.x * total / page_ctas;
-    const long long u_end = (long long)(blockIdx.x + 1) * total / page_ctas;
+    // (64-bit divisions only where they are needed: they would be half of a decode step's instructions)
+    const bool small = total <= (long long)(0xffffffffu / (unsigned)page_ctas);
+    auto share = [&](unsigned i) -> long long {
+      return small ? (long long)(i * (unsigned)total / (unsigned)page_ctas) : (long long)i * total / page_ctas;
+    };
+    long long u = share(blockIdx.x);
+    const long long u_end = share(blockIdx.x + 1);
     if (u >= u_end) return;
-    const long long page0 = u / (2 * hk);
+    const long long page0 = small ? (unsigned)u / (unsigned)(2 * hk) : u / (2 * hk);
     long long before = 0;
     for (int n0 = 0; n0 < N && before <= page0; n0 += blockDim.x) {
       const long long w = n0 == 0 ? first : (n0 + tid < N ? seq_pages(p, n0 + tid, false).pages : 0);
@@ -177,7 +182,7 @@ __global__ void __launch_bounds__(kThreads, 65536 / kRegs / kThreads)
     }
     int n = n_s;
     SeqPages q = seq_pages(p, n, false);
-    int blk = (int)(page0 - first_s), unit = (int)(u % (2 * hk));   // page of the sequence, unit of the page
+    int blk = (int)(page0 - first_s), unit = (int)(u - page0 * (2 * hk));   // page of the sequence, unit of the page
     // ---- the units: keys or values of one (page, kv head)
     for (uint32_t par = 0; u < u_end; ++u, par ^= 1) {
       while (blk >= q.pages) {
@@ -213,30 +218,38 @@ __global__ void __launch_bounds__(kThreads, 65536 / kRegs / kThreads)
       const float old = s0 > 0 ? *scale_p : 0.0f;
       float x[kRows][8];
       float top = 0.0f;
+      bool some = kHeads > 2;       // of this warp's rows are new (few tokens: mostly none)
+      if (kHeads <= 2) {
 #pragma unroll
-      for (int i = 0; i < kRows; ++i) {
-        const int row = grp + i * groups;
-        unpack_row(raw[i], x[i]);
-        if (!is_v && p.rot_dim && row >= s0 && row < s1) {
-          const int64_t pos = p.positions ? (int64_t)p.positions[t_row0 + row] : (int64_t)b * P + row;
-          if (pos >= 0 && pos < p.rope_rows)
-            rotate8<kInter>(x[i], ln, load_turn(p.rope + pos * p.rot_dim, p.rot_dim, ln));
-          else if (lane16 == 0)   // the row is stored unrotated
-            record_error(p.status, KDA_ERR_BAD_CACHE_INDEX, 204);
+        for (int i = 0; i < kRows; ++i) some = some || (grp + i * groups >= s0 && grp + i * groups < s1);
+        some = __any_sync(0xffffffffu, some);
+      }
+      if (some) {
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+          const int row = grp + i * groups;
+          unpack_row(raw[i], x[i]);
+          if (!is_v && p.rot_dim && row >= s0 && row < s1) {
+            const int64_t pos = p.positions ? (int64_t)p.positions[t_row0 + row] : (int64_t)b * P + row;
+            if (pos >= 0 && pos < p.rope_rows)
+              rotate8<kInter>(x[i], ln, load_turn(p.rope + pos * p.rot_dim, p.rot_dim, ln));
+            else if (lane16 == 0)   // the row is stored unrotated
+              record_error(p.status, KDA_ERR_BAD_CACHE_INDEX, 204);
+          }
+#pragma unroll
+          for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(x[i][e]));
+        }
+        if (top > 3.402823466e38f) {   // an infinity: the maximum of the finite ones
+          top = 0.0f;
+#pragma unroll
+          for (int i = 0; i < kRows; ++i)
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              if (fabsf(x[i][e]) <= 3.402823466e38f) top = fmaxf(top, fabsf(x[i][e]));
         }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(x[i][e]));
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
       }
-      if (top > 3.402823466e38f) {   // an infinity: the maximum of the finite ones
-        top = 0.0f;
-#pragma unroll
-        for (int i = 0; i < kRows; ++i)
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (fabsf(x[i][e]) <= 3.402823466e38f) top = fmaxf(top, fabsf(x[i][e]));
-      }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
       if ((tid & 31) == 0) top_s[par][warp] = top;
       __syncthreads();              // (the other parity's readers are past the barrier before this)
       for (int w = 0; w < warps; ++w) top = fmaxf(top, top_s[par][w]);
@@ -246,7 +259,7 @@ __global__ void __launch_bounds__(kThreads, 65536 / kRegs / kThreads)
 #pragma unroll
       for (int i = 0; i < kRows; ++i) {
         const int row = grp + i * groups;
-        if (row >= s0 && row < s1) {
+        if (some && row >= s0 && row < s1) {
           uint8_t* w = dst + row * p.c.token_stride;
           *reinterpret_cast<uint32_t*>(w + ln.c0) = e4m3x4(x[i][0] * inv, x[i][1] * inv, x[i][2] * inv, x[i][3] * inv);
           *reinterpret_cast<uint32_t*>(w + ln.c1) = e4m3x4(x[i][4] * inv, x[i][5] * inv, x[i][6] * inv, x[i][7] * inv);
