@@ -674,11 +674,12 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
 }
 
-// Merges the parts of the item that CTA blockIdx.x of the first kernel began and did not
-// finish: sums and denominators by their maxima, in a fixed order.  Eight warps a CTA take NR / 8
-// rows; the warps of a row take its parts in turn, 4 channels a lane, four parts in flight.  (One
+// Merges the parts of the items that two CTAs of the first kernel began and did not finish: sums and
+// denominators by their maxima, in a fixed order.  Eight warps a CTA take NR / 8 rows; as many of
+// a row's warps as have work take its parts in turn, 4 channels a lane, four parts in flight.  (One
 // sequence of 65536 tokens leaves 76 parts an item: a chain of loads per part would cost more
-// than reading the cache.)
+// than reading the cache.)  Two neighbours' items, since where items have many parts
+// only one of them begins any: so all CTAs run at once.
 constexpr int kMergeWarps = 8, kInFlight = 4;
 template <int NR>
 __global__ void __launch_bounds__(32 * kMergeWarps)
@@ -688,78 +689,88 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
   __shared__ float2 ml_s[kMergeWarps];
   pdl_wait();
   pdl_launch_dependents();
-  const int4 d4 = *reinterpret_cast<const int4*>(p.desc + blockIdx.x);
-  const PartDesc d = {d4.x, d4.y, d4.z, d4.w};
-  if (d.parts == 0) return;
+  const int4* desc = reinterpret_cast<const int4*>(p.desc + 2 * blockIdx.x);
+  const int4 both[2] = {desc[0], desc[1]};
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, w0 = warp % kPerRow;
   const int r = blockIdx.y * (NR / 8) + warp / kPerRow;
-  const bool live = r < d.rows;
-  float m = -INFINITY, den = 0.0f;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  // four parts merged into the running maximum, sum and denominator
-  auto merge = [&](const float (&mi)[kInFlight], const float (&di)[kInFlight], const float4 (&ai)[kInFlight]) {
-    float top = m;
+#pragma unroll 1
+  for (int j = 0; j < 2; ++j) {
+    const int4 d4 = j ? both[1] : both[0];
+    const PartDesc d = {d4.x, d4.y, d4.z, d4.w};
+    if (d.parts == 0) continue;
+    const int cta = 2 * blockIdx.x + j;
+    const int used = min(kPerRow, (d.parts + kInFlight - 1) / kInFlight);   // warps of a row with work
+    const bool live = r < d.rows && w0 < used;
+    float m = -INFINITY, den = 0.0f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    // four parts merged into the running maximum, sum and denominator
+    auto merge = [&](const float (&mi)[kInFlight], const float (&di)[kInFlight], const float4 (&ai)[kInFlight]) {
+      float top = m;
 #pragma unroll
-    for (int u = 0; u < kInFlight; ++u) top = fmaxf(top, mi[u]);
-    const float ref = top == -INFINITY ? 0.0f : top, f = ex2(m - ref);
-    m = top;
-    den *= f;
-    acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
+      for (int u = 0; u < kInFlight; ++u) top = fmaxf(top, mi[u]);
+      const float ref = top == -INFINITY ? 0.0f : top, f = ex2(m - ref);
+      m = top;
+      den *= f;
+      acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
 #pragma unroll
-    for (int u = 0; u < kInFlight; ++u) {
-      const float w = ex2(mi[u] - ref);
-      den += di[u] * w;
-      acc.x += ai[u].x * w;
-      acc.y += ai[u].y * w;
-      acc.z += ai[u].z * w;
-      acc.w += ai[u].w * w;
+      for (int u = 0; u < kInFlight; ++u) {
+        const float w = ex2(mi[u] - ref);
+        den += di[u] * w;
+        acc.x += ai[u].x * w;
+        acc.y += ai[u].y * w;
+        acc.z += ai[u].z * w;
+        acc.w += ai[u].w * w;
+      }
+    };
+    if (live) {
+      for (int i0 = w0; i0 < d.parts; i0 += used * kInFlight) {
+        float mi[kInFlight], di[kInFlight];
+        float4 ai[kInFlight];
+#pragma unroll
+        for (int u = 0; u < kInFlight; ++u) {
+          const int i = i0 + u * used;
+          const float* s = p.slots + ((int64_t)2 * (cta + i) + (i == 0 ? 1 : 0)) * kSlotFloats<NR>;
+          mi[u] = -INFINITY;
+          di[u] = 0.0f;
+          ai[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (i < d.parts) {
+            mi[u] = s[NR * 128 + r];
+            di[u] = s[NR * 129 + r];
+            ai[u] = *reinterpret_cast<const float4*>(s + r * 128 + 4 * lane);
+          }
+        }
+        merge(mi, di, ai);
+      }
     }
-  };
-  if (live) {
-    for (int i0 = w0; i0 < d.parts; i0 += kPerRow * kInFlight) {
+    if (used > 1) {
+      __syncthreads();     // (the item before has been read)
+      acc_s[warp][lane] = acc;
+      if (lane == 0) ml_s[warp] = make_float2(m, den);
+      __syncthreads();
+    }
+    if (w0 != 0 || !live) continue;
+    for (int w = 1; w < used; w += kInFlight) {
       float mi[kInFlight], di[kInFlight];
       float4 ai[kInFlight];
 #pragma unroll
       for (int u = 0; u < kInFlight; ++u) {
-        const int i = i0 + u * kPerRow;
-        const float* s = p.slots + ((int64_t)2 * (blockIdx.x + i) + (i == 0 ? 1 : 0)) * kSlotFloats<NR>;
-        mi[u] = -INFINITY;
-        di[u] = 0.0f;
-        ai[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (i < d.parts) {
-          mi[u] = s[NR * 128 + r];
-          di[u] = s[NR * 129 + r];
-          ai[u] = *reinterpret_cast<const float4*>(s + r * 128 + 4 * lane);
-        }
+        const bool in = w + u < used;
+        const float2 ml = in ? ml_s[warp + w + u] : make_float2(-INFINITY, 0.0f);
+        mi[u] = ml.x;
+        di[u] = ml.y;
+        ai[u] = in ? acc_s[warp + w + u][lane] : make_float4(0.f, 0.f, 0.f, 0.f);
       }
       merge(mi, di, ai);
     }
-    acc_s[warp][lane] = acc;
-    if (lane == 0) ml_s[warp] = make_float2(m, den);
+    const float il = den == 0.0f ? 0.0f : 1.0f / den;
+    const int i = div_small(r, p.group_magic);
+    const int64_t tok = d.tok0 + i;
+    const int head = d.head0 + r - i * p.group;
+    *reinterpret_cast<uint2*>(p.a.out + tok * p.a.out_stride + head * kHeadDim + 4 * lane) =
+        make_uint2(pack_bf16x2(acc.x * il, acc.y * il), pack_bf16x2(acc.z * il, acc.w * il));
+    if (p.a.lse && lane == 0)
+      p.a.lse[tok * p.a.heads + head] = den == 0.0f ? -INFINITY : (m + lg2(den)) * kLn2;
   }
-  __syncthreads();
-  if (w0 != 0 || !live) return;
-  for (int w = 1; w < kPerRow; w += kInFlight) {
-    float mi[kInFlight], di[kInFlight];
-    float4 ai[kInFlight];
-#pragma unroll
-    for (int u = 0; u < kInFlight; ++u) {
-      const bool in = w + u < kPerRow;
-      const float2 ml = in ? ml_s[warp + w + u] : make_float2(-INFINITY, 0.0f);
-      mi[u] = ml.x;
-      di[u] = ml.y;
-      ai[u] = in ? acc_s[warp + w + u][lane] : make_float4(0.f, 0.f, 0.f, 0.f);
-    }
-    merge(mi, di, ai);
-  }
-  const float il = den == 0.0f ? 0.0f : 1.0f / den;
-  const int i = div_small(r, p.group_magic);
-  const int64_t tok = d.tok0 + i;
-  const int head = d.head0 + r - i * p.group;
-  *reinterpret_cast<uint2*>(p.a.out + tok * p.a.out_stride + head * kHeadDim + 4 * lane) =
-      make_uint2(pack_bf16x2(acc.x * il, acc.y * il), pack_bf16x2(acc.z * il, acc.w * il));
-  if (p.a.lse && lane == 0)
-    p.a.lse[tok * p.a.heads + head] = den == 0.0f ? -INFINITY : (m + lg2(den)) * kLn2;
 }
 
 int decode_ctas(int sms) { return 2 * sms; }
@@ -780,7 +791,7 @@ cudaError_t launch_nr(const DecodeParams& d, int sms, cudaStream_t stream) {
 }
 template <int NR>
 cudaError_t launch_merge(const DecodeParams& d, int sms, cudaStream_t stream) {
-  return launch(kda_attn_merge_kernel<NR>, dim3((unsigned)decode_ctas(sms), 8), dim3(32 * kMergeWarps),
+  return launch(kda_attn_merge_kernel<NR>, dim3((unsigned)(decode_ctas(sms) / 2), 8), dim3(32 * kMergeWarps),
                 0, true, stream, d);
 }
 
