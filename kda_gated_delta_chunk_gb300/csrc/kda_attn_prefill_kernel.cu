@@ -66,7 +66,9 @@ constexpr uint32_t kTS = 0, kTOP = 256;     // S (P) of half h at 128 h, O at 25
 constexpr int kSlotFloatsP = kRowsP * 130;
 
 struct PartDescP {
-  int n, h, rt, parts;
+  int parts;          // CTAs whose parts make up the item that this CTA begins; 0: none is cut
+  int tok0, rows;     // its first token's row of q and out, its query rows
+  int head0;          // its first query head
 };
 
 struct PrefillParams {
@@ -105,7 +107,7 @@ struct WalkP {
   SeqInfo s;
   ItemP it;
   int a, b;                  // segment: tiles [a, b) of the item
-  int ch, crt;               // its head and row tile
+  int ch;                    // its head
   int64_t last;              // unit of the item's last tile
   __device__ __forceinline__ bool next(const PrefillParams& p) {
     while (pos < end) {
@@ -122,7 +124,7 @@ struct WalkP {
       }
       it = item_of(s.q_len, s.len, rt, p.tokens, p.a.window);
       ch = h;
-      crt = rt++;
+      ++rt;
       const int size = it.tiles + kOver, o = off, o1 = (int)min((int64_t)size, o + (end - pos));
       last = pos - o + size - 1;
       pos += o1 - o;
@@ -550,9 +552,9 @@ __global__ void __launch_bounds__(kThreadsP, 1)
                         min(16, G - h) * kHeadDim * 2);
           }
         if (walk.a == 0 && walk.b < walk.it.tiles) {   // the CTA that the item's last tile lies in
-          part.n = walk.n;
-          part.h = walk.ch;
-          part.rt = walk.crt;
+          part.tok0 = tok0;
+          part.rows = walk.it.cnt * G;
+          part.head0 = walk.ch * G;
           part.parts = (int)(((walk.last + 1) * ranges - 1) / total - blockIdx.x) + 1;
         }
       }
@@ -936,13 +938,10 @@ __global__ void __launch_bounds__(32 * kMergeRows)
   // (not waiting: one CTA still does, so that this grid does not end before the one beside it)
   if (p.wait || (blockIdx.x == 0 && blockIdx.y == 0)) pdl_wait();
   if (p.wait) pdl_launch_dependents();
-  const PartDescP d = p.desc[blockIdx.x];
-  if (d.parts == 0) return;
-  const int lane = threadIdx.x & 31, G = p.a.heads / p.a.c.kv_heads;
-  const int tok0 = p.a.cu_seqlens[d.n], q_len = p.a.cu_seqlens[d.n + 1] - tok0;
-  const int first = d.rt * p.tokens, rows = min(p.tokens, q_len - first) * G;
-  const int r = blockIdx.y * kMergeRows + (threadIdx.x >> 5);
-  if (r >= rows) return;
+  const int4 d4 = *reinterpret_cast<const int4*>(p.desc + blockIdx.x);
+  const PartDescP d = {d4.x, d4.y, d4.z, d4.w};
+  const int lane = threadIdx.x & 31, r = blockIdx.y * kMergeRows + (threadIdx.x >> 5);
+  if (d.parts == 0 || r >= d.rows) return;
   // four parts in flight, merged into the running maximum, sum and denominator
   constexpr int kInFlight = 4;
   float m = -INFINITY, den = 0.0f;
@@ -980,8 +979,9 @@ __global__ void __launch_bounds__(32 * kMergeRows)
     }
   }
   const float il = den == 0.0f ? 0.0f : 1.0f / den;
-  const int64_t tok = tok0 + first + r / G;
-  const int head = d.h * G + r % G;
+  const int i_tok = div_small(r, p.group_magic);
+  const int64_t tok = d.tok0 + i_tok;
+  const int head = d.head0 + r - i_tok * p.group;
   const uint2 o2 = make_uint2(pack_bf16x2(acc.x * il, acc.y * il), pack_bf16x2(acc.z * il, acc.w * il));
   *reinterpret_cast<uint2*>(p.a.out + tok * p.a.out_stride + head * kHeadDim + 4 * lane) = o2;
   if (p.a.lse && lane == 0)
