@@ -75,14 +75,20 @@ def build_binding(force: bool = False) -> str:
 
 
 def build(force: bool = False, verbose_ptxas: bool = False, stamps: bool = False) -> str:
-    """Build (if stale) and return the path of libkda.so (or of the stamps variant)."""
+    """Build (if stale) and return the path of libkda.so (or of the stamps variant); with
+    libkda.so, the marshalling module too."""
+    path = _build_library(force, verbose_ptxas, stamps)
+    if not stamps:
+        build_binding(force)
+    return path
+
+
+def _build_library(force: bool, verbose_ptxas: bool, stamps: bool) -> str:
     lib = STAMPS_LIB if stamps else LIB
     bdir = BUILD + ("_stamps" if stamps else "")
     os.makedirs(bdir, exist_ok=True)
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
     deps = srcs + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(INCLUDE, "*.h"))
-    if not stamps:
-        build_binding(force)
     if not force and os.path.exists(lib):
         if os.path.getmtime(lib) >= max(os.path.getmtime(d) for d in deps):
             return lib

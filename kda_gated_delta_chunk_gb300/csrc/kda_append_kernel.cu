@@ -23,7 +23,7 @@
 // the token's table row in registers.  A lane holds both channels of its pairs -- four and four
 // half the rotated part apart, or eight in a row -- so that the rotation needs no exchange.
 // Bound by memory in a prefill, by the chain of dependent loads in a decode step: 8 x 2048 tokens of
-// 16 heads over 4 in 36.4 us (5.3 TB/s), 16 ragged sequences of up to 1000 in pages of 16 in 19.5 us
+// 16 heads over 4 in 36.3 us (5.3 TB/s), 16 ragged sequences of up to 1000 in pages of 16 in 19.4 us
 // (4.1 TB/s), 64 x 1 token of 32 heads over 8 in 7.4 us.
 #include "kda_attn.cuh"
 
@@ -357,8 +357,9 @@ cudaError_t launch_rows(const AppendParams& p, int sms, cudaStream_t stream) {
 }  // namespace
 
 // Page sizes 16 to 128: a group of 16 lanes takes four rows, whose fp32 values and table entries
-// are kept to 64 registers.  Against two rows a group (and twice the threads) on a GB300: 8 x 2048
-// tokens in pages of 64 36.9 / 40.8 us, 64 single tokens 8.2 / 10.5; pages of 16, ragged, the same.
+// are kept to 64 registers.  Against two rows a group (and twice the threads) on a GB300, as first
+// measured: 8 x 2048 tokens in pages of 64 36.9 / 40.8 us, 64 single tokens 8.2 / 10.5; pages of
+// 16, ragged, the same.
 cudaError_t launch_append(const AppendParams& p, int sms, cudaStream_t stream) {
   switch (p.c.page_size) {
     case 16: return launch_rows<4, 64>(p, sms, stream);

@@ -12,7 +12,7 @@
 // registers of one CTA (kV chunks of 8 columns a thread, 16-byte accesses) between the sum of
 // squares and the outputs, so nothing is read twice; rows of at most 256 columns take one warp
 // each.  16384 x 7168 in bf16: 150.4 us, 6.25 TB/s; 4096 x 7168 to 8 bits with an fp32 residual:
-// 52.0 us, 6.23 TB/s.  Groups of 128 columns are 16 adjacent lanes: their maximum is four shuffles.
+// 52.0 us, 6.23 TB/s; 14 x 7168 2.4 us.  Groups of 128 columns are 16 adjacent lanes: their maximum is four shuffles.
 #include "kda_attn.cuh"
 
 namespace kda {
