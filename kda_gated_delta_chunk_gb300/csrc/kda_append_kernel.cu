@@ -22,8 +22,7 @@
 // maximum and the store.  The others rotate the queries, 16 lanes a (token, group of heads) with
 // the token's table row in registers.  A lane holds both channels of its pairs -- four and four
 // half the rotated part apart, or eight in a row -- so that the rotation needs no exchange.
-// Bound by memory in a prefill, by the chain of dependent loads in a decode step: 8 x 2048 tokens of
-// 16 heads over 4 in 36.3 us (5.3 TB/s), 16 ragged sequences of up to 1000 in pages of 16 in 19.4 us
+// Bound by memory in a prefill, by the chain of dependent loads in a decode step: 8 x 2048 tokens 64 x 1 token of 32 heads over 8 in 5.8 us. (5.3 TB/s), 16 ragged sequences of up to 1000 in pages of 16 in 19.4 us
 // (4.1 TB/s), 64 x 1 token of 32 heads over 8 in 7.4 us.
 #include "kda_attn.cuh"
 
@@ -115,9 +114,9 @@ __device__ __forceinline__ SeqPages seq_pages(const AppendParams& p, int n, bool
   return q;
 }
 
-// kRows: token rows a 16-lane group takes of a page (page size = kRows * groups).
+// kRows: token rows a 16-lane group takes of a page at a time (page size = kRows * groups * kPasses).
 // kHeads: query heads a 16-lane group takes of a token.
-template <int kRows, int kHeads, int kThreads, bool kInter>
+template <int kRows, int kHeads, int kThreads, int kPasses, bool kInter>
 __global__ void __launch_bounds__(kThreads, 65536 / kRegs / kThreads)
     kda_append_kernel(const __grid_constant__ AppendParams p, int page_ctas) {
   __shared__ float top_s[2][kThreads / 32];
@@ -125,7 +124,7 @@ __global__ void __launch_bounds__(kThreads, 65536 / kRegs / kThreads)
   __shared__ int n_s;
   __shared__ int64_t pos_s[kThreads / 16];
   const int tid = threadIdx.x, lane16 = tid & 15, grp = tid >> 4;
-  constexpr int groups = kThreads / 16, warps = kThreads / 32;
+  constexpr int groups = kThreads / 16, warps = kThreads / 32, kStep = kRows * groups;
   const int warp = tid >> 5;
   const Lane ln = lane_of<kInter>(lane16, p.rot_dim);
   const int32_t* cu = p.cu_seqlens;
@@ -202,13 +201,18 @@ __global__ void __launch_bounds__(kThreads, 65536 / kRegs / kThreads)
       const int page = p.c.block_table[n * p.c.table_stride + b];
       const __nv_bfloat16* src = (is_v ? p.v : p.k) + h * kHeadDim;
       const int64_t stride = is_v ? p.v_stride : p.k_stride;
+      // rows are taken kStep at a time, from the first pass that holds a new one to the last
+      const int pass0 = kPasses > 1 ? s0 / kStep : 0, pass1 = kPasses > 1 ? (s1 - 1) / kStep : 0;
       Row8 raw[kRows];
+      auto fetch = [&](int pass) {
 #pragma unroll
-      for (int i = 0; i < kRows; ++i) {
-        const int row = grp + i * groups;
-        raw[i] = {make_uint2(0, 0), make_uint2(0, 0)};
-        if (row >= s0 && row < s1) raw[i] = load_row(src + (int64_t)(t_row0 + row) * stride, ln);
-      }
+        for (int i = 0; i < kRows; ++i) {
+          const int row = pass * kStep + grp + i * groups;
+          raw[i] = {make_uint2(0, 0), make_uint2(0, 0)};
+          if (row >= s0 && row < s1) raw[i] = load_row(src + (int64_t)(t_row0 + row) * stride, ln);
+        }
+      };
+      fetch(pass0);
       if (page < 0 || page >= p.c.num_pages) {
         if (tid == 0) record_error(p.status, KDA_ERR_BAD_CACHE_INDEX, 203);
         continue;
@@ -219,15 +223,21 @@ __global__ void __launch_bounds__(kThreads, 65536 / kRegs / kThreads)
       float x[kRows][8];
       float top = 0.0f;
       bool some = kHeads > 2;       // of this warp's rows are new (few tokens: mostly none)
-      if (kHeads <= 2) {
+      auto turn = [&](int pass) -> float {   // the rows fetched, rotated; their largest finite entry
+        if (kHeads <= 2) {
+          some = false;
 #pragma unroll
-        for (int i = 0; i < kRows; ++i) some = some || (grp + i * groups >= s0 && grp + i * groups < s1);
-        some = __any_sync(0xffffffffu, some);
-      }
-      if (some) {
+          for (int i = 0; i < kRows; ++i) {
+            const int row = pass * kStep + grp + i * groups;
+            some = some || (row >= s0 && row < s1);
+          }
+          some = __any_sync(0xffffffffu, some);
+        }
+        float most = 0.0f;
+        if (!some) return most;
 #pragma unroll
         for (int i = 0; i < kRows; ++i) {
-          const int row = grp + i * groups;
+          const int row = pass * kStep + grp + i * groups;
           unpack_row(raw[i], x[i]);
           if (!is_v && p.rot_dim && row >= s0 && row < s1) {
             const int64_t pos = p.positions ? (int64_t)p.positions[t_row0 + row] : (int64_t)b * P + row;
@@ -237,49 +247,65 @@ __global__ void __launch_bounds__(kThreads, 65536 / kRegs / kThreads)
               record_error(p.status, KDA_ERR_BAD_CACHE_INDEX, 204);
           }
 #pragma unroll
-          for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(x[i][e]));
+          for (int e = 0; e < 8; ++e) most = fmaxf(most, fabsf(x[i][e]));
         }
-        if (top > 3.402823466e38f) {   // an infinity: the maximum of the finite ones
-          top = 0.0f;
+        if (most > 3.402823466e38f) {   // an infinity: the maximum of the finite ones
+          most = 0.0f;
 #pragma unroll
           for (int i = 0; i < kRows; ++i)
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-              if (fabsf(x[i][e]) <= 3.402823466e38f) top = fmaxf(top, fabsf(x[i][e]));
+              if (fabsf(x[i][e]) <= 3.402823466e38f) most = fmaxf(most, fabsf(x[i][e]));
         }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        return most;
+      };
+      top = turn(pass0);
+      for (int pass = pass0 + 1; kPasses > 1 && pass <= pass1; ++pass) {
+        fetch(pass);
+        top = fmaxf(top, turn(pass));
       }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
       if ((tid & 31) == 0) top_s[par][warp] = top;
       __syncthreads();              // (the other parity's readers are past the barrier before this)
       for (int w = 0; w < warps; ++w) top = fmaxf(top, top_s[par][w]);
       float scale = pow2_scale(top);
       if (s0 > 0) scale = fmaxf(scale, old);
       const float inv = 1.0f / scale;
+      for (int pass = pass0; pass <= pass1; ++pass) {
+        if (pass1 > pass0) {        // (more than one: the registers hold the last)
+          fetch(pass);
+          turn(pass);
+        }
 #pragma unroll
-      for (int i = 0; i < kRows; ++i) {
-        const int row = grp + i * groups;
-        if (some && row >= s0 && row < s1) {
-          uint8_t* w = dst + row * p.c.token_stride;
-          *reinterpret_cast<uint32_t*>(w + ln.c0) = e4m3x4(x[i][0] * inv, x[i][1] * inv, x[i][2] * inv, x[i][3] * inv);
-          *reinterpret_cast<uint32_t*>(w + ln.c1) = e4m3x4(x[i][4] * inv, x[i][5] * inv, x[i][6] * inv, x[i][7] * inv);
+        for (int i = 0; i < kRows; ++i) {
+          const int row = pass * kStep + grp + i * groups;
+          if (some && row >= s0 && row < s1) {
+            uint8_t* w = dst + row * p.c.token_stride;
+            *reinterpret_cast<uint32_t*>(w + ln.c0) = e4m3x4(x[i][0] * inv, x[i][1] * inv, x[i][2] * inv, x[i][3] * inv);
+            *reinterpret_cast<uint32_t*>(w + ln.c1) = e4m3x4(x[i][4] * inv, x[i][5] * inv, x[i][6] * inv, x[i][7] * inv);
+          }
         }
       }
       if (s0 > 0 && scale > old) {   // the page's older rows, brought to the new scale
         const float ratio = old * inv;
-        uint2 kept[kRows];
+        for (int first = 0; first < (kPasses > 1 ? s0 : 1); first += kStep) {
+          uint2 kept[kRows];
 #pragma unroll
-        for (int i = 0; i < kRows; ++i)
-          if (grp + i * groups < s0)
-            kept[i] = *reinterpret_cast<const uint2*>(dst + (grp + i * groups) * p.c.token_stride + 8 * lane16);
+          for (int i = 0; i < kRows; ++i) {
+            const int row = first + grp + i * groups;
+            if (row < s0) kept[i] = *reinterpret_cast<const uint2*>(dst + row * p.c.token_stride + 8 * lane16);
+          }
 #pragma unroll
-        for (int i = 0; i < kRows; ++i) {
-          if (grp + i * groups >= s0) continue;
-          const float2 a = from_e4m3x2(kept[i].x & 0xffff), b2 = from_e4m3x2(kept[i].x >> 16);
-          const float2 c = from_e4m3x2(kept[i].y & 0xffff), d = from_e4m3x2(kept[i].y >> 16);
-          *reinterpret_cast<uint2*>(dst + (grp + i * groups) * p.c.token_stride + 8 * lane16) =
-              make_uint2(e4m3x4(a.x * ratio, a.y * ratio, b2.x * ratio, b2.y * ratio),
-                         e4m3x4(c.x * ratio, c.y * ratio, d.x * ratio, d.y * ratio));
+          for (int i = 0; i < kRows; ++i) {
+            const int row = first + grp + i * groups;
+            if (row >= s0) continue;
+            const float2 a = from_e4m3x2(kept[i].x & 0xffff), b2 = from_e4m3x2(kept[i].x >> 16);
+            const float2 c = from_e4m3x2(kept[i].y & 0xffff), d = from_e4m3x2(kept[i].y >> 16);
+            *reinterpret_cast<uint2*>(dst + row * p.c.token_stride + 8 * lane16) =
+                make_uint2(e4m3x4(a.x * ratio, a.y * ratio, b2.x * ratio, b2.y * ratio),
+                           e4m3x4(c.x * ratio, c.y * ratio, d.x * ratio, d.y * ratio));
+          }
         }
       }
       if (tid == 0 && (s0 == 0 || scale > old)) *scale_p = scale;
@@ -332,7 +358,7 @@ __global__ void __launch_bounds__(kThreads, 65536 / kRegs / kThreads)
   }
 }
 
-template <int kRows, int kHeads, int kThreads>
+template <int kRows, int kHeads, int kThreads, int kPasses>
 cudaError_t launch_heads(const AppendParams& p, int sms, cudaStream_t stream) {
   const int64_t resident = (int64_t)sms * (65536 / kRegs / kThreads);
   // at most so many units: every sequence has a partial page at both ends
@@ -342,16 +368,16 @@ cudaError_t launch_heads(const AppendParams& p, int sms, cudaStream_t stream) {
   const int64_t grid = page_ctas + (units + kThreads / 16 - 1) / (kThreads / 16);
   if (grid > 0x7fffffff) return cudaErrorInvalidValue;
   const dim3 g((unsigned)grid), t(kThreads);
-  return p.interleaved ? launch(kda_append_kernel<kRows, kHeads, kThreads, true>, g, t, 0, true, stream, p, page_ctas)
-                       : launch(kda_append_kernel<kRows, kHeads, kThreads, false>, g, t, 0, true, stream, p, page_ctas);
+  return p.interleaved ? launch(kda_append_kernel<kRows, kHeads, kThreads, kPasses, true>, g, t, 0, true, stream, p, page_ctas)
+                       : launch(kda_append_kernel<kRows, kHeads, kThreads, kPasses, false>, g, t, 0, true, stream, p, page_ctas);
 }
 
 // Query heads of a token that share one read of its table row: 4 where there are tokens enough
 // to fill the GPU all the same, else 2 for the shorter chain.
-template <int kRows, int kThreads>
+template <int kRows, int kThreads, int kPasses = 1>
 cudaError_t launch_rows(const AppendParams& p, int sms, cudaStream_t stream) {
-  return p.total_tokens >= 1024 ? launch_heads<kRows, 4, kThreads>(p, sms, stream)
-                                : launch_heads<kRows, 2, kThreads>(p, sms, stream);
+  return p.total_tokens >= 1024 ? launch_heads<kRows, 4, kThreads, kPasses>(p, sms, stream)
+                                : launch_heads<kRows, 2, kThreads, kPasses>(p, sms, stream);
 }
 
 }  // namespace
@@ -360,7 +386,16 @@ cudaError_t launch_rows(const AppendParams& p, int sms, cudaStream_t stream) {
 // are kept to 64 registers.  Against two rows a group (and twice the threads) on a GB300, as first
 // measured: 8 x 2048 tokens in pages of 64 36.9 / 40.8 us, 64 single tokens 8.2 / 10.5; pages of
 // 16, ragged, the same.
+// In pages of 64 and 128 with few new tokens a sequence (P / 16 on average) a CTA of 64 threads takes
+// a page 16 rows at a time, and the new rows twice where they are in more than one such part: most
+// warps of a CTA that covers the page would have no new row.  Against that, 64 sequences in pages
+// of 64: one token each 5.8 / 7.4 us, 8 9.2 / 9.2, 1 to 40 14.6 / 10.1; in pages of 128: one 6.0 / 11.4,
+// 1 to 10 8.4 / 11.6, 1 to 40 15.3 / 14.4.  In pages of 32 one token each 5.9 / 5.7.
 cudaError_t launch_append(const AppendParams& p, int sms, cudaStream_t stream) {
+  if (p.total_tokens <= p.c.page_size / 16 * (int64_t)p.num_seqs) {
+    if (p.c.page_size == 64) return launch_rows<4, 64, 4>(p, sms, stream);
+    if (p.c.page_size == 128) return launch_rows<4, 64, 8>(p, sms, stream);
+  }
   switch (p.c.page_size) {
     case 16: return launch_rows<4, 64>(p, sms, stream);
     case 32: return launch_rows<4, 128>(p, sms, stream);

@@ -222,6 +222,22 @@ def test_strided_inputs_positions_and_in_place_queries():
     assert torch.equal(k.cpu(), d["k"]) and bool((qkv[:, :8] == 0).all()) and bool((qkv[:, -56:] == 0).all())
 
 
+@pytest.mark.parametrize("page,long,inter", [(64, 70, False), (64, 19, True), (128, 130, True), (128, 40, False)])
+def test_few_new_tokens_in_large_pages(page, long, inter):
+    """Pages that are taken in parts: single rows anywhere in a page, and sequences whose new rows
+    lie in several parts, with older rows before them."""
+    lens = [1] * 30 + [long, 2, 0, 3]
+    starts = [(11 * n) % (2 * page) for n in range(30)] + [page - 9, page - 1, 5, 15]
+    d = make(lens, starts, 4, 2, page, 64, seed=9)
+    caches = on_gpu(d, "hpd")
+    q, status = run(d, caches, inter)
+    assert status == kda.OK
+    q64, size = expect(d, inter)
+    assert bool(((q.cpu().double() - q64).abs() <= 2.0 ** -8 * q64.abs() + 2.0 ** -22 * size).all())
+    check_cache(caches[0], caches[2], d["k_ref"], False)
+    check_cache(caches[1], caches[3], d["v_ref"], True)
+
+
 def test_many_sequences():
     """More sequences than a CTA has threads, for the pages and for the queries' positions."""
     g = torch.Generator().manual_seed(3)
