@@ -22,8 +22,9 @@
 // maximum and the store.  The others rotate the queries, 16 lanes a (token, group of heads) with
 // the token's table row in registers.  A lane holds both channels of its pairs -- four and four
 // half the rotated part apart, or eight in a row -- so that the rotation needs no exchange.
-// Bound by memory in a prefill, by the chain of dependent loads in a decode step: 8 x 2048 tokens 64 x 1 token of 32 heads over 8 in 5.8 us. (5.3 TB/s), 16 ragged sequences of up to 1000 in pages of 16 in 19.4 us
-// (4.1 TB/s), 64 x 1 token of 32 heads over 8 in 7.4 us.
+// Bound by memory in a prefill, by the chain of dependent loads in a decode step: 8 x 2048 tokens of
+// 16 heads over 4 in 36.5 us (5.3 TB/s), 16 ragged sequences of up to 1000 in pages of 16 in 19.4 us
+// (4.1 TB/s), 64 x 1 token of 32 heads over 8 in 5.8 us.
 #include "kda_attn.cuh"
 
 namespace kda {
