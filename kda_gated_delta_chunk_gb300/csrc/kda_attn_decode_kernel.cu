@@ -365,6 +365,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     const float cap2 = kCap ? 2.0f * kLog2e / p.a.softcap : 0.0f, cap1 = kCap ? p.a.softcap * kLog2e : 0.0f;
     PartDesc part = {0, 0, 0, 0};
     uint32_t it = 0;
+    // A wait that gives up clears its thread's `ok`; the thread leaves with the others, at a barrier
+    // that has told them.
     bool ok = true;
     uint4 qraw[NR / 8];     // this thread's part of the next segment's queries, 16 lanes a row
     auto load_q = [&](const Walk& w) {
@@ -423,9 +425,11 @@ __global__ void __launch_bounds__(kThreads, 2)
       for (int r = 0; r < NR; ++r) acc[r] = l[r] = 0.0f;
       float run = -INFINITY;         // lane r: running maximum of row r
       bool poisoned = false;         // the tile before has NaN entries that some rows do not see
+      bool left = false;             // somebody's wait gave up: all 128 threads leave
       // O^T of tile i added to the sums (its factors and poison words: parity i & 1)
       auto add_o = [&](uint32_t i, int t) {
         ok = mbar_wait_sleep(bar_o, i & 1) && ok;
+        __syncwarp();
         tc_fence_after();
         const float4* f = fac + ((i & 1) * 4 + warp) * NR;
         if (NR <= 16) {
@@ -470,6 +474,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         // (the scales and V are read here too; S comes last)
         ok = mbar_wait_sleep(bar_full + 8 * st, (it / kStages) & 1) && ok;
         ok = mbar_wait_sleep(bar_s + 8 * par, (it >> 1) & 1) && ok;
+        __syncwarp();
         tc_fence_after();
         const int key0 = (walk.s.tile0 + t) * kTile, key = key0 + tid;
         // some key of the tile is hidden from some row
@@ -562,7 +567,8 @@ __global__ void __launch_bounds__(kThreads, 2)
           if (lane == r) mine_max = m;
         }
         if (lane < NR) wmax[(par * NR + lane) * 4 + warp] = mine_max;
-        if (bar_any(1, 128, !ok)) { ok = false; break; }
+        left = bar_any(1, 128, !ok);
+        if (left) break;
         if (lane < NR) {
           const float4 w = *reinterpret_cast<const float4*>(wmax + (par * NR + lane) * 4);
           const float m = fmaxf(fmaxf(w.x, w.y), fmaxf(w.z, w.w));
@@ -599,7 +605,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         fence_proxy_async();
         mbar_arrive(bar_p);
       }
-      if (!ok) break;
+      if (left) { ok = false; break; }
       add_o(it - 1, walk.b - 1);
       // ---- denominators over the 128 key threads
       // (each step exchanges half of the rows: after log2 NR steps a lane holds row lane * NR / 32)

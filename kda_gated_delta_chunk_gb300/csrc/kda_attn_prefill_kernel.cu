@@ -370,10 +370,10 @@ __global__ void __launch_bounds__(kThreadsP, 1)
 
   const Segment* ring = reinterpret_cast<const Segment*>(sm + kOffSeg);
   static_assert(sizeof(Segment) <= 64 && kSegs <= 4, "segment ring");
-  // The next segment (false when there is none, or the wait gave up), and done with one.
+  // The next segment (`ok`: none of the warp's waits gave up), and done with one.
   auto seg_wait = [&](uint32_t seg, bool& ok) -> const Segment* {
     ok = ok && mbar_wait_sleep(bar_gf + 8 * (seg % kSegs), (seg / kSegs) & 1);
-    __syncwarp();
+    ok = __all_sync(0xffffffffu, ok);
     return ring + seg % kSegs;
   };
   auto seg_done = [&](uint32_t seg) {
@@ -581,6 +581,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
         const uint32_t sv = it % kVStages, vb = it & 1;
         ok = mbar_wait_sleep(bar_vf + 8 * sv, (it / kVStages) & 1);
         if (it >= 2) ok = ok && mbar_wait_sleep(bar_be + 8 * vb, ((it >> 1) - 1) & 1);
+        ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         const unsigned char* src = sm + kOffV8 + sv * 16384;
         unsigned char* dst = sm + kOffVB + vb * 32768 + (c >> 2) * 16384;
