@@ -467,6 +467,9 @@ __global__ void __launch_bounds__(kThreads, 2)
               if (key <= pos && (p.a.window <= 0 || key > pos - p.a.window)) acc[r] = NAN;
             }
           }
+          // all have read these words before anyone writes the next ones of this parity: S of the
+          // tile after this one is there already, so nothing else would hold a fast warp back
+          group_sync(2, 128);
         }
       };
       for (int t = walk.a; t < walk.b; ++t, ++it) {
