@@ -416,7 +416,9 @@ int kda_rope_append(const void* q, int64_t q_stride, const void* k, int64_t k_st
  *   lse     fp32 [T, heads] or NULL
  * A query that sees no key (p < 0) gets a row of zeros and lse = -infinity.  Cache entries that
  * no query of the sequence sees (slots past the cache length, other pages) may hold anything,
- * NaN included; an entry that one query does not see does not reach that query's row.
+ * NaN included; an entry that one query does not see does not reach that query's row.  The same
+ * holds for the scales of such pages, and block_table entries of pages that lie wholly before the
+ * window of a sequence's first new query, or past its length, are not followed.
  * max_q_len: an upper bound of the new tokens of one sequence (host-known); a sequence with
  * more records KDA_ERR_INVALID_ARG on the device and its rows are not written.  The workspace
  * holds the status words and partial results: kda_attention_workspace_size() bytes for the

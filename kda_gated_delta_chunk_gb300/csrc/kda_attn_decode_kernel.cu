@@ -27,9 +27,10 @@
 // Warps: 0-3 softmax and accumulation, 4 the TMA producer, 5 the MMA issuer.  Every wait is
 // bounded; one that gives up records KDA_ERR_DEVICE_TIMEOUT and the CTA leaves.
 //
-// Masked entries: scores by selection; a V row that no query sees (past the length, before every
-// window) is zeroed in shared memory before the product, since 0 x NaN is NaN; a NaN in a row that
-// only some of the queries see is zeroed too and put into those queries' sums by hand.
+// Masked entries: pages before every window are not read; scores by selection; a V row that no query
+// sees (past the length, before every window) is zeroed in shared memory before the product, since
+// 0 x NaN is NaN; a NaN in a row that only some of the queries see is zeroed too and put into those
+// queries' sums by hand.
 #include "kda_attn_tc.cuh"
 
 namespace kda {
@@ -259,7 +260,10 @@ __global__ void __launch_bounds__(kThreads, 2)
         t = walk.a;
       }
       const int b = (walk.s.tile0 + t++) * boxes + lane;
-      if (lane >= boxes || b >= (walk.s.len + P - 1) / P) return {walk.h, 0, true, false};
+      // (a page wholly before every query's window is not looked up: its entry may be stale)
+      if (lane >= boxes || b >= (walk.s.len + P - 1) / P ||
+          (b + 1) * P <= first_seen(walk.s.len - walk.s.q_len, p.a.window))
+        return {walk.h, 0, true, false};
       return {walk.h, p.a.c.block_table[walk.n * p.a.c.table_stride + b], true, true};
     };
     float ks = 1.0f, vs = 1.0f;
@@ -297,7 +301,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (lane < boxes) {
         float* sc = reinterpret_cast<float*>(sm + C::kOffScale + st * 64);
         sc[lane] = ks_now;
-        sc[8 + lane] = vs_now;
+        sc[8 + lane] = vs_now > 0.0f ? vs_now : NAN;
       }
       const uint32_t loads = __popc(__ballot_sync(0xffffffffu, cur.load));
       __syncwarp();
@@ -489,7 +493,8 @@ __global__ void __launch_bounds__(kThreads, 2)
           ks = sc[tid / P];
           vs = sc[8 + tid / P];
         }
-        const float lvs = lg2(vs), ivs = __fdividef(1.0f / kPScale, vs);
+        const float lvs = lg2(vs);
+        float ivs = __fdividef(1.0f / kPScale, vs);
         float x[NR];
         if (NR <= 16) {
           uint32_t o[C::kN <= 16 ? 16 : 32];
@@ -521,6 +526,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
         bool hidden_nan = false;
         if (masked) {
+          if (!(vs > 0.0f)) ivs = 0.0f;   // (a page without a scale: NaN to the rows that see it only)
           bool all = true, any = false;
           for (int i = 0; i < walk.s.q_len; ++i) {
             const int pos = first_pos + i;

@@ -27,9 +27,9 @@
 // issuer, 22 the scheduler, which walks the CTA's range and hands its segments to the others
 // through a ring in shared memory (23 only gives its registers).  Every wait is bounded.
 //
-// Masked entries as in the decode kernel: scores by selection, V rows that no row of the tile
-// sees as zeros, and a NaN in a V row that only some rows see as zero, put back into those rows
-// at the end from the cache itself.
+// Masked entries as in the decode kernel: pages before every window are not read, scores by selection,
+// V rows that no row of the tile sees as zeros, and a NaN in a V row that only some rows see as zero,
+// put back into those rows at the end from the cache itself.
 #include "kda_attn_tc.cuh"
 
 namespace kda {
@@ -93,8 +93,7 @@ __device__ __forceinline__ ItemP item_of(int q_len, int len, int rt, int tokens,
   it.tok = rt * tokens;
   it.cnt = min(tokens, q_len - it.tok);
   const int p_first = len - q_len + it.tok, p_last = p_first + it.cnt - 1;
-  const int lo = window > 0 ? max(0, p_first - window + 1) : 0;
-  it.tile0 = lo / kTile;
+  it.tile0 = first_seen(p_first, window) / kTile;
   it.tiles = max(1, (max(p_last, -1) + kTile) / kTile - it.tile0);
   return it;
 }
@@ -388,10 +387,12 @@ __global__ void __launch_bounds__(kThreadsP, 1)
       uint32_t it = 0, seg = 0;
       bool ok = true;
       const int per = P / 16;                            // 16-key groups per page
-      // lanes 0-7: the page that holds keys 16 lane .. of a tile (its first lane loads it)
+      // lanes 0-7: the page that holds keys 16 lane .. of a tile (its first lane loads it); one wholly
+      // before every window is not looked up: its entry may be stale
       auto page_of = [&](const Segment& g, int key) -> int {
         const int b = (key + 16 * lane) / P;
-        if (lane >= 8 || key >= g.key1 || b >= g.used) return -2;
+        if (lane >= 8 || key >= g.key1 || b >= g.used || (b + 1) * P <= first_seen(g.p_first, p.a.window))
+          return -2;
         const int pg = g.table[b];
         if (pg < 0 || pg >= p.a.c.num_pages) {
           record_error(p.a.status, KDA_ERR_BAD_CACHE_INDEX, 332);
@@ -416,9 +417,9 @@ __global__ void __launch_bounds__(kThreadsP, 1)
           if (!ok) break;
           // (slot it % 4 was last read for tile it - 4, whose P precedes the products of tile
           // it - 3 that the wait above saw done)
-          if (lane < 8)
+          if (lane < 8)   // (a page without a scale is NaN to the rows that see it, and nothing to the others)
             reinterpret_cast<float4*>(sm + kOffSc)[(it & 3) * 8 + lane] =
-                make_float4(ks, lg2(vs), __fdividef(1.0f, vs), 0.0f);
+                make_float4(ks, vs > 0.0f ? lg2(vs) : NAN, vs > 0.0f ? __fdividef(1.0f, vs) : 0.0f, 0.0f);
           const bool loads = pg != -2 && lane % per == 0;
           const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, loads)) * P * kHeadDim;
           const int row = lane * 16;

@@ -214,6 +214,10 @@ struct SeqInfo {
   int tile0, tiles;       // key tiles any of its queries sees; at least one (whose keys may all
                           // be masked), so that every query row is written; 0: not in this launch
 };
+// The first position that a query at `pos` or a later one sees.
+__device__ __forceinline__ int first_seen(int pos, int window) {
+  return window > 0 ? max(0, pos - window + 1) : 0;
+}
 // Sequences with min_rows <= q_len * group <= max_rows are this launch's.  `err`: the code to
 // record for a malformed sequence (which is left out), or KDA_OK.
 __device__ __forceinline__ SeqInfo seq_info(const AttnParams& p, int n, int min_rows, int max_rows,
@@ -239,8 +243,7 @@ __device__ __forceinline__ SeqInfo seq_info(const AttnParams& p, int n, int min_
   }
   const int64_t rows = (int64_t)s.q_len * (p.heads / p.c.kv_heads);
   if (s.q_len == 0 || rows < min_rows || rows > max_rows) return s;
-  const int lo = p.window > 0 ? max(0, s.len - s.q_len - p.window + 1) : 0;
-  s.tile0 = lo / kTile;
+  s.tile0 = first_seen(s.len - s.q_len, p.window) / kTile;
   s.tiles = max(1, (s.len + kTile - 1) / kTile - s.tile0);
   return s;
 }

@@ -46,3 +46,66 @@ def test_nan_at_both_ends_of_a_window_over_three_tiles():
         assert status == kda.OK
         assert torch.equal(out.isnan().cpu(), want)
         assert torch.equal(out.cpu()[~want], clean.cpu()[~want]) and torch.equal(lse, clean_lse)
+
+
+WINDOWED = [
+    # q_lens, kv_lens, heads, kv_heads, window
+    ([1, 1, 1], [300, 131, 1000], 8, 2, 20),
+    ([1] * 4, [260, 511, 640, 100], 16, 2, 70),
+    ([4, 4, 2], [700, 333, 129], 16, 4, 33),
+    ([8, 1], [900, 555], 16, 4, 150),
+    ([100], [500], 16, 4, 40),
+    ([150, 1, 3], [800, 400, 270], 4, 4, 64),
+    ([300], [1500], 8, 1, 200),
+]
+
+
+@pytest.mark.parametrize("stale", ["index", "nan", "zero", "inf"])
+@pytest.mark.parametrize("page", [16, 32, 64])
+@pytest.mark.parametrize("case", WINDOWED, ids=lambda c: f"q{c[0]}kv{c[1]}w{c[4]}")
+def test_pages_given_back_behind_the_window(case, page, stale):
+    """Pages wholly before the window of the sequence's first new query: their table entries point
+    nowhere, or their entries are NaN and their scales NaN, zero or infinite."""
+    q_lens, kv_lens, H, hk, window = case
+    d = make(q_lens, kv_lens, H, hk, page, seed=33)
+    for n, (a, b) in enumerate(zip(q_lens, kv_lens)):
+        gone = max(0, b - a - window + 1) // page
+        pg = d["table"][n, :gone].long()
+        if stale == "index":
+            d["table"][n, :gone] = -1
+        else:
+            x = {"nan": float("nan"), "zero": 0.0, "inf": math.inf}[stale]
+            for c in "kv":
+                d[c][pg] = NAN8
+                d[c + "s"][pg] = x
+    out, lse, status = launch(d, window=window)
+    assert status == kda.OK
+    # (the reference reads pages that are not there: give it the last one, which the window hides)
+    host = dict(d, table=d["table"].clone())
+    for n, b in enumerate(kv_lens):
+        row = host["table"][n, :-(-b // page)]
+        row[row < 0] = row[-1]
+    check(host, out, lse, window=window)
+
+
+@pytest.mark.parametrize("q_len,kv_len,H,hk", [(4, 308, 8, 2), (120, 400, 4, 2)])
+def test_a_page_without_a_scale_stays_with_the_rows_that_see_it(q_len, kv_len, H, hk):
+    """A NaN value scale of a page that only the first queries' windows reach: those rows are NaN,
+    the others as without it."""
+    page, window = 16, 50
+    d = make([q_len], [kv_len], H, hk, page, seed=35)
+    clean, clean_lse, _ = launch(d, window=window)
+    j = kv_len - q_len - window + 1               # the first key of the first query's window
+    last = j // page * page + page - 1            # last key of its page
+    pg = int(d["table"][0, j // page])
+    bad = dict(d, vs=d["vs"].clone())
+    bad["vs"][pg, 0] = float("nan")
+    out, lse, status = launch(bad, window=window)
+    assert status == kda.OK
+    p = kv_len - q_len + torch.arange(q_len)
+    sees = p - window < last
+    assert bool(sees.any()) and not bool(sees.all())
+    want = sees[:, None] & (torch.arange(H) < H // hk)
+    assert torch.equal(out.cpu().isnan().all(-1), want) and torch.equal(out.cpu().isnan().any(-1), want)
+    assert torch.equal(out.cpu()[~want], clean.cpu()[~want])
+    assert torch.equal(lse.cpu()[~want], clean_lse.cpu()[~want])
