@@ -216,6 +216,29 @@ def last_device_status(workspace: torch.Tensor, stream=None) -> int:
                                             ctypes.c_void_p(s.cuda_stream)))
 
 
+def _other_stream(stream, device):
+    """The torch stream for a call's ``stream`` argument where that is not the current one, else None."""
+    if stream is None or stream.cuda_stream == torch.cuda.current_stream(device).cuda_stream:
+        return None
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    return torch.cuda.ExternalStream(stream.cuda_stream, device=device)
+
+
+def _on_stream(side, call, given, *args, **kw):
+    """``call(*args, **kw)`` with ``side`` as the current stream.  What the call allocates then
+    belongs to that stream: a workspace is filled in order with the kernels that use it, and its
+    memory goes back to that stream's work only.  Outputs that the call allocated (those whose
+    ``given`` is None) are handed to the stream that was current."""
+    here = torch.cuda.current_stream(side.device)
+    with torch.cuda.stream(side):
+        done = call(*args, **kw)
+    for t, g in zip(done if isinstance(done, tuple) else (done,), given):
+        if g is None and t is not None:
+            t.record_stream(here)
+    return done
+
+
 def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
@@ -272,6 +295,11 @@ def chunk_prefill_fwd(q, k, v, g, beta, A_log, dt_bias, lower_bound, scale,
     a caller's [R, H, 128] buffer.  Returns (out, final_state).  Asynchronous on ``stream``
     (default: the current torch stream).
     """
+    side = _other_stream(stream, q.device) if stream is not None else None
+    if side is not None:
+        return _on_stream(side, chunk_prefill_fwd, (out, final_state), q, k, v, g, beta, A_log, dt_bias,
+                          lower_bound, scale, initial_state, cu_seqlens, out, final_state, workspace,
+                          state_dtype, None, vsplit, kernel, out_index)
     squeeze = q.dim() == 4
     if squeeze:
         q, k, v, g = (x.view(x.shape[1:]) for x in (q, k, v, g))
@@ -340,6 +368,12 @@ def recurrent_fwd(q, k, v, g, beta, A_log, dt_bias, lower_bound, scale, initial_
     token.  out_index as in chunk_prefill_fwd.  Returns (out, final_state, token_states or
     None).
     """
+    side = _other_stream(stream, q.device) if stream is not None else None
+    if side is not None:
+        return _on_stream(side, recurrent_fwd,
+                          (out, final_state, token_states if isinstance(token_states, torch.Tensor) else None),
+                          q, k, v, g, beta, A_log, dt_bias, lower_bound, scale, initial_state, cu_seqlens,
+                          out, final_state, token_states, workspace, state_dtype, None, out_index)
     if q.dim() == 4:
         q, k, v, g = (x.view(x.shape[1:]) for x in (q, k, v, g))
         if beta.dim() == 3:
@@ -399,6 +433,9 @@ def skinny_proj(x, w_ab, w_b, r: int = 128, y=None, z=None, workspace=None, stre
     ``skinny_proj_workspace_size(k, n_ab)`` bytes, reusable across calls on one stream.
     Returns (y, z).
     """
+    side = _other_stream(stream, x.device) if stream is not None else None
+    if side is not None:
+        return _on_stream(side, skinny_proj, (y, z), x, w_ab, w_b, r, y, z, workspace)
     if x.dim() != 2 or w_ab.dim() != 2 or w_b.dim() != 2:
         raise ValueError("x, w_ab and w_b must be 2-D")
     m, k = x.shape
