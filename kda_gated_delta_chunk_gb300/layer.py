@@ -192,7 +192,7 @@ def rope_table(max_positions: int, rot_dim: int, base: float = 10000.0, scaling:
         # the pair that turns b times within the original context
         pair = lambda b: rot_dim * math.log(original_positions / (2 * math.pi * b)) / (2 * math.log(base))  # noqa: E731
         lo = max(math.floor(pair(beta_fast)), 0)
-        hi = min(math.ceil(pair(beta_slow)), rot_dim // 2 - 1)
+        hi = math.ceil(pair(beta_slow))     # may lie past the last pair, which then keeps a part
         slow = ((j - lo) / max(hi - lo, 1e-3)).clamp(0.0, 1.0)
         inv = inv * (1.0 - slow) + inv / factor * slow
         amp = 0.1 * math.log(factor) + 1.0

@@ -158,3 +158,22 @@ def test_binding_packs_the_cache_as_the_header_lays_it_out():
     got = Cache.from_buffer_copy(raw)
     assert layer._CACHE.size == ctypes.sizeof(Cache)
     assert [getattr(got, n) for n in names] == list(range(1, len(names) + 1))
+
+
+@pytest.mark.parametrize("original,rot,base", [(131072, 128, 10000.0), (65536, 64, 10000.0), (1024, 128, 10000.0),
+                                               (4096, 32, 500000.0)])
+def test_ramp_divides_in_full_only_what_turns_slowly(original, rot, base):
+    """A pair keeps its frequency when it turns beta_fast times or more within the original context,
+    is divided in full when it turns beta_slow times or less, and between the two first pairs
+    of either kind (wherever they lie) the share grows linearly with the pair's index."""
+    factor, fast, slow = 8.0, 32.0, 1.0
+    t = kda.rope_table(2, rot, base=base, scaling="ramp", factor=factor, original_positions=original,
+                       device="cpu").double()
+    amp = 0.1 * math.log(factor) + 1.0
+    turns = lambda j: original * base ** (-2 * j / rot) / (2 * math.pi)  # noqa: E731
+    last_kept = max(j for j in range(1000) if turns(j) >= fast)
+    first_cut = min(j for j in range(1000) if turns(j) <= slow)
+    for j in range(rot // 2):
+        share = min(max((j - last_kept) / (first_cut - last_kept), 0.0), 1.0)
+        want = base ** (-2 * j / rot) * (1 - share + share / factor)
+        assert abs(t[1, j] - amp * math.cos(want)) < 2e-7 and abs(t[1, rot // 2 + j] - amp * math.sin(want)) < 2e-7, j
