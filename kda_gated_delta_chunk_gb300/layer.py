@@ -16,6 +16,7 @@ import ctypes
 import importlib.machinery
 import importlib.util
 import math
+import operator
 import os
 import struct
 
@@ -102,6 +103,14 @@ def _need_cuda(t, name):
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     return t.get_device()
+
+
+def _i32(x, name):
+    """A number the entry points take in 32 bits (ctypes would cut a larger one to them)."""
+    x = operator.index(x)
+    if not -2 ** 31 <= x < 2 ** 31:
+        raise KDAError(ERR_INVALID_ARG, f"{name} {x} does not fit 32 bits")
+    return x
 
 
 def _stream(stream, dev):
@@ -266,6 +275,7 @@ def add_rms_norm(x, residual, weight, eps: float = 1e-6, want: str = "bf16", gro
         y8_ptr, sc_ptr = y8.data_ptr(), y_scale.data_ptr()
     elif y8 is not None or y_scale is not None:
         raise ValueError("y8 and y_scale are not written with want='bf16'")
+    group = _i32(group, "group")
     rc = lib().kda_add_rms_norm(
         x.data_ptr(), ldx, r_ptr, ldr, r_kind, weight.data_ptr(),
         STATE_F32 if weight.dtype is _F32 else STATE_BF16, eps, s_ptr, lds, y_ptr, ldy, y8_ptr, ldy8,
@@ -348,8 +358,9 @@ def rope_append(q, k, v, rope, k_cache, v_cache, k_scale, v_scale, block_table, 
 
 
 def attention_workspace_size(num_seqs: int, heads: int, kv_heads: int, max_q_len: int) -> int:
-    return int(lib().kda_attention_workspace_size(int(num_seqs), int(heads), int(kv_heads),
-                                                  int(max_q_len)))
+    return int(lib().kda_attention_workspace_size(
+        _i32(int(num_seqs), "num_seqs"), _i32(int(heads), "heads"), _i32(int(kv_heads), "kv_heads"),
+        _i32(int(max_q_len), "max_q_len")))
 
 
 def alloc_attention_workspace(num_seqs: int, heads: int, kv_heads: int, max_q_len: int,
@@ -391,6 +402,7 @@ def cached_attention(q, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens
     if d != HEAD_DIM:
         raise KDAError(ERR_INVALID_ARG, f"head_dim {d} (only {HEAD_DIM} is supported)")
     N = cu_seqlens.numel() - 1
+    window, max_q_len = _i32(window, "window"), _i32(max_q_len, "max_q_len")
     q_row = _check(q, "q", _HALF, shape, dev)
     _check(cu_seqlens, "cu_seqlens", _INT, (N + 1,), dev, 0)
     c, hk = _cache(k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, N, dev)

@@ -109,3 +109,20 @@ def test_a_page_without_a_scale_stays_with_the_rows_that_see_it(q_len, kv_len, H
     assert torch.equal(out.cpu().isnan().all(-1), want) and torch.equal(out.cpu().isnan().any(-1), want)
     assert torch.equal(out.cpu()[~want], clean.cpu()[~want])
     assert torch.equal(lse.cpu()[~want], clean_lse.cpu()[~want])
+
+
+def test_numbers_past_32_bits_are_refused():
+    """... and not cut to their low 32 bits; others of an integer type are taken."""
+    d = make([2], [90], 4, 2, 16, seed=37)
+    for kw in (dict(window=2 ** 32 + 5), dict(window=2 ** 31), dict(max_q=2 ** 32 + 2)):
+        with pytest.raises(kda.KDAError) as e:
+            launch(d, workspace=kda.alloc_attention_workspace(1, 4, 2, 2), **kw)
+        assert e.value.code == kda.ERR_INVALID_ARG, kw
+    x = torch.zeros(2, 256, dtype=BF16, device="cuda")
+    with pytest.raises(kda.KDAError) as e:
+        kda.add_rms_norm(x, None, x[0], want="fp8", group=2 ** 32 + 128)
+    assert e.value.code == kda.ERR_INVALID_ARG
+    numpy = pytest.importorskip("numpy")
+    out, lse, status = launch(d, window=numpy.int64(7), max_q=numpy.int32(2))
+    assert status == kda.OK
+    check(d, out, lse, window=7)

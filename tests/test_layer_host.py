@@ -177,3 +177,10 @@ def test_ramp_divides_in_full_only_what_turns_slowly(original, rot, base):
         share = min(max((j - last_kept) / (first_cut - last_kept), 0.0), 1.0)
         want = base ** (-2 * j / rot) * (1 - share + share / factor)
         assert abs(t[1, j] - amp * math.cos(want)) < 2e-7 and abs(t[1, rot // 2 + j] - amp * math.sin(want)) < 2e-7, j
+
+
+@pytest.mark.parametrize("args", [(2 ** 32 + 1, 8, 2, 1), (1, 2 ** 32 + 8, 2, 1), (1, 8, 2, 2 ** 32), (1, 8, 2, -2 ** 31 - 1)])
+def test_sizes_past_32_bits_are_refused(args):
+    with pytest.raises(kda.KDAError) as e:
+        kda.attention_workspace_size(*args)
+    assert e.value.code == kda.ERR_INVALID_ARG
