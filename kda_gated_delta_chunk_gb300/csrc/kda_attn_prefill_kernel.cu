@@ -586,13 +586,14 @@ __global__ void __launch_bounds__(kThreadsP, 1)
         if (!ok) break;
         const unsigned char* src = sm + kOffV8 + sv * 16384;
         unsigned char* dst = sm + kOffVB + vb * 32768 + (c >> 2) * 16384;
-        const bool masked = key0 + kTile - 1 > p_first || (p.a.window > 0 && key0 <= p_last - p.a.window);
+        const int seen0 = first_seen(p_first, p.a.window);   // no row of the tile sees an earlier key
+        const bool masked = key0 + kTile - 1 > p_first || key0 < first_seen(p_last, p.a.window);
 #pragma unroll 2
         for (int j = 0; j < 8; ++j) {
           const int row = (vt >> 3) + 16 * j, key = key0 + row;
           uint4 u = *reinterpret_cast<const uint4*>(src + row * 128 + ((c ^ (row & 7)) << 4));
           // seen by no row of the tile: whatever is there reads as zero
-          if (masked && (key > p_last || (p.a.window > 0 && key <= p_first - p.a.window)))
+          if (masked && (key > p_last || key < seen0))
             u = make_uint4(0, 0, 0, 0);
           uint32_t w[4] = {u.x, u.y, u.z, u.w}, o[8];
           if (masked) {     // NaN entries (rare) of a row that only some may see: noted, read as zero
@@ -785,7 +786,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
             group_sync(id_pair, 64);
           } else if (scaled) {
             // bits of the 64 keys that this row sees: lo <= e <= hi
-            const int lo = p.a.window > 0 ? hi - p.a.window + 1 : 0;
+            const int lo = p.a.window > 0 && hi >= 0 ? hi - p.a.window + 1 : 0;
             const uint64_t upto = hi < 0 ? 0 : (hi >= 63 ? ~0ull : (2ull << hi) - 1);
             const uint64_t see = lo <= 0 ? upto : (lo >= 64 ? 0 : upto & (~0ull << lo));
 #pragma unroll
@@ -864,8 +865,8 @@ __global__ void __launch_bounds__(kThreadsP, 1)
         if (poisoned && live) {    // NaN entries that this row sees, in tiles that some rows do not
           const int p0 = sg->p_first, p1 = p0 + last, pos = p0 + i_tok;
           for (int key0 = sg->key0; key0 < sg->key1; key0 += kTile) {
-            if (!(key0 + kTile - 1 > p0 || (p.a.window > 0 && key0 <= p1 - p.a.window))) continue;
-            for (int key = max(key0, p.a.window > 0 ? pos - p.a.window + 1 : 0); key <= min(key0 + kTile - 1, pos); ++key) {
+            if (!(key0 + kTile - 1 > p0 || key0 < first_seen(p1, p.a.window))) continue;
+            for (int key = max(key0, first_seen(pos, p.a.window)); key <= min(key0 + kTile - 1, pos); ++key) {
               const int pg = sg->table[key / P];
               if (pg < 0 || pg >= p.a.c.num_pages) continue;
               const uint8_t* v = p.a.c.v + pg * p.a.c.page_stride + sg->ch * p.a.c.head_stride +

@@ -214,9 +214,10 @@ struct SeqInfo {
   int tile0, tiles;       // key tiles any of its queries sees; at least one (whose keys may all
                           // be masked), so that every query row is written; 0: not in this launch
 };
-// The first position that a query at `pos` or a later one sees.
+// The first position that a query at `pos` or a later one sees.  (A position before 0 sees nothing;
+// taken as 0, it leaves the difference in range whatever the window.)
 __device__ __forceinline__ int first_seen(int pos, int window) {
-  return window > 0 ? max(0, pos - window + 1) : 0;
+  return window > 0 ? max(0, max(pos, 0) - window + 1) : 0;
 }
 // Sequences with min_rows <= q_len * group <= max_rows are this launch's.  `err`: the code to
 // record for a malformed sequence (which is left out), or KDA_OK.

@@ -231,7 +231,8 @@ int kda_cached_attention(const void* q, int64_t q_stride, const kda_kv_cache* ca
   p.cu_seqlens = cu_seqlens;
   p.scale = scale;
   p.softcap = softcap;
-  p.window = window;
+  // (a window as long as the longest sequence that the table holds hides nothing)
+  p.window = window < (int64_t)cache->max_blocks * cache->page_size ? window : 0;
   p.total_tokens = total_tokens;
   p.num_seqs = num_seqs;
   p.heads = heads;

@@ -126,3 +126,13 @@ def test_numbers_past_32_bits_are_refused():
     out, lse, status = launch(d, window=numpy.int64(7), max_q=numpy.int32(2))
     assert status == kda.OK
     check(d, out, lse, window=7)
+
+
+@pytest.mark.parametrize("q_lens,kv_lens", [([6, 2], [3, 40]), ([40, 300], [30, 250]), ([8, 1], [2, 0])])
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 3, 2 ** 30])
+def test_windows_as_long_as_an_integer(q_lens, kv_lens, window):
+    """A window that hides nothing, with queries that sit before position 0."""
+    d = make(q_lens, kv_lens, 4, 2, 16, seed=39)
+    out, lse, status = launch(d, window=window)
+    assert status == kda.OK
+    check(d, out, lse, window=window)
