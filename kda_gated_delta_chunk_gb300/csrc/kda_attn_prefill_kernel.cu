@@ -786,7 +786,8 @@ __global__ void __launch_bounds__(kThreadsP, 1)
             group_sync(id_pair, 64);
           } else if (scaled) {
             // bits of the 64 keys that this row sees: lo <= e <= hi
-            const int lo = p.a.window > 0 && hi >= 0 ? hi - p.a.window + 1 : 0;
+            // (below hi < 0 the difference may wrap: nothing is seen then)
+            const int lo = p.a.window > 0 ? (int)((uint32_t)hi - (uint32_t)p.a.window + 1u) : 0;
             const uint64_t upto = hi < 0 ? 0 : (hi >= 63 ? ~0ull : (2ull << hi) - 1);
             const uint64_t see = lo <= 0 ? upto : (lo >= 64 ? 0 : upto & (~0ull << lo));
 #pragma unroll

@@ -13,6 +13,7 @@ namespace attn {
 using namespace sm100;
 
 constexpr int kTile = 128;              // keys of a tile
+constexpr int kMaxLen = 0x7fffffff - (kTile - 1);   // cached tokens of a sequence: whole tiles end below 2^31
 constexpr int kOver = 3;                // units (tiles' worth of time) an item takes besides its tiles
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -234,7 +235,7 @@ __device__ __forceinline__ SeqInfo seq_info(const AttnParams& p, int n, int min_
     *err = KDA_ERR_BAD_CU_SEQLENS;
     return s;
   }
-  if (s.len < 0 || (int64_t)s.len > (int64_t)p.c.max_blocks * p.c.page_size) {
+  if (s.len < 0 || s.len > kMaxLen || (int64_t)s.len > (int64_t)p.c.max_blocks * p.c.page_size) {
     *err = KDA_ERR_BAD_CACHE_INDEX;
     return s;
   }

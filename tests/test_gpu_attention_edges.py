@@ -136,3 +136,35 @@ def test_windows_as_long_as_an_integer(q_lens, kv_lens, window):
     out, lse, status = launch(d, window=window)
     assert status == kda.OK
     check(d, out, lse, window=window)
+
+
+def test_lengths_near_two_to_the_31():
+    """The last tiles below position 2^31 - 128, windows nearly as long, and a cache length past
+    that bound: refused for its sequence, the others as they are."""
+    page, H, hk, window = 16, 2, 1, 100
+    top = 2 ** 31 - 128
+    for q_len in (1, 3, 40):
+        d = make([q_len, q_len], [256, 256], H, hk, page, seed=51)
+        near, near_lse, status = launch(d, window=window)
+        assert status == kda.OK
+        width = 2 ** 27 - 1                                        # 2^31 - 16 positions
+        table = torch.zeros(2, width, dtype=torch.int32, device="cuda")
+        b = (top - 256) // page
+        table[0, b:b + 16] = d["table"][0, :16].cuda()
+        table[1, :16] = d["table"][1, :16].cuda()
+        far = dict(d, table=table, kv=torch.tensor([top, 256], dtype=torch.int32))
+        out, lse, status = launch(far, window=window)
+        assert status == kda.OK
+        assert torch.equal(out, near) and torch.equal(lse, near_lse)
+        far["kv"] = torch.tensor([top + 28, 256], dtype=torch.int32)
+        out, lse, status = launch(far, window=window)
+        assert status == kda.ERR_BAD_CACHE_INDEX
+        assert torch.equal(out[q_len:], near[q_len:]) and torch.equal(lse[q_len:], near_lse[q_len:])
+        # queries before position 0 under a window that reaches from there past the integers
+        some = dict(far, kv=torch.tensor([q_len // 2, 256], dtype=torch.int32))
+        table[0, :16] = d["table"][0, :16].cuda()
+        few = dict(some, table=table[:, :17].cpu(), kv_lens=[q_len // 2, 256])
+        for w in (2 ** 31 - 129, 2 ** 31 - 20):
+            out, lse, status = launch(some, window=w)
+            assert status == kda.OK
+            check(few, out, lse)
