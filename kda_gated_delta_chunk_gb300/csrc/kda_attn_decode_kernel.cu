@@ -366,7 +366,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     float* sums = reinterpret_cast<float*>(sm + C::kOffSum);
     uint4* poison = reinterpret_cast<uint4*>(sm + C::kOffPoison);
     float* qmul = reinterpret_cast<float*>(sm + C::kOffQmul);
-    const float cap2 = kCap ? 2.0f * kLog2e / p.a.softcap : 0.0f, cap1 = kCap ? p.a.softcap * kLog2e : 0.0f;
+    const Cap cap = kCap ? cap_of(p.a.softcap) : Cap{0.0f, 0.0f};
     PartDesc part = {0, 0, 0, 0};
     uint32_t it = 0;
     // A wait that gives up clears its thread's `ok`; the thread leaves with the others, at a barrier
@@ -414,7 +414,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         *reinterpret_cast<uint2*>(sm + C::kOffQ + tile_off(NR + r, 8 * c)) = make_uint2(w2[0], w2[1]);
         if (c == 0) {   // a non-finite query makes its row NaN
           const float sq = top <= 3.402823466e38f ? __uint_as_float((uint32_t)(127 + e2c) << 23) : NAN;
-          qmul[r] = sq * p.a.scale * (kCap ? 1.0f : kLog2e);
+          qmul[r] = sq * p.a.scale * kLog2e;
         }
       }
       fence_proxy_async();
@@ -519,9 +519,27 @@ __global__ void __launch_bounds__(kThreads, 2)
           const float4 m4 = *reinterpret_cast<const float4*>(qmul + r);
           const float m[4] = {m4.x, m4.y, m4.z, m4.w};
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            if (kCap) x[r + e] = cap_score(x[r + e], m[e] * ks * cap2, -2.0f * cap1, cap1 + lvs);
-            else x[r + e] = x[r + e] * (m[e] * ks) + lvs;
+          for (int e = 0; e < 4; ++e) x[r + e] = kCap ? x[r + e] * (m[e] * ks) : x[r + e] * (m[e] * ks) + lvs;
+        }
+        if (kCap) {
+          float top = 0.0f;
+#pragma unroll
+          for (int r = 0; r < NR; r += 2) top = max3_abs(top, x[r], x[r + 1]);
+          const float2 add = make_float2(lvs, lvs);
+          if (__any_sync(0xffffffffu, top * cap.inv >= kCapSmall)) {
+#pragma unroll
+            for (int r = 0; r < NR; r += 2) {
+              const float2 y = cap_any(make_float2(x[r], x[r + 1]), cap, add);
+              x[r] = y.x;
+              x[r + 1] = y.y;
+            }
+          } else {
+#pragma unroll
+            for (int r = 0; r < NR; r += 2) {
+              const float2 y = cap_small(make_float2(x[r], x[r + 1]), cap, add);
+              x[r] = y.x;
+              x[r + 1] = y.y;
+            }
           }
         }
         bool hidden_nan = false;

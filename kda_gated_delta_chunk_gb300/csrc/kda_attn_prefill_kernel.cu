@@ -16,7 +16,8 @@
 //
 // Bound by the tensor cores: 4 x 128 flops per visible (row, key).  4096 tokens at the end of 16384,
 // 16 heads over 2: 326.6 us, 1473 TFLOP/s; 289 us with the softmax left out.  With capped scores
-// 594 us: three special functions a score.  Two halves keep the tensor cores busy: while one half's
+// 585 us: the cap's polynomial (nine fp32 operations a score), and a tile's maximum before its
+// numerators.  Two halves keep the tensor cores busy: while one half's
 // softmax runs, the other half's products do.  The matrix instructions of a CTA
 // run in the order they are issued, so S(i+1) of a half may follow its O += P(i) V, whose P it
 // overwrites, without a wait.  Key tiles of all (sequence, kv head, row tile) items are laid end
@@ -645,7 +646,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
     const uint32_t ts = tmem + kTS + 128 * half + lanes;
     const uint32_t to = tmem + kTOP + 128 * half + 64 * cg + lanes;
     const uint32_t id_pair = 1 + 4 * half + (warp & 3), id_half = 9 + half;
-    const float cap2 = kCap ? 2.0f * kLog2e / p.a.softcap : 0.0f, cap1 = kCap ? p.a.softcap * kLog2e : 0.0f;
+    const Cap cap = kCap ? cap_of(p.a.softcap) : Cap{0.0f, 0.0f};
     const float sign = p.a.scale < 0.0f ? -1.0f : 1.0f;  // (the row maximum is taken before the scale)
     float* qmul_s = reinterpret_cast<float*>(sm + kOffQmul);
     float* mx_s = reinterpret_cast<float*>(sm + kOffMx) + row;
@@ -697,7 +698,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
           *reinterpret_cast<uint2*>(q1 + 16384 + tile_off(r & 127, 8 * c)) = make_uint2(w2[0], w2[1]);
           if (c == 0) {   // a non-finite query makes its row NaN
             const float sq = top <= 3.402823466e38f ? __uint_as_float((uint32_t)(127 + e2c) << 23) : NAN;
-            qmul_s[r] = sq * fabsf(p.a.scale) * (kCap ? 1.0f : kLog2e);
+            qmul_s[r] = sq * fabsf(p.a.scale) * kLog2e;
           }
         }
         fence_proxy_async();
@@ -793,12 +794,40 @@ __global__ void __launch_bounds__(kThreadsP, 1)
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
               const float4 f = sc[g];
-              const float mul = qmul * f.x * (kCap ? cap2 : 1.0f), add = kCap ? cap1 + f.y : f.y;
+              const float mul = qmul * f.x, add = f.y;
               const uint32_t bits = (uint32_t)(see >> (32 * (g >> 1))) >> (16 * (g & 1));
+              if (kCap) {
+                float top = 0.0f;
+#pragma unroll
+                for (int e = 16 * g; e < 16 * g + 16; e += 2)
+                  top = max3_abs(top, __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
+                const float2 mul_2 = make_float2(mul, mul), add_2 = make_float2(add, add);
+                if (__any_sync(0xffffffffu, top * mul * cap.inv >= kCapSmall)) {
+#pragma unroll
+                  for (int e = 16 * g; e < 16 * g + 16; e += 2) {
+                    const float2 t = mul2(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), mul_2);
+                    const float2 y = cap_any(t, cap, add_2);
+                    s[e] = __float_as_uint(y.x);
+                    s[e + 1] = __float_as_uint(y.y);
+                  }
+                } else {
+#pragma unroll
+                  for (int e = 16 * g; e < 16 * g + 16; e += 2) {
+                    const float2 t = mul2(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), mul_2);
+                    const float2 y = cap_small(t, cap, add_2);
+                    s[e] = __float_as_uint(y.x);
+                    s[e + 1] = __float_as_uint(y.y);
+                  }
+                }
+              }
+              if (kCap && !masked) {
+                mt = fmaxf(mt, max_of(g));
+                continue;
+              }
 #pragma unroll
               for (int e = 0; e < 16; ++e) {
                 float x = __uint_as_float(s[16 * g + e]);
-                x = kCap ? cap_score(x, mul, -2.0f * cap1, add) : fmaf(x, mul, add);
+                if (!kCap) x = fmaf(x, mul, add);
                 if (!((bits >> e) & 1)) x = -INFINITY;
                 mt = fmaxf(mt, x);
                 s[16 * g + e] = __float_as_uint(x);

@@ -64,10 +64,52 @@ __device__ __forceinline__ float rcp(float x) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// cap * tanh(x / cap) * log2(e) + a to fp32's absolute precision, from tanh y = 1 - 2 / (1 + e^(2 y)):
-// m2cap = -2 cap log2(e), to_e = 2 log2(e) / cap (a factor of x may be in it), cap_a = cap log2(e) + a.
-__device__ __forceinline__ float cap_score(float x, float to_e, float m2cap, float cap_a) {
-  return fmaf(m2cap, rcp(1.0f + ex2(x * to_e)), cap_a);
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  uint64_t r, x, y;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(a.x), "f"(a.y));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(y) : "f"(b.x), "f"(b.y));
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+  float2 o;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(o.x), "=f"(o.y) : "l"(r));
+  return o;
+}
+
+// ------------------------------------------------------------ capped scores
+// cap tanh(s / cap) log2(e) + a from t = s log2(e), to fp32's relative precision of the capped score
+// whatever the cap (its own precision would leave an error of 2^-23 cap): with y = s / cap
+//   |y| < 0.6:  tanh y = y + y^3 g(y^2), g of degree 3 with the least largest relative error of tanh there
+//               (6.6e-8; with the roundings of fp32 1.6e-7), found by linear programming
+//   else:       tanh y = 1 - 2 / (1 + e^(2 y)), which cancels no more than half of itself
+// The first form takes no special function.  Scores that small are most of those that a cap of
+// several tens meets, so a group of them is looked at first and the second form left out.
+constexpr float kCapSmall = 0.6f;
+struct Cap {
+  float inv, cap;     // 1 / (cap log2(e)), cap log2(e)
+};
+__device__ __forceinline__ Cap cap_of(float softcap) { return {1.0f / (softcap * kLog2e), softcap * kLog2e}; }
+__device__ __forceinline__ float2 cap_small(float2 t, const Cap& c, float2 a) {
+  const float2 y = mul2(t, make_float2(c.inv, c.inv)), u = mul2(y, y);
+  float2 g = fma2(u, make_float2(0.0154861547f, 0.0154861547f), make_float2(-0.0521145090f, -0.0521145090f));
+  g = fma2(g, u, make_float2(0.133107468f, 0.133107468f));
+  g = fma2(g, u, make_float2(-0.333324194f, -0.333324194f));
+  return fma2(mul2(t, u), g, add2(t, a));
+}
+__device__ __forceinline__ float cap_large(float t, const Cap& c, float a) {
+  const float z = fmaf(-2.0f, rcp(1.0f + ex2(t * c.inv * (2.0f * kLog2e))), 1.0f);
+  return fmaf(z, c.cap, a);
+}
+// Either form by the size of each.
+__device__ __forceinline__ float2 cap_any(float2 t, const Cap& c, float2 a) {
+  float2 r = cap_small(t, c, a);
+  if (!(fabsf(t.x * c.inv) < kCapSmall)) r.x = cap_large(t.x, c, a.x);
+  if (!(fabsf(t.y * c.inv) < kCapSmall)) r.y = cap_large(t.y, c, a.y);
+  return r;
+}
+// max(a, |b|, |c|), a not negative
+__device__ __forceinline__ float max3_abs(float a, float b, float c) {
+  float y;
+  asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
 }
 
 // D[tmem] (+)= A[smem] * B[smem]^T, kind::f8f6f4 with e4m3 operands, fp32 accumulate; K = 32.

@@ -230,7 +230,8 @@ int kda_cached_attention(const void* q, int64_t q_stride, const kda_kv_cache* ca
   p.out_stride = out_stride;
   p.cu_seqlens = cu_seqlens;
   p.scale = scale;
-  p.softcap = softcap;
+  // (a cap below 2^-100 differs from that by less than a score's precision; its reciprocal would overflow)
+  p.softcap = softcap > 0.0f ? fmaxf(softcap, 0x1p-100f) : 0.0f;
   // (a window as long as the longest sequence that the table holds hides nothing)
   p.window = window < (int64_t)cache->max_blocks * cache->page_size ? window : 0;
   p.total_tokens = total_tokens;

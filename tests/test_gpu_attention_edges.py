@@ -168,3 +168,19 @@ def test_lengths_near_two_to_the_31():
             out, lse, status = launch(some, window=w)
             assert status == kda.OK
             check(few, out, lse)
+
+
+@pytest.mark.parametrize("softcap", [0.01, 2.0, 30.0, 1e3, 1e4, 1e5, 1e30, 3e38, 1e-44])
+@pytest.mark.parametrize("q_lens,kv_lens,H,hk", [([1, 1], [700, 90], 8, 2), ([4, 3], [300, 1000], 16, 4),
+                                                 ([130, 2], [400, 300], 4, 2)])
+def test_caps_of_any_size(softcap, q_lens, kv_lens, H, hk):
+    """A capped score keeps its relative precision whether it is small beside the cap or not: rows
+    whose scores all are, rows with both, rows far beyond it.  The score's error of test_gpu_attention
+    holds: capping adds 2^-21 of the capped score at most, and 2^-14 of a bound of the score is there."""
+    d = make(q_lens, kv_lens, H, hk, 32, seed=61)
+    d["q"][:, 1] *= 0.05
+    d["q"][:, 2] *= 40.0
+    d["q"][0] *= 8.0
+    out, lse, status = launch(d, softcap=softcap)
+    assert status == kda.OK
+    check(d, out, lse, softcap=softcap)
