@@ -78,7 +78,7 @@ struct DecodeParams {
   CacheMaps maps;
   int group;                 // query heads of a kv head
   uint32_t group_magic;      // 65535 / group + 1 (div_small)
-  int wait;                  // wait for the kernel before this one (programmatic launch)
+  int gate;                  // the call's number, when this kernel runs beside the prefill kernel; else 0
   int64_t least;             // units below which the prefill kernel takes these sequences too
   int min_rows, max_rows;
   PartDesc* desc;
@@ -168,8 +168,14 @@ __global__ void __launch_bounds__(kThreads, 2)
     tmem_relinquish();
   }
   // (launched as a programmatic dependent: of the work before this call, or of the prefill kernel,
-  // which has waited for that and shares nothing with this one)
-  if (p.wait) pdl_wait();
+  // which has waited for that and says so)
+  if (p.gate == 0) {
+    pdl_wait();
+  } else {
+    if (tid == 0 && ld_acquire_gpu(p.a.status + kGateWord) != p.gate) pdl_wait();
+    __syncthreads();
+    fence_proxy_async_global();
+  }
   pdl_launch_dependents();
 
   // ---- this CTA's range: total tiles, then the sequence its first tile lies in
@@ -858,9 +864,9 @@ size_t decode_workspace_bytes(int sms) {
 }
 
 namespace {
-void make_params(const AttnParams& a, int max_rows, bool wait, void* work, int sms, DecodeParams* d) {
+void make_params(const AttnParams& a, int max_rows, int gate, void* work, int sms, DecodeParams* d) {
   d->a = a;
-  d->wait = wait;
+  d->gate = gate;
   d->least = 0;
   d->group = a.heads / a.c.kv_heads;
   d->group_magic = 65535u / (uint32_t)d->group + 1;
@@ -873,9 +879,9 @@ void make_params(const AttnParams& a, int max_rows, bool wait, void* work, int s
 
 // The operands are padded to 8, 16 or 32 rows.
 cudaError_t launch_attn_decode(const AttnParams& a, const CacheMaps& maps, int max_rows, int64_t least,
-                               bool beside, void* work, int sms, cudaStream_t stream) {
+                               int gate, void* work, int sms, cudaStream_t stream) {
   DecodeParams d;
-  make_params(a, max_rows, !beside, work, sms, &d);
+  make_params(a, max_rows, gate, work, sms, &d);
   d.maps = maps;
   d.least = least;
   const bool cap = a.softcap > 0.0f;
@@ -887,7 +893,7 @@ cudaError_t launch_attn_decode(const AttnParams& a, const CacheMaps& maps, int m
 cudaError_t launch_attn_decode_merge(const AttnParams& a, int max_rows, void* work, int sms,
                                      cudaStream_t stream) {
   DecodeParams d = {};
-  make_params(a, max_rows, true, work, sms, &d);
+  make_params(a, max_rows, 0, work, sms, &d);
   return max_rows <= 8    ? launch_merge<8>(d, sms, stream)
          : max_rows <= 16 ? launch_merge<16>(d, sms, stream)
                           : launch_merge<32>(d, sms, stream);

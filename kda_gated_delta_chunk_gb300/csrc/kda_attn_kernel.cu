@@ -1,4 +1,6 @@
 // Attention over the paged e4m3 cache: which kernel takes which sequences of a call.
+#include <atomic>
+
 #include "kda_attn_tc.cuh"
 
 namespace kda {
@@ -24,6 +26,12 @@ int device_sms() {
   return sms;
 }
 
+// Numbers calls that run both kernels, from 1.
+int call_number() {
+  static std::atomic<unsigned> calls{0};
+  return (int)(calls.fetch_add(1) & 0x3fffffffu) + 1;
+}
+
 size_t align16(size_t n) { return (n + 15) & ~(size_t)15; }
 
 // Rows (new tokens x heads per kv head) of a sequence that go to the decode kernel: up to 32.
@@ -46,10 +54,11 @@ size_t attn_workspace_bytes(int32_t num_seqs, int32_t heads, int32_t kv_heads, i
 // the prefill kernel, which takes the first ones too when they are few (both kernels find that out
 // from the lengths on the device).  A launch is left out when the sizes say that no sequence can
 // need it: none can have more rows than max_q_len gives, and with num_seqs * max_q_len tokens in
-// the batch all have that many.  With both, the decode kernel is launched as the prefill kernel's
-// dependent and waits for nothing but, at its end, for the prefill kernel (its CTAs start as SMs
-// come free), the first merge waits for the decode kernel and so for both, and the second one
-// runs beside it.
+// the batch all have that many.  With both, the decode kernel runs beside the prefill kernel
+// (kda_attn_tc.cuh; its CTAs start as SMs come free) and does not end before that has; the first merge
+// waits for the decode kernel and so for both, the second one for the first.  Decode kernel after the
+// prefill kernel's end, 16 heads over 4: 16 ragged sequences 85.5 us against 81.2, without a window
+// 128.9 : 123.1, 64 of 4096 to 8192 keys 453.5 : 438.0.
 cudaError_t launch_attn(const AttnParams& p, int sms, cudaStream_t stream) {
   const int group = p.heads / p.c.kv_heads;
   const int64_t rows = (int64_t)p.max_q_len * group;
@@ -61,11 +70,13 @@ cudaError_t launch_attn(const AttnParams& p, int sms, cudaStream_t stream) {
   CacheMaps maps;
   if (!make_cache_maps(p.c, &maps)) return cudaErrorNotSupported;
   cudaError_t e = cudaSuccess;
-  const int64_t least = many && few > 0 ? (int64_t)kFewUnits * sms : 0;
-  if (many && (e = launch_attn_prefill(p, maps, few, least, work2, sms, stream)) != cudaSuccess) return e;
-  if (few > 0 && (e = launch_attn_decode(p, maps, few, least, many, work, sms, stream)) != cudaSuccess) return e;
+  const bool both = many && few > 0;
+  const int64_t least = both ? (int64_t)kFewUnits * sms : 0;
+  const int gate = both ? call_number() : 0;
+  if (many && (e = launch_attn_prefill(p, maps, few, least, gate, work2, sms, stream)) != cudaSuccess) return e;
+  if (few > 0 && (e = launch_attn_decode(p, maps, few, least, gate, work, sms, stream)) != cudaSuccess) return e;
   if (few > 0 && (e = launch_attn_decode_merge(p, few, work, sms, stream)) != cudaSuccess) return e;
-  return many ? launch_attn_prefill_merge(p, work2, sms, few == 0, stream) : cudaSuccess;
+  return many ? launch_attn_prefill_merge(p, gate, work2, sms, stream) : cudaSuccess;
 }
 
 }  // namespace attn

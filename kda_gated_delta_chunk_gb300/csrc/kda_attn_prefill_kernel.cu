@@ -77,7 +77,7 @@ struct PrefillParams {
   CacheMaps maps;
   int group;                 // query heads of a kv head
   uint32_t group_magic;      // 65535 / group + 1 (div_small)
-  int wait;                  // wait for the kernel before this one (programmatic launch)
+  int gate;                  // the call's number, when the decode kernel runs beside this one; else 0
   int few, tokens;           // rows of the decode kernel's sequences at most; new tokens per row tile (256 / group)
   int64_t least;             // units of those below which this kernel takes them too
   PartDescP* desc;
@@ -210,9 +210,9 @@ __global__ void __launch_bounds__(kThreadsP, 1)
     tmem_alloc(smem_u32(&misc->tmem), 512);
     tmem_relinquish();
   }
-  // (launched as a programmatic dependent: of the work before this call, or of the decode kernel,
-  // which has waited for that and shares nothing with this one)
-  if (p.wait) pdl_wait();
+  // (launched as a programmatic dependent of the work before this call)
+  pdl_wait();
+  if (p.gate && tid == 0 && blockIdx.x == 0) st_release_gpu(p.a.status + kGateWord, p.gate);
   pdl_launch_dependents();
   if (tid == 0 && blockIdx.x == 0 && p.a.cu_seqlens[0] != 0) record_error(p.a.status, KDA_ERR_BAD_CU_SEQLENS, 330);
 
@@ -953,8 +953,6 @@ __global__ void __launch_bounds__(kThreadsP, 1)
     }
     if (!ok && lane == 0) record_error(p.a.status, KDA_ERR_DEVICE_TIMEOUT, 336);
   }
-  // (beside the decode kernel: this grid does not end before that one)
-  if (blockIdx.x == 0 && warp == 0) pdl_wait();
   tc_fence_before();
   __syncthreads();
   if (warp == kSoftWarps + 5) {
@@ -968,9 +966,9 @@ __global__ void __launch_bounds__(kThreadsP, 1)
 constexpr int kMergeRows = 8;
 __global__ void __launch_bounds__(32 * kMergeRows)
     kda_attn_prefill_merge_kernel(const __grid_constant__ PrefillParams p) {
-  // (not waiting: one CTA still does, so that this grid does not end before the one beside it)
-  if (p.wait || (blockIdx.x == 0 && blockIdx.y == 0)) pdl_wait();
-  if (p.wait) pdl_launch_dependents();
+  pdl_wait();
+  pdl_launch_dependents();
+  if (p.gate && threadIdx.x == 0 && blockIdx.x == 0 && blockIdx.y == 0) p.a.status[kGateWord] = 0;
   const int4 d4 = *reinterpret_cast<const int4*>(p.desc + blockIdx.x);
   const PartDescP d = {d4.x, d4.y, d4.z, d4.w};
   const int lane = threadIdx.x & 31, r = blockIdx.y * kMergeRows + (threadIdx.x >> 5);
@@ -1047,9 +1045,9 @@ size_t prefill_workspace_bytes(int sms) {
 }
 
 namespace {
-void make_params(const AttnParams& a, int few, int64_t least, void* work, int sms, PrefillParams* d) {
+void make_params(const AttnParams& a, int few, int64_t least, int gate, void* work, int sms, PrefillParams* d) {
   d->a = a;
-  d->wait = 0;
+  d->gate = gate;
   d->few = few;
   d->least = least;
   d->group = a.heads / a.c.kv_heads;
@@ -1061,19 +1059,17 @@ void make_params(const AttnParams& a, int few, int64_t least, void* work, int sm
 }  // namespace
 
 cudaError_t launch_attn_prefill(const AttnParams& a, const CacheMaps& maps, int few, int64_t least,
-                                void* work, int sms, cudaStream_t stream) {
+                                int gate, void* work, int sms, cudaStream_t stream) {
   PrefillParams d;
-  make_params(a, few, least, work, sms, &d);
+  make_params(a, few, least, gate, work, sms, &d);
   d.maps = maps;
-  d.wait = 1;
   return a.softcap > 0.0f ? launch_cap<true>(d, sms, stream) : launch_cap<false>(d, sms, stream);
 }
 
-cudaError_t launch_attn_prefill_merge(const AttnParams& a, void* work, int sms, bool wait,
+cudaError_t launch_attn_prefill_merge(const AttnParams& a, int gate, void* work, int sms,
                                       cudaStream_t stream) {
   PrefillParams d = {};
-  make_params(a, 0, 0, work, sms, &d);
-  d.wait = wait;
+  make_params(a, 0, 0, gate, work, sms, &d);
   return launch(kda_attn_prefill_merge_kernel, dim3((unsigned)sms, kRowsP / kMergeRows),
                 dim3(32 * kMergeRows), 0, true, stream, d);
 }

@@ -232,23 +232,30 @@ struct CacheMaps {
 bool make_cache_maps(const CacheView& c, CacheMaps* m);
 
 // ------------------------------------------------------------ the kernels of a call
+// With both kernels in a call the decode kernel runs beside the prefill kernel, whose programmatic
+// dependent it is: were it to wait for that grid, as a dependent does for what it reads, nothing
+// would overlap.  It reads nothing of the prefill kernel's, only what the work before the call
+// wrote, and gets that through a word of the workspace: a thread of the prefill kernel, having
+// waited for that work, stores the call's number there (release) before it lets dependents start, and
+// the decode kernel's CTAs load it (acquire).  A CTA that does not find the number waits for the
+// whole prefill grid instead.  The last kernel of the call sets the word back to 0.
+constexpr int kGateWord = 16;      // int index in the workspace's 256 bytes of status words
 // Sequences with at most max_rows (at most 32) rows: new tokens x heads per kv head, unless they
-// add up to fewer than `least` units.  `beside`: launched as the programmatic dependent of the
-// prefill kernel, which it shares nothing with.
+// add up to fewer than `least` units.  `gate`: the call's number when the prefill kernel is launched
+// before it, else 0.
 size_t decode_workspace_bytes(int sms);
 cudaError_t launch_attn_decode(const AttnParams& p, const CacheMaps& maps, int max_rows, int64_t least,
-                               bool beside, void* work, int sms, cudaStream_t stream);
+                               int gate, void* work, int sms, cudaStream_t stream);
 // Sequences with more than `few` rows, and the others when those add up to fewer than `least`
 // units (heads per kv head at most 256).
 size_t prefill_workspace_bytes(int sms);
 cudaError_t launch_attn_prefill(const AttnParams& p, const CacheMaps& maps, int few, int64_t least,
-                                void* work, int sms, cudaStream_t stream);
+                                int gate, void* work, int sms, cudaStream_t stream);
 // The parts of items that the cut divided, merged: as the programmatic dependent of the kernel
-// before (the decode kernel; with `wait` the prefill kernel, else the merge of the decode kernel's,
-// beside which this one runs).
+// before, which they wait for.
 cudaError_t launch_attn_decode_merge(const AttnParams& p, int max_rows, void* work, int sms,
                                      cudaStream_t stream);
-cudaError_t launch_attn_prefill_merge(const AttnParams& p, void* work, int sms, bool wait,
+cudaError_t launch_attn_prefill_merge(const AttnParams& p, int gate, void* work, int sms,
                                       cudaStream_t stream);
 
 // ------------------------------------------------------------ one sequence of a batch

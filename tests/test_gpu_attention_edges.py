@@ -184,3 +184,73 @@ def test_caps_of_any_size(softcap, q_lens, kv_lens, H, hk):
     out, lse, status = launch(d, softcap=softcap)
     assert status == kda.OK
     check(d, out, lse, softcap=softcap)
+
+
+def test_mixed_calls_follow_the_work_before_them():
+    """Calls with both kernels right behind the kernels that write their queries, cache and lengths,
+    over one workspace, eagerly and from a graph with several such calls: the rows are those of
+    the same steps with the GPU waited for between them, and the workspace's status words are left zero."""
+    H, hk, page, steps = 16, 4, 64, 6
+    q_lens = [1] * 40 + [70, 200]
+    base = [2500 + 13 * n for n in range(42)]     # (more than the prefill kernel takes along)
+    N, T = len(q_lens), sum(q_lens)
+    width = (max(base) + steps * 200) // page + 2
+    g = torch.Generator(device="cuda").manual_seed(71)
+    table = torch.randperm(N * width, generator=g, device="cuda").int().view(N, width)
+    cu = torch.tensor([0] + torch.tensor(q_lens).cumsum(0).tolist(), dtype=torch.int32, device="cuda")
+    step = torch.tensor(q_lens, dtype=torch.int32, device="cuda")
+    rope = kda.rope_table(width * page, D)
+    qkv = torch.randn(steps, T, H + 2 * hk, D, generator=g, device="cuda").to(BF16)
+    status = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    ws = kda.alloc_attention_workspace(N, H, hk, 200)
+    first = [torch.randint(0, 0x70, (N * width, hk, page, D), generator=g, device="cuda", dtype=torch.uint8)
+             for _ in range(2)] + [torch.full((N * width, hk), 2.0 ** -7, device="cuda") for _ in range(2)]
+
+    def run(wait, cache, lens, x):
+        for a, b in zip(cache, first):
+            a.copy_(b)
+        lens.copy_(torch.tensor(base, dtype=torch.int32))
+        rows = []
+        for i in range(steps):
+            lens.add_(step)
+            x.copy_(qkv[i])
+            q = kda.rope_append(*x.split((H, hk, hk), 1), rope, *cache, table, lens, cu, workspace=status)
+            if wait:
+                torch.cuda.synchronize()
+            rows.append(kda.cached_attention(q, *cache, table, lens, cu, SCALE, 200, lse=True, workspace=ws))
+            if wait:
+                torch.cuda.synchronize()
+        return [t for r in rows for t in r]
+
+    own = lambda: ([torch.empty_like(t) for t in first], torch.empty(N, dtype=torch.int32, device="cuda"),  # noqa: E731
+                   torch.empty_like(qkv[0]))
+    want = run(True, *own())
+    assert kda.last_device_status(ws) == kda.OK and not bool(ws[:256].any())
+    args = own()
+    for _ in range(5):
+        got = run(False, *args)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert not bool(ws[:256].any()) and not bool(status.any())
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    pinned = torch.tensor(base, dtype=torch.int32, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    cache, lens, x = args
+    with torch.cuda.graph(graph, stream=side):
+        for a, b in zip(cache, first):
+            a.copy_(b)
+        lens.copy_(pinned)
+        rows = []
+        for i in range(steps):
+            lens.add_(step)
+            x.copy_(qkv[i])
+            q = kda.rope_append(*x.split((H, hk, hk), 1), rope, *cache, table, lens, cu, workspace=status)
+            rows += kda.cached_attention(q, *cache, table, lens, cu, SCALE, 200, lse=True, workspace=ws)
+    for _ in range(4):
+        for t in rows:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(rows, want))
+    assert not bool(ws[:256].any())
