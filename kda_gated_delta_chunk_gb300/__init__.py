@@ -216,23 +216,31 @@ def last_device_status(workspace: torch.Tensor, stream=None) -> int:
                                             ctypes.c_void_p(s.cuda_stream)))
 
 
-def _other_stream(stream, device):
-    """The torch stream for a call's ``stream`` argument where that is not the current one, else None."""
-    if stream is None or stream.cuda_stream == torch.cuda.current_stream(device).cuda_stream:
-        return None
-    if isinstance(stream, torch.cuda.Stream):
-        return stream
-    return torch.cuda.ExternalStream(stream.cuda_stream, device=device)
+def _elsewhere(stream, t):
+    """Where a call on tensor ``t`` with this ``stream`` argument belongs: the stream, if another one
+    than the current one of t's device is named, or t's device, if another is current (the entry
+    points launch on the current device); None if it is already there."""
+    device = t.device
+    if device.type != "cuda":
+        return None          # (the checks will name it)
+    if stream is not None and stream.cuda_stream != torch.cuda.current_stream(device).cuda_stream:
+        if isinstance(stream, torch.cuda.Stream):
+            return stream
+        return torch.cuda.ExternalStream(stream.cuda_stream, device=device)
+    return torch.cuda.device(device) if device.index != torch.cuda.current_device() else None
 
 
-def _on_stream(side, call, given, *args, **kw):
-    """``call(*args, **kw)`` with ``side`` as the current stream.  What the call allocates then
-    belongs to that stream: a workspace is filled in order with the kernels that use it, and its
-    memory goes back to that stream's work only.  Outputs that the call allocated (those whose
-    ``given`` is None) are handed to the stream that was current."""
-    here = torch.cuda.current_stream(side.device)
-    with torch.cuda.stream(side):
-        done = call(*args, **kw)
+def _within(place, call, given, *args):
+    """``call(*args)`` with ``place`` (of ``_elsewhere``) as the current stream or device.  What the
+    call allocates then belongs to that stream: a workspace is filled in order with the kernels
+    that use it, and its memory goes back to that stream's work only.  Outputs that the call
+    allocated (those whose ``given`` is None) are handed to the stream that was current."""
+    if not isinstance(place, torch.cuda.Stream):
+        with place:
+            return call(*args)
+    here = torch.cuda.current_stream(place.device)
+    with torch.cuda.stream(place):
+        done = call(*args)
     for t, g in zip(done if isinstance(done, tuple) else (done,), given):
         if g is None and t is not None:
             t.record_stream(here)
@@ -295,9 +303,9 @@ def chunk_prefill_fwd(q, k, v, g, beta, A_log, dt_bias, lower_bound, scale,
     a caller's [R, H, 128] buffer.  Returns (out, final_state).  Asynchronous on ``stream``
     (default: the current torch stream).
     """
-    side = _other_stream(stream, q.device) if stream is not None else None
-    if side is not None:
-        return _on_stream(side, chunk_prefill_fwd, (out, final_state), q, k, v, g, beta, A_log, dt_bias,
+    place = _elsewhere(stream, q)
+    if place is not None:
+        return _within(place, chunk_prefill_fwd, (out, final_state), q, k, v, g, beta, A_log, dt_bias,
                           lower_bound, scale, initial_state, cu_seqlens, out, final_state, workspace,
                           state_dtype, None, vsplit, kernel, out_index)
     squeeze = q.dim() == 4
@@ -368,9 +376,9 @@ def recurrent_fwd(q, k, v, g, beta, A_log, dt_bias, lower_bound, scale, initial_
     token.  out_index as in chunk_prefill_fwd.  Returns (out, final_state, token_states or
     None).
     """
-    side = _other_stream(stream, q.device) if stream is not None else None
-    if side is not None:
-        return _on_stream(side, recurrent_fwd,
+    place = _elsewhere(stream, q)
+    if place is not None:
+        return _within(place, recurrent_fwd,
                           (out, final_state, token_states if isinstance(token_states, torch.Tensor) else None),
                           q, k, v, g, beta, A_log, dt_bias, lower_bound, scale, initial_state, cu_seqlens,
                           out, final_state, token_states, workspace, state_dtype, None, out_index)
@@ -433,9 +441,9 @@ def skinny_proj(x, w_ab, w_b, r: int = 128, y=None, z=None, workspace=None, stre
     ``skinny_proj_workspace_size(k, n_ab)`` bytes, reusable across calls on one stream.
     Returns (y, z).
     """
-    side = _other_stream(stream, x.device) if stream is not None else None
-    if side is not None:
-        return _on_stream(side, skinny_proj, (y, z), x, w_ab, w_b, r, y, z, workspace)
+    place = _elsewhere(stream, x)
+    if place is not None:
+        return _within(place, skinny_proj, (y, z), x, w_ab, w_b, r, y, z, workspace)
     if x.dim() != 2 or w_ab.dim() != 2 or w_b.dim() != 2:
         raise ValueError("x, w_ab and w_b must be 2-D")
     m, k = x.shape

@@ -1,9 +1,9 @@
 // Marshalling of the full-attention layer's usual calls in C++: on small calls the checks and
 // allocations of the Python binding take longer than the kernels.  A call that is usual -- plain
-// tensors of the right types, shapes and device, caches and indexes contiguous, outputs left to
-// the call, the current stream -- is checked, given its outputs and passed to the C entry point
-// here.  Anything else returns None without having done anything, and the Python binding, which
-// accepts more and names what is wrong, takes the call.
+// tensors of the right types and shapes on the current device, caches and indexes contiguous,
+// outputs left to the call, the current stream -- is checked, given its outputs and passed to the C
+// entry point here.  Anything else returns None without having done anything, and the Python
+// binding, which accepts more and names what is wrong, takes the call.
 #include <Python.h>
 
 #include <climits>
@@ -12,6 +12,7 @@
 #include <cstring>
 
 #include <ATen/ops/empty.h>
+#include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -26,6 +27,9 @@ using at::Tensor;
 decltype(&kda_add_rms_norm) norm_entry;
 decltype(&kda_rope_append) append_entry;
 decltype(&kda_cached_attention) attention_entry;
+
+// (the entry points launch on the current device)
+bool here(int64_t dev) { return dev == c10::cuda::current_device(); }
 
 // The tensor behind an argument; null for anything but a plain one.
 const Tensor* tensor(PyObject* o) { return THPVariable_CheckExact(o) ? &THPVariable_Unpack(o) : nullptr; }
@@ -115,7 +119,7 @@ PyObject* add_rms_norm(PyObject*, PyObject* const* args, Py_ssize_t n) {
   int64_t ldx, ldr = C;
   float eps;
   int32_t group;
-  if (C > INT32_MAX || !rows(x, dev, ScalarType::BFloat16, x->sizes(), &ldx)) UNUSUAL;
+  if (C > INT32_MAX || !here(dev) || !rows(x, dev, ScalarType::BFloat16, x->sizes(), &ldx)) UNUSUAL;
   const ScalarType wt = w->scalar_type();
   if ((wt != ScalarType::BFloat16 && wt != ScalarType::Float) || !dense(w, dev, wt, {C})) UNUSUAL;
   if (!number(args[3], &eps) || !PyUnicode_Check(args[4]) || !integer(args[5], &group)) UNUSUAL;
@@ -165,7 +169,7 @@ PyObject* rope_append(PyObject*, PyObject* const* args, Py_ssize_t n) {
   int64_t seqs, k_row, v_row, q_row, table_rows = 0, rot = 0;
   const Tensor* cu = lengths(args[10], dev, &seqs);
   kda_kv_cache c;
-  if (!cu || heads > INT32_MAX || k->size(2) != KDA_HEAD_DIM ||
+  if (!cu || !here(dev) || heads > INT32_MAX || k->size(2) != KDA_HEAD_DIM ||
       !rows(k, dev, ScalarType::BFloat16, k->sizes(), &k_row) ||
       !rows(v, dev, ScalarType::BFloat16, k->sizes(), &v_row) ||
       !rows(q, dev, ScalarType::BFloat16, {T, heads, KDA_HEAD_DIM}, &q_row) ||
@@ -211,7 +215,7 @@ PyObject* cached_attention(PyObject*, PyObject* const* args, Py_ssize_t n) {
   kda_kv_cache c;
   float scale, cap;
   int32_t max_q, window;
-  if (!cu || heads > INT32_MAX || !rows(q, dev, ScalarType::BFloat16, q->sizes(), &q_row) ||
+  if (!cu || !here(dev) || heads > INT32_MAX || !rows(q, dev, ScalarType::BFloat16, q->sizes(), &q_row) ||
       !dense(ws, dev, ScalarType::Byte, ws->sizes()) || !cache_of(args + 1, dev, seqs, &c) ||
       !number(args[8], &scale) || !integer(args[9], &max_q) || !number(args[10], &cap) ||
       !integer(args[11], &window) || !PyBool_Check(args[12]))

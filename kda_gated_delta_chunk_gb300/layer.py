@@ -22,8 +22,8 @@ import struct
 
 import torch
 
-from . import (ERR_INVALID_ARG, HEAD_DIM, KDAError, OK, STATE_BF16, STATE_F32, _on_stream,
-               _other_stream, lib)
+from . import (ERR_INVALID_ARG, HEAD_DIM, KDAError, OK, STATE_BF16, STATE_F32, _elsewhere,
+               _within, lib)
 
 _BF16, _F32 = torch.bfloat16, torch.float32
 _BYTES = (torch.float8_e4m3fn, torch.uint8)
@@ -226,9 +226,9 @@ def add_rms_norm(x, residual, weight, eps: float = 1e-6, want: str = "bf16", gro
         if done is not None:
             raise KDAError(done, "kda_add_rms_norm")
     dev = _need_cuda(x, "x")
-    side = _other_stream(stream, x.device) if stream is not None else None
-    if side is not None:
-        return _on_stream(side, add_rms_norm, (residual_out, y, y8, y_scale), x, residual, weight, eps,
+    place = _elsewhere(stream, x)
+    if place is not None:
+        return _within(place, add_rms_norm, (residual_out, y, y8, y_scale), x, residual, weight, eps,
                           want, group, residual_out, y, y8, y_scale)
     shape = x.shape
     if len(shape) != 2:
@@ -305,9 +305,9 @@ def rope_append(q, k, v, rope, k_cache, v_cache, k_scale, v_scale, block_table, 
         if done is not None:
             return done
     dev = _need_cuda(k, "k")
-    side = _other_stream(stream, k.device) if stream is not None else None
-    if side is not None:
-        return _on_stream(side, rope_append, (q_out,), q, k, v, rope, k_cache, v_cache, k_scale, v_scale,
+    place = _elsewhere(stream, k)
+    if place is not None:
+        return _within(place, rope_append, (q_out,), q, k, v, rope, k_cache, v_cache, k_scale, v_scale,
                           block_table, kv_lens, cu_seqlens, interleaved, positions, q_out, workspace)
     shape = k.shape
     if len(shape) != 3:
@@ -390,9 +390,9 @@ def cached_attention(q, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens
         if done is not None:
             raise KDAError(done, "kda_cached_attention")
     dev = _need_cuda(q, "q")
-    side = _other_stream(stream, q.device) if stream is not None else None
-    if side is not None:
-        return _on_stream(side, cached_attention, (out, lse if isinstance(lse, torch.Tensor) else None), q,
+    place = _elsewhere(stream, q)
+    if place is not None:
+        return _within(place, cached_attention, (out, lse if isinstance(lse, torch.Tensor) else None), q,
                           k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, cu_seqlens, scale,
                           max_q_len, softcap, window, out, lse, workspace)
     shape = q.shape

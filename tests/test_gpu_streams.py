@@ -116,3 +116,34 @@ def test_other_stream_objects():
     b = call([], stream=h)
     torch.cuda.synchronize()
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_a_call_runs_on_its_tensors_device(name, monkeypatch):
+    """With another device current (here: said to be), the call is made again with the tensors' one."""
+    fresh, call = CALLS[name]()
+    want = call(fresh())
+    now, entered = [1], []
+
+    class Device(torch.cuda.device):
+        def __enter__(self):
+            entered.append(self.idx)
+            now.append(self.idx)
+            return super().__enter__()
+
+        def __exit__(self, *a):
+            now.pop()
+            return super().__exit__(*a)
+
+    class NoNative:          # (the C++ marshalling asks the runtime itself, and leaves such calls alone)
+        add_rms_norm = rope_append = cached_attention = staticmethod(lambda *a: None)
+
+    monkeypatch.setattr(kda.layer, "_native", NoNative)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: now[-1])
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    got = call(fresh())
+    monkeypatch.undo()
+    assert 0 in entered and now == [1]
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert (a is None) == (b is None) and (a is None or torch.equal(a.view(torch.uint8), b.view(torch.uint8)))
