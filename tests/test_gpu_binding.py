@@ -103,3 +103,15 @@ def test_what_is_not_usual_is_left_alone():
     assert type(native.cached_attention(*good[:9], 0, *good[10:])) is int      # refused by the entry point
     with pytest.raises(kda.KDAError):
         kda.cached_attention(*good[:9], 0, workspace=ws)
+
+
+def test_without_the_module_the_results_are_the_same(monkeypatch, tmp_path):
+    from kda_gated_delta_chunk_gb300 import build as kbuild
+    x, w = torch.randn(4, 64, device="cuda").to(BF16), torch.ones(64, dtype=BF16, device="cuda")
+    want = kda.add_rms_norm(x, x, w, 1e-6, "both", 128)
+    monkeypatch.setattr(kbuild, "binding_path", lambda: str(tmp_path / "none.so"))
+    monkeypatch.setattr(layer, "_native", None)
+    with pytest.warns(RuntimeWarning):
+        got = kda.add_rms_norm(x, x, w, 1e-6, "both", 128)
+    for a, b in zip(got, want):
+        same(a, b)

@@ -184,3 +184,19 @@ def test_sizes_past_32_bits_are_refused(args):
     with pytest.raises(kda.KDAError) as e:
         kda.attention_workspace_size(*args)
     assert e.value.code == kda.ERR_INVALID_ARG
+
+
+def test_without_the_marshalling_module_the_python_code_takes_the_calls(monkeypatch, tmp_path):
+    """... with one warning; it is built per torch version, and a call does not need it."""
+    from kda_gated_delta_chunk_gb300 import layer
+    monkeypatch.setattr(kbuild, "binding_path", lambda: str(tmp_path / "none.so"))
+    monkeypatch.setattr(layer, "_native", None)
+    x = torch.zeros(2, 64, dtype=torch.bfloat16)
+    with pytest.warns(RuntimeWarning, match="none.so is missing"):
+        with pytest.raises(ValueError, match="CUDA tensor"):
+            kda.add_rms_norm(x, x, x[0])
+    import warnings
+    with warnings.catch_warnings():
+        warnings.simplefilter("error")
+        with pytest.raises(ValueError, match="CUDA tensor"):
+            kda.add_rms_norm(x, x, x[0])
