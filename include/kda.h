@@ -422,8 +422,9 @@ int kda_rope_append(const void* q, int64_t q_stride, const void* k, int64_t k_st
  * max_q_len: an upper bound of the new tokens of one sequence (host-known); a sequence with
  * more records KDA_ERR_INVALID_ARG on the device and its rows are not written.  The workspace
  * holds the status words and partial results: kda_attention_workspace_size() bytes for the
- * same num_seqs, heads, kv_heads and max_q_len (or larger ones), zero-filled once before its
- * first use; calls that overlap need one each.  A sequence may have 2^31 - 128 cached tokens.
+ * same num_seqs, heads, kv_heads and max_q_len or larger ones (each on its own: the size never
+ * falls as one of them grows), zero-filled once before its first use; calls that overlap need
+ * one each.  A sequence may have 2^31 - 128 cached tokens.
  * Device errors otherwise as kda_rope_append.
  */
 size_t kda_attention_workspace_size(int32_t num_seqs, int32_t heads, int32_t kv_heads,

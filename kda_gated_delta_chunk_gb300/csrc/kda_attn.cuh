@@ -144,7 +144,9 @@ struct AttnParams {
   int32_t num_seqs, heads, max_q_len;
   int* status;               // workspace: 256 bytes of status words, then the partial results
 };
-size_t attn_workspace_bytes(int32_t num_seqs, int32_t heads, int32_t kv_heads, int32_t max_q_len);
+// What serves any call with at most these sizes, and what one of exactly these uses.
+size_t attn_workspace_bytes(int32_t heads, int32_t max_q_len);
+size_t attn_call_bytes(int32_t heads, int32_t kv_heads, int32_t max_q_len);
 cudaError_t launch_attn(const AttnParams& p, int sms, cudaStream_t stream);
 
 // The sequence that token t belongs to: the last n with cu[n] <= t (cu non-decreasing,

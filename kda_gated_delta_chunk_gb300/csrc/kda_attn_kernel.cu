@@ -41,8 +41,15 @@ int decode_rows(int64_t rows, int group) {
 
 }  // namespace
 
-size_t attn_workspace_bytes(int32_t num_seqs, int32_t heads, int32_t kv_heads, int32_t max_q_len) {
-  (void)num_seqs;
+// The parts that some call with at most these sizes lays out: one with fewer heads or kv heads
+// may have a larger group and need what this one does not.
+size_t attn_workspace_bytes(int32_t heads, int32_t max_q_len) {
+  const int sms = device_sms();
+  return (size_t)kWorkspaceBytes + (max_q_len > 0 ? align16(decode_workspace_bytes(sms)) : 0) +
+         ((int64_t)heads * max_q_len > kDecodeRows ? prefill_workspace_bytes(sms) : 0);
+}
+
+size_t attn_call_bytes(int32_t heads, int32_t kv_heads, int32_t max_q_len) {
   const int sms = device_sms(), group = heads / kv_heads;
   const int64_t rows = (int64_t)max_q_len * group;
   const int few = decode_rows(rows, group);

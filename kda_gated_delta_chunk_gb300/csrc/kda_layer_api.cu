@@ -195,7 +195,7 @@ size_t kda_attention_workspace_size(int32_t num_seqs, int32_t heads, int32_t kv_
   if (num_seqs < 0 || heads < 1 || kv_heads < 1 || heads % kv_heads != 0 ||
       heads / kv_heads > 256 || max_q_len < 0)
     return 0;
-  return (kda::attn::attn_workspace_bytes(num_seqs, heads, kv_heads, max_q_len) + 15) & ~(size_t)15;
+  return (kda::attn::attn_workspace_bytes(heads, max_q_len) + 15) & ~(size_t)15;
 }
 
 int kda_cached_attention(const void* q, int64_t q_stride, const kda_kv_cache* cache,
@@ -217,7 +217,7 @@ int kda_cached_attention(const void* q, int64_t q_stride, const kda_kv_cache* ca
     if (max_q_len < 1) return KDA_ERR_INVALID_ARG;
   }
   if (!aligned(lse, 4)) return KDA_ERR_MISALIGNED;
-  if (workspace_bytes < kda::attn::attn_workspace_bytes(num_seqs, heads, cache->kv_heads, max_q_len))
+  if (workspace_bytes < kda::attn::attn_call_bytes(heads, cache->kv_heads, max_q_len))
     return KDA_ERR_WORKSPACE_TOO_SMALL;
   int sms = 0;
   rc = current_device(&sms);

@@ -431,7 +431,10 @@ def cached_attention(q, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens
             _check(lse, "lse", _FLOAT, (T, heads), dev, 0)
         lse_ptr = lse.data_ptr()
     if workspace is None:
-        workspace = alloc_attention_workspace(N, heads, hk, max_q_len, dev)
+        # (this call's alone: its status words are zeroed, the rest is written before it is read)
+        workspace = torch.empty(max(attention_workspace_size(N, heads, hk, max_q_len), 256),
+                                dtype=torch.uint8, device=dev)
+        workspace[:256].zero_()
     else:
         _check(workspace, "workspace", _UINT8, workspace.shape, dev, 0)
     rc = lib().kda_cached_attention(

@@ -200,3 +200,22 @@ def test_without_the_marshalling_module_the_python_code_takes_the_calls(monkeypa
         warnings.simplefilter("error")
         with pytest.raises(ValueError, match="CUDA tensor"):
             kda.add_rms_norm(x, x, x[0])
+
+
+SIZES = [(h, kv, q) for h in (1, 2, 8, 32, 33, 64, 96, 256) for kv in (1, 2, 4, 8, 32, 64)
+         if h % kv == 0 for q in (0, 1, 2, 4, 8, 33, 300)]
+
+
+def test_attention_workspace_grows_with_every_size(L):
+    """A workspace sized for larger heads, kv heads, sequences or query lengths (each on its own)
+    serves the smaller call: the size does not fall, and the call does not refuse it."""
+    size = {a: kda.attention_workspace_size(3, *a) for a in SIZES}
+    for (h, kv, q), n in size.items():
+        assert n > 0 and kda.attention_workspace_size(7, h, kv, q) >= n
+        for (h2, kv2, q2), m in size.items():
+            if h2 <= h and kv2 <= kv and q2 <= q:
+                assert m <= n, ((h2, kv2, q2), (h, kv, q))
+                if q2:
+                    c = cache(kv_heads=kv2, scale_stride=kv2)
+                    rc = attend(L, c, T=0, N=0, H=h2, qs=h2 * 128, os=h2 * 128, mq=q2, wsb=n)   # launches nothing
+                    assert rc in (kda.OK, kda.ERR_CUDA, kda.ERR_UNSUPPORTED_DEVICE), (rc, h2, kv2, q2)
