@@ -93,3 +93,29 @@ def test_a_faulty_sequence_leaves_the_others_whole(broken, inter):
         raw, scale = before[c]
         rc.q[own], rc.s[own] = raw[own].float().double(), scale[own].double()
         check_cache(caches[i], caches[2 + i], rc, c == "v")
+
+
+def test_pages_past_32_bits():
+    """Appends to pages more than 4 GB into the pool, one of them partly filled."""
+    page, hk, pages = 128, 8, 36000      # 131072 bytes a page: 4.7 GB
+    d = make([150, 1], [100, 0], 2, hk, page, 64, seed=7)
+    small = on_gpu(d, "hpd")
+    want_q, status = run(d, small)
+    assert status == kda.OK
+    big = [torch.zeros(pages, hk, page, 128, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn) for _ in range(2)]
+    big += [torch.ones(pages, hk, device="cuda") for _ in range(2)]
+    far = {0: [35999, 33000], 1: [35500]}
+    d2 = dict(d, table=torch.zeros_like(d["table"]))
+    for n, pgs in far.items():
+        for b, f in enumerate(pgs):
+            src = int(d["table"][n, b])
+            d2["table"][n, b] = f
+            for x, raw in zip(big, (d["k_raw"], d["v_raw"], d["k_scale"], d["v_scale"])):
+                x[f] = raw[src].cuda()
+    q, status = run(d2, big)
+    assert status == kda.OK and torch.equal(q, want_q)
+    for n, pgs in far.items():
+        for b, f in enumerate(pgs):
+            src = int(d["table"][n, b])
+            for x, y in zip(big, small):
+                assert torch.equal(x[f].contiguous().view(torch.uint8), y[src].contiguous().view(torch.uint8))

@@ -254,3 +254,52 @@ def test_mixed_calls_follow_the_work_before_them():
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(rows, want))
     assert not bool(ws[:256].any())
+
+
+@pytest.mark.parametrize("softcap", [0.0, 30.0, 1e4])
+@pytest.mark.parametrize("q_lens,kv_lens,H,hk", [([1, 3], [700, 90], 8, 2), ([4, 2], [300, 200], 32, 8), ([130, 1], [400, 300], 4, 2)])
+def test_a_query_that_is_no_number_stays_in_its_row(softcap, q_lens, kv_lens, H, hk):
+    """NaN or infinite entries of a query make its own row NaN (token and head), and no other."""
+    d = make(q_lens, kv_lens, H, hk, 16, seed=73)
+    clean, clean_lse, _ = launch(d, softcap=softcap)
+    bad = dict(d, q=d["q"].clone())
+    want = torch.zeros(sum(q_lens), H, dtype=torch.bool)
+    for i, (t, h, x) in enumerate([(0, 0, math.nan), (0, H - 1, math.inf), (sum(q_lens) - 1, 1, -math.inf),
+                                   (sum(q_lens) // 2, 2, math.nan)]):
+        bad["q"][t, h, 5 * i] = x
+        want[t, h] = True
+    out, lse, status = launch(bad, softcap=softcap)
+    assert status == kda.OK
+    assert torch.equal(out.cpu().isnan().all(-1), want) and torch.equal(out.cpu().isnan().any(-1), want)
+    assert torch.equal(lse.cpu().isnan(), want)
+    assert torch.equal(out.cpu()[~want], clean.cpu()[~want]) and torch.equal(lse.cpu()[~want], clean_lse.cpu()[~want])
+
+
+@pytest.mark.parametrize("scale", [-D ** -0.5, 0.0, 1.0])
+@pytest.mark.parametrize("softcap", [0.0, 3.0])
+def test_scales_of_any_sign(scale, softcap):
+    q_lens, kv_lens, H, hk, page = [1, 4, 90], [300, 77, 200], 8, 2, 16
+    d = make(q_lens, kv_lens, H, hk, page, seed=75)
+    g = {k: v.cuda() if isinstance(v, torch.Tensor) else v for k, v in d.items()}
+    out, lse = kda.cached_attention(g["q"], g["k"], g["v"], g["ks"], g["vs"], g["table"], g["kv"], g["cu"], scale,
+                                    90, softcap=softcap, lse=True)
+    kf, vf = d["k"].view(FP8).float(), d["v"].view(FP8).float()
+    for n in range(3):
+        a, b = int(d["cu"][n]), int(d["cu"][n + 1])
+        args = (d["ks"], d["vs"], d["table"][n], kv_lens[n], scale, softcap)
+        o64, l64 = ref.attention(d["q"][a:b], kf, vf, *args)
+        big, _ = ref.attention(d["q"][a:b], kf, vf.abs(), *args)
+        # as in test_gpu_attention, with |k|_1 below 128 times the largest |k| (3.5 here)
+        es = 2.0 ** -14 * abs(scale) * d["q"][a:b].double().abs().amax(-1) * 128 * 3.5
+        assert bool(((out[a:b].cpu().double() - o64).abs()
+                     <= 2.0 ** -8 * o64.abs() + (2.0 ** -7 + 2.0 ** -14 + 2 * es[..., None]) * big).all())
+        assert bool(((lse[a:b].cpu().double() - l64).abs() <= es + 2.0 ** -20 * l64.abs() + 2.0 ** -20).all())
+
+
+def test_the_largest_group():
+    """256 query heads of one kv head, and 255: a row tile is one token."""
+    for H in (256, 255):
+        d = make([3, 1], [200, 500], H, 1, 64, seed=77)
+        out, lse, status = launch(d)
+        assert status == kda.OK
+        check(d, out, lse)
