@@ -184,7 +184,8 @@ __global__ void __launch_bounds__(kThreads, 65536 / kRegs / kThreads)
     SeqPages q = seq_pages(p, n, false);
     int blk = (int)(page0 - first_s), unit = (int)(u - page0 * (2 * hk));   // page of the sequence, unit of the page
     // ---- the units: keys or values of one (page, kv head)
-    for (uint32_t par = 0; u < u_end; ++u, par ^= 1) {
+    uint32_t par = 0;      // buffer of the warps' maxima: the other one at each unit that reaches the barrier
+    for (; u < u_end; ++u) {
       while (blk >= q.pages) {
         if (++n >= N) return;   // (lengths that changed under the kernel)
         q = seq_pages(p, n, false);
@@ -270,6 +271,7 @@ __global__ void __launch_bounds__(kThreads, 65536 / kRegs / kThreads)
       if ((tid & 31) == 0) top_s[par][warp] = top;
       __syncthreads();              // (the other parity's readers are past the barrier before this)
       for (int w = 0; w < warps; ++w) top = fmaxf(top, top_s[par][w]);
+      par ^= 1;
       float scale = pow2_scale(top);
       if (s0 > 0) scale = fmaxf(scale, old);
       const float inv = 1.0f / scale;

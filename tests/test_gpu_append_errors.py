@@ -119,3 +119,31 @@ def test_pages_past_32_bits():
             src = int(d["table"][n, b])
             for x, y in zip(big, small):
                 assert torch.equal(x[f].contiguous().view(torch.uint8), y[src].contiguous().view(torch.uint8))
+
+
+@pytest.mark.parametrize("page,step", [(64, 64), (128, 128), (16, 40), (128, 9)])
+def test_bad_pages_between_good_ones(page, step):
+    """Every other page of a long batch is outside the pool: a CTA passes over such units between good
+    ones, whose maxima are its own (rows of very different size from page to page)."""
+    n, hk = 60, 4
+    lens = [step] * n
+    d, good = (make(lens, [0] * n, 2, hk, page, 0, seed=11) for _ in range(2))
+    g = torch.Generator().manual_seed(13)
+    e = torch.randint(-12, 13, (n, hk), generator=g)
+    for x in (d, good):
+        for c in "kv":
+            x[c] = (x[c].float() * torch.ldexp(torch.ones(n, hk), e).repeat_interleave(step, 0)[..., None]).to(x[c].dtype)
+    for seq in range(0, n, 2):
+        d["table"][seq] = -1
+    expect(good)
+    for seq in range(0, n, 2):       # nothing of these is stored
+        pg = good["table"][seq, :-(-step // page)].long()
+        for c in "kv":
+            good[c + "_ref"].q[pg] = d[c + "_raw"].float()[pg].double()
+            good[c + "_ref"].s[pg] = d[c + "_scale"][pg].double()
+    for _ in range(10):
+        caches = on_gpu(d, "hpd")
+        status = run(d, caches)[1]
+        assert status == kda.ERR_BAD_CACHE_INDEX
+        check_cache(caches[0], caches[2], good["k_ref"], True)
+        check_cache(caches[1], caches[3], good["v_ref"], True)
