@@ -359,7 +359,7 @@ int kda_add_rms_norm(const void* x, int64_t ldx, const void* residual, int64_t l
  * j % page_size of page block_table[n * table_stride + j / page_size].  kv_lens[n] counts
  * the sequence's cached tokens INCLUDING the new ones of the step, for the append and for the
  * attention alike.  The value of an entry is its e4m3 value times its page's scale; a scale is
- * positive, and kda_rope_append makes it a power of two.
+ * positive and finite, and kda_rope_append makes it a power of two.
  */
 typedef struct kda_kv_cache {
   void* k;                     /* 16-byte aligned                                */
@@ -419,6 +419,15 @@ int kda_rope_append(const void* q, int64_t q_stride, const void* k, int64_t k_st
  * NaN included; an entry that one query does not see does not reach that query's row.  The same
  * holds for the scales of such pages, and block_table entries of pages that lie wholly before the
  * window of a sequence's first new query, or past its length, are not followed.
+ * Precision: scores, maxima, denominators and sums are fp32, rounded once to bf16.  A query enters
+ * the products as two e4m3 terms, exact to 2^-18 of the largest entry of its (token, head): what a
+ * row holds below that is lost, so entries a thousand times smaller than the largest keep a
+ * relative 2^-8.  A weight enters the product with the values to 2^-8 of itself and 2^-18 of its
+ * tile's largest in sequences of at most 32 rows (new tokens x heads per kv head), to 2^-11 in
+ * others; the denominators take it in fp32.  A capped score is exact to 2^-21 of itself, or for
+ * caps of at most 64 to 2^-22 of the cap.  The value scales of the pages that a row sees should lie
+ * within a factor of 2^100 of each other (beyond, the weights of the smaller ones leave fp32's range
+ * in the denominators).
  * max_q_len: an upper bound of the new tokens of one sequence (host-known); a sequence with
  * more records KDA_ERR_INVALID_ARG on the device and its rows are not written.  The workspace
  * holds the status words and partial results: kda_attention_workspace_size() bytes for the

@@ -124,7 +124,7 @@ struct Walk {
   }
 };
 
-template <int NR, bool kCap>
+template <int NR, int kCap>
 __global__ void __launch_bounds__(kThreads, 2)
     kda_attn_decode_kernel(const __grid_constant__ DecodeParams p) {
   using C = Cfg<NR>;
@@ -373,6 +373,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     uint4* poison = reinterpret_cast<uint4*>(sm + C::kOffPoison);
     float* qmul = reinterpret_cast<float*>(sm + C::kOffQmul);
     const Cap cap = kCap ? cap_of(p.a.softcap) : Cap{0.0f, 0.0f};
+    const float to_e = 2.0f * kLog2e * cap.inv;
     PartDesc part = {0, 0, 0, 0};
     uint32_t it = 0;
     // A wait that gives up clears its thread's `ok`; the thread leaves with the others, at a barrier
@@ -527,7 +528,10 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
           for (int e = 0; e < 4; ++e) x[r + e] = kCap ? x[r + e] * (m[e] * ks) : x[r + e] * (m[e] * ks) + lvs;
         }
-        if (kCap) {
+        if (kCap == kCapPlain) {
+#pragma unroll
+          for (int r = 0; r < NR; ++r) x[r] = cap_plain(x[r], to_e, cap, lvs);
+        } else if (kCap == kCapExact) {
           float top = 0.0f;
 #pragma unroll
           for (int r = 0; r < NR; r += 2) top = max3_abs(top, x[r], x[r + 1]);
@@ -814,7 +818,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
 
 int decode_ctas(int sms) { return 2 * sms; }
 
-template <int NR, bool kCap>
+template <int NR, int kCap>
 cudaError_t launch_nr(const DecodeParams& d, int sms, cudaStream_t stream) {
   static PerDeviceOnce once;
   int dev = 0;
@@ -827,6 +831,14 @@ cudaError_t launch_nr(const DecodeParams& d, int sms, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   return launch(kda_attn_decode_kernel<NR, kCap>, dim3((unsigned)decode_ctas(sms)), dim3(kThreads),
                 Cfg<NR>::kBytes, true, stream, d);
+}
+template <int NR>
+cudaError_t launch_cap(const DecodeParams& d, int sms, cudaStream_t stream) {
+  switch (cap_kind(d.a.softcap)) {
+    case kNoCap: return launch_nr<NR, kNoCap>(d, sms, stream);
+    case kCapPlain: return launch_nr<NR, kCapPlain>(d, sms, stream);
+    default: return launch_nr<NR, kCapExact>(d, sms, stream);
+  }
 }
 template <int NR>
 cudaError_t launch_merge(const DecodeParams& d, int sms, cudaStream_t stream) {
@@ -884,10 +896,8 @@ cudaError_t launch_attn_decode(const AttnParams& a, const CacheMaps& maps, int m
   make_params(a, max_rows, gate, work, sms, &d);
   d.maps = maps;
   d.least = least;
-  const bool cap = a.softcap > 0.0f;
-  if (max_rows <= 8) return cap ? launch_nr<8, true>(d, sms, stream) : launch_nr<8, false>(d, sms, stream);
-  if (max_rows <= 16) return cap ? launch_nr<16, true>(d, sms, stream) : launch_nr<16, false>(d, sms, stream);
-  return cap ? launch_nr<32, true>(d, sms, stream) : launch_nr<32, false>(d, sms, stream);
+  return max_rows <= 8 ? launch_cap<8>(d, sms, stream) : max_rows <= 16 ? launch_cap<16>(d, sms, stream)
+                                                                     : launch_cap<32>(d, sms, stream);
 }
 
 cudaError_t launch_attn_decode_merge(const AttnParams& a, int max_rows, void* work, int sms,

@@ -16,8 +16,8 @@
 //
 // Bound by the tensor cores: 4 x 128 flops per visible (row, key).  4096 tokens at the end of 16384,
 // 16 heads over 2: 326.6 us, 1473 TFLOP/s; 289 us with the softmax left out.  With capped scores
-// 585 us: the cap's polynomial (nine fp32 operations a score), and a tile's maximum before its
-// numerators.  Two halves keep the tensor cores busy: while one half's
+// 597 us (three special functions a score; caps above 64 585: nine fp32 operations and one), and a
+// tile's maximum before its numerators.  Two halves keep the tensor cores busy: while one half's
 // softmax runs, the other half's products do.  The matrix instructions of a CTA
 // run in the order they are issued, so S(i+1) of a half may follow its O += P(i) V, whose P it
 // overwrites, without a wait.  Key tiles of all (sequence, kv head, row tile) items are laid end
@@ -151,7 +151,7 @@ struct Segment {
   const int32_t* table;      // the sequence's pages
 };
 
-template <bool kCap>
+template <int kCap>
 __global__ void __launch_bounds__(kThreadsP, 1)
     kda_attn_prefill_kernel(const __grid_constant__ PrefillParams p) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -796,7 +796,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
               const float4 f = sc[g];
               const float mul = qmul * f.x, add = f.y;
               const uint32_t bits = (uint32_t)(see >> (32 * (g >> 1))) >> (16 * (g & 1));
-              if (kCap) {
+              if (kCap == kCapExact) {
                 float top = 0.0f;
 #pragma unroll
                 for (int e = 16 * g; e < 16 * g + 16; e += 2)
@@ -820,14 +820,15 @@ __global__ void __launch_bounds__(kThreadsP, 1)
                   }
                 }
               }
-              if (kCap && !masked) {
+              if (kCap == kCapExact && !masked) {
                 mt = fmaxf(mt, max_of(g));
                 continue;
               }
+              const float mul_e = mul * (2.0f * kLog2e * cap.inv);
 #pragma unroll
               for (int e = 0; e < 16; ++e) {
                 float x = __uint_as_float(s[16 * g + e]);
-                if (!kCap) x = fmaf(x, mul, add);
+                if (kCap != kCapExact) x = kCap ? cap_plain(x, mul_e, cap, add) : fmaf(x, mul, add);
                 if (!((bits >> e) & 1)) x = -INFINITY;
                 mt = fmaxf(mt, x);
                 s[16 * g + e] = __float_as_uint(x);
@@ -1019,7 +1020,7 @@ __global__ void __launch_bounds__(32 * kMergeRows)
     p.a.lse[tok * p.a.heads + head] = den == 0.0f ? -INFINITY : (m + lg2(den)) * kLn2;
 }
 
-template <bool kCap>
+template <int kCap>
 cudaError_t launch_cap(const PrefillParams& d, int sms, cudaStream_t stream) {
   static PerDeviceOnce once;
   int dev = 0;
@@ -1063,7 +1064,11 @@ cudaError_t launch_attn_prefill(const AttnParams& a, const CacheMaps& maps, int 
   PrefillParams d;
   make_params(a, few, least, gate, work, sms, &d);
   d.maps = maps;
-  return a.softcap > 0.0f ? launch_cap<true>(d, sms, stream) : launch_cap<false>(d, sms, stream);
+  switch (cap_kind(a.softcap)) {
+    case kNoCap: return launch_cap<kNoCap>(d, sms, stream);
+    case kCapPlain: return launch_cap<kCapPlain>(d, sms, stream);
+    default: return launch_cap<kCapExact>(d, sms, stream);
+  }
 }
 
 cudaError_t launch_attn_prefill_merge(const AttnParams& a, int gate, void* work, int sms,

@@ -176,7 +176,8 @@ def test_lengths_near_two_to_the_31():
 def test_caps_of_any_size(softcap, q_lens, kv_lens, H, hk):
     """A capped score keeps its relative precision whether it is small beside the cap or not: rows
     whose scores all are, rows with both, rows far beyond it.  The score's error of test_gpu_attention
-    holds: capping adds 2^-21 of the capped score at most, and 2^-14 of a bound of the score is there."""
+    holds: capping adds 2^-21 of the capped score at most (2^-22 of a cap up to 64: 2^-16), and 2^-14 of
+    a bound of the score is there (a sum of 128 magnitudes times the query's largest: 2^-13 and more)."""
     d = make(q_lens, kv_lens, H, hk, 32, seed=61)
     d["q"][:, 1] *= 0.05
     d["q"][:, 2] *= 40.0
