@@ -22,7 +22,7 @@
 // With the merge: 64 ragged sequences of up to 16384 tokens, 32 heads over 8, 67.4 us (5.4 TB/s);
 // 4 of 65536, 32 heads over 4, 50.0 us (5.4 TB/s), 16 of them 97% of the rate of a copy; 512 tokens
 // 8.8 us.  At 16 rows with capped scores the softmax of a tile takes as long as its copy (16 x 4
-// tokens over up to 16384: 52.7 us, 4.3 TB/s), at 32 rows longer (8 tokens each: 85 us, 2.7 TB/s).
+// tokens over up to 16384: 52.9 us, 4.3 TB/s), at 32 rows longer (8 tokens each: 86 us, 2.7 TB/s).
 //
 // Warps: 0-3 softmax and accumulation, 4 the TMA producer, 5 the MMA issuer.  Every wait is
 // bounded; one that gives up records KDA_ERR_DEVICE_TIMEOUT and the CTA leaves.
