@@ -9,6 +9,9 @@ the rest of the binding, marshalling only.  A cache is four tensors and two inde
     k_scale, v_scale   fp32 [pages, kv_heads]
     block_table        int32 [num_seqs, max_blocks]: the pages of each sequence, in order
     kv_lens            int32 [num_seqs]: cached tokens, the step's new ones included
+
+A call with ``stream`` allocates its outputs and workspace on that stream; the tensors given to it
+must be ready there.
 """
 from __future__ import annotations
 

@@ -172,7 +172,7 @@ def test_lengths_near_two_to_the_31():
 
 @pytest.mark.parametrize("softcap", [0.01, 2.0, 30.0, 1e3, 1e4, 1e5, 1e30, 3e38, 1e-44])
 @pytest.mark.parametrize("q_lens,kv_lens,H,hk", [([1, 1], [700, 90], 8, 2), ([4, 3], [300, 1000], 16, 4),
-                                                 ([130, 2], [400, 300], 4, 2)])
+                                                 ([8, 7], [900, 130], 16, 4), ([130, 2], [400, 300], 4, 2)])
 def test_caps_of_any_size(softcap, q_lens, kv_lens, H, hk):
     """A capped score keeps its relative precision whether it is small beside the cap or not: rows
     whose scores all are, rows with both, rows far beyond it.  The score's error of test_gpu_attention
