@@ -89,6 +89,10 @@ typedef struct CUstream_st* kda_stream_t;
                                             outside [0, out_rows)            */
 #define KDA_ERR_BAD_CACHE_INDEX (-11)    /* (device) a page index, cache length
                                             or position out of its range     */
+#define KDA_ERR_BAD_TREE (-12)           /* (device) a parent or an accepted
+                                            node out of its range            */
+#define KDA_ERR_OUT_OF_PAGES (-13)       /* (device) fewer free pages than the
+                                            call needs                       */
 
 /* kernel selectors for kda_chunk_prefill_fwd_ex */
 #define KDA_KERNEL_AUTO 0  /* SPLIT_STREAMED when N * heads * P <= SMs / 2 for
@@ -443,6 +447,48 @@ int kda_cached_attention(const void* q, int64_t q_stride, const kda_kv_cache* ca
                          void* out, int64_t out_stride, float* lse, void* workspace,
                          kda_stream_t stream, int64_t total_tokens, int32_t num_seqs, int32_t heads,
                          int32_t max_q_len, size_t workspace_bytes);
+
+/*
+ * Trees of drafted tokens, for speculative steps that verify more than one continuation.  A
+ * sequence's new tokens are the nodes of a forest over its cached text: parents[t] is the index,
+ * among the sequence's new tokens, of the one that token t follows, or -1 for one that follows
+ * the cached text itself.  A parent comes before its children (parents[t] < t's own index); any
+ * other entry records KDA_ERR_BAD_TREE and counts as -1.  At most KDA_TREE_NODES new tokens a
+ * sequence; max_q_len is a host-known upper bound as for the attention.  Tokens past
+ * cu_seqlens[num_seqs] are not touched.  Conventions as above: device pointers, asynchronous on
+ * `stream`, a workspace of at least 256 bytes with the status word.
+ *
+ * kda_tree_plan: what a step needs of its trees, once for all layers.
+ *   parents    int32 [T]
+ *   kv_lens    int32 [num_seqs]: cached tokens, the new ones included (as in kda_kv_cache)
+ *   mask       uint64 [T]: bit j set where the node descends from node j of its sequence or is it
+ *   positions  int32 [T]: kv_lens - new tokens + the node's depth (0 for those that follow the
+ *              cached text): the table rows for kda_rope_append
+ * A sequence whose kv_lens is below its new tokens' count records KDA_ERR_BAD_CACHE_INDEX, one
+ * with more than max_q_len of them KDA_ERR_INVALID_ARG; their rows are not written.
+ */
+#define KDA_TREE_NODES 64
+int kda_tree_plan(const int32_t* parents, const int32_t* cu_seqlens, const int32_t* kv_lens,
+                  void* mask, int32_t* positions, void* workspace, kda_stream_t stream,
+                  int64_t total_tokens, int32_t num_seqs, int32_t max_q_len, size_t workspace_bytes);
+
+/*
+ * Attention of a tree's nodes over the cache, which holds their own keys and values already (node i
+ * of a sequence with n nodes in position kv_lens - n + i, whatever its depth): kda_cached_attention
+ * but for what a query sees:
+ *   mask    uint64 [T]: node i sees every cached token before the nodes, and node j where bit j of
+ *           its mask is set (kda_tree_plan's, or any other; bits past the sequence's nodes do not count)
+ *   window  0, or at least max_q_len: a node sees the last `window` of those, in the order of the cache.
+ *           With the masks of kda_tree_plan that is the window by position, depth counted.
+ * A node that sees nothing gets a row of zeros and lse = -infinity.  A sequence whose kv_lens is
+ * below its nodes' count records KDA_ERR_BAD_CACHE_INDEX and its rows are not written.  Workspace as
+ * for kda_cached_attention (the same may serve both, one call after the other).
+ */
+int kda_tree_attention(const void* q, int64_t q_stride, const kda_kv_cache* cache,
+                       const int32_t* cu_seqlens, const void* mask, float scale, float softcap,
+                       int32_t window, void* out, int64_t out_stride, float* lse, void* workspace,
+                       kda_stream_t stream, int64_t total_tokens, int32_t num_seqs, int32_t heads,
+                       int32_t max_q_len, size_t workspace_bytes);
 
 /*
  * The value-dimension split factor the automatic path uses for a batch of

@@ -21,6 +21,7 @@ names follow the C ABI in ``include/kda.h``:
     status_string(code) -> str
     add_rms_norm, rope_table, rope_append, cached_attention: the full-attention layer beside the KDA layers
         (layer.py)
+    tree_plan, tree_attention: trees of drafted tokens (tree.py, layer.py)
 
 There is no CPU fallback: if the library is missing or the device is not an
 sm_103 GPU, these calls raise.
@@ -52,6 +53,9 @@ ERR_BAD_CU_SEQLENS = -8
 ERR_CUDA = -9
 ERR_BAD_OUT_INDEX = -10
 ERR_BAD_CACHE_INDEX = -11
+ERR_BAD_TREE = -12
+ERR_OUT_OF_PAGES = -13
+TREE_NODES = 64
 
 # every symbol include/kda.h declares
 EXPORTS = ("kda_workspace_size", "kda_chunk_prefill_fwd", "kda_chunk_prefill_fwd_ex",
@@ -60,7 +64,8 @@ EXPORTS = ("kda_workspace_size", "kda_chunk_prefill_fwd", "kda_chunk_prefill_fwd
            "kda_recurrent_fwd", "kda_chunk_prefill_fwd_noalloc", "kda_chunk_prefill_fwd_scatter",
            "kda_recurrent_fwd_scatter", "kda_skinny_proj_workspace_size", "kda_skinny_proj",
            "kda_test_drop_one_record", "kda_add_rms_norm", "kda_rope_append",
-           "kda_attention_workspace_size", "kda_cached_attention")
+           "kda_attention_workspace_size", "kda_cached_attention", "kda_tree_plan",
+           "kda_tree_attention")
 
 _lib = None
 _lock = threading.Lock()
@@ -153,6 +158,11 @@ def lib() -> ctypes.CDLL:
             L.kda_cached_attention.restype = I
             L.kda_cached_attention.argtypes = [P, I64, P, P, F, F, I32, P, I64, P, P, P, I64, I32,
                                                I32, I32, SZ]
+            L.kda_tree_plan.restype = I
+            L.kda_tree_plan.argtypes = [P, P, P, P, P, P, P, I64, I32, I32, SZ]
+            L.kda_tree_attention.restype = I
+            L.kda_tree_attention.argtypes = [P, I64, P, P, P, F, F, I32, P, I64, P, P, P, I64, I32, I32,
+                                             I32, SZ]
             _lib = L
     return _lib
 
@@ -518,4 +528,6 @@ def chunk_prefill_fwd_noalloc(q, k, v, g, beta, A_log, dt_bias, lower_bound, sca
 
 
 from .layer import (add_rms_norm, alloc_attention_workspace,  # noqa: E402  (uses the names above)
-                    attention_workspace_size, cached_attention, rope_append, rope_table)
+                    attention_workspace_size, cached_attention, rope_append, rope_table,
+                    tree_attention)
+from .tree import tree_plan  # noqa: E402

@@ -483,6 +483,8 @@ const char* kda_status_string(int status) {
     case KDA_ERR_CUDA: return "CUDA runtime error";
     case KDA_ERR_BAD_OUT_INDEX: return "an out_index entry lies outside [0, out_rows)";
     case KDA_ERR_BAD_CACHE_INDEX: return "a page index, cache length or position out of its range";
+    case KDA_ERR_BAD_TREE: return "a tree's parent or accepted node out of its range";
+    case KDA_ERR_OUT_OF_PAGES: return "fewer free pages than the call needs";
     default: return "unknown status";
   }
 }

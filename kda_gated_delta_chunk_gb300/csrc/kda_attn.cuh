@@ -140,6 +140,7 @@ struct AttnParams {
   CacheView c;
   float scale, softcap;      // softcap 0: none
   int32_t window;            // 0: none
+  const uint64_t* tree;      // [total_tokens] masks of a tree's nodes, or null (causal)
   int64_t total_tokens;
   int32_t num_seqs, heads, max_q_len;
   int* status;               // workspace: 256 bytes of status words, then the partial results

@@ -87,6 +87,7 @@ struct DecodeParams {
 
 // The walk over a CTA's range, segment by segment (every role runs its own).  The range is in
 // units: an item has kOver of them, then one per tile.
+template <bool kTree>
 struct Walk {
   int64_t pos, end, base;   // global unit; base: of sequence n's first
   int n, n0;                // sequence; the first of the cached ones
@@ -104,7 +105,7 @@ struct Walk {
           s = cache[n - n0];
         } else {
           int err;
-          s = seq_info(p.a, n, p.min_rows, p.max_rows, &err);
+          s = seq_info<kTree>(p.a, n, p.min_rows, p.max_rows, &err);
         }
       }
       const int size = s.tiles + kOver;
@@ -124,7 +125,7 @@ struct Walk {
   }
 };
 
-template <int NR, int kCap>
+template <int NR, int kCap, bool kTree>
 __global__ void __launch_bounds__(kThreads, 2)
     kda_attn_decode_kernel(const __grid_constant__ DecodeParams p) {
   using C = Cfg<NR>;
@@ -183,7 +184,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   auto cost = [&](int n, bool report) -> long long {
     if (n >= N) return 0;
     int err;
-    const SeqInfo s = seq_info(p.a, n, p.min_rows, p.max_rows, &err);
+    const SeqInfo s = seq_info<kTree>(p.a, n, p.min_rows, p.max_rows, &err);
     if (err != KDA_OK && report && blockIdx.x == 0) record_error(p.a.status, err, 311);
     return s.tiles ? (long long)(s.tiles + kOver) * hk : 0;
   };
@@ -202,7 +203,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   for (int w = 0; w < kThreads / 32; ++w) total += misc->part[w];
   __syncthreads();
   if (total < p.least) total = 0;
-  Walk walk;
+  Walk<kTree> walk;
   // (no more ranges than tiles: between two CTAs of an item there is none without a part)
   const int ranges = (int)min((long long)gridDim.x, total);
   walk.pos = walk.end = 0;
@@ -238,7 +239,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     walk.cache = reinterpret_cast<const SeqInfo*>(sm + C::kOffSeq);
     if (tid < kCached && walk.n + tid < N) {
       int err;
-      reinterpret_cast<SeqInfo*>(sm + C::kOffSeq)[tid] = seq_info(p.a, walk.n + tid, p.min_rows, p.max_rows, &err);
+      reinterpret_cast<SeqInfo*>(sm + C::kOffSeq)[tid] =
+          seq_info<kTree>(p.a, walk.n + tid, p.min_rows, p.max_rows, &err);
     }
   }
   tc_fence_before();
@@ -268,7 +270,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       const int b = (walk.s.tile0 + t++) * boxes + lane;
       // (a page wholly before every query's window is not looked up: its entry may be stale)
       if (lane >= boxes || b >= (walk.s.len + P - 1) / P ||
-          (b + 1) * P <= first_seen(walk.s.len - walk.s.q_len, p.a.window))
+          (b + 1) * P <= first_seen(low_pos<kTree>(walk.s.len - walk.s.q_len), p.a.window))
         return {walk.h, 0, true, false};
       return {walk.h, p.a.c.block_table[walk.n * p.a.c.table_stride + b], true, true};
     };
@@ -380,7 +382,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     // that has told them.
     bool ok = true;
     uint4 qraw[NR / 8];     // this thread's part of the next segment's queries, 16 lanes a row
-    auto load_q = [&](const Walk& w) {
+    auto load_q = [&](const Walk<kTree>& w) {
 #pragma unroll
       for (int i = 0; i < NR / 8; ++i) {
         const int r = 8 * i + (tid >> 4);
@@ -427,7 +429,11 @@ __global__ void __launch_bounds__(kThreads, 2)
       fence_proxy_async();
       mbar_arrive(bar_q);
       if (bar_any(1, 128, !ok)) { ok = false; break; }   // qmul is written (and nobody gave up)
-      Walk ahead = walk;
+      // a tree's masks: lane i that of node i (there are at most 32)
+      const uint32_t nodes =
+          kTree && lane < walk.s.q_len
+              ? (uint32_t)(p.a.tree[walk.s.tok0 + lane] & node_bits(walk.s.q_len)) : 0;
+      Walk<kTree> ahead = walk;
       more = ahead.next(p);
       if (more) load_q(ahead);
 
@@ -472,10 +478,19 @@ __global__ void __launch_bounds__(kThreads, 2)
           for (int x = 0; x < kTile; ++x) {
             if (!((w[4 * x + warp] >> lane) & 1)) continue;
             const int key = (walk.s.tile0 + t) * kTile + x;
+            uint32_t seen = 0;      // of a tree: the nodes that see this key
+            if (kTree) {
+#pragma unroll 1
+              for (int i = 0; i < walk.s.q_len; ++i) {
+                const uint64_t w = p.a.tree[walk.s.tok0 + i] & node_bits(walk.s.q_len);
+                seen |= (uint32_t)tree_sees(w, __popcll(w), key, first_pos, walk.s.len, p.a.window) << i;
+              }
+            }
 #pragma unroll
             for (int r = 0; r < NR; ++r) {
-              const int pos = first_pos + div_small(r, gm);
-              if (key <= pos && (p.a.window <= 0 || key > pos - p.a.window)) acc[r] = NAN;
+              const int i = div_small(r, gm), pos = first_pos + i;
+              if (kTree ? (seen >> i) & 1 : key <= pos && (p.a.window <= 0 || key > pos - p.a.window))
+                acc[r] = NAN;
             }
           }
           // all have read these words before anyone writes the next ones of this parity: S of the
@@ -492,7 +507,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         tc_fence_after();
         const int key0 = (walk.s.tile0 + t) * kTile, key = key0 + tid;
         // some key of the tile is hidden from some row
-        const bool masked = key0 + kTile - 1 > first_pos ||
+        const bool masked = key0 + kTile - 1 > low_pos<kTree>(first_pos) ||
                             (p.a.window > 0 && key0 <= walk.s.len - 1 - p.a.window);
         const float* sc = reinterpret_cast<const float*>(sm + C::kOffScale + st * 64);
         float ks = 1.0f, vs = 1.0f;
@@ -556,9 +571,17 @@ __global__ void __launch_bounds__(kThreads, 2)
         if (masked) {
           if (!(vs > 0.0f)) ivs = 0.0f;   // (a page without a scale: NaN to the rows that see it only)
           bool all = true, any = false;
+          uint32_t seen = 0;        // of a tree: the nodes that see this key
           for (int i = 0; i < walk.s.q_len; ++i) {
-            const int pos = first_pos + i;
-            const bool see = key <= pos && (p.a.window <= 0 || key > pos - p.a.window);
+            bool see;
+            if (kTree) {
+              const uint32_t w = __shfl_sync(0xffffffffu, nodes, i);
+              see = tree_sees(w, __popc(w), key, first_pos, walk.s.len, p.a.window);
+              seen |= (uint32_t)see << i;
+            } else {
+              const int pos = first_pos + i;
+              see = key <= pos && (p.a.window <= 0 || key > pos - p.a.window);
+            }
             all = all && see;
             any = any || see;
           }
@@ -592,8 +615,10 @@ __global__ void __launch_bounds__(kThreads, 2)
           }
 #pragma unroll
           for (int r = 0; r < NR; ++r) {
-            const int pos = first_pos + div_small(r, gm);
-            if (!(key <= pos && (p.a.window <= 0 || key > pos - p.a.window))) x[r] = -INFINITY;
+            const int i = div_small(r, gm), pos = first_pos + i;
+            const bool see = kTree ? (seen >> i) & 1
+                                   : key <= pos && (p.a.window <= 0 || key > pos - p.a.window);
+            if (!see) x[r] = -INFINITY;
           }
         }
         // ---- the tile's maxima: the warp's by redux, the four warps' through shared memory
@@ -818,27 +843,31 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
 
 int decode_ctas(int sms) { return 2 * sms; }
 
-template <int NR, int kCap>
+template <int NR, int kCap, bool kTree>
 cudaError_t launch_nr(const DecodeParams& d, int sms, cudaStream_t stream) {
   static PerDeviceOnce once;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   e = once.run(dev, [&]() -> cudaError_t {
-    return cudaFuncSetAttribute(kda_attn_decode_kernel<NR, kCap>,
+    return cudaFuncSetAttribute(kda_attn_decode_kernel<NR, kCap, kTree>,
                                 cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<NR>::kBytes);
   });
   if (e != cudaSuccess) return e;
-  return launch(kda_attn_decode_kernel<NR, kCap>, dim3((unsigned)decode_ctas(sms)), dim3(kThreads),
+  return launch(kda_attn_decode_kernel<NR, kCap, kTree>, dim3((unsigned)decode_ctas(sms)), dim3(kThreads),
                 Cfg<NR>::kBytes, true, stream, d);
 }
-template <int NR>
+template <int NR, bool kTree>
 cudaError_t launch_cap(const DecodeParams& d, int sms, cudaStream_t stream) {
   switch (cap_kind(d.a.softcap)) {
-    case kNoCap: return launch_nr<NR, kNoCap>(d, sms, stream);
-    case kCapPlain: return launch_nr<NR, kCapPlain>(d, sms, stream);
-    default: return launch_nr<NR, kCapExact>(d, sms, stream);
+    case kNoCap: return launch_nr<NR, kNoCap, kTree>(d, sms, stream);
+    case kCapPlain: return launch_nr<NR, kCapPlain, kTree>(d, sms, stream);
+    default: return launch_nr<NR, kCapExact, kTree>(d, sms, stream);
   }
+}
+template <int NR>
+cudaError_t launch_mask(const DecodeParams& d, int sms, cudaStream_t stream) {
+  return d.a.tree ? launch_cap<NR, true>(d, sms, stream) : launch_cap<NR, false>(d, sms, stream);
 }
 template <int NR>
 cudaError_t launch_merge(const DecodeParams& d, int sms, cudaStream_t stream) {
@@ -896,8 +925,8 @@ cudaError_t launch_attn_decode(const AttnParams& a, const CacheMaps& maps, int m
   make_params(a, max_rows, gate, work, sms, &d);
   d.maps = maps;
   d.least = least;
-  return max_rows <= 8 ? launch_cap<8>(d, sms, stream) : max_rows <= 16 ? launch_cap<16>(d, sms, stream)
-                                                                     : launch_cap<32>(d, sms, stream);
+  return max_rows <= 8 ? launch_mask<8>(d, sms, stream) : max_rows <= 16 ? launch_mask<16>(d, sms, stream)
+                                                                      : launch_mask<32>(d, sms, stream);
 }
 
 cudaError_t launch_attn_decode_merge(const AttnParams& a, int max_rows, void* work, int sms,

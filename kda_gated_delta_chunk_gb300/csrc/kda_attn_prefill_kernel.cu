@@ -89,17 +89,20 @@ struct ItemP {
   int tok, cnt;              // tokens [tok, tok + cnt) of the sequence's new ones
   int tile0, tiles;
 };
+template <bool kTree>
 __device__ __forceinline__ ItemP item_of(int q_len, int len, int rt, int tokens, int window) {
   ItemP it;
   it.tok = rt * tokens;
   it.cnt = min(tokens, q_len - it.tok);
-  const int p_first = len - q_len + it.tok, p_last = p_first + it.cnt - 1;
+  const int p_first = kTree ? low_pos<true>(len - q_len) : len - q_len + it.tok;
+  const int p_last = kTree ? len - 1 : p_first + it.cnt - 1;
   it.tile0 = first_seen(p_first, window) / kTile;
   it.tiles = max(1, (max(p_last, -1) + kTile) / kTile - it.tile0);
   return it;
 }
 
 // The walk over a CTA's range, in units: an item has kOver of them, then one per key tile.
+template <bool kTree>
 struct WalkP {
   int64_t pos, end;
   int n, h, rt, off;         // the next item and the units of it that lie before this range
@@ -119,10 +122,10 @@ struct WalkP {
         }
         int err;
         if (++n >= p.a.num_seqs) return false;             // (lengths that changed under the kernel)
-        s = seq_info(p.a, n, min_rows, 0x7fffffff, &err);
+        s = seq_info<kTree>(p.a, n, min_rows, 0x7fffffff, &err);
         h = rt = 0;
       }
-      it = item_of(s.q_len, s.len, rt, p.tokens, p.a.window);
+      it = item_of<kTree>(s.q_len, s.len, rt, p.tokens, p.a.window);
       ch = h;
       ++rt;
       const int size = it.tiles + kOver, o = off, o1 = (int)min((int64_t)size, o + (end - pos));
@@ -142,16 +145,15 @@ struct Segment {
   int more;                  // 0: there is none, the CTA is done
   int tok0, cnt;             // its tokens, as rows of q and out
   int head0;                 // first query head
-  int p_first;               // position of the first token
+  int p_first, p_last;       // positions of the first and last token (of a tree: bounds, low_pos)
   int key0, key1;            // keys [key0, key1), whole tiles; those past the last position are masked
   int ch;                    // kv head
   int used;                  // pages of the sequence
   int whole, begins;         // the item's tiles are all here / its first one is
-  int pad;
   const int32_t* table;      // the sequence's pages
 };
 
-template <int kCap>
+template <int kCap, bool kTree>
 __global__ void __launch_bounds__(kThreadsP, 1)
     kda_attn_prefill_kernel(const __grid_constant__ PrefillParams p) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -223,7 +225,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
     few = 0;                 // ... of one that the decode kernel may take
     if (n < N) {
       int err;
-      const SeqInfo s = seq_info(p.a, n, 1, 0x7fffffff, &err);
+      const SeqInfo s = seq_info<kTree>(p.a, n, 1, 0x7fffffff, &err);
       if (err != KDA_OK && report && blockIdx.x == 0) record_error(p.a.status, err, 331);
       if (s.tiles && (int64_t)s.q_len * G <= p.few) {
         few = (int)min((long long)(s.tiles + kOver) * hk, 1ll << 24);   // (as the decode kernel counts)
@@ -236,14 +238,14 @@ __global__ void __launch_bounds__(kThreadsP, 1)
     long long mine = 0;
     const int rts = (q_len + p.tokens - 1) / p.tokens;
     if (rts <= 32)
-      for (int rt = 0; rt < rts; ++rt) mine += item_of(q_len, len, rt, p.tokens, p.a.window).tiles + kOver;
+      for (int rt = 0; rt < rts; ++rt) mine += item_of<kTree>(q_len, len, rt, p.tokens, p.a.window).tiles + kOver;
     uint32_t todo = __ballot_sync(0xffffffffu, rts > 32);
     while (todo) {
       const int k = __ffs(todo) - 1;
       todo &= todo - 1;
       const int ql = __shfl_sync(0xffffffffu, q_len, k), ln = __shfl_sync(0xffffffffu, len, k);
       int sum = 0;
-      for (int rt = lane; rt * p.tokens < ql; rt += 32) sum += item_of(ql, ln, rt, p.tokens, p.a.window).tiles + kOver;
+      for (int rt = lane; rt * p.tokens < ql; rt += 32) sum += item_of<kTree>(ql, ln, rt, p.tokens, p.a.window).tiles + kOver;
       // (millions of new tokens over as many keys: the warp's sum passes 31 bits)
       const long long all = __reduce_add_sync(0xffffffffu, (unsigned)sum & 0xffffu) +
                             ((long long)__reduce_add_sync(0xffffffffu, (unsigned)sum >> 16) << 16);
@@ -281,7 +283,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
   __syncthreads();
   const bool all = total_few < p.least;
   if (all) total += total_few;
-  WalkP walk;
+  WalkP<kTree> walk;
   walk.min_rows = all ? 1 : p.few + 1;
   // (no more ranges than units: between two CTAs of an item there is none without a part)
   const int ranges = (int)min((long long)gridDim.x, total);
@@ -333,13 +335,13 @@ __global__ void __launch_bounds__(kThreadsP, 1)
     walk.n = misc->start_n;
     walk.h = misc->start_h;
     int err;
-    walk.s = seq_info(p.a, walk.n, walk.min_rows, 0x7fffffff, &err);
+    walk.s = seq_info<kTree>(p.a, walk.n, walk.min_rows, 0x7fffffff, &err);
     if (warp == 0) {     // the row tile: 32 at a time
       long long left = misc->rest;
       for (int r0 = 0;; r0 += 32) {
         const int rt = r0 + lane;
         const int c = rt * p.tokens < walk.s.q_len
-                          ? item_of(walk.s.q_len, walk.s.len, rt, p.tokens, p.a.window).tiles + kOver : 0;
+                          ? item_of<kTree>(walk.s.q_len, walk.s.len, rt, p.tokens, p.a.window).tiles + kOver : 0;
         int inc = c;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -535,7 +537,9 @@ __global__ void __launch_bounds__(kThreadsP, 1)
             g->tok0 = tok0;
             g->cnt = walk.it.cnt;
             g->head0 = walk.ch * G;
-            g->p_first = walk.s.len - walk.s.q_len + walk.it.tok;
+            g->p_first = kTree ? low_pos<true>(walk.s.len - walk.s.q_len)
+                               : walk.s.len - walk.s.q_len + walk.it.tok;
+            g->p_last = kTree ? walk.s.len - 1 : g->p_first + walk.it.cnt - 1;
             g->key0 = (walk.it.tile0 + walk.a) * kTile;
             g->key1 = (walk.it.tile0 + walk.b) * kTile;
             g->ch = walk.ch;
@@ -575,7 +579,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
     while (true) {
       const Segment* sg = seg_wait(seg, ok);
       if (!ok || !sg->more) break;
-      const int p_first = sg->p_first, p_last = p_first + sg->cnt - 1, key1 = sg->key1;
+      const int p_first = sg->p_first, p_last = sg->p_last, key1 = sg->key1;
       int key0 = sg->key0;
       seg_done(seg);
       if (vt == 0) misc->poison[(seg + 4) & 7] = 0;      // last read four segments ago
@@ -711,6 +715,15 @@ __global__ void __launch_bounds__(kThreadsP, 1)
       int hi = rel + (row < rows ? div_small(row, gm) : last) - 64 * cg;
       int p_lo = rel + min(div_small(128 * half, gm), last);
       int p_hi = rel + div_small(max(min(rows, 128 * half + 128) - 1, 0), gm);
+      // of a tree: this row's mask, and the cached tokens before the new ones from its first key on
+      uint64_t node = 0;
+      if (kTree) {
+        node = p.a.tree[sg->tok0 + (row < rows ? div_small(row, gm) : last)] &
+               node_bits(sg->p_last - sg->p_first);
+        hi = rel + 1 - 64 * cg;
+        p_lo = rel;
+        p_hi = sg->p_last - sg->key0;
+      }
       const int tiles = (sg->key1 - sg->key0) / kTile;
       float m = -INFINITY, l = 0.0f;
       for (int t = 0; t < tiles; ++t, ++it, hi -= kTile, p_lo -= kTile, p_hi -= kTile) {
@@ -788,8 +801,14 @@ __global__ void __launch_bounds__(kThreadsP, 1)
           } else if (scaled) {
             // bits of the 64 keys that this row sees: lo <= e <= hi
             // (below hi < 0 the difference may wrap: nothing is seen then)
-            const int lo = p.a.window > 0 ? (int)((uint32_t)hi - (uint32_t)p.a.window + 1u) : 0;
-            const uint64_t upto = hi < 0 ? 0 : (hi >= 63 ? ~0ull : (2ull << hi) - 1);
+            int lo = p.a.window > 0 ? (int)((uint32_t)hi - (uint32_t)p.a.window + 1u) : 0;
+            uint64_t upto = hi < 0 ? 0 : (hi >= 63 ? ~0ull : (2ull << hi) - 1);
+            if (kTree) {     // hi cached keys, then the new ones (the window has room for those seen)
+              lo = p.a.window > 0 && hi > 0 ? hi + __popcll(node) - p.a.window : 0;
+              upto = hi >= 64 ? ~0ull
+                     : hi >= 0 ? ((1ull << hi) - 1) | (node << hi)
+                               : (hi > -64 ? node >> -hi : 0);
+            }
             const uint64_t see = lo <= 0 ? upto : (lo >= 64 ? 0 : upto & (~0ull << lo));
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
@@ -894,10 +913,13 @@ __global__ void __launch_bounds__(kThreadsP, 1)
         tmem_ld32(to + 32 * c, o);
         tmem_wait_ld();
         if (poisoned && live) {    // NaN entries that this row sees, in tiles that some rows do not
-          const int p0 = sg->p_first, p1 = p0 + last, pos = p0 + i_tok;
+          const int p0 = sg->p_first, p1 = sg->p_last, pos = kTree ? p1 : p0 + i_tok;
+          const int cnt = __popcll(node);
           for (int key0 = sg->key0; key0 < sg->key1; key0 += kTile) {
             if (!(key0 + kTile - 1 > p0 || key0 < first_seen(p1, p.a.window))) continue;
-            for (int key = max(key0, first_seen(pos, p.a.window)); key <= min(key0 + kTile - 1, pos); ++key) {
+            for (int key = kTree ? key0 : max(key0, first_seen(pos, p.a.window));
+                 key <= min(key0 + kTile - 1, pos); ++key) {
+              if (kTree && !tree_sees(node, cnt, key, p0 + 1, p1 + 1, p.a.window)) continue;
               const int pg = sg->table[key / P];
               if (pg < 0 || pg >= p.a.c.num_pages) continue;
               const uint8_t* v = p.a.c.v + pg * p.a.c.page_stride + sg->ch * p.a.c.head_stride +
@@ -1020,23 +1042,28 @@ __global__ void __launch_bounds__(32 * kMergeRows)
     p.a.lse[tok * p.a.heads + head] = den == 0.0f ? -INFINITY : (m + lg2(den)) * kLn2;
 }
 
-template <int kCap>
-cudaError_t launch_cap(const PrefillParams& d, int sms, cudaStream_t stream) {
+template <int kCap, bool kTree>
+cudaError_t launch_kernel(const PrefillParams& d, int sms, cudaStream_t stream) {
   static PerDeviceOnce once;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   e = once.run(dev, [&]() -> cudaError_t {
     cudaFuncAttributes at;
-    cudaError_t x = cudaFuncGetAttributes(&at, kda_attn_prefill_kernel<kCap>);
+    cudaError_t x = cudaFuncGetAttributes(&at, kda_attn_prefill_kernel<kCap, kTree>);
     if (x != cudaSuccess) return x;
     // the warpgroups' register shares must fit what the block is launched with
     if ((at.numRegs + 7) / 8 * 8 * kThreadsP < kRegsNeeded) return cudaErrorInvalidConfiguration;
-    return cudaFuncSetAttribute(kda_attn_prefill_kernel<kCap>,
+    return cudaFuncSetAttribute(kda_attn_prefill_kernel<kCap, kTree>,
                                 cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemP);
   });
   if (e != cudaSuccess) return e;
-  return launch(kda_attn_prefill_kernel<kCap>, dim3((unsigned)sms), dim3(kThreadsP), kSmemP, true, stream, d);
+  return launch(kda_attn_prefill_kernel<kCap, kTree>, dim3((unsigned)sms), dim3(kThreadsP), kSmemP, true,
+                stream, d);
+}
+template <int kCap>
+cudaError_t launch_cap(const PrefillParams& d, int sms, cudaStream_t stream) {
+  return d.a.tree ? launch_kernel<kCap, true>(d, sms, stream) : launch_kernel<kCap, false>(d, sms, stream);
 }
 
 }  // namespace

@@ -278,8 +278,22 @@ struct SeqInfo {
 __device__ __forceinline__ int first_seen(int pos, int window) {
   return window > 0 ? max(0, max(pos, 0) - window + 1) : 0;
 }
+// A tree's new tokens all see the cached ones before them, and of each other those that the bits of
+// their masks name.  The position of every one is taken as that of the last cached token where a
+// lower bound is wanted, as the last new one's where an upper one is.
+template <bool kTree>
+__device__ __forceinline__ int low_pos(int first_new) { return kTree ? first_new - 1 : first_new; }
+// Bits of a tree's mask that name one of its `n` (1 to 64) nodes.
+__device__ __forceinline__ uint64_t node_bits(int n) { return ~0ull >> (64 - n); }
+// Whether the node with mask w (cnt bits set) sees `key`; start: the first new token's position,
+// len: one past the last one's.  (The window keeps the last of what it sees; it has room for cnt.)
+__device__ __forceinline__ bool tree_sees(uint64_t w, int cnt, int key, int start, int len, int window) {
+  if (key >= start) return key < len && ((w >> (key - start)) & 1);
+  return window <= 0 || key >= start + cnt - window;
+}
 // Sequences with min_rows <= q_len * group <= max_rows are this launch's.  `err`: the code to
 // record for a malformed sequence (which is left out), or KDA_OK.
+template <bool kTree>
 __device__ __forceinline__ SeqInfo seq_info(const AttnParams& p, int n, int min_rows, int max_rows,
                                             int* err) {
   SeqInfo s;
@@ -301,9 +315,13 @@ __device__ __forceinline__ SeqInfo seq_info(const AttnParams& p, int n, int min_
     *err = KDA_ERR_INVALID_ARG;
     return s;
   }
+  if (kTree && s.q_len > s.len) {
+    *err = KDA_ERR_BAD_CACHE_INDEX;
+    return s;
+  }
   const int64_t rows = (int64_t)s.q_len * (p.heads / p.c.kv_heads);
   if (s.q_len == 0 || rows < min_rows || rows > max_rows) return s;
-  s.tile0 = first_seen(s.len - s.q_len, p.window) / kTile;
+  s.tile0 = first_seen(low_pos<kTree>(s.len - s.q_len), p.window) / kTile;
   s.tiles = max(1, (s.len + kTile - 1) / kTile - s.tile0);
   return s;
 }

@@ -3,91 +3,9 @@
 #include <cmath>
 #include <cstdint>
 
-#include "kda_attn.cuh"
+#include "kda_checks.cuh"
 
-namespace {
-
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
-bool known_dtype(int d) { return d == KDA_STATE_F32 || d == KDA_STATE_BF16; }
-
-// KDA_OK on a supported current device; its multiprocessor count in *sms.
-int current_device(int* sms) {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) {
-    cudaGetLastError();
-    return KDA_ERR_CUDA;
-  }
-  const int rc = kda_device_check(dev);
-  if (rc != KDA_OK) return rc;
-  if (cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
-    cudaGetLastError();
-    return KDA_ERR_CUDA;
-  }
-  return KDA_OK;
-}
-
-int launched(cudaError_t e) {
-  if (e == cudaSuccess) return KDA_OK;
-  cudaGetLastError();
-  return KDA_ERR_LAUNCH_FAILED;
-}
-
-// The cache's own fields, and its view for the kernels.
-int check_cache(const kda_kv_cache* c, int32_t num_seqs, kda::attn::CacheView* out) {
-  if (!c || !c->k || !c->v || !c->k_scale || !c->v_scale) return KDA_ERR_INVALID_ARG;
-  if (num_seqs > 0 && (!c->block_table || !c->kv_lens)) return KDA_ERR_INVALID_ARG;
-  if (c->page_size != 16 && c->page_size != 32 && c->page_size != 64 && c->page_size != 128)
-    return KDA_ERR_INVALID_ARG;
-  if (c->num_pages < 1 || c->kv_heads < 1 || c->max_blocks < 0 || c->table_stride < c->max_blocks ||
-      c->scale_stride < c->kv_heads)
-    return KDA_ERR_INVALID_ARG;
-  if ((int64_t)c->max_blocks * c->page_size > INT32_MAX) return KDA_ERR_INVALID_ARG;
-  const int64_t most = (int64_t)1 << 39;   // a TMA stride is below 2^40 bytes
-  if (c->token_stride < KDA_HEAD_DIM || c->token_stride > most || c->head_stride < KDA_HEAD_DIM ||
-      c->head_stride > most || c->page_stride < KDA_HEAD_DIM || c->page_stride > most)
-    return KDA_ERR_INVALID_ARG;
-  if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->k_scale, 4) || !aligned(c->v_scale, 4) ||
-      !aligned(c->block_table, 4) || !aligned(c->kv_lens, 4) ||
-      (c->token_stride | c->head_stride | c->page_stride) % 16 != 0)
-    return KDA_ERR_MISALIGNED;
-  out->k = static_cast<uint8_t*>(c->k);
-  out->v = static_cast<uint8_t*>(c->v);
-  out->k_scale = c->k_scale;
-  out->v_scale = c->v_scale;
-  out->page_stride = c->page_stride;
-  out->head_stride = c->head_stride;
-  out->token_stride = c->token_stride;
-  out->scale_stride = c->scale_stride;
-  out->num_pages = c->num_pages;
-  out->page_size = c->page_size;
-  out->kv_heads = c->kv_heads;
-  out->block_table = c->block_table;
-  out->table_stride = c->table_stride;
-  out->max_blocks = c->max_blocks;
-  out->kv_lens = c->kv_lens;
-  return KDA_OK;
-}
-
-int check_batch(const int32_t* cu_seqlens, const void* workspace, int64_t total_tokens,
-                int32_t num_seqs, int32_t heads, size_t workspace_bytes) {
-  if (total_tokens < 0 || total_tokens > INT32_MAX || num_seqs < 0 || heads < 1 || !cu_seqlens ||
-      !workspace)
-    return KDA_ERR_INVALID_ARG;
-  if (workspace_bytes < (size_t)kda::kWorkspaceBytes) return KDA_ERR_WORKSPACE_TOO_SMALL;
-  if (!aligned(cu_seqlens, 4) || !aligned(workspace, 16)) return KDA_ERR_MISALIGNED;
-  return KDA_OK;
-}
-
-// A [T, heads, 128] bf16 tensor with dense heads and a token stride.
-int check_rows(const void* p, int64_t stride, int32_t heads) {
-  if (!p) return KDA_ERR_INVALID_ARG;
-  if (stride < (int64_t)heads * KDA_HEAD_DIM || stride > ((int64_t)1 << 40)) return KDA_ERR_INVALID_ARG;
-  if (!aligned(p, 16) || stride % 8 != 0) return KDA_ERR_MISALIGNED;
-  return KDA_OK;
-}
-
-}  // namespace
+using namespace kda::checks;
 
 extern "C" {
 
@@ -198,11 +116,15 @@ size_t kda_attention_workspace_size(int32_t num_seqs, int32_t heads, int32_t kv_
   return (kda::attn::attn_workspace_bytes(heads, max_q_len) + 15) & ~(size_t)15;
 }
 
-int kda_cached_attention(const void* q, int64_t q_stride, const kda_kv_cache* cache,
-                         const int32_t* cu_seqlens, float scale, float softcap, int32_t window,
-                         void* out, int64_t out_stride, float* lse, void* workspace,
-                         kda_stream_t stream, int64_t total_tokens, int32_t num_seqs, int32_t heads,
-                         int32_t max_q_len, size_t workspace_bytes) {
+}  // extern "C"
+
+namespace {
+// `tree`: the new tokens are nodes that see each other by `mask`; else causal.
+int attention_impl(const void* q, int64_t q_stride, const kda_kv_cache* cache, const int32_t* cu_seqlens,
+                   bool tree, const void* mask, float scale, float softcap, int32_t window, void* out,
+                   int64_t out_stride, float* lse, void* workspace, kda_stream_t stream,
+                   int64_t total_tokens, int32_t num_seqs, int32_t heads, int32_t max_q_len,
+                   size_t workspace_bytes) {
   kda::attn::AttnParams p{};
   int rc = check_batch(cu_seqlens, workspace, total_tokens, num_seqs, heads, workspace_bytes);
   if (rc != KDA_OK) return rc;
@@ -215,7 +137,10 @@ int kda_cached_attention(const void* q, int64_t q_stride, const kda_kv_cache* ca
     if ((rc = check_rows(q, q_stride, heads)) != KDA_OK) return rc;
     if ((rc = check_rows(out, out_stride, heads)) != KDA_OK) return rc;
     if (max_q_len < 1) return KDA_ERR_INVALID_ARG;
+    if (tree && !mask) return KDA_ERR_INVALID_ARG;
   }
+  if (tree && (max_q_len > KDA_TREE_NODES || (window > 0 && window < max_q_len))) return KDA_ERR_INVALID_ARG;
+  if (!aligned(mask, 8)) return KDA_ERR_MISALIGNED;
   if (!aligned(lse, 4)) return KDA_ERR_MISALIGNED;
   if (workspace_bytes < kda::attn::attn_call_bytes(heads, cache->kv_heads, max_q_len))
     return KDA_ERR_WORKSPACE_TOO_SMALL;
@@ -238,8 +163,32 @@ int kda_cached_attention(const void* q, int64_t q_stride, const kda_kv_cache* ca
   p.num_seqs = num_seqs;
   p.heads = heads;
   p.max_q_len = max_q_len;
+  p.tree = static_cast<const uint64_t*>(mask);
   p.status = static_cast<int*>(workspace);
   return launched(kda::attn::launch_attn(p, sms, reinterpret_cast<cudaStream_t>(stream)));
+}
+}  // namespace
+
+extern "C" {
+
+int kda_cached_attention(const void* q, int64_t q_stride, const kda_kv_cache* cache,
+                         const int32_t* cu_seqlens, float scale, float softcap, int32_t window,
+                         void* out, int64_t out_stride, float* lse, void* workspace,
+                         kda_stream_t stream, int64_t total_tokens, int32_t num_seqs, int32_t heads,
+                         int32_t max_q_len, size_t workspace_bytes) {
+  return attention_impl(q, q_stride, cache, cu_seqlens, false, nullptr, scale, softcap, window, out,
+                        out_stride, lse, workspace, stream, total_tokens, num_seqs, heads, max_q_len,
+                        workspace_bytes);
+}
+
+int kda_tree_attention(const void* q, int64_t q_stride, const kda_kv_cache* cache,
+                       const int32_t* cu_seqlens, const void* mask, float scale, float softcap,
+                       int32_t window, void* out, int64_t out_stride, float* lse, void* workspace,
+                       kda_stream_t stream, int64_t total_tokens, int32_t num_seqs, int32_t heads,
+                       int32_t max_q_len, size_t workspace_bytes) {
+  return attention_impl(q, q_stride, cache, cu_seqlens, true, mask, scale, softcap, window, out,
+                        out_stride, lse, workspace, stream, total_tokens, num_seqs, heads, max_q_len,
+                        workspace_bytes);
 }
 
 }  // extern "C"

@@ -1,0 +1,50 @@
+// Trees of drafted tokens: what the operators on them share.  A tree's nodes are a sequence's new
+// tokens, at most KDA_TREE_NODES; node i follows node parents[i] < i of the same sequence, or the
+// cached text (-1).
+#pragma once
+
+#include "kda_attn.cuh"
+
+namespace kda {
+namespace tree {
+
+constexpr int kNodes = KDA_TREE_NODES;
+
+// The nodes of one sequence of a batch.
+struct Nodes {
+  int tok0, n;        // first row, nodes
+};
+// False, with the code to record in *err, for a malformed sequence.
+__device__ __forceinline__ bool nodes_of(const int32_t* cu, int seq, int64_t total, int max_q_len,
+                                         Nodes* s, int* err) {
+  const int t0 = cu[seq], t1 = cu[seq + 1];
+  s->tok0 = t0;
+  s->n = t1 - t0;
+  *err = KDA_OK;
+  if (t0 < 0 || t1 < t0 || (int64_t)t1 > total || (seq == 0 && t0 != 0)) *err = KDA_ERR_BAD_CU_SEQLENS;
+  else if (s->n > max_q_len) *err = KDA_ERR_INVALID_ARG;
+  return *err == KDA_OK;
+}
+// Node i's parent, -1 for one out of range.
+__device__ __forceinline__ int parent_of(const int32_t* parents, const Nodes& s, int i, int* status,
+                                         bool report) {
+  const int p = parents[s.tok0 + i];
+  if (p >= -1 && p < i) return p;
+  if (report) record_error(status, KDA_ERR_BAD_TREE, 400);
+  return -1;
+}
+
+struct PlanParams {
+  const int32_t* parents;
+  const int32_t* cu_seqlens;
+  const int32_t* kv_lens;
+  uint64_t* mask;
+  int32_t* positions;
+  int* status;
+  int64_t total_tokens;
+  int32_t num_seqs, max_q_len;
+};
+cudaError_t launch_plan(const PlanParams& p, cudaStream_t stream);
+
+}  // namespace tree
+}  // namespace kda

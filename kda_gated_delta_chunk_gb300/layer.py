@@ -36,6 +36,7 @@ _HALF, _EITHER = (_BF16,), (_BF16, _F32)
 _FLOAT = (_F32,)
 _I32 = torch.int32
 _INT = (_I32,)
+_MASK = (torch.int64,)
 _UINT8 = (torch.uint8,)
 # the current stream's handle without a Stream object around it (a call's host time counts in decode)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
@@ -402,12 +403,32 @@ def cached_attention(q, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens
             return done
         if done is not None:
             raise KDAError(done, "kda_cached_attention")
+    return _attention("kda_cached_attention", None, q, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens,
+                      cu_seqlens, scale, max_q_len, softcap, window, out, lse, workspace, stream)
+
+
+def tree_attention(q, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, cu_seqlens, mask,
+                   scale: float, max_q_len: int, softcap: float = 0.0, window: int = 0, out=None, lse=False,
+                   workspace=None, stream=None):
+    """Run ``kda_tree_attention``: attention of drafted trees' nodes over the cache.
+
+    As ``cached_attention``, but a node sees every cached token before its sequence's nodes, and
+    those of the nodes that its mask names: int64 [T], bit j for the sequence's node j
+    (``tree_plan`` makes it).  At most 64 nodes a sequence; window is 0 or at least max_q_len.
+    Returns (out, lse or None).
+    """
+    return _attention("kda_tree_attention", mask, q, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens,
+                      cu_seqlens, scale, max_q_len, softcap, window, out, lse, workspace, stream)
+
+
+def _attention(entry, mask, q, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, cu_seqlens, scale,
+               max_q_len, softcap, window, out, lse, workspace, stream):
     dev = _need_cuda(q, "q")
     place = _elsewhere(stream, q)
     if place is not None:
-        return _within(place, cached_attention, (out, lse if isinstance(lse, torch.Tensor) else None), q,
+        return _within(place, _attention, (out, lse if isinstance(lse, torch.Tensor) else None), entry, mask, q,
                           k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, cu_seqlens, scale,
-                          max_q_len, softcap, window, out, lse, workspace)
+                          max_q_len, softcap, window, out, lse, workspace, None)
     shape = q.shape
     if len(shape) != 3:
         raise ValueError("q must be [T, heads, 128]")
@@ -440,9 +461,13 @@ def cached_attention(q, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens
         workspace[:256].zero_()
     else:
         _check(workspace, "workspace", _UINT8, workspace.shape, dev, 0)
-    rc = lib().kda_cached_attention(
-        q.data_ptr(), q_row, c, cu_seqlens.data_ptr(), scale, softcap, window, out.data_ptr(), out_row,
+    masks = ()
+    if entry == "kda_tree_attention":
+        _check(mask, "mask", _MASK, (T,), dev, 0)
+        masks = (mask.data_ptr(),)
+    rc = getattr(lib(), entry)(
+        q.data_ptr(), q_row, c, cu_seqlens.data_ptr(), *masks, scale, softcap, window, out.data_ptr(), out_row,
         lse_ptr, workspace.data_ptr(), _stream(stream, dev), T, N, heads, max_q_len, workspace.numel())
     if rc != OK:
-        raise KDAError(rc, "kda_cached_attention")
+        raise KDAError(rc, entry)
     return out, lse

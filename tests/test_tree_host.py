@@ -1,0 +1,57 @@
+"""The C entry points and the binding of the operators on drafted trees on a host without a GPU:
+refusals come before any device is touched."""
+import ctypes
+
+import pytest
+import torch
+
+import kda_gated_delta_chunk_gb300 as kda
+from test_layer_host import A, L, cache  # noqa: F401  (L: the library, a fixture)
+
+INVALID, MISALIGNED = kda.ERR_INVALID_ARG, kda.ERR_MISALIGNED
+
+
+def plan(L, **over):
+    a = dict(parents=A, cu=A, kv=A, mask=A, pos=A, ws=A, stream=None, T=4, N=1, most=4, wsb=256)
+    a.update(over)
+    return L.kda_tree_plan(*a.values())
+
+
+@pytest.mark.parametrize("over,code", [
+    (dict(T=-1), INVALID), (dict(T=2 ** 31), INVALID), (dict(N=-1), INVALID), (dict(most=65), INVALID), (dict(most=0), INVALID),
+    (dict(most=-1), INVALID), (dict(parents=None), INVALID), (dict(cu=None), INVALID), (dict(kv=None), INVALID),
+    (dict(mask=None), INVALID), (dict(pos=None), INVALID), (dict(ws=None), INVALID), (dict(parents=A + 2), MISALIGNED),
+    (dict(mask=A + 4), MISALIGNED), (dict(pos=A + 1), MISALIGNED), (dict(kv=A + 2), MISALIGNED),
+    (dict(ws=A + 8), MISALIGNED), (dict(wsb=255), kda.ERR_WORKSPACE_TOO_SMALL)])
+def test_plan_refuses(L, over, code):
+    assert plan(L, **over) == code
+
+
+def attend(L, c=None, **over):
+    a = dict(q=A, qs=512, c=ctypes.byref(c if c is not None else cache()), cu=A, mask=A, scale=0.1, cap=0.0,
+             window=0, out=A, os=512, lse=A, ws=A, stream=None, T=4, N=1, H=4, most=4, wsb=1 << 30)
+    a.update(over)
+    return L.kda_tree_attention(*a.values())
+
+
+@pytest.mark.parametrize("over,code", [
+    (dict(most=65), INVALID), (dict(mask=None), INVALID), (dict(window=3), INVALID), (dict(window=-1), INVALID),
+    (dict(mask=A + 4), MISALIGNED), (dict(H=3), INVALID), (dict(scale=float("nan")), INVALID), (dict(cap=-1.0), INVALID),
+    (dict(q=None), INVALID), (dict(out=None), INVALID), (dict(most=0), INVALID), (dict(qs=500), INVALID),
+    (dict(qs=516), MISALIGNED), (dict(wsb=300), kda.ERR_WORKSPACE_TOO_SMALL)])
+def test_attention_refuses(L, over, code):
+    assert attend(L, **over) == code
+
+
+def test_binding_refuses_host_tensors():
+    i = torch.zeros(2, dtype=torch.int32)
+    with pytest.raises(ValueError, match="CUDA tensor"):
+        kda.tree_plan(i, i, i[:1], 2)
+    q = torch.zeros(2, 1, 128, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="CUDA tensor"):
+        kda.tree_attention(q, q, q, q, q, i, i, i, i, 1.0, 2)
+
+
+def test_new_codes_have_texts(L):
+    assert "tree" in kda.status_string(kda.ERR_BAD_TREE)
+    assert "pages" in kda.status_string(kda.ERR_OUT_OF_PAGES)
