@@ -491,6 +491,67 @@ int kda_tree_attention(const void* q, int64_t q_stride, const kda_kv_cache* cach
                        int32_t max_q_len, size_t workspace_bytes);
 
 /*
+ * Moves the accepted branch of each sequence's tree together in one layer's cache.  With
+ * start = kv_lens - nodes, the e-th node of the branch that ends at node accepted[n] (-1: none is accepted)
+ * goes from cache position start + its index to start + e; positions behind the branch keep what they
+ * hold, rejected nodes and all.  A page that takes entries gets, per kv head and for keys and values
+ * each, the largest scale of the pages that its cached text and its new entries come from; entries whose
+ * scale changes are requantised (exact for powers of two, but for what falls below e4m3's smallest
+ * normal).
+ *   accepted   int32 [num_seqs]: a node of the sequence, or -1
+ *   lens_out   int32 [num_seqs]: start + the branch's length, the next step's cached tokens.  Not the
+ *              cache's kv_lens itself: every layer's call reads those.
+ * No two sequences may have a page in common among those of their nodes.  Device errors:
+ * KDA_ERR_BAD_CU_SEQLENS, KDA_ERR_INVALID_ARG (more nodes than max_q_len), KDA_ERR_BAD_TREE (accepted out
+ * of range; a bad parent counts as -1), KDA_ERR_BAD_CACHE_INDEX (kv_lens below the nodes' count or beyond the
+ * table: nothing is moved and lens_out is kv_lens; a page outside the pool: its entries are not moved).
+ */
+int kda_cache_accept(const kda_kv_cache* cache, const int32_t* cu_seqlens, const int32_t* parents,
+                     const int32_t* accepted, int32_t* lens_out, void* workspace, kda_stream_t stream,
+                     int64_t total_tokens, int32_t num_seqs, int32_t max_q_len, size_t workspace_bytes);
+
+/*
+ * Pages of a cache on the device.  refs[page] (int32 [num_pages], 16-byte aligned) counts the rows of the
+ * block table that hold a page; a free page has 0.  A row's pages come first, in order, and -1 fills it to
+ * max_blocks (at row * table_stride).  Each call leaves refs, block_table and kv_lens in order for the
+ * next on the stream; who gets pages gets the lowest free ones, in the order of rows (pairs) and blocks,
+ * whatever the order in which threads run.  page_size is any positive number.  A layer's caches are
+ * copied by kda_pages_copy; the rest is done once for all layers.
+ *
+ * kda_pages_free: gives pages back.  rows NULL: every row's pages beyond those that its kv_lens fill (as
+ *   after a step whose drafts were partly rejected).  Else the rows named in rows [num] end: all
+ *   their pages go back and their kv_lens become 0 (a row may be named twice).
+ * kda_pages_reserve: pages for new_tokens [num_rows] more tokens a row: its empty blocks up to
+ *   ceil((kv_lens + new_tokens) / page_size) get one each.  kv_lens stays.  At most 16384 rows.
+ * kda_pages_fork: row dst[i] becomes a copy of row src[i] (kv_lens too): whole pages are held in common,
+ *   a partly filled last one is given a page of its own, to be copied: from_pages[i] -> to_pages[i], both
+ *   -1 where there is none.  What dst[i] held before is overwritten, not given back.  A source may
+ *   be named often; a pair whose dst is named twice, or is a source too, is reported and left out.
+ *   At most 16384 rows and pairs.
+ * kda_pages_copy: pages from[i] to pages to[i] of one layer's cache, keys, values and scales; pairs with a
+ *   negative page are left out (of the cache, block_table and kv_lens are not read).  No page
+ *   may be written by two pairs, or written and read by two.
+ * Device errors: KDA_ERR_BAD_CACHE_INDEX for a row, page, length or count out of range, a page that nobody
+ * held, or a row with a page behind an empty block (the row, page or pair is left out);
+ * KDA_ERR_OUT_OF_PAGES when the free pages do not suffice: the first requests got them, the others'
+ * entries are -1.  Workspace: the 256 bytes with the status word.
+ */
+int kda_pages_free(int32_t* refs, int32_t num_pages, int32_t* block_table, int64_t table_stride,
+                   int32_t num_rows, int32_t max_blocks, int32_t* kv_lens, int32_t page_size,
+                   const int32_t* rows, int32_t num, void* workspace, size_t workspace_bytes,
+                   kda_stream_t stream);
+int kda_pages_reserve(int32_t* refs, int32_t num_pages, int32_t* block_table, int64_t table_stride,
+                      int32_t num_rows, int32_t max_blocks, int32_t* kv_lens, int32_t page_size,
+                      const int32_t* new_tokens, void* workspace, size_t workspace_bytes,
+                      kda_stream_t stream);
+int kda_pages_fork(int32_t* refs, int32_t num_pages, int32_t* block_table, int64_t table_stride,
+                   int32_t num_rows, int32_t max_blocks, int32_t* kv_lens, int32_t page_size,
+                   const int32_t* src, const int32_t* dst, int32_t num, int32_t* from_pages,
+                   int32_t* to_pages, void* workspace, size_t workspace_bytes, kda_stream_t stream);
+int kda_pages_copy(const kda_kv_cache* cache, const int32_t* from_pages, const int32_t* to_pages, int64_t num,
+                   void* workspace, size_t workspace_bytes, kda_stream_t stream);
+
+/*
  * The value-dimension split factor the automatic path uses for a batch of
  * `num_seqs` sequences and `heads` heads on a GPU with `sm_count` SMs.
  * The trigger is PR #52458's: split only when 2 * heads * num_seqs <=

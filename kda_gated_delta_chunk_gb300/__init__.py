@@ -21,7 +21,8 @@ names follow the C ABI in ``include/kda.h``:
     status_string(code) -> str
     add_rms_norm, rope_table, rope_append, cached_attention: the full-attention layer beside the KDA layers
         (layer.py)
-    tree_plan, tree_attention: trees of drafted tokens (tree.py, layer.py)
+    tree_plan, tree_attention, cache_accept: trees of drafted tokens (tree.py, layer.py)
+    free_pages, reserve_pages, fork_pages, copy_pages: the paged cache's pages (pages.py)
 
 There is no CPU fallback: if the library is missing or the device is not an
 sm_103 GPU, these calls raise.
@@ -65,7 +66,8 @@ EXPORTS = ("kda_workspace_size", "kda_chunk_prefill_fwd", "kda_chunk_prefill_fwd
            "kda_recurrent_fwd_scatter", "kda_skinny_proj_workspace_size", "kda_skinny_proj",
            "kda_test_drop_one_record", "kda_add_rms_norm", "kda_rope_append",
            "kda_attention_workspace_size", "kda_cached_attention", "kda_tree_plan",
-           "kda_tree_attention")
+           "kda_tree_attention", "kda_cache_accept", "kda_pages_free", "kda_pages_reserve",
+           "kda_pages_fork", "kda_pages_copy")
 
 _lib = None
 _lock = threading.Lock()
@@ -163,6 +165,17 @@ def lib() -> ctypes.CDLL:
             L.kda_tree_attention.restype = I
             L.kda_tree_attention.argtypes = [P, I64, P, P, P, F, F, I32, P, I64, P, P, P, I64, I32, I32,
                                              I32, SZ]
+            L.kda_cache_accept.restype = I
+            L.kda_cache_accept.argtypes = [P, P, P, P, P, P, P, I64, I32, I32, SZ]
+            pool = [P, I32, P, I64, I32, I32, P, I32]
+            L.kda_pages_free.restype = I
+            L.kda_pages_free.argtypes = pool + [P, I32, P, SZ, P]
+            L.kda_pages_reserve.restype = I
+            L.kda_pages_reserve.argtypes = pool + [P, P, SZ, P]
+            L.kda_pages_fork.restype = I
+            L.kda_pages_fork.argtypes = pool + [P, P, I32, P, P, P, SZ, P]
+            L.kda_pages_copy.restype = I
+            L.kda_pages_copy.argtypes = [P, P, P, I64, P, SZ, P]
             _lib = L
     return _lib
 
@@ -530,4 +543,5 @@ def chunk_prefill_fwd_noalloc(q, k, v, g, beta, A_log, dt_bias, lower_bound, sca
 from .layer import (add_rms_norm, alloc_attention_workspace,  # noqa: E402  (uses the names above)
                     attention_workspace_size, cached_attention, rope_append, rope_table,
                     tree_attention)
-from .tree import tree_plan  # noqa: E402
+from .tree import cache_accept, tree_plan  # noqa: E402
+from .pages import copy_pages, fork_pages, free_pages, reserve_pages  # noqa: E402

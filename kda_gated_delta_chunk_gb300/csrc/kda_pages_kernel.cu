@@ -1,0 +1,368 @@
+// Pages of the cache given back, shared, copied and reserved, on the device, so that a decode loop
+// with a changing batch can be captured whole.
+//
+// The pool's state is the count of rows that hold each page; a free page has 0.  Whoever needs pages gets the
+// lowest free ones, in the order of rows and blocks: the outcome does not depend on the order in
+// which threads run, and there is no list of free pages to keep.  The search is one CTA's scan over the
+// counts, 16 a thread at a time, which ends at the page that serves the last request; a page that is
+// found knows its rank, and the rank the request (a binary search over the requests' prefix sums in
+// shared memory).  Counts go up and down by atomics on integers, whose order does not show.
+#include "kda_pages.cuh"
+
+namespace kda {
+namespace pages {
+namespace {
+
+constexpr int kThreads = 1024, kWarps = kThreads / 32;
+
+// Exclusive prefix of v over the CTA, and the sum; `part` has kWarps + 1 ints.  Barriers inside.
+__device__ __forceinline__ int block_scan(int v, int* part, int* sum) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int inc = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += u;
+  }
+  __syncthreads();       // (the sums of the scan before have been read)
+  if (lane == 31) part[warp] = inc;
+  __syncthreads();
+  if (warp == 0) {
+    const int w = part[lane];
+    int s = w;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, s, o);
+      if (lane >= o) s += u;
+    }
+    part[lane] = s - w;
+    if (lane == 31) part[kWarps] = s;
+  }
+  __syncthreads();
+  *sum = part[kWarps];
+  return part[warp] + inc - v;
+}
+
+// Calls give(rank, page) for the first `total` free pages; false when there are fewer.  For a whole CTA.
+template <class Give>
+__device__ bool find_free(const int32_t* refs, int num_pages, int total, int* part, Give give) {
+  constexpr int kPer = 16;
+  int before = 0;
+  for (int64_t p0 = 0; p0 < num_pages && before < total; p0 += kThreads * kPer) {
+    const int64_t base = p0 + (int64_t)threadIdx.x * kPer;
+    uint32_t free = 0;
+    int4 r[kPer / 4];
+#pragma unroll
+    for (int j = 0; j < kPer / 4; ++j) {
+      const int64_t i = base + 4 * j;
+      r[j] = make_int4(1, 1, 1, 1);
+      if (i + 4 <= num_pages) {
+        r[j] = *reinterpret_cast<const int4*>(refs + i);
+      } else {
+        if (i < num_pages) r[j].x = refs[i];
+        if (i + 1 < num_pages) r[j].y = refs[i + 1];
+        if (i + 2 < num_pages) r[j].z = refs[i + 2];
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kPer / 4; ++j)
+      free |= ((uint32_t)(r[j].x == 0) | (uint32_t)(r[j].y == 0) << 1 | (uint32_t)(r[j].z == 0) << 2 |
+               (uint32_t)(r[j].w == 0) << 3) << (4 * j);
+    int found;
+    int rank = before + block_scan(__popc(free), part, &found);
+    for (; free && rank < total; ++rank, free &= free - 1) give(rank, (int)(base + __ffs(free) - 1));
+    before += found;
+  }
+  return before >= total;
+}
+
+// The request that takes rank r: the last i with first[i] <= r (first[0] = 0, non-decreasing).
+__device__ __forceinline__ int request_of(const int* first, int n, int r) {
+  int lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (first[mid] <= r) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+constexpr int kFreeThreads = 256;
+__global__ void __launch_bounds__(kFreeThreads)
+    kda_pages_free_kernel(const Pool p, const int32_t* rows) {
+  sm100::pdl_wait();
+  sm100::pdl_launch_dependents();
+  const int row = rows ? rows[blockIdx.x] : (int)blockIdx.x;
+  if (row < 0 || row >= p.num_rows) {
+    if (threadIdx.x == 0) record_error(p.status, KDA_ERR_BAD_CACHE_INDEX, 420);
+    return;
+  }
+  int first = 0;
+  if (rows) {
+    if (threadIdx.x == 0) p.kv_lens[row] = 0;
+  } else {
+    const int len = p.kv_lens[row];
+    if (len < 0 || (int64_t)len > (int64_t)p.max_blocks * p.page_size) {
+      if (threadIdx.x == 0) record_error(p.status, KDA_ERR_BAD_CACHE_INDEX, 421);
+      return;
+    }
+    first = (len + p.page_size - 1) / p.page_size;
+  }
+  int32_t* table = p.table + (int64_t)row * p.table_stride;
+  for (int b = first + threadIdx.x; b < p.max_blocks; b += kFreeThreads) {
+    if (table[b] == -1) continue;
+    const int pg = atomicExch(table + b, -1);      // (a row that is named twice gives its pages once)
+    if (pg == -1) continue;
+    if (pg < 0 || pg >= p.num_pages) {
+      record_error(p.status, KDA_ERR_BAD_CACHE_INDEX, 422);
+      continue;
+    }
+    if (atomicSub(p.refs + pg, 1) <= 0) {          // nobody held it
+      atomicAdd(p.refs + pg, 1);
+      record_error(p.status, KDA_ERR_BAD_CACHE_INDEX, 423);
+    }
+  }
+}
+
+// One CTA: requests counted and scanned, then served.
+__global__ void __launch_bounds__(kThreads)
+    kda_pages_reserve_kernel(const Pool p, const int32_t* new_tokens) {
+  extern __shared__ int smem[];
+  int* first = smem;                 // [num_rows] prefix sums of the requests
+  int* start = smem + p.num_rows;    // [num_rows] first block of each
+  __shared__ int part[kWarps + 1];
+  const int lane = threadIdx.x & 31;
+  sm100::pdl_wait();
+  sm100::pdl_launch_dependents();
+  int total = 0;
+  for (int r0 = 0; r0 < p.num_rows; r0 += kThreads) {
+    const int row = r0 + threadIdx.x;
+    int b = 0, end = 0, bad = 0;
+    if (row < p.num_rows) {
+      const int64_t len = p.kv_lens[row], add = new_tokens[row];
+      const int64_t need = (len + add + p.page_size - 1) / p.page_size;
+      if (len < 0 || add < 0 || need > p.max_blocks) {
+        bad = 1;
+      } else if (add > 0) {
+        b = (int)(len / p.page_size);
+        end = (int)need;
+      }
+    }
+    // empty blocks from the first empty one on: a lane its own row, or the warp a long one together
+    int at = b;
+    const int32_t* table = p.table + (int64_t)row * p.table_stride;
+    const bool far = end - b > 8;
+    if (!far) {
+      while (at < end && table[at] != -1) ++at;
+      for (int i = at; i < end; ++i) bad |= table[i] != -1;
+    }
+    uint32_t todo = __ballot_sync(0xffffffffu, far);
+    while (todo) {
+      const int k = __ffs(todo) - 1;
+      todo &= todo - 1;
+      const int bk = __shfl_sync(0xffffffffu, b, k), ek = __shfl_sync(0xffffffffu, end, k);
+      const int32_t* t = p.table + (int64_t)(row - lane + k) * p.table_stride;
+      int found = ek, hole = 0;
+      for (int i0 = bk; i0 < ek; i0 += 32) {
+        const bool in = i0 + lane < ek, empty = in && t[i0 + lane] == -1;
+        const uint32_t e = __ballot_sync(0xffffffffu, empty), f = __ballot_sync(0xffffffffu, in && !empty);
+        if (found == ek && e) found = i0 + __ffs(e) - 1;
+        // a page behind an empty block
+        if (found < ek && (f >> max(0, found - i0)) != 0 && i0 + 31 >= found) hole = 1;
+      }
+      if (lane == k) {
+        at = found;
+        bad |= hole;
+      }
+    }
+    if (bad) {
+      record_error(p.status, KDA_ERR_BAD_CACHE_INDEX, 424);
+      at = end;
+    }
+    int sum;
+    const int before = total + block_scan(end - at, part, &sum);
+    if (row < p.num_rows) {
+      first[row] = before;
+      start[row] = at;
+    }
+    total += sum;
+  }
+  __syncthreads();
+  const bool enough = find_free(p.refs, p.num_pages, total, part, [&](int rank, int page) {
+    const int row = request_of(first, p.num_rows, rank);
+    p.table[(int64_t)row * p.table_stride + start[row] + rank - first[row]] = page;
+    p.refs[page] = 1;
+  });
+  if (!enough && threadIdx.x == 0) record_error(p.status, KDA_ERR_OUT_OF_PAGES, 425);
+}
+
+// CTA 0 finds the pages for the partial last ones; the others share whole pages, a row each.  A pair is in
+// order when its rows exist, its source's length fits the table, and no other pair writes to its dst
+// or reads from it: then nothing that one CTA reads is another's to write.
+constexpr int kIsSource = 1 << 30;
+__global__ void __launch_bounds__(kThreads)
+    kda_pages_fork_kernel(const Pool p, const int32_t* src, const int32_t* dst, int num, int32_t* from,
+                          int32_t* to) {
+  extern __shared__ int smem[];
+  int* who = smem;                   // [num] pairs that need a page
+  int* uses = smem + num;            // [num_rows] pairs that write to the row, and whether one reads it
+  __shared__ int part[kWarps + 1];
+  sm100::pdl_wait();
+  sm100::pdl_launch_dependents();
+  if (blockIdx.x > 0) {
+    const int i = blockIdx.x - 1;
+    const int s = src[i], d = dst[i];
+    bool mine = true;
+    for (int j = threadIdx.x; j < num; j += kThreads) mine = mine && src[j] != d && (j == i || dst[j] != d);
+    if (!__syncthreads_and(mine) || s < 0 || s >= p.num_rows || d < 0 || d >= p.num_rows) return;
+    const int len = p.kv_lens[s];
+    if (len < 0 || (int64_t)len > (int64_t)p.max_blocks * p.page_size) return;
+    const int whole = len / p.page_size, tail = len % p.page_size > 0 ? whole : -1;
+    const int32_t* a = p.table + (int64_t)s * p.table_stride;
+    int32_t* b = p.table + (int64_t)d * p.table_stride;
+    for (int x = threadIdx.x; x < p.max_blocks; x += kThreads) {
+      if (x == tail) continue;
+      int pg = -1;
+      if (x < whole) {
+        pg = a[x];
+        if (pg < 0 || pg >= p.num_pages) {
+          record_error(p.status, KDA_ERR_BAD_CACHE_INDEX, 426);
+          pg = -1;
+        } else {
+          atomicAdd(p.refs + pg, 1);
+        }
+      }
+      b[x] = pg;
+    }
+    return;
+  }
+  for (int r = threadIdx.x; r < p.num_rows; r += kThreads) uses[r] = 0;
+  __syncthreads();
+  for (int i = threadIdx.x; i < num; i += kThreads) {
+    const int s = src[i], d = dst[i];
+    if (s >= 0 && s < p.num_rows) atomicOr(uses + s, kIsSource);
+    if (d >= 0 && d < p.num_rows) atomicAdd(uses + d, 1);
+  }
+  __syncthreads();
+  int total = 0;
+  for (int i0 = 0; i0 < num; i0 += kThreads) {
+    const int i = i0 + threadIdx.x;
+    int need = 0;
+    if (i < num) {
+      int pg = -1;
+      const int s = src[i], d = dst[i];
+      bool ok = s >= 0 && s < p.num_rows && d >= 0 && d < p.num_rows && uses[d] == 1;
+      const int len = ok ? p.kv_lens[s] : 0;
+      ok = ok && len >= 0 && (int64_t)len <= (int64_t)p.max_blocks * p.page_size;
+      if (!ok) {
+        record_error(p.status, KDA_ERR_BAD_CACHE_INDEX, 427);
+      } else {
+        p.kv_lens[d] = len;
+        if (len % p.page_size) {
+          pg = p.table[(int64_t)s * p.table_stride + len / p.page_size];
+          need = 1;
+          p.table[(int64_t)d * p.table_stride + len / p.page_size] = -1;
+          if (pg < 0 || pg >= p.num_pages) {
+            record_error(p.status, KDA_ERR_BAD_CACHE_INDEX, 428);
+            need = 0;
+            pg = -1;
+          }
+        }
+      }
+      from[i] = pg;
+      to[i] = -1;
+    }
+    int sum;
+    const int before = total + block_scan(need, part, &sum);
+    if (need) who[before] = i;
+    total += sum;
+  }
+  __syncthreads();
+  const bool enough = find_free(p.refs, p.num_pages, total, part, [&](int rank, int page) {
+    const int i = who[rank];
+    p.table[(int64_t)dst[i] * p.table_stride + p.kv_lens[src[i]] / p.page_size] = page;
+    p.refs[page] = 1;
+    to[i] = page;
+  });
+  if (!enough && threadIdx.x == 0) record_error(p.status, KDA_ERR_OUT_OF_PAGES, 429);
+}
+
+// A CTA copies one side of one head of a page: page_size rows of 128 bytes, eight threads a row.
+constexpr int kCopyThreads = 128;
+__global__ void __launch_bounds__(kCopyThreads)
+    kda_pages_copy_kernel(const __grid_constant__ attn::CacheView c, const int32_t* from, const int32_t* to,
+                          int* status) {
+  sm100::pdl_wait();
+  sm100::pdl_launch_dependents();
+  const int units = 2 * c.kv_heads, i = blockIdx.x / units, h = (blockIdx.x % units) >> 1, side = blockIdx.x & 1;
+  const int a = from[i], b = to[i];
+  if (a < 0 || b < 0 || a == b) return;
+  if (a >= c.num_pages || b >= c.num_pages) {
+    if (threadIdx.x == 0) record_error(status, KDA_ERR_BAD_CACHE_INDEX, 430);
+    return;
+  }
+  uint8_t* base = (side ? c.v : c.k) + h * c.head_stride + (threadIdx.x & 7) * 16;
+  const uint8_t* src = base + (int64_t)a * c.page_stride;
+  uint8_t* dst = base + (int64_t)b * c.page_stride;
+  constexpr int kRows = kCopyThreads / 8, kAhead = 4;
+  for (int r0 = threadIdx.x >> 3; r0 < c.page_size; r0 += kRows * kAhead) {
+    uint4 u[kAhead];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j)
+      if (r0 + kRows * j < c.page_size)
+        u[j] = *reinterpret_cast<const uint4*>(src + (int64_t)(r0 + kRows * j) * c.token_stride);
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j)
+      if (r0 + kRows * j < c.page_size)
+        *reinterpret_cast<uint4*>(dst + (int64_t)(r0 + kRows * j) * c.token_stride) = u[j];
+  }
+  if (threadIdx.x == 0) {
+    float* s = side ? c.v_scale : c.k_scale;
+    s[(int64_t)b * c.scale_stride + h] = s[(int64_t)a * c.scale_stride + h];
+  }
+}
+
+cudaError_t allow_smem(const void* kernel, PerDeviceOnce& once, int bytes) {
+  int dev = 0;
+  const cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  return once.run(dev, [&]() -> cudaError_t {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  });
+}
+
+}  // namespace
+
+cudaError_t launch_free(const Pool& p, const int32_t* rows, int32_t num, cudaStream_t stream) {
+  return attn::launch(kda_pages_free_kernel, dim3((unsigned)(rows ? num : p.num_rows)), dim3(kFreeThreads), 0,
+                      true, stream, p, rows);
+}
+
+cudaError_t launch_reserve(const Pool& p, const int32_t* new_tokens, cudaStream_t stream) {
+  static PerDeviceOnce once;
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kda_pages_reserve_kernel), once,
+                                   kMaxRows * 8);
+  if (e != cudaSuccess) return e;
+  return attn::launch(kda_pages_reserve_kernel, dim3(1), dim3(kThreads), (size_t)p.num_rows * 8, true, stream,
+                      p, new_tokens);
+}
+
+cudaError_t launch_fork(const Pool& p, const int32_t* src, const int32_t* dst, int32_t num, int32_t* from,
+                        int32_t* to, cudaStream_t stream) {
+  static PerDeviceOnce once;
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kda_pages_fork_kernel), once, kMaxRows * 8);
+  if (e != cudaSuccess) return e;
+  return attn::launch(kda_pages_fork_kernel, dim3((unsigned)num + 1), dim3(kThreads), (size_t)(num + p.num_rows) * 4, true,
+                      stream, p, src, dst, num, from, to);
+}
+
+cudaError_t launch_copy(const attn::CacheView& c, const int32_t* from, const int32_t* to, int64_t num,
+                        int* status, cudaStream_t stream) {
+  const int64_t ctas = num * c.kv_heads * 2;
+  if (ctas > INT32_MAX) return cudaErrorInvalidValue;
+  return attn::launch(kda_pages_copy_kernel, dim3((unsigned)ctas), dim3(kCopyThreads), 0, true, stream, c, from,
+                      to, status);
+}
+
+}  // namespace pages
+}  // namespace kda

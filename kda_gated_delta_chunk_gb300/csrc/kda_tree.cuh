@@ -46,5 +46,28 @@ struct PlanParams {
 };
 cudaError_t launch_plan(const PlanParams& p, cudaStream_t stream);
 
+// A sequence's accepted branch, for a CTA's threads: parents into `links` (shared, kNodes ints), then
+// the nodes from the cached text to `node` as bits.  Every warp walks by itself.  Barriers inside.
+__device__ __forceinline__ uint64_t branch_of(const int32_t* parents, const Nodes& s, int node, int* links,
+                                              int* status, bool report) {
+  for (int i = threadIdx.x; i < s.n; i += blockDim.x) links[i] = parent_of(parents, s, i, status, report);
+  __syncthreads();
+  uint64_t on = 0;
+  for (int i = node; i >= 0; i = links[i]) on |= 1ull << i;
+  return on;
+}
+
+struct AcceptParams {
+  attn::CacheView c;
+  const int32_t* cu_seqlens;
+  const int32_t* parents;
+  const int32_t* accepted;
+  int32_t* lens_out;
+  int* status;
+  int64_t total_tokens;
+  int32_t num_seqs, max_q_len;
+};
+cudaError_t launch_accept(const AcceptParams& p, cudaStream_t stream);
+
 }  // namespace tree
 }  // namespace kda

@@ -1,6 +1,7 @@
-// C entry points of the operators on drafted trees: argument checks and dispatch.  Declared in
+// C entry points of the operators on drafted trees and on the cache's pages: argument checks and dispatch.  Declared in
 // include/kda.h.
 #include "kda_checks.cuh"
+#include "kda_pages.cuh"
 #include "kda_tree.cuh"
 
 using namespace kda::checks;
@@ -16,6 +17,29 @@ int check_trees(const void* cu_seqlens, const void* parents, const void* workspa
   if (total_tokens > 0 && (!parents || max_q_len < 1)) return KDA_ERR_INVALID_ARG;
   if (workspace_bytes < (size_t)kda::kWorkspaceBytes) return KDA_ERR_WORKSPACE_TOO_SMALL;
   if (!aligned(cu_seqlens, 4) || !aligned(parents, 4) || !aligned(workspace, 16)) return KDA_ERR_MISALIGNED;
+  return KDA_OK;
+}
+
+// The pool's own fields.
+int check_pool(int32_t* refs, int32_t num_pages, int32_t* block_table, int64_t table_stride, int32_t num_rows,
+               int32_t max_blocks, int32_t* kv_lens, int32_t page_size, void* workspace, size_t workspace_bytes,
+               kda::pages::Pool* p) {
+  if (!refs || !workspace || num_pages < 1 || num_rows < 0 || max_blocks < 0 || table_stride < max_blocks ||
+      table_stride > ((int64_t)1 << 40) || page_size < 1 || (int64_t)max_blocks * page_size > INT32_MAX)
+    return KDA_ERR_INVALID_ARG;
+  if (num_rows > 0 && (!kv_lens || (!block_table && max_blocks > 0))) return KDA_ERR_INVALID_ARG;
+  if (workspace_bytes < (size_t)kda::kWorkspaceBytes) return KDA_ERR_WORKSPACE_TOO_SMALL;
+  if (!aligned(refs, 16) || !aligned(block_table, 4) || !aligned(kv_lens, 4) || !aligned(workspace, 16))
+    return KDA_ERR_MISALIGNED;
+  p->refs = refs;
+  p->table = block_table;
+  p->table_stride = table_stride;
+  p->kv_lens = kv_lens;
+  p->status = static_cast<int*>(workspace);
+  p->num_pages = num_pages;
+  p->page_size = page_size;
+  p->num_rows = num_rows;
+  p->max_blocks = max_blocks;
   return KDA_OK;
 }
 
@@ -46,6 +70,104 @@ int kda_tree_plan(const int32_t* parents, const int32_t* cu_seqlens, const int32
   p.num_seqs = num_seqs;
   p.max_q_len = max_q_len;
   return launched(kda::tree::launch_plan(p, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int kda_cache_accept(const kda_kv_cache* cache, const int32_t* cu_seqlens, const int32_t* parents,
+                     const int32_t* accepted, int32_t* lens_out, void* workspace, kda_stream_t stream,
+                     int64_t total_tokens, int32_t num_seqs, int32_t max_q_len, size_t workspace_bytes) {
+  kda::tree::AcceptParams p{};
+  int rc = check_trees(cu_seqlens, parents, workspace, total_tokens, num_seqs, max_q_len, workspace_bytes);
+  if (rc != KDA_OK) return rc;
+  if ((rc = check_cache(cache, num_seqs, &p.c)) != KDA_OK) return rc;
+  if (num_seqs > 0 && (!accepted || !lens_out || (const void*)lens_out == (const void*)cache->kv_lens))
+    return KDA_ERR_INVALID_ARG;
+  if ((int64_t)num_seqs * cache->kv_heads * 2 > INT32_MAX) return KDA_ERR_INVALID_ARG;
+  if (!aligned(accepted, 4) || !aligned(lens_out, 4)) return KDA_ERR_MISALIGNED;
+  int sms = 0;
+  rc = current_device(&sms);
+  if (rc != KDA_OK) return rc;
+  if (num_seqs == 0) return KDA_OK;
+  p.cu_seqlens = cu_seqlens;
+  p.parents = parents;
+  p.accepted = accepted;
+  p.lens_out = lens_out;
+  p.status = static_cast<int*>(workspace);
+  p.total_tokens = total_tokens;
+  p.num_seqs = num_seqs;
+  p.max_q_len = max_q_len;
+  return launched(kda::tree::launch_accept(p, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int kda_pages_free(int32_t* refs, int32_t num_pages, int32_t* block_table, int64_t table_stride,
+                   int32_t num_rows, int32_t max_blocks, int32_t* kv_lens, int32_t page_size,
+                   const int32_t* rows, int32_t num, void* workspace, size_t workspace_bytes,
+                   kda_stream_t stream) {
+  kda::pages::Pool p{};
+  int rc = check_pool(refs, num_pages, block_table, table_stride, num_rows, max_blocks, kv_lens, page_size,
+                      workspace, workspace_bytes, &p);
+  if (rc != KDA_OK) return rc;
+  if (num < 0) return KDA_ERR_INVALID_ARG;
+  if (!aligned(rows, 4)) return KDA_ERR_MISALIGNED;
+  int sms = 0;
+  rc = current_device(&sms);
+  if (rc != KDA_OK) return rc;
+  if (num_rows == 0 || (rows && num == 0)) return KDA_OK;
+  return launched(kda::pages::launch_free(p, rows, num, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int kda_pages_reserve(int32_t* refs, int32_t num_pages, int32_t* block_table, int64_t table_stride,
+                      int32_t num_rows, int32_t max_blocks, int32_t* kv_lens, int32_t page_size,
+                      const int32_t* new_tokens, void* workspace, size_t workspace_bytes,
+                      kda_stream_t stream) {
+  kda::pages::Pool p{};
+  int rc = check_pool(refs, num_pages, block_table, table_stride, num_rows, max_blocks, kv_lens, page_size,
+                      workspace, workspace_bytes, &p);
+  if (rc != KDA_OK) return rc;
+  if (num_rows > kda::pages::kMaxRows || (num_rows > 0 && !new_tokens)) return KDA_ERR_INVALID_ARG;
+  if (!aligned(new_tokens, 4)) return KDA_ERR_MISALIGNED;
+  int sms = 0;
+  rc = current_device(&sms);
+  if (rc != KDA_OK) return rc;
+  if (num_rows == 0) return KDA_OK;
+  return launched(kda::pages::launch_reserve(p, new_tokens, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int kda_pages_fork(int32_t* refs, int32_t num_pages, int32_t* block_table, int64_t table_stride,
+                   int32_t num_rows, int32_t max_blocks, int32_t* kv_lens, int32_t page_size,
+                   const int32_t* src, const int32_t* dst, int32_t num, int32_t* from_pages,
+                   int32_t* to_pages, void* workspace, size_t workspace_bytes, kda_stream_t stream) {
+  kda::pages::Pool p{};
+  int rc = check_pool(refs, num_pages, block_table, table_stride, num_rows, max_blocks, kv_lens, page_size,
+                      workspace, workspace_bytes, &p);
+  if (rc != KDA_OK) return rc;
+  if (num < 0 || num > kda::pages::kMaxRows || num_rows > kda::pages::kMaxRows) return KDA_ERR_INVALID_ARG;
+  if (num > 0 && (!src || !dst || !from_pages || !to_pages)) return KDA_ERR_INVALID_ARG;
+  if (!aligned(src, 4) || !aligned(dst, 4) || !aligned(from_pages, 4) || !aligned(to_pages, 4))
+    return KDA_ERR_MISALIGNED;
+  int sms = 0;
+  rc = current_device(&sms);
+  if (rc != KDA_OK) return rc;
+  if (num == 0) return KDA_OK;
+  return launched(kda::pages::launch_fork(p, src, dst, num, from_pages, to_pages,
+                                          reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int kda_pages_copy(const kda_kv_cache* cache, const int32_t* from_pages, const int32_t* to_pages, int64_t num,
+                   void* workspace, size_t workspace_bytes, kda_stream_t stream) {
+  kda::attn::CacheView c{};
+  int rc = check_cache(cache, 0, &c);
+  if (rc != KDA_OK) return rc;
+  if (!workspace || num < 0 || num > INT32_MAX || num * cache->kv_heads * 2 > INT32_MAX ||
+      (num > 0 && (!from_pages || !to_pages)))
+    return KDA_ERR_INVALID_ARG;
+  if (workspace_bytes < (size_t)kda::kWorkspaceBytes) return KDA_ERR_WORKSPACE_TOO_SMALL;
+  if (!aligned(from_pages, 4) || !aligned(to_pages, 4) || !aligned(workspace, 16)) return KDA_ERR_MISALIGNED;
+  int sms = 0;
+  rc = current_device(&sms);
+  if (rc != KDA_OK) return rc;
+  if (num == 0) return KDA_OK;
+  return launched(kda::pages::launch_copy(c, from_pages, to_pages, num, static_cast<int*>(workspace),
+                                          reinterpret_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

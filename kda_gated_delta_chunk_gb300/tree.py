@@ -15,7 +15,7 @@ from __future__ import annotations
 import torch
 
 from . import KDAError, OK, _elsewhere, _within, lib
-from .layer import _I32, _INT, _MASK, _check, _i32, _need_cuda, _status_workspace, _stream
+from .layer import _I32, _INT, _MASK, _cache, _check, _i32, _need_cuda, _status_workspace, _stream
 
 
 def _batch(parents, cu_seqlens, dev):
@@ -58,3 +58,32 @@ def tree_plan(parents, cu_seqlens, kv_lens, max_q_len: int, mask=None, positions
     if rc != OK:
         raise KDAError(rc, "kda_tree_plan")
     return mask, positions
+
+
+def cache_accept(k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, cu_seqlens, parents, accepted,
+                 max_q_len: int, lens_out=None, workspace=None, stream=None):
+    """Run ``kda_cache_accept``: move each tree's accepted branch together in one layer's cache.
+
+    The cache and its indexes as for ``tree_attention``; accepted: int32 [num_seqs], the last accepted
+    node of each sequence (-1: none).  The cache is updated in place.  Returns lens_out, int32
+    [num_seqs]: the cached tokens from there on (a tensor of its own: every layer's call reads kv_lens).
+    """
+    dev = _need_cuda(k_cache, "k_cache")
+    place = _elsewhere(stream, k_cache)
+    if place is not None:
+        return _within(place, cache_accept, (lens_out,), k_cache, v_cache, k_scale, v_scale, block_table, kv_lens,
+                       cu_seqlens, parents, accepted, max_q_len, lens_out, workspace)
+    T, N = _batch(parents, cu_seqlens, dev)
+    c, _ = _cache(k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, N, dev)
+    _check(accepted, "accepted", _INT, (N,), dev, 0)
+    if lens_out is None:
+        lens_out = torch.empty(N, dtype=_I32, device=k_cache.device)
+    else:
+        _check(lens_out, "lens_out", _INT, (N,), dev, 0)
+    workspace = _status_workspace(workspace, dev)
+    rc = lib().kda_cache_accept(c, cu_seqlens.data_ptr(), parents.data_ptr(), accepted.data_ptr(),
+                                lens_out.data_ptr(), workspace.data_ptr(), _stream(stream, dev), T, N,
+                                _i32(max_q_len, "max_q_len"), workspace.numel())
+    if rc != OK:
+        raise KDAError(rc, "kda_cache_accept")
+    return lens_out

@@ -55,3 +55,56 @@ def test_binding_refuses_host_tensors():
 def test_new_codes_have_texts(L):
     assert "tree" in kda.status_string(kda.ERR_BAD_TREE)
     assert "pages" in kda.status_string(kda.ERR_OUT_OF_PAGES)
+
+
+def accept(L, c=None, **over):
+    a = dict(c=ctypes.byref(c if c is not None else cache()), cu=A, parents=A, node=A, lens=2 * A, ws=A, stream=None,
+             T=4, N=1, most=4, wsb=256)
+    a.update(over)
+    return L.kda_cache_accept(*a.values())
+
+
+@pytest.mark.parametrize("over,code", [
+    (dict(most=65), INVALID), (dict(parents=None), INVALID), (dict(node=None), INVALID), (dict(lens=None), INVALID),
+    (dict(lens=A), INVALID), (dict(N=2 ** 30), INVALID), (dict(node=A + 2), MISALIGNED), (dict(lens=A + 1), MISALIGNED),
+    (dict(wsb=0), kda.ERR_WORKSPACE_TOO_SMALL)])
+def test_accept_refuses(L, over, code):
+    assert accept(L, **over) == code
+
+
+POOL = dict(refs=A, pages=10, table=A, stride=4, rows=3, blocks=4, lens=A, page=16)
+
+
+def pool(L, call, **over):
+    tail = dict(free=dict(list=A, num=2), reserve=dict(new=A), fork=dict(src=A, dst=A, num=2, fro=A, to=A))[call]
+    a = dict(POOL, **tail, ws=A, wsb=256, stream=None)
+    a.update(over)
+    return getattr(L, "kda_pages_" + call)(*a.values())
+
+
+@pytest.mark.parametrize("call", ["free", "reserve", "fork"])
+@pytest.mark.parametrize("over,code", [
+    (dict(refs=None), INVALID), (dict(pages=0), INVALID), (dict(table=None), INVALID), (dict(stride=3), INVALID),
+    (dict(rows=-1), INVALID), (dict(blocks=-1), INVALID), (dict(lens=None), INVALID), (dict(page=0), INVALID),
+    (dict(page=2 ** 30), INVALID), (dict(ws=None), INVALID), (dict(refs=A + 4), MISALIGNED), (dict(table=A + 2), MISALIGNED),
+    (dict(lens=A + 2), MISALIGNED), (dict(ws=A + 4), MISALIGNED), (dict(wsb=16), kda.ERR_WORKSPACE_TOO_SMALL)])
+def test_pool_refuses(L, call, over, code):
+    assert pool(L, call, **over) == code
+
+
+@pytest.mark.parametrize("call,over", [
+    ("free", dict(num=-1)), ("reserve", dict(new=None)), ("reserve", dict(rows=16385)), ("fork", dict(num=16385)),
+    ("fork", dict(num=-1)), ("fork", dict(rows=16385)), ("fork", dict(src=None)), ("fork", dict(dst=None)),
+    ("fork", dict(fro=None)), ("fork", dict(to=None))])
+def test_pool_calls_refuse(L, call, over):
+    assert pool(L, call, **over) == INVALID
+
+
+@pytest.mark.parametrize("over,code", [
+    (dict(fro=None), INVALID), (dict(to=None), INVALID), (dict(num=-1), INVALID), (dict(num=2 ** 30), INVALID),
+    (dict(ws=None), INVALID), (dict(c=None), INVALID), (dict(fro=A + 2), MISALIGNED),
+    (dict(wsb=0), kda.ERR_WORKSPACE_TOO_SMALL)])
+def test_copy_refuses(L, over, code):
+    a = dict(c=ctypes.byref(cache()), fro=A, to=A, num=2, ws=A, wsb=256, stream=None)
+    a.update(over)
+    assert L.kda_pages_copy(*a.values()) == code

@@ -69,3 +69,77 @@ def attention(q, masks, kc, vc, ks, vs, table, kv_len, scale, softcap=0.0, windo
             out[i, g * G:(g + 1) * G] = p @ v[keys]
             big[i, g * G:(g + 1) * G] = p @ v[keys].abs()
     return out, lse, big
+
+
+def accept(values, scales, table, kv_len, parents, node):
+    """One side of one layer's cache after a sequence's branch to `node` was accepted.  values: float64
+    e4m3 values [pages, heads, slots, D], scales float64 [pages, heads]; both changed in place.  Returns
+    the sequence's new length."""
+    from layer_ref import e4m3_grid
+    P, n = values.shape[2], len(parents)
+    start, path = kv_len - n, branch(parents, node)
+    was, old = values.clone(), scales.clone()
+    at = lambda pos: (int(table[pos // P]), pos % P)  # noqa: E731
+    for blk in range(start // P, (start + len(path) - 1) // P + 1 if path else 0):
+        pg = int(table[blk])
+        mine = [e for e in range(len(path)) if (start + e) // P == blk]
+        if all(path[e] == e for e in mine):
+            continue
+        kept = max(0, start - blk * P)
+        for h in range(values.shape[1]):
+            froms = [at(start + path[e]) for e in mine]
+            s = max([float(old[q, h]) for q, _ in froms] + ([float(old[pg, h])] if kept else []))
+            scales[pg, h] = s
+            if float(old[pg, h]) != s:
+                values[pg, h, :kept] = e4m3_grid(was[pg, h, :kept] * (float(old[pg, h]) / s))
+            for e, (q, slot) in zip(mine, froms):
+                x = was[q, h, slot]
+                values[pg, h, (start + e) % P] = x if float(old[q, h]) == s else e4m3_grid(x * (float(old[q, h]) / s))
+    return start + len(path)
+
+
+class Pool:
+    """The pool's calls in plain Python."""
+
+    def __init__(self, refs, table, lens, page):
+        self.refs, self.table, self.lens, self.page = list(refs), [list(r) for r in table], list(lens), page
+
+    def free(self, rows=None):
+        for r in range(len(self.lens)) if rows is None else dict.fromkeys(rows):
+            if rows is not None:
+                self.lens[r] = 0
+            for b in range(-(-self.lens[r] // self.page), len(self.table[r])):
+                if self.table[r][b] >= 0:
+                    self.refs[self.table[r][b]] -= 1
+                self.table[r][b] = -1
+
+    def take(self):
+        if 0 not in self.refs:
+            return -1
+        pg = self.refs.index(0)
+        self.refs[pg] = 1
+        return pg
+
+    def reserve(self, new):
+        for r, a in enumerate(new):
+            if a == 0:
+                continue
+            for b in range(self.lens[r] // self.page, -(-(self.lens[r] + a) // self.page)):
+                if self.table[r][b] < 0:
+                    self.table[r][b] = self.take()
+
+    def fork(self, src, dst):
+        """The rows share whole pages first, then the partial ones are given out."""
+        fro, to = [-1] * len(src), [-1] * len(src)
+        for s, d in zip(src, dst):
+            whole = self.lens[s] // self.page
+            self.table[d] = [self.table[s][b] if b < whole else -1 for b in range(len(self.table[d]))]
+            for b in range(whole):
+                self.refs[self.table[s][b]] += 1
+            self.lens[d] = self.lens[s]
+        for i, (s, d) in enumerate(zip(src, dst)):
+            if self.lens[s] % self.page:
+                whole = self.lens[s] // self.page
+                fro[i], to[i] = self.table[s][whole], self.take()
+                self.table[d][whole] = to[i]
+        return fro, to
