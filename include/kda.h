@@ -491,6 +491,43 @@ int kda_tree_attention(const void* q, int64_t q_stride, const kda_kv_cache* cach
                        int32_t max_q_len, size_t workspace_bytes);
 
 /*
+ * The KDA recurrence (kda_recurrent_fwd) along the branches of trees: the state that node i continues from is its
+ * parent's, or the sequence's initial state.  No state is written: the outputs are, and u, from which
+ * kda_tree_commit makes the accepted node's state.
+ *   q, k, v, g   bf16 [T, heads, 128], beta bf16 [T, heads]: a token's heads dense, strides (elements)
+ *                between tokens; those of q, k, v, g multiples of 8 from 16-byte aligned pointers
+ *   initial_state, state_dtype, A_log, dt_bias, lower_bound, scale: as kda_recurrent_fwd; the state is
+ *                read only, and may be NULL (zeros)
+ *   out          bf16 [T, heads, 128], dense
+ *   u            fp32 [T, heads, 128], dense, 16-byte aligned: what each node adds to the state,
+ *                S_i = diag(decay_i) S_parent + kh_i u_i^T
+ * Sums, decays and u are fp32; the state's products take two f16 terms of each factor (22 bits).  Device errors:
+ * KDA_ERR_BAD_CU_SEQLENS, KDA_ERR_INVALID_ARG (more nodes than max_q_len): that sequence's rows are not
+ * written; KDA_ERR_BAD_TREE.
+ */
+int kda_tree_recurrent_fwd(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                           int64_t v_stride, const void* g, int64_t g_stride, const void* beta,
+                           int64_t beta_stride, const float* A_log, const float* dt_bias, float lower_bound,
+                           float scale, const void* initial_state, int state_dtype,
+                           const int32_t* cu_seqlens, const int32_t* parents, void* out, float* u,
+                           void* workspace, kda_stream_t stream, int64_t total_tokens, int32_t num_seqs,
+                           int32_t heads, int32_t max_q_len, size_t workspace_bytes);
+
+/*
+ * The state after node accepted[n] (-1: as before the tree) of each sequence, from the k, g and u of
+ * kda_tree_recurrent_fwd's call, the other arguments being that call's.
+ *   accepted      int32 [num_seqs]
+ *   final_state   [num_seqs, heads, 128, 128] in state_dtype; may be initial_state (the update is then in place)
+ * A malformed sequence (KDA_ERR_BAD_CU_SEQLENS, KDA_ERR_INVALID_ARG, KDA_ERR_BAD_TREE for accepted out of range) keeps its
+ * initial state.
+ */
+int kda_tree_commit(const void* k, int64_t k_stride, const void* g, int64_t g_stride, const float* A_log,
+                    const float* dt_bias, float lower_bound, const void* initial_state, void* final_state,
+                    int state_dtype, const int32_t* cu_seqlens, const int32_t* parents, const float* u,
+                    const int32_t* accepted, void* workspace, kda_stream_t stream, int64_t total_tokens,
+                    int32_t num_seqs, int32_t heads, int32_t max_q_len, size_t workspace_bytes);
+
+/*
  * Moves the accepted branch of each sequence's tree together in one layer's cache.  With
  * start = kv_lens - nodes, the e-th node of the branch that ends at node accepted[n] (-1: none is accepted)
  * goes from cache position start + its index to start + e; positions behind the branch keep what they

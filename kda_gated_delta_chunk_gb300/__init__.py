@@ -21,7 +21,8 @@ names follow the C ABI in ``include/kda.h``:
     status_string(code) -> str
     add_rms_norm, rope_table, rope_append, cached_attention: the full-attention layer beside the KDA layers
         (layer.py)
-    tree_plan, tree_attention, cache_accept: trees of drafted tokens (tree.py, layer.py)
+    tree_plan, tree_attention, tree_recurrent_fwd, tree_commit, cache_accept: trees of drafted
+        tokens (tree.py, layer.py)
     free_pages, reserve_pages, fork_pages, copy_pages: the paged cache's pages (pages.py)
 
 There is no CPU fallback: if the library is missing or the device is not an
@@ -66,7 +67,7 @@ EXPORTS = ("kda_workspace_size", "kda_chunk_prefill_fwd", "kda_chunk_prefill_fwd
            "kda_recurrent_fwd_scatter", "kda_skinny_proj_workspace_size", "kda_skinny_proj",
            "kda_test_drop_one_record", "kda_add_rms_norm", "kda_rope_append",
            "kda_attention_workspace_size", "kda_cached_attention", "kda_tree_plan",
-           "kda_tree_attention", "kda_cache_accept", "kda_pages_free", "kda_pages_reserve",
+           "kda_tree_attention", "kda_tree_recurrent_fwd", "kda_tree_commit", "kda_cache_accept", "kda_pages_free", "kda_pages_reserve",
            "kda_pages_fork", "kda_pages_copy")
 
 _lib = None
@@ -165,6 +166,12 @@ def lib() -> ctypes.CDLL:
             L.kda_tree_attention.restype = I
             L.kda_tree_attention.argtypes = [P, I64, P, P, P, F, F, I32, P, I64, P, P, P, I64, I32, I32,
                                              I32, SZ]
+            L.kda_tree_recurrent_fwd.restype = I
+            L.kda_tree_recurrent_fwd.argtypes = [P, I64] * 5 + [P, P, F, F, P, I, P, P, P, P, P, P, I64, I32,
+                                                              I32, I32, SZ]
+            L.kda_tree_commit.restype = I
+            L.kda_tree_commit.argtypes = [P, I64, P, I64, P, P, F, P, P, I, P, P, P, P, P, P, I64, I32, I32,
+                                          I32, SZ]
             L.kda_cache_accept.restype = I
             L.kda_cache_accept.argtypes = [P, P, P, P, P, P, P, I64, I32, I32, SZ]
             pool = [P, I32, P, I64, I32, I32, P, I32]
@@ -543,5 +550,5 @@ def chunk_prefill_fwd_noalloc(q, k, v, g, beta, A_log, dt_bias, lower_bound, sca
 from .layer import (add_rms_norm, alloc_attention_workspace,  # noqa: E402  (uses the names above)
                     attention_workspace_size, cached_attention, rope_append, rope_table,
                     tree_attention)
-from .tree import cache_accept, tree_plan  # noqa: E402
+from .tree import cache_accept, tree_commit, tree_plan, tree_recurrent_fwd  # noqa: E402
 from .pages import copy_pages, fork_pages, free_pages, reserve_pages  # noqa: E402

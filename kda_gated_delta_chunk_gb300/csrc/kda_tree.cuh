@@ -69,5 +69,37 @@ struct AcceptParams {
 };
 cudaError_t launch_accept(const AcceptParams& p, cudaStream_t stream);
 
+// The KDA recurrence along trees.  q, k, v, g, beta: bf16, a token's heads dense, strides between tokens.
+struct RecurParams {
+  const __nv_bfloat16* q;
+  const __nv_bfloat16* k;
+  const __nv_bfloat16* v;
+  const __nv_bfloat16* g;
+  const __nv_bfloat16* beta;
+  int64_t s_q, s_k, s_v, s_g, s_beta;
+  const float* A_log;
+  const float* dt_bias;
+  float lower_bound, scale;
+  const void* initial_state;   // [num_seqs, heads, 128, 128] or null (zeros)
+  int state_bf16;
+  const int32_t* cu_seqlens;
+  const int32_t* parents;
+  __nv_bfloat16* out;          // [total_tokens, heads, 128]
+  float* u;                    // [total_tokens, heads, 128]
+  const int32_t* accepted;     // commit: [num_seqs]
+  void* final_state;           // commit
+  int* status;
+  int64_t total_tokens;
+  int32_t num_seqs, heads, max_q_len;
+};
+cudaError_t launch_recur(const RecurParams& p, cudaStream_t stream);
+cudaError_t launch_commit(const RecurParams& p, cudaStream_t stream);
+
+// Decay of a channel: exp(lower_bound sigmoid(exp(A_log) (g + dt_bias))), with exp and division to fp32's
+// precision: the states it multiplies are held in fp32.
+__device__ __forceinline__ float decay_of(float g, float dt, float gsc, float lower_bound) {
+  return expf(lower_bound / (1.0f + expf(-gsc * (g + dt))));
+}
+
 }  // namespace tree
 }  // namespace kda

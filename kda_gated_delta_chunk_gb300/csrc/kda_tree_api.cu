@@ -1,5 +1,7 @@
 // C entry points of the operators on drafted trees and on the cache's pages: argument checks and dispatch.  Declared in
 // include/kda.h.
+#include <cmath>
+
 #include "kda_checks.cuh"
 #include "kda_pages.cuh"
 #include "kda_tree.cuh"
@@ -17,6 +19,38 @@ int check_trees(const void* cu_seqlens, const void* parents, const void* workspa
   if (total_tokens > 0 && (!parents || max_q_len < 1)) return KDA_ERR_INVALID_ARG;
   if (workspace_bytes < (size_t)kda::kWorkspaceBytes) return KDA_ERR_WORKSPACE_TOO_SMALL;
   if (!aligned(cu_seqlens, 4) || !aligned(parents, 4) || !aligned(workspace, 16)) return KDA_ERR_MISALIGNED;
+  return KDA_OK;
+}
+
+// What the recurrence and its commit have in common.  Nodes' tensors are checked where there are any.
+int check_recur(const void* k, int64_t k_stride, const void* g, int64_t g_stride, const float* A_log,
+                const float* dt_bias, float lower_bound, const void* initial_state, int state_dtype,
+                const float* u, int64_t total_tokens, int32_t num_seqs, int32_t heads,
+                kda::tree::RecurParams* p) {
+  if (heads < 1 || (int64_t)num_seqs * heads > INT32_MAX || !known_dtype(state_dtype) || !A_log || !dt_bias)
+    return KDA_ERR_INVALID_ARG;
+  if (!(lower_bound >= KDA_MIN_LOWER_BOUND && lower_bound <= 0.0f)) return KDA_ERR_UNSAFE_LOWER_BOUND;
+  if (!aligned(A_log, 4) || !aligned(dt_bias, 16) || !aligned(initial_state, 16)) return KDA_ERR_MISALIGNED;
+  if (total_tokens > 0) {
+    int rc;
+    if ((rc = check_rows(k, k_stride, heads)) != KDA_OK) return rc;
+    if ((rc = check_rows(g, g_stride, heads)) != KDA_OK) return rc;
+    if (!u) return KDA_ERR_INVALID_ARG;
+    if (!aligned(u, 16)) return KDA_ERR_MISALIGNED;
+  }
+  p->k = static_cast<const __nv_bfloat16*>(k);
+  p->g = static_cast<const __nv_bfloat16*>(g);
+  p->s_k = k_stride;
+  p->s_g = g_stride;
+  p->A_log = A_log;
+  p->dt_bias = dt_bias;
+  p->lower_bound = lower_bound;
+  p->initial_state = initial_state;
+  p->state_bf16 = state_dtype == KDA_STATE_BF16;
+  p->u = const_cast<float*>(u);
+  p->total_tokens = total_tokens;
+  p->num_seqs = num_seqs;
+  p->heads = heads;
   return KDA_OK;
 }
 
@@ -70,6 +104,71 @@ int kda_tree_plan(const int32_t* parents, const int32_t* cu_seqlens, const int32
   p.num_seqs = num_seqs;
   p.max_q_len = max_q_len;
   return launched(kda::tree::launch_plan(p, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int kda_tree_recurrent_fwd(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                           int64_t v_stride, const void* g, int64_t g_stride, const void* beta,
+                           int64_t beta_stride, const float* A_log, const float* dt_bias, float lower_bound,
+                           float scale, const void* initial_state, int state_dtype,
+                           const int32_t* cu_seqlens, const int32_t* parents, void* out, float* u,
+                           void* workspace, kda_stream_t stream, int64_t total_tokens, int32_t num_seqs,
+                           int32_t heads, int32_t max_q_len, size_t workspace_bytes) {
+  kda::tree::RecurParams p{};
+  int rc = check_trees(cu_seqlens, parents, workspace, total_tokens, num_seqs, max_q_len, workspace_bytes);
+  if (rc != KDA_OK) return rc;
+  rc = check_recur(k, k_stride, g, g_stride, A_log, dt_bias, lower_bound, initial_state, state_dtype, u,
+                   total_tokens, num_seqs, heads, &p);
+  if (rc != KDA_OK) return rc;
+  if (!std::isfinite(scale)) return KDA_ERR_INVALID_ARG;
+  if (total_tokens > 0) {
+    if ((rc = check_rows(q, q_stride, heads)) != KDA_OK) return rc;
+    if ((rc = check_rows(v, v_stride, heads)) != KDA_OK) return rc;
+    if (!beta || beta_stride < heads || beta_stride > ((int64_t)1 << 40) || !out) return KDA_ERR_INVALID_ARG;
+    if (!aligned(beta, 2) || !aligned(out, 16)) return KDA_ERR_MISALIGNED;
+  }
+  int sms = 0;
+  rc = current_device(&sms);
+  if (rc != KDA_OK) return rc;
+  if (num_seqs == 0 || total_tokens == 0) return KDA_OK;
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.v = static_cast<const __nv_bfloat16*>(v);
+  p.beta = static_cast<const __nv_bfloat16*>(beta);
+  p.s_q = q_stride;
+  p.s_v = v_stride;
+  p.s_beta = beta_stride;
+  p.scale = scale;
+  p.cu_seqlens = cu_seqlens;
+  p.parents = parents;
+  p.out = static_cast<__nv_bfloat16*>(out);
+  p.status = static_cast<int*>(workspace);
+  p.max_q_len = max_q_len;
+  return launched(kda::tree::launch_recur(p, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int kda_tree_commit(const void* k, int64_t k_stride, const void* g, int64_t g_stride, const float* A_log,
+                    const float* dt_bias, float lower_bound, const void* initial_state, void* final_state,
+                    int state_dtype, const int32_t* cu_seqlens, const int32_t* parents, const float* u,
+                    const int32_t* accepted, void* workspace, kda_stream_t stream, int64_t total_tokens,
+                    int32_t num_seqs, int32_t heads, int32_t max_q_len, size_t workspace_bytes) {
+  kda::tree::RecurParams p{};
+  int rc = check_trees(cu_seqlens, parents, workspace, total_tokens, num_seqs, max_q_len, workspace_bytes);
+  if (rc != KDA_OK) return rc;
+  rc = check_recur(k, k_stride, g, g_stride, A_log, dt_bias, lower_bound, initial_state, state_dtype, u,
+                   total_tokens, num_seqs, heads, &p);
+  if (rc != KDA_OK) return rc;
+  if (num_seqs > 0 && (!accepted || !final_state)) return KDA_ERR_INVALID_ARG;
+  if (!aligned(accepted, 4) || !aligned(final_state, 16)) return KDA_ERR_MISALIGNED;
+  int sms = 0;
+  rc = current_device(&sms);
+  if (rc != KDA_OK) return rc;
+  if (num_seqs == 0) return KDA_OK;
+  p.final_state = final_state;
+  p.cu_seqlens = cu_seqlens;
+  p.parents = parents;
+  p.accepted = accepted;
+  p.status = static_cast<int*>(workspace);
+  p.max_q_len = max_q_len;
+  return launched(kda::tree::launch_commit(p, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 int kda_cache_accept(const kda_kv_cache* cache, const int32_t* cu_seqlens, const int32_t* parents,

@@ -14,8 +14,8 @@ from __future__ import annotations
 
 import torch
 
-from . import KDAError, OK, _elsewhere, _within, lib
-from .layer import _I32, _INT, _MASK, _cache, _check, _i32, _need_cuda, _status_workspace, _stream
+from . import ERR_INVALID_ARG, HEAD_DIM, KDAError, OK, STATE_BF16, STATE_F32, _elsewhere, _within, lib
+from .layer import _EITHER, _F32, _FLOAT, _HALF, _I32, _INT, _MASK, _cache, _check, _i32, _need_cuda, _status_workspace, _stream
 
 
 def _batch(parents, cu_seqlens, dev):
@@ -58,6 +58,118 @@ def tree_plan(parents, cu_seqlens, kv_lens, max_q_len: int, mask=None, positions
     if rc != OK:
         raise KDAError(rc, "kda_tree_plan")
     return mask, positions
+
+
+def _rows(t, name, shape, dev):
+    """Token stride of a bf16 [T, heads, 128] (or [T, heads]) tensor, tokens strided, the rest dense."""
+    return _check(t, name, _HALF, shape, dev)
+
+
+def _state(initial_state, state_dtype, n, heads, dev):
+    """Pointer, kind and dtype of the state before the tree."""
+    if initial_state is None:
+        dtype = _F32 if state_dtype is None else state_dtype
+    else:
+        dtype = initial_state.dtype if state_dtype is None else state_dtype
+        _check(initial_state, "initial_state", (dtype,), (n, heads, HEAD_DIM, HEAD_DIM), dev, 0)
+    if dtype not in _EITHER:
+        raise TypeError("state dtype must be float32 or bfloat16")
+    return (None if initial_state is None else initial_state.data_ptr(),
+            STATE_F32 if dtype is _F32 else STATE_BF16, dtype)
+
+
+def _heads(k, dev):
+    if k.dim() != 3:
+        raise ValueError("k must be [T, heads, 128]")
+    T, H, d = k.shape
+    if d != HEAD_DIM:
+        raise KDAError(ERR_INVALID_ARG, f"head_dim {d} (only {HEAD_DIM} is supported)")
+    return T, H
+
+
+def tree_recurrent_fwd(q, k, v, g, beta, A_log, dt_bias, lower_bound: float, scale: float, initial_state,
+                       cu_seqlens, parents, max_q_len: int, out=None, u=None, state_dtype=None, workspace=None,
+                       stream=None):
+    """Run ``kda_tree_recurrent_fwd``: the KDA recurrence along the branches of drafted trees.
+
+    q, k, v, g: bf16 [T, heads, 128] and beta: bf16 [T, heads] (tokens may be strided, e.g. column ranges of
+    one fused projection); A_log, dt_bias, initial_state and cu_seqlens as in ``recurrent_fwd``; parents:
+    int32 [T]; max_q_len: an upper bound of one sequence's nodes, at most 64.  The state is read
+    only.  Returns (out, u): bf16 [T, heads, 128], and fp32 [T, heads, 128] for ``tree_commit``.
+    """
+    dev = _need_cuda(k, "k")
+    place = _elsewhere(stream, k)
+    if place is not None:
+        return _within(place, tree_recurrent_fwd, (out, u), q, k, v, g, beta, A_log, dt_bias, lower_bound, scale,
+                       initial_state, cu_seqlens, parents, max_q_len, out, u, state_dtype, workspace)
+    T, H = _heads(k, dev)
+    shape = k.shape
+    nodes, N = _batch(parents, cu_seqlens, dev)
+    if nodes != T:
+        raise ValueError(f"parents has {nodes} entries, k {T} tokens")
+    strides = [_rows(t, name, shape, dev) for t, name in ((q, "q"), (k, "k"), (v, "v"), (g, "g"))]
+    beta_row = _rows(beta, "beta", (T, H), dev)
+    _check(A_log, "A_log", _FLOAT, (H,), dev, 0)
+    _check(dt_bias, "dt_bias", _FLOAT, (H, HEAD_DIM), dev, 0)
+    state, kind, _ = _state(initial_state, state_dtype, N, H, dev)
+    if out is None:
+        out = torch.empty(shape, dtype=k.dtype, device=k.device)
+    else:
+        _check(out, "out", _HALF, shape, dev, 0)
+    if u is None:
+        u = torch.empty(shape, dtype=_F32, device=k.device)
+    else:
+        _check(u, "u", _FLOAT, shape, dev, 0)
+    workspace = _status_workspace(workspace, dev)
+    rc = lib().kda_tree_recurrent_fwd(
+        q.data_ptr(), strides[0], k.data_ptr(), strides[1], v.data_ptr(), strides[2], g.data_ptr(), strides[3],
+        beta.data_ptr(), beta_row, A_log.data_ptr(), dt_bias.data_ptr(), lower_bound, scale, state, kind,
+        cu_seqlens.data_ptr(), parents.data_ptr(), out.data_ptr(), u.data_ptr(), workspace.data_ptr(),
+        _stream(stream, dev), T, N, H, _i32(max_q_len, "max_q_len"), workspace.numel())
+    if rc != OK:
+        raise KDAError(rc, "kda_tree_recurrent_fwd")
+    return out, u
+
+
+def tree_commit(k, g, A_log, dt_bias, lower_bound: float, initial_state, cu_seqlens, parents, u, accepted,
+                max_q_len: int, final_state=None, state_dtype=None, workspace=None, stream=None):
+    """Run ``kda_tree_commit``: the state after each tree's accepted branch.
+
+    k, g, A_log, dt_bias, lower_bound, initial_state, cu_seqlens, parents and max_q_len as given to
+    ``tree_recurrent_fwd``, u as it returned it; accepted: int32 [num_seqs], the last accepted node of
+    each sequence (-1: none, its state stays).  final_state may be initial_state (the update is then
+    in place).  Returns final_state.
+    """
+    dev = _need_cuda(k, "k")
+    place = _elsewhere(stream, k)
+    if place is not None:
+        return _within(place, tree_commit, (final_state,), k, g, A_log, dt_bias, lower_bound, initial_state,
+                       cu_seqlens, parents, u, accepted, max_q_len, final_state, state_dtype, workspace)
+    T, H = _heads(k, dev)
+    nodes, N = _batch(parents, cu_seqlens, dev)
+    if nodes != T:
+        raise ValueError(f"parents has {nodes} entries, k {T} tokens")
+    k_row, g_row = _rows(k, "k", k.shape, dev), _rows(g, "g", k.shape, dev)
+    _check(A_log, "A_log", _FLOAT, (H,), dev, 0)
+    _check(dt_bias, "dt_bias", _FLOAT, (H, HEAD_DIM), dev, 0)
+    _check(u, "u", _FLOAT, k.shape, dev, 0)
+    _check(accepted, "accepted", _INT, (N,), dev, 0)
+    if initial_state is None and state_dtype is None and final_state is not None:
+        state_dtype = final_state.dtype
+    state, kind, dtype = _state(initial_state, state_dtype, N, H, dev)
+    if final_state is None:
+        final_state = torch.empty((N, H, HEAD_DIM, HEAD_DIM), dtype=dtype, device=k.device)
+    else:
+        _check(final_state, "final_state", (dtype,), (N, H, HEAD_DIM, HEAD_DIM), dev, 0)
+    workspace = _status_workspace(workspace, dev)
+    rc = lib().kda_tree_commit(
+        k.data_ptr(), k_row, g.data_ptr(), g_row, A_log.data_ptr(), dt_bias.data_ptr(), lower_bound, state,
+        final_state.data_ptr(), kind, cu_seqlens.data_ptr(), parents.data_ptr(), u.data_ptr(),
+        accepted.data_ptr(), workspace.data_ptr(), _stream(stream, dev), T, N, H, _i32(max_q_len, "max_q_len"),
+        workspace.numel())
+    if rc != OK:
+        raise KDAError(rc, "kda_tree_commit")
+    return final_state
 
 
 def cache_accept(k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, cu_seqlens, parents, accepted,

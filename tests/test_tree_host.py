@@ -108,3 +108,39 @@ def test_copy_refuses(L, over, code):
     a = dict(c=ctypes.byref(cache()), fro=A, to=A, num=2, ws=A, wsb=256, stream=None)
     a.update(over)
     assert L.kda_pages_copy(*a.values()) == code
+
+
+def recur(L, **over):
+    a = dict(q=A, qs=512, k=A, ks=512, v=A, vs=512, g=A, gs=512, beta=A, bs=4, A_log=A, dt=A, lb=-5.0, scale=0.1, s0=A,
+             sd=0, cu=A, parents=A, out=A, u=A, ws=A, stream=None, T=4, N=1, H=4, most=4, wsb=256)
+    a.update(over)
+    return L.kda_tree_recurrent_fwd(*a.values())
+
+
+def commit(L, **over):
+    a = dict(k=A, ks=512, g=A, gs=512, A_log=A, dt=A, lb=-5.0, s0=A, s1=A, sd=0, cu=A, parents=A, u=A, node=A, ws=A,
+             stream=None, T=4, N=1, H=4, most=4, wsb=256)
+    a.update(over)
+    return L.kda_tree_commit(*a.values())
+
+
+@pytest.mark.parametrize("call", [recur, commit])
+@pytest.mark.parametrize("over,code", [
+    (dict(T=-1), INVALID), (dict(N=-1), INVALID), (dict(H=0), INVALID), (dict(N=2 ** 20, H=2 ** 12, ks=2 ** 19, gs=2 ** 19), INVALID),
+    (dict(most=65), INVALID), (dict(most=0), INVALID), (dict(sd=2), INVALID), (dict(k=None), INVALID), (dict(g=None), INVALID),
+    (dict(A_log=None), INVALID), (dict(dt=None), INVALID), (dict(u=None), INVALID), (dict(parents=None), INVALID),
+    (dict(ks=500), INVALID), (dict(gs=511), INVALID), (dict(lb=-5.1), kda.ERR_UNSAFE_LOWER_BOUND),
+    (dict(lb=0.1), kda.ERR_UNSAFE_LOWER_BOUND), (dict(lb=float("nan")), kda.ERR_UNSAFE_LOWER_BOUND),
+    (dict(ks=516), MISALIGNED), (dict(k=A + 8), MISALIGNED), (dict(dt=A + 4), MISALIGNED), (dict(s0=A + 8), MISALIGNED),
+    (dict(u=A + 4), MISALIGNED), (dict(wsb=255), kda.ERR_WORKSPACE_TOO_SMALL)])
+def test_recurrence_refuses(L, call, over, code):
+    assert call(L, **over) == code
+
+
+@pytest.mark.parametrize("call,over,code", [
+    (recur, dict(q=None), INVALID), (recur, dict(v=None), INVALID), (recur, dict(beta=None), INVALID), (recur, dict(bs=3), INVALID),
+    (recur, dict(out=None), INVALID), (recur, dict(scale=float("inf")), INVALID), (recur, dict(beta=A + 1), MISALIGNED),
+    (recur, dict(out=A + 2), MISALIGNED), (commit, dict(s1=None), INVALID), (commit, dict(node=None), INVALID),
+    (commit, dict(s1=A + 8), MISALIGNED), (commit, dict(node=A + 1), MISALIGNED)])
+def test_recurrence_and_commit_refuse(L, call, over, code):
+    assert call(L, **over) == code

@@ -143,3 +143,31 @@ class Pool:
                 fro[i], to[i] = self.table[s][whole], self.take()
                 self.table[d][whole] = to[i]
         return fro, to
+
+
+def recurrence(q, k, v, g, beta, A_log, dt_bias, lower_bound, scale, state, parents):
+    """One sequence's nodes [n, heads, 128] (beta [n, heads]) from state [heads, 128, 128], all float64.
+    Returns out, u, the state after each node, and magnitudes of the last three: the same sums over
+    absolute values, which bound every term that enters."""
+    n, H, _ = q.shape
+    unit = lambda x: x / torch.sqrt((x * x).sum(-1, keepdim=True) + 1e-6)  # noqa: E731
+    qh, kh = unit(q) * scale, unit(k)
+    a = torch.exp(lower_bound / (1 + torch.exp(-A_log.exp()[:, None] * (g + dt_bias))))
+    b = 1 / (1 + torch.exp(-beta))
+    out, us, after = [], [], []
+    big_out, big_u, big_after = [], [], []
+    for i in range(n):
+        p = parents[i]
+        s = (after[p] if p >= 0 else state) * a[i][:, :, None]
+        u = b[i][:, None] * (v[i] - torch.einsum("hkv,hk->hv", s, kh[i]))
+        s = s + kh[i][:, :, None] * u[:, None]
+        m = (big_after[p] if p >= 0 else state.abs()) * a[i][:, :, None]
+        mu = b[i][:, None] * (v[i].abs() + torch.einsum("hkv,hk->hv", m, kh[i].abs()))
+        m = m + kh[i].abs()[:, :, None] * mu[:, None]
+        out.append(torch.einsum("hkv,hk->hv", s, qh[i]))
+        big_out.append(torch.einsum("hkv,hk->hv", m, qh[i].abs()))
+        us.append(u)
+        big_u.append(mu)
+        after.append(s)
+        big_after.append(m)
+    return tuple(torch.stack(x) for x in (out, us, after, big_out, big_u, big_after))
