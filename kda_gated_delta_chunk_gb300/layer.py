@@ -53,7 +53,9 @@ _native = None
 class _NoneUsual:
     """In the module's place where it was not built, or for another torch: every call is the Python
     code's."""
-    add_rms_norm = rope_append = cached_attention = staticmethod(lambda *args: None)
+    add_rms_norm = rope_append = cached_attention = tree_attention = staticmethod(lambda *args: None)
+    tree_plan = tree_recurrent_fwd = tree_commit = cache_accept = add_rms_norm
+    free_pages = reserve_pages = fork_pages = copy_pages = add_rms_norm
 
 
 def _load_native():
@@ -70,9 +72,17 @@ def _load_native():
     loader.exec_module(module)
     L = lib()
     module.entries(*(ctypes.cast(f, ctypes.c_void_p).value
-                     for f in (L.kda_add_rms_norm, L.kda_rope_append, L.kda_cached_attention)))
+                     for f in (L.kda_add_rms_norm, L.kda_rope_append, L.kda_cached_attention,
+                               L.kda_tree_attention, L.kda_tree_plan, L.kda_tree_recurrent_fwd,
+                               L.kda_tree_commit, L.kda_cache_accept, L.kda_pages_free, L.kda_pages_reserve,
+                               L.kda_pages_fork, L.kda_pages_copy)))
     _native = module
     return module
+
+
+def native():
+    """The marshalling module (or its stand-in)."""
+    return _native or _load_native()
 
 
 # kda_kv_cache of kda.h, as ``_cache`` packs it
@@ -417,6 +427,14 @@ def tree_attention(q, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, 
     (``tree_plan`` makes it).  At most 64 nodes a sequence; window is 0 or at least max_q_len.
     Returns (out, lse or None).
     """
+    if out is None and stream is None:
+        done = (_native or _load_native()).tree_attention(
+            q, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, cu_seqlens, scale, max_q_len,
+            softcap, window, lse, workspace, mask)
+        if done.__class__ is tuple:
+            return done
+        if done is not None:
+            raise KDAError(done, "kda_tree_attention")
     return _attention("kda_tree_attention", mask, q, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens,
                       cu_seqlens, scale, max_q_len, softcap, window, out, lse, workspace, stream)
 

@@ -14,7 +14,7 @@ from __future__ import annotations
 import torch
 
 from . import KDAError, OK, _elsewhere, _within, lib
-from .layer import _I32, _INT, _cache, _check, _i32, _need_cuda, _status_workspace, _stream
+from .layer import _I32, _INT, _cache, _check, _i32, _need_cuda, _status_workspace, _stream, native
 
 
 def _pool(refs, block_table, kv_lens, page_size, dev):
@@ -44,6 +44,12 @@ def free_pages(refs, block_table, kv_lens, page_size: int, rows=None, workspace=
     rows: None (every row gives back the pages beyond its kv_lens) or int32 [m] (those rows end: all
     their pages go back, their kv_lens become 0).
     """
+    if stream is None:
+        done = native().free_pages(refs, block_table, kv_lens, page_size, rows, workspace)
+        if done is True:
+            return
+        if done is not None:
+            raise KDAError(done, "kda_pages_free")
     dev = _need_cuda(refs, "refs")
     place = _elsewhere(stream, refs)
     if place is not None:
@@ -61,6 +67,12 @@ def free_pages(refs, block_table, kv_lens, page_size: int, rows=None, workspace=
 
 def reserve_pages(refs, block_table, kv_lens, new_tokens, page_size: int, workspace=None, stream=None):
     """Run ``kda_pages_reserve``: pages for new_tokens (int32 [rows]) more tokens of each row."""
+    if stream is None:
+        done = native().reserve_pages(refs, block_table, kv_lens, new_tokens, page_size, workspace)
+        if done is True:
+            return
+        if done is not None:
+            raise KDAError(done, "kda_pages_reserve")
     dev = _need_cuda(refs, "refs")
     place = _elsewhere(stream, refs)
     if place is not None:
@@ -82,6 +94,12 @@ def fork_pages(refs, block_table, kv_lens, src, dst, page_size: int, from_pages=
     cache: a partly filled last page and the one to copy it to, -1 where there is none.  The rows of dst
     hold no pages before (``free_pages``), and none is a source.
     """
+    if from_pages is None and to_pages is None and stream is None:
+        done = native().fork_pages(refs, block_table, kv_lens, src, dst, page_size, workspace)
+        if done.__class__ is tuple:
+            return done
+        if done is not None:
+            raise KDAError(done, "kda_pages_fork")
     dev = _need_cuda(refs, "refs")
     place = _elsewhere(stream, refs)
     if place is not None:
@@ -110,6 +128,12 @@ def fork_pages(refs, block_table, kv_lens, src, dst, page_size: int, from_pages=
 def copy_pages(k_cache, v_cache, k_scale, v_scale, from_pages, to_pages, workspace=None, stream=None):
     """Run ``kda_pages_copy``: pages from_pages to pages to_pages (int32 [m]) of one layer's cache, with
     their scales; pairs with a negative page are left out."""
+    if stream is None:
+        done = native().copy_pages(k_cache, v_cache, k_scale, v_scale, from_pages, to_pages, workspace)
+        if done is True:
+            return
+        if done is not None:
+            raise KDAError(done, "kda_pages_copy")
     dev = _need_cuda(k_cache, "k_cache")
     place = _elsewhere(stream, k_cache)
     if place is not None:

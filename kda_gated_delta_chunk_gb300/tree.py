@@ -15,7 +15,7 @@ from __future__ import annotations
 import torch
 
 from . import ERR_INVALID_ARG, HEAD_DIM, KDAError, OK, STATE_BF16, STATE_F32, _elsewhere, _within, lib
-from .layer import _EITHER, _F32, _FLOAT, _HALF, _I32, _INT, _MASK, _cache, _check, _i32, _need_cuda, _status_workspace, _stream
+from .layer import _EITHER, _F32, _FLOAT, _HALF, _I32, _INT, _MASK, _cache, _check, _i32, _need_cuda, _status_workspace, _stream, native
 
 
 def _batch(parents, cu_seqlens, dev):
@@ -36,6 +36,12 @@ def tree_plan(parents, cu_seqlens, kv_lens, max_q_len: int, mask=None, positions
     included; max_q_len: an upper bound of one sequence's nodes, at most 64.  Returns (mask, positions):
     int64 [T] for ``tree_attention`` and int32 [T] for ``rope_append``.
     """
+    if mask is None and positions is None and stream is None:
+        done = native().tree_plan(parents, cu_seqlens, kv_lens, max_q_len, workspace)
+        if done.__class__ is tuple:
+            return done
+        if done is not None:
+            raise KDAError(done, "kda_tree_plan")
     dev = _need_cuda(parents, "parents")
     place = _elsewhere(stream, parents)
     if place is not None:
@@ -97,6 +103,13 @@ def tree_recurrent_fwd(q, k, v, g, beta, A_log, dt_bias, lower_bound: float, sca
     int32 [T]; max_q_len: an upper bound of one sequence's nodes, at most 64.  The state is read
     only.  Returns (out, u): bf16 [T, heads, 128], and fp32 [T, heads, 128] for ``tree_commit``.
     """
+    if out is None and u is None and state_dtype is None and stream is None:
+        done = native().tree_recurrent_fwd(q, k, v, g, beta, A_log, dt_bias, lower_bound, scale, initial_state,
+                                           cu_seqlens, parents, max_q_len, workspace)
+        if done.__class__ is tuple:
+            return done
+        if done is not None:
+            raise KDAError(done, "kda_tree_recurrent_fwd")
     dev = _need_cuda(k, "k")
     place = _elsewhere(stream, k)
     if place is not None:
@@ -140,6 +153,13 @@ def tree_commit(k, g, A_log, dt_bias, lower_bound: float, initial_state, cu_seql
     each sequence (-1: none, its state stays).  final_state may be initial_state (the update is then
     in place).  Returns final_state.
     """
+    if state_dtype is None and stream is None:
+        done = native().tree_commit(k, g, A_log, dt_bias, lower_bound, initial_state, cu_seqlens, parents, u,
+                                    accepted, max_q_len, final_state, workspace)
+        if done.__class__ is int:
+            raise KDAError(done, "kda_tree_commit")
+        if done is not None:
+            return done
     dev = _need_cuda(k, "k")
     place = _elsewhere(stream, k)
     if place is not None:
@@ -180,6 +200,13 @@ def cache_accept(k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, cu_se
     node of each sequence (-1: none).  The cache is updated in place.  Returns lens_out, int32
     [num_seqs]: the cached tokens from there on (a tensor of its own: every layer's call reads kv_lens).
     """
+    if lens_out is None and stream is None:
+        done = native().cache_accept(k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, cu_seqlens,
+                                     parents, accepted, max_q_len, workspace)
+        if done.__class__ is int:
+            raise KDAError(done, "kda_cache_accept")
+        if done is not None:
+            return done
     dev = _need_cuda(k_cache, "k_cache")
     place = _elsewhere(stream, k_cache)
     if place is not None:
