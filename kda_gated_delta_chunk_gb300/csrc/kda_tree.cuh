@@ -95,11 +95,5 @@ struct RecurParams {
 cudaError_t launch_recur(const RecurParams& p, cudaStream_t stream);
 cudaError_t launch_commit(const RecurParams& p, cudaStream_t stream);
 
-// Decay of a channel: exp(lower_bound sigmoid(exp(A_log) (g + dt_bias))), with exp and division to fp32's
-// precision: the states it multiplies are held in fp32.
-__device__ __forceinline__ float decay_of(float g, float dt, float gsc, float lower_bound) {
-  return expf(lower_bound / (1.0f + expf(-gsc * (g + dt))));
-}
-
 }  // namespace tree
 }  // namespace kda

@@ -6,62 +6,80 @@
 // which is the gated delta rule with every node's state written out from S0.  So the state is read once and
 // none is written (a state a node would be 64 KB each); kda_tree_commit makes the accepted one of the u.
 //
-// S0^T times the 2 n vectors is one tcgen05 product: M = 128 value channels (S0 as it lies in memory is the
-// MN-major operand), N = 2 n, K = 128 key channels, f16 with fp32 sums.  fp32 values enter as two f16
-// terms, hi hi + hi lo + lo hi: 22 bits.  f16's range is met by powers of two: one a key channel, which
-// goes from S0's row to the vectors, one a vector, taken out of its sums.  (A state in bf16 is exact in one term.)
-// The rest is fp32: a node's walk up its branch carries kh and qh times the decays met, 8 lanes a node
-// and 16 channels a lane, one pair of products an ancestor, and ends as c_i kh_i and c_i qh_i; then a thread a
-// value channel takes the nodes in order, its own u in shared memory (no barriers).
+// S0^T times the 2 n vectors is one tcgen05 product: M = 128 value channels, N = 2 n, K = 128 key channels, f16
+// with fp32 sums.  fp32 values enter as two f16 terms, hi hi + hi lo + lo hi: 22 bits.  f16's range is met
+// by powers of two, one a value channel of S0 and one a vector, taken out of the sums again.  (A state in
+// bf16 is exact in one term.)  S0 goes from registers to tensor memory, a thread half a column of it: that
+// operand needs no shared memory and no transposition.  The rest is fp32:
+//  - a node's walk up its branch carries kh and qh times the decays met, 8 lanes a node and 16 channels a
+//    lane, one pair of products an ancestor, and ends as c_i kh_i and c_i qh_i;
+//  - then the nodes in blocks of 8, a thread a value channel: four warps make u, the other four follow a block
+//    behind with o.  Sums over earlier blocks have no chain but their own length, and blocks without a pair
+//    of node and ancestor are left out.
 #include <cuda_fp16.h>
 
-#include "kda_tree.cuh"
+#include "kda_attn_tc.cuh"
 #include "kda_tc_common.cuh"
+#include "kda_tree.cuh"
 
 namespace kda {
 namespace tree {
 namespace {
 
 using namespace sm100;
+using attn::kLog2e;
+using tcc::unpack_bf16x2;
 
 constexpr int kThreads = 256;
+constexpr int kBlock = 8;          // nodes of a block
 
-// Instruction descriptor of kind::f16 with f16 operands, fp32 sums.
-constexpr uint32_t idesc_half(int M, int N, int a_mn, int b_mn) {
-  return (1u << 4) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16) | ((uint32_t)(N >> 3) << 17) |
-         ((uint32_t)(M >> 4) << 24);
-}
-
-template <int NT>      // nodes at most
+template <int NT, bool kBf16>      // nodes at most; the state's type
 struct Cfg {
   static constexpr int kRows = 2 * NT;
-  static constexpr int kA = 32768, kB = kRows * 256;              // one term
-  static constexpr int kOffB = 2 * kA;
-  static constexpr int kOffDecay = kOffB + 2 * kB;                // float [NT][128], see decay_at
-  static constexpr int kOffK = kOffDecay + NT * 512;              // bf16 [NT][128]
-  static constexpr int kOffV = kOffK + NT * 256;                  // bf16 [NT][128]
-  static constexpr int kPairs = NT * (NT + 1) / 2;
-  static constexpr int kOffKQ = kOffV + NT * 256;                 // float2 [kPairs]: node i's ancestors, itself first
-  static constexpr int kOffAnc = kOffKQ + kPairs * 8;             // uint8 [kPairs]
-  static constexpr int kOffEk = (kOffAnc + kPairs + 15) / 16 * 16;   // float [128]
-  static constexpr int kOffMul = kOffEk + 512;                    // float [kRows]
-  static constexpr int kOffIk = kOffMul + kRows * 4;              // float [NT]
-  static constexpr int kOffBeta = kOffIk + NT * 4;                // float [NT]
+  static constexpr int kB = kRows * 256;                          // one term of the vectors
+  static constexpr int kBlocks = NT / kBlock, kPairs = kBlocks * (kBlocks + 1) / 2;
+  // keys [NT][128] and decays [NT][128] (fp32), then over them the vectors' two terms, then u [NT][128]
+  static constexpr int kOffDecay = NT * 512;
+  static constexpr int kOffV = NT * 1024;                         // bf16 [NT][128]
+  static constexpr int kOffKK = kOffV + NT * 256;                 // K: blocks (b, pb <= b) of [8 j][8 i]
+  static constexpr int kOffQQ = kOffKK + kPairs * 256;
+  static constexpr int kOffMax = kOffQQ + kPairs * 256;           // uint [2][128]
+  static constexpr int kOffMul = kOffMax + 1024;                  // float [kRows]
+  static constexpr int kOffBeta = kOffMul + kRows * 4;            // float [NT]
   static constexpr int kOffLink = kOffBeta + NT * 4;              // int [NT]
-  static constexpr int kOffDepth = kOffLink + NT * 4;             // int [NT]: ancestors, itself included
-  static constexpr int kOffBar = kOffDepth + NT * 4;
+  static constexpr int kOffFlag = kOffLink + NT * 4;              // int [kPairs]: the block has a pair
+  static constexpr int kOffAnc = (kOffFlag + kPairs * 4 + 15) / 16 * 16;   // uint64 [NT]: a node's branch
+  static constexpr int kOffBar = kOffAnc + NT * 8;
   static constexpr int kBytes = kOffBar + 16 + 1024;
-  static constexpr uint32_t kTmem = kRows <= 32 ? 32 : kRows;
-  static_assert(NT * 512 <= 2 * kA, "u over the state's terms");
-  static_assert(kBytes <= 227 * 1024, "shared memory");
+  static constexpr uint32_t kTD = kBf16 ? 64 : 128;               // the state's terms, then the sums
+  static constexpr uint32_t kTmem = kTD + kRows <= 128 ? 128 : 256;
+  static_assert(2 * kB == NT * 1024, "the vectors over keys and decays");
+  static_assert(2 * kBytes <= 226 * 1024, "two CTAs an SM");
 };
+__device__ __forceinline__ int pair_block(int b, int pb) { return b * (b + 1) / 2 + pb; }
 
-__device__ __forceinline__ void mma_half(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+// D[tmem] (+)= A[tmem] B[smem]^T with f16 operands.
+__device__ __forceinline__ void mma_half_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
       "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(acc)
       : "memory");
+}
+// Instruction descriptor of kind::f16 with f16 operands, both K-major, fp32 sums.
+constexpr uint32_t idesc_half(int M, int N) {
+  return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+__device__ __forceinline__ void bar_arrive(uint32_t id, uint32_t count) {
+  asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(count) : "memory");
+}
+
+// 1 / (1 + e^-x), and a channel's decay exp(lower sigmoid(exp(A_log) x)), x = g + dt_bias, with gate =
+// -exp(A_log) log2(e) and lower = lower_bound log2(e).  The special functions are within 2^-22 of their
+// results and lower within 7.3, so a decay is within 2^-20 of itself.
+__device__ __forceinline__ float sigmoid_of(float x) { return attn::rcp(1.0f + attn::ex2(-kLog2e * x)); }
+__device__ __forceinline__ float decay_of(float x, float gate, float lower) {
+  return attn::ex2(lower * attn::rcp(1.0f + attn::ex2(gate * x)));
 }
 
 // 2^e as a float, -126 <= e <= 127
@@ -74,23 +92,25 @@ __device__ __forceinline__ uint32_t magnitude(float x) {
   return b < 0x7f800000u ? b : 0u;
 }
 // Two f16 terms of a pair of floats
-__device__ __forceinline__ void split(float x, float y, uint32_t& hi, uint32_t& lo) {
-  const __half2 h = __floats2half2_rn(x, y);
+__device__ __forceinline__ void split(float2 x, uint32_t& hi, uint32_t& lo) {
+  const __half2 h = __floats2half2_rn(x.x, x.y);
   const float2 b = __half22float2(h);
-  const __half2 l = __floats2half2_rn(x - b.x, y - b.y);
+  const __half2 l = __floats2half2_rn(x.x - b.x, x.y - b.y);
   hi = *reinterpret_cast<const uint32_t*>(&h);
   lo = *reinterpret_cast<const uint32_t*>(&l);
 }
-// Place of channel ch in a row of decays: a lane's eight channels are two runs of four, so that the 8 lanes of a
-// node read whole lines.
-__device__ __forceinline__ int decay_at(int ch) {
+// Place of channel ch in a row of keys or decays: a lane's eight channels are two runs of four, so that the
+// 8 lanes of a node read whole lines.
+__device__ __forceinline__ int place(int ch) {
   return (ch & 64) + ((ch & 4) << 3) + ((ch & 63) >> 3) * 4 + (ch & 3);
 }
 
 template <int NT, bool kBf16>
-__global__ void __launch_bounds__(kThreads, NT <= 16 ? 2 : 1)
+__global__ void __launch_bounds__(kThreads, 2)
     kda_tree_recur_kernel(const __grid_constant__ RecurParams p) {
-  using C = Cfg<NT>;
+  using C = Cfg<NT, kBf16>;
+  using attn::fma2;
+  using attn::mul2;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const uint32_t sb = smem_u32(sm);
@@ -98,7 +118,6 @@ __global__ void __launch_bounds__(kThreads, NT <= 16 ? 2 : 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int h = blockIdx.x % p.heads, seq = blockIdx.x / p.heads;
   pdl_wait();
-  pdl_launch_dependents();
   Nodes s;
   int err;
   if (!nodes_of(p.cu_seqlens, seq, p.total_tokens, p.max_q_len, &s, &err) || s.n == 0) {
@@ -107,22 +126,47 @@ __global__ void __launch_bounds__(kThreads, NT <= 16 ? 2 : 1)
   }
   const int64_t hoff = (int64_t)h * kHeadDim;
 
-  // ---- the state's rows on their way: 16 a warp, 4 channels a lane
-  float4 st[16];
-  {
-    const int64_t at = ((int64_t)seq * p.heads + h) * (kHeadDim * kHeadDim) + 16 * warp * kHeadDim + 4 * lane;
+  // ---- loads on their way: the nodes' (a warp a node, 4 channels a lane; kAhead nodes a warp at a time),
+  // then the state, a thread half a column of it (64 of its 128 key channels)
+  constexpr int kPer = NT / 8, kAhead = kPer < 4 ? kPer : 4;
+  uint2 kw[kAhead], vw[kAhead], gw[kAhead];
+  auto load_nodes = [&](int m0) {
 #pragma unroll
-    for (int r = 0; r < 16; ++r) {
-      st[r] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (!p.initial_state) continue;
-      if (kBf16) {
-        const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p.initial_state) + at +
-                                                        r * kHeadDim);
-        const float2 a = tcc::unpack_bf16x2(w.x), b = tcc::unpack_bf16x2(w.y);
-        st[r] = make_float4(a.x, a.y, b.x, b.y);
-      } else {
-        st[r] = *reinterpret_cast<const float4*>(static_cast<const float*>(p.initial_state) + at + r * kHeadDim);
+    for (int m = 0; m < kAhead; ++m) {
+      const int i = warp + 8 * (m0 + m);
+      kw[m] = vw[m] = gw[m] = make_uint2(0, 0);
+      if (i < s.n) {
+        const int64_t t = s.tok0 + i, at = hoff + 4 * lane;
+        kw[m] = *reinterpret_cast<const uint2*>(p.k + t * p.s_k + at);
+        gw[m] = *reinterpret_cast<const uint2*>(p.g + t * p.s_g + at);
+        vw[m] = *reinterpret_cast<const uint2*>(p.v + t * p.s_v + at);
       }
+    }
+  };
+  load_nodes(0);
+  float beta_in = 0.0f;
+  int link_in = -1;
+  if (tid < s.n) {
+    beta_in = __bfloat162float(p.beta[(s.tok0 + tid) * p.s_beta + h]);
+    link_in = parent_of(p.parents, s, tid, p.status, h == 0);
+  }
+  const float4 dt = *reinterpret_cast<const float4*>(p.dt_bias + hoff + 4 * lane);
+  const float gate = -kLog2e * expf(p.A_log[h]), lower = p.lower_bound * kLog2e;
+  const int col = tid & 127, part = tid >> 7;
+  float st[64];
+  {
+    const int64_t at = ((int64_t)seq * p.heads + h) * (kHeadDim * kHeadDim) + part * (64 * kHeadDim) + col;
+    if (!p.initial_state) {
+#pragma unroll
+      for (int r = 0; r < 64; ++r) st[r] = 0.0f;
+    } else if (kBf16) {
+      const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.initial_state) + at;
+#pragma unroll
+      for (int r = 0; r < 64; ++r) st[r] = __bfloat162float(src[r * kHeadDim]);
+    } else {
+      const float* src = static_cast<const float*>(p.initial_state) + at;
+#pragma unroll
+      for (int r = 0; r < 64; ++r) st[r] = src[r * kHeadDim];
     }
   }
   if (warp == 0) {
@@ -133,204 +177,210 @@ __global__ void __launch_bounds__(kThreads, NT <= 16 ? 2 : 1)
     mbar_init(sb + C::kOffBar, 1);
     mbar_fence_init();
   }
+  float* keys = reinterpret_cast<float*>(sm);
   float* decay = reinterpret_cast<float*>(sm + C::kOffDecay);
-  float* ek = reinterpret_cast<float*>(sm + C::kOffEk);
+  float* kk = reinterpret_cast<float*>(sm + C::kOffKK);
+  float* qq = reinterpret_cast<float*>(sm + C::kOffQQ);
+  float* maxs = reinterpret_cast<float*>(sm + C::kOffMax);
   float* mul = reinterpret_cast<float*>(sm + C::kOffMul);
-  float* ik = reinterpret_cast<float*>(sm + C::kOffIk);
   float* beta = reinterpret_cast<float*>(sm + C::kOffBeta);
   int* link = reinterpret_cast<int*>(sm + C::kOffLink);
-  int* depth = reinterpret_cast<int*>(sm + C::kOffDepth);
-  float2* kq = reinterpret_cast<float2*>(sm + C::kOffKQ);
-  uint8_t* anc = sm + C::kOffAnc;
-  const float gsc = expf(p.A_log[h]);
+  int* flag = reinterpret_cast<int*>(sm + C::kOffFlag);
+  uint64_t* anc = reinterpret_cast<uint64_t*>(sm + C::kOffAnc);
+  int* bad_s = reinterpret_cast<int*>(sm + C::kOffMax);      // (over the maxima)
 
-  // ---- the nodes' keys, values, decays: a warp a node, 4 channels a lane
-  {
-    const float4 dt = *reinterpret_cast<const float4*>(p.dt_bias + hoff + 4 * lane);
-    for (int i = warp; i < s.n; i += kThreads / 32) {
-      const int64_t t = s.tok0 + i;
-      const uint2 kw = *reinterpret_cast<const uint2*>(p.k + t * p.s_k + hoff + 4 * lane);
-      const uint2 vw = *reinterpret_cast<const uint2*>(p.v + t * p.s_v + hoff + 4 * lane);
-      const uint2 gw = *reinterpret_cast<const uint2*>(p.g + t * p.s_g + hoff + 4 * lane);
-      const float2 k0 = tcc::unpack_bf16x2(kw.x), k1 = tcc::unpack_bf16x2(kw.y);
-      const float2 g0 = tcc::unpack_bf16x2(gw.x), g1 = tcc::unpack_bf16x2(gw.y);
-      float sum = k0.x * k0.x + k0.y * k0.y + k1.x * k1.x + k1.y * k1.y;
+  if (tid < NT) {      // (past the nodes: zeros)
+    beta[tid] = tid < s.n ? sigmoid_of(beta_in) : 0.0f;
+    link[tid] = link_in;
+    anc[tid] = 0;
+  }
+  for (int i = tid; i < C::kPairs * 32; i += kThreads)      // (K and Q, 512 bytes a block)
+    reinterpret_cast<float4*>(kk)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (tid < C::kPairs) flag[tid] = 0;
+  // ---- the nodes' keys, values, decays
+#pragma unroll
+  for (int m0 = 0; m0 < kPer; m0 += kAhead) {
+    if (m0 > 0) load_nodes(m0);
+#pragma unroll
+    for (int m = 0; m < kAhead; ++m) {
+      const int i = warp + 8 * (m0 + m);
+      const float2 k0 = unpack_bf16x2(kw[m].x), k1 = unpack_bf16x2(kw[m].y);
+      const float2 g0 = unpack_bf16x2(gw[m].x), g1 = unpack_bf16x2(gw[m].y);
+      float sum = fmaf(k0.x, k0.x, k0.y * k0.y) + fmaf(k1.x, k1.x, k1.y * k1.y);
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      *reinterpret_cast<uint2*>(sm + C::kOffK + i * 256 + 8 * lane) = kw;
-      *reinterpret_cast<uint2*>(sm + C::kOffV + i * 256 + 8 * lane) = vw;
-      *reinterpret_cast<float4*>(decay + i * 128 + decay_at(4 * lane)) =
-          make_float4(decay_of(g0.x, dt.x, gsc, p.lower_bound), decay_of(g0.y, dt.y, gsc, p.lower_bound),
-                      decay_of(g1.x, dt.z, gsc, p.lower_bound), decay_of(g1.y, dt.w, gsc, p.lower_bound));
-      if (lane == 0) {
-        ik[i] = rsqrtf(sum + kL2Eps);
-        beta[i] = 1.0f / (1.0f + expf(-__bfloat162float(p.beta[t * p.s_beta + h])));
-        link[i] = parent_of(p.parents, s, i, p.status, h == 0);
-      }
+      const float ik = rsqrtf(sum + kL2Eps);
+      *reinterpret_cast<float4*>(keys + i * 128 + place(4 * lane)) =
+          make_float4(k0.x * ik, k0.y * ik, k1.x * ik, k1.y * ik);
+      *reinterpret_cast<float4*>(decay + i * 128 + place(4 * lane)) =
+          make_float4(decay_of(g0.x + dt.x, gate, lower), decay_of(g0.y + dt.y, gate, lower),
+                      decay_of(g1.x + dt.z, gate, lower), decay_of(g1.y + dt.w, gate, lower));
+      *reinterpret_cast<uint2*>(sm + C::kOffV + i * 256 + 8 * lane) = vw[m];
     }
   }
-  // ---- the state as two f16 terms, a power of two a row
+  // the queries of this lane's nodes in the walks: 8 lanes a node, channels 8 sub .. and 64 + 8 sub ..
+  constexpr int kPasses = (NT + kThreads / 8 - 1) / (kThreads / 8);
+  const int sub = lane & 7, node0 = 4 * warp + (lane >> 3);
+  uint4 qw[kPasses][2];
 #pragma unroll
-  for (int r = 0; r < 16; ++r) {
-    const int k = 16 * warp + r;
-    const float4 x = st[r];
-    const uint32_t top = __reduce_max_sync(
-        0xffffffffu, max(max(magnitude(x.x), magnitude(x.y)), max(magnitude(x.z), magnitude(x.w))));
-    const int e = to_half_range(top);
-    const float f = pow2(-e);
-    uint2 hi, lo;
-    split(x.x * f, x.y * f, hi.x, lo.x);
-    split(x.z * f, x.w * f, hi.y, lo.y);
-    const uint32_t off = mnmajor_off(4 * lane, k, 16384);
-    *reinterpret_cast<uint2*>(sm + off) = hi;
-    if (!kBf16) *reinterpret_cast<uint2*>(sm + C::kA + off) = lo;
-    if (lane == 0) ek[k] = pow2(e);
-  }
-  __syncthreads();
-  const uint32_t tmem = tmem_s;
-
-  // ---- walks: 8 lanes a node, channels 8 s .. 8 s + 7 and 64 + 8 s .. a lane
+  for (int pass = 0; pass < kPasses; ++pass)
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      qw[pass][c] = make_uint4(0, 0, 0, 0);
+      if (32 * pass + node0 < s.n)
+        qw[pass][c] = *reinterpret_cast<const uint4*>(p.q + (int64_t)(s.tok0 + 32 * pass + node0) * p.s_q + hoff +
+                                                      64 * c + 8 * sub);
+    }
   {
-    const int sub = lane & 7;
-    auto load_decay = [&](int j, float (&a)[16]) {
+    float top = 0.0f;
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const float4 x = *reinterpret_cast<const float4*>(decay + j * 128 + (c >> 1) * 64 + (c & 1) * 32 + 4 * sub);
-        a[4 * c] = x.x;
-        a[4 * c + 1] = x.y;
-        a[4 * c + 2] = x.z;
-        a[4 * c + 3] = x.w;
-      }
-    };
-    auto load_k = [&](int j, float (&x)[16]) {
+    for (int r = 0; r < 64; r += 2) top = attn::max3_abs(top, st[r], st[r + 1]);
+    if (top > 3.402823466e38f) {     // (infinities: the largest of the others)
+      top = 0.0f;
+#pragma unroll
+      for (int r = 0; r < 64; ++r) top = fmaxf(top, __uint_as_float(magnitude(st[r])));
+    }
+    maxs[tid] = top;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  // (not before this CTA has its tensor memory: a dependent might take it, and wait for this grid's end)
+  pdl_launch_dependents();
+  const uint32_t tmem = tmem_s;
+  const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+
+  // ---- the state as f16 terms, a power of two a column: channels 2 c, 2 c + 1 in column c
+  const int fe = to_half_range(__float_as_uint(fmaxf(maxs[col], maxs[128 + col])));
+  const float unscale = pow2(fe);
+  {
+    const float f = pow2(-fe);
+    uint32_t hi[32], lo[32];
+#pragma unroll
+    for (int c = 0; c < 32; ++c) split(mul2(make_float2(st[2 * c], st[2 * c + 1]), make_float2(f, f)), hi[c], lo[c]);
+    tmem_st32(tmem + lanes + 32 * part, hi);
+    if (!kBf16) tmem_st32(tmem + lanes + 64 + 32 * part, lo);
+  }
+
+  // ---- walks
+  float2 wk[kPasses][8], wq[kPasses][8];
+  auto load_row = [&](const float* row, float2 (&x)[8]) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const float4 y = *reinterpret_cast<const float4*>(row + (c >> 1) * 64 + (c & 1) * 32 + 4 * sub);
+      x[2 * c] = make_float2(y.x, y.y);
+      x[2 * c + 1] = make_float2(y.z, y.w);
+    }
+  };
+#pragma unroll
+  for (int pass = 0; pass < kPasses; ++pass) {
+    const int i = 32 * pass + node0;
+    const bool live = i < s.n;
+    if (!__any_sync(0xffffffffu, live)) break;
+    {
+      float2 sum = make_float2(0.0f, 0.0f);
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        float y[8];
-        attn::unpack8(*reinterpret_cast<const uint4*>(sm + C::kOffK + j * 256 + c * 128 + 16 * sub), y);
+        const uint32_t x[4] = {qw[pass][c].x, qw[pass][c].y, qw[pass][c].z, qw[pass][c].w};
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[8 * c + e] = y[e];
-      }
-    };
-    for (int i0 = 4 * warp; i0 < NT; i0 += kThreads / 8) {
-      const int i = i0 + (lane >> 3);
-      const bool live = i < s.n;
-      if (!__any_sync(0xffffffffu, live)) break;
-      float wk[16], wq[16], x[16];
-      {
-        float sum = 0.0f;
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint4 w = make_uint4(0, 0, 0, 0);
-          if (live)
-            w = *reinterpret_cast<const uint4*>(p.q + (int64_t)(s.tok0 + i) * p.s_q + hoff + 64 * c + 8 * sub);
-          float y[8];
-          attn::unpack8(w, y);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            wq[8 * c + e] = y[e];
-            sum += y[e] * y[e];
-          }
-        }
-#pragma unroll
-        for (int o = 4; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        const float iq = p.scale * rsqrtf(sum + kL2Eps);
-        const float ki = live ? ik[i] : 0.0f;
-        load_k(live ? i : 0, x);
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          wq[e] *= iq;
-          wk[e] = x[e] * ki;
+        for (int e = 0; e < 4; ++e) {
+          wq[pass][4 * c + e] = unpack_bf16x2(x[e]);
+          sum = fma2(wq[pass][4 * c + e], wq[pass][4 * c + e], sum);
         }
       }
-      int j = live ? i : -1, d = 0;
-      const int base = i * (i + 1) / 2;
-      while (__any_sync(0xffffffffu, j >= 0)) {
-        const int jj = max(j, 0);
-        load_k(jj, x);
-        float a[16];
-        load_decay(jj, a);
-        float dk = 0.0f, dq = 0.0f;
+      float all = sum.x + sum.y;
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          dk = fmaf(wk[e], x[e], dk);
-          dq = fmaf(wq[e], x[e], dq);
-        }
+      for (int o = 4; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+      const float iq = p.scale * rsqrtf(all + kL2Eps);
+      load_row(keys + (live ? i : 0) * 128, wk[pass]);
 #pragma unroll
-        for (int o = 4; o > 0; o >>= 1) {
-          dk += __shfl_xor_sync(0xffffffffu, dk, o);
-          dq += __shfl_xor_sync(0xffffffffu, dq, o);
-        }
-        if (j >= 0) {
-          if (sub == 0) {
-            kq[base + d] = make_float2(dk * ik[j], dq * ik[j]);
-            anc[base + d] = (uint8_t)j;
-          }
+      for (int e = 0; e < 8; ++e) wq[pass][e] = mul2(wq[pass][e], make_float2(iq, iq));
+    }
+    int j = live ? i : -1;
+    uint64_t branch = 0;
+    const int row0 = (i / kBlock) * (i / kBlock + 1) / 2, in_block = i % kBlock;
+    while (__any_sync(0xffffffffu, j >= 0)) {
+      const int jj = max(j, 0);
+      float2 x[8], a[8];
+      load_row(keys + jj * 128, x);
+      load_row(decay + jj * 128, a);
+      const int up = link[jj];
+      float2 dk = make_float2(0.f, 0.f), dq = make_float2(0.f, 0.f);
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            wk[e] *= a[e];
-            wq[e] *= a[e];
-          }
-          j = link[j];
-          ++d;
-        }
+      for (int e = 0; e < 8; ++e) {
+        dk = fma2(wk[pass][e], x[e], dk);
+        dq = fma2(wq[pass][e], x[e], dq);
       }
-      if (live && sub == 0) depth[i] = d;
-      // c_i kh_i and c_i qh_i as rows of the operand, a power of two each
-      uint32_t tk = 0, tq = 0;
-#pragma unroll
-      for (int c = 0; c < 2; ++c)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float f = ek[64 * c + 8 * sub + e];
-          wk[8 * c + e] *= f;
-          wq[8 * c + e] *= f;
-          tk = max(tk, magnitude(wk[8 * c + e]));
-          tq = max(tq, magnitude(wq[8 * c + e]));
-        }
+      float rk = dk.x + dk.y, rq = dq.x + dq.y;
 #pragma unroll
       for (int o = 4; o > 0; o >>= 1) {
-        tk = max(tk, __shfl_xor_sync(0xffffffffu, tk, o));
-        tq = max(tq, __shfl_xor_sync(0xffffffffu, tq, o));
+        rk += __shfl_xor_sync(0xffffffffu, rk, o);
+        rq += __shfl_xor_sync(0xffffffffu, rq, o);
       }
-      const int fk = to_half_range(tk), fq = to_half_range(tq);
-      const int rk = 16 * (i >> 3) + (i & 7), rq = rk + 8;
-      if (i < NT) {
-        const float mk = pow2(-fk), mq = pow2(-fq);
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t hi[4], lo[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) split(wk[8 * c + 2 * e] * mk, wk[8 * c + 2 * e + 1] * mk, hi[e], lo[e]);
-          uint32_t off = C::kOffB + kmajor_off(rk, 64 * c + 8 * sub, C::kRows);
-          *reinterpret_cast<uint4*>(sm + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          *reinterpret_cast<uint4*>(sm + off + C::kB) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) split(wq[8 * c + 2 * e] * mq, wq[8 * c + 2 * e + 1] * mq, hi[e], lo[e]);
-          off = C::kOffB + kmajor_off(rq, 64 * c + 8 * sub, C::kRows);
-          *reinterpret_cast<uint4*>(sm + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          *reinterpret_cast<uint4*>(sm + off + C::kB) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-        }
+      if (j >= 0) {
+        branch |= 1ull << j;
         if (sub == 0) {
-          mul[rk] = pow2(fk);
-          mul[rq] = pow2(fq);
+          const int blk = row0 + j / kBlock, at = blk * 64 + (j % kBlock) * 8 + in_block;
+          kk[at] = rk;          // (a node's with itself is not used)
+          qq[at] = rq;
+          flag[blk] = 1;
         }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          wk[pass][e] = mul2(wk[pass][e], a[e]);
+          wq[pass][e] = mul2(wq[pass][e], a[e]);
+        }
+        j = up;
       }
     }
+    if (live && sub == 0) anc[i] = branch;
+  }
+  tmem_wait_st();
+  __syncthreads();            // keys and decays have been read: the vectors go over them
+#pragma unroll
+  for (int pass = 0; pass < kPasses; ++pass) {
+    const int i = 32 * pass + node0;
+    if (i >= NT) break;
+    auto put = [&](float2 (&w)[8], int row, bool live) {
+      float top = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        if (!live) w[e] = make_float2(0.f, 0.f);
+        top = attn::max3_abs(top, w[e].x, w[e].y);
+      }
+#pragma unroll
+      for (int o = 4; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const int f = to_half_range(__float_as_uint(top));     // (infinite: the vector's sums are no numbers)
+      const float m = pow2(-f);
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) split(mul2(w[4 * c + e], make_float2(m, m)), hi[e], lo[e]);
+        const uint32_t off = kmajor_off(row, 64 * c + 8 * sub, C::kRows);
+        *reinterpret_cast<uint4*>(sm + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4*>(sm + C::kB + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+      }
+      if (sub == 0) mul[row] = pow2(f);
+    };
+    const int row = 2 * kBlock * (i / kBlock) + i % kBlock;       // a block's vectors of k, then of q
+    put(wk[pass], row, i < s.n);
+    put(wq[pass], row + kBlock, i < s.n);
   }
   fence_proxy_async();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
 
-  // ---- S0^T [c kh; c qh]^T: 128 value channels by 2 NT vectors (rows past the nodes are not read back)
+  // ---- S0^T [c kh; c qh]^T
   if (tid == 0) {
-    constexpr uint32_t id = idesc_half(128, C::kRows, 1, 0);
+    constexpr uint32_t id = idesc_half(128, C::kRows);
 #pragma unroll
     for (int term = 0; term < (kBf16 ? 2 : 3); ++term) {
-      const uint32_t a = sb + (term == 2 ? C::kA : 0), b = sb + C::kOffB + (term == 1 ? C::kB : 0);
+      const uint32_t a = tmem + (term == 2 ? 64 : 0), b = sb + (term == 1 ? C::kB : 0);
 #pragma unroll
       for (int ks = 0; ks < 8; ++ks)
-        mma_half(tmem, tcc::mndesc(a, 16384, ks), tcc::kdesc(b, C::kRows, ks), id, term > 0 || ks > 0);
+        mma_half_ts(tmem + C::kTD, a + 8 * ks, tcc::kdesc(b, C::kRows, ks), id, term > 0 || ks > 0);
     }
     mma_commit(sb + C::kOffBar);
   }
@@ -338,39 +388,116 @@ __global__ void __launch_bounds__(kThreads, NT <= 16 ? 2 : 1)
   ok = __syncthreads_and(ok);
   tc_fence_after();
 
-  // ---- the nodes in order, a thread a value channel (u over the state's terms: the product is done)
+  // ---- the nodes in order (u over the vectors: the product is done)
   if (!ok) {
     if (tid == 0) record_error(p.status, KDA_ERR_DEVICE_TIMEOUT, 441);
-  } else if (warp < 4) {
-    float* us = reinterpret_cast<float*>(sm) + tid;
-    const uint32_t lanes = (uint32_t)(32 * warp) << 16;
-    const __nv_bfloat16* vs = reinterpret_cast<const __nv_bfloat16*>(sm + C::kOffV) + tid;
-    const int64_t row = ((int64_t)s.tok0 * p.heads + h) * kHeadDim + tid;
-    for (int i0 = 0; i0 < s.n; i0 += 8) {
+  } else {
+    float* us = reinterpret_cast<float*>(sm) + col;
+    const __nv_bfloat16* vs = reinterpret_cast<const __nv_bfloat16*>(sm + C::kOffV) + col;
+    const int64_t row = ((int64_t)s.tok0 * p.heads + h) * kHeadDim + col;
+    const int step = p.heads * kHeadDim;
+    const float* pairs = part == 0 ? kk : qq;
+    float* u_out = p.u + row;
+    __nv_bfloat16* o_out = p.out + row;
+    bool bad = false;       // some node so far has no number in this channel
+    for (int b = 0; b * kBlock < s.n; ++b) {
+      const int left = s.n - b * kBlock;
+      const float* diag = pairs + pair_block(b, b) * 64;
       uint32_t x[16];
-      tmem_ld16(tmem + lanes + 2 * i0, x);
+      tmem_ld16(tmem + lanes + C::kTD + 2 * kBlock * b, x);
       tmem_wait_ld();
+      float first[8];
 #pragma unroll
-      for (int r = 0; r < 8; ++r) {
-        const int i = i0 + r;
-        if (i < s.n) {
-          const int base = i * (i + 1) / 2;
-          float stk = __uint_as_float(x[r]) * mul[2 * i0 + r], o = __uint_as_float(x[8 + r]) * mul[2 * i0 + 8 + r];
-          const int d = depth[i];
-#pragma unroll 4
-          for (int e = 1; e < d; ++e) {
-            const float2 w = kq[base + e];
-            const float uj = us[anc[base + e] * 128];
-            stk = fmaf(w.x, uj, stk);
-            o = fmaf(w.y, uj, o);
-          }
-          const float u = beta[i] * (__bfloat162float(vs[i * 128]) - stk);
-          us[i * 128] = u;
-          o = fmaf(kq[base].y, u, o);
-          const int64_t at = row + (int64_t)i * p.heads * kHeadDim;
-          p.u[at] = u;
-          p.out[at] = __float2bfloat16_rn(o);
+      for (int r = 0; r < 8; r += 4) {
+        const float4 m = *reinterpret_cast<const float4*>(mul + 2 * kBlock * b + kBlock * part + r);
+        const float ms[4] = {m.x, m.y, m.z, m.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) first[r + e] = __uint_as_float(part == 0 ? x[r + e] : x[8 + r + e]) * unscale * ms[e];
+      }
+      float2 acc[4];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) acc[r] = make_float2(first[2 * r], first[2 * r + 1]);
+      // block (b, pb)'s part of the eight sums
+      auto add = [&](int pb) {
+        const float* w = pairs + pair_block(b, pb) * 64;
+        const float* uj = us + pb * (kBlock * 128);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float u = uj[j * 128];
+          const float4 w0 = *reinterpret_cast<const float4*>(w + 8 * j), w1 = *reinterpret_cast<const float4*>(w + 8 * j + 4);
+          const float2 uu = make_float2(u, u);
+          acc[0] = fma2(make_float2(w0.x, w0.y), uu, acc[0]);
+          acc[1] = fma2(make_float2(w0.z, w0.w), uu, acc[1]);
+          acc[2] = fma2(make_float2(w1.x, w1.y), uu, acc[2]);
+          acc[3] = fma2(make_float2(w1.z, w1.w), uu, acc[3]);
         }
+      };
+      // The same sum for node r of the block by its own branch: a node without a number must not meet the
+      // zeros of those that do not descend from it.
+      auto sum_of = [&](int r, uint64_t on) -> float {
+        float sum = first[r];
+        while (on) {
+          const int j = __ffsll((long long)on) - 1;
+          on &= on - 1;
+          sum = fmaf(pairs[pair_block(b, j / kBlock) * 64 + (j % kBlock) * 8 + r], us[j * 128], sum);
+        }
+        return sum;
+      };
+      for (int pb = 0; pb < b; ++pb)
+        if (flag[pair_block(b, pb)]) add(pb);
+      if (part == 0) {
+        float v[8], u[8];
+#pragma unroll
+        for (int r = 0; r < 8; ++r) v[r] = __bfloat162float(vs[(kBlock * b + r) * 128]);
+        const float4 b0 = *reinterpret_cast<const float4*>(beta + kBlock * b);
+        const float4 b1 = *reinterpret_cast<const float4*>(beta + kBlock * b + 4);
+        const float bs[8] = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
+        float sums[8], most = 0.0f;
+#pragma unroll
+        for (int r = 0; r < 8; ++r) sums[r] = r & 1 ? acc[r >> 1].y : acc[r >> 1].x;
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+          u[r] = bs[r] * (v[r] - sums[r]);
+          most = attn::max_nan(most, fabsf(u[r]));
+          float w[8];
+          *reinterpret_cast<float4*>(w) = *reinterpret_cast<const float4*>(diag + 8 * r);
+          *reinterpret_cast<float4*>(w + 4) = *reinterpret_cast<const float4*>(diag + 8 * r + 4);
+#pragma unroll
+          for (int y = r + 1; y < 8; ++y) sums[y] = fmaf(w[y], u[r], sums[y]);
+        }
+        if (bad || !(most <= 3.402823466e38f)) {
+          bad = true;
+#pragma unroll
+          for (int r = 0; r < 8; ++r) {
+            const int i = kBlock * b + r;
+            u[r] = i < s.n ? bs[r] * (v[r] - sum_of(r, anc[i] & ~(1ull << i))) : 0.0f;
+            us[i * 128] = u[r];
+          }
+        }
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+          us[(kBlock * b + r) * 128] = u[r];
+          if (r < left) u_out[r * step] = u[r];
+        }
+        u_out += (int64_t)kBlock * step;
+        bad_s[col] = bad;
+        bar_arrive(1 + b, kThreads);
+      } else {
+        named_barrier_sync(1 + b, kThreads);
+        bad = bad_s[col] != 0;
+        add(b);
+        if (bad) {
+#pragma unroll
+          for (int r = 0; r < 8; ++r) {
+            const float o = sum_of(r, anc[kBlock * b + r]);
+            if (r & 1) acc[r >> 1].y = o;
+            else acc[r >> 1].x = o;
+          }
+        }
+#pragma unroll
+        for (int r = 0; r < 8; ++r)
+          if (r < left) o_out[r * step] = __float2bfloat16_rn(r & 1 ? acc[r >> 1].y : acc[r >> 1].x);
+        o_out += (int64_t)kBlock * step;
       }
     }
   }
@@ -414,7 +541,7 @@ __global__ void __launch_bounds__(kThreads, 2) kda_tree_commit_kernel(const __gr
     if (kBf16) {
       const uint2 w =
           *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p.initial_state) + at + r * kHeadDim);
-      const float2 a = tcc::unpack_bf16x2(w.x), b = tcc::unpack_bf16x2(w.y);
+      const float2 a = unpack_bf16x2(w.x), b = unpack_bf16x2(w.y);
       st[r] = make_float4(a.x, a.y, b.x, b.y);
     } else {
       st[r] = *reinterpret_cast<const float4*>(static_cast<const float*>(p.initial_state) + at + r * kHeadDim);
@@ -431,14 +558,14 @@ __global__ void __launch_bounds__(kThreads, 2) kda_tree_commit_kernel(const __gr
     if (tid < s.n && ((on >> tid) & 1)) node_s[__popcll(on & ((1ull << tid) - 1))] = tid;
     __syncthreads();
     // keys of the branch, their decays beside them in the place of u
-    const float gsc = expf(p.A_log[h]);
+    const float gate = -kLog2e * expf(p.A_log[h]), lower = p.lower_bound * kLog2e;
     const float4 dt = *reinterpret_cast<const float4*>(p.dt_bias + hoff + 4 * lane);
     for (int e = warp; e < L; e += kThreads / 32) {
       const int64_t t = s.tok0 + node_s[e];
       const uint2 kw = *reinterpret_cast<const uint2*>(p.k + t * p.s_k + hoff + 4 * lane);
       const uint2 gw = *reinterpret_cast<const uint2*>(p.g + t * p.s_g + hoff + 4 * lane);
-      const float2 k0 = tcc::unpack_bf16x2(kw.x), k1 = tcc::unpack_bf16x2(kw.y);
-      const float2 g0 = tcc::unpack_bf16x2(gw.x), g1 = tcc::unpack_bf16x2(gw.y);
+      const float2 k0 = unpack_bf16x2(kw.x), k1 = unpack_bf16x2(kw.y);
+      const float2 g0 = unpack_bf16x2(gw.x), g1 = unpack_bf16x2(gw.y);
       float sum = k0.x * k0.x + k0.y * k0.y + k1.x * k1.x + k1.y * k1.y;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
@@ -446,8 +573,8 @@ __global__ void __launch_bounds__(kThreads, 2) kda_tree_commit_kernel(const __gr
       *reinterpret_cast<float4*>(keys + e * kHeadDim + 4 * lane) =
           make_float4(k0.x * ik, k0.y * ik, k1.x * ik, k1.y * ik);
       *reinterpret_cast<float4*>(us + e * kHeadDim + 4 * lane) =
-          make_float4(decay_of(g0.x, dt.x, gsc, p.lower_bound), decay_of(g0.y, dt.y, gsc, p.lower_bound),
-                      decay_of(g1.x, dt.z, gsc, p.lower_bound), decay_of(g1.y, dt.w, gsc, p.lower_bound));
+          make_float4(decay_of(g0.x + dt.x, gate, lower), decay_of(g0.y + dt.y, gate, lower),
+                      decay_of(g1.x + dt.z, gate, lower), decay_of(g1.y + dt.w, gate, lower));
     }
     __syncthreads();
     if (tid < kHeadDim) {
@@ -503,11 +630,11 @@ cudaError_t launch_nodes(const RecurParams& p, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   e = once.run(dev, [&]() -> cudaError_t {
     return cudaFuncSetAttribute(kda_tree_recur_kernel<NT, kBf16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                Cfg<NT>::kBytes);
+                                (Cfg<NT, kBf16>::kBytes));
   });
   if (e != cudaSuccess) return e;
   return attn::launch(kda_tree_recur_kernel<NT, kBf16>, dim3((unsigned)(p.num_seqs * p.heads)), dim3(kThreads),
-                      Cfg<NT>::kBytes, true, stream, p);
+                      (Cfg<NT, kBf16>::kBytes), true, stream, p);
 }
 template <bool kBf16>
 cudaError_t launch_dtype(const RecurParams& p, cudaStream_t stream) {
