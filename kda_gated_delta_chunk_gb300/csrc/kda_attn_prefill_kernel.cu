@@ -50,19 +50,22 @@ constexpr int kOffQ = 0;                                    // [half][term] 128 
 constexpr int kOffVB = kOffQ + 4 * 16384;                   // [2] V as f16, two 64-channel blocks
 constexpr int kOffK = kOffVB + 2 * 32768;                   // [kKStages] K tiles
 constexpr int kOffV8 = kOffK + kKStages * 16384;            // [kVStages] V tiles
-constexpr int kOffSc = kOffV8 + kVStages * 16384;           // float4 [4][8]: k scale, log2 v scale, 1 / v scale
-constexpr int kOffQmul = kOffSc + 4 * 8 * 16;               // float [256]
+constexpr int kOffSc = kOffV8 + kVStages * 16384;           // float4 [4 or 8][8]: k scale, log2 v scale, 1 / v scale
+constexpr int kOffQmul = kOffSc + 8 * 8 * 16;               // float [256]
 constexpr int kOffMx = kOffQmul + 4 * kRowsP;               // float [2][2][256]: maxima of a row's two threads
 constexpr int kOffL = kOffMx + 16 * kRowsP;                 // float [256][2]: denominators
 constexpr int kOffSeg = kOffL + 8 * kRowsP;                 // Segment [kSegs]
 constexpr int kOffBars = kOffSeg + 64 * 4;
-constexpr int kNumBars = 2 * kKStages + 2 * kVStages + 2 * 7 + 4 + 2 * kSegs;
+constexpr int kNumBars = 2 * kKStages + 2 * 4 + 2 * 7 + 8 + 2 * kSegs;
 constexpr int kOffMiscP = kOffBars + 8 * kNumBars;
 constexpr int kSmemP = kOffMiscP + 384 + 1024;
 static_assert(kSmemP <= 227 * 1024, "shared memory");
 
 // tensor memory columns
 constexpr uint32_t kTS = 0, kTOP = 256;     // S (P) of half h at 128 h, O at 256 + 128 h
+
+// named barriers beside the pairs' (1-8) and the halves' (9, 10)
+constexpr uint32_t kIdBoth = 11, kIdMerge = 12;
 
 constexpr int kSlotFloatsP = kRowsP * 130;
 
@@ -72,13 +75,17 @@ struct PartDescP {
   int head0;          // its first query head
 };
 
+// What a launch works on: causal rows; the nodes of trees; the same in row tiles of 128, both halves taking the
+// key tiles of one row tile in turn (even ones half A, odd ones half B).
+enum { kCausal = 0, kNodesWide = 1, kNodesTurns = 2 };
+
 struct PrefillParams {
   AttnParams a;
   CacheMaps maps;
   int group;                 // query heads of a kv head
   uint32_t group_magic;      // 65535 / group + 1 (div_small)
   int gate;                  // the call's number, when the decode kernel runs beside this one; else 0
-  int few, tokens;           // rows of the decode kernel's sequences at most; new tokens per row tile (256 / group)
+  int few, tokens;           // rows of the decode kernel's sequences at most; new tokens per row tile (256 or 128 / group)
   int64_t least;             // units of those below which this kernel takes them too
   PartDescP* desc;
   float* slots;
@@ -153,19 +160,26 @@ struct Segment {
   const int32_t* table;      // the sequence's pages
 };
 
-template <int kCap, bool kTree>
+template <int kCap, int kKind>
 __global__ void __launch_bounds__(kThreadsP, 1)
     kda_attn_prefill_kernel(const __grid_constant__ PrefillParams p) {
+  constexpr bool kTree = kKind != kCausal, kTurns = kKind == kNodesTurns;
+  constexpr int kScales = kTurns ? 8 : 4;            // tiles whose scales are kept
+  // (in turns there is one row tile's queries, and two V tiles in the place of the other's)
+  constexpr int kVS = kTurns ? 4 : kVStages;
+  auto v8_at = [](uint32_t stage) -> uint32_t {
+    return kTurns && stage >= 2 ? kOffQ + 32768 + (stage - 2) * 16384 : kOffV8 + stage * 16384;
+  };
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const uint32_t sb = smem_u32(sm);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t bar_kf = sb + kOffBars, bar_ke = bar_kf + 8 * kKStages;
-  const uint32_t bar_vf = bar_ke + 8 * kKStages, bar_ve = bar_vf + 8 * kVStages;
-  const uint32_t bar_be = bar_ve + 8 * kVStages;                             // widened V read
+  const uint32_t bar_vf = bar_ke + 8 * kKStages, bar_ve = bar_vf + 8 * kVS;
+  const uint32_t bar_be = bar_ve + 8 * kVS;                             // widened V read
   const uint32_t bar_q = bar_be + 16, bar_s = bar_q + 16, bar_p = bar_s + 16, bar_o = bar_p + 16;
   const uint32_t bar_of = bar_o + 16, bar_end = bar_of + 16, bar_sc = bar_end + 16;   // bar_sc: scales
-  const uint32_t bar_gf = bar_sc + 32, bar_ge = bar_gf + 8 * kSegs;               // segment ring
+  const uint32_t bar_gf = bar_sc + 64, bar_ge = bar_gf + 8 * kSegs;               // segment ring
   struct Misc {
     long long part[kThreadsP / 32];
     long long rest;          // first tile's place in its sequence
@@ -185,7 +199,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
       mbar_init(bar_kf + 8 * i, 1);
       mbar_init(bar_ke + 8 * i, 1);
     }
-    for (int i = 0; i < kVStages; ++i) {
+    for (int i = 0; i < kVS; ++i) {
       mbar_init(bar_vf + 8 * i, 1);
       mbar_init(bar_ve + 8 * i, 128);
     }
@@ -198,10 +212,10 @@ __global__ void __launch_bounds__(kThreadsP, 1)
       mbar_init(bar_of + 8 * i, kSoftWarps / 2);
       mbar_init(bar_end + 8 * i, 1);
     }
-    for (int i = 0; i < 4; ++i) mbar_init(bar_sc + 8 * i, 1);
+    for (int i = 0; i < 8; ++i) mbar_init(bar_sc + 8 * i, 1);
     for (int i = 0; i < kSegs; ++i) {
       mbar_init(bar_gf + 8 * i, 1);
-      mbar_init(bar_ge + 8 * i, kSoftWarps + 6);   // softmax, V, producer, MMA
+      mbar_init(bar_ge + 8 * i, kSoftWarps + (kTurns ? 7 : 6));   // softmax, V, producer(s), MMA
     }
     mbar_fence_init();
     for (int i = 0; i < 8; ++i) misc->poison[i] = 0;
@@ -385,8 +399,11 @@ __global__ void __launch_bounds__(kThreadsP, 1)
 
   if (warp >= kSoftWarps + 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
-    if (warp == kSoftWarps + 4) {
-      // ================= producer; a tile's pages and scales are looked up one tile ahead
+    if (warp == kSoftWarps + 4 || (kTurns && warp == kSoftWarps + 7)) {
+      // ================= producer; a tile's pages and scales are looked up one tile ahead.  In turns the
+      // values have a warp of their own: a tile is half as long there, and keys that waited for a place of
+      // the values before them came late (tile 2350 -> 1400 cycles, with four places for values)
+      const bool feeds_k = warp == kSoftWarps + 4, feeds_v = !kTurns || !feeds_k;
       uint32_t it = 0, seg = 0;
       bool ok = true;
       const int per = P / 16;                            // 16-key groups per page
@@ -412,43 +429,55 @@ __global__ void __launch_bounds__(kThreadsP, 1)
         };
         int pg = page_of(g, g.key0);
         for (int key = g.key0; key < g.key1; key += kTile, ++it) {
-          const float ks = scale_of(p.a.c.k_scale, pg), vs = scale_of(p.a.c.v_scale, pg);
-          const int pg_next = page_of(g, key + kTile);
-          const uint32_t sk = it % kKStages, sv = it % kVStages;
-          if (it >= kKStages) ok = mbar_wait_sleep(bar_ke + 8 * sk, (it / kKStages - 1) & 1);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          // (slot it % 4 was last read for tile it - 4, whose P precedes the products of tile
-          // it - 3 that the wait above saw done)
-          if (lane < 8)   // (a page without a scale is NaN to the rows that see it, and nothing to the others)
-            reinterpret_cast<float4*>(sm + kOffSc)[(it & 3) * 8 + lane] =
-                make_float4(ks, vs > 0.0f ? lg2(vs) : NAN, vs > 0.0f ? __fdividef(1.0f, vs) : 0.0f, 0.0f);
+          const uint32_t sk = it % kKStages, sv = it % kVS;
           const bool loads = pg != -2 && lane % per == 0;
-          const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, loads)) * P * kHeadDim;
           const int row = lane * 16;
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(bar_sc + 8 * (it & 3));
-            mbar_expect_tx(bar_kf + 8 * sk, bytes);
+          int pg_next = 0;
+          if (feeds_k) {
+            const float ks = scale_of(p.a.c.k_scale, pg), vs = scale_of(p.a.c.v_scale, pg);
+            pg_next = page_of(g, key + kTile);
+            if (it >= kKStages) ok = mbar_wait_sleep(bar_ke + 8 * sk, (it / kKStages - 1) & 1);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            // (slot it % 4 was last read for tile it - 4, whose P precedes the products of tile
+            // it - 3 that the wait above saw done; in turns slot it % 8 for tile it - 8, whose P precedes that
+            // of tile it - 6, which precedes those products)
+            if (lane < 8)   // (a page without a scale is NaN to the rows that see it, and nothing to the others)
+              reinterpret_cast<float4*>(sm + kOffSc)[(it % kScales) * 8 + lane] =
+                  make_float4(ks, vs > 0.0f ? lg2(vs) : NAN, vs > 0.0f ? __fdividef(1.0f, vs) : 0.0f, 0.0f);
           }
+          const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, loads)) * P * kHeadDim;
           __syncwarp();
-          if (loads) tma_load_4d(sb + kOffK + sk * 16384 + row * 128, &p.maps.k, 0, 0, g.ch, pg, bar_kf + 8 * sk);
-          if (it >= kVStages) ok = mbar_wait_sleep(bar_ve + 8 * sv, (it / kVStages - 1) & 1);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          if (lane == 0) mbar_expect_tx(bar_vf + 8 * sv, bytes);
-          __syncwarp();
-          if (loads) tma_load_4d(sb + kOffV8 + sv * 16384 + row * 128, &p.maps.v, 0, 0, g.ch, pg, bar_vf + 8 * sv);
+          if (feeds_k) {
+            if (lane == 0) {
+              mbar_arrive(bar_sc + 8 * (it % kScales));
+              mbar_expect_tx(bar_kf + 8 * sk, bytes);
+            }
+            __syncwarp();
+            if (loads) tma_load_4d(sb + kOffK + sk * 16384 + row * 128, &p.maps.k, 0, 0, g.ch, pg, bar_kf + 8 * sk);
+          } else {
+            pg_next = page_of(g, key + kTile);
+          }
+          if (feeds_v) {
+            if (it >= kVS) ok = mbar_wait_sleep(bar_ve + 8 * sv, (it / kVS - 1) & 1);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            if (lane == 0) mbar_expect_tx(bar_vf + 8 * sv, bytes);
+            __syncwarp();
+            if (loads) tma_load_4d(sb + v8_at(sv) + row * 128, &p.maps.v, 0, 0, g.ch, pg, bar_vf + 8 * sv);
+          }
           pg = pg_next;
         }
         if (!ok) break;
       }
       if (!ok && lane == 0) record_error(p.a.status, KDA_ERR_DEVICE_TIMEOUT, 333);
       // the copies in flight end before the CTA does (a failed wait left at most one K behind)
-      for (uint32_t i = it > kKStages ? it - kKStages : 0; i < it + (ok ? 0 : 1); ++i)
-        mbar_wait_sleep(bar_kf + 8 * (i % kKStages), (i / kKStages) & 1);
-      for (uint32_t i = it > kVStages ? it - kVStages : 0; i < it; ++i)
-        mbar_wait_sleep(bar_vf + 8 * (i % kVStages), (i / kVStages) & 1);
+      if (feeds_k)
+        for (uint32_t i = it > kKStages ? it - kKStages : 0; i < it + (ok ? 0 : 1); ++i)
+          mbar_wait_sleep(bar_kf + 8 * (i % kKStages), (i / kKStages) & 1);
+      if (feeds_v)
+        for (uint32_t i = it > kVS ? it - kVS : 0; i < it; ++i)
+          mbar_wait_sleep(bar_vf + 8 * (i % kVS), (i / kVS) & 1);
     } else if (warp == kSoftWarps + 5) {
       // ================= MMA issuer (the warp stays together; one lane issues)
       constexpr uint32_t id_s = idesc_e4m3(128, 128, 0, 0), id_o = idesc_f16(128, 128, 0, 1);
@@ -459,7 +488,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
       bool ok = true;
       uint32_t sk = 0;                                   // stage of the next keys
       auto qk = [&](int h) {                             // S of half h from the keys of stage sk
-        const uint64_t dk = dk0 + sk * (16384 >> 4), q = dq + h * (32768 >> 4);
+        const uint64_t dk = dk0 + sk * (16384 >> 4), q = dq + (kTurns ? 0 : h * (32768 >> 4));
 #pragma unroll
         for (int x = 0; x < 8; ++x)
           mma_e4m3_on(lead, tmem + kTS + 128 * h, q + ((x >> 2) * 16384 + (x & 3) * 32) / 16,
@@ -469,7 +498,8 @@ __global__ void __launch_bounds__(kThreadsP, 1)
       auto pv = [&](uint32_t i, int h, bool first_tile, bool last_tile) {   // O of half h += P(i) V(i)
         // (the segment before has read its O)
         if (first_tile && seg > 0) ok = ok && mbar_wait_sleep(bar_of + 8 * h, (seg - 1) & 1);
-        ok = ok && mbar_wait_sleep(bar_p + 8 * h, i & 1);      // P(i), V(i) and the keys of the tile after
+        // P(i), V(i) and the keys of the half's next tile
+        ok = ok && mbar_wait_sleep(bar_p + 8 * h, (kTurns ? i >> 1 : i) & 1);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) return;
         tc_fence_after();
@@ -485,6 +515,41 @@ __global__ void __launch_bounds__(kThreadsP, 1)
         if (!ok || !sg->more) break;
         const int tiles = (sg->key1 - sg->key0) / kTile;
         seg_done(seg);
+        if (kTurns) {
+          // tile i is half i & 1's: S of the first two, then O of a tile and S of the half's next
+          ok = mbar_wait_sleep(bar_q, seg & 1);
+          const uint32_t end = it + tiles;
+          for (uint32_t i = it; ok && i < end && i < it + 2; ++i) {
+            sk = i % kKStages;
+            ok = mbar_wait_sleep(bar_kf + 8 * sk, (i / kKStages) & 1);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            tc_fence_after();
+            qk(i & 1);
+            mma_commit_on(lead, bar_ke + 8 * sk);
+          }
+          ok = __all_sync(0xffffffffu, ok);
+          const uint32_t start = it;
+          for (; ok && it < end; ++it) {
+            pv(it, it & 1, it < start + 2, it + 2 >= end);
+            if (!ok) break;
+            mma_commit_on(lead, bar_be + 8 * (it & 1));
+            if (it + 2 < end) {
+              sk = (it + 2) % kKStages;
+              qk(it & 1);
+              mma_commit_on(lead, bar_ke + 8 * sk);
+            }
+          }
+          if (ok && tiles == 1) {      // the other half's O of nothing
+            const int h = it & 1;
+            if (seg > 0) ok = mbar_wait_sleep(bar_of + 8 * h, (seg - 1) & 1);
+            ok = __all_sync(0xffffffffu, ok);
+            mma_commit_on(lead, bar_o + 8 * h);
+          }
+          ++seg;
+          if (!ok) break;
+          continue;
+        }
         ok = mbar_wait_sleep(bar_kf + 8 * sk, (it / kKStages) & 1);
         for (int h = 0; h < 2; ++h) {
           ok = ok && mbar_wait_sleep(bar_q + 8 * h, seg & 1);
@@ -584,12 +649,12 @@ __global__ void __launch_bounds__(kThreadsP, 1)
       seg_done(seg);
       if (vt == 0) misc->poison[(seg + 4) & 7] = 0;      // last read four segments ago
       for (; key0 < key1; key0 += kTile, ++it) {
-        const uint32_t sv = it % kVStages, vb = it & 1;
-        ok = mbar_wait_sleep(bar_vf + 8 * sv, (it / kVStages) & 1);
+        const uint32_t sv = it % kVS, vb = it & 1;
+        ok = mbar_wait_sleep(bar_vf + 8 * sv, (it / kVS) & 1);
         if (it >= 2) ok = ok && mbar_wait_sleep(bar_be + 8 * vb, ((it >> 1) - 1) & 1);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        const unsigned char* src = sm + kOffV8 + sv * 16384;
+        const unsigned char* src = sm + v8_at(sv);
         unsigned char* dst = sm + kOffVB + vb * 32768 + (c >> 2) * 16384;
         const int seen0 = first_seen(p_first, p.a.window);   // no row of the tile sees an earlier key
         const bool masked = key0 + kTile - 1 > p_first || key0 < first_seen(p_last, p.a.window);
@@ -628,6 +693,18 @@ __global__ void __launch_bounds__(kThreadsP, 1)
         // This warp's arrival on the barriers of P(it) tells the MMA issuer that V(it) is there, and
         // the next keys: it then has one thing to wait for (a wait behind matrix instructions takes
         // until they have left its queue).  Not before P(it - 1), whose phase it would count in.
+        if (kTurns) {
+          // the half's tile before, and the other half's (so the keys whose stage the next ones wanted
+          // here take have been there)
+          const uint32_t h = it & 1, next = it + 2;
+          if (it > 1) ok = mbar_wait_sleep(bar_p + 8 * h, ((it - 2) >> 1) & 1);
+          if (it > 0) ok = ok && mbar_wait_sleep(bar_p + 8 * (h ^ 1), ((it - 1) >> 1) & 1);
+          if (key0 + 2 * kTile < key1) ok = ok && mbar_wait_sleep(bar_kf + 8 * (next % kKStages), (next / kKStages) & 1);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          if (lane == 0) mbar_arrive(bar_p + 8 * h);
+          continue;
+        }
         if (it > 0) ok = mbar_wait_sleep(bar_p, (it - 1) & 1) && mbar_wait_sleep(bar_p + 8, (it - 1) & 1);
         if (key0 + kTile < key1) ok = ok && mbar_wait_sleep(bar_kf + 8 * ((it + 1) % kKStages), ((it + 1) / kKStages) & 1);
         ok = __all_sync(0xffffffffu, ok);
@@ -645,7 +722,8 @@ __global__ void __launch_bounds__(kThreadsP, 1)
     // ================= softmax: two threads a row, 64 keys (64 channels of O) each.  A wait that
     // gives up clears `ok`, after which nothing is waited for any more but every barrier is met.
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
-    const int half = warp >> 3, cg = (warp >> 2) & 1, row = 128 * half + 32 * (warp & 3) + lane;
+    const int half = warp >> 3, cg = (warp >> 2) & 1, place = 128 * half + 32 * (warp & 3) + lane;
+    const int row = kTurns ? place & 127 : place;
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t ts = tmem + kTS + 128 * half + lanes;
     const uint32_t to = tmem + kTOP + 128 * half + 64 * cg + lanes;
@@ -653,20 +731,24 @@ __global__ void __launch_bounds__(kThreadsP, 1)
     const Cap cap = kCap ? cap_of(p.a.softcap) : Cap{0.0f, 0.0f};
     const float sign = p.a.scale < 0.0f ? -1.0f : 1.0f;  // (the row maximum is taken before the scale)
     float* qmul_s = reinterpret_cast<float*>(sm + kOffQmul);
-    float* mx_s = reinterpret_cast<float*>(sm + kOffMx) + row;
-    float* l_s = reinterpret_cast<float*>(sm + kOffL) + 2 * row;
+    float* mx_s = reinterpret_cast<float*>(sm + kOffMx) + place;
+    float* l_s = reinterpret_cast<float*>(sm + kOffL) + 2 * place;
     uint32_t it = 0, seg = 0;
     bool ok = true;
     while (true) {
       const Segment* sg = seg_wait(seg, ok);
       // (the half's threads go on or leave together; its staging of the segment before is over)
-      if (bar_any(id_half, 256, !ok)) {
+      // (in turns: both halves', whose merge is a barrier)
+      if (bar_any(kTurns ? kIdBoth : id_half, kTurns ? 512 : 256, !ok)) {
         ok = false;
         break;
       }
       if (!sg->more) break;
       const int rows = sg->cnt * G;
-      {   // ---- queries as two e4m3 terms: 16 lanes a row, 16 rows a warp
+      if (kTurns && half == 1) {      // (the other half's, for both)
+        ok = ok && mbar_wait_sleep(bar_q, seg & 1);
+        __syncwarp();
+      } else {   // ---- queries as two e4m3 terms: 16 lanes a row, 16 rows a warp
         const int c = lane & 15, r0 = 128 * half + 16 * (warp & 7) + (lane >> 4);
         const __nv_bfloat16* src = p.a.q + (int64_t)sg->tok0 * p.a.q_stride + sg->head0 * kHeadDim + 8 * c;
         uint4 u[8];
@@ -726,11 +808,20 @@ __global__ void __launch_bounds__(kThreadsP, 1)
       }
       const int tiles = (sg->key1 - sg->key0) / kTile;
       float m = -INFINITY, l = 0.0f;
-      for (int t = 0; t < tiles; ++t, ++it, hi -= kTile, p_lo -= kTile, p_hi -= kTile) {
+      // in turns every second tile, from the segment's first or second on
+      constexpr int kStep = kTurns ? 2 : 1;
+      const uint32_t after = it + tiles;
+      const int skip = kTurns ? (int)((it ^ half) & 1) : 0;
+      it += skip;
+      hi -= skip * kTile;
+      p_lo -= skip * kTile;
+      p_hi -= skip * kTile;
+      for (int t = 0; it < after; ++t, it += kStep, hi -= kStep * kTile, p_lo -= kStep * kTile, p_hi -= kStep * kTile) {
+        const uint32_t turn = kTurns ? it >> 1 : it;      // the half's tiles before
         // (a wait costs over 100 cycles even when it need not wait: S, the last to come, last)
-        ok = ok && mbar_wait_sleep(bar_sc + 8 * (it & 3), (it >> 2) & 1);
+        ok = ok && mbar_wait_sleep(bar_sc + 8 * (it % kScales), (it / kScales) & 1);
         // (S was issued behind the O of the tile before, so that is there as well)
-        ok = ok && mbar_wait_sleep(bar_s + 8 * half, it & 1);
+        ok = ok && mbar_wait_sleep(bar_s + 8 * half, turn & 1);
         __syncwarp();
         tc_fence_after();
         uint32_t s[64];
@@ -738,7 +829,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
         tmem_ld32(ts + 64 * cg, *reinterpret_cast<uint32_t(*)[32]>(s));
         tmem_wait_ld_of(*reinterpret_cast<uint32_t(*)[32]>(s));
         tmem_ld32(ts + 64 * cg + 32, s_hi);    // on its way while the first keys are worked on
-        const float4* sc = reinterpret_cast<const float4*>(sm + kOffSc) + (it & 3) * 8 + 4 * cg;
+        const float4* sc = reinterpret_cast<const float4*>(sm + kOffSc) + (it % kScales) * 8 + 4 * cg;
         const bool masked = kTile - 1 > p_lo || (p.a.window > 0 && p.a.window <= p_hi);
         const bool scaled = kCap || masked;    // s holds the finished exponents (else raw products)
         float mt = -INFINITY;
@@ -767,9 +858,9 @@ __global__ void __launch_bounds__(kThreadsP, 1)
           return fmaxf(a, b);
         };
         auto with_pair = [&] {        // the row's other 64 keys
-          mx_s[((it & 1) * 2 + cg) * kRowsP] = mt;
+          mx_s[((turn & 1) * 2 + cg) * kRowsP] = mt;
           group_sync(id_pair, 64);    // (also: both have S in registers, P may go over it)
-          mt = fmaxf(mt, mx_s[((it & 1) * 2 + (cg ^ 1)) * kRowsP]);
+          mt = fmaxf(mt, mx_s[((turn & 1) * 2 + (cg ^ 1)) * kRowsP]);
         };
         uint32_t pk[32];
         bool keep = false;
@@ -889,12 +980,36 @@ __global__ void __launch_bounds__(kThreadsP, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(bar_p + 8 * half);
       }
+      it = after;
       ok = ok && mbar_wait_sleep(bar_o + 8 * half, seg & 1);
       m -= kPShift;       // (the numerators' reference)
       l_s[cg] = l;
       group_sync(id_pair, 64);
       l = l_s[0] + l_s[1];
       tc_fence_after();
+      // ---- in turns: half A takes half B's maxima and denominators, and its sums from tensor memory (the rows of
+      // a warp are the same lanes there)
+      float mine = 1.0f, other = 0.0f;
+      if (kTurns) {
+        if (half == 1) {
+          if (cg == 0) {
+            mx_s[0] = m;
+            l_s[0] = l;
+          }
+          group_sync(kIdMerge, 512);
+          seg_done(seg);
+          ++seg;
+          continue;
+        }
+        ok = ok && mbar_wait_sleep(bar_o + 8, seg & 1);
+        group_sync(kIdMerge, 512);
+        tc_fence_after();
+        const float m1 = mx_s[128], l1 = l_s[256], top = fmaxf(m, m1), ref = top == -INFINITY ? 0.0f : top;
+        mine = ex2(m - ref);
+        other = ex2(m1 - ref);
+        m = top;
+        l = l * mine + l1 * other;
+      }
       // ---- the segment's rows out: 128 bytes of a row at a time through this warp's 4 KB of the
       // query area (all products of the half are done), so that the stores are whole lines
       const bool poisoned = *reinterpret_cast<volatile int*>(&misc->poison[seg & 7]) != 0;
@@ -912,6 +1027,20 @@ __global__ void __launch_bounds__(kThreadsP, 1)
         uint32_t o[32];
         tmem_ld32(to + 32 * c, o);
         tmem_wait_ld();
+        if (kTurns) {
+          // (a half without a tile, or without a key that the row sees, has nothing to add, whatever lies there)
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            uint32_t x[16];
+            tmem_ld16(to + 128 + 32 * c + 16 * g, x);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const float a = mine > 0.0f ? __uint_as_float(o[16 * g + e]) * mine : 0.0f;
+              o[16 * g + e] = __float_as_uint(other > 0.0f ? fmaf(__uint_as_float(x[e]), other, a) : a);
+            }
+          }
+        }
         if (poisoned && live) {    // NaN entries that this row sees, in tiles that some rows do not
           const int p0 = sg->p_first, p1 = sg->p_last, pos = kTree ? p1 : p0 + i_tok;
           const int cnt = __popcll(node);
@@ -962,7 +1091,10 @@ __global__ void __launch_bounds__(kThreadsP, 1)
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar_of + 8 * half);
+      if (lane == 0) {
+        mbar_arrive(bar_of + 8 * half);
+        if (kTurns) mbar_arrive(bar_of + 8);
+      }
       if (live && cg == 0) {
         if (!whole) {
           slot[kRowsP * 128 + row] = m;
@@ -1042,7 +1174,7 @@ __global__ void __launch_bounds__(32 * kMergeRows)
     p.a.lse[tok * p.a.heads + head] = den == 0.0f ? -INFINITY : (m + lg2(den)) * kLn2;
 }
 
-template <int kCap, bool kTree>
+template <int kCap, int kKind>
 cudaError_t launch_kernel(const PrefillParams& d, int sms, cudaStream_t stream) {
   static PerDeviceOnce once;
   int dev = 0;
@@ -1050,20 +1182,27 @@ cudaError_t launch_kernel(const PrefillParams& d, int sms, cudaStream_t stream) 
   if (e != cudaSuccess) return e;
   e = once.run(dev, [&]() -> cudaError_t {
     cudaFuncAttributes at;
-    cudaError_t x = cudaFuncGetAttributes(&at, kda_attn_prefill_kernel<kCap, kTree>);
+    cudaError_t x = cudaFuncGetAttributes(&at, kda_attn_prefill_kernel<kCap, kKind>);
     if (x != cudaSuccess) return x;
     // the warpgroups' register shares must fit what the block is launched with
     if ((at.numRegs + 7) / 8 * 8 * kThreadsP < kRegsNeeded) return cudaErrorInvalidConfiguration;
-    return cudaFuncSetAttribute(kda_attn_prefill_kernel<kCap, kTree>,
+    return cudaFuncSetAttribute(kda_attn_prefill_kernel<kCap, kKind>,
                                 cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemP);
   });
   if (e != cudaSuccess) return e;
-  return launch(kda_attn_prefill_kernel<kCap, kTree>, dim3((unsigned)sms), dim3(kThreadsP), kSmemP, true,
+  return launch(kda_attn_prefill_kernel<kCap, kKind>, dim3((unsigned)sms), dim3(kThreadsP), kSmemP, true,
                 stream, d);
+}
+// Trees of at most 256 rows take the halves in turns.
+bool in_turns(const AttnParams& a) {
+  const int group = a.heads / a.c.kv_heads;
+  return a.tree && group <= kRowsP / 2 && (int64_t)a.max_q_len * group <= kRowsP;
 }
 template <int kCap>
 cudaError_t launch_cap(const PrefillParams& d, int sms, cudaStream_t stream) {
-  return d.a.tree ? launch_kernel<kCap, true>(d, sms, stream) : launch_kernel<kCap, false>(d, sms, stream);
+  if (!d.a.tree) return launch_kernel<kCap, kCausal>(d, sms, stream);
+  return in_turns(d.a) ? launch_kernel<kCap, kNodesTurns>(d, sms, stream)
+                       : launch_kernel<kCap, kNodesWide>(d, sms, stream);
 }
 
 }  // namespace
@@ -1080,7 +1219,7 @@ void make_params(const AttnParams& a, int few, int64_t least, int gate, void* wo
   d->least = least;
   d->group = a.heads / a.c.kv_heads;
   d->group_magic = 65535u / (uint32_t)d->group + 1;
-  d->tokens = kRowsP / d->group;
+  d->tokens = (in_turns(a) ? kRowsP / 2 : kRowsP) / d->group;
   d->desc = static_cast<PartDescP*>(work);
   d->slots = reinterpret_cast<float*>(d->desc + sms);
 }
