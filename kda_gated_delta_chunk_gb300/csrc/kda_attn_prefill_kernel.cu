@@ -37,11 +37,14 @@ namespace kda {
 namespace attn {
 namespace {
 
-constexpr int kThreadsP = 768;
+constexpr int kThreadsP = 768, kThreadsTurns = 896;     // (in turns two groups of V warps)
 constexpr int kRowsP = 256;
 constexpr int kKStages = 3, kVStages = 2, kSegs = 4;
 constexpr int kSoftWarps = 16, kRegsSoftmax = 104, kRegsOther = 32;
 constexpr int kRegsNeeded = 32 * (kSoftWarps * kRegsSoftmax + (kThreadsP / 32 - kSoftWarps) * kRegsOther);
+constexpr int kRegsSoftmaxTurns = 96, kRegsOtherTurns = 40;
+constexpr int kRegsNeededTurns =
+    32 * (kSoftWarps * kRegsSoftmaxTurns + (kThreadsTurns / 32 - kSoftWarps) * kRegsOtherTurns);
 constexpr float kSlack = 8.0f;              // log2 growth of the maximum before O is rescaled
 constexpr float kPShift = 7.0f;             // log2 of the numerator at the maximum: at most 2^15 with the slack
 
@@ -58,7 +61,7 @@ constexpr int kOffSeg = kOffL + 8 * kRowsP;                 // Segment [kSegs]
 constexpr int kOffBars = kOffSeg + 64 * 4;
 constexpr int kNumBars = 2 * kKStages + 2 * 4 + 2 * 7 + 8 + 2 * kSegs;
 constexpr int kOffMiscP = kOffBars + 8 * kNumBars;
-constexpr int kSmemP = kOffMiscP + 384 + 1024;
+constexpr int kSmemP = kOffMiscP + 448 + 1024;
 static_assert(kSmemP <= 227 * 1024, "shared memory");
 
 // tensor memory columns
@@ -161,9 +164,12 @@ struct Segment {
 };
 
 template <int kCap, int kKind>
-__global__ void __launch_bounds__(kThreadsP, 1)
+__global__ void __launch_bounds__(kKind == kNodesTurns ? kThreadsTurns : kThreadsP, 1)
     kda_attn_prefill_kernel(const __grid_constant__ PrefillParams p) {
   constexpr bool kTree = kKind != kCausal, kTurns = kKind == kNodesTurns;
+  constexpr int kT = kTurns ? kThreadsTurns : kThreadsP;
+  constexpr int kSoftRegs = kTurns ? kRegsSoftmaxTurns : kRegsSoftmax;
+  constexpr int kOtherRegs = kTurns ? kRegsOtherTurns : kRegsOther;
   constexpr int kScales = kTurns ? 8 : 4;            // tiles whose scales are kept
   // (in turns there is one row tile's queries, and two V tiles in the place of the other's)
   constexpr int kVS = kTurns ? 4 : kVStages;
@@ -181,15 +187,15 @@ __global__ void __launch_bounds__(kThreadsP, 1)
   const uint32_t bar_of = bar_o + 16, bar_end = bar_of + 16, bar_sc = bar_end + 16;   // bar_sc: scales
   const uint32_t bar_gf = bar_sc + 64, bar_ge = bar_gf + 8 * kSegs;               // segment ring
   struct Misc {
-    long long part[kThreadsP / 32];
+    long long part[kThreadsTurns / 32];
     long long rest;          // first tile's place in its sequence
-    int few[kThreadsP / 32];
+    int few[kThreadsTurns / 32];
     int start_n, poison[8];
     int start_h, start_rt, start_off;
     uint32_t tmem;
   };
   Misc* misc = reinterpret_cast<Misc*>(sm + kOffMiscP);
-  static_assert(sizeof(Misc) <= 384, "misc");
+  static_assert(sizeof(Misc) <= 448, "misc");
   const int hk = p.a.c.kv_heads, N = p.a.num_seqs, P = p.a.c.page_size;
   const int G = p.group;
   const uint32_t gm = p.group_magic;
@@ -215,7 +221,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
     for (int i = 0; i < 8; ++i) mbar_init(bar_sc + 8 * i, 1);
     for (int i = 0; i < kSegs; ++i) {
       mbar_init(bar_gf + 8 * i, 1);
-      mbar_init(bar_ge + 8 * i, kSoftWarps + (kTurns ? 7 : 6));   // softmax, V, producer(s), MMA
+      mbar_init(bar_ge + 8 * i, kSoftWarps + (kTurns ? 11 : 6));   // softmax, V, producer(s), MMA
     }
     mbar_fence_init();
     for (int i = 0; i < 8; ++i) misc->poison[i] = 0;
@@ -270,7 +276,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
   };
   long long mine = 0, first = 0;
   int few = 0, first_few = 0;
-  for (int n0 = 0; n0 < N; n0 += kThreadsP) {
+  for (int n0 = 0; n0 < N; n0 += kT) {
     int f;
     const long long w = cost(n0 + tid, true, f);
     if (n0 == 0) {
@@ -290,7 +296,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
   __syncthreads();
   long long total = 0, total_few = 0;
 #pragma unroll
-  for (int w = 0; w < kThreadsP / 32; ++w) {
+  for (int w = 0; w < kT / 32; ++w) {
     total += misc->part[w];
     total_few += misc->few[w];
   }
@@ -308,7 +314,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
   }
   if (walk.pos < walk.end) {
     long long before = 0;
-    for (int n0 = 0; n0 < N; n0 += kThreadsP) {
+    for (int n0 = 0; n0 < N; n0 += kT) {
       int f = first_few;
       long long w = n0 == 0 ? first : cost(n0 + tid, false, f);
       if (all) w += f;
@@ -321,7 +327,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
       if (lane == 31) misc->part[warp] = inc;
       __syncthreads();
       // the warps' sums scanned by every warp, a lane each
-      const long long mine_w = lane < kThreadsP / 32 ? misc->part[lane] : 0;
+      const long long mine_w = lane < kT / 32 ? misc->part[lane] : 0;
       long long scan = mine_w;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -397,8 +403,8 @@ __global__ void __launch_bounds__(kThreadsP, 1)
     if (lane == 0) mbar_arrive(bar_ge + 8 * (seg % kSegs));
   };
 
-  if (warp >= kSoftWarps + 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
+  if (warp >= kSoftWarps + 4 && warp < kSoftWarps + 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (warp == kSoftWarps + 4 || (kTurns && warp == kSoftWarps + 7)) {
       // ================= producer; a tile's pages and scales are looked up one tile ahead.  In turns the
       // values have a warp of their own: a tile is half as long there, and keys that waited for a place of
@@ -531,6 +537,9 @@ __global__ void __launch_bounds__(kThreadsP, 1)
           ok = __all_sync(0xffffffffu, ok);
           const uint32_t start = it;
           for (; ok && it < end; ++it) {
+            if (it + 2 < end)
+              ok = mbar_wait_sleep(bar_kf + 8 * ((it + 2) % kKStages), ((it + 2) / kKStages) & 1);
+            ok = __all_sync(0xffffffffu, ok);
             pv(it, it & 1, it < start + 2, it + 2 >= end);
             if (!ok) break;
             mma_commit_on(lead, bar_be + 8 * (it & 1));
@@ -636,9 +645,11 @@ __global__ void __launch_bounds__(kThreadsP, 1)
       __syncwarp();
     }
   } else if (warp >= kSoftWarps) {
-    // ================= V to f16, MN-major, 64-channel blocks 16 KB apart
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
-    const int vt = tid - 32 * kSoftWarps, c = vt & 7;                // 16-channel chunk of this thread
+    // ================= V to f16, MN-major, 64-channel blocks 16 KB apart.  In turns four warps a half: a tile takes
+    // them longer than the tensor cores
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    const int vt = (tid - 32 * kSoftWarps) & 127, c = vt & 7;        // 16-channel chunk of this thread
+    const uint32_t vh = warp >= kSoftWarps + 8 ? 1 : 0;
     uint32_t it = 0, seg = 0;
     bool ok = true;
     while (true) {
@@ -647,8 +658,9 @@ __global__ void __launch_bounds__(kThreadsP, 1)
       const int p_first = sg->p_first, p_last = sg->p_last, key1 = sg->key1;
       int key0 = sg->key0;
       seg_done(seg);
-      if (vt == 0) misc->poison[(seg + 4) & 7] = 0;      // last read four segments ago
+      if (vt == 0 && vh == 0) misc->poison[(seg + 4) & 7] = 0;      // last read four segments ago
       for (; key0 < key1; key0 += kTile, ++it) {
+        if (kTurns && (it & 1) != vh) continue;
         const uint32_t sv = it % kVS, vb = it & 1;
         ok = mbar_wait_sleep(bar_vf + 8 * sv, (it / kVS) & 1);
         if (it >= 2) ok = ok && mbar_wait_sleep(bar_be + 8 * vb, ((it >> 1) - 1) & 1);
@@ -694,15 +706,9 @@ __global__ void __launch_bounds__(kThreadsP, 1)
         // the next keys: it then has one thing to wait for (a wait behind matrix instructions takes
         // until they have left its queue).  Not before P(it - 1), whose phase it would count in.
         if (kTurns) {
-          // the half's tile before, and the other half's (so the keys whose stage the next ones wanted
-          // here take have been there)
-          const uint32_t h = it & 1, next = it + 2;
-          if (it > 1) ok = mbar_wait_sleep(bar_p + 8 * h, ((it - 2) >> 1) & 1);
-          if (it > 0) ok = ok && mbar_wait_sleep(bar_p + 8 * (h ^ 1), ((it - 1) >> 1) & 1);
-          if (key0 + 2 * kTile < key1) ok = ok && mbar_wait_sleep(bar_kf + 8 * (next % kKStages), (next / kKStages) & 1);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          if (lane == 0) mbar_arrive(bar_p + 8 * h);
+          // (P(it - 2) is done: its products are, which the wait above saw.  The issuer waits for keys itself:
+          // of three stages those of neighbouring tiles share one, and a half's warps see every second)
+          if (lane == 0) mbar_arrive(bar_p + 8 * vh);
           continue;
         }
         if (it > 0) ok = mbar_wait_sleep(bar_p, (it - 1) & 1) && mbar_wait_sleep(bar_p + 8, (it - 1) & 1);
@@ -721,7 +727,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
   } else {
     // ================= softmax: two threads a row, 64 keys (64 channels of O) each.  A wait that
     // gives up clears `ok`, after which nothing is waited for any more but every barrier is met.
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
     const int half = warp >> 3, cg = (warp >> 2) & 1, place = 128 * half + 32 * (warp & 3) + lane;
     const int row = kTurns ? place & 127 : place;
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
@@ -824,6 +830,11 @@ __global__ void __launch_bounds__(kThreadsP, 1)
         ok = ok && mbar_wait_sleep(bar_s + 8 * half, turn & 1);
         __syncwarp();
         tc_fence_after();
+        if (kTurns && row - lane >= rows) {      // none of the warp's rows: whatever lies there is its P
+          tc_fence_before();
+          if (lane == 0) mbar_arrive(bar_p + 8 * half);
+          continue;
+        }
         uint32_t s[64];
         uint32_t (&s_hi)[32] = *reinterpret_cast<uint32_t(*)[32]>(s + 32);
         tmem_ld32(ts + 64 * cg, *reinterpret_cast<uint32_t(*)[32]>(s));
@@ -1176,6 +1187,7 @@ __global__ void __launch_bounds__(32 * kMergeRows)
 
 template <int kCap, int kKind>
 cudaError_t launch_kernel(const PrefillParams& d, int sms, cudaStream_t stream) {
+  constexpr int threads = kKind == kNodesTurns ? kThreadsTurns : kThreadsP;
   static PerDeviceOnce once;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -1185,12 +1197,13 @@ cudaError_t launch_kernel(const PrefillParams& d, int sms, cudaStream_t stream) 
     cudaError_t x = cudaFuncGetAttributes(&at, kda_attn_prefill_kernel<kCap, kKind>);
     if (x != cudaSuccess) return x;
     // the warpgroups' register shares must fit what the block is launched with
-    if ((at.numRegs + 7) / 8 * 8 * kThreadsP < kRegsNeeded) return cudaErrorInvalidConfiguration;
+    if ((at.numRegs + 7) / 8 * 8 * threads < (kKind == kNodesTurns ? kRegsNeededTurns : kRegsNeeded))
+      return cudaErrorInvalidConfiguration;
     return cudaFuncSetAttribute(kda_attn_prefill_kernel<kCap, kKind>,
                                 cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemP);
   });
   if (e != cudaSuccess) return e;
-  return launch(kda_attn_prefill_kernel<kCap, kKind>, dim3((unsigned)sms), dim3(kThreadsP), kSmemP, true,
+  return launch(kda_attn_prefill_kernel<kCap, kKind>, dim3((unsigned)sms), dim3(threads), kSmemP, true,
                 stream, d);
 }
 // Trees of at most 256 rows take the halves in turns.

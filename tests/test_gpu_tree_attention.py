@@ -251,3 +251,23 @@ def test_graph_and_stream():
     torch.cuda.current_stream().wait_stream(other)
     assert torch.equal(o2, out) and torch.equal(l2, lse)
     assert kda.last_device_status(ws) == kda.OK and kda.last_device_status(plan_ws) == kda.OK
+
+
+@pytest.mark.parametrize("n,H,hk,page", [(16, 16, 4, 128), (16, 16, 4, 16), (32, 16, 4, 64), (64, 16, 4, 32), (64, 32, 4, 64),
+                                         (3, 16, 4, 64)])
+def test_many_tiles_a_cta(n, H, hk, page):
+    """Long caches: every CTA takes dozens of key tiles one after the other, and starts and ends inside
+    sequences."""
+    lens, kv = [n] * 8, [15000 + 131 * i for i in range(8)]
+    d = make(lens, kv, H, hk, page, seed=41)
+    masks = masks_of(trees_of(lens, 42))
+    out, lse, status = launch(d, masks)
+    assert status == kda.OK
+    again = launch(d, masks)
+    assert torch.equal(again[0], out) and torch.equal(again[1], lse)
+    some = [0, 3, 7]
+    cu = [0, n, 2 * n, 3 * n]
+    part = dict(d, q_lens=[n] * 3, kv_lens=[kv[i] for i in some], cu=torch.tensor(cu, dtype=torch.int32),
+                table=d["table"][some], q=torch.cat([d["q"][n * i:n * (i + 1)] for i in some]))
+    pick = lambda x: torch.cat([x[n * i:n * (i + 1)] for i in some])  # noqa: E731
+    check(part, [masks[i] for i in some], pick(out), pick(lse))
