@@ -4,9 +4,9 @@
 // The pool's state is the count of rows that hold each page; a free page has 0.  Whoever needs pages gets the
 // lowest free ones, in the order of rows and blocks: the outcome does not depend on the order in
 // which threads run, and there is no list of free pages to keep.  The search is one CTA's scan over the
-// counts, 16 a thread at a time, which ends at the page that serves the last request; a page that is
+// counts, 16384 at a time, which ends at the page that serves the last request; a page that is
 // found knows its rank, and the rank the request (a binary search over the requests' prefix sums in
-// shared memory).  Counts go up and down by atomics on integers, whose order does not show.
+// shared memory).  The first counts are on their way while the requests are counted.  Counts go up and down by atomics on integers, whose order does not show.
 #include "kda_pages.cuh"
 
 namespace kda {
@@ -43,34 +43,58 @@ __device__ __forceinline__ int block_scan(int v, int* part, int* sum) {
   return part[warp] + inc - v;
 }
 
-// Calls give(rank, page) for the first `total` free pages; false when there are fewer.  For a whole CTA.
+// Exclusive prefix over the CTA's warps of a number that a warp's lanes have in common, and the sum.
+__device__ __forceinline__ int warp_scan(int v, int* part, int* sum) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  __syncthreads();       // (the sums of the scan before have been read)
+  if (lane == 0) part[warp] = v;
+  __syncthreads();
+  const int w = part[lane];
+  int inc = w;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += u;
+  }
+  *sum = __shfl_sync(0xffffffffu, inc, 31);
+  return __shfl_sync(0xffffffffu, inc - w, warp);
+}
+
+// A CTA's look at the counts: warp w takes 512 pages from 512 w on, 32 at a time.
+constexpr int kLooks = 16, kChunk = kWarps * 32 * kLooks;
+struct Counts {
+  int32_t r[kLooks];
+  __device__ __forceinline__ void load(const int32_t* refs, int num_pages, int64_t p0) {
+    const int64_t base = p0 + (threadIdx.x >> 5) * (32 * kLooks) + (threadIdx.x & 31);
+#pragma unroll
+    for (int j = 0; j < kLooks; ++j) r[j] = base + 32 * j < num_pages ? refs[base + 32 * j] : 1;
+  }
+};
+// Calls give(rank, page) for the first `total` free pages; false when there are fewer.  For a whole CTA, with
+// the counts of the first kChunk pages loaded.  (A lane a page: with 16 neighbouring pages a thread a few
+// threads gave all of them, one after the other.)
 template <class Give>
-__device__ bool find_free(const int32_t* refs, int num_pages, int total, int* part, Give give) {
-  constexpr int kPer = 16;
+__device__ bool find_free(const int32_t* refs, int num_pages, int total, int* part, Counts& c, Give give) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int before = 0;
-  for (int64_t p0 = 0; p0 < num_pages && before < total; p0 += kThreads * kPer) {
-    const int64_t base = p0 + (int64_t)threadIdx.x * kPer;
-    uint32_t free = 0;
-    int4 r[kPer / 4];
+  for (int64_t p0 = 0; p0 < num_pages && before < total; p0 += kChunk) {
+    if (p0 > 0) c.load(refs, num_pages, p0);
+    uint32_t free[kLooks];
+    int mine = 0;
 #pragma unroll
-    for (int j = 0; j < kPer / 4; ++j) {
-      const int64_t i = base + 4 * j;
-      r[j] = make_int4(1, 1, 1, 1);
-      if (i + 4 <= num_pages) {
-        r[j] = *reinterpret_cast<const int4*>(refs + i);
-      } else {
-        if (i < num_pages) r[j].x = refs[i];
-        if (i + 1 < num_pages) r[j].y = refs[i + 1];
-        if (i + 2 < num_pages) r[j].z = refs[i + 2];
-      }
+    for (int j = 0; j < kLooks; ++j) {
+      free[j] = __ballot_sync(0xffffffffu, c.r[j] == 0);
+      mine += __popc(free[j]);
     }
-#pragma unroll
-    for (int j = 0; j < kPer / 4; ++j)
-      free |= ((uint32_t)(r[j].x == 0) | (uint32_t)(r[j].y == 0) << 1 | (uint32_t)(r[j].z == 0) << 2 |
-               (uint32_t)(r[j].w == 0) << 3) << (4 * j);
     int found;
-    int rank = before + block_scan(__popc(free), part, &found);
-    for (; free && rank < total; ++rank, free &= free - 1) give(rank, (int)(base + __ffs(free) - 1));
+    int rank = before + warp_scan(mine, part, &found);
+    const int64_t base = p0 + warp * (32 * kLooks) + lane;
+#pragma unroll
+    for (int j = 0; j < kLooks; ++j) {
+      const int r = rank + __popc(free[j] & ((1u << lane) - 1));
+      if (((free[j] >> lane) & 1) && r < total) give(r, (int)(base + 32 * j));
+      rank += __popc(free[j]);
+    }
     before += found;
   }
   return before >= total;
@@ -134,6 +158,8 @@ __global__ void __launch_bounds__(kThreads)
   const int lane = threadIdx.x & 31;
   sm100::pdl_wait();
   sm100::pdl_launch_dependents();
+  Counts counts;
+  counts.load(p.refs, p.num_pages, 0);
   int total = 0;
   for (int r0 = 0; r0 < p.num_rows; r0 += kThreads) {
     const int row = r0 + threadIdx.x;
@@ -188,7 +214,7 @@ __global__ void __launch_bounds__(kThreads)
     total += sum;
   }
   __syncthreads();
-  const bool enough = find_free(p.refs, p.num_pages, total, part, [&](int rank, int page) {
+  const bool enough = find_free(p.refs, p.num_pages, total, part, counts, [&](int rank, int page) {
     const int row = request_of(first, p.num_rows, rank);
     p.table[(int64_t)row * p.table_stride + start[row] + rank - first[row]] = page;
     p.refs[page] = 1;
@@ -236,6 +262,8 @@ __global__ void __launch_bounds__(kThreads)
     }
     return;
   }
+  Counts counts;        // (a page that the other CTAs share is held by its source already)
+  counts.load(p.refs, p.num_pages, 0);
   for (int r = threadIdx.x; r < p.num_rows; r += kThreads) uses[r] = 0;
   __syncthreads();
   for (int i = threadIdx.x; i < num; i += kThreads) {
@@ -278,7 +306,7 @@ __global__ void __launch_bounds__(kThreads)
     total += sum;
   }
   __syncthreads();
-  const bool enough = find_free(p.refs, p.num_pages, total, part, [&](int rank, int page) {
+  const bool enough = find_free(p.refs, p.num_pages, total, part, counts, [&](int rank, int page) {
     const int i = who[rank];
     p.table[(int64_t)dst[i] * p.table_stride + p.kv_lens[src[i]] / p.page_size] = page;
     p.refs[page] = 1;
