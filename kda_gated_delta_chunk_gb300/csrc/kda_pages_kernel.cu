@@ -133,18 +133,28 @@ __global__ void __launch_bounds__(kFreeThreads)
     first = (len + p.page_size - 1) / p.page_size;
   }
   int32_t* table = p.table + (int64_t)row * p.table_stride;
-  for (int b = first + threadIdx.x; b < p.max_blocks; b += kFreeThreads) {
-    if (table[b] == -1) continue;
-    const int pg = atomicExch(table + b, -1);      // (a row that is named twice gives its pages once)
-    if (pg == -1) continue;
-    if (pg < 0 || pg >= p.num_pages) {
-      record_error(p.status, KDA_ERR_BAD_CACHE_INDEX, 422);
-      continue;
+  // (four entries of a thread in flight: each takes three trips to memory)
+  constexpr int kAhead = 4;
+  for (int b0 = first + threadIdx.x; b0 < p.max_blocks; b0 += kFreeThreads * kAhead) {
+    int pg[kAhead], held[kAhead];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j)
+      pg[j] = b0 + kFreeThreads * j < p.max_blocks ? table[b0 + kFreeThreads * j] : -1;
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j)        // (a row that is named twice gives its pages once)
+      if (pg[j] != -1) pg[j] = atomicExch(table + b0 + kFreeThreads * j, -1);
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      held[j] = 1;
+      if (pg[j] >= 0 && pg[j] < p.num_pages) held[j] = atomicSub(p.refs + pg[j], 1);
+      else if (pg[j] != -1) record_error(p.status, KDA_ERR_BAD_CACHE_INDEX, 422);
     }
-    if (atomicSub(p.refs + pg, 1) <= 0) {          // nobody held it
-      atomicAdd(p.refs + pg, 1);
-      record_error(p.status, KDA_ERR_BAD_CACHE_INDEX, 423);
-    }
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j)
+      if (held[j] <= 0) {                    // nobody held it
+        atomicAdd(p.refs + pg[j], 1);
+        record_error(p.status, KDA_ERR_BAD_CACHE_INDEX, 423);
+      }
   }
 }
 
@@ -179,8 +189,11 @@ __global__ void __launch_bounds__(kThreads)
     const int32_t* table = p.table + (int64_t)row * p.table_stride;
     const bool far = end - b > 8;
     if (!far) {
-      while (at < end && table[at] != -1) ++at;
-      for (int i = at; i < end; ++i) bad |= table[i] != -1;
+      uint32_t empty = 0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) empty |= (uint32_t)(b + j < end && table[b + j] == -1) << j;
+      at = empty ? b + __ffs(empty) - 1 : end;
+      bad |= at < end && (empty >> (at - b)) != (1u << (end - at)) - 1;      // a page behind an empty block
     }
     uint32_t todo = __ballot_sync(0xffffffffu, far);
     while (todo) {
@@ -266,10 +279,23 @@ __global__ void __launch_bounds__(kThreads)
   counts.load(p.refs, p.num_pages, 0);
   for (int r = threadIdx.x; r < p.num_rows; r += kThreads) uses[r] = 0;
   __syncthreads();
+  // a pair's rows, its source's length (-1: out of range) and last page; the first ones loaded at once
+  auto load = [&](int i, int& s, int& d, int& len, int& last) {
+    s = d = len = last = -1;
+    if (i >= num) return;
+    s = src[i];
+    d = dst[i];
+    if (s < 0 || s >= p.num_rows) return;
+    len = p.kv_lens[s];
+    if ((int64_t)len > (int64_t)p.max_blocks * p.page_size) len = -1;
+    if (len > 0 && len % p.page_size) last = p.table[(int64_t)s * p.table_stride + len / p.page_size];
+  };
+  int s, d, len, last;
+  load(threadIdx.x, s, d, len, last);
   for (int i = threadIdx.x; i < num; i += kThreads) {
-    const int s = src[i], d = dst[i];
-    if (s >= 0 && s < p.num_rows) atomicOr(uses + s, kIsSource);
-    if (d >= 0 && d < p.num_rows) atomicAdd(uses + d, 1);
+    const int a = src[i], b = dst[i];
+    if (a >= 0 && a < p.num_rows) atomicOr(uses + a, kIsSource);
+    if (b >= 0 && b < p.num_rows) atomicAdd(uses + b, 1);
   }
   __syncthreads();
   int total = 0;
@@ -278,16 +304,13 @@ __global__ void __launch_bounds__(kThreads)
     int need = 0;
     if (i < num) {
       int pg = -1;
-      const int s = src[i], d = dst[i];
-      bool ok = s >= 0 && s < p.num_rows && d >= 0 && d < p.num_rows && uses[d] == 1;
-      const int len = ok ? p.kv_lens[s] : 0;
-      ok = ok && len >= 0 && (int64_t)len <= (int64_t)p.max_blocks * p.page_size;
-      if (!ok) {
+      if (i0 > 0) load(i, s, d, len, last);
+      if (!(len >= 0 && d >= 0 && d < p.num_rows && uses[d] == 1)) {
         record_error(p.status, KDA_ERR_BAD_CACHE_INDEX, 427);
       } else {
         p.kv_lens[d] = len;
         if (len % p.page_size) {
-          pg = p.table[(int64_t)s * p.table_stride + len / p.page_size];
+          pg = last;
           need = 1;
           p.table[(int64_t)d * p.table_stride + len / p.page_size] = -1;
           if (pg < 0 || pg >= p.num_pages) {
