@@ -510,17 +510,21 @@ __global__ void __launch_bounds__(kThreads, 2)
 }
 
 // The state after the accepted branch: S' = diag(c) S0 + sum_e (decays after e . kh_e) u_e^T over the branch's nodes e.
-// A CTA takes a (sequence, head): the state's rows in registers, 16 a warp and 4 value channels a lane, on
-// their way while the branch is found and its keys are scaled.  Bound by the state's read and write.
+// A CTA takes half of a (sequence, head)'s key channels: the state's rows in registers, kRows a warp and 4 value
+// channels a lane, on their way while the branch is found and its keys are scaled.  Bound by the state's
+// read and write.
+constexpr int kCommitRows = 8, kHalves = kHeadDim / (kCommitRows * kThreads / 32);
 __host__ __device__ constexpr int commit_bytes(int nodes) { return nodes * 1024; }   // keys and u, fp32
 
 template <bool kBf16>
-__global__ void __launch_bounds__(kThreads, 2) kda_tree_commit_kernel(const __grid_constant__ RecurParams p) {
+__global__ void __launch_bounds__(kThreads, 4) kda_tree_commit_kernel(const __grid_constant__ RecurParams p) {
   extern __shared__ __align__(16) float dyn[];
   __shared__ int links[kNodes], node_s[kNodes];
   __shared__ float c_s[kHeadDim];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int h = blockIdx.x % p.heads, seq = blockIdx.x / p.heads;
+  const int ch0 = (int)(blockIdx.x % kHalves) * (kHeadDim / kHalves), item = blockIdx.x / kHalves;
+  const int h = item % p.heads, seq = item / p.heads;
+  const bool lead = h == 0 && ch0 == 0;      // reports
   pdl_wait();
   pdl_launch_dependents();
   Nodes s;
@@ -532,10 +536,11 @@ __global__ void __launch_bounds__(kThreads, 2) kda_tree_commit_kernel(const __gr
     ok = false;
   }
   const int64_t hoff = (int64_t)h * kHeadDim;
-  const int64_t at = ((int64_t)seq * p.heads + h) * (kHeadDim * kHeadDim) + 16 * warp * kHeadDim + 4 * lane;
-  float4 st[16];
+  const int64_t at = ((int64_t)seq * p.heads + h) * (kHeadDim * kHeadDim) +
+                     (ch0 + kCommitRows * warp) * kHeadDim + 4 * lane;
+  float4 st[kCommitRows];
 #pragma unroll
-  for (int r = 0; r < 16; ++r) {
+  for (int r = 0; r < kCommitRows; ++r) {
     st[r] = make_float4(0.f, 0.f, 0.f, 0.f);
     if (!p.initial_state) continue;
     if (kBf16) {
@@ -551,9 +556,9 @@ __global__ void __launch_bounds__(kThreads, 2) kda_tree_commit_kernel(const __gr
   float* keys = dyn;                                   // [L][128]
   float* us = dyn + p.max_q_len * kHeadDim;            // [L][128]
   if (!ok) {      // (the state stays)
-    if (h == 0 && tid == 0) record_error(p.status, err, 442);
+    if (lead && tid == 0) record_error(p.status, err, 442);
   } else if (s.n > 0 && node >= 0) {
-    const uint64_t on = branch_of(p.parents, s, node, links, p.status, h == 0);
+    const uint64_t on = branch_of(p.parents, s, node, links, p.status, lead);
     L = __popcll(on);
     if (tid < s.n && ((on >> tid) & 1)) node_s[__popcll(on & ((1ull << tid) - 1))] = tid;
     __syncthreads();
@@ -591,15 +596,15 @@ __global__ void __launch_bounds__(kThreads, 2) kda_tree_commit_kernel(const __gr
           p.u + ((int64_t)(s.tok0 + node_s[e]) * p.heads + h) * kHeadDim + 4 * lane);
     __syncthreads();
 #pragma unroll
-    for (int r = 0; r < 16; ++r) {
-      const float c = c_s[16 * warp + r];
+    for (int r = 0; r < kCommitRows; ++r) {
+      const float c = c_s[ch0 + kCommitRows * warp + r];
       st[r] = make_float4(st[r].x * c, st[r].y * c, st[r].z * c, st[r].w * c);
     }
     for (int e = 0; e < L; ++e) {
       const float4 u = *reinterpret_cast<const float4*>(us + e * kHeadDim + 4 * lane);
 #pragma unroll
-      for (int r = 0; r < 16; r += 4) {
-        const float4 k4 = *reinterpret_cast<const float4*>(keys + e * kHeadDim + 16 * warp + r);
+      for (int r = 0; r < kCommitRows; r += 4) {
+        const float4 k4 = *reinterpret_cast<const float4*>(keys + e * kHeadDim + ch0 + kCommitRows * warp + r);
         const float k[4] = {k4.x, k4.y, k4.z, k4.w};
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
@@ -613,7 +618,7 @@ __global__ void __launch_bounds__(kThreads, 2) kda_tree_commit_kernel(const __gr
   }
   if (L == 0 && p.final_state == p.initial_state) return;
 #pragma unroll
-  for (int r = 0; r < 16; ++r) {
+  for (int r = 0; r < kCommitRows; ++r) {
     if (kBf16)
       *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.final_state) + at + r * kHeadDim) =
           make_uint2(pack_bf16x2(st[r].x, st[r].y), pack_bf16x2(st[r].z, st[r].w));
@@ -654,7 +659,7 @@ cudaError_t launch_commit_dtype(const RecurParams& p, cudaStream_t stream) {
                                 commit_bytes(kNodes));
   });
   if (e != cudaSuccess) return e;
-  return attn::launch(kda_tree_commit_kernel<kBf16>, dim3((unsigned)(p.num_seqs * p.heads)), dim3(kThreads),
+  return attn::launch(kda_tree_commit_kernel<kBf16>, dim3((unsigned)(p.num_seqs * p.heads * kHalves)), dim3(kThreads),
                       (size_t)commit_bytes(p.max_q_len), true, stream, p);
 }
 
