@@ -271,3 +271,40 @@ def test_many_tiles_a_cta(n, H, hk, page):
                 table=d["table"][some], q=torch.cat([d["q"][n * i:n * (i + 1)] for i in some]))
     pick = lambda x: torch.cat([x[n * i:n * (i + 1)] for i in some])  # noqa: E731
     check(part, [masks[i] for i in some], pick(out), pick(lse))
+
+
+@pytest.mark.parametrize("softcap,window", [(0.0, 0), (5.0, 0), (100.0, 150), (0.0, 64)])
+@pytest.mark.parametrize("lens,kv,H,hk,page", [
+    ([40, 3, 5, 8, 64, 2], [300, 900, 131, 128, 1000, 70], 16, 4, 32),     # row tiles of 128: two, and one beside
+    ([20, 9, 32], [900, 700, 33], 8, 2, 16),
+    ([16, 1, 16], [129, 1500, 640], 16, 2, 64)])
+def test_half_filled_row_tiles(lens, kv, H, hk, page, softcap, window):
+    """Batches whose trees fill less than half of the largest row tile, with windows and capped scores."""
+    d = make(lens, kv, H, hk, page, seed=51, spread=2)
+    masks = masks_of(trees_of(lens, 52))
+    out, lse, status = launch(d, masks, softcap=softcap, window=window)
+    assert status == kda.OK
+    check(d, masks, out, lse, softcap, window)
+
+
+def test_nan_entries_in_half_filled_row_tiles():
+    """As above at 128 rows and at 160 beside small trees."""
+    for lens in ([16] * 6, [20, 2, 3, 9]):
+        test_nan_entries_reach_the_nodes_that_see_them(lens, 16, 2)
+
+
+def test_a_node_that_is_no_number():
+    """A NaN or infinite query makes its own rows NaN and no others, in both kernels and both orders."""
+    for lens, H, hk in (([6, 3], 8, 2), ([20, 9], 8, 2), ([40, 64], 16, 2)):
+        d = make(lens, [300, 400], H, hk, 16, seed=53)
+        masks = masks_of(trees_of(lens, 54))
+        clean, clean_lse, status = launch(d, masks)
+        bad = dict(d, q=d["q"].clone())
+        bad["q"][2, 1, 5] = float("nan")
+        bad["q"][4, 3, 7] = float("inf")
+        out, lse, status = launch(bad, masks)
+        assert status == kda.OK
+        want = torch.zeros(sum(lens), H, dtype=torch.bool)
+        want[2, 1] = want[4, 3] = True
+        assert torch.equal(out.isnan().all(-1).cpu(), want) and torch.equal(out.isnan().any(-1).cpu(), want)
+        assert torch.equal(out.cpu()[~want], clean.cpu()[~want]) and torch.equal(lse.cpu()[~want], clean_lse.cpu()[~want])
