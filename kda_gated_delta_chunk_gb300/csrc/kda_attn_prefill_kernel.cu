@@ -31,6 +31,19 @@
 // Masked entries as in the decode kernel: pages before every window are not read, scores by selection,
 // V rows that no row of the tile sees as zeros, and a NaN in a V row that only some rows see as zero,
 // put back into those rows at the end from the cache itself.
+//
+// Trees of drafted tokens: what a row sees among the new tokens are the bits of its node's mask, shifted to the
+// thread's 64 keys; everything else is as above, and 4 sequences of 64 nodes over 65536 keys, 32 heads over 4,
+// take 204 us (1346 TFLOP/s).  Where trees fill half of a row tile or less, the second half would work on
+// nothing: there a row tile has 128 rows, and the two halves take its key tiles in turns (even ones A, odd
+// ones B), each with a maximum, a denominator and an O of its own, which A merges at the end.  Half as long a
+// tile wants more of what feeds it: a producer warp for values beside the one for keys, four places for V,
+// and four warps a half to widen it.  16 sequences of 16 nodes over up to 16384 keys, 32 heads over 8: 83 us
+// (2.8 TB/s), side by side 104; 8 sequences over 65536, pages of 128, 243 us (4.4 TB/s).  Neither memory (35%)
+// nor the tensor cores (27%) bound it but the chain of a half's tile (S, softmax, P, O: 4400 cycles), and at
+// the size above two changes of item a CTA, 9 us each.  Measured and not kept: P as two e4m3 terms and V as it
+// lies in memory (90 us: the conversions), a third place for widened V in that of two for V (84), the next
+// item's queries made by half B while A writes (91).
 #include "kda_attn_tc.cuh"
 
 namespace kda {
