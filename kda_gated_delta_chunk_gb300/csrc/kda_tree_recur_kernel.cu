@@ -91,7 +91,7 @@ __device__ __forceinline__ float decay_of(float x, float gate, float lower) {
 // 2^e as a float, -126 <= e <= 127
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 // Exponent that brings a row with this largest magnitude (its bits) to [2^13, 2^14)
-__device__ __forceinline__ int to_half_range(uint32_t bits) { return min(max((int)(bits >> 23) - 127 - 13, -100), 100); }
+__device__ __forceinline__ int to_half_range(uint32_t bits) { return min(max((int)(bits >> 23) - 127 - 13, -100), 114); }
 // |x|'s bits, 0 for what is not finite
 __device__ __forceinline__ uint32_t magnitude(float x) {
   const uint32_t b = __float_as_uint(x) & 0x7fffffffu;
@@ -412,13 +412,13 @@ __global__ void __launch_bounds__(kThreads, 2)
       uint32_t x[16];
       tmem_ld16(tmem + lanes + C::kTD + 2 * kBlock * b, x);
       tmem_wait_ld();
-      float first[8];
+      float first[8];       // (a vector's power first, 2^-13 at most for keys: a column's may take the sum past fp32's end)
 #pragma unroll
       for (int r = 0; r < 8; r += 4) {
         const float4 m = *reinterpret_cast<const float4*>(mul + 2 * kBlock * b + kBlock * part + r);
         const float ms[4] = {m.x, m.y, m.z, m.w};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) first[r + e] = __uint_as_float(part == 0 ? x[r + e] : x[8 + r + e]) * unscale * ms[e];
+        for (int e = 0; e < 4; ++e) first[r + e] = __uint_as_float(part == 0 ? x[r + e] : x[8 + r + e]) * ms[e] * unscale;
       }
       float2 acc[4];
 #pragma unroll

@@ -270,3 +270,35 @@ def test_graph_and_stream():
     torch.cuda.current_stream().wait_stream(other)
     assert all(torch.equal(x, y) for x, y in zip(again, (out, u, fin)))
     assert kda.last_device_status(ws) == kda.OK
+
+
+def test_states_at_the_end_of_fp32():
+    """Values whose column's largest is near fp32's: still within f16 once scaled."""
+    lens, H = [9], 1
+    d = make(lens, H, seed=9, std=1.0)
+    d["state"].clamp_(-2, 2)
+    d["state"][:, :, :, 7] *= 2.0 ** 120
+    d["state"][:, :, 3, 8] = 2.0 ** 122
+    trees = trees_of(lens, 40)
+    out, u, status = forward(d, lens, trees[0])
+    assert status == kda.OK and bool(torch.isfinite(out.float()).all())
+    fin, status = commit(d, lens, trees[0], u, [8])
+    assert status == kda.OK
+    check(d, lens, trees, [8], out, u, fin)
+
+
+def test_calls_without_tokens_or_sequences():
+    d = make([1], 2, seed=10)
+    none = {x: d[x][:0] for x in ("q", "k", "v", "g", "beta")}
+    empty = i32([])
+    out, u = kda.tree_recurrent_fwd(*none.values(), d["A_log"], d["dt_bias"], -5.0, W.SCALE, d["state"], i32([0, 0]),
+                                    empty, 4)
+    assert out.shape == (0, 2, D) and u.shape == (0, 2, D)
+    fin = kda.tree_commit(none["k"], none["g"], d["A_log"], d["dt_bias"], -5.0, d["state"], i32([0, 0]), empty, u,
+                          i32([-1]), 4)
+    assert torch.equal(fin, d["state"])
+    out, u = kda.tree_recurrent_fwd(*none.values(), d["A_log"], d["dt_bias"], -5.0, W.SCALE, d["state"][:0], i32([0]),
+                                    empty, 4)
+    assert out.shape == (0, 2, D)
+    mask, pos = kda.tree_plan(empty, i32([0, 0]), i32([5]), 4)
+    assert mask.shape == pos.shape == (0,)
