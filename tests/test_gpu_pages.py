@@ -339,3 +339,58 @@ def test_graph_of_a_fork():
                 assert torch.equal(cache[0][a].view(torch.uint8), cache[0][b].view(torch.uint8))
                 assert torch.equal(cache[3][a], cache[3][b])
     assert kda.last_device_status(ws) == kda.OK
+
+
+def test_pages_past_4_gb():
+    """Copies between the ends of a cache of more than 2^32 bytes a side, and a branch accepted there."""
+    page, hk = 16, 8
+    pages = 2 ** 32 // (page * hk * D) + 1000
+    k, v = (torch.empty(pages, hk, page, D, dtype=torch.uint8, device="cuda").view(FP8) for _ in "kv")
+    ks, vs = (torch.ones(pages, hk, device="cuda") for _ in "kv")
+    g = torch.Generator(device="cuda").manual_seed(1)
+    ends = [0, 1, pages - 3, pages - 2, pages - 1]
+    for c in (k, v):
+        for p in ends:
+            c[p] = (40 * torch.randn(hk, page, D, generator=g, device="cuda")).to(FP8)
+    raw = lambda c, p: c[p].view(torch.uint8).clone()  # noqa: E731
+    was = {p: (raw(k, p), raw(v, p)) for p in ends}
+    ws = status_words()
+    kda.copy_pages(k, v, ks, vs, i32([pages - 1, 0]), i32([1, pages - 2]), workspace=ws)
+    assert torch.equal(raw(k, 1), was[pages - 1][0]) and torch.equal(raw(v, pages - 2), was[0][1])
+    # 20 cached tokens and 12 nodes in the last two pages; nodes 1, 5, 9 are kept
+    table = i32([[pages - 1, pages - 3]])
+    tree = [-1, -1, 0, 0, 2, 1, 3, 4, 2, 5, 6, 7]
+    lens = kda.cache_accept(k, v, ks, vs, table, i32([32]), i32([0, 12]), i32(tree), i32([9]), 12, workspace=ws)
+    assert lens.tolist() == [23] and kda.last_device_status(ws) == kda.OK
+    for c, old in ((k, was[pages - 3][0]), (v, was[pages - 3][1])):
+        got = raw(c, pages - 3)
+        for e, node in enumerate((1, 5, 9)):
+            assert torch.equal(got[:, 4 + e], old[:, 4 + node])
+        assert torch.equal(got[:, :4], old[:, :4]) and torch.equal(got[:, 7:], old[:, 7:])
+
+
+def test_the_largest_pool_calls():
+    """16384 rows at once; a pool searched to its end."""
+    rows, page, pages = 16384, 16, 60000
+    refs = torch.zeros(pages, dtype=torch.int32, device="cuda")
+    refs[:30000] = 1
+    table = torch.full((rows, 2), -1, dtype=torch.int32, device="cuda")
+    lens = torch.zeros(rows, dtype=torch.int32, device="cuda")
+    ws = status_words()
+    half = rows // 2
+    new = torch.zeros(rows, dtype=torch.int32, device="cuda")
+    new[:half] = 5
+    kda.reserve_pages(refs, table, lens, new, page, workspace=ws)
+    assert table[:half, 0].tolist() == list(range(30000, 30000 + half)) and int((table[half:] >= 0).sum()) == 0
+    lens[:half] = 5
+    src, dst = torch.arange(half, dtype=torch.int32, device="cuda"), torch.arange(half, rows, dtype=torch.int32, device="cuda")
+    fro, to = kda.fork_pages(refs, table, lens, src, dst, page, workspace=ws)
+    assert fro.tolist() == list(range(30000, 30000 + half)) and to.tolist() == list(range(30000 + half, 30000 + rows))
+    assert torch.equal(table[half:, 0], to) and torch.equal(lens[half:], lens[:half])
+    assert kda.last_device_status(ws) == kda.OK
+    new[:] = 20                      # a second page for every row: 16384 more than the 13616 that are left
+    kda.reserve_pages(refs, table, lens, new, page, workspace=ws)
+    assert kda.last_device_status(ws) == kda.ERR_OUT_OF_PAGES
+    left = pages - 30000 - rows
+    assert int((table[:, 1] >= 0).sum()) == left and int((refs == 0).sum()) == 0
+    assert table[:left, 1].tolist() == list(range(30000 + rows, pages))
