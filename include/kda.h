@@ -559,7 +559,8 @@ int kda_cache_accept(const kda_kv_cache* cache, const int32_t* cu_seqlens, const
  *   after a step whose drafts were partly rejected).  Else the rows named in rows [num] end: all
  *   their pages go back and their kv_lens become 0 (a row may be named twice).
  * kda_pages_reserve: pages for new_tokens [num_rows] more tokens a row: its empty blocks up to
- *   ceil((kv_lens + new_tokens) / page_size) get one each.  kv_lens stays.  At most 16384 rows.
+ *   ceil((kv_lens + new_tokens) / page_size) get one each.  kv_lens stays.  At most 16384 rows,
+ *   and 2^31 - 1 blocks in all of them.
  * kda_pages_fork: row dst[i] becomes a copy of row src[i] (kv_lens too): whole pages are held in common,
  *   a partly filled last one is given a page of its own, to be copied: from_pages[i] -> to_pages[i], both
  *   -1 where there is none.  What dst[i] held before is overwritten, not given back.  A source may

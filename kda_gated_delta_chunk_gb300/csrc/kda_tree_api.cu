@@ -222,7 +222,10 @@ int kda_pages_reserve(int32_t* refs, int32_t num_pages, int32_t* block_table, in
   int rc = check_pool(refs, num_pages, block_table, table_stride, num_rows, max_blocks, kv_lens, page_size,
                       workspace, workspace_bytes, &p);
   if (rc != KDA_OK) return rc;
-  if (num_rows > kda::pages::kMaxRows || (num_rows > 0 && !new_tokens)) return KDA_ERR_INVALID_ARG;
+  // (the requests' sum has 32 bits)
+  if (num_rows > kda::pages::kMaxRows || (int64_t)num_rows * max_blocks > INT32_MAX ||
+      (num_rows > 0 && !new_tokens))
+    return KDA_ERR_INVALID_ARG;
   if (!aligned(new_tokens, 4)) return KDA_ERR_MISALIGNED;
   int sms = 0;
   rc = current_device(&sms);

@@ -100,6 +100,12 @@ def test_pool_calls_refuse(L, call, over):
     assert pool(L, call, **over) == INVALID
 
 
+def test_reserve_refuses_tables_whose_requests_may_pass_32_bits(L):
+    assert pool(L, "reserve", rows=16384, blocks=2 ** 17, stride=2 ** 17) == INVALID
+    assert pool(L, "reserve", rows=2, blocks=2 ** 30, stride=2 ** 30, page=1) == INVALID
+    assert pool(L, "reserve", rows=16384, blocks=2 ** 17 - 1, stride=2 ** 17, new=A + 1) == MISALIGNED
+
+
 @pytest.mark.parametrize("over,code", [
     (dict(fro=None), INVALID), (dict(to=None), INVALID), (dict(num=-1), INVALID), (dict(num=2 ** 30), INVALID),
     (dict(ws=None), INVALID), (dict(c=None), INVALID), (dict(fro=A + 2), MISALIGNED),
