@@ -537,7 +537,7 @@ int kda_tree_commit(const void* k, int64_t k_stride, const void* g, int64_t g_st
  * normal).
  *   accepted   int32 [num_seqs]: a node of the sequence, or -1
  *   lens_out   int32 [num_seqs]: start + the branch's length, the next step's cached tokens.  Not the
- *              cache's kv_lens itself: every layer's call reads those.
+ *              cache's kv_lens itself, which every layer's call reads, and not accepted.
  * No two sequences may have a page in common among those of their nodes.  Device errors:
  * KDA_ERR_BAD_CU_SEQLENS, KDA_ERR_INVALID_ARG (more nodes than max_q_len), KDA_ERR_BAD_TREE (accepted out
  * of range; a bad parent counts as -1), KDA_ERR_BAD_CACHE_INDEX (kv_lens below the nodes' count or beyond the

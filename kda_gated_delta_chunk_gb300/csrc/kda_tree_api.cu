@@ -178,7 +178,8 @@ int kda_cache_accept(const kda_kv_cache* cache, const int32_t* cu_seqlens, const
   int rc = check_trees(cu_seqlens, parents, workspace, total_tokens, num_seqs, max_q_len, workspace_bytes);
   if (rc != KDA_OK) return rc;
   if ((rc = check_cache(cache, num_seqs, &p.c)) != KDA_OK) return rc;
-  if (num_seqs > 0 && (!accepted || !lens_out || (const void*)lens_out == (const void*)cache->kv_lens))
+  // (every head's CTAs read what one of them would write)
+  if (num_seqs > 0 && (!accepted || !lens_out || lens_out == cache->kv_lens || lens_out == accepted))
     return KDA_ERR_INVALID_ARG;
   if ((int64_t)num_seqs * cache->kv_heads * 2 > INT32_MAX) return KDA_ERR_INVALID_ARG;
   if (!aligned(accepted, 4) || !aligned(lens_out, 4)) return KDA_ERR_MISALIGNED;

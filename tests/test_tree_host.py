@@ -72,6 +72,11 @@ def test_accept_refuses(L, over, code):
     assert accept(L, **over) == code
 
 
+def test_accept_refuses_lengths_over_its_inputs(L):
+    assert accept(L, node=3 * A, lens=3 * A) == INVALID
+    assert accept(L, node=3 * A, lens=A) == INVALID
+
+
 POOL = dict(refs=A, pages=10, table=A, stride=4, rows=3, blocks=4, lens=A, page=16)
 
 
