@@ -494,6 +494,7 @@ int kda_tree_attention(const void* q, int64_t q_stride, const kda_kv_cache* cach
  * The KDA recurrence (kda_recurrent_fwd) along the branches of trees: the state that node i continues from is its
  * parent's, or the sequence's initial state.  No state is written: the outputs are, and u, from which
  * kda_tree_commit makes the accepted node's state.
+ *   heads        at most 2^20
  *   q, k, v, g   bf16 [T, heads, 128], beta bf16 [T, heads]: a token's heads dense, strides (elements)
  *                between tokens; those of q, k, v, g multiples of 8 from 16-byte aligned pointers
  *   initial_state, state_dtype, A_log, dt_bias, lower_bound, scale: as kda_recurrent_fwd; the state is

@@ -27,7 +27,8 @@ int check_recur(const void* k, int64_t k_stride, const void* g, int64_t g_stride
                 const float* dt_bias, float lower_bound, const void* initial_state, int state_dtype,
                 const float* u, int64_t total_tokens, int32_t num_seqs, int32_t heads,
                 kda::tree::RecurParams* p) {
-  if (heads < 1 || (int64_t)num_seqs * heads > INT32_MAX / 2 || !known_dtype(state_dtype) || !A_log || !dt_bias)
+  // (a row's stride times the nodes of a block has 32 bits)
+  if (heads < 1 || heads > 1 << 20 || (int64_t)num_seqs * heads > INT32_MAX / 2 || !known_dtype(state_dtype) || !A_log || !dt_bias)
     return KDA_ERR_INVALID_ARG;
   if (!(lower_bound >= KDA_MIN_LOWER_BOUND && lower_bound <= 0.0f)) return KDA_ERR_UNSAFE_LOWER_BOUND;
   if (!aligned(A_log, 4) || !aligned(dt_bias, 16) || !aligned(initial_state, 16)) return KDA_ERR_MISALIGNED;

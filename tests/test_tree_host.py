@@ -155,3 +155,11 @@ def test_recurrence_refuses(L, call, over, code):
     (commit, dict(s1=A + 8), MISALIGNED), (commit, dict(node=A + 1), MISALIGNED)])
 def test_recurrence_and_commit_refuse(L, call, over, code):
     assert call(L, **over) == code
+
+
+@pytest.mark.parametrize("call", [recur, commit])
+def test_recurrence_refuses_rows_past_32_bits(L, call):
+    wide = dict(ks=2 ** 28, gs=2 ** 28, qs=2 ** 28, vs=2 ** 28, bs=2 ** 21)
+    wide = {k: v for k, v in wide.items() if call is recur or k in ("ks", "gs")}
+    assert call(L, H=2 ** 20 + 1, **wide) == INVALID
+    assert call(L, H=2 ** 20, **dict(wide, ks=2 ** 28 + 4)) == MISALIGNED
