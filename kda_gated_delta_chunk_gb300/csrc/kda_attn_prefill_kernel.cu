@@ -670,8 +670,10 @@ __global__ void __launch_bounds__(kKind == kNodesTurns ? kThreadsTurns : kThread
       if (!ok || !sg->more) break;
       const int p_first = sg->p_first, p_last = sg->p_last, key1 = sg->key1;
       int key0 = sg->key0;
+      // (last read four segments ago; before this segment's place is given back, or the other four warps
+      // might be there already)
+      if (vt == 0 && vh == 0) misc->poison[(seg + 4) & 7] = 0;
       seg_done(seg);
-      if (vt == 0 && vh == 0) misc->poison[(seg + 4) & 7] = 0;      // last read four segments ago
       for (; key0 < key1; key0 += kTile, ++it) {
         if (kTurns && (it & 1) != vh) continue;
         const uint32_t sv = it % kVS, vb = it & 1;
