@@ -92,7 +92,7 @@ struct RecurParams {
   int64_t total_tokens;
   int32_t num_seqs, heads, max_q_len;
 };
-cudaError_t launch_recur(const RecurParams& p, cudaStream_t stream);
+cudaError_t launch_recur(const RecurParams& p, int sms, cudaStream_t stream);
 cudaError_t launch_commit(const RecurParams& p, cudaStream_t stream);
 
 }  // namespace tree

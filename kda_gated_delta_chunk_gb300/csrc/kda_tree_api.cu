@@ -143,7 +143,7 @@ int kda_tree_recurrent_fwd(const void* q, int64_t q_stride, const void* k, int64
   p.out = static_cast<__nv_bfloat16*>(out);
   p.status = static_cast<int*>(workspace);
   p.max_q_len = max_q_len;
-  return launched(kda::tree::launch_recur(p, reinterpret_cast<cudaStream_t>(stream)));
+  return launched(kda::tree::launch_recur(p, sms, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 int kda_tree_commit(const void* k, int64_t k_stride, const void* g, int64_t g_stride, const float* A_log,

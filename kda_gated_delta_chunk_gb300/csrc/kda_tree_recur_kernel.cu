@@ -16,12 +16,13 @@
 //  - then the nodes in blocks of 8, a thread a value channel: four warps make u, the other four follow a block
 //    behind with o.  Sums over earlier blocks have no chain but their own length, and blocks without a pair
 //    of node and ancestor are left out.
-// 64 sequences of 32 nodes, 32 heads, fp32 states (134 MB of them): 95 us, 2.4 TB/s of what has to move; one
-// tree of 8 nodes, 16 heads 5.4 us.  Not bound by memory: a (sequence, head) takes 23,500 cycles of two on an
-// SM (loads 4,700, gates and norms 2,000, the terms of S0 3,000, walks and vectors 7,600, the product 1,600, the
-// nodes in order 6,200), at 1.9 instructions a cycle and 56% of the shared memory's wavefronts.  Measured and
-// not kept: 512 threads a CTA (99 us), the next CTA's state towards L2 (95), the next ancestor's rows loaded
-// ahead (95), the inverse of 1 + b K solved for beside the product and a second product with it (101).
+// 64 sequences of 32 nodes, 32 heads, fp32 states (134 MB of them): 82 us, 2.8 TB/s of what has to move; one
+// tree of 8 nodes, 16 heads 5.4 us.  Not bound by memory: a (sequence, head) takes 30,000 cycles of three on an
+// SM (the nodes' loads 3,000, gates and norms 2,400, walks and vectors 10,000, the state 3,500 and its terms
+// 1,400, the products 2,300, the nodes in order 7,000), and a bf16 state takes 75 us to fp32's 78.  Measured and not
+// kept: 512 threads a CTA (99 us, two CTAs of 256 95), the state towards L2 ahead (no gain), the next ancestor's
+// rows loaded ahead (none), half the shuffles of a walk (none), the inverse of 1 + b K solved for beside the
+// product and a second product with it (101).
 #include <cuda_fp16.h>
 
 #include "kda_attn_tc.cuh"
@@ -39,8 +40,16 @@ using tcc::unpack_bf16x2;
 constexpr int kThreads = 256;
 constexpr int kBlock = 8;          // nodes of a block
 
-template <int NT, bool kBf16>      // nodes at most; the state's type
+template <int NT, bool kBf16, bool kMany>      // nodes at most; the state's type; more CTAs than run at once
 struct Cfg {
+  // Three CTAs an SM have 80 registers a thread and 128 columns of tensor memory each.  So the state comes late, when
+  // the walks are done (its first rows a little earlier), and its two terms take the same columns one after the
+  // other.  Alone on an SM that costs time, beside two others it hides: 64 sequences of 8, 16, 32 nodes, 32 heads
+  // 44, 53, 78 us (all of the state late 45, 54, 80), two CTAs with the state on its way from the start 52, 62, 91;
+  // 10 sequences of 32 nodes 20 : 23.
+  static constexpr int kCtas = kMany && NT <= 32 ? 3 : 2;         // an SM
+  static constexpr bool kLate = kCtas == 3;
+  static constexpr int kEarly = 24;                               // (of 64)
   static constexpr int kRows = 2 * NT;
   static constexpr int kB = kRows * 256;                          // one term of the vectors
   static constexpr int kBlocks = NT / kBlock, kPairs = kBlocks * (kBlocks + 1) / 2;
@@ -57,10 +66,10 @@ struct Cfg {
   static constexpr int kOffAnc = (kOffFlag + kPairs * 4 + 15) / 16 * 16;   // uint64 [NT]: a node's branch
   static constexpr int kOffBar = kOffAnc + NT * 8;
   static constexpr int kBytes = kOffBar + 16 + 1024;
-  static constexpr uint32_t kTD = kBf16 ? 64 : 128;               // the state's terms, then the sums
+  static constexpr uint32_t kTD = kBf16 || kLate ? 64 : 128;      // the state's terms, then the sums
   static constexpr uint32_t kTmem = kTD + kRows <= 128 ? 128 : 256;
   static_assert(2 * kB == NT * 1024, "the vectors over keys and decays");
-  static_assert(2 * kBytes <= 226 * 1024, "two CTAs an SM");
+  static_assert(kCtas * kBytes <= 226 * 1024 && kCtas * kTmem <= 512, "CTAs an SM");
 };
 __device__ __forceinline__ int pair_block(int b, int pb) { return b * (b + 1) / 2 + pb; }
 
@@ -111,10 +120,10 @@ __device__ __forceinline__ int place(int ch) {
   return (ch & 64) + ((ch & 4) << 3) + ((ch & 63) >> 3) * 4 + (ch & 3);
 }
 
-template <int NT, bool kBf16>
-__global__ void __launch_bounds__(kThreads, 2)
+template <int NT, bool kBf16, bool kMany>
+__global__ void __launch_bounds__(kThreads, Cfg<NT, kBf16, kMany>::kCtas)
     kda_tree_recur_kernel(const __grid_constant__ RecurParams p) {
-  using C = Cfg<NT, kBf16>;
+  using C = Cfg<NT, kBf16, kMany>;
   using attn::fma2;
   using attn::mul2;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -133,7 +142,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int64_t hoff = (int64_t)h * kHeadDim;
 
   // ---- loads on their way: the nodes' (a warp a node, 4 channels a lane; kAhead nodes a warp at a time),
-  // then the state, a thread half a column of it (64 of its 128 key channels)
+  // then the state (or later), a thread half a column of it (64 of its 128 key channels)
   constexpr int kPer = NT / 8, kAhead = kPer < 4 ? kPer : 4;
   uint2 kw[kAhead], vw[kAhead], gw[kAhead];
   auto load_nodes = [&](int m0) {
@@ -160,21 +169,22 @@ __global__ void __launch_bounds__(kThreads, 2)
   const float gate = -kLog2e * expf(p.A_log[h]), lower = p.lower_bound * kLog2e;
   const int col = tid & 127, part = tid >> 7;
   float st[64];
-  {
+  auto load_state = [&](int r0, int r1) {       // rows [r0, r1) of the 64
     const int64_t at = ((int64_t)seq * p.heads + h) * (kHeadDim * kHeadDim) + part * (64 * kHeadDim) + col;
     if (!p.initial_state) {
 #pragma unroll
-      for (int r = 0; r < 64; ++r) st[r] = 0.0f;
+      for (int r = r0; r < r1; ++r) st[r] = 0.0f;
     } else if (kBf16) {
       const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.initial_state) + at;
 #pragma unroll
-      for (int r = 0; r < 64; ++r) st[r] = __bfloat162float(src[r * kHeadDim]);
+      for (int r = r0; r < r1; ++r) st[r] = __bfloat162float(src[r * kHeadDim]);
     } else {
       const float* src = static_cast<const float*>(p.initial_state) + at;
 #pragma unroll
-      for (int r = 0; r < 64; ++r) st[r] = src[r * kHeadDim];
+      for (int r = r0; r < r1; ++r) st[r] = src[r * kHeadDim];
     }
-  }
+  };
+  if (!C::kLate) load_state(0, 64);
   if (warp == 0) {
     tmem_alloc(smem_u32(&tmem_s), C::kTmem);
     tmem_relinquish();
@@ -237,7 +247,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         qw[pass][c] = *reinterpret_cast<const uint4*>(p.q + (int64_t)(s.tok0 + 32 * pass + node0) * p.s_q + hoff +
                                                       64 * c + 8 * sub);
     }
-  {
+  auto column_max = [&] {
     float top = 0.0f;
 #pragma unroll
     for (int r = 0; r < 64; r += 2) top = attn::max3_abs(top, st[r], st[r + 1]);
@@ -247,7 +257,8 @@ __global__ void __launch_bounds__(kThreads, 2)
       for (int r = 0; r < 64; ++r) top = fmaxf(top, __uint_as_float(magnitude(st[r])));
     }
     maxs[tid] = top;
-  }
+  };
+  if (!C::kLate) column_max();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -257,16 +268,23 @@ __global__ void __launch_bounds__(kThreads, 2)
   const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
 
   // ---- the state as f16 terms, a power of two a column: channels 2 c, 2 c + 1 in column c
-  const int fe = to_half_range(__float_as_uint(fmaxf(maxs[col], maxs[128 + col])));
-  const float unscale = pow2(fe);
-  {
+  float unscale = 1.0f;
+  uint32_t hi[32];       // (late: the low terms go first, and these take their place)
+  auto put_state = [&] {
+    const int fe = to_half_range(__float_as_uint(fmaxf(maxs[col], maxs[128 + col])));
+    unscale = pow2(fe);
     const float f = pow2(-fe);
-    uint32_t hi[32], lo[32];
 #pragma unroll
-    for (int c = 0; c < 32; ++c) split(mul2(make_float2(st[2 * c], st[2 * c + 1]), make_float2(f, f)), hi[c], lo[c]);
-    tmem_st32(tmem + lanes + 32 * part, hi);
-    if (!kBf16) tmem_st32(tmem + lanes + 64 + 32 * part, lo);
-  }
+    for (int c0 = 0; c0 < 32; c0 += 16) {
+      uint32_t lo[16];
+#pragma unroll
+      for (int c = 0; c < 16; ++c)
+        split(mul2(make_float2(st[2 * (c0 + c)], st[2 * (c0 + c) + 1]), make_float2(f, f)), hi[c0 + c], lo[c]);
+      if (!kBf16) tmem_st16(tmem + lanes + (C::kLate ? 0 : 64) + 32 * part + c0, lo);
+    }
+    if (kBf16 || !C::kLate) tmem_st32(tmem + lanes + 32 * part, hi);
+  };
+  if (!C::kLate) put_state();
 
   // ---- walks
   float2 wk[kPasses][8], wq[kPasses][8];
@@ -341,7 +359,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     if (live && sub == 0) anc[i] = branch;
   }
-  tmem_wait_st();
+  if (C::kLate) load_state(0, C::kEarly);
+  else tmem_wait_st();
   __syncthreads();            // keys and decays have been read: the vectors go over them
 #pragma unroll
   for (int pass = 0; pass < kPasses; ++pass) {
@@ -373,24 +392,49 @@ __global__ void __launch_bounds__(kThreads, 2)
     put(wk[pass], row, i < s.n);
     put(wq[pass], row + kBlock, i < s.n);
   }
+  if (C::kLate) {
+    load_state(C::kEarly, 64);
+    column_max();
+    __syncthreads();
+    put_state();
+    tmem_wait_st();
+  }
   fence_proxy_async();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
 
   // ---- S0^T [c kh; c qh]^T
-  if (tid == 0) {
-    constexpr uint32_t id = idesc_half(128, C::kRows);
+  constexpr uint32_t id = idesc_half(128, C::kRows);
+  auto product = [&](uint32_t a, uint32_t b, bool more) {
 #pragma unroll
-    for (int term = 0; term < (kBf16 ? 2 : 3); ++term) {
-      const uint32_t a = tmem + (term == 2 ? 64 : 0), b = sb + (term == 1 ? C::kB : 0);
-#pragma unroll
-      for (int ks = 0; ks < 8; ++ks)
-        mma_half_ts(tmem + C::kTD, a + 8 * ks, tcc::kdesc(b, C::kRows, ks), id, term > 0 || ks > 0);
+    for (int ks = 0; ks < 8; ++ks)
+      mma_half_ts(tmem + C::kTD, a + 8 * ks, tcc::kdesc(b, C::kRows, ks), id, more || ks > 0);
+  };
+  constexpr bool kTwice = C::kLate && !kBf16;
+  if (tid == 0) {           // (the state's low terms first, whichever way: a sequence's sums are the same in every batch)
+    if (!kBf16) product(tmem + (kTwice ? 0 : 64), sb, false);
+    if (!kTwice) {
+      product(tmem, sb, !kBf16);
+      product(tmem, sb + C::kB, true);
     }
     mma_commit(sb + C::kOffBar);
   }
   bool ok = mbar_wait(sb + C::kOffBar, 0);
+  if (kTwice) {
+    tc_fence_after();
+    tmem_st32(tmem + lanes + 32 * part, hi);
+    tmem_wait_st();
+    tc_fence_before();
+    ok = __syncthreads_and(ok);
+    tc_fence_after();
+    if (ok && tid == 0) {
+      product(tmem, sb, true);
+      product(tmem, sb + C::kB, true);
+      mma_commit(sb + C::kOffBar);
+    }
+    if (ok) ok = mbar_wait(sb + C::kOffBar, 1);
+  }
   ok = __syncthreads_and(ok);
   tc_fence_after();
 
@@ -634,26 +678,27 @@ __global__ void __launch_bounds__(kThreads, 4) kda_tree_commit_kernel(const __gr
   }
 }
 
-template <int NT, bool kBf16>
+template <int NT, bool kBf16, bool kMany>
 cudaError_t launch_nodes(const RecurParams& p, cudaStream_t stream) {
+  using C = Cfg<NT, kBf16, kMany>;
   static PerDeviceOnce once;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   e = once.run(dev, [&]() -> cudaError_t {
-    return cudaFuncSetAttribute(kda_tree_recur_kernel<NT, kBf16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                (Cfg<NT, kBf16>::kBytes));
+    return cudaFuncSetAttribute(kda_tree_recur_kernel<NT, kBf16, kMany>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                C::kBytes);
   });
   if (e != cudaSuccess) return e;
-  return attn::launch(kda_tree_recur_kernel<NT, kBf16>, dim3((unsigned)(p.num_seqs * p.heads)), dim3(kThreads),
-                      (Cfg<NT, kBf16>::kBytes), true, stream, p);
+  return attn::launch(kda_tree_recur_kernel<NT, kBf16, kMany>, dim3((unsigned)(p.num_seqs * p.heads)), dim3(kThreads),
+                      C::kBytes, true, stream, p);
 }
-template <bool kBf16>
+template <bool kBf16, bool kMany>
 cudaError_t launch_dtype(const RecurParams& p, cudaStream_t stream) {
-  return p.max_q_len <= 8    ? launch_nodes<8, kBf16>(p, stream)
-         : p.max_q_len <= 16 ? launch_nodes<16, kBf16>(p, stream)
-         : p.max_q_len <= 32 ? launch_nodes<32, kBf16>(p, stream)
-                             : launch_nodes<64, kBf16>(p, stream);
+  return p.max_q_len <= 8    ? launch_nodes<8, kBf16, kMany>(p, stream)
+         : p.max_q_len <= 16 ? launch_nodes<16, kBf16, kMany>(p, stream)
+         : p.max_q_len <= 32 ? launch_nodes<32, kBf16, kMany>(p, stream)
+                             : launch_nodes<64, kBf16, false>(p, stream);
 }
 template <bool kBf16>
 cudaError_t launch_commit_dtype(const RecurParams& p, cudaStream_t stream) {
@@ -672,8 +717,10 @@ cudaError_t launch_commit_dtype(const RecurParams& p, cudaStream_t stream) {
 
 }  // namespace
 
-cudaError_t launch_recur(const RecurParams& p, cudaStream_t stream) {
-  return p.state_bf16 ? launch_dtype<true>(p, stream) : launch_dtype<false>(p, stream);
+cudaError_t launch_recur(const RecurParams& p, int sms, cudaStream_t stream) {
+  const bool many = p.num_seqs * p.heads > 2 * sms;
+  if (many) return p.state_bf16 ? launch_dtype<true, true>(p, stream) : launch_dtype<false, true>(p, stream);
+  return p.state_bf16 ? launch_dtype<true, false>(p, stream) : launch_dtype<false, false>(p, stream);
 }
 cudaError_t launch_commit(const RecurParams& p, cudaStream_t stream) {
   return p.state_bf16 ? launch_commit_dtype<true>(p, stream) : launch_commit_dtype<false>(p, stream);

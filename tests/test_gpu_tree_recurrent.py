@@ -302,3 +302,26 @@ def test_calls_without_tokens_or_sequences():
     assert out.shape == (0, 2, D)
     mask, pos = kda.tree_plan(empty, i32([0, 0]), i32([5]), 4)
     assert mask.shape == pos.shape == (0,)
+
+
+@pytest.mark.parametrize("state", ["f32", "bf16"])
+@pytest.mark.parametrize("most", [8, 16, 32])
+def test_more_sequences_than_run_at_once(most, state):
+    """Several (sequence, head) pairs a multiprocessor, one after the other; a sequence's results do not depend on
+    the batch that it is in."""
+    H = 8
+    lens = [(5 * n + 3) % (most + 1) for n in range(41)] + [most]
+    d = make(lens, H, state, seed=11, strided=True)
+    trees = trees_of(lens, 41)
+    parents = [p for t in trees for p in t]
+    ends = [n - 1 for n in lens]
+    out, u, status = forward(d, lens, parents, most)
+    assert status == kda.OK
+    fin, status = commit(d, lens, parents, u, ends, most)
+    assert status == kda.OK
+    check(d, lens, trees, ends, out, u, fin)
+    some = {x: d[x] for x in ("A_log", "dt_bias")}
+    n, T = 7, sum(lens[:7])
+    some.update({x: d[x][:T] for x in ("q", "k", "v", "g", "beta")}, state=d["state"][:n])
+    few = forward(some, lens[:n], parents[:T], most)
+    assert few[2] == kda.OK and torch.equal(few[0], out[:T]) and torch.equal(few[1], u[:T])
