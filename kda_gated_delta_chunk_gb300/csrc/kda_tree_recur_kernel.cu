@@ -21,8 +21,8 @@
 // SM (the nodes' loads 3,000, gates and norms 2,400, walks and vectors 10,000, the state 3,500 and its terms
 // 1,400, the products 2,300, the nodes in order 7,000), and a bf16 state takes 75 us to fp32's 78.  Measured and not
 // kept: 512 threads a CTA (99 us, two CTAs of 256 95), the state towards L2 ahead (no gain), the next ancestor's
-// rows loaded ahead (none), half the shuffles of a walk (none), the inverse of 1 + b K solved for beside the
-// product and a second product with it (101).
+// rows loaded ahead, half the shuffles of a walk, keys in bf16 there (none), the inverse of 1 + b K solved for
+// beside the product and a second product with it (101).
 #include <cuda_fp16.h>
 
 #include "kda_attn_tc.cuh"
