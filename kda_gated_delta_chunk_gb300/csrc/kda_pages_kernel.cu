@@ -248,8 +248,9 @@ __global__ void __launch_bounds__(kThreads)
     kda_pages_fork_kernel(const Pool p, const int32_t* src, const int32_t* dst, int num, int32_t* from,
                           int32_t* to) {
   extern __shared__ int smem[];
-  int* who = smem;                   // [num] pairs that need a page
-  int* uses = smem + num;            // [num_rows] pairs that write to the row, and whether one reads it
+  int* found = smem;                 // [num] the pages that were found, in order
+  int* rank = smem + num;            // [num] which of them is a pair's, or -1
+  int* uses = smem + 2 * num;        // [num_rows] pairs that write to the row, and whether one reads it
   __shared__ int part[kWarps + 1];
   sm100::pdl_wait();
   sm100::pdl_launch_dependents();
@@ -326,20 +327,29 @@ __global__ void __launch_bounds__(kThreads)
         }
       }
       from[i] = pg;
-      to[i] = -1;
     }
     int sum;
     const int before = total + block_scan(need, part, &sum);
-    if (need) who[before] = i;
+    if (i < num) {
+      rank[i] = need ? before : -1;
+      found[i] = -1;
+    }
     total += sum;
   }
   __syncthreads();
-  const bool enough = find_free(p.refs, p.num_pages, total, part, counts, [&](int rank, int page) {
-    const int i = who[rank];
-    p.table[(int64_t)dst[i] * p.table_stride + p.kv_lens[src[i]] / p.page_size] = page;
+  const bool enough = find_free(p.refs, p.num_pages, total, part, counts, [&](int r, int page) {
+    found[r] = page;
     p.refs[page] = 1;
-    to[i] = page;
   });
+  __syncthreads();
+  // (a thread with one pair has its rows still)
+  for (int i = threadIdx.x; i < num; i += kThreads) {
+    const int page = rank[i] >= 0 ? found[rank[i]] : -1;
+    to[i] = page;
+    if (page < 0) continue;
+    if (num > kThreads) load(i, s, d, len, last);
+    p.table[(int64_t)d * p.table_stride + len / p.page_size] = page;
+  }
   if (!enough && threadIdx.x == 0) record_error(p.status, KDA_ERR_OUT_OF_PAGES, 429);
 }
 
@@ -406,9 +416,9 @@ cudaError_t launch_reserve(const Pool& p, const int32_t* new_tokens, cudaStream_
 cudaError_t launch_fork(const Pool& p, const int32_t* src, const int32_t* dst, int32_t num, int32_t* from,
                         int32_t* to, cudaStream_t stream) {
   static PerDeviceOnce once;
-  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kda_pages_fork_kernel), once, kMaxRows * 8);
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kda_pages_fork_kernel), once, kMaxRows * 12);
   if (e != cudaSuccess) return e;
-  return attn::launch(kda_pages_fork_kernel, dim3((unsigned)num + 1), dim3(kThreads), (size_t)(num + p.num_rows) * 4, true,
+  return attn::launch(kda_pages_fork_kernel, dim3((unsigned)num + 1), dim3(kThreads), (size_t)(2 * num + p.num_rows) * 4, true,
                       stream, p, src, dst, num, from, to);
 }
 
