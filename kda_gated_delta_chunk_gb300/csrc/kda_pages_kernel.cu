@@ -6,12 +6,13 @@
 // which threads run, and there is no list of free pages to keep.  The search is one CTA's scan over the
 // counts, 16384 at a time, which ends at the page that serves the last request; a page that is
 // found knows its rank, and the rank the request (a binary search over the requests' prefix sums in
-// shared memory).  The first counts are on their way while the requests are counted.  Counts go up
+// shared memory).  The first counts are on their way while the requests are counted (the next ones as well: 19.4 us, an
+SM's loads bound the scan).  Counts go up
 // and down by atomics on integers, whose order does not show.
 //
 // Nothing here moves bytes that count; each call is a launch and a chain of dependent loads.  64 rows ended,
 // forked from 16 prompts of up to 65535 tokens, their last pages copied (2 kv heads, pages of 64) and 64 tokens a
-// row reserved, in a pool of 24000 pages: 18.6 us for the four calls, about 3, 6.3, 2 and 7.
+// row reserved, in a pool of 24000 pages: 17.9 us for the four calls, about 3, 5.6, 2 and 7.
 #include "kda_pages.cuh"
 
 namespace kda {
