@@ -6,8 +6,8 @@
 // which threads run, and there is no list of free pages to keep.  The search is one CTA's scan over the
 // counts, 16384 at a time, which ends at the page that serves the last request; a page that is
 // found knows its rank, and the rank the request (a binary search over the requests' prefix sums in
-// shared memory).  The first counts are on their way while the requests are counted (the next ones as well: 19.4 us, an
-SM's loads bound the scan).  Counts go up
+// shared memory).  The first counts are on their way while the requests are counted (the next ones
+// as well: 19.4 us; an SM's loads bound the scan).  Counts go up
 // and down by atomics on integers, whose order does not show.
 //
 // Nothing here moves bytes that count; each call is a launch and a chain of dependent loads.  64 rows ended,
