@@ -561,7 +561,10 @@ int kda_cache_accept(const kda_kv_cache* cache, const int32_t* cu_seqlens, const
  *   their pages go back and their kv_lens become 0 (a row may be named twice).
  * kda_pages_reserve: pages for new_tokens [num_rows] more tokens a row: its empty blocks up to
  *   ceil((kv_lens + new_tokens) / page_size) get one each.  kv_lens stays.  At most 16384 rows,
- *   and 2^31 - 1 blocks in all of them.
+ *   and 2^31 - 1 blocks in all of them.  The pages from the kv_lens-th token on have to be the row's
+ *   alone (counts of 1), since the new tokens are written there: a row whose kv_lens was set back into
+ *   a page that a fork shares is reported and gets nothing.  It may be read, and a fork of it has a
+ *   copy of that page.
  * kda_pages_fork: row dst[i] becomes a copy of row src[i] (kv_lens too): whole pages are held in common,
  *   a partly filled last one is given a page of its own, to be copied: from_pages[i] -> to_pages[i], both
  *   -1 where there is none.  What dst[i] held before is overwritten, not given back.  A source may

@@ -190,14 +190,23 @@ __global__ void __launch_bounds__(kThreads)
         end = (int)need;
       }
     }
-    // empty blocks from the first empty one on: a lane its own row, or the warp a long one together
+    // empty blocks from the first empty one on: a lane its own row, or the warp a long one together.  A page
+    // before them takes new tokens: it has to be this row's alone (kv_lens may have been set back into one that
+    // a fork shares).
+    auto others = [&](int pg) { return pg < 0 || pg >= p.num_pages || p.refs[pg] != 1; };
     int at = b;
     const int32_t* table = p.table + (int64_t)row * p.table_stride;
     const bool far = end - b > 8;
     if (!far) {
       uint32_t empty = 0;
+      int pg[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) empty |= (uint32_t)(b + j < end && table[b + j] == -1) << j;
+      for (int j = 0; j < 8; ++j) {
+        pg[j] = b + j < end ? table[b + j] : -1;
+        empty |= (uint32_t)(b + j < end && pg[j] == -1) << j;
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) bad |= pg[j] != -1 && others(pg[j]);
       at = empty ? b + __ffs(empty) - 1 : end;
       bad |= at < end && (empty >> (at - b)) != (1u << (end - at)) - 1;      // a page behind an empty block
     }
@@ -207,17 +216,20 @@ __global__ void __launch_bounds__(kThreads)
       todo &= todo - 1;
       const int bk = __shfl_sync(0xffffffffu, b, k), ek = __shfl_sync(0xffffffffu, end, k);
       const int32_t* t = p.table + (int64_t)(row - lane + k) * p.table_stride;
-      int found = ek, hole = 0;
+      int found = ek, wrong = 0;
       for (int i0 = bk; i0 < ek; i0 += 32) {
-        const bool in = i0 + lane < ek, empty = in && t[i0 + lane] == -1;
+        const bool in = i0 + lane < ek;
+        const int pg = in ? t[i0 + lane] : -1;
+        const bool empty = in && pg == -1;
         const uint32_t e = __ballot_sync(0xffffffffu, empty), f = __ballot_sync(0xffffffffu, in && !empty);
+        if (__any_sync(0xffffffffu, in && !empty && others(pg))) wrong = 1;
         if (found == ek && e) found = i0 + __ffs(e) - 1;
         // a page behind an empty block
-        if (found < ek && (f >> max(0, found - i0)) != 0 && i0 + 31 >= found) hole = 1;
+        if (found < ek && (f >> max(0, found - i0)) != 0 && i0 + 31 >= found) wrong = 1;
       }
       if (lane == k) {
         at = found;
-        bad |= hole;
+        bad |= wrong;
       }
     }
     if (bad) {

@@ -66,7 +66,11 @@ def free_pages(refs, block_table, kv_lens, page_size: int, rows=None, workspace=
 
 
 def reserve_pages(refs, block_table, kv_lens, new_tokens, page_size: int, workspace=None, stream=None):
-    """Run ``kda_pages_reserve``: pages for new_tokens (int32 [rows]) more tokens of each row."""
+    """Run ``kda_pages_reserve``: pages for new_tokens (int32 [rows]) more tokens of each row.
+
+    A row whose new tokens would go into a page that other rows hold as well (its kv_lens was set back into a
+    shared one) is reported and gets none; a fork of it has a page of its own there.
+    """
     if stream is None:
         done = native().reserve_pages(refs, block_table, kv_lens, new_tokens, page_size, workspace)
         if done is True:
