@@ -573,10 +573,19 @@ int kda_cache_accept(const kda_kv_cache* cache, const int32_t* cu_seqlens, const
  * kda_pages_copy: pages from[i] to pages to[i] of one layer's cache, keys, values and scales; pairs with a
  *   negative page are left out (of the cache, block_table and kv_lens are not read).  No page
  *   may be written by two pairs, or written and read by two.
- * Device errors: KDA_ERR_BAD_CACHE_INDEX for a row, page, length or count out of range, a page that nobody
- * held, or a row with a page behind an empty block (the row, page or pair is left out);
- * KDA_ERR_OUT_OF_PAGES when the free pages do not suffice: the first requests got them, the others'
- * entries are -1.  Workspace: the 256 bytes with the status word.
+ * Device errors, KDA_ERR_BAD_CACHE_INDEX but for the last:
+ *   free: a row or length out of range is left out; an entry outside the pool, or whose page nobody held,
+ *     becomes -1 and no count changes.
+ *   reserve: a length or request out of range, a page that is not the row's alone or outside the pool where new
+ *     tokens go, a page behind an empty block, a partly filled last page that is missing: the row gets nothing.
+ *   fork: a pair with a row or length out of range, or a dst as above, is left out (from and to -1).  A page of
+ *     the source outside the pool is -1 in the copy, whose kv_lens is the source's all the same.
+ *   copy: a pair with a page past the pool's end is left out.
+ *   KDA_ERR_OUT_OF_PAGES when the free pages do not suffice: the first requests got them, the others'
+ *     entries are -1.  A fork's copy without its last page (to_pages[i] -1, from_pages[i] not) has the source's
+ *     kv_lens: end it (kda_pages_free), or set its kv_lens down to its whole pages.  Until then the
+ *     attention and kda_pages_reserve report it.
+ * Workspace: the 256 bytes with the status word.
  */
 int kda_pages_free(int32_t* refs, int32_t num_pages, int32_t* block_table, int64_t table_stride,
                    int32_t num_rows, int32_t max_blocks, int32_t* kv_lens, int32_t page_size,

@@ -180,6 +180,7 @@ __global__ void __launch_bounds__(kThreads)
   for (int r0 = 0; r0 < p.num_rows; r0 += kThreads) {
     const int row = r0 + threadIdx.x;
     int b = 0, end = 0, bad = 0;
+    bool begun = false;         // the first block holds cached text
     if (row < p.num_rows) {
       const int64_t len = p.kv_lens[row], add = new_tokens[row];
       const int64_t need = (len + add + p.page_size - 1) / p.page_size;
@@ -188,6 +189,7 @@ __global__ void __launch_bounds__(kThreads)
       } else if (add > 0) {
         b = (int)(len / p.page_size);
         end = (int)need;
+        begun = len % p.page_size != 0;
       }
     }
     // empty blocks from the first empty one on: a lane its own row, or the warp a long one together.  A page
@@ -232,7 +234,8 @@ __global__ void __launch_bounds__(kThreads)
         bad |= wrong;
       }
     }
-    if (bad) {
+    // (an empty page in the place of cached text, as after a fork that found none, would pass for it)
+    if (bad || (begun && at == b)) {
       record_error(p.status, KDA_ERR_BAD_CACHE_INDEX, 424);
       at = end;
     }

@@ -96,7 +96,8 @@ def fork_pages(refs, block_table, kv_lens, src, dst, page_size: int, from_pages=
 
     Whole pages are shared.  Returns (from_pages, to_pages), int32 [m] for ``copy_pages`` on every layer's
     cache: a partly filled last page and the one to copy it to, -1 where there is none.  The rows of dst
-    hold no pages before (``free_pages``), and none is a source.
+    hold no pages before (``free_pages``), and none is a source.  Where the pool has too few pages
+    (ERR_OUT_OF_PAGES), a row without its last page is to be ended, or its kv_lens set down to its whole pages.
     """
     if from_pages is None and to_pages is None and stream is None:
         done = native().fork_pages(refs, block_table, kv_lens, src, dst, page_size, workspace)

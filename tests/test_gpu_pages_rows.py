@@ -101,3 +101,61 @@ def test_blocks_that_hold_a_page_outside_the_pool_or_a_free_one(new):
         assert kda.last_device_status(ws) == BAD, what
         plain.reserve([0, 0, 0, 5, 0])
         same(gpu, plain)
+
+
+def test_a_fork_that_found_too_few_pages():
+    """The copy without its last page gets none from reserve_pages (an empty one would pass for cached text), also
+    once there are free pages again; it is reported until it is ended or set down to its whole pages."""
+    page, rows = 16, 5
+    state = pool_of([20, 0, 0, 21, 0], page, 40, 5, 12)
+    gpu, plain, ws = on_gpu(*state), ref.Pool(*state, page), status_words()
+    got = kda.fork_pages(*gpu, i32([0, 0]), i32([1, 2]), page, workspace=ws)
+    want = plain.fork([0, 0], [1, 2])
+    assert kda.last_device_status(ws) == kda.ERR_OUT_OF_PAGES
+    assert [x.tolist() for x in got] == list(want) and want[1][0] >= 0 and want[1][1] == -1
+    same(gpu, plain)
+    kda.free_pages(*gpu, page, rows=i32([3]), workspace=ws)
+    plain.free([3])
+    for new in (1, 300):
+        ws.zero_()
+        kda.reserve_pages(*gpu, i32([0, 0, new, 0, 10]), page, workspace=ws)
+        assert kda.last_device_status(ws) == BAD
+        plain.reserve([0, 0, 0, 0, 10])
+        same(gpu, plain)
+    gpu[2][2] = plain.lens[2] = 16
+    ws.zero_()
+    kda.reserve_pages(*gpu, i32([0, 0, 5, 0, 0]), page, workspace=ws)
+    plain.reserve([0, 0, 5, 0, 0])
+    assert kda.last_device_status(ws) == kda.OK
+    same(gpu, plain)
+
+
+@pytest.mark.parametrize("what", [-1, -5, 60, 1 << 30])
+@pytest.mark.parametrize("block", [0, 3, 6])        # (6: the partly filled one)
+def test_a_fork_of_a_row_with_a_page_outside_the_pool(block, what):
+    """The copy has -1 there and is otherwise whole; the pair beside it is done, and where it is the last page, no
+    page is taken for it and the copy gets none from reserve_pages."""
+    state = pool_of([100, 0, 37, 0, 0], 16, 40, 60, 13)
+    gpu, plain, ws = on_gpu(*state), ref.Pool(*state, 16), status_words()
+    held = plain.table[0][block]
+    gpu[1][0, block] = what
+    fro, to = kda.fork_pages(*gpu, i32([0, 2]), i32([1, 3]), 16, workspace=ws)
+    assert kda.last_device_status(ws) == BAD
+    if block == 6:
+        plain.lens[0] = 96                # (the definition of a source that ends there)
+        want = plain.fork([0, 2], [1, 3])
+        plain.lens[0] = plain.lens[1] = 100
+        assert want[0][0] == want[1][0] == -1
+    else:
+        want = plain.fork([0, 2], [1, 3])
+        plain.refs[held] -= 1             # (its copy's entry holds nothing)
+        plain.table[1][block] = -1
+    plain.table[0][block] = what
+    assert [fro.tolist(), to.tolist()] == list(want)
+    same(gpu, plain)
+    if block == 6:
+        ws.zero_()
+        kda.reserve_pages(*gpu, i32([0, 5, 0, 40, 0]), 16, workspace=ws)
+        assert kda.last_device_status(ws) == BAD
+        plain.reserve([0, 0, 0, 40, 0])
+        same(gpu, plain)
