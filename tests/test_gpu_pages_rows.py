@@ -159,3 +159,19 @@ def test_a_fork_of_a_row_with_a_page_outside_the_pool(block, what):
         assert kda.last_device_status(ws) == BAD
         plain.reserve([0, 0, 0, 40, 0])
         same(gpu, plain)
+
+
+def test_entries_that_nobody_holds_are_given_back_as_nothing():
+    """free_pages with a page behind an empty block: a page that is free stays free and is reported, one that the
+    row holds goes back like the others."""
+    for counted in (False, True):
+        state = pool_of([40, 0, 20], 16, 6, 12, 14)
+        free = state[0].index(0)
+        state[1][1][3] = free
+        state[0][free] = int(counted)
+        gpu, plain, ws = on_gpu(*state), ref.Pool(*state, 16), status_words()
+        kda.free_pages(*gpu, 16, workspace=ws)
+        assert kda.last_device_status(ws) == (kda.OK if counted else BAD)
+        plain.free()
+        plain.refs[free] = 0
+        same(gpu, plain)
