@@ -537,8 +537,9 @@ int kda_tree_commit(const void* k, int64_t k_stride, const void* g, int64_t g_st
  * scale changes are requantised (exact for powers of two, but for what falls below e4m3's smallest
  * normal).
  *   accepted   int32 [num_seqs]: a node of the sequence, or -1
- *   lens_out   int32 [num_seqs]: start + the branch's length, the next step's cached tokens.  Not the
- *              cache's kv_lens itself, which every layer's call reads, and not accepted.
+ *   lens_out   int32 [num_seqs]: start + the branch's length, the next step's cached tokens.  An array of
+ *              its own: one that has bytes in common with kv_lens, which every layer's call reads, or with
+ *              accepted, cu_seqlens, parents or block_table is refused.
  * No two sequences may have a page in common among those of their nodes.  Device errors:
  * KDA_ERR_BAD_CU_SEQLENS, KDA_ERR_INVALID_ARG (more nodes than max_q_len), KDA_ERR_BAD_TREE (accepted out
  * of range; a bad parent counts as -1), KDA_ERR_BAD_CACHE_INDEX (kv_lens below the nodes' count or beyond the

@@ -10,6 +10,12 @@ namespace checks {
 
 inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
+// Whether two arrays of na and nb int32 have bytes in common.
+inline bool overlap(const int32_t* a, int64_t na, const int32_t* b, int64_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return na > 0 && nb > 0 && x < y + 4 * (uintptr_t)nb && y < x + 4 * (uintptr_t)na;
+}
+
 inline bool known_dtype(int d) { return d == KDA_STATE_F32 || d == KDA_STATE_BF16; }
 
 // KDA_OK on a supported current device; its multiprocessor count in *sms.

@@ -179,11 +179,15 @@ int kda_cache_accept(const kda_kv_cache* cache, const int32_t* cu_seqlens, const
   int rc = check_trees(cu_seqlens, parents, workspace, total_tokens, num_seqs, max_q_len, workspace_bytes);
   if (rc != KDA_OK) return rc;
   if ((rc = check_cache(cache, num_seqs, &p.c)) != KDA_OK) return rc;
-  // (every head's CTAs read what one of them would write)
-  if (num_seqs > 0 && (!accepted || !lens_out || lens_out == cache->kv_lens || lens_out == accepted))
-    return KDA_ERR_INVALID_ARG;
+  if (num_seqs > 0 && (!accepted || !lens_out)) return KDA_ERR_INVALID_ARG;
   if ((int64_t)num_seqs * cache->kv_heads * 2 > INT32_MAX) return KDA_ERR_INVALID_ARG;
   if (!aligned(accepted, 4) || !aligned(lens_out, 4)) return KDA_ERR_MISALIGNED;
+  // (every head's CTAs, and other sequences', read what one of them would write)
+  const int64_t table = num_seqs > 0 ? (int64_t)((uint64_t)(num_seqs - 1) * (uint64_t)cache->table_stride) + cache->max_blocks : 0;
+  if (overlap(lens_out, num_seqs, cache->kv_lens, num_seqs) || overlap(lens_out, num_seqs, accepted, num_seqs) ||
+      overlap(lens_out, num_seqs, cu_seqlens, (int64_t)num_seqs + 1) ||
+      overlap(lens_out, num_seqs, parents, total_tokens) || overlap(lens_out, num_seqs, cache->block_table, table))
+    return KDA_ERR_INVALID_ARG;
   int sms = 0;
   rc = current_device(&sms);
   if (rc != KDA_OK) return rc;
