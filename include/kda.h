@@ -574,6 +574,8 @@ int kda_cache_accept(const kda_kv_cache* cache, const int32_t* cu_seqlens, const
  * kda_pages_copy: pages from[i] to pages to[i] of one layer's cache, keys, values and scales; pairs with a
  *   negative page are left out (of the cache, block_table and kv_lens are not read).  No page
  *   may be written by two pairs, or written and read by two.
+ * Lists (rows, src, dst, from_pages, to_pages) that share bytes with the pool's arrays are refused, and
+ * from_pages and to_pages that do with each other, src or dst.
  * Device errors, KDA_ERR_BAD_CACHE_INDEX but for the last:
  *   free: a row or length out of range is left out; an entry outside the pool, or whose page nobody held,
  *     becomes -1 and no count changes.

@@ -77,6 +77,12 @@ int check_pool(int32_t* refs, int32_t num_pages, int32_t* block_table, int64_t t
   p->max_blocks = max_blocks;
   return KDA_OK;
 }
+// Whether a list shares bytes with what a call on the pool changes.
+bool over_pool(const int32_t* list, int64_t n, const kda::pages::Pool& p) {
+  const int64_t table = p.num_rows > 0 ? (int64_t)((uint64_t)(p.num_rows - 1) * (uint64_t)p.table_stride) + p.max_blocks : 0;
+  return overlap(list, n, p.refs, p.num_pages) || overlap(list, n, p.table, table) ||
+         overlap(list, n, p.kv_lens, p.num_rows);
+}
 
 }  // namespace
 
@@ -213,6 +219,7 @@ int kda_pages_free(int32_t* refs, int32_t num_pages, int32_t* block_table, int64
   if (rc != KDA_OK) return rc;
   if (num < 0) return KDA_ERR_INVALID_ARG;
   if (!aligned(rows, 4)) return KDA_ERR_MISALIGNED;
+  if (rows && over_pool(rows, num, p)) return KDA_ERR_INVALID_ARG;
   int sms = 0;
   rc = current_device(&sms);
   if (rc != KDA_OK) return rc;
@@ -252,6 +259,12 @@ int kda_pages_fork(int32_t* refs, int32_t num_pages, int32_t* block_table, int64
   if (num > 0 && (!src || !dst || !from_pages || !to_pages)) return KDA_ERR_INVALID_ARG;
   if (!aligned(src, 4) || !aligned(dst, 4) || !aligned(from_pages, 4) || !aligned(to_pages, 4))
     return KDA_ERR_MISALIGNED;
+  // (every pair's CTA reads all of src and dst)
+  for (const int32_t* list : {src, dst, const_cast<const int32_t*>(from_pages), const_cast<const int32_t*>(to_pages)})
+    if (over_pool(list, num, p)) return KDA_ERR_INVALID_ARG;
+  for (const int32_t* out : {from_pages, to_pages})
+    if (overlap(out, num, src, num) || overlap(out, num, dst, num)) return KDA_ERR_INVALID_ARG;
+  if (overlap(from_pages, num, to_pages, num)) return KDA_ERR_INVALID_ARG;
   int sms = 0;
   rc = current_device(&sms);
   if (rc != KDA_OK) return rc;
