@@ -58,7 +58,7 @@ struct Cfg {
   static constexpr int kOffV = NT * 1024;                         // bf16 [NT][128]
   static constexpr int kOffKK = kOffV + NT * 256;                 // K: blocks (b, pb <= b) of [8 j][8 i]
   static constexpr int kOffQQ = kOffKK + kPairs * 256;
-  static constexpr int kOffMax = kOffQQ + kPairs * 256;           // uint [2][128]
+  static constexpr int kOffMax = kOffQQ + kPairs * 256;           // float [2][128]; then uint8 [kBlocks][128]
   static constexpr int kOffMul = kOffMax + 1024;                  // float [kRows]
   static constexpr int kOffBeta = kOffMul + kRows * 4;            // float [NT]
   static constexpr int kOffLink = kOffBeta + NT * 4;              // int [NT]
@@ -69,6 +69,7 @@ struct Cfg {
   static constexpr uint32_t kTD = kBf16 || kLate ? 64 : 128;      // the state's terms, then the sums
   static constexpr uint32_t kTmem = kTD + kRows <= 128 ? 128 : 256;
   static_assert(2 * kB == NT * 1024, "the vectors over keys and decays");
+  static_assert(kBlocks * 128 <= 1024, "the blocks' marks over the maxima");
   static_assert(kCtas * kBytes <= 226 * 1024 && kCtas * kTmem <= 512, "CTAs an SM");
 };
 __device__ __forceinline__ int pair_block(int b, int pb) { return b * (b + 1) / 2 + pb; }
@@ -203,7 +204,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<NT, kBf16, kMany>::kCtas)
   int* link = reinterpret_cast<int*>(sm + C::kOffLink);
   int* flag = reinterpret_cast<int*>(sm + C::kOffFlag);
   uint64_t* anc = reinterpret_cast<uint64_t*>(sm + C::kOffAnc);
-  int* bad_s = reinterpret_cast<int*>(sm + C::kOffMax);      // (over the maxima)
+  uint8_t* bad_s = sm + C::kOffMax;      // (over the maxima; a block its own: u's warps run ahead of o's)
 
   if (tid < NT) {      // (past the nodes: zeros)
     beta[tid] = tid < s.n ? sigmoid_of(beta_in) : 0.0f;
@@ -530,11 +531,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<NT, kBf16, kMany>::kCtas)
           if (r < left) u_out[r * step] = u[r];
         }
         u_out += (int64_t)kBlock * step;
-        bad_s[col] = bad;
+        bad_s[128 * b + col] = bad;
         bar_arrive(1 + b, kThreads);
       } else {
         named_barrier_sync(1 + b, kThreads);
-        bad = bad_s[col] != 0;
+        bad = bad_s[128 * b + col] != 0;
         add(b);
         if (bad) {
 #pragma unroll
