@@ -502,7 +502,11 @@ int kda_tree_attention(const void* q, int64_t q_stride, const kda_kv_cache* cach
  *   out          bf16 [T, heads, 128], dense
  *   u            fp32 [T, heads, 128], dense, 16-byte aligned: what each node adds to the state,
  *                S_i = diag(decay_i) S_parent + kh_i u_i^T
- * Sums, decays and u are fp32; the state's products take two f16 terms of each factor (22 bits).  Device errors:
+ * out and u must not overlap any input or each other.
+ * Precision: sums, decays and u are fp32.  A decay is exact to 2^-20 of itself.  The state's products take two f16
+ * terms of each factor: exact to 2^-22 of itself and 2^-38 of the largest, of its value channel (state) or of
+ * the node's vector (a key or query times the decays of its branch), so what lies more than a factor of 2^16 below
+ * that loses bits.  Device errors:
  * KDA_ERR_BAD_CU_SEQLENS, KDA_ERR_INVALID_ARG (more nodes than max_q_len): that sequence's rows are not
  * written; KDA_ERR_BAD_TREE.
  */
@@ -518,7 +522,8 @@ int kda_tree_recurrent_fwd(const void* q, int64_t q_stride, const void* k, int64
  * The state after node accepted[n] (-1: as before the tree) of each sequence, from the k, g and u of
  * kda_tree_recurrent_fwd's call, the other arguments being that call's.
  *   accepted      int32 [num_seqs]
- *   final_state   [num_seqs, heads, 128, 128] in state_dtype; may be initial_state (the update is then in place)
+ *   final_state   [num_seqs, heads, 128, 128] in state_dtype; may be initial_state (the update is then in place),
+ *                 but not overlap it otherwise, nor the other inputs
  * A malformed sequence (KDA_ERR_BAD_CU_SEQLENS, KDA_ERR_INVALID_ARG, KDA_ERR_BAD_TREE for accepted out of range) keeps its
  * initial state.
  */

@@ -7,9 +7,11 @@
 // none is written (a state a node would be 64 KB each); kda_tree_commit makes the accepted one of the u.
 //
 // S0^T times the 2 n vectors is one tcgen05 product: M = 128 value channels, N = 2 n, K = 128 key channels, f16
-// with fp32 sums.  fp32 values enter as two f16 terms, hi hi + hi lo + lo hi: 22 bits.  f16's range is met
-// by powers of two, one a value channel of S0 and one a vector, taken out of the sums again.  (A state in
-// bf16 is exact in one term.)  S0 goes from registers to tensor memory, a thread half a column of it: that
+// with fp32 sums.  fp32 values enter as two f16 terms, hi hi + hi lo + lo hi.  f16's range is met by powers of two,
+// one a value channel of S0 and one a vector, which bring the largest to 2^13 or more and are taken out of the sums
+// again: a factor is exact to 2^-22 of itself, and to f16's half step of 2^-25, 2^-38 of the largest (so one of 2^-24
+// of it keeps 14 bits).  The low terms' own product, 2^-22 again, is left out.  (A state in bf16 is exact in one
+// term down to 2^-30 of its column's largest.)  S0 goes from registers to tensor memory, a thread half a column of it: that
 // operand needs no shared memory and no transposition.  The rest is fp32:
 //  - a node's walk up its branch carries kh and qh times the decays met, 8 lanes a node and 16 channels a
 //    lane, one pair of products an ancestor, and ends as c_i kh_i and c_i qh_i;
