@@ -18,10 +18,12 @@
 //  - then the nodes in blocks of 8, a thread a value channel: four warps make u, the other four follow a block
 //    behind with o.  Sums over earlier blocks have no chain but their own length, and blocks without a pair
 //    of node and ancestor are left out.
-// 64 sequences of 32 nodes, 32 heads, fp32 states (134 MB of them): 82 us, 2.8 TB/s of what has to move; one
-// tree of 8 nodes, 16 heads 5.4 us.  Not bound by memory: a (sequence, head) takes 30,000 cycles of three on an
-// SM (the nodes' loads 3,000, gates and norms 2,400, walks and vectors 10,000, the state 3,500 and its terms
-// 1,400, the products 2,300, the nodes in order 7,000), and a bf16 state takes 75 us to fp32's 78.  Measured and not
+// 64 sequences of 32 nodes, 32 heads, fp32 states, inputs cold: 78 us with random parents, 82.6 where every second
+// node follows the one before it (252 MB of inputs and outputs, 134 of them states: 3.1 TB/s), 115 for chains; with
+// bf16 states (185 MB) 75 and 79.5; 64 nodes 193 and 206 (fp32), 183 and 197 (bf16), two CTAs an SM; one tree of 8 nodes,
+// 16 heads 5.5.  Not bound by memory: a (sequence, head) takes 30,000 cycles of three on an SM (the nodes' loads
+// 3,000, gates and norms 2,400, walks and vectors 10,000, the state 3,500 and its terms 1,400, the products 2,300,
+// the nodes in order 7,000), and half the state's bytes save 3 us.  Measured and not
 // kept: 512 threads a CTA (99 us, two CTAs of 256 95), the state towards L2 ahead (no gain), the next ancestor's
 // rows loaded ahead, half the shuffles of a walk, keys in bf16 there (none), the inverse of 1 + b K solved for
 // beside the product and a second product with it (101).
@@ -46,9 +48,9 @@ template <int NT, bool kBf16, bool kMany>      // nodes at most; the state's typ
 struct Cfg {
   // Three CTAs an SM have 80 registers a thread and 128 columns of tensor memory each.  So the state comes late, when
   // the walks are done (its first rows a little earlier), and its two terms take the same columns one after the
-  // other.  Alone on an SM that costs time, beside two others it hides: 64 sequences of 8, 16, 32 nodes, 32 heads
-  // 44, 53, 78 us (all of the state late 45, 54, 80), two CTAs with the state on its way from the start 52, 62, 91;
-  // 10 sequences of 32 nodes 20 : 23.
+  // other.  Alone on an SM that costs time, beside two others it hides: 64 sequences of 8, 16, 32 nodes with random
+  // parents, 32 heads, fp32 44, 53, 78 us (all of the state late 45, 54, 80), two CTAs with the state on its way from
+  // the start 52, 62, 91; 10 sequences of 32 nodes 20 : 23.
   static constexpr int kCtas = kMany && NT <= 32 ? 3 : 2;         // an SM
   static constexpr bool kLate = kCtas == 3;
   static constexpr int kEarly = 24;                               // (of 64)
@@ -565,8 +567,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<NT, kBf16, kMany>::kCtas)
 // The state after the accepted branch: S' = diag(c) S0 + sum_e (decays after e . kh_e) u_e^T over the branch's nodes e.
 // A CTA takes half of a (sequence, head)'s key channels: the state's rows in registers, kRows a warp and 4 value
 // channels a lane, on their way while the branch is found and its keys are scaled.  Bound by the state's
-// read and write: 64 sequences, 32 heads, fp32 (268 MB) 50.1 us, 5.4 TB/s; a whole (sequence, head) a CTA and
-// two CTAs an SM 54.4.
+// read and write: 64 sequences of 32 nodes, 32 heads, fp32 (268 MB) 50.2 us, 5.4 TB/s; a whole (sequence, head) a CTA
+// and two CTAs an SM 54.4.  bf16 (134 MB) takes 40, and 34 with 8 nodes: what a CTA does
+// before its sums (the branch, its keys, decays and u) does not shrink with the state.
 constexpr int kCommitRows = 8, kHalves = kHeadDim / (kCommitRows * kThreads / 32);
 __host__ __device__ constexpr int commit_bytes(int nodes) { return nodes * 1024; }   // keys and u, fp32
 
