@@ -562,6 +562,9 @@ int kda_cache_accept(const kda_kv_cache* cache, const int32_t* cu_seqlens, const
  * whatever the order in which threads run.  page_size is any positive number.  A layer's caches are
  * copied by kda_pages_copy; the rest is done once for all layers.
  *
+ * A page that more than one row holds is for reading: kda_rope_append and kda_cache_accept, which write to
+ * pages, do not know the counts, so kda_pages_reserve comes before them.
+ *
  * kda_pages_free: gives pages back.  rows NULL: every row's pages beyond those that its kv_lens fill (as
  *   after a step whose drafts were partly rejected).  Else the rows named in rows [num] end: all
  *   their pages go back and their kv_lens become 0 (a row may be named twice).

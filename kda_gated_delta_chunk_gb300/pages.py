@@ -7,7 +7,8 @@ The calls of ``include/kda.h``'s section on pages, on torch tensors; marshalling
     kv_lens       int32 [rows]
 
 updated in place; who needs pages gets the lowest free ones, in the order of rows and blocks.
-block_table and kv_lens are those of ``rope_append`` and the attention calls.
+block_table and kv_lens are those of ``rope_append`` and the attention calls.  A page that more than one row holds
+is for reading: ``reserve_pages`` looks at the counts before ``rope_append`` and ``cache_accept`` write.
 """
 from __future__ import annotations
 
